@@ -143,6 +143,9 @@ size_t mixer_prefill_ws_bytes(const gdn_config *cfg, long long T, long long n_se
     return prefill_ws_bytes(d, cfg->act == GDN_BF16, T, n_seqs);
 }
 
+gdn_status device_error_word(unsigned **out) { return error_word(out); }
+unsigned long long wait_limit_ns() { return g_wait_ns.load(); }
+
 int sm_count() {
     static int cached[kMaxDevices];
     int dev = 0;

@@ -1,0 +1,267 @@
+// ssm_conv.cu -- the causal convolution of the state space mixer over packed
+// prompts, and the one-token step (convolution, then scan).
+#include "ssm_common.cuh"
+
+namespace gdn {
+
+namespace {
+
+constexpr int kVec = 8;          // channels of a thread
+constexpr int kConvThreads = 128;
+constexpr int kRun = 16;         // tokens of a thread
+
+__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
+    const float4 a = load4f(p), b = load4f(p + 4);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[8]) {
+    const uint4 u = *reinterpret_cast<const uint4 *>(p);
+    const float4 a = bf16x4_f32(make_uint2(u.x, u.y)), b = bf16x4_f32(make_uint2(u.z, u.w));
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
+    store4f(p, make_float4(v[0], v[1], v[2], v[3]));
+    store4f(p + 4, make_float4(v[4], v[5], v[6], v[7]));
+}
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8]) {
+    __nv_bfloat162 h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(h);
+}
+
+// Sequence that holds token t, or -1 (in front of the first or behind the last one).
+__device__ __forceinline__ int seq_of(const int32_t *cu, int n_seqs, long long t) {
+    int lo = 0, hi = n_seqs - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cu[mid] <= t) lo = mid; else hi = mid - 1;
+    }
+    return cu[lo] <= t ? lo : -1;
+}
+
+}  // namespace
+
+// ------------------------------------------------------------- packed prompts
+// out_t[c] = SiLU(bias[c] + sum_j w[c][j] x_{t-3+j}[c]).  A thread owns 8
+// channels of kRun packed tokens and slides the three-token window in
+// registers.  HBM-bound: the input once (three tokens in kRun again, from L2)
+// and the output once.
+//
+// The history is replaced by the same launch: the thread whose run holds a
+// sequence's first token also computes the two tokens behind it (the ones that
+// still reach into the history) wherever they lie, so it alone reads that
+// history and may then overwrite it.  The two tokens' own run leaves them out.
+template <typename TA>
+__global__ void __launch_bounds__(kConvThreads) ssm_conv_kernel(SsmConvArgs a) {
+    const SsmDims &d = a.d;
+    const int c0 = (blockIdx.y * kConvThreads + threadIdx.x) * kVec;
+    if (c0 >= d.ch) return;
+    const TA *x = (const TA *)a.x + c0;
+    TA *out = (TA *)a.out + c0, *hist = (TA *)a.conv_state;
+    const long long r0 = (long long)blockIdx.x * kRun, r1 = r0 + kRun < a.T ? r0 + kRun : a.T;
+    float w[4][kVec], bias[kVec];
+#pragma unroll
+    for (int i = 0; i < kVec / 2; ++i) {
+        float u[8];
+        load8((const TA *)a.w + (long long)c0 * 4 + 8 * i, u);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) { w[j][2 * i] = u[j]; w[j][2 * i + 1] = u[4 + j]; }
+    }
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) bias[i] = 0.f;
+    if (a.bias) load8((const TA *)a.bias + c0, bias);
+
+    // first sequence that has a token at r0 or later
+    int n = seq_of(a.cu, a.n_seqs, r0);
+    if (n < 0) n = 0;
+    for (; n < a.n_seqs; ++n) {
+        long long s, e;
+        seq_bounds(a.cu, n, a.T, a.err, s, e);
+        if (s >= r1) break;
+        if (e <= r0 || e <= s) continue;
+        const int slot = slot_of(a.state_idx, n, d.n_slots, a.err);
+        const bool starts = s >= r0;                   // this run holds its first token
+        const long long head_end = s + 3 < e ? s + 3 : e;
+        long long t = starts ? s : (r0 > head_end ? r0 : head_end);
+        const long long end = (starts && head_end > r1) ? head_end : (e < r1 ? e : r1);
+        if (t >= end && !starts) continue;
+        if (slot < 0) {
+            const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            for (; t < end; ++t) store8(out + t * d.ch, zero);
+            continue;
+        }
+        float win[3][kVec];
+        if (starts) {
+#pragma unroll
+            for (int j = 0; j < 3; ++j)
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) win[j][i] = 0.f;
+            if (hist) {
+                TA *hp = hist + ((long long)slot * d.ch + c0) * 3;
+                float u[3][8];
+#pragma unroll
+                for (int i = 0; i < 3; ++i) load8(hp + 8 * i, u[i]);
+#pragma unroll
+                for (int i = 0; i < kVec; ++i)
+#pragma unroll
+                    for (int j = 0; j < 3; ++j) win[j][i] = u[(3 * i + j) / 8][(3 * i + j) % 8];
+                // the new history: the last three inputs, of the old history where e - s < 3
+                float last[3][kVec];
+#pragma unroll
+                for (int j = 0; j < 3; ++j) {
+                    const long long tt = e - 3 + j;
+                    if (tt >= s) {
+                        load8(x + tt * a.ld_x, last[j]);
+                    } else {
+                        const int k = (int)(tt - s + 3);
+#pragma unroll
+                        for (int i = 0; i < kVec; ++i)
+                            last[j][i] = k == 1 ? win[1][i] : k == 2 ? win[2][i] : win[0][i];
+                    }
+                }
+                float v[3][8];
+#pragma unroll
+                for (int i = 0; i < kVec; ++i)
+#pragma unroll
+                    for (int j = 0; j < 3; ++j) v[(3 * i + j) / 8][(3 * i + j) % 8] = last[j][i];
+#pragma unroll
+                for (int i = 0; i < 3; ++i) store8(hp + 8 * i, v[i]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 3; ++j) load8(x + (t - 3 + j) * a.ld_x, win[j]);
+        }
+        for (; t < end; ++t) {
+            float cur[kVec], o[kVec];
+            load8(x + t * a.ld_x, cur);
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) {
+                o[i] = silu_f(fmaf(w[3][i], cur[i],
+                                   fmaf(w[2][i], win[2][i],
+                                        fmaf(w[1][i], win[1][i], fmaf(w[0][i], win[0][i], bias[i])))));
+                win[0][i] = win[1][i];
+                win[1][i] = win[2][i];
+                win[2][i] = cur[i];
+            }
+            store8(out + t * d.ch, o);
+        }
+    }
+}
+
+cudaError_t launch_ssm_conv(const SsmConvArgs &a, bool act_bf16, cudaStream_t s) {
+    const dim3 grid((unsigned)((a.T + kRun - 1) / kRun),
+                    (unsigned)((a.d.ch / kVec + kConvThreads - 1) / kConvThreads));
+    if (act_bf16) ssm_conv_kernel<__nv_bfloat16><<<grid, kConvThreads, 0, s>>>(a);
+    else ssm_conv_kernel<float><<<grid, kConvThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------ one token
+// Convolution step: one thread per channel; the history is shifted in place by
+// its only reader and the fp32 result goes to the workspace.
+template <typename TA>
+__global__ void __launch_bounds__(256) ssm_step_conv_kernel(SsmStepArgs a) {
+    const SsmDims &d = a.d;
+    const int n = blockIdx.y, c = blockIdx.x * 256 + threadIdx.x;
+    if (c >= d.ch) return;
+    const int slot = slot_of(a.state_idx, n, d.n_slots, a.err);
+    if (slot < 0) return;
+    TA *hp = (TA *)a.conv_state + ((long long)slot * d.ch + c) * 3;
+    const TA h0 = hp[0], h1 = hp[1], h2 = hp[2], cur = ((const TA *)a.x)[(long long)n * a.ld_x + c];
+    float w[4];
+    taps_f32(load_taps((const TA *)a.w, c), w);
+    const float b = a.bias ? to_f32(((const TA *)a.bias)[c]) : 0.f;
+    hp[0] = h1; hp[1] = h2; hp[2] = cur;
+    a.ws[(long long)n * d.ch + c] =
+        silu_f(fmaf(w[3], to_f32(cur), fmaf(w[2], to_f32(h2), fmaf(w[1], to_f32(h1), fmaf(w[0], to_f32(h0), b)))));
+}
+
+// State step: one CTA per (head, sequence) reads the head's state once, writes
+// it once and reduces y over the rows.  HBM-bound on the state.
+template <int N, int P, typename TA>
+__global__ void __launch_bounds__(256) ssm_step_state_kernel(SsmStepArgs a) {
+    constexpr int LP = P / 4, NT = N * LP < 256 ? N * LP : 256, NS = NT / LP, RPT = N / NS;
+    __shared__ __align__(16) float part[NS][P];
+    const SsmDims &d = a.d;
+    const int h = blockIdx.x, n = blockIdx.y, g = h / d.per, tid = threadIdx.x;
+    const int p0 = (tid % LP) * 4, ns = tid / LP;
+    const int slot = slot_of(a.state_idx, n, d.n_slots, a.err);
+    TA *y = (TA *)a.y + ((long long)n * d.heads + h) * P;
+    if (slot < 0) {
+        if (tid < LP) store4f(y + p0, make_float4(0.f, 0.f, 0.f, 0.f));
+        return;
+    }
+    float *S = a.state + ((long long)slot * d.heads + h) * N * P;
+    float4 m[RPT];
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) m[i] = load4f(S + (long long)(ns + i * NS) * P + p0);
+    const float *row = a.ws + (long long)n * d.ch;
+    const float *B = row + d.heads * P + g * N, *C = B + d.groups * N;
+    const float dt = ssm_dt(to_f32(((const TA *)a.dt)[(long long)n * a.ld_dt + h]),
+                            a.dt_bias ? a.dt_bias[h] : 0.f, d);
+    const float dec = expf(-expf(a.A_log[h]) * dt);
+    const float4 x = load4f(row + h * P + p0);
+    const float4 u = make_float4(dt * x.x, dt * x.y, dt * x.z, dt * x.w);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+        const int k = ns + i * NS;
+        const float b = B[k], c = C[k];
+        m[i].x = fmaf(dec, m[i].x, b * u.x); m[i].y = fmaf(dec, m[i].y, b * u.y);
+        m[i].z = fmaf(dec, m[i].z, b * u.z); m[i].w = fmaf(dec, m[i].w, b * u.w);
+        acc.x = fmaf(c, m[i].x, acc.x); acc.y = fmaf(c, m[i].y, acc.y);
+        acc.z = fmaf(c, m[i].z, acc.z); acc.w = fmaf(c, m[i].w, acc.w);
+        store4f(S + (long long)k * P + p0, m[i]);
+    }
+    store4f(&part[ns][p0], acc);
+    __syncthreads();
+    if (tid < LP) {
+        float4 o = load4f(&part[0][p0]);
+#pragma unroll
+        for (int k = 1; k < NS; ++k) {
+            const float4 q = load4f(&part[k][p0]);
+            o.x += q.x; o.y += q.y; o.z += q.z; o.w += q.w;
+        }
+        const float skip = a.D ? a.D[h] : 0.f;
+        o.x = fmaf(skip, x.x, o.x); o.y = fmaf(skip, x.y, o.y);
+        o.z = fmaf(skip, x.z, o.z); o.w = fmaf(skip, x.w, o.w);
+        if (a.z) {
+            const float4 z = load4f((const TA *)a.z + (long long)n * a.ld_z + (long long)h * P + p0);
+            o.x *= silu_f(z.x); o.y *= silu_f(z.y); o.z *= silu_f(z.z); o.w *= silu_f(z.w);
+        }
+        store4f(y + p0, o);
+    }
+}
+
+size_t ssm_step_ws_bytes(const SsmDims &d, long long n) { return (size_t)n * d.ch * 4; }
+
+namespace {
+template <int N, int P, typename TA> cudaError_t run_step(const SsmStepArgs &a, cudaStream_t s) {
+    ssm_step_conv_kernel<TA><<<dim3((a.d.ch + 255) / 256, a.n), 256, 0, s>>>(a);
+    constexpr int NT = N * P / 4 < 256 ? N * P / 4 : 256;
+    ssm_step_state_kernel<N, P, TA><<<dim3(a.d.heads, a.n), NT, 0, s>>>(a);
+    return cudaGetLastError();
+}
+template <int N, typename TA> cudaError_t run_step_p(const SsmStepArgs &a, cudaStream_t s) {
+    switch (a.d.P) {
+        case 32: return run_step<N, 32, TA>(a, s);
+        case 64: return run_step<N, 64, TA>(a, s);
+        default: return run_step<N, 128, TA>(a, s);
+    }
+}
+template <typename TA> cudaError_t run_step_np(const SsmStepArgs &a, cudaStream_t s) {
+    switch (a.d.N) {
+        case 16: return run_step_p<16, TA>(a, s);
+        case 32: return run_step_p<32, TA>(a, s);
+        case 64: return run_step_p<64, TA>(a, s);
+        default: return run_step_p<128, TA>(a, s);
+    }
+}
+}  // namespace
+
+cudaError_t launch_ssm_step(const SsmStepArgs &a, bool act_bf16, cudaStream_t s) {
+    return act_bf16 ? run_step_np<__nv_bfloat16>(a, s) : run_step_np<float>(a, s);
+}
+
+}  // namespace gdn

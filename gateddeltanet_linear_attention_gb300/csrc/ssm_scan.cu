@@ -1,0 +1,408 @@
+// ssm_scan.cu -- the selective state space scan over packed prompts: the fp32
+// kernel that serves every size and type, and the cutting of long sequences
+// into segments that run side by side.
+//
+// Per head (B, C of its group), with a_t = exp(A dt_t), A = -exp(A_log):
+//   S_t[n][p] = a_t S_{t-1}[n][p] + dt_t B_t[n] x_t[p]
+//   y_t[p]    = (sum_n C_t[n] S_t[n][p] + D x_t[p]) SiLU(z_t[p])
+//
+// Segments: the map from a segment's entering state to its leaving one is
+// S -> exp(sum of its log-decays) S + E, E being the leaving state from zero.
+// So a first pass computes every segment's E and summed log-decay at once, a
+// short second one chains them, and the last one runs all segments with
+// outputs, each from the state that enters it.
+#include "ssm_common.cuh"
+
+namespace gdn {
+
+namespace {
+
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// Two packed fp32 values: one instruction for two multiply-adds.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(f32x2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+}  // namespace
+
+// ------------------------------------------------------------- segment map
+// seg_base and enter_base: exclusive scans over the sequences of their segments
+// (one at least) and of the entering states that are kept (none for a sequence
+// of one segment).  Sequences whose entries would not fit (lengths that sum to
+// more than T: malformed cu_seqlens) get no segment and are reported.
+__global__ void __launch_bounds__(1024) ssm_segment_map_kernel(SsmScanArgs a) {
+    __shared__ long long ws_seg[32], ws_ent[32];   // 64 bits: malformed lengths may sum to any size
+    __shared__ long long run_seg, run_ent;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const long long max_seg = (long long)a.n_seqs + a.max_enter, max_ent = a.max_enter;
+    if (tid == 0) run_seg = run_ent = 0;
+    __syncthreads();
+    for (int n0 = 0; n0 < a.n_seqs; n0 += 1024) {
+        const int n = n0 + tid;
+        long long seg = 0, ent = 0;
+        if (n < a.n_seqs) {
+            long long s, e;
+            seq_bounds(a.cu, n, a.T, a.err, s, e);
+            seg = e > s ? (e - s + a.seg_len - 1) / a.seg_len : 1;
+            ent = seg > 1 ? seg : 0;
+        }
+        auto scan = [&](long long v) {
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long u = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += u;
+            }
+            return v;
+        };
+        const long long is = scan(seg), ie = scan(ent);
+        if (lane == 31) { ws_seg[warp] = is; ws_ent[warp] = ie; }
+        __syncthreads();
+        if (warp == 0) {
+            const long long vs = scan(ws_seg[lane]), ve = scan(ws_ent[lane]);
+            ws_seg[lane] = vs;
+            ws_ent[lane] = ve;
+        }
+        __syncthreads();
+        const long long bs = run_seg + (warp ? ws_seg[warp - 1] : 0) + is - seg;
+        const long long be = run_ent + (warp ? ws_ent[warp - 1] : 0) + ie - ent;
+        if (n < a.n_seqs) {
+            if (be + ent > max_ent) set_error(a.err, GDN_DEVERR_CU_SEQLENS);
+            a.seg_base[n] = (int)(bs < max_seg ? bs : max_seg);
+            a.enter_base[n] = (int)(be < max_ent ? be : max_ent);
+        }
+        __syncthreads();
+        if (tid == 0) {
+            run_seg += ws_seg[31];
+            run_ent += ws_ent[31];
+        }
+        __syncthreads();
+    }
+    if (tid == 0) {
+        a.seg_base[a.n_seqs] = (int)(run_seg < max_seg ? run_seg : max_seg);
+        a.enter_base[a.n_seqs] = (int)(run_ent < max_ent ? run_ent : max_ent);
+    }
+}
+
+// ------------------------------------------------------------ chained states
+// enter[0] = the initial state, enter[k+1] = exp(log-decay of segment k) *
+// enter[k] + (what pass 1 left in enter[k+1]); one thread per float4 of a head.
+__global__ void __launch_bounds__(256) ssm_chain_states_kernel(SsmScanArgs a) {
+    const int h = blockIdx.x, vec = a.d.N * a.d.P / 4;
+    const int i = blockIdx.y * 256 + threadIdx.x;
+    if (i >= vec) return;
+    const long long head = (long long)a.d.N * a.d.P, all = head * a.d.heads;
+    for (int n = blockIdx.z; n < a.n_seqs; n += gridDim.z) {
+        const int e0 = a.enter_base[n];
+        int e1 = a.enter_base[n + 1];
+        const int segs = a.seg_base[n + 1] - a.seg_base[n];
+        if (e1 - e0 < 2 || segs < 2) continue;
+        const int slot = slot_of(a.state_idx, n, a.d.n_slots, a.err);
+        if (slot < 0) continue;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (a.state_in) v = load4f(a.state_in + (long long)slot * all + h * head + 4 * i);
+        store4f(a.enter + (long long)e0 * all + h * head + 4 * i, v);
+        for (int e = e0 + 1; e < e1; ++e) {
+            float *at = a.enter + (long long)e * all + h * head + 4 * i;
+            const float4 u = load4f(at);
+            const float k = expf(a.seg_log[(long long)(e - 1) * a.d.heads + h]);
+            v = make_float4(fmaf(k, v.x, u.x), fmaf(k, v.y, u.y), fmaf(k, v.z, u.z), fmaf(k, v.w, u.w));
+            store4f(at, v);
+        }
+    }
+}
+
+// ----------------------------------------------------------------- the scan
+// One CTA walks the tokens of one (segment, head) with the head's N x P fp32
+// state in registers: a thread owns 4 columns p and NPT rows n, packed in pairs
+// of n so that one packed multiply-add serves two state elements.  Tokens come
+// in blocks of TB through shared memory, the next block's loads in flight
+// while this one is computed; the row slices' parts of y are summed per block.
+// FP32-bound: 3 packed operations per two state elements and token.
+// STATES: pass 1, no outputs: the leaving state from zero and the log-decay.
+template <int N, int P> struct ScanShape {
+    static constexpr int NPT = N * P / 128 >= 16 ? 16 : N * P / 128;   // rows of a thread
+    static constexpr int LP = P / 4;                                   // threads across the columns
+    static constexpr int NS = N / NPT;                                 // row slices
+    static constexpr int NT = LP * NS;
+    static constexpr int TB = 8;
+    static constexpr int ROW = P + 2 * N;                              // x | B | C of a token
+    static constexpr int VPT = (TB * ROW / 4 + NT - 1) / NT;           // vectors of a thread
+};
+template <typename TA> struct Vec4Of { using type = float4; };
+template <> struct Vec4Of<__nv_bfloat16> { using type = uint2; };
+__device__ __forceinline__ float4 vec4_f32(float4 v) { return v; }
+__device__ __forceinline__ float4 vec4_f32(uint2 v) { return bf16x4_f32(v); }
+
+template <int N, int P, typename TA, bool STATES>
+__global__ void __launch_bounds__(ScanShape<N, P>::NT) ssm_scan_kernel(SsmScanArgs a) {
+    using Sh = ScanShape<N, P>;
+    using V4 = typename Vec4Of<TA>::type;
+    constexpr int NPT = Sh::NPT, LP = Sh::LP, NS = Sh::NS, NT = Sh::NT, TB = Sh::TB, ROW = Sh::ROW,
+                  VPT = Sh::VPT;
+    __shared__ __align__(16) float tok[TB][ROW];
+    __shared__ __align__(16) float part[STATES ? 1 : TB][NS][P];
+    __shared__ float s_dt[TB], s_g[TB], s_a[TB];
+    const SsmDims &d = a.d;
+    const int tid = threadIdx.x, h = blockIdx.x % d.heads, g = h / d.per;
+    SsmSegment sg;
+    if (!ssm_segment(a, blockIdx.x / d.heads, sg)) return;
+    if (STATES && (sg.last || sg.slot < 0)) return;
+    const long long out_cols = (long long)d.heads * P;
+    if (sg.slot < 0) {
+        TA *y = (TA *)a.y;
+        for (long long i = tid; i < (sg.t1 - sg.t0) * LP; i += NT)
+            store4f(y + (sg.t0 + i / LP) * out_cols + (long long)h * P + (i % LP) * 4,
+                    make_float4(0.f, 0.f, 0.f, 0.f));
+        return;
+    }
+    const int lp = tid % LP, ns = tid / LP, p0 = lp * 4, n0 = ns * NPT;
+    const long long head = (long long)N * P, all = head * d.heads;
+    f32x2 S[NPT / 2][4];
+    {
+        const float *from = nullptr;
+        if (!STATES) {
+            if (sg.entry >= 0) from = a.enter + (long long)sg.entry * all;
+            else if (a.state_in) from = a.state_in + (long long)sg.slot * all;
+        }
+#pragma unroll
+        for (int i = 0; i < NPT / 2; ++i) {
+            float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
+            if (from) {
+                u = load4f(from + h * head + (long long)(n0 + 2 * i) * P + p0);
+                v = load4f(from + h * head + (long long)(n0 + 2 * i + 1) * P + p0);
+            }
+            S[i][0] = pack2(u.x, v.x); S[i][1] = pack2(u.y, v.y);
+            S[i][2] = pack2(u.z, v.z); S[i][3] = pack2(u.w, v.w);
+        }
+    }
+    const float rate = -expf(a.A_log[h]), bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+    const float skip = a.D ? a.D[h] : 0.f;
+    double log_sum = 0.0;
+    V4 raw[VPT];
+    float raw_dt = 0.f;
+    auto fetch = [&](long long t0) {          // the block at t0 into registers
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = i * NT + tid, r = v / (ROW / 4), c = (v % (ROW / 4)) * 4;
+            const long long t = t0 + r;
+            if (r < TB && t < sg.t1) {
+                const TA *src;
+                if (c < P) src = (const TA *)a.x + t * a.ld_x + (long long)h * P + c;
+                else if (c < P + N) src = (const TA *)a.b + t * a.ld_bc + (long long)g * N + (c - P);
+                else src = (const TA *)a.c + t * a.ld_bc + (long long)g * N + (c - P - N);
+                raw[i] = *reinterpret_cast<const V4 *>(src);
+            }
+        }
+        if (tid < TB && t0 + tid < sg.t1)
+            raw_dt = to_f32(((const TA *)a.dt)[(t0 + tid) * a.ld_dt + h]);
+    };
+    fetch(sg.t0);
+    for (long long tb = sg.t0; tb < sg.t1; tb += TB) {
+        const int count = (int)(sg.t1 - tb < TB ? sg.t1 - tb : TB);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = i * NT + tid, r = v / (ROW / 4), c = (v % (ROW / 4)) * 4;
+            if (r < count) store4f(&tok[r][c], vec4_f32(raw[i]));
+        }
+        if (tid < count) {
+            const float dt = ssm_dt(raw_dt, bias, d);
+            s_dt[tid] = dt;
+            s_g[tid] = rate * dt;
+            s_a[tid] = expf(rate * dt);
+        }
+        __syncthreads();
+        if (tb + TB < sg.t1) fetch(tb + TB);
+        if (STATES) {
+            float sum = 0.f;
+            for (int r = 0; r < count; ++r) sum += s_g[r];
+            log_sum += (double)sum;
+        }
+        for (int r = 0; r < count; ++r) {
+            const float4 x = load4f(&tok[r][p0]);
+            const float dt = s_dt[r], dec = s_a[r];
+            const f32x2 a2 = pack2(dec, dec);
+            const f32x2 x2[4] = {pack2(dt * x.x, dt * x.x), pack2(dt * x.y, dt * x.y),
+                                 pack2(dt * x.z, dt * x.z), pack2(dt * x.w, dt * x.w)};
+            f32x2 acc[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+            for (int i = 0; i < NPT / 2; i += 2) {
+                const ulonglong2 B = *reinterpret_cast<const ulonglong2 *>(&tok[r][P + n0 + 2 * i]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    S[i][j] = fma2(a2, S[i][j], mul2(B.x, x2[j]));
+                    S[i + 1][j] = fma2(a2, S[i + 1][j], mul2(B.y, x2[j]));
+                }
+                if (!STATES) {
+                    const ulonglong2 C =
+                        *reinterpret_cast<const ulonglong2 *>(&tok[r][P + N + n0 + 2 * i]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        acc[j] = fma2(S[i][j], C.x, acc[j]);
+                        acc[j] = fma2(S[i + 1][j], C.y, acc[j]);
+                    }
+                }
+            }
+            if (!STATES) {
+                float4 o;
+                float2 q;
+                q = unpack2(acc[0]); o.x = q.x + q.y;
+                q = unpack2(acc[1]); o.y = q.x + q.y;
+                q = unpack2(acc[2]); o.z = q.x + q.y;
+                q = unpack2(acc[3]); o.w = q.x + q.y;
+                store4f(&part[r][ns][p0], o);
+            }
+        }
+        __syncthreads();
+        if (!STATES) {
+            TA *y = (TA *)a.y;
+            for (int i = tid; i < count * LP; i += NT) {
+                const int r = i / LP, c = (i % LP) * 4;
+                const long long t = tb + r;
+                float4 o = load4f(&part[r][0][c]);
+#pragma unroll
+                for (int k = 1; k < NS; ++k) {
+                    const float4 q = load4f(&part[r][k][c]);
+                    o.x += q.x; o.y += q.y; o.z += q.z; o.w += q.w;
+                }
+                const float4 x = load4f(&tok[r][c]);
+                o.x = fmaf(skip, x.x, o.x); o.y = fmaf(skip, x.y, o.y);
+                o.z = fmaf(skip, x.z, o.z); o.w = fmaf(skip, x.w, o.w);
+                if (a.z) {
+                    const float4 z = load4f((const TA *)a.z + t * a.ld_z + (long long)h * P + c);
+                    o.x *= silu_f(z.x); o.y *= silu_f(z.y); o.z *= silu_f(z.z); o.w *= silu_f(z.w);
+                }
+                store4f(y + t * out_cols + (long long)h * P + c, o);
+            }
+            __syncthreads();
+        }
+    }
+    float *to = nullptr;
+    if (STATES) to = a.enter + (long long)(sg.entry + 1) * all;
+    else if (sg.last && a.state_out) to = a.state_out + (long long)sg.slot * all;
+    if (to) {
+#pragma unroll
+        for (int i = 0; i < NPT / 2; ++i) {
+            const float2 q0 = unpack2(S[i][0]), q1 = unpack2(S[i][1]), q2 = unpack2(S[i][2]),
+                         q3 = unpack2(S[i][3]);
+            store4f(to + h * head + (long long)(n0 + 2 * i) * P + p0, make_float4(q0.x, q1.x, q2.x, q3.x));
+            store4f(to + h * head + (long long)(n0 + 2 * i + 1) * P + p0,
+                    make_float4(q0.y, q1.y, q2.y, q3.y));
+        }
+    }
+    if (STATES && tid == 0) a.seg_log[(long long)sg.entry * d.heads + h] = (float)log_sum;
+}
+
+// ---------------------------------------------------------------- launching
+namespace {
+
+// Tokens of a segment: enough CTAs to fill the GPU about twice over (`slots`
+// resident (segment, head) walks), a multiple of 128, at least 256 tokens.
+// A batch whose sequences fill it by themselves is then not cut.
+long long segment_len(const SsmDims &d, long long T, int slots) {
+    const long long want = (T * d.heads + slots - 1) / slots;
+    long long len = (want + 127) / 128 * 128;
+    return len < 256 ? 256 : len;
+}
+
+int scan_slots(const SsmDims &d) {
+    // resident CTAs: the state takes one register in four of an SM's file at 128 x 128
+    const int per_sm = d.N * d.P >= 16384 ? 2 : d.N * d.P >= 8192 ? 4 : 8;
+    return sm_count() * per_sm;
+}
+
+// Sequences of k >= 2 segments keep k entering states, and have more than
+// (k - 1) seg_len tokens.
+long long max_entries(long long T, long long seg_len) { return seg_len >= T ? 0 : 2 * (T / seg_len); }
+
+struct ScanWs {
+    size_t seg, ent, log, enter, size;
+};
+ScanWs scan_ws(const SsmDims &d, long long entries, long long n_seqs) {
+    ScanWs w{};
+    if (entries == 0) return w;
+    size_t at = 0;
+    w.seg = at; at += align256((size_t)(n_seqs + 1) * 4);
+    w.ent = at; at += align256((size_t)(n_seqs + 1) * 4);
+    w.log = at; at += align256((size_t)entries * d.heads * 4);
+    w.enter = at; at += (size_t)entries * d.heads * d.N * d.P * 4;
+    w.size = at;
+    return w;
+}
+
+template <int N, int P, typename TA>
+cudaError_t run_scan(const SsmScanArgs &a, cudaStream_t s) {
+    constexpr int NT = ScanShape<N, P>::NT;
+    const bool cut = a.seg_len < a.T;
+    const unsigned segs = cut ? (unsigned)(a.n_seqs + a.max_enter) : (unsigned)a.n_seqs;
+    const dim3 grid(a.d.heads * segs);     // the heads of a group side by side: B and C come from L2
+    if (cut) {
+        ssm_segment_map_kernel<<<1, 1024, 0, s>>>(a);
+        ssm_scan_kernel<N, P, TA, true><<<grid, NT, 0, s>>>(a);
+        const dim3 chain(a.d.heads, (N * P / 4 + 255) / 256, a.n_seqs < 32 ? a.n_seqs : 32);
+        ssm_chain_states_kernel<<<chain, 256, 0, s>>>(a);
+    }
+    ssm_scan_kernel<N, P, TA, false><<<grid, NT, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <int N, typename TA> cudaError_t run_scan_p(const SsmScanArgs &a, cudaStream_t s) {
+    switch (a.d.P) {
+        case 32: return run_scan<N, 32, TA>(a, s);
+        case 64: return run_scan<N, 64, TA>(a, s);
+        default: return run_scan<N, 128, TA>(a, s);
+    }
+}
+template <typename TA> cudaError_t run_scan_np(const SsmScanArgs &a, cudaStream_t s) {
+    switch (a.d.N) {
+        case 16: return run_scan_p<16, TA>(a, s);
+        case 32: return run_scan_p<32, TA>(a, s);
+        case 64: return run_scan_p<64, TA>(a, s);
+        default: return run_scan_p<128, TA>(a, s);
+    }
+}
+
+}  // namespace
+
+// Grows with T: segments are 256 tokens or longer, and no more than `slots` of them per batch.
+size_t ssm_scan_ws_bytes(const SsmDims &d, bool, long long T, long long n_seqs) {
+    const long long most = scan_slots(d) / d.heads;
+    return scan_ws(d, 2 * (T / 256 < most ? T / 256 : most), n_seqs).size;
+}
+
+size_t ssm_scan_carve(SsmScanArgs &a, bool, void *ws) {
+    a.seg_len = segment_len(a.d, a.T, scan_slots(a.d));
+    a.max_enter = (int)max_entries(a.T, a.seg_len);
+    const ScanWs w = scan_ws(a.d, a.max_enter, a.n_seqs);
+    char *p = (char *)ws;
+    if (w.size == 0 || !p) return w.size;
+    a.seg_base = (int *)(p + w.seg);
+    a.enter_base = (int *)(p + w.ent);
+    a.seg_log = (float *)(p + w.log);
+    a.enter = (float *)(p + w.enter);
+    return w.size;
+}
+
+cudaError_t launch_ssm_scan(const SsmScanArgs &a, bool act_bf16, cudaStream_t s) {
+    return act_bf16 ? run_scan_np<__nv_bfloat16>(a, s) : run_scan_np<float>(a, s);
+}
+
+}  // namespace gdn

@@ -48,6 +48,43 @@ class MixerIO(ctypes.Structure):
                 ("y", ctypes.c_void_p), ("y_dtype", ctypes.c_int32)]
 
 
+class SSMConfig(ctypes.Structure):
+    _fields_ = [("groups", ctypes.c_int32), ("heads", ctypes.c_int32), ("d_state", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("act", ctypes.c_int32), ("n_slots", ctypes.c_int32),
+                ("dt_min", ctypes.c_float), ("dt_max", ctypes.c_float)]
+
+
+class SSMIO(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("ld_x", ctypes.c_int64), ("b", ctypes.c_void_p),
+                ("c", ctypes.c_void_p), ("ld_bc", ctypes.c_int64), ("dt", ctypes.c_void_p),
+                ("ld_dt", ctypes.c_int64), ("z", ctypes.c_void_p), ("ld_z", ctypes.c_int64),
+                ("A_log", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p), ("D", ctypes.c_void_p),
+                ("conv_w", ctypes.c_void_p), ("conv_bias", ctypes.c_void_p),
+                ("cu_seqlens", ctypes.c_void_p), ("n_seqs", ctypes.c_int32), ("T", ctypes.c_int64),
+                ("state_idx", ctypes.c_void_p), ("state_in", ctypes.c_void_p),
+                ("state_out", ctypes.c_void_p), ("conv_state", ctypes.c_void_p),
+                ("y", ctypes.c_void_p)]
+
+
+class BlockNormIO(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("dim", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("res", ctypes.c_int32), ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float),
+                ("res_scale", ctypes.c_float),
+                ("block", ctypes.c_void_p), ("ld_block", ctypes.c_int64),
+                ("gate", ctypes.c_void_p), ("ld_gate", ctypes.c_int64), ("gate_cols", ctypes.c_int32),
+                ("residual", ctypes.c_void_p), ("ld_residual", ctypes.c_int64),
+                ("w_post", ctypes.c_void_p), ("w_pre", ctypes.c_void_p),
+                ("res_out", ctypes.c_void_p), ("ld_res_out", ctypes.c_int64),
+                ("h", ctypes.c_void_p), ("ld_h", ctypes.c_int64),
+                ("rstd_post", ctypes.c_void_p), ("rstd_pre", ctypes.c_void_p),
+                ("dh", ctypes.c_void_p), ("ld_dh", ctypes.c_int64),
+                ("d_res_out", ctypes.c_void_p), ("ld_d_res_out", ctypes.c_int64),
+                ("d_residual", ctypes.c_void_p), ("ld_d_residual", ctypes.c_int64),
+                ("d_block", ctypes.c_void_p), ("ld_d_block", ctypes.c_int64),
+                ("d_gate", ctypes.c_void_p), ("ld_d_gate", ctypes.c_int64),
+                ("dw_post", ctypes.c_void_p), ("dw_pre", ctypes.c_void_p)]
+
+
 _lib = None
 _lock = threading.Lock()
 LIB_PATH = build_lib.LIB
@@ -97,6 +134,14 @@ def load(path: str | None = None):
             "gdn_chunk_states": ([CP, P, I64, P, I64, I32, P, P, P, I32, I64, P, P, P, P, P, SZ, V], I32),
             "gdn_chunk_backward": ([CP, P, P, I64, P, I64, I32, P, P, P, I32, I64, P, P, P, P, P, P, P,
                                     I64, P, P, P, P, P, SZ, V], I32),
+            "gdn_ssm_workspace_size": ([ctypes.POINTER(SSMConfig), I64, I32], SZ),
+            "gdn_ssm_conv_prefill": ([ctypes.POINTER(SSMConfig), P, I64, P, I32, I64, P, P, P, P, P, V],
+                                     I32),
+            "gdn_ssm_prefill": ([ctypes.POINTER(SSMConfig), ctypes.POINTER(SSMIO), P, SZ, V], I32),
+            "gdn_ssm_decode": ([ctypes.POINTER(SSMConfig), ctypes.POINTER(SSMIO), P, SZ, V], I32),
+            "gdn_block_norm": ([ctypes.POINTER(BlockNormIO), V], I32),
+            "gdn_block_norm_workspace_size": ([I64, I32], SZ),
+            "gdn_block_norm_backward": ([ctypes.POINTER(BlockNormIO), P, SZ, V], I32),
             "gdn_device_error": ([V, ctypes.POINTER(U32)], I32),
             "gdn_debug_set_wait": ([ctypes.c_uint64, U32], I32),
             "gdn_status_string": ([I32], ctypes.c_char_p),
@@ -341,6 +386,187 @@ def gdn_state_copy(cfg, src_state, src_conv, dst_state, dst_conv, src_idx, dst_i
                                  slots(src_state, src_conv), _ptr(dst_state), _ptr(dst_conv),
                                  slots(dst_state, dst_conv), _ptr(src_idx), _ptr(dst_idx), n,
                                  _stream(stream)), "gdn_state_copy")
+
+
+# ------------------------------------- selective state space mixer, block norms
+
+def make_ssm_config(groups, heads, d_state, head_dim, act="bf16", n_slots=0, dt_min=0.0,
+                    dt_max=float("inf")) -> SSMConfig:
+    return SSMConfig(groups, heads, d_state, head_dim, GDN_BF16 if act == "bf16" else GDN_FP32,
+                     n_slots, dt_min, dt_max)
+
+
+class _Args:
+    """Checks of one call's tensors: all on the current device, of the expected type and shape."""
+
+    def __init__(self, where, act=None):
+        import torch
+        self.where, self.device = where, torch.cuda.current_device()
+        self.f32, self.i32 = torch.float32, torch.int32
+        self.act = None if act is None else torch.bfloat16 if act == GDN_BF16 else torch.float32
+
+    def refuse(self, name, what):
+        raise ValueError("%s: %s %s" % (self.where, name, what))
+
+    def on_device(self, t, name, dtype):
+        if t.dtype != dtype:
+            self.refuse(name, "is %s, not %s" % (t.dtype, dtype))
+        if t.get_device() != self.device:
+            self.refuse(name, "is on %s, not on the current device cuda:%d" % (t.device, self.device))
+
+    def view(self, t, name, rows, cols, dtype):
+        """(pointer, row stride) of a [rows][cols] view with contiguous rows."""
+        if t is None:
+            return None, 0
+        self.on_device(t, name, dtype)
+        if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+            self.refuse(name, "has shape %s, not %s" % (tuple(t.shape), (rows, cols)))
+        if cols > 1 and t.stride(1) != 1:
+            self.refuse(name, "has rows that are not contiguous")
+        ld = t.stride(0) if rows > 1 else max(cols, t.stride(0))
+        if ld < cols:
+            self.refuse(name, "has rows that overlap")
+        return t.data_ptr(), ld
+
+    def whole(self, t, name, shape, dtype):
+        """Pointer of a contiguous tensor; None in `shape`: any size."""
+        if t is None:
+            return None
+        self.on_device(t, name, dtype)
+        if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+            self.refuse(name, "has shape %s, not %s" % (tuple(t.shape), tuple(shape)))
+        if not t.is_contiguous():
+            self.refuse(name, "is not contiguous")
+        return t.data_ptr()
+
+    def pool(self, t, name, n_slots, shape, dtype):
+        p = self.whole(t, name, (None,) + shape, dtype)
+        if t is not None and t.shape[0] < n_slots:
+            self.refuse(name, "has %d slots, and the configuration %d" % (t.shape[0], n_slots))
+        return p
+
+    def bytes_of(self, t):
+        if t is None:
+            return None, 0
+        if t.get_device() != self.device or not t.is_contiguous():
+            self.refuse("workspace", "is not a contiguous tensor on the current device")
+        return t.data_ptr(), t.numel() * t.element_size()
+
+
+def gdn_ssm_workspace_size(cfg, max_tokens, max_seqs) -> int:
+    return load().gdn_ssm_workspace_size(ctypes.byref(cfg), max_tokens, max_seqs)
+
+
+def gdn_ssm_conv_prefill(cfg, x, cu_seqlens, w, bias, conv_state, state_idx, out, stream=None):
+    """x [T, CH] raw channels -> out [T, CH]; bias, conv_state and state_idx may be None."""
+    a = _Args("gdn_ssm_conv_prefill", cfg.act)
+    CH = cfg.heads * cfg.head_dim + 2 * cfg.groups * cfg.d_state
+    T, n = x.shape[0], cu_seqlens.shape[0] - 1
+    px, ld_x = a.view(x, "x", T, CH, a.act)
+    _check(load().gdn_ssm_conv_prefill(
+        ctypes.byref(cfg), px, ld_x, a.whole(cu_seqlens, "cu_seqlens", (n + 1,), a.i32), n, T,
+        a.whole(w, "w", (CH, 4), a.act), a.whole(bias, "bias", (CH,), a.act),
+        a.pool(conv_state, "conv_state", cfg.n_slots, (CH, 3), a.act),
+        a.whole(state_idx, "state_idx", (n,), a.i32), a.whole(out, "out", (T, CH), a.act),
+        _stream(stream)), "gdn_ssm_conv_prefill")
+
+
+def gdn_ssm_prefill(cfg, x, b, c, dt, A_log, cu_seqlens, y, D=None, dt_bias=None, z=None, state_in=None,
+                    state_out=None, state_idx=None, workspace=None, stream=None):
+    """x [T, heads*head_dim], b and c [T, groups*d_state] (one row stride), dt [T, heads] -> y."""
+    a = _Args("gdn_ssm_prefill", cfg.act)
+    H, N, P, T, n = cfg.heads, cfg.d_state, cfg.head_dim, x.shape[0], cu_seqlens.shape[0] - 1
+    px, ld_x = a.view(x, "x", T, H * P, a.act)
+    pb, ld_bc = a.view(b, "b", T, cfg.groups * N, a.act)
+    pc, ld_c = a.view(c, "c", T, cfg.groups * N, a.act)
+    if T > 1 and ld_c != ld_bc:
+        a.refuse("c", "has another row stride than b")
+    pdt, ld_dt = a.view(dt, "dt", T, H, a.act)
+    pz, ld_z = a.view(z, "z", T, H * P, a.act)
+    io = SSMIO(px, ld_x, pb, pc, ld_bc, pdt, ld_dt, pz, ld_z, a.whole(A_log, "A_log", (H,), a.f32),
+               a.whole(dt_bias, "dt_bias", (H,), a.f32), a.whole(D, "D", (H,), a.f32), None, None,
+               a.whole(cu_seqlens, "cu_seqlens", (n + 1,), a.i32), n, T,
+               a.whole(state_idx, "state_idx", (n,), a.i32),
+               a.pool(state_in, "state_in", cfg.n_slots, (H, N, P), a.f32),
+               a.pool(state_out, "state_out", cfg.n_slots, (H, N, P), a.f32), None,
+               a.whole(y, "y", (T, H * P), a.act))
+    ws, ws_bytes = a.bytes_of(workspace)
+    _check(load().gdn_ssm_prefill(ctypes.byref(cfg), ctypes.byref(io), ws, ws_bytes, _stream(stream)),
+           "gdn_ssm_prefill")
+
+
+def gdn_ssm_decode(cfg, x, dt, conv_w, conv_state, A_log, state, y, workspace, conv_bias=None, D=None,
+                   dt_bias=None, z=None, state_idx=None, stream=None):
+    """One token per sequence: x [n, CH] raw channels, dt [n, heads] -> y [n, heads*head_dim];
+    conv_state and state are updated in place."""
+    a = _Args("gdn_ssm_decode", cfg.act)
+    H, N, P, n = cfg.heads, cfg.d_state, cfg.head_dim, x.shape[0]
+    CH = H * P + 2 * cfg.groups * N
+    px, ld_x = a.view(x, "x", n, CH, a.act)
+    pdt, ld_dt = a.view(dt, "dt", n, H, a.act)
+    pz, ld_z = a.view(z, "z", n, H * P, a.act)
+    ps = a.pool(state, "state", cfg.n_slots, (H, N, P), a.f32)
+    io = SSMIO(px, ld_x, None, None, 0, pdt, ld_dt, pz, ld_z, a.whole(A_log, "A_log", (H,), a.f32),
+               a.whole(dt_bias, "dt_bias", (H,), a.f32), a.whole(D, "D", (H,), a.f32),
+               a.whole(conv_w, "conv_w", (CH, 4), a.act), a.whole(conv_bias, "conv_bias", (CH,), a.act),
+               None, n, n, a.whole(state_idx, "state_idx", (n,), a.i32), ps, ps,
+               a.pool(conv_state, "conv_state", cfg.n_slots, (CH, 3), a.act),
+               a.whole(y, "y", (n, H * P), a.act))
+    ws, ws_bytes = a.bytes_of(workspace)
+    _check(load().gdn_ssm_decode(ctypes.byref(cfg), ctypes.byref(io), ws, ws_bytes, _stream(stream)),
+           "gdn_ssm_decode")
+
+
+def gdn_block_norm_workspace_size(rows, dim) -> int:
+    return load().gdn_block_norm_workspace_size(rows, dim)
+
+
+def gdn_block_norm(residual, w_pre=None, h=None, block=None, res_out=None, w_post=None, gate=None,
+                   res_scale=1.0, eps=1e-6, weight_offset=0.0, rstd_post=None, rstd_pre=None, stream=None):
+    """r' = residual + res_scale * sigmoid(gate) * norm(block) -> res_out, norm(r') -> h; all [rows, dim]
+    (gate: [rows, dim] or [rows, 1]).  res_out may be residual."""
+    a = _Args("gdn_block_norm")
+    rows, dim = residual.shape
+    like = h if h is not None else block
+    if like is None:
+        a.refuse("h", "and block are both missing: nothing to do")
+    act, res = like.dtype, residual.dtype
+    cols = 0 if gate is None else gate.shape[1]
+    io = BlockNormIO(rows, dim, _dt(like), _dt(residual), eps, weight_offset, res_scale,
+                     *a.view(block, "block", rows, dim, act), *a.view(gate, "gate", rows, cols, act), cols,
+                     *a.view(residual, "residual", rows, dim, res), a.whole(w_post, "w_post", (dim,), a.f32),
+                     a.whole(w_pre, "w_pre", (dim,), a.f32), *a.view(res_out, "res_out", rows, dim, res),
+                     *a.view(h, "h", rows, dim, act), a.whole(rstd_post, "rstd_post", (rows,), a.f32),
+                     a.whole(rstd_pre, "rstd_pre", (rows,), a.f32))
+    _check(load().gdn_block_norm(ctypes.byref(io), _stream(stream)), "gdn_block_norm")
+
+
+def gdn_block_norm_backward(res_out, rstd_pre=None, w_pre=None, dh=None, d_res_out=None, d_residual=None,
+                            dw_pre=None, block=None, rstd_post=None, w_post=None, gate=None, res_scale=1.0,
+                            weight_offset=0.0, d_block=None, d_gate=None, dw_post=None, workspace=None,
+                            stream=None):
+    """Gradients of gdn_block_norm for sum(dh * h) + sum(d_res_out * r'): res_out, rstd_pre and
+    rstd_post as the forward call wrote them.  Every output may be None."""
+    a = _Args("gdn_block_norm_backward")
+    rows, dim = res_out.shape
+    like = next((t for t in (dh, block) if t is not None), None)
+    if like is None:
+        a.refuse("dh", "and block are both missing: nothing to do")
+    act, res = like.dtype, res_out.dtype
+    cols = 0 if gate is None else gate.shape[1]
+    io = BlockNormIO(rows, dim, _dt(like), _dt(res_out), 0.0, weight_offset, res_scale,
+                     *a.view(block, "block", rows, dim, act), *a.view(gate, "gate", rows, cols, act), cols,
+                     *a.view(res_out, "res_out", rows, dim, res), a.whole(w_post, "w_post", (dim,), a.f32),
+                     a.whole(w_pre, "w_pre", (dim,), a.f32), None, 0, None, 0,
+                     a.whole(rstd_post, "rstd_post", (rows,), a.f32),
+                     a.whole(rstd_pre, "rstd_pre", (rows,), a.f32), *a.view(dh, "dh", rows, dim, act),
+                     *a.view(d_res_out, "d_res_out", rows, dim, res),
+                     *a.view(d_residual, "d_residual", rows, dim, res),
+                     *a.view(d_block, "d_block", rows, dim, act), *a.view(d_gate, "d_gate", rows, cols, act),
+                     a.whole(dw_post, "dw_post", (dim,), a.f32), a.whole(dw_pre, "dw_pre", (dim,), a.f32))
+    ws, ws_bytes = a.bytes_of(workspace)
+    _check(load().gdn_block_norm_backward(ctypes.byref(io), ws, ws_bytes, _stream(stream)),
+           "gdn_block_norm_backward")
 
 
 def gdn_device_error(stream=None) -> int:

@@ -372,6 +372,138 @@ gdn_status gdn_state_copy(const gdn_config *cfg, const float *src_state, const v
                           int32_t n_dst_slots, const int32_t *src_idx, const int32_t *dst_idx,
                           int32_t n, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Selective state space mixer: the other recurrent mixer of a hybrid model,
+ * beside the gated delta rule, with the same packed batches, state slots and
+ * padding lanes.  (haskell-infer-demo and hyperflare core-design name only
+ * the delta rule; the forms below are the standard statement.)
+ * Per token t, head h and its group g = h / (heads / groups):
+ *
+ *   xBC_t = SiLU( bias + sum_{j=0..3} w[c][j] * raw_{t-3+j}[c] )   channels [x | B | C]
+ *   dt_t  = min(max(softplus(u_t[h] + dt_bias[h]), dt_min), dt_max)
+ *   S_t   = exp(-exp(A_log[h]) dt_t) S_{t-1} + dt_t B_t[g] x_t[h]^T     S: d_state x head_dim
+ *   y_t   = (S_t^T C_t[g] + D[h] x_t[h]) * SiLU(z_t[h])
+ *
+ * State: fp32 [n_slots][heads][d_state][head_dim].  Conv history: act
+ * [n_slots][CH][3], oldest input first, CH = heads*head_dim +
+ * 2*groups*d_state.  The rules of the top of this file hold: slots, padding
+ * lanes (zero outputs, nothing written), views, alignment, streams, errors.
+ * Packed rows behind cu_seqlens[n_seqs] are neither read nor written, so a
+ * captured call may carry a smaller batch than its T.  */
+typedef struct gdn_ssm_config {
+    int32_t groups, heads;     /* heads % groups == 0; heads <= 4096 */
+    int32_t d_state, head_dim; /* d_state in {16, 32, 64, 128}, head_dim in {32, 64, 128} */
+    gdn_dtype act;             /* dtype of x, b, c, dt, z, y, conv weights and history */
+    int32_t n_slots;           /* number of state / history slots (capacity) */
+    float dt_min, dt_max;      /* clamp of the step size; 0 and +inf: none */
+} gdn_ssm_config;
+
+typedef struct gdn_ssm_io {
+    const void *x;            /* prefill: [T][ld_x] act, heads*head_dim channels after the convolution;
+                               * decode: [T][ld_x] act, the CH raw channels [x | B | C] */
+    int64_t ld_x;
+    const void *b, *c;        /* prefill: [T][ld_bc] act, groups*d_state channels; decode: NULL */
+    int64_t ld_bc;
+    const void *dt;           /* [T][ld_dt] act: the step sizes' projection u, heads channels */
+    int64_t ld_dt;
+    const void *z;            /* [T][ld_z] act or NULL: no gate */
+    int64_t ld_z;
+    const float *A_log;       /* [heads] */
+    const float *dt_bias;     /* [heads] or NULL = 0 */
+    const float *D;           /* [heads] or NULL = 0 */
+    const void *conv_w;       /* decode: [CH][4] act, w[c][3] multiplies the current token */
+    const void *conv_bias;    /* decode: [CH] act or NULL = 0 */
+    const int32_t *cu_seqlens;/* prefill: [n_seqs+1] */
+    int32_t n_seqs;
+    int64_t T;                /* prefill: packed rows; decode: T == n_seqs */
+    const int32_t *state_idx; /* [n_seqs] or NULL */
+    const float *state_in;    /* [n_slots][heads][d_state][head_dim] or NULL = zero */
+    float *state_out;         /* the same or NULL = not written; may == state_in */
+    void *conv_state;         /* decode: [n_slots][CH][3] act, in/out */
+    void *y;                  /* [T][heads*head_dim] act */
+} gdn_ssm_io;
+
+/* Bytes of workspace gdn_ssm_prefill and gdn_ssm_decode need for up to
+ * max_tokens packed tokens and max_seqs sequences on the current device (0
+ * when cfg is invalid).  HOST only.
+ * Calls that may overlap on the GPU need workspaces of their own. */
+size_t gdn_ssm_workspace_size(const gdn_ssm_config *cfg, int64_t max_tokens, int32_t max_seqs);
+
+/* Causal convolution of width 4 with bias and SiLU over a packed batch: x
+ * [T][ld_x] act, w [CH][4] act, bias [CH] act or NULL, conv_state
+ * [n_slots][CH][3] act in/out (NULL = zero history, not written), out
+ * [T][CH] act.  An empty sequence leaves its history as it is. */
+gdn_status gdn_ssm_conv_prefill(const gdn_ssm_config *cfg, const void *x, int64_t ld_x,
+                                const int32_t *cu_seqlens, int32_t n_seqs, int64_t T, const void *w,
+                                const void *bias, void *conv_state, const int32_t *state_idx, void *out,
+                                void *stream);
+
+/* The scan over a packed batch, from x, B and C after the convolution
+ * (conv_w, conv_bias and conv_state are not used).  An empty sequence's state
+ * goes to state_out as it is.  `workspace` of gdn_ssm_workspace_size(cfg, T,
+ * n_seqs) bytes, 16-byte aligned: states between the segments that long
+ * sequences are cut into (a batch that is not cut needs none). */
+gdn_status gdn_ssm_prefill(const gdn_ssm_config *cfg, const gdn_ssm_io *io, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
+/* One token for each of n_seqs sequences: convolution step, then scan step;
+ * histories and states in place (state_out == state_in, conv_state non-NULL).
+ * The convolution's result is not rounded on its way into the scan.
+ * `workspace` of gdn_ssm_workspace_size(cfg, n_seqs, n_seqs) bytes. */
+gdn_status gdn_ssm_decode(const gdn_ssm_config *cfg, const gdn_ssm_io *io, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Norms around a block of a residual stream, fused with the block's gate and
+ * the residual scale (for a block such as a mixer: post-norm of its output,
+ * gated and scaled residual add, pre-norm of the next block).  Per row, with
+ * rms(v) = sqrt(mean(v^2) + eps), w^ = weight_offset + w:
+ *
+ *   n  = block / rms(block) * w_post^        (w_post NULL: n = block)
+ *   r' = residual + res_scale * sigmoid(gate) * n      (gate NULL: factor 1)
+ *   h  = r' / rms(r') * w_pre^               (r' before its rounding)
+ *
+ * block NULL: r' = residual (a plain pre-norm; gate, w_post and res_out
+ * NULL).  w_pre and h are both given or both NULL.  gate has gate_cols = dim
+ * columns or 1 (one value per row).  Row strides are in elements, >= the
+ * columns; views need element alignment only (all of them 16-byte aligned
+ * with 16-byte row strides and dim % 8 == 0 take vector loads).  res_out may
+ * be residual, d_residual may be d_res_out; nothing else may alias.
+ * dim <= 16384; act fp32 needs res fp32.  rows == 0 is no work (a backward
+ * call then writes zero weight gradients). */
+typedef struct gdn_block_norm_io {
+    int64_t rows;
+    int32_t dim;
+    gdn_dtype act;              /* block, gate, h, dh, d_block, d_gate */
+    gdn_dtype res;              /* residual, res_out, d_res_out, d_residual */
+    float eps, weight_offset, res_scale;
+    const void *block;    int64_t ld_block;
+    const void *gate;     int64_t ld_gate;
+    int32_t gate_cols;
+    const void *residual; int64_t ld_residual;  /* backward: r' (res_out of the forward) */
+    const float *w_post, *w_pre;                /* [dim] */
+    void *res_out;        int64_t ld_res_out;   /* forward: NULL = not written */
+    void *h;              int64_t ld_h;
+    float *rstd_post, *rstd_pre;  /* [rows] 1/rms(block), 1/rms(r'): forward out or NULL, backward in */
+    /* backward only */
+    const void *dh;        int64_t ld_dh;         /* given exactly when w_pre is */
+    const void *d_res_out; int64_t ld_d_res_out;  /* NULL = zero (then dh is needed) */
+    void *d_residual;      int64_t ld_d_residual; /* outputs, each NULL = not written */
+    void *d_block;         int64_t ld_d_block;
+    void *d_gate;          int64_t ld_d_gate;     /* gate_cols columns */
+    float *dw_post, *dw_pre;                      /* [dim], summed over the rows */
+} gdn_block_norm_io;
+
+gdn_status gdn_block_norm(const gdn_block_norm_io *io, void *stream);
+
+/* Gradients for the loss sum(dh * h) + sum(d_res_out * r').  `workspace` of
+ * gdn_block_norm_workspace_size(rows, dim) bytes, 16-byte aligned, where a
+ * weight gradient is asked for.  The sums over rows are taken in a fixed
+ * order: equal calls give equal bits. */
+size_t gdn_block_norm_workspace_size(int64_t rows, int32_t dim);
+gdn_status gdn_block_norm_backward(const gdn_block_norm_io *io, void *workspace, size_t workspace_bytes,
+                                   void *stream);
+
 /* Bounded waits (no page counterpart: it makes the device-side timeout
  * testable without a GPU fault).  Every wait of a kernel on another part of
  * the kernel (an mbarrier, a copy, a peer CTA's flag) gives up after wait_ns
