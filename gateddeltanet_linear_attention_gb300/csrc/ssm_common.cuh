@@ -79,6 +79,16 @@ __device__ __forceinline__ bool ssm_segment(const SsmScanArgs &a, int b, SsmSegm
     return true;
 }
 
+// Sigmoid and SiLU of values that end in the type T: through the approximate exp and quotient
+// (relative error below 2e-6 where the result matters) for 16-bit results, whose half step is
+// 4e-3; through the accurate ones for 32-bit results.
+template <typename T> __device__ __forceinline__ float sigmoid_for(float x) { return sigmoid_f(x); }
+template <> __device__ __forceinline__ float sigmoid_for<__nv_bfloat16>(float x) {
+    return __fdividef(1.0f, 1.0f + __expf(-x));
+}
+template <typename T> __device__ __forceinline__ float silu_for(float x) { return silu_f(x); }
+template <> __device__ __forceinline__ float silu_for<__nv_bfloat16>(float x) { return silu_fast(x); }
+
 // Row vectors of four elements.
 __device__ __forceinline__ float4 load4f(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 __device__ __forceinline__ float4 bf16x4_f32(uint2 v) {

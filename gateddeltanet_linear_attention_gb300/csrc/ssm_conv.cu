@@ -9,16 +9,20 @@ namespace {
 constexpr int kVec = 8;          // channels of a thread
 constexpr int kConvThreads = 128;
 constexpr int kRun = 16;         // tokens of a thread
+constexpr int kStepThreads = 128; // of the one-token state kernel
+constexpr int kBatch = 4;        // tokens whose loads are issued together
 
-__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
-    const float4 a = load4f(p), b = load4f(p + 4);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+// Eight channels as the memory holds them, and as fp32.
+struct Raw8F { float4 a, b; };
+__device__ __forceinline__ Raw8F load_raw8(const float *p) { return {load4f(p), load4f(p + 4)}; }
+__device__ __forceinline__ uint4 load_raw8(const __nv_bfloat16 *p) { return *reinterpret_cast<const uint4 *>(p); }
+__device__ __forceinline__ void raw_f32(const Raw8F &r, float (&v)[8]) {
+    v[0] = r.a.x; v[1] = r.a.y; v[2] = r.a.z; v[3] = r.a.w; v[4] = r.b.x; v[5] = r.b.y; v[6] = r.b.z; v[7] = r.b.w;
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[8]) {
-    const uint4 u = *reinterpret_cast<const uint4 *>(p);
-    const float4 a = bf16x4_f32(make_uint2(u.x, u.y)), b = bf16x4_f32(make_uint2(u.z, u.w));
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+__device__ __forceinline__ void raw_f32(const uint4 &u, float (&v)[8]) {
+    raw_f32(Raw8F{bf16x4_f32(make_uint2(u.x, u.y)), bf16x4_f32(make_uint2(u.z, u.w))}, v);
 }
+template <typename T> __device__ __forceinline__ void load8(const T *p, float (&v)[8]) { raw_f32(load_raw8(p), v); }
 __device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
     store4f(p, make_float4(v[0], v[1], v[2], v[3]));
     store4f(p + 4, make_float4(v[4], v[5], v[6], v[7]));
@@ -54,11 +58,13 @@ __device__ __forceinline__ int seq_of(const int32_t *cu, int n_seqs, long long t
 // history and may then overwrite it.  The two tokens' own run leaves them out.
 template <typename TA>
 __global__ void __launch_bounds__(kConvThreads) ssm_conv_kernel(SsmConvArgs a) {
+    using Raw = decltype(load_raw8((const TA *)nullptr));
     const SsmDims &d = a.d;
     const int c0 = (blockIdx.y * kConvThreads + threadIdx.x) * kVec;
     if (c0 >= d.ch) return;
-    const TA *x = (const TA *)a.x + c0;
-    TA *out = (TA *)a.out + c0, *hist = (TA *)a.conv_state;
+    const TA *__restrict__ x = (const TA *)a.x + c0;
+    TA *__restrict__ out = (TA *)a.out + c0;
+    TA *hist = (TA *)a.conv_state;
     const long long r0 = (long long)blockIdx.x * kRun, r1 = r0 + kRun < a.T ? r0 + kRun : a.T;
     float w[4][kVec], bias[kVec];
 #pragma unroll
@@ -132,19 +138,34 @@ __global__ void __launch_bounds__(kConvThreads) ssm_conv_kernel(SsmConvArgs a) {
 #pragma unroll
             for (int j = 0; j < 3; ++j) load8(x + (t - 3 + j) * a.ld_x, win[j]);
         }
-        for (; t < end; ++t) {
-            float cur[kVec], o[kVec];
-            load8(x + t * a.ld_x, cur);
+        auto emit = [&](const float (&cur)[kVec], long long at) {
+            float o[kVec];
 #pragma unroll
             for (int i = 0; i < kVec; ++i) {
-                o[i] = silu_f(fmaf(w[3][i], cur[i],
-                                   fmaf(w[2][i], win[2][i],
-                                        fmaf(w[1][i], win[1][i], fmaf(w[0][i], win[0][i], bias[i])))));
+                o[i] = silu_for<TA>(fmaf(w[3][i], cur[i],
+                                         fmaf(w[2][i], win[2][i],
+                                              fmaf(w[1][i], win[1][i], fmaf(w[0][i], win[0][i], bias[i])))));
                 win[0][i] = win[1][i];
                 win[1][i] = win[2][i];
                 win[2][i] = cur[i];
             }
-            store8(out + t * d.ch, o);
+            store8(out + at * d.ch, o);
+        };
+        for (; t + kBatch <= end; t += kBatch) {       // the loads of kBatch tokens in flight at once
+            Raw raw[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) raw[k] = load_raw8(x + (t + k) * a.ld_x);
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                float cur[kVec];
+                raw_f32(raw[k], cur);
+                emit(cur, t + k);
+            }
+        }
+        for (; t < end; ++t) {
+            float cur[kVec];
+            load8(x + t * a.ld_x, cur);
+            emit(cur, t);
         }
     }
 }
@@ -162,6 +183,8 @@ cudaError_t launch_ssm_conv(const SsmConvArgs &a, bool act_bf16, cudaStream_t s)
 // its only reader and the fp32 result goes to the workspace.
 template <typename TA>
 __global__ void __launch_bounds__(256) ssm_step_conv_kernel(SsmStepArgs a) {
+    // the state kernel may start loading states now; it waits for this grid before it reads `ws`
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const SsmDims &d = a.d;
     const int n = blockIdx.y, c = blockIdx.x * 256 + threadIdx.x;
     if (c >= d.ch) return;
@@ -177,15 +200,19 @@ __global__ void __launch_bounds__(256) ssm_step_conv_kernel(SsmStepArgs a) {
         silu_f(fmaf(w[3], to_f32(cur), fmaf(w[2], to_f32(h2), fmaf(w[1], to_f32(h1), fmaf(w[0], to_f32(h0), b)))));
 }
 
-// State step: one CTA per (head, sequence) reads the head's state once, writes
-// it once and reduces y over the rows.  HBM-bound on the state.
+// State step: one CTA per (sequence, head, 32 columns) reads its part of the
+// state once, writes it once and reduces y over the rows.  HBM-bound on the
+// state.  32 columns: whole 128-byte lines, and parts small enough that many
+// CTAs of an SM overlap their loads and stores.  Launched while the convolution
+// step still runs: the state's loads are issued before its results are awaited.
 template <int N, int P, typename TA>
-__global__ void __launch_bounds__(256) ssm_step_state_kernel(SsmStepArgs a) {
-    constexpr int LP = P / 4, NT = N * LP < 256 ? N * LP : 256, NS = NT / LP, RPT = N / NS;
-    __shared__ __align__(16) float part[NS][P];
+__global__ void __launch_bounds__(kStepThreads) ssm_step_state_kernel(SsmStepArgs a) {
+    constexpr int LP = 8, NS = kStepThreads / LP, RPT = N / NS;     // 16 row slices
+    __shared__ __align__(16) float part[NS][32];
     const SsmDims &d = a.d;
-    const int h = blockIdx.x, n = blockIdx.y, g = h / d.per, tid = threadIdx.x;
-    const int p0 = (tid % LP) * 4, ns = tid / LP;
+    constexpr int parts = P / 32;
+    const int h = blockIdx.x / parts, n = blockIdx.y, g = h / d.per, tid = threadIdx.x;
+    const int p0 = (blockIdx.x % parts) * 32 + (tid % LP) * 4, ns = tid / LP;
     const int slot = slot_of(a.state_idx, n, d.n_slots, a.err);
     TA *y = (TA *)a.y + ((long long)n * d.heads + h) * P;
     if (slot < 0) {
@@ -196,38 +223,43 @@ __global__ void __launch_bounds__(256) ssm_step_state_kernel(SsmStepArgs a) {
     float4 m[RPT];
 #pragma unroll
     for (int i = 0; i < RPT; ++i) m[i] = load4f(S + (long long)(ns + i * NS) * P + p0);
-    const float *row = a.ws + (long long)n * d.ch;
-    const float *B = row + d.heads * P + g * N, *C = B + d.groups * N;
     const float dt = ssm_dt(to_f32(((const TA *)a.dt)[(long long)n * a.ld_dt + h]),
                             a.dt_bias ? a.dt_bias[h] : 0.f, d);
-    const float dec = expf(-expf(a.A_log[h]) * dt);
+    const float dec = expf(-expf(a.A_log[h]) * dt), skip = a.D ? a.D[h] : 0.f;
+    float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (a.z && tid < LP) z = load4f((const TA *)a.z + (long long)n * a.ld_z + (long long)h * P + p0);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const float *row = a.ws + (long long)n * d.ch;
+    const float *B = row + d.heads * P + g * N, *C = B + d.groups * N;
     const float4 x = load4f(row + h * P + p0);
+    float b[RPT], c[RPT];
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+        b[i] = B[ns + i * NS];
+        c[i] = C[ns + i * NS];
+    }
     const float4 u = make_float4(dt * x.x, dt * x.y, dt * x.z, dt * x.w);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
-        const int k = ns + i * NS;
-        const float b = B[k], c = C[k];
-        m[i].x = fmaf(dec, m[i].x, b * u.x); m[i].y = fmaf(dec, m[i].y, b * u.y);
-        m[i].z = fmaf(dec, m[i].z, b * u.z); m[i].w = fmaf(dec, m[i].w, b * u.w);
-        acc.x = fmaf(c, m[i].x, acc.x); acc.y = fmaf(c, m[i].y, acc.y);
-        acc.z = fmaf(c, m[i].z, acc.z); acc.w = fmaf(c, m[i].w, acc.w);
-        store4f(S + (long long)k * P + p0, m[i]);
+        m[i].x = fmaf(dec, m[i].x, b[i] * u.x); m[i].y = fmaf(dec, m[i].y, b[i] * u.y);
+        m[i].z = fmaf(dec, m[i].z, b[i] * u.z); m[i].w = fmaf(dec, m[i].w, b[i] * u.w);
+        acc.x = fmaf(c[i], m[i].x, acc.x); acc.y = fmaf(c[i], m[i].y, acc.y);
+        acc.z = fmaf(c[i], m[i].z, acc.z); acc.w = fmaf(c[i], m[i].w, acc.w);
+        store4f(S + (long long)(ns + i * NS) * P + p0, m[i]);
     }
-    store4f(&part[ns][p0], acc);
+    store4f(&part[ns][(tid % LP) * 4], acc);
     __syncthreads();
     if (tid < LP) {
-        float4 o = load4f(&part[0][p0]);
+        float4 o = load4f(&part[0][tid * 4]);
 #pragma unroll
         for (int k = 1; k < NS; ++k) {
-            const float4 q = load4f(&part[k][p0]);
+            const float4 q = load4f(&part[k][tid * 4]);
             o.x += q.x; o.y += q.y; o.z += q.z; o.w += q.w;
         }
-        const float skip = a.D ? a.D[h] : 0.f;
         o.x = fmaf(skip, x.x, o.x); o.y = fmaf(skip, x.y, o.y);
         o.z = fmaf(skip, x.z, o.z); o.w = fmaf(skip, x.w, o.w);
         if (a.z) {
-            const float4 z = load4f((const TA *)a.z + (long long)n * a.ld_z + (long long)h * P + p0);
             o.x *= silu_f(z.x); o.y *= silu_f(z.y); o.z *= silu_f(z.z); o.w *= silu_f(z.w);
         }
         store4f(y + p0, o);
@@ -239,9 +271,18 @@ size_t ssm_step_ws_bytes(const SsmDims &d, long long n) { return (size_t)n * d.c
 namespace {
 template <int N, int P, typename TA> cudaError_t run_step(const SsmStepArgs &a, cudaStream_t s) {
     ssm_step_conv_kernel<TA><<<dim3((a.d.ch + 255) / 256, a.n), 256, 0, s>>>(a);
-    constexpr int NT = N * P / 4 < 256 ? N * P / 4 : 256;
-    ssm_step_state_kernel<N, P, TA><<<dim3(a.d.heads, a.n), NT, 0, s>>>(a);
-    return cudaGetLastError();
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(a.d.heads * (P / 32), a.n);
+    cfg.blockDim = dim3(kStepThreads);
+    cfg.stream = s;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, ssm_step_state_kernel<N, P, TA>, a);
 }
 template <int N, typename TA> cudaError_t run_step_p(const SsmStepArgs &a, cudaStream_t s) {
     switch (a.d.P) {

@@ -288,7 +288,8 @@ __global__ void __launch_bounds__(ScanShape<N, P>::NT) ssm_scan_kernel(SsmScanAr
                 o.z = fmaf(skip, x.z, o.z); o.w = fmaf(skip, x.w, o.w);
                 if (a.z) {
                     const float4 z = load4f((const TA *)a.z + t * a.ld_z + (long long)h * P + c);
-                    o.x *= silu_f(z.x); o.y *= silu_f(z.y); o.z *= silu_f(z.z); o.w *= silu_f(z.w);
+                    o.x *= silu_for<TA>(z.x); o.y *= silu_for<TA>(z.y);
+                    o.z *= silu_for<TA>(z.z); o.w *= silu_for<TA>(z.w);
                 }
                 store4f(y + t * out_cols + (long long)h * P + c, o);
             }
