@@ -128,8 +128,14 @@ template <bool WARP> __device__ __forceinline__ float row_sum(float v, float2 (*
 
 }  // namespace
 
-template <typename TA, typename TR, int NV, bool WARP, bool VEC>
-__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) block_norm_kernel(NormArgs a) {
+// Blocks of MAXT threads at most, and how many of them an SM's registers hold.  Rows that fill
+// 1,024 threads leave 64 registers a thread: those kernels read the weights at every row (from
+// L1) and do not load ahead (LEAN).
+constexpr int fwd_blocks(int maxt) { return 1024 / maxt; }
+constexpr int bwd_blocks(int maxt) { return maxt >= 512 ? 1 : 512 / maxt; }
+
+template <typename TA, typename TR, int NV, int MAXT, bool WARP, bool VEC>
+__global__ void __launch_bounds__(MAXT, fwd_blocks(MAXT)) block_norm_kernel(NormArgs a) {
     __shared__ float2 buf[2][32];
     int turn = 0;
     using Ch = Chunk<VEC>;
@@ -139,15 +145,21 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) block_norm_kerne
     const float inv_dim = 1.0f / (float)a.dim;
     const bool channel_gate = a.gate && a.gate_cols > 1, row_gate = a.gate && a.gate_cols == 1;
 
+    constexpr bool LEAN = MAXT == 1024;
     float w1[NV][8], w2[NV][8];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const Ch c(i, lane, nt, a.dim);
+    auto weight = [&](const float *w, int i, float (&v)[8]) {
         Raw8<float> r;
-        if (a.w_post) { load_raw<VEC>(c, a.w_post, r); r.get(w1[i]); }
-        if (a.w_pre) { load_raw<VEC>(c, a.w_pre, r); r.get(w2[i]); }
+        load_raw<VEC>(Ch(i, lane, nt, a.dim), w, r);
+        r.get(v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) { w1[i][j] += a.offset; w2[i][j] += a.offset; }
+        for (int j = 0; j < 8; ++j) v[j] += a.offset;
+    };
+    if (!LEAN) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (a.w_post) weight(a.w_post, i, w1[i]);
+            if (a.w_pre) weight(a.w_pre, i, w2[i]);
+        }
     }
     Raw8<TA> rp[NV], rg[NV];
     Raw8<TR> rr[NV];
@@ -162,8 +174,9 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) block_norm_kerne
         }
         if (row_gate) gate1 = to_f32(((const TA *)a.gate)[row * a.ld_gate]);
     };
-    if (first < a.rows) fetch(first);
+    if (!LEAN && first < a.rows) fetch(first);
     for (long long row = first; row < a.rows; row += step) {
+        if (LEAN) fetch(row);
         float u[NV][8], p[NV][8], gt[NV][8];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -172,7 +185,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) block_norm_kerne
             if (channel_gate) rg[i].get(gt[i]);
         }
         const float g1 = gate1;
-        if (row + step < a.rows) fetch(row + step);
+        if (!LEAN && row + step < a.rows) fetch(row + step);
         if (a.block) {
             float k = 1.0f;
             if (a.w_post) {
@@ -187,13 +200,15 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) block_norm_kerne
             }
             const float rs = a.scale * (row_gate ? sigmoid_f(g1) : 1.0f);
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
+            for (int i = 0; i < NV; ++i) {
+                if (LEAN && a.w_post) weight(a.w_post, i, w1[i]);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     float v = a.w_post ? p[i][j] * k * w1[i][j] : p[i][j];
-                    if (channel_gate) v *= sigmoid_f(gt[i][j]);
+                    if (channel_gate) v *= sigmoid_for<TA>(gt[i][j]);
                     u[i][j] = fmaf(rs, v, u[i][j]);
                 }
+            }
             if (a.res_out) {
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
@@ -212,6 +227,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) block_norm_kerne
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 float v[8];
+                if (LEAN) weight(a.w_pre, i, w2[i]);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[j] = u[i][j] * k * w2[i][j];
                 store8v<VEC>(Ch(i, lane, nt, a.dim), (TA *)a.h + row * a.ld_h, v);
@@ -227,8 +243,8 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) block_norm_kerne
 //   dw1   = sum over rows of dn p^,  dw2 = sum over rows of dh r^
 // The weight gradients are summed in registers over a CTA's rows, then over the
 // CTAs by norm_weight_grad_kernel, always in the same order.
-template <typename TA, typename TR, int NV, bool WARP, bool VEC>
-__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) block_norm_bwd_kernel(NormArgs a) {
+template <typename TA, typename TR, int NV, int MAXT, bool WARP, bool VEC>
+__global__ void __launch_bounds__(MAXT, bwd_blocks(MAXT)) block_norm_bwd_kernel(NormArgs a) {
     __shared__ float2 buf[2][32];
     int turn = 0;
     using Ch = Chunk<VEC>;
@@ -243,20 +259,30 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) block_norm_bwd_k
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw1[i][j] = dw2[i][j] = 0.f;
 
-    for (long long row = first; row < a.rows; row += step) {
-        Raw8<TA> rp[NV], rg[NV], rh[NV];
-        Raw8<TR> ru[NV], rd[NV];
+    Raw8<TA> np[NV], ng[NV], nh[NV];
+    Raw8<TR> nu[NV], nd[NV];
+    auto fetch = [&](long long row) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const Ch c(i, lane, nt, a.dim);
             if (a.dh) {
-                load_raw<VEC>(c, (const TA *)a.dh + row * a.ld_dh, rh[i]);
-                load_raw<VEC>(c, (const TR *)a.residual + row * a.ld_res, ru[i]);
+                load_raw<VEC>(c, (const TA *)a.dh + row * a.ld_dh, nh[i]);
+                load_raw<VEC>(c, (const TR *)a.residual + row * a.ld_res, nu[i]);
             }
-            if (a.d_res_out) load_raw<VEC>(c, (const TR *)a.d_res_out + row * a.ld_dout, rd[i]);
-            if (a.block) load_raw<VEC>(c, (const TA *)a.block + row * a.ld_block, rp[i]);
-            if (channel_gate) load_raw<VEC>(c, (const TA *)a.gate + row * a.ld_gate, rg[i]);
+            if (a.d_res_out) load_raw<VEC>(c, (const TR *)a.d_res_out + row * a.ld_dout, nd[i]);
+            if (a.block) load_raw<VEC>(c, (const TA *)a.block + row * a.ld_block, np[i]);
+            if (channel_gate) load_raw<VEC>(c, (const TA *)a.gate + row * a.ld_gate, ng[i]);
         }
+    };
+    constexpr bool LEAN = MAXT == 1024;
+    if (!LEAN && first < a.rows) fetch(first);
+    for (long long row = first; row < a.rows; row += step) {
+        if (LEAN) fetch(row);
+        Raw8<TA> rp[NV], rg[NV], rh[NV];
+        Raw8<TR> ru[NV], rd[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) { rp[i] = np[i]; rg[i] = ng[i]; rh[i] = nh[i]; ru[i] = nu[i]; rd[i] = nd[i]; }
+        if (!LEAN && row + step < a.rows) fetch(row + step);
         float du[NV][8];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -317,7 +343,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) block_norm_bwd_k
                 for (int j = 0; j < 8; ++j) {
                     const float wj = a.w_post ? w[j] + a.offset : 1.0f;
                     ph[j] *= k;
-                    const float sg = channel_gate ? sigmoid_f(gt[j]) : s1;
+                    const float sg = channel_gate ? sigmoid_for<TA>(gt[j]) : s1;
                     const float dn = a.scale * du[i][j] * sg;
                     if (a.gate) {
                         gt[j] = dn * (1.0f - sg) * ph[j] * wj;
@@ -379,39 +405,36 @@ __global__ void __launch_bounds__(1024) norm_weight_grad_kernel(const float *ws,
 
 namespace {
 
-bool warp_rows(int dim) { return dim <= 1024; }
+// A warp owns a row of up to 256 elements, a CTA a longer one.
+bool warp_rows(int dim) { return dim <= 256; }
+int max_threads(int dim) { return dim <= 1024 ? 128 : dim <= 4096 ? 512 : 1024; }
 
 // CTAs of the backward, and the parts of the weight gradients that they leave.
 int bwd_ctas(long long rows, int dim) {
-    const long long cap = (long long)sm_count() * (warp_rows(dim) ? 4 : dim <= 4096 ? 2 : 1);
+    const long long cap = (long long)sm_count() * bwd_blocks(max_threads(dim));
     const long long want = warp_rows(dim) ? (rows + kWarpRows - 1) / kWarpRows : rows;
     return (int)(want < cap ? want : cap);
 }
 
-template <typename TA, typename TR, int NV, bool WARP, bool VEC>
+template <typename TA, typename TR, int NV, int MAXT, bool WARP, bool VEC>
 void run(const NormArgs &a, bool backward, int threads, cudaStream_t s) {
     if (backward) {
         const int ctas = bwd_ctas(a.rows, a.dim);
-        block_norm_bwd_kernel<TA, TR, NV, WARP, VEC><<<ctas, threads, 0, s>>>(a);
+        block_norm_bwd_kernel<TA, TR, NV, MAXT, WARP, VEC><<<ctas, threads, 0, s>>>(a);
     } else {
-        const long long cap = (long long)sm_count() * (2048 / threads);
+        const long long cap = (long long)sm_count() * fwd_blocks(MAXT);
         const long long want = WARP ? (a.rows + kWarpRows - 1) / kWarpRows : a.rows;
-        block_norm_kernel<TA, TR, NV, WARP, VEC><<<(unsigned)(want < cap ? want : cap), threads, 0, s>>>(a);
+        block_norm_kernel<TA, TR, NV, MAXT, WARP, VEC><<<(unsigned)(want < cap ? want : cap), threads, 0, s>>>(a);
     }
 }
 
 template <typename TA, typename TR, bool VEC> void run_dim(const NormArgs &a, bool backward, cudaStream_t s) {
-    const int chunks = (a.dim + 7) / 8;
-    if (warp_rows(a.dim)) {
-        const int nt = 32 * kWarpRows;
-        if (chunks <= 32) run<TA, TR, 1, true, VEC>(a, backward, nt, s);
-        else if (chunks <= 64) run<TA, TR, 2, true, VEC>(a, backward, nt, s);
-        else run<TA, TR, 4, true, VEC>(a, backward, nt, s);
-    } else if (chunks <= 1024) {
-        run<TA, TR, 1, false, VEC>(a, backward, (chunks + 31) / 32 * 32, s);
-    } else {
-        run<TA, TR, 2, false, VEC>(a, backward, (chunks + 63) / 64 * 32, s);
-    }
+    const int chunks = (a.dim + 7) / 8, threads = (chunks + 31) / 32 * 32;
+    if (warp_rows(a.dim)) run<TA, TR, 1, 32 * kWarpRows, true, VEC>(a, backward, 32 * kWarpRows, s);
+    else if (chunks <= 128) run<TA, TR, 1, 128, false, VEC>(a, backward, threads, s);
+    else if (chunks <= 512) run<TA, TR, 1, 512, false, VEC>(a, backward, threads, s);
+    else if (chunks <= 1024) run<TA, TR, 1, 1024, false, VEC>(a, backward, threads, s);
+    else run<TA, TR, 2, 1024, false, VEC>(a, backward, (chunks + 63) / 64 * 32, s);
 }
 
 template <bool VEC> void run_types(const NormArgs &a, bool backward, cudaStream_t s) {
