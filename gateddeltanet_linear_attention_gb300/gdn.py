@@ -399,6 +399,8 @@ def make_ssm_config(groups, heads, d_state, head_dim, act="bf16", n_slots=0, dt_
 class _Args:
     """Checks of one call's tensors: all on the current device, of the expected type and shape."""
 
+    __slots__ = ("where", "device", "f32", "i32", "act")
+
     def __init__(self, where, act=None):
         import torch
         self.where, self.device = where, torch.cuda.current_device()
@@ -408,42 +410,45 @@ class _Args:
     def refuse(self, name, what):
         raise ValueError("%s: %s %s" % (self.where, name, what))
 
-    def on_device(self, t, name, dtype):
+    def explain(self, t, name, shape, dtype):
         if t.dtype != dtype:
             self.refuse(name, "is %s, not %s" % (t.dtype, dtype))
         if t.get_device() != self.device:
             self.refuse(name, "is on %s, not on the current device cuda:%d" % (t.device, self.device))
+        self.refuse(name, "has shape %s, not %s" % (tuple(t.shape), shape))
 
-    def view(self, t, name, rows, cols, dtype):
-        """(pointer, row stride) of a [rows][cols] view with contiguous rows."""
+    def view(self, t, name, shape, dtype):
+        """(pointer, row stride) of a two-dimensional view with contiguous rows."""
         if t is None:
             return None, 0
-        self.on_device(t, name, dtype)
-        if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
-            self.refuse(name, "has shape %s, not %s" % (tuple(t.shape), (rows, cols)))
-        if cols > 1 and t.stride(1) != 1:
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != self.device:
+            self.explain(t, name, shape, dtype)
+        ld, one = t.stride()
+        if one != 1 and shape[1] > 1:
             self.refuse(name, "has rows that are not contiguous")
-        ld = t.stride(0) if rows > 1 else max(cols, t.stride(0))
-        if ld < cols:
-            self.refuse(name, "has rows that overlap")
+        if ld < shape[1]:
+            if shape[0] > 1:
+                self.refuse(name, "has rows that overlap")
+            ld = shape[1]
         return t.data_ptr(), ld
 
     def whole(self, t, name, shape, dtype):
-        """Pointer of a contiguous tensor; None in `shape`: any size."""
+        """Pointer of a contiguous tensor."""
         if t is None:
             return None
-        self.on_device(t, name, dtype)
-        if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-            self.refuse(name, "has shape %s, not %s" % (tuple(t.shape), tuple(shape)))
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != self.device:
+            self.explain(t, name, shape, dtype)
         if not t.is_contiguous():
             self.refuse(name, "is not contiguous")
         return t.data_ptr()
 
     def pool(self, t, name, n_slots, shape, dtype):
-        p = self.whole(t, name, (None,) + shape, dtype)
-        if t is not None and t.shape[0] < n_slots:
-            self.refuse(name, "has %d slots, and the configuration %d" % (t.shape[0], n_slots))
-        return p
+        """Pointer of a contiguous pool of n_slots slots or more."""
+        if t is None:
+            return None
+        if t.dim() == 0 or t.shape[0] < n_slots:
+            self.refuse(name, "has fewer than the configuration's %d slots" % n_slots)
+        return self.whole(t, name, (t.shape[0],) + shape, dtype)
 
     def bytes_of(self, t):
         if t is None:
@@ -451,6 +456,12 @@ class _Args:
         if t.get_device() != self.device or not t.is_contiguous():
             self.refuse("workspace", "is not a contiguous tensor on the current device")
         return t.data_ptr(), t.numel() * t.element_size()
+
+    def stream(self, stream):
+        if stream is None:
+            import torch
+            return torch._C._cuda_getCurrentRawStream(self.device)
+        return getattr(stream, "cuda_stream", stream)
 
 
 def gdn_ssm_workspace_size(cfg, max_tokens, max_seqs) -> int:
@@ -462,13 +473,13 @@ def gdn_ssm_conv_prefill(cfg, x, cu_seqlens, w, bias, conv_state, state_idx, out
     a = _Args("gdn_ssm_conv_prefill", cfg.act)
     CH = cfg.heads * cfg.head_dim + 2 * cfg.groups * cfg.d_state
     T, n = x.shape[0], cu_seqlens.shape[0] - 1
-    px, ld_x = a.view(x, "x", T, CH, a.act)
-    _check(load().gdn_ssm_conv_prefill(
+    px, ld_x = a.view(x, "x", (T, CH), a.act)
+    _check((_lib or load()).gdn_ssm_conv_prefill(
         ctypes.byref(cfg), px, ld_x, a.whole(cu_seqlens, "cu_seqlens", (n + 1,), a.i32), n, T,
         a.whole(w, "w", (CH, 4), a.act), a.whole(bias, "bias", (CH,), a.act),
         a.pool(conv_state, "conv_state", cfg.n_slots, (CH, 3), a.act),
         a.whole(state_idx, "state_idx", (n,), a.i32), a.whole(out, "out", (T, CH), a.act),
-        _stream(stream)), "gdn_ssm_conv_prefill")
+        a.stream(stream)), "gdn_ssm_conv_prefill")
 
 
 def gdn_ssm_prefill(cfg, x, b, c, dt, A_log, cu_seqlens, y, D=None, dt_bias=None, z=None, state_in=None,
@@ -476,13 +487,13 @@ def gdn_ssm_prefill(cfg, x, b, c, dt, A_log, cu_seqlens, y, D=None, dt_bias=None
     """x [T, heads*head_dim], b and c [T, groups*d_state] (one row stride), dt [T, heads] -> y."""
     a = _Args("gdn_ssm_prefill", cfg.act)
     H, N, P, T, n = cfg.heads, cfg.d_state, cfg.head_dim, x.shape[0], cu_seqlens.shape[0] - 1
-    px, ld_x = a.view(x, "x", T, H * P, a.act)
-    pb, ld_bc = a.view(b, "b", T, cfg.groups * N, a.act)
-    pc, ld_c = a.view(c, "c", T, cfg.groups * N, a.act)
+    px, ld_x = a.view(x, "x", (T, H * P), a.act)
+    pb, ld_bc = a.view(b, "b", (T, cfg.groups * N), a.act)
+    pc, ld_c = a.view(c, "c", (T, cfg.groups * N), a.act)
     if T > 1 and ld_c != ld_bc:
         a.refuse("c", "has another row stride than b")
-    pdt, ld_dt = a.view(dt, "dt", T, H, a.act)
-    pz, ld_z = a.view(z, "z", T, H * P, a.act)
+    pdt, ld_dt = a.view(dt, "dt", (T, H), a.act)
+    pz, ld_z = a.view(z, "z", (T, H * P), a.act)
     io = SSMIO(px, ld_x, pb, pc, ld_bc, pdt, ld_dt, pz, ld_z, a.whole(A_log, "A_log", (H,), a.f32),
                a.whole(dt_bias, "dt_bias", (H,), a.f32), a.whole(D, "D", (H,), a.f32), None, None,
                a.whole(cu_seqlens, "cu_seqlens", (n + 1,), a.i32), n, T,
@@ -491,7 +502,7 @@ def gdn_ssm_prefill(cfg, x, b, c, dt, A_log, cu_seqlens, y, D=None, dt_bias=None
                a.pool(state_out, "state_out", cfg.n_slots, (H, N, P), a.f32), None,
                a.whole(y, "y", (T, H * P), a.act))
     ws, ws_bytes = a.bytes_of(workspace)
-    _check(load().gdn_ssm_prefill(ctypes.byref(cfg), ctypes.byref(io), ws, ws_bytes, _stream(stream)),
+    _check((_lib or load()).gdn_ssm_prefill(ctypes.byref(cfg), ctypes.byref(io), ws, ws_bytes, a.stream(stream)),
            "gdn_ssm_prefill")
 
 
@@ -502,9 +513,9 @@ def gdn_ssm_decode(cfg, x, dt, conv_w, conv_state, A_log, state, y, workspace, c
     a = _Args("gdn_ssm_decode", cfg.act)
     H, N, P, n = cfg.heads, cfg.d_state, cfg.head_dim, x.shape[0]
     CH = H * P + 2 * cfg.groups * N
-    px, ld_x = a.view(x, "x", n, CH, a.act)
-    pdt, ld_dt = a.view(dt, "dt", n, H, a.act)
-    pz, ld_z = a.view(z, "z", n, H * P, a.act)
+    px, ld_x = a.view(x, "x", (n, CH), a.act)
+    pdt, ld_dt = a.view(dt, "dt", (n, H), a.act)
+    pz, ld_z = a.view(z, "z", (n, H * P), a.act)
     ps = a.pool(state, "state", cfg.n_slots, (H, N, P), a.f32)
     io = SSMIO(px, ld_x, None, None, 0, pdt, ld_dt, pz, ld_z, a.whole(A_log, "A_log", (H,), a.f32),
                a.whole(dt_bias, "dt_bias", (H,), a.f32), a.whole(D, "D", (H,), a.f32),
@@ -513,7 +524,7 @@ def gdn_ssm_decode(cfg, x, dt, conv_w, conv_state, A_log, state, y, workspace, c
                a.pool(conv_state, "conv_state", cfg.n_slots, (CH, 3), a.act),
                a.whole(y, "y", (n, H * P), a.act))
     ws, ws_bytes = a.bytes_of(workspace)
-    _check(load().gdn_ssm_decode(ctypes.byref(cfg), ctypes.byref(io), ws, ws_bytes, _stream(stream)),
+    _check((_lib or load()).gdn_ssm_decode(ctypes.byref(cfg), ctypes.byref(io), ws, ws_bytes, a.stream(stream)),
            "gdn_ssm_decode")
 
 
@@ -526,19 +537,19 @@ def gdn_block_norm(residual, w_pre=None, h=None, block=None, res_out=None, w_pos
     """r' = residual + res_scale * sigmoid(gate) * norm(block) -> res_out, norm(r') -> h; all [rows, dim]
     (gate: [rows, dim] or [rows, 1]).  res_out may be residual."""
     a = _Args("gdn_block_norm")
-    rows, dim = residual.shape
+    rows, dim = wide = tuple(residual.shape)
     like = h if h is not None else block
     if like is None:
         a.refuse("h", "and block are both missing: nothing to do")
     act, res = like.dtype, residual.dtype
     cols = 0 if gate is None else gate.shape[1]
     io = BlockNormIO(rows, dim, _dt(like), _dt(residual), eps, weight_offset, res_scale,
-                     *a.view(block, "block", rows, dim, act), *a.view(gate, "gate", rows, cols, act), cols,
-                     *a.view(residual, "residual", rows, dim, res), a.whole(w_post, "w_post", (dim,), a.f32),
-                     a.whole(w_pre, "w_pre", (dim,), a.f32), *a.view(res_out, "res_out", rows, dim, res),
-                     *a.view(h, "h", rows, dim, act), a.whole(rstd_post, "rstd_post", (rows,), a.f32),
+                     *a.view(block, "block", wide, act), *a.view(gate, "gate", (rows, cols), act), cols,
+                     *a.view(residual, "residual", wide, res), a.whole(w_post, "w_post", (dim,), a.f32),
+                     a.whole(w_pre, "w_pre", (dim,), a.f32), *a.view(res_out, "res_out", wide, res),
+                     *a.view(h, "h", wide, act), a.whole(rstd_post, "rstd_post", (rows,), a.f32),
                      a.whole(rstd_pre, "rstd_pre", (rows,), a.f32))
-    _check(load().gdn_block_norm(ctypes.byref(io), _stream(stream)), "gdn_block_norm")
+    _check((_lib or load()).gdn_block_norm(ctypes.byref(io), a.stream(stream)), "gdn_block_norm")
 
 
 def gdn_block_norm_backward(res_out, rstd_pre=None, w_pre=None, dh=None, d_res_out=None, d_residual=None,
@@ -548,24 +559,24 @@ def gdn_block_norm_backward(res_out, rstd_pre=None, w_pre=None, dh=None, d_res_o
     """Gradients of gdn_block_norm for sum(dh * h) + sum(d_res_out * r'): res_out, rstd_pre and
     rstd_post as the forward call wrote them.  Every output may be None."""
     a = _Args("gdn_block_norm_backward")
-    rows, dim = res_out.shape
+    rows, dim = wide = tuple(res_out.shape)
     like = next((t for t in (dh, block) if t is not None), None)
     if like is None:
         a.refuse("dh", "and block are both missing: nothing to do")
     act, res = like.dtype, res_out.dtype
     cols = 0 if gate is None else gate.shape[1]
     io = BlockNormIO(rows, dim, _dt(like), _dt(res_out), 0.0, weight_offset, res_scale,
-                     *a.view(block, "block", rows, dim, act), *a.view(gate, "gate", rows, cols, act), cols,
-                     *a.view(res_out, "res_out", rows, dim, res), a.whole(w_post, "w_post", (dim,), a.f32),
+                     *a.view(block, "block", wide, act), *a.view(gate, "gate", (rows, cols), act), cols,
+                     *a.view(res_out, "res_out", wide, res), a.whole(w_post, "w_post", (dim,), a.f32),
                      a.whole(w_pre, "w_pre", (dim,), a.f32), None, 0, None, 0,
                      a.whole(rstd_post, "rstd_post", (rows,), a.f32),
-                     a.whole(rstd_pre, "rstd_pre", (rows,), a.f32), *a.view(dh, "dh", rows, dim, act),
-                     *a.view(d_res_out, "d_res_out", rows, dim, res),
-                     *a.view(d_residual, "d_residual", rows, dim, res),
-                     *a.view(d_block, "d_block", rows, dim, act), *a.view(d_gate, "d_gate", rows, cols, act),
+                     a.whole(rstd_pre, "rstd_pre", (rows,), a.f32), *a.view(dh, "dh", wide, act),
+                     *a.view(d_res_out, "d_res_out", wide, res),
+                     *a.view(d_residual, "d_residual", wide, res),
+                     *a.view(d_block, "d_block", wide, act), *a.view(d_gate, "d_gate", (rows, cols), act),
                      a.whole(dw_post, "dw_post", (dim,), a.f32), a.whole(dw_pre, "dw_pre", (dim,), a.f32))
     ws, ws_bytes = a.bytes_of(workspace)
-    _check(load().gdn_block_norm_backward(ctypes.byref(io), ws, ws_bytes, _stream(stream)),
+    _check((_lib or load()).gdn_block_norm_backward(ctypes.byref(io), ws, ws_bytes, a.stream(stream)),
            "gdn_block_norm_backward")
 
 
