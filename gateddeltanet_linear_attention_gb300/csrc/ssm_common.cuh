@@ -138,6 +138,10 @@ struct SsmStepArgs {
 size_t ssm_scan_ws_bytes(const SsmDims &d, bool act_bf16, long long T, long long n_seqs);
 size_t ssm_scan_carve(SsmScanArgs &a, bool act_bf16, void *ws);
 cudaError_t launch_ssm_scan(const SsmScanArgs &a, bool act_bf16, cudaStream_t s);
+// The tensor-core form (bf16 activations): a unit is 128 value columns of a group's heads.
+bool ssm_tc_supported(const SsmDims &d);
+int ssm_tc_units(const SsmDims &d);
+cudaError_t launch_ssm_scan_tc(const SsmScanArgs &a, bool states, unsigned segments, cudaStream_t s);
 cudaError_t launch_ssm_conv(const SsmConvArgs &a, bool act_bf16, cudaStream_t s);
 size_t ssm_step_ws_bytes(const SsmDims &d, long long n);
 cudaError_t launch_ssm_step(const SsmStepArgs &a, bool act_bf16, cudaStream_t s);

@@ -315,19 +315,27 @@ __global__ void __launch_bounds__(ScanShape<N, P>::NT) ssm_scan_kernel(SsmScanAr
 // ---------------------------------------------------------------- launching
 namespace {
 
-// Tokens of a segment: enough CTAs to fill the GPU about twice over (`slots`
-// resident (segment, head) walks), a multiple of 128, at least 256 tokens.
-// A batch whose sequences fill it by themselves is then not cut.
-long long segment_len(const SsmDims &d, long long T, int slots) {
-    const long long want = (T * d.heads + slots - 1) / slots;
-    long long len = (want + 127) / 128 * 128;
-    return len < 256 ? 256 : len;
+bool on_tensor_cores(const SsmDims &d, bool act_bf16) { return act_bf16 && ssm_tc_supported(d); }
+
+// Segments that run side by side when one sequence has the GPU to itself: the resident CTAs over
+// those of one segment (heads, or units of the tensor-core form, one CTA per SM there).
+int segments_wanted(const SsmDims &d, bool act_bf16) {
+    int want;
+    if (on_tensor_cores(d, act_bf16)) {
+        want = sm_count() / ssm_tc_units(d);
+    } else {
+        const int per_sm = d.N * d.P >= 16384 ? 2 : d.N * d.P >= 8192 ? 4 : 8;
+        want = sm_count() * per_sm / d.heads;
+    }
+    return want < 1 ? 1 : want;
 }
 
-int scan_slots(const SsmDims &d) {
-    // resident CTAs: the state takes one register in four of an SM's file at 128 x 128
-    const int per_sm = d.N * d.P >= 16384 ? 2 : d.N * d.P >= 8192 ? 4 : 8;
-    return sm_count() * per_sm;
+// Tokens of a segment: whole chunks of 128, 256 or more.  A batch whose sequences fill the GPU by
+// themselves is then not cut: none of them is longer than its share of T.
+long long segment_len(const SsmDims &d, bool act_bf16, long long T) {
+    const int want = segments_wanted(d, act_bf16);
+    const long long len = ((T + want - 1) / want + 127) / 128 * 128;
+    return len < 256 ? 256 : len;
 }
 
 // Sequences of k >= 2 segments keep k entering states, and have more than
@@ -350,47 +358,40 @@ ScanWs scan_ws(const SsmDims &d, long long entries, long long n_seqs) {
 }
 
 template <int N, int P, typename TA>
-cudaError_t run_scan(const SsmScanArgs &a, cudaStream_t s) {
+cudaError_t run_scan(const SsmScanArgs &a, bool states, unsigned segments, cudaStream_t s) {
     constexpr int NT = ScanShape<N, P>::NT;
-    const bool cut = a.seg_len < a.T;
-    const unsigned segs = cut ? (unsigned)(a.n_seqs + a.max_enter) : (unsigned)a.n_seqs;
-    const dim3 grid(a.d.heads * segs);     // the heads of a group side by side: B and C come from L2
-    if (cut) {
-        ssm_segment_map_kernel<<<1, 1024, 0, s>>>(a);
-        ssm_scan_kernel<N, P, TA, true><<<grid, NT, 0, s>>>(a);
-        const dim3 chain(a.d.heads, (N * P / 4 + 255) / 256, a.n_seqs < 32 ? a.n_seqs : 32);
-        ssm_chain_states_kernel<<<chain, 256, 0, s>>>(a);
-    }
-    ssm_scan_kernel<N, P, TA, false><<<grid, NT, 0, s>>>(a);
+    const unsigned grid = a.d.heads * segments;   // the heads of a group side by side: B and C come from L2
+    if (states) ssm_scan_kernel<N, P, TA, true><<<grid, NT, 0, s>>>(a);
+    else ssm_scan_kernel<N, P, TA, false><<<grid, NT, 0, s>>>(a);
     return cudaGetLastError();
 }
 
-template <int N, typename TA> cudaError_t run_scan_p(const SsmScanArgs &a, cudaStream_t s) {
+template <int N, typename TA> cudaError_t run_scan_p(const SsmScanArgs &a, bool states, unsigned segments, cudaStream_t s) {
     switch (a.d.P) {
-        case 32: return run_scan<N, 32, TA>(a, s);
-        case 64: return run_scan<N, 64, TA>(a, s);
-        default: return run_scan<N, 128, TA>(a, s);
+        case 32: return run_scan<N, 32, TA>(a, states, segments, s);
+        case 64: return run_scan<N, 64, TA>(a, states, segments, s);
+        default: return run_scan<N, 128, TA>(a, states, segments, s);
     }
 }
-template <typename TA> cudaError_t run_scan_np(const SsmScanArgs &a, cudaStream_t s) {
+template <typename TA> cudaError_t run_scan_np(const SsmScanArgs &a, bool states, unsigned segments, cudaStream_t s) {
     switch (a.d.N) {
-        case 16: return run_scan_p<16, TA>(a, s);
-        case 32: return run_scan_p<32, TA>(a, s);
-        case 64: return run_scan_p<64, TA>(a, s);
-        default: return run_scan_p<128, TA>(a, s);
+        case 16: return run_scan_p<16, TA>(a, states, segments, s);
+        case 32: return run_scan_p<32, TA>(a, states, segments, s);
+        case 64: return run_scan_p<64, TA>(a, states, segments, s);
+        default: return run_scan_p<128, TA>(a, states, segments, s);
     }
 }
 
 }  // namespace
 
-// Grows with T: segments are 256 tokens or longer, and no more than `slots` of them per batch.
-size_t ssm_scan_ws_bytes(const SsmDims &d, bool, long long T, long long n_seqs) {
-    const long long most = scan_slots(d) / d.heads;
-    return scan_ws(d, 2 * (T / 256 < most ? T / 256 : most), n_seqs).size;
+// Grows with T: segments are 256 tokens or longer, and a batch has no more than are wanted.
+size_t ssm_scan_ws_bytes(const SsmDims &d, bool act_bf16, long long T, long long n_seqs) {
+    const long long most = segments_wanted(d, act_bf16);
+    return most < 2 ? 0 : scan_ws(d, 2 * (T / 256 < most ? T / 256 : most), n_seqs).size;
 }
 
-size_t ssm_scan_carve(SsmScanArgs &a, bool, void *ws) {
-    a.seg_len = segment_len(a.d, a.T, scan_slots(a.d));
+size_t ssm_scan_carve(SsmScanArgs &a, bool act_bf16, void *ws) {
+    a.seg_len = segment_len(a.d, act_bf16, a.T);
     a.max_enter = (int)max_entries(a.T, a.seg_len);
     const ScanWs w = scan_ws(a.d, a.max_enter, a.n_seqs);
     char *p = (char *)ws;
@@ -403,7 +404,22 @@ size_t ssm_scan_carve(SsmScanArgs &a, bool, void *ws) {
 }
 
 cudaError_t launch_ssm_scan(const SsmScanArgs &a, bool act_bf16, cudaStream_t s) {
-    return act_bf16 ? run_scan_np<__nv_bfloat16>(a, s) : run_scan_np<float>(a, s);
+    const bool cut = a.seg_len < a.T;
+    const unsigned segments = cut ? (unsigned)(a.n_seqs + a.max_enter) : (unsigned)a.n_seqs;
+    auto pass = [&](bool states) {
+        if (on_tensor_cores(a.d, act_bf16)) return launch_ssm_scan_tc(a, states, segments, s);
+        return act_bf16 ? run_scan_np<__nv_bfloat16>(a, states, segments, s) : run_scan_np<float>(a, states, segments, s);
+    };
+    if (cut) {
+        ssm_segment_map_kernel<<<1, 1024, 0, s>>>(a);
+        cudaError_t e = cudaGetLastError();
+        if (e == cudaSuccess) e = pass(true);
+        if (e != cudaSuccess) return e;
+        const dim3 chain(a.d.heads, (a.d.N * a.d.P / 4 + 255) / 256, a.n_seqs < 32 ? a.n_seqs : 32);
+        ssm_chain_states_kernel<<<chain, 256, 0, s>>>(a);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    return pass(false);
 }
 
 }  // namespace gdn
