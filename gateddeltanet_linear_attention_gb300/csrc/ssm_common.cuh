@@ -43,40 +43,117 @@ __device__ __forceinline__ float ssm_dt(float raw, float bias, const SsmDims &d)
     return fminf(fmaxf(softplus_f(raw + bias), d.dt_min), d.dt_max);
 }
 
-// Segment `b` of the batch: its sequence, tokens [t0, t1), whether it is the sequence's first or
-// last one, the state slot (-1: padding lane) and the entry of `enter` that holds the state it
-// starts from (-1: it starts from state_in).  False: nothing to do.
+// How a batch is cut: every sequence has one segment or more (one of an empty sequence), and a
+// sequence of two or more keeps the states that enter them, side by side in `enter`.  Batches of
+// up to kWarpSeqs sequences are laid out by every warp for itself, longest sequence first so that
+// the last CTAs to start are short ones; larger ones in order, by ssm_segment_map_kernel if cut.
+constexpr int kWarpSeqs = 32;
+struct SsmCut {
+    int seg0, segs, entry0;           // first segment, segments; first entry of `enter`, -1: none
+    int front0;                       // segments before it that are not their sequence's last
+};
+// The cut of sequence `lane` (n_seqs <= kWarpSeqs; a whole warp calls it).
+__device__ __forceinline__ SsmCut ssm_warp_cut(const SsmScanArgs &a, int lane) {
+    long long len = -1;
+    if (lane < a.n_seqs) {
+        long long s, e;
+        seq_bounds(a.cu, lane, a.T, a.err, s, e);
+        len = e - s;
+    }
+    const int segs = lane >= a.n_seqs ? 0 : len <= a.seg_len ? 1 : (int)((len + a.seg_len - 1) / a.seg_len);
+    SsmCut c{0, segs, 0, 0};
+    for (int m = 0; m < a.n_seqs; ++m) {
+        const long long other = __shfl_sync(0xffffffffu, len, m);
+        const int count = __shfl_sync(0xffffffffu, segs, m);
+        if (other > len || (other == len && m < lane)) {
+            c.seg0 += count;
+            c.entry0 += count > 1 ? count : 0;
+            c.front0 += count - 1;
+        }
+    }
+    if (segs < 2) c.entry0 = -1;
+    return c;
+}
+
+// Segment `b` of the batch, or (FRONT) of its segments that are not their sequence's last: its
+// sequence, tokens [t0, t1), whether it is the sequence's first or last one, the state slot (-1:
+// padding lane) and the entry of `enter` that holds the state it starts from (-1: it starts from
+// state_in).  False: nothing to do.  Whole warps call it.
 struct SsmSegment {
     int seq, slot, entry;
     long long t0, t1;
     bool first, last;
 };
-__device__ __forceinline__ bool ssm_segment(const SsmScanArgs &a, int b, SsmSegment &g) {
-    long long s, e;
-    if (a.seg_len >= a.T) {
-        g.seq = b;
-        seq_bounds(a.cu, b, a.T, a.err, s, e);
-        g.t0 = s; g.t1 = e; g.first = g.last = true; g.entry = -1;
-    } else {
-        if (b >= a.seg_base[a.n_seqs]) return false;
+template <bool FRONT> __device__ __forceinline__ bool ssm_segment(const SsmScanArgs &a, int b, SsmSegment &g) {
+    SsmCut c{b, 1, -1, 0};
+    g.seq = b;
+    int k = 0;
+    if (a.n_seqs <= kWarpSeqs) {
+        c = ssm_warp_cut(a, threadIdx.x & 31);
+        k = FRONT ? b - c.front0 : b - c.seg0;
+        const unsigned mine = __ballot_sync(0xffffffffu, k >= 0 && k < (FRONT ? c.segs - 1 : c.segs));
+        if (mine == 0) return false;
+        g.seq = __ffs(mine) - 1;
+        k = __shfl_sync(0xffffffffu, k, g.seq);
+        c.segs = __shfl_sync(0xffffffffu, c.segs, g.seq);
+        c.entry0 = __shfl_sync(0xffffffffu, c.entry0, g.seq);
+    } else if (a.seg_len < a.T) {
+        // seg_base[n], less n for the front segments: every sequence has one last segment
+        if (b >= a.seg_base[a.n_seqs] - (FRONT ? a.n_seqs : 0)) return false;
         int lo = 0, hi = a.n_seqs - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (a.seg_base[mid] <= b) lo = mid; else hi = mid - 1;
+            if (a.seg_base[mid] - (FRONT ? mid : 0) <= b) lo = mid; else hi = mid - 1;
         }
         g.seq = lo;
-        seq_bounds(a.cu, lo, a.T, a.err, s, e);
-        const int k = b - a.seg_base[lo], count = a.seg_base[lo + 1] - a.seg_base[lo];
-        // malformed lengths (already reported): what has no room is not run
-        if (count > 1 && a.enter_base[lo] + count > a.max_enter) return false;
-        g.t0 = s + (long long)k * a.seg_len;
-        g.t1 = g.t0 + a.seg_len < e ? g.t0 + a.seg_len : e;
-        g.first = k == 0;
-        g.last = k == count - 1;
-        g.entry = count > 1 ? a.enter_base[lo] + k : -1;
+        k = b - (a.seg_base[lo] - (FRONT ? lo : 0));
+        c.segs = a.seg_base[lo + 1] - a.seg_base[lo];
+        if (c.segs > 1) c.entry0 = a.enter_base[lo];
     }
+    // malformed lengths (reported below or by the map): what has no room is not run
+    if (c.entry0 >= 0 && c.entry0 + c.segs > a.max_enter) {
+        set_error(a.err, GDN_DEVERR_CU_SEQLENS);
+        return false;
+    }
+    long long s, e;
+    seq_bounds(a.cu, g.seq, a.T, a.err, s, e);
+    g.t0 = s + (long long)k * a.seg_len;
+    g.t1 = g.t0 + a.seg_len < e ? g.t0 + a.seg_len : e;
+    if (g.t0 > g.t1) return false;
+    g.first = k == 0;
+    g.last = k == c.segs - 1;
+    g.entry = c.entry0 >= 0 ? c.entry0 + k : -1;
     g.slot = slot_of(a.state_idx, g.seq, a.d.n_slots, a.err);
     return true;
+}
+
+// Two packed fp32 values: one instruction for two multiply-adds.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(f32x2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
 // Sigmoid and SiLU of values that end in the type T: through the approximate exp and quotient
@@ -132,6 +209,26 @@ struct SsmStepArgs {
     SsmDims d;
     unsigned *err;
 };
+
+// Launch a kernel that may start before the one in front of it in the stream ends
+// (programmatic dependent launch).  It calls await_previous() before it touches what that one
+// writes, and at the latest before it ends, so that the order of the stream holds for what follows.
+template <typename... A>
+cudaError_t launch_early(void (*kernel)(A...), dim3 grid, int threads, int smem, cudaStream_t s, const A &...args) {
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+__device__ __forceinline__ void await_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // Workspace for up to T tokens and n_seqs sequences; and the cut of a batch, its arrays laid out
 // in ws (unless null), with the bytes that this batch needs.

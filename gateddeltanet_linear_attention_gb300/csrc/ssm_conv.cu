@@ -184,7 +184,7 @@ cudaError_t launch_ssm_conv(const SsmConvArgs &a, bool act_bf16, cudaStream_t s)
 template <typename TA>
 __global__ void __launch_bounds__(256) ssm_step_conv_kernel(SsmStepArgs a) {
     // the state kernel may start loading states now; it waits for this grid before it reads `ws`
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    let_next_start();
     const SsmDims &d = a.d;
     const int n = blockIdx.y, c = blockIdx.x * 256 + threadIdx.x;
     if (c >= d.ch) return;
@@ -217,6 +217,7 @@ __global__ void __launch_bounds__(kStepThreads) ssm_step_state_kernel(SsmStepArg
     TA *y = (TA *)a.y + ((long long)n * d.heads + h) * P;
     if (slot < 0) {
         if (tid < LP) store4f(y + p0, make_float4(0.f, 0.f, 0.f, 0.f));
+        await_previous();
         return;
     }
     float *S = a.state + ((long long)slot * d.heads + h) * N * P;
@@ -228,7 +229,7 @@ __global__ void __launch_bounds__(kStepThreads) ssm_step_state_kernel(SsmStepArg
     const float dec = expf(-expf(a.A_log[h]) * dt), skip = a.D ? a.D[h] : 0.f;
     float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
     if (a.z && tid < LP) z = load4f((const TA *)a.z + (long long)n * a.ld_z + (long long)h * P + p0);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    await_previous();
     const float *row = a.ws + (long long)n * d.ch;
     const float *B = row + d.heads * P + g * N, *C = B + d.groups * N;
     const float4 x = load4f(row + h * P + p0);
@@ -273,16 +274,7 @@ template <int N, int P, typename TA> cudaError_t run_step(const SsmStepArgs &a, 
     ssm_step_conv_kernel<TA><<<dim3((a.d.ch + 255) / 256, a.n), 256, 0, s>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute early{};
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(a.d.heads * (P / 32), a.n);
-    cfg.blockDim = dim3(kStepThreads);
-    cfg.stream = s;
-    cfg.attrs = &early;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, ssm_step_state_kernel<N, P, TA>, a);
+    return launch_early(ssm_step_state_kernel<N, P, TA>, dim3(a.d.heads * (P / 32), a.n), kStepThreads, 0, s, a);
 }
 template <int N, typename TA> cudaError_t run_step_p(const SsmStepArgs &a, cudaStream_t s) {
     switch (a.d.P) {

@@ -19,29 +19,6 @@ namespace {
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// Two packed fp32 values: one instruction for two multiply-adds.
-typedef unsigned long long f32x2;
-__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
-    f32x2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ float2 unpack2(f32x2 v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-    f32x2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-    f32x2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
 }  // namespace
 
 // ------------------------------------------------------------- segment map
@@ -53,7 +30,7 @@ __global__ void __launch_bounds__(1024) ssm_segment_map_kernel(SsmScanArgs a) {
     __shared__ long long ws_seg[32], ws_ent[32];   // 64 bits: malformed lengths may sum to any size
     __shared__ long long run_seg, run_ent;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const long long max_seg = (long long)a.n_seqs + a.max_enter, max_ent = a.max_enter;
+    const long long max_seg = (long long)a.n_seqs + a.max_enter / 2, max_ent = a.max_enter;
     if (tid == 0) run_seg = run_ent = 0;
     __syncthreads();
     for (int n0 = 0; n0 < a.n_seqs; n0 += 1024) {
@@ -105,27 +82,56 @@ __global__ void __launch_bounds__(1024) ssm_segment_map_kernel(SsmScanArgs a) {
 // ------------------------------------------------------------ chained states
 // enter[0] = the initial state, enter[k+1] = exp(log-decay of segment k) *
 // enter[k] + (what pass 1 left in enter[k+1]); one thread per float4 of a head.
+// The loads of kAhead segments are in flight at once: only the multiply-adds
+// form a chain.
 __global__ void __launch_bounds__(256) ssm_chain_states_kernel(SsmScanArgs a) {
-    const int h = blockIdx.x, vec = a.d.N * a.d.P / 4;
+    constexpr int kAhead = 8;
+    let_next_start();
+    const int h = blockIdx.x, vec = a.d.N * a.d.P / 4, lane = threadIdx.x & 31;
     const int i = blockIdx.y * 256 + threadIdx.x;
-    if (i >= vec) return;
     const long long head = (long long)a.d.N * a.d.P, all = head * a.d.heads;
-    for (int n = blockIdx.z; n < a.n_seqs; n += gridDim.z) {
-        const int e0 = a.enter_base[n];
-        int e1 = a.enter_base[n + 1];
-        const int segs = a.seg_base[n + 1] - a.seg_base[n];
-        if (e1 - e0 < 2 || segs < 2) continue;
+    const bool small = a.n_seqs <= kWarpSeqs;
+    SsmCut mine{0, 0, -1};
+    if (small) mine = ssm_warp_cut(a, lane);
+    await_previous();
+    unsigned cut = __ballot_sync(0xffffffffu, small && mine.segs > 1);
+    for (int n = blockIdx.z, turn = 0;; n += gridDim.z) {
+        int e0, segs;
+        if (small) {                                   // the sequences of two segments or more in turn
+            if (cut == 0) break;
+            n = __ffs(cut) - 1;
+            cut &= cut - 1;
+            if (turn++ % gridDim.z != blockIdx.z) continue;
+            e0 = __shfl_sync(0xffffffffu, mine.entry0, n);
+            segs = __shfl_sync(0xffffffffu, mine.segs, n);
+        } else {
+            if (n >= a.n_seqs) break;
+            e0 = a.enter_base[n];
+            segs = a.seg_base[n + 1] - a.seg_base[n];
+        }
+        if (segs < 2 || e0 + segs > a.max_enter) continue;     // (too many: malformed, reported)
         const int slot = slot_of(a.state_idx, n, a.d.n_slots, a.err);
-        if (slot < 0) continue;
+        if (slot < 0 || i >= vec) continue;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         if (a.state_in) v = load4f(a.state_in + (long long)slot * all + h * head + 4 * i);
-        store4f(a.enter + (long long)e0 * all + h * head + 4 * i, v);
-        for (int e = e0 + 1; e < e1; ++e) {
-            float *at = a.enter + (long long)e * all + h * head + 4 * i;
-            const float4 u = load4f(at);
-            const float k = expf(a.seg_log[(long long)(e - 1) * a.d.heads + h]);
-            v = make_float4(fmaf(k, v.x, u.x), fmaf(k, v.y, u.y), fmaf(k, v.z, u.z), fmaf(k, v.w, u.w));
-            store4f(at, v);
+        float *at = a.enter + (long long)e0 * all + h * head + 4 * i;
+        store4f(at, v);
+        for (int k0 = 1; k0 < segs; k0 += kAhead) {
+            float4 u[kAhead];
+            float g[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (k0 + k < segs) {
+                    u[k] = load4f(at + (k0 + k) * all);
+                    g[k] = a.seg_log[(long long)(e0 + k0 + k - 1) * a.d.heads + h];
+                }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (k0 + k < segs) {
+                    const float f = expf(g[k]);
+                    v = make_float4(fmaf(f, v.x, u[k].x), fmaf(f, v.y, u[k].y), fmaf(f, v.z, u[k].z), fmaf(f, v.w, u[k].w));
+                    store4f(at + (k0 + k) * all, v);
+                }
         }
     }
 }
@@ -164,7 +170,11 @@ __global__ void __launch_bounds__(ScanShape<N, P>::NT) ssm_scan_kernel(SsmScanAr
     const SsmDims &d = a.d;
     const int tid = threadIdx.x, h = blockIdx.x % d.heads, g = h / d.per;
     SsmSegment sg;
-    if (!ssm_segment(a, blockIdx.x / d.heads, sg)) return;
+    let_next_start();
+    const bool run = ssm_segment<STATES>(a, blockIdx.x / d.heads, sg);
+    // a segment that starts from an initial state needs nothing of the passes in front of this one
+    if (!STATES && (!run || sg.entry >= 0 || sg.slot < 0)) await_previous();
+    if (!run) return;
     if (STATES && (sg.last || sg.slot < 0)) return;
     const long long out_cols = (long long)d.heads * P;
     if (sg.slot < 0) {
@@ -309,6 +319,7 @@ __global__ void __launch_bounds__(ScanShape<N, P>::NT) ssm_scan_kernel(SsmScanAr
                     make_float4(q0.y, q1.y, q2.y, q3.y));
         }
     }
+    if (!STATES) await_previous();
     if (STATES && tid == 0) a.seg_log[(long long)sg.entry * d.heads + h] = (float)log_sum;
 }
 
@@ -361,6 +372,7 @@ template <int N, int P, typename TA>
 cudaError_t run_scan(const SsmScanArgs &a, bool states, unsigned segments, cudaStream_t s) {
     constexpr int NT = ScanShape<N, P>::NT;
     const unsigned grid = a.d.heads * segments;   // the heads of a group side by side: B and C come from L2
+    if (!states && a.seg_len < a.T) return launch_early(ssm_scan_kernel<N, P, TA, false>, dim3(grid), NT, 0, s, a);
     if (states) ssm_scan_kernel<N, P, TA, true><<<grid, NT, 0, s>>>(a);
     else ssm_scan_kernel<N, P, TA, false><<<grid, NT, 0, s>>>(a);
     return cudaGetLastError();
@@ -405,19 +417,24 @@ size_t ssm_scan_carve(SsmScanArgs &a, bool act_bf16, void *ws) {
 
 cudaError_t launch_ssm_scan(const SsmScanArgs &a, bool act_bf16, cudaStream_t s) {
     const bool cut = a.seg_len < a.T;
-    const unsigned segments = cut ? (unsigned)(a.n_seqs + a.max_enter) : (unsigned)a.n_seqs;
+    // with states only: the segments that are not their sequence's last
+    const unsigned all = cut ? (unsigned)(a.n_seqs + a.max_enter / 2) : (unsigned)a.n_seqs;
     auto pass = [&](bool states) {
+        const unsigned segments = states ? (unsigned)(a.max_enter / 2) : all;
         if (on_tensor_cores(a.d, act_bf16)) return launch_ssm_scan_tc(a, states, segments, s);
         return act_bf16 ? run_scan_np<__nv_bfloat16>(a, states, segments, s) : run_scan_np<float>(a, states, segments, s);
     };
     if (cut) {
-        ssm_segment_map_kernel<<<1, 1024, 0, s>>>(a);
-        cudaError_t e = cudaGetLastError();
+        cudaError_t e = cudaSuccess;
+        if (a.n_seqs > kWarpSeqs) {
+            ssm_segment_map_kernel<<<1, 1024, 0, s>>>(a);
+            e = cudaGetLastError();
+        }
         if (e == cudaSuccess) e = pass(true);
+        const int most = a.n_seqs <= kWarpSeqs ? a.max_enter / 2 : 32;          // sequences that are cut
+        const dim3 chain(a.d.heads, (a.d.N * a.d.P / 4 + 255) / 256, a.n_seqs < most ? a.n_seqs : most);
+        if (e == cudaSuccess) e = launch_early(ssm_chain_states_kernel, chain, 256, 0, s, a);
         if (e != cudaSuccess) return e;
-        const dim3 chain(a.d.heads, (a.d.N * a.d.P / 4 + 255) / 256, a.n_seqs < 32 ? a.n_seqs : 32);
-        ssm_chain_states_kernel<<<chain, 256, 0, s>>>(a);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     return pass(false);
 }

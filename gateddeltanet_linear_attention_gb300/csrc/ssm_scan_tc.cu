@@ -17,18 +17,18 @@
 // Y2 reads are rounded to bf16 (half a step each, like y itself).  The state is
 // a 32-bit output that goes on for the whole sequence: it stays in fp32 and is
 // updated by fp32 multiply-adds outside the tensor core, and w x enters dS in
-// three bf16 parts (2^-26 of each value), smallest first, in a fresh
+// three bf16 parts (all its 24 bits), smallest first, in a fresh
 // accumulator per chunk: the tensor core truncates its sums, which would bias a
 // state that it carried along itself.  w comes from a suffix sum of the
 // log-decays (exact where it matters, near the chunk's end).  Log-decays are
 // clamped at -60 a token: exp(-60) is nothing beside what the token adds, and
 // differences of running sums keep their meaning.
 //
-// Roles (24 warps, one CTA per SM): warp 0 loads tiles by TMA, warp 1 issues
-// the products, warp 2 stores y by TMA; A: log-decays, then G -> P; B: the
-// state; C (two groups of 64 columns): Y2's scaling, the skip, the gate, y;
-// D: the parts of w X.  Tiles (128 tokens x 128 columns, 128-byte swizzle) go
-// through one ring in the order C, B, X, z; y leaves in the place of X.
+// Roles (30 or 32 warps, one CTA per SM): warp 0 loads tiles by TMA, warp 1
+// issues G, Y2 and P X, warp 3 dS, warp 2 stores y by TMA; E (a warp per head
+// and chunk parity): the log-decays' sums and their exponentials, up to two
+// chunks ahead; A: G -> P; B: the state; C (two groups of 64 columns): Y2's scaling, the skip, the gate, y;
+// D (two groups, 16 tokens each in turn): the parts of w X.
 //
 // Bound by instruction issue (conversions between TMEM, registers and shared
 // memory), not by memory or the tensor cores.
@@ -44,8 +44,8 @@ namespace gdn {
 namespace {
 
 constexpr int kL = 128;                        // tokens of a chunk
-constexpr int kThreads = 24 * 32;
-constexpr int kSlots = 5;
+template <int HU> constexpr int kThreads = (28 + 2 * HU) * 32;
+constexpr int kSlots = 5;                      // C, two of B, two of X
 constexpr int kTile = kL * 128 * 2;            // bytes of a ring slot
 constexpr int kHalfTile = kTile / 2;           // 128 rows x 128 bytes: one TMA box
 constexpr int kXwPart = 16 * 128 * 2;          // one bf16 part of w X for 16 tokens (MN-major)
@@ -60,10 +60,11 @@ template <int N, int HU> struct TcSmem {
     static constexpr int RING = 0;
     static constexpr int S = RING + kSlots * kTile;          // bf16 state, 128 rows (value columns) x N
     static constexpr int XW = S + N * 256;
-    static constexpr int ARR = XW + 2 * kXwBuf;              // [2][HU][3][128]: cp, w, e
-    static constexpr int SUM = ARR + 2 * HU * 3 * 512;       // [2][HU][4] warp sums, then [2][HU] decays
-    static constexpr int BAR = SUM + 2 * HU * 4 * 4 + 2 * HU * 4;
-    static constexpr int NBAR = 2 * kSlots + 20;
+    static constexpr int ARR = XW + 2 * kXwBuf;              // [2][HU][4][128]: cs, cp, w, e
+    static constexpr int DEC = ARR + 2 * HU * 4 * 512;       // [2][HU] chunk decays
+    static constexpr int LOG = DEC + 2 * HU * 4;             // [2][HU] doubles: summed log-decays
+    static constexpr int BAR = LOG + 2 * HU * 8;
+    static constexpr int NBAR = 2 * kSlots + 22;
     static constexpr int SLOT = (BAR + 7) / 8 * 8 + NBAR * 8;
     static constexpr int BYTES = SLOT + 16;
     static_assert(BYTES <= 232448, "shared memory of an SM");
@@ -71,10 +72,10 @@ template <int N, int HU> struct TcSmem {
 
 // Barriers behind the ring's full[] and empty[].
 // Where a waiter may be a phase
-// behind (DS, A, ST), even and odd chunks have a barrier each: the next phase of either then
+// behind (G, DS, Y, A, ST), even and odd chunks have a barrier each: the next phase of either then
 // needs the waiter's own progress.
-enum { B_G = 0, B_P, B_S, B_XF0, B_XF1, B_XE0, B_XE1, B_DS0, B_DS1, B_Y2, B_YC, B_Y, B_YE, B_A0, B_A1, B_ST0, B_ST1,
-       B_WG, B_FIX, B_END, B_COUNT };
+enum { B_G0 = 0, B_G1, B_P, B_S, B_XF0, B_XF1, B_XE0, B_XE1, B_DS0, B_DS1, B_Y2, B_YC, B_Y0, B_Y1, B_YE, B_A0, B_A1, B_ST0, B_ST1,
+       B_FIX, B_END, B_END2, B_COUNT };
 
 // 128-byte-swizzled operands: rows of 128 bytes, 8-row groups of 1,024 bytes, 64-element blocks
 // kHalfTile apart.  K-major: the row index is M or N, a 16-wide K step is 32 bytes further.
@@ -88,17 +89,6 @@ __device__ __forceinline__ uint64_t step_k(int ks) { return (uint64_t)((ks >> 2)
 __device__ __forceinline__ uint64_t step_mn(int ks) { return (uint64_t)(ks * 128); }
 
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
-        :: "r"(taddr), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
-           "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]),
-           "f"(v[16]), "f"(v[17]), "f"(v[18]), "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]),
-           "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]), "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31])
-        : "memory");
-}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -107,15 +97,125 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
            "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
-__device__ __forceinline__ void tma_store_2d(const void *tmap, uint32_t src_saddr, int x, int y) {
-    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];"
-                 :: "l"(tmap), "r"(src_saddr), "r"(x), "r"(y) : "memory");
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 :: "r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
 }
-// 2^x, two units in the last place at most: its results are rounded to bf16.
+__device__ __forceinline__ void tmem_st16f(uint32_t taddr, const float (&v)[16]) {
+    uint32_t r[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[i]);
+    tmem_st16(taddr, r);
+}
+// Two loads of 16 columns behind one wait.
+__device__ __forceinline__ void tmem_ld16x2(uint32_t t0, uint32_t t1, float (&a)[16], float (&b)[16]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(t0), "r"(t1) : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) { a[i] = __uint_as_float(r[i]); b[i] = __uint_as_float(r[16 + i]); }
+}
+// 2^x to two units in the last place.  exp(x) through it is off by |x| 2^-24 more: for the weights
+// of a state that is at most 2^-25 of the largest one, |x| exp(x) being below 0.37.
 __device__ __forceinline__ float exp2_fast(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
+}
+// A bounded wait.  Waiting warps share the issue slots and the instruction cache with the working
+// ones: a poll is a few instructions, and the wall clock is read out of line, once in 256 polls.
+__device__ __forceinline__ uint32_t poll256(uint32_t b, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+        "mov.u32 n, 256;\n\t"
+        "POLL%=:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra DONE%=;\n\t"
+        "sub.u32 n, n, 1;\n\t"
+        "setp.ne.u32 q, n, 0;\n\t"
+        "@q bra POLL%=;\n\t"
+        "DONE%=:\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(done) : "r"(b), "r"(parity) : "memory");
+    return done;
+}
+// A wait that ran out sets the CTA's flag: the roles then run on without waiting (over their own
+// tiles and rows, with no copy started), the state is not stored, and the error is reported.
+__device__ __noinline__ void poll_to_limit(uint32_t b, uint32_t parity, uint64_t limit_ns, volatile uint32_t *gave_up) {
+    const uint64_t t0 = tc::globaltimer_ns();
+    while (!*gave_up) {
+        if (poll256(b, parity)) return;
+        if (tc::globaltimer_ns() - t0 > limit_ns) *gave_up = 1;
+    }
+}
+__device__ __noinline__ void poll_some(uint32_t b, uint32_t parity, uint64_t limit_ns) {
+    const uint64_t t0 = tc::globaltimer_ns();
+    while (!poll256(b, parity) && tc::globaltimer_ns() - t0 <= limit_ns) {}
+}
+// Products, commits, copies and arrivals of one lane (`lead`) of a warp that stays together: the
+// instructions take their operands from warp-uniform registers, and in a branch of one lane the
+// compiler would move every operand there in a loop of its own (several times the product's time).
+__device__ __forceinline__ uint32_t elect_lane() {
+    uint32_t lead;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(lead));
+    return lead;
+}
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n"
+        :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead) : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n"
+        :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead) : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t lead, uint32_t b) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n"
+        :: "r"(b), "r"(lead) : "memory");
+}
+__device__ __forceinline__ void arrive(uint32_t lead, uint32_t b) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t@q mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}\n"
+        :: "r"(b), "r"(lead) : "memory");
+}
+__device__ __forceinline__ void expect_tx(uint32_t lead, uint32_t b, uint32_t bytes) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}\n"
+        :: "r"(b), "r"(bytes), "r"(lead) : "memory");
+}
+__device__ __forceinline__ void tma_load(uint32_t lead, uint32_t dst, const void *tmap, int x, int y, uint32_t b) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n\t}\n"
+        :: "r"(dst), "l"(tmap), "r"(x), "r"(y), "r"(b), "r"(lead) : "memory");
+}
+__device__ __forceinline__ void tma_store(uint32_t lead, const void *tmap, uint32_t src, int x, int y) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %4, 0;\n\t"
+        "@q cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];\n\t}\n"
+        :: "l"(tmap), "r"(src), "r"(x), "r"(y), "r"(lead) : "memory");
+}
+__device__ __forceinline__ void tma_prefetch(uint32_t lead, const void *tmap, int x, int y) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %3, 0;\n\t"
+        "@q cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];\n\t}\n"
+        :: "l"(tmap), "r"(x), "r"(y), "r"(lead) : "memory");
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
@@ -123,55 +223,82 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+__device__ __forceinline__ f32x2 bf16_pair(uint32_t v) { return pack2(bf16_lo(v), bf16_hi(v)); }
+__device__ __forceinline__ uint32_t pack_bf16(f32x2 v) {
+    const float2 f = unpack2(v);
+    return pack_bf16(f.x, f.y);
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// v SiLU(z): approximate exp and reciprocal, two values at a time.
+__device__ __forceinline__ f32x2 gate2(f32x2 v, f32x2 z) {
+    const float2 t = unpack2(mul2(z, pack2(-kLog2e, -kLog2e)));
+    const float2 q = unpack2(add2(pack2(exp2_fast(t.x), exp2_fast(t.y)), pack2(1.f, 1.f)));
+    return mul2(v, mul2(z, pack2(rcp_fast(q.x), rcp_fast(q.y))));
+}
 
 }  // namespace
+
+// TMEM column of P's tokens 16 j .. 16 j + 15 (8 columns, two tokens each) of a unit's head: in the
+// 16 columns that G's tokens 16 j .. had, so that a warp overwrites only what it has read.
+__device__ __forceinline__ uint32_t p_col(int j, int hh) { return kColG + 16 * j + 8 * hh; }
 
 struct SsmMaps {
     CUtensorMap x, b, c, z, y;
 };
 
 template <int N, int HU, bool STATES>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads<HU>, 1)
     ssm_scan_tc_kernel(const __grid_constant__ SsmScanArgs a, const __grid_constant__ SsmMaps maps) {
     using L = TcSmem<N, HU>;
     constexpr int P = 128 / HU;
     static_assert(L::NBAR == 2 * kSlots + B_COUNT, "barriers");
     extern __shared__ __align__(1024) unsigned char sm[];
     const SsmDims &d = a.d;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // (the shuffles tell the compiler that a value is the same in a whole warp)
+    auto uniform = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+    const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
     const int per_group = (d.per + HU - 1) / HU, units = d.groups * per_group;
     const int unit = blockIdx.x % units, g = unit / per_group, k0 = unit % per_group;
     const int h0 = g * d.per + k0 * HU, heads = min(HU, d.per - k0 * HU);
     SsmSegment sg;
-    if (!ssm_segment(a, blockIdx.x / units, sg)) return;
+    let_next_start();
+    const bool run = ssm_segment<STATES>(a, blockIdx.x / units, sg);
+    if (!STATES && (!run || sg.slot < 0)) await_previous();
+    if (!run) return;
     if (STATES && (sg.last || sg.slot < 0)) return;
     const long long out_cols = (long long)d.heads * P;
     if (sg.slot < 0) {
         __nv_bfloat16 *y = (__nv_bfloat16 *)a.y + (long long)h0 * P;
         const int vecs = heads * P / 8;
-        for (long long i = tid; i < (sg.t1 - sg.t0) * vecs; i += kThreads)
+        for (long long i = tid; i < (sg.t1 - sg.t0) * vecs; i += kThreads<HU>)
             *reinterpret_cast<uint4 *>(y + (sg.t0 + i / vecs) * out_cols + (i % vecs) * 8) = make_uint4(0, 0, 0, 0);
         return;
     }
-    const int chunks = (int)((sg.t1 - sg.t0 + kL - 1) / kL);
-    const int tail = (int)((sg.t1 - sg.t0) - (long long)(chunks - 1) * kL);   // tokens of the last chunk
+    const int first = uniform((int)sg.t0);                         // its first token
+    const int chunks = uniform((int)((sg.t1 - sg.t0 + kL - 1) / kL));
+    const int tail = uniform((int)(sg.t1 - sg.t0)) - (chunks - 1) * kL;      // tokens of the last chunk
     const bool partial = chunks > 0 && tail < kL;
     const bool has_z = !STATES && a.z != nullptr;
-    const int tpc = STATES ? 2 : has_z ? 4 : 3;        // tiles of a chunk: [C] B X [z]
-    const int tB = STATES ? 0 : 1, tX = tB + 1, tZ = 3;
 
     const uint32_t sbase = tc::smem_u32(sm), bars = sbase + (L::BAR + 7) / 8 * 8;
     auto bar_full = [&](int s) { return bars + 8u * s; };
     auto bar_empty = [&](int s) { return bars + 8u * (kSlots + s); };
     auto bar = [&](int k) { return bars + 8u * (2 * kSlots + k); };
-    float *arr = reinterpret_cast<float *>(sm + L::ARR);          // [stage][head][cp, w, e][128]
-    float *sums = reinterpret_cast<float *>(sm + L::SUM);         // [stage][head][4]
-    float *decs = sums + 2 * HU * 4;                              // [stage][head]
-    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(sm + L::SLOT);
+    float *arr = reinterpret_cast<float *>(sm + L::ARR);
+    // one of a chunk's arrays (0 cs, 1 cp, 2 w, 3 e, see role E), and its decays
+    auto array = [&](int st, int hh, int k) { return arr + ((st * HU + hh) * 4 + k) * 128; };
+    float *decs = reinterpret_cast<float *>(sm + L::DEC);
+    double *logs = reinterpret_cast<double *>(sm + L::LOG);
+    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(sm + L::SLOT), *gave_up = tmem_slot + 1;
 
     if (tid == 0) {
+        *gave_up = 0;
         for (int s = 0; s < kSlots; ++s) { tc::mbar_init(bar_full(s), 1); tc::mbar_init(bar_empty(s), 1); }
-        const int counts[B_COUNT] = {1, 128, 128, 128, 128, 1, 1, 1, 1, 1, 256, 1, 256, 128, 128, 256, 256, 4, 128, 1};
+        const int counts[B_COUNT] = {1, 1, 128, 128, 128, 128, 1, 1, 1, 1, 1, 256, 1, 1, 256, HU, HU, 256, 256, 128, 1, 1};
         for (int k = 0; k < B_COUNT; ++k) tc::mbar_init(bar(k), counts[k]);
         tc::mbar_fence_init();
     }
@@ -182,19 +309,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
 
-    bool ok = true;
-    // bounded waits; a whole warp agrees on the outcome
-    auto wait1 = [&](uint32_t b, uint32_t parity) { return ok = ok && tc::mbar_wait(b, parity & 1u, a.wait_ns); };
     auto wait = [&](uint32_t b, uint32_t parity) {
-        const bool got = ok && tc::mbar_wait(b, parity & 1u, a.wait_ns);
-        return ok = __all_sync(0xffffffffu, got);
+        if (!poll256(b, parity & 1u)) poll_to_limit(b, parity & 1u, a.wait_ns, gave_up);
+        __syncwarp();
     };
-    // tile j of chunk c: its slot and how often the slot was used before
-    auto slot_of_tile = [&](int c, int j) { return (c * tpc + j) % kSlots; };
-    auto use_of_tile = [&](int c, int j) { return (uint32_t)((c * tpc + j) / kSlots); };
-    auto tile_addr = [&](int c, int j) { return sbase + L::RING + slot_of_tile(c, j) * kTile; };
+    // the slots of a chunk's tiles (also their barriers), and the parity of their use
+    auto slot_b = [&](int c) { return 1 + (c & 1); };
+    auto slot_x = [&](int c) { return 3 + (c & 1); };
+    auto half = [&](int c) { return (uint32_t)c >> 1; };
+    auto tile = [&](int slot) { return sbase + L::RING + slot * kTile; };
+    constexpr int kSlotC = 0;
 
     const int wq = warp & 3;                       // TMEM lanes of a warp: 32 wq ..
     const int row = wq * 32 + lane;
@@ -202,262 +328,218 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == 0) {
         // ------------------------------------------------------------- loads
-        if (lane == 0) {
-            int issued = 0;
-            for (int c = 0; c < chunks && ok; ++c) {
-                const int t = (int)(sg.t0 + (long long)c * kL);
-                for (int j = 0; j < tpc; ++j) {
-                    const int s = slot_of_tile(c, j);
-                    const uint32_t use = use_of_tile(c, j);
-                    if (use > 0 && !wait1(bar_empty(s), use - 1)) break;
-                    const bool bc = j <= tB;               // C or B
-                    const CUtensorMap *m = j == tX ? &maps.x : j == tB ? &maps.b : bc ? &maps.c : &maps.z;
-                    const int col = bc ? g * N : h0 * P, boxes = bc ? N / 64 : 2;
-                    tc::mbar_arrive_expect_tx(bar_full(s), boxes * kHalfTile);
-                    for (int q = 0; q < boxes; ++q)
-                        tc::tma_load_2d(tile_addr(c, j) + q * kHalfTile, m, col + q * 64, t, bar_full(s));
-                    ++issued;
+        const uint32_t lead = elect_lane();
+        auto load = [&](int slot, const CUtensorMap *m, int col, int boxes, int t) {
+            expect_tx(lead, bar_full(slot), boxes * kHalfTile);
+            for (int q = 0; q < boxes; ++q)
+                tma_load(lead, tile(slot) + q * kHalfTile, m, col + q * 64, t, bar_full(slot));
+        };
+        int c = 0;
+#pragma unroll 1
+        for (; c < chunks && !*gave_up; ++c) {
+            const int t = first + c * kL;
+            if (c >= 2) wait(bar_empty(slot_b(c)), half(c) - 1);
+            if (*gave_up) break;
+            load(slot_b(c), &maps.b, g * N, N / 64, t);
+            if (c >= 2) wait(bar_empty(slot_x(c)), half(c) - 1);
+            if (*gave_up) break;
+            load(slot_x(c), &maps.x, h0 * P, 2, t);
+            if (!STATES) {
+                if (c >= 1) wait(bar_empty(kSlotC), c - 1);
+                if (*gave_up) break;
+                load(kSlotC, &maps.c, g * N, N / 64, t);
+                if (has_z) {                           // z goes straight to registers later: into L2 for now
+                    tma_prefetch(lead, &maps.z, h0 * P, t);
+                    tma_prefetch(lead, &maps.z, h0 * P + 64, t);
                 }
             }
-            if (!ok)                                       // copies in flight land before the CTA ends
-                for (int k = max(0, issued - kSlots); k < issued; ++k)
-                    tc::mbar_wait(bar_full(k % kSlots), (uint32_t)(k / kSlots) & 1u, a.wait_ns);
+        }
+        // copies in flight land before the CTA ends (a slot whose last copy was not started runs out)
+        if (*gave_up) {
+            for (int k = max(0, c - 2); k <= min(c, chunks - 1); ++k) {
+                poll_some(bar_full(slot_b(k)), half(k) & 1u, a.wait_ns);
+                if (!STATES) poll_some(bar_full(kSlotC), k & 1u, a.wait_ns);
+                poll_some(bar_full(slot_x(k)), half(k) & 1u, a.wait_ns);
+            }
         }
     } else if (warp == 1) {
-        // ---------------------------------------------------------- products
-        if (lane == 0) {
+        // ------------------------------------------------- products: G, Y2, P X
+        if (!STATES) {
+            const uint32_t lead = elect_lane();
             constexpr uint32_t id_full = tc::idesc_bf16(128, 128);
             constexpr uint32_t id_px = tc::idesc_bf16(128, P) | tc::kTransB;
-            constexpr uint32_t id_ds = tc::idesc_bf16(128, N) | tc::kTransA | tc::kTransB;
-            const uint64_t dS = desc_k(sbase + L::S);
+            const uint64_t dS = desc_k(sbase + L::S), dC = desc_k(tile(kSlotC));
+#pragma unroll 1
             for (int c = 0; c < chunks; ++c) {
-                if (!wait1(bar_full(slot_of_tile(c, tB)), use_of_tile(c, tB))) break;
-                const uint32_t tb = tile_addr(c, tB);
-                if (!STATES) {
-                    if (!wait1(bar_full(slot_of_tile(c, 0)), use_of_tile(c, 0))) break;
-                    if (partial && c == chunks - 1 && !wait1(bar(B_FIX), 0)) break;
-                    tc::fence_after_sync();
-                    const uint64_t dC = desc_k(tile_addr(c, 0)), dB = desc_k(tb);
+                wait(bar_full(kSlotC), c);
+                wait(bar_full(slot_b(c)), half(c));
+                if (partial && c == chunks - 1) wait(bar(B_FIX), 0);
+                tc::fence_after_sync();
+                const uint64_t dB = desc_k(tile(slot_b(c)));
 #pragma unroll
-                    for (int k = 0; k < N / 16; ++k)
-                        tc::mma_bf16(tmem + kColG, dC + step_k(k), dB + step_k(k), id_full, k > 0);
-                    tc::mma_commit(bar(B_G));
-                    if (!wait1(bar(B_S), c) || (c > 0 && !wait1(bar(B_YE), c - 1))) break;
-                    tc::fence_after_sync();
+                for (int k = 0; k < N / 16; ++k) mma_ss(lead, tmem + kColG, dC + step_k(k), dB + step_k(k), id_full, k > 0);
+                commit(lead, bar(B_G0 + (c & 1)));
+                wait(bar(B_S), c);
+                if (c > 0) wait(bar(B_YE), c - 1);
+                tc::fence_after_sync();
 #pragma unroll
-                    for (int k = 0; k < N / 16; ++k)
-                        tc::mma_bf16(tmem + kColY, dC + step_k(k), dS + step_k(k), id_full, k > 0);
-                    tc::mma_commit(bar(B_Y2));
-                    tc::mma_commit(bar_empty(slot_of_tile(c, 0)));
-                } else if (!wait1(bar(B_S), c)) {
-                    break;
+                for (int k = 0; k < N / 16; ++k) mma_ss(lead, tmem + kColY, dC + step_k(k), dS + step_k(k), id_full, k > 0);
+                commit(lead, bar(B_Y2));
+                commit(lead, bar_empty(kSlotC));
+                wait(bar_full(slot_x(c)), half(c));
+                wait(bar(B_YC), c);
+                wait(bar(B_P), c);
+                tc::fence_after_sync();
+#pragma unroll
+                for (int hh = 0; hh < HU; ++hh) {
+                    const uint64_t dX = desc_mn(tile(slot_x(c)) + hh * kHalfTile);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        mma_ts(lead, tmem + kColY + hh * P, tmem + p_col(k, hh), dX + step_mn(k), id_px, 1);
                 }
-                const uint64_t dBt = desc_mn(tb);
-                for (int e = 0; e < 8; ++e) {
-                    const uint32_t use = (uint32_t)(c * 4 + (e >> 1));
-                    if (!wait1(bar(B_XF0 + (e & 1)), use)) break;
-                    tc::fence_after_sync();
-                    const uint32_t xw = sbase + L::XW + (e & 1) * kXwBuf;
-#pragma unroll
-                    for (int part = 2; part >= 0; --part)      // smallest first
-                        tc::mma_bf16(tmem + kColDS, tc::mnmaj_desc(xw + part * kXwPart, 128, 0), dBt + step_mn(e),
-                                     id_ds, e > 0 || part < 2);
-                    tc::mma_commit(bar(B_XE0 + (e & 1)));
-                }
-                if (!ok) break;
-                tc::mma_commit(bar(B_DS0 + (c & 1)));
-                tc::mma_commit(bar_empty(slot_of_tile(c, tB)));
-                if (STATES) {
-                    tc::mma_commit(bar_empty(slot_of_tile(c, tX)));
-                } else {
-                    if (!wait1(bar(B_P), c) || !wait1(bar(B_YC), c)) break;
-                    tc::fence_after_sync();
-#pragma unroll
-                    for (int hh = 0; hh < HU; ++hh) {
-                        const uint64_t dX = desc_mn(tile_addr(c, tX) + hh * kHalfTile);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            tc::mma_bf16_ta(tmem + kColY + hh * P, tmem + kColG + 32 * (k >> 1) + 16 * hh + 8 * (k & 1),
-                                            dX + step_mn(k), id_px, 1);
-                    }
-                    tc::mma_commit(bar(B_Y));
-                }
+                commit(lead, bar(B_Y0 + (c & 1)));
             }
-            tc::mma_commit(bar(B_END));                    // nothing in flight when the CTA ends
-            ok = tc::mbar_wait(bar(B_END), 0, a.wait_ns) && ok;
+            commit(lead, bar(B_END));                      // nothing in flight when the CTA ends
+            wait(bar(B_END), 0);
         }
+    } else if (warp == 3) {
+        // -------------------------------------------------------- product: dS
+        const uint32_t lead = elect_lane();
+        constexpr uint32_t id_ds = tc::idesc_bf16(128, N) | tc::kTransA | tc::kTransB;
+#pragma unroll 1
+        for (int c = 0; c < chunks; ++c) {
+            wait(bar_full(slot_b(c)), half(c));
+            if (partial && c == chunks - 1) wait(bar(B_FIX), 0);
+            if (!STATES) wait(bar(B_G0 + (c & 1)), half(c));   // G has read B too before the slot is given back
+            wait(bar(B_S), c);
+            const uint64_t dBt = desc_mn(tile(slot_b(c)));
+#pragma unroll 1
+            for (int e = 0; e < 8; ++e) {
+                wait(bar(B_XF0 + (e & 1)), (uint32_t)(c * 4 + (e >> 1)));
+                tc::fence_after_sync();
+                const uint64_t dW = tc::mnmaj_desc(sbase + L::XW + (e & 1) * kXwBuf, 128, 0);
+#pragma unroll
+                for (int part = 2; part >= 0; --part)      // smallest first
+                    mma_ss(lead, tmem + kColDS, dW + part * (kXwPart >> 4), dBt + step_mn(e), id_ds, e > 0 || part < 2);
+                commit(lead, bar(B_XE0 + (e & 1)));
+            }
+            commit(lead, bar(B_DS0 + (c & 1)));
+            commit(lead, bar_empty(slot_b(c)));
+            if (STATES) commit(lead, bar_empty(slot_x(c)));
+        }
+        commit(lead, bar(B_END2));
+        wait(bar(B_END2), 0);
     } else if (warp == 2) {
         // ------------------------------------------------------------ y out
-        if (!STATES && lane == 0) {
+        if (!STATES) {
+            const uint32_t lead = elect_lane();
+#pragma unroll 1
             for (int c = 0; c < chunks; ++c) {
-                if (!wait1(bar(B_ST0 + (c & 1)), (uint32_t)(c >> 1))) break;
-                if (!(partial && c == chunks - 1)) {
+                wait(bar(B_ST0 + (c & 1)), half(c));
+                if (!(partial && c == chunks - 1) && !*gave_up) {
                     for (int q = 0; q < heads * P / 64; ++q)
-                        tma_store_2d(&maps.y, tile_addr(c, tX) + q * kHalfTile, h0 * P + q * 64,
-                                     (int)(sg.t0 + (long long)c * kL));
-                    tc::bulk_commit();
+                        tma_store(lead, &maps.y, tile(slot_x(c)) + q * kHalfTile, h0 * P + q * 64, first + c * kL);
+                    tc::bulk_commit();                     // (empty groups in the other lanes)
                     tc::bulk_wait_read_all();
                 }
-                tc::mbar_arrive(bar_empty(slot_of_tile(c, tX)));
-                if (has_z) tc::mbar_arrive(bar_empty(slot_of_tile(c, tZ)));
+                __syncwarp();
+                arrive(lead, bar_empty(slot_x(c)));
             }
             tc::bulk_wait_all();
         }
     } else if (warp >= 4 && warp < 8) {
-        // --------------------------------------------- A: log-decays, G -> P
-        float rate[HU], bias[HU];
-        double log_sum[HU];
+        // ------------------------------------------------------- A: G -> P
+        if (!STATES) {
+#pragma unroll 1
+            for (int c = 0; c < chunks; ++c) {
+                const int st = c & 1;
+                if (partial && c == chunks - 1) {
+                    // rows behind the sequence's end: a neighbour's tokens, whatever they hold
+                    wait(bar_full(slot_b(c)), half(c));
+                    wait(bar_full(slot_x(c)), half(c));
+                    if (row >= tail) {
+                        unsigned char *B = sm + L::RING + slot_b(c) * kTile + row * 128;
+                        unsigned char *X = sm + L::RING + slot_x(c) * kTile + row * 128;
 #pragma unroll
-        for (int hh = 0; hh < HU; ++hh) {
-            const int h = h0 + min(hh, heads - 1);
-            rate[hh] = -expf(a.A_log[h]);
-            bias[hh] = a.dt_bias ? a.dt_bias[h] : 0.f;
-            log_sum[hh] = 0.0;
-        }
-        const __nv_bfloat16 *pdt = (const __nv_bfloat16 *)a.dt;
-        float raw[HU];
-        auto fetch = [&](int c) {
-            const long long t = sg.t0 + (long long)c * kL + row;
+                        for (int k = 0; k < 8; ++k) {
 #pragma unroll
-            for (int hh = 0; hh < HU; ++hh)
-                raw[hh] = t < sg.t1 ? to_f32(pdt[t * a.ld_dt + h0 + min(hh, heads - 1)]) : 0.f;
-        };
-        if (chunks > 0) fetch(0);
-        for (int c = 0; c < chunks; ++c) {
-            const int st = c & 1;
-            const bool valid = sg.t0 + (long long)c * kL + row < sg.t1;
-            float pre[HU], suf[HU], dt[HU];
+                            for (int q = 0; q < N / 64; ++q)
+                                *reinterpret_cast<uint4 *>(B + q * kHalfTile + k * 16) = make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int hh = 0; hh < HU; ++hh) {
-                dt[hh] = valid && hh < heads ? ssm_dt(raw[hh], bias[hh], d) : 0.f;
-                const float lg = valid && hh < heads ? fmaxf(rate[hh] * dt[hh], kMinLog) : 0.f;
-                float p = lg, s = lg;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const float u = __shfl_up_sync(0xffffffffu, p, o), v = __shfl_down_sync(0xffffffffu, s, o);
-                    if (lane >= o) p += u;
-                    if (lane + o < 32) s += v;
+                            for (int q = 0; q < 2; ++q)
+                                *reinterpret_cast<uint4 *>(X + q * kHalfTile + k * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                    tc::fence_async_smem();
+                    tc::mbar_arrive(bar(B_FIX));
                 }
-                if (lane == 31) sums[(st * HU + hh) * 4 + wq] = p;
-                pre[hh] = p;
-                const float after = __shfl_down_sync(0xffffffffu, s, 1);
-                suf[hh] = lane < 31 ? after : 0.f;
-            }
-            if (c + 1 < chunks) fetch(c + 1);
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(bar(B_WG));
-            if (!wait(bar(B_WG), c)) break;
-            // chunk c - 2 is done with this stage of the arrays (C's part by G of chunk
-            // c - 1, which came behind its last product)
-            if (c >= 2 && !wait(bar(B_DS0 + st), (uint32_t)(c >> 1) - 1)) break;
-            float csl[HU];
+                wait(bar(B_A0 + st), half(c));
+                wait(bar(B_G0 + st), half(c));
+                tc::fence_after_sync();
+#pragma unroll 1
+                for (int j = 0; j <= 2 * wq + 1; ++j) {                   // 16 tokens i at a time
+                    float G[16];
+                    tc::tmem_ld16(tmem + lanes + kColG + 16 * j, G);
+                    if (16 * j + 15 > wq * 32) {                          // across the diagonal: i <= r
 #pragma unroll
-            for (int hh = 0; hh < HU; ++hh) {
-                const float4 ws = load4f(sums + (st * HU + hh) * 4);
-                const float w4[4] = {ws.x, ws.y, ws.z, ws.w};
-                float before = 0.f, behind = 0.f;
+                        for (int i = 0; i < 16; ++i) G[i] = 16 * j + i <= row ? G[i] : 0.f;
+                    }
+#pragma unroll 1
+                    for (int hh = 0; hh < HU; ++hh) {
+                        const float csr = array(st, hh, 0)[row];
+                        const f32x2 cs = pack2(csr, csr);
+                        const float *cp = array(st, hh, 1) + 16 * j;
+                        uint32_t p[8];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (k < wq) before += w4[k];
-                    if (3 - k > wq) behind += w4[3 - k];
-                }
-                const float cs = pre[hh] + before;
-                csl[hh] = cs * kLog2e;
-                float *to = arr + ((st * HU + hh) * 3) * 128 + row;
-                to[0] = valid ? csl[hh] - log2f(dt[hh]) : __int_as_float(0x7f800000);
-                to[128] = valid ? expf(suf[hh] + behind) * dt[hh] : 0.f;
-                to[256] = expf(cs);
-                if (row == 0) decs[st * HU + hh] = expf(ws.x + ws.y + ws.z + ws.w);
-                if (STATES) log_sum[hh] += (double)(ws.x + ws.y) + (double)(ws.z + ws.w);
-            }
-            tc::mbar_arrive(bar(B_A0 + st));
-            if (STATES) continue;
-            if (!wait(bar(B_A0 + st), (uint32_t)(c >> 1))) break;
-            if (partial && c == chunks - 1) {
-                // rows behind the sequence's end: a neighbour's tokens, whatever they hold
-                if (!wait(bar_full(slot_of_tile(c, tB)), use_of_tile(c, tB)) ||
-                    !wait(bar_full(slot_of_tile(c, tX)), use_of_tile(c, tX)))
-                    break;
-                if (!valid) {
-                    unsigned char *B = sm + L::RING + slot_of_tile(c, tB) * kTile + row * 128;
-                    unsigned char *X = sm + L::RING + slot_of_tile(c, tX) * kTile + row * 128;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-#pragma unroll
-                        for (int q = 0; q < N / 64; ++q)
-                            *reinterpret_cast<uint4 *>(B + q * kHalfTile + k * 16) = make_uint4(0, 0, 0, 0);
-#pragma unroll
-                        for (int q = 0; q < 2; ++q)
-                            *reinterpret_cast<uint4 *>(X + q * kHalfTile + k * 16) = make_uint4(0, 0, 0, 0);
+                        for (int i = 0; i < 16; i += 4) {
+                            // above the diagonal an exponent may be anything: finite, for G = 0 there
+                            const ulonglong2 k = *reinterpret_cast<const ulonglong2 *>(cp + i);
+                            const float2 u = unpack2(add2(cs, k.x)), v = unpack2(add2(cs, k.y));
+                            p[i / 2] = pack_bf16(mul2(pack2(exp2_fast(fminf(u.x, 126.f)), exp2_fast(fminf(u.y, 126.f))),
+                                                      pack2(G[i], G[i + 1])));
+                            p[i / 2 + 1] = pack_bf16(mul2(pack2(exp2_fast(fminf(v.x, 126.f)), exp2_fast(fminf(v.y, 126.f))),
+                                                          pack2(G[i + 2], G[i + 3])));
+                        }
+                        tmem_st8(tmem + lanes + p_col(j, hh), p);
                     }
                 }
-                tc::fence_async_smem();
-                tc::mbar_arrive(bar(B_FIX));
+                const uint32_t zero[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+#pragma unroll 1
+                for (int j = 2 * wq + 2; j < 8; ++j)                      // above the diagonal
+#pragma unroll 1
+                    for (int hh = 0; hh < HU; ++hh) tmem_st8(tmem + lanes + p_col(j, hh), zero);
+                tmem_wait_st();
+                tc::fence_before_sync();
+               tc::mbar_arrive(bar(B_P));
             }
-            if (!wait(bar(B_G), c)) break;
-            tc::fence_after_sync();
-            for (int j = 0; j < 4; ++j) {
-                uint32_t p[16];
-                if (j > wq) {                              // above the diagonal
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) p[i] = 0u;
-#pragma unroll
-                    for (int hh = 0; hh < HU; ++hh) tmem_st16(tmem + lanes + kColG + 32 * j + 16 * hh, p);
-                    continue;
-                }
-                float G[32];
-                tc::tmem_ld32(tmem + lanes + kColG + 32 * j, G);
-                const int limit = j == wq ? lane : 31;
-#pragma unroll
-                for (int hh = 0; hh < HU; ++hh) {
-                    const float *cp = arr + ((st * HU + hh) * 3) * 128 + 32 * j;
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        const float4 k = load4f(cp + i);
-                        float v[4] = {exp2_fast(csl[hh] - k.x), exp2_fast(csl[hh] - k.y), exp2_fast(csl[hh] - k.z),
-                                      exp2_fast(csl[hh] - k.w)};
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) v[q] = i + q <= limit ? v[q] * G[i + q] : 0.f;
-                        p[i / 2] = pack_bf16(v[0], v[1]);
-                        p[i / 2 + 1] = pack_bf16(v[2], v[3]);
-                    }
-                    tmem_st16(tmem + lanes + kColG + 32 * j + 16 * hh, p);
-                }
-            }
-            tmem_wait_st();
-            tc::fence_before_sync();
-            tc::mbar_arrive(bar(B_P));
         }
-        if (STATES && ok && row == 0)
-#pragma unroll
-            for (int hh = 0; hh < HU; ++hh)
-                if (hh < heads) a.seg_log[(long long)sg.entry * d.heads + h0 + hh] = (float)log_sum[hh];
     } else if (warp >= 8 && warp < 12) {
         // ------------------------------------------------------ B: the state
         const int hh = row / P, h = h0 + hh;
         const bool mine = hh < heads;
         const long long head = (long long)N * P, all = head * d.heads, at = (long long)h * head + row % P;
         const float *from = nullptr;
+        if (!STATES && sg.entry >= 0) await_previous();        // the state that enters the segment
         if (!STATES && mine) {
             if (sg.entry >= 0) from = a.enter + (long long)sg.entry * all + at;
             else if (a.state_in) from = a.state_in + (long long)sg.slot * all + at;
         }
         unsigned char *Srow = sm + L::S + row * 128;
-        auto put_row = [&](int j, const float (&v)[32]) {      // columns 32 j .. of this row, bf16
+        auto put_row = [&](int j, const float (&v)[16]) {      // columns 16 j .. of this row, bf16
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < 2; ++k) {
                 const uint4 u = make_uint4(pack_bf16(v[8 * k], v[8 * k + 1]), pack_bf16(v[8 * k + 2], v[8 * k + 3]),
                                            pack_bf16(v[8 * k + 4], v[8 * k + 5]), pack_bf16(v[8 * k + 6], v[8 * k + 7]));
-                const int ch = (j & 1) * 4 + k;
-                *reinterpret_cast<uint4 *>(Srow + (j >> 1) * kHalfTile + ((ch ^ (row & 7)) << 4)) = u;
+                const int ch = (j & 3) * 2 + k;
+                *reinterpret_cast<uint4 *>(Srow + (j >> 2) * kHalfTile + ((ch ^ (row & 7)) << 4)) = u;
             }
         };
 #pragma unroll 1
-        for (int j = 0; j < N / 32; ++j) {
-            float v[32];
+        for (int j = 0; j < N / 16; ++j) {
+            float v[16];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = from ? from[(long long)(32 * j + i) * P] : 0.f;
-            tmem_st32(tmem + lanes + kColS + 32 * j, v);
+            for (int i = 0; i < 16; ++i) v[i] = from ? from[(long long)(16 * j + i) * P] : 0.f;
+            tmem_st16f(tmem + lanes + kColS + 16 * j, v);
             if (!STATES) put_row(j, v);
         }
         tmem_wait_st();
@@ -468,25 +550,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (c >= chunks) return;
             if (!STATES) tc::fence_async_smem();
             tc::fence_before_sync();
-            if (!wait(bar(B_A0 + (c & 1)), (uint32_t)(c >> 1))) return;
+            wait(bar(B_A0 + (c & 1)), half(c));
             dec = decs[(c & 1) * HU + hh];
             tc::mbar_arrive(bar(B_S));
         };
         announce(0);
+#pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
-            if (!wait(bar(B_DS0 + (c & 1)), (uint32_t)(c >> 1))) break;
+            wait(bar(B_DS0 + (c & 1)), half(c));
+            if (!STATES) wait(bar(B_Y2), c);
             tc::fence_after_sync();
             const bool next = c + 1 < chunks;
 #pragma unroll 1
-            for (int j = 0; j < N / 32; ++j) {
-                float v[32], s[32];
-                tc::tmem_ld32(tmem + lanes + kColDS + 32 * j, v);
-                tc::tmem_ld32(tmem + lanes + kColS + 32 * j, s);
+            for (int j = 0; j < N / 16; ++j) {
+                float v[16], s[16];
+                tmem_ld16x2(tmem + lanes + kColDS + 16 * j, tmem + lanes + kColS + 16 * j, v, s);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = fmaf(dec, s[i], v[i]);
-                tmem_st32(tmem + lanes + kColS + 32 * j, v);
-                // the wait above also says that Y2 of this chunk has read the tile
-                if (!STATES && next) put_row(j, v);
+                for (int i = 0; i < 16; ++i) v[i] = fmaf(dec, s[i], v[i]);
+                tmem_st16f(tmem + lanes + kColS + 16 * j, v);
+                if (!STATES && next) put_row(j, v);            // Y2 of this chunk has read the tile
             }
             tmem_wait_st();
             announce(c + 1);
@@ -494,138 +576,226 @@ __global__ void __launch_bounds__(kThreads, 1)
         float *to = nullptr;
         if (STATES) to = a.enter + (long long)(sg.entry + 1) * all + at;
         else if (sg.last && a.state_out) to = a.state_out + (long long)sg.slot * all + at;
-        if (ok && to && chunks > 0) {
+        if (*gave_up) to = nullptr;
+        if (to && chunks > 0) {
 #pragma unroll 1
-            for (int j = 0; j < N / 32; ++j) {
-                float v[32];
-                tc::tmem_ld32(tmem + lanes + kColS + 32 * j, v);
+            for (int j = 0; j < N / 16; ++j) {
+                float v[16];
+                tc::tmem_ld16(tmem + lanes + kColS + 16 * j, v);
                 if (mine)
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) to[(long long)(32 * j + i) * P] = v[i];
+                    for (int i = 0; i < 16; ++i) to[(long long)(16 * j + i) * P] = v[i];
             }
-        } else if (ok && to && mine) {                         // no tokens: the state as it came, bit for bit
+        } else if (to && mine) {                         // no tokens: the state as it came, bit for bit
             for (int i = 0; i < N; ++i) to[(long long)i * P] = from ? from[(long long)i * P] : 0.f;
         }
     } else if (warp >= 12 && warp < 20) {
-        // ------------------------------------------------- C: outputs (half = 64 columns)
+        // ------------------------------------------------- C: outputs (side = 64 columns)
         if (!STATES) {
-            const int half = (warp - 12) >> 2, hh = HU == 2 ? half : 0;
+            const int side = (warp - 12) >> 2, hh = HU == 2 ? side : 0;
             const bool mine = hh < heads;
             const float skip = a.D && mine ? a.D[h0 + hh] : 0.f;
-            const uint32_t ycol = tmem + lanes + kColY + half * 64;
+            const f32x2 skip2 = pack2(skip, skip);
+            const uint32_t ycol = tmem + lanes + kColY + side * 64;
+#pragma unroll 1
             for (int c = 0; c < chunks; ++c) {
                 const int st = c & 1;
-                if (!wait(bar(B_A0 + st), (uint32_t)(c >> 1)) || !wait(bar(B_Y2), c)) break;
+                wait(bar(B_A0 + st), half(c));
+                wait(bar(B_Y2), c);
                 tc::fence_after_sync();
-                const float e = arr[((st * HU + hh) * 3 + 2) * 128 + row];
+                const float e = array(st, hh, 3)[row];
+                const f32x2 e2 = pack2(e, e);
+#pragma unroll 1
+                for (int j = 0; j < 4; ++j) {
+                    float v[16];
+                    tc::tmem_ld16(ycol + 16 * j, v);
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    float v[32];
-                    tc::tmem_ld32(ycol + 32 * j, v);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] *= e;
-                    tmem_st32(ycol + 32 * j, v);
+                    for (int i = 0; i < 16; i += 2) {
+                        const float2 u = unpack2(mul2(pack2(v[i], v[i + 1]), e2));
+                        v[i] = u.x;
+                        v[i + 1] = u.y;
+                    }
+                    tmem_st16f(ycol + 16 * j, v);
                 }
                 tmem_wait_st();
                 tc::fence_before_sync();
-                tc::mbar_arrive(bar(B_YC));
-                if (!wait(bar_full(slot_of_tile(c, tX)), use_of_tile(c, tX)) ||
-                    (has_z && !wait(bar_full(slot_of_tile(c, tZ)), use_of_tile(c, tZ))) || !wait(bar(B_Y), c))
-                    break;
-                tc::fence_after_sync();
-                unsigned char *X = sm + L::RING + slot_of_tile(c, tX) * kTile + half * kHalfTile + row * 128;
-                const unsigned char *Z = sm + L::RING + slot_of_tile(c, tZ) * kTile + half * kHalfTile + row * 128;
+               tc::mbar_arrive(bar(B_YC));
                 const bool short_chunk = partial && c == chunks - 1;
-                const bool direct = short_chunk && mine && row < tail;
-                __nv_bfloat16 *yrow = (__nv_bfloat16 *)a.y + (sg.t0 + (long long)c * kL + row) * out_cols +
-                                      (long long)h0 * P + half * 64;
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    float v[32];
-                    tc::tmem_ld32(ycol + 32 * j, v);
-                    if (j == 1) {
+                const bool live = mine && !(short_chunk && row >= tail);
+                const long long t = sg.t0 + (long long)c * kL + row;
+                const uint4 *zrow = reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)a.z + t * a.ld_z +
+                                                                    (long long)h0 * P + side * 64);
+                uint4 z0 = make_uint4(0, 0, 0, 0), z1 = z0;    // z of the next 16 columns
+                if (has_z && live) { z0 = zrow[0]; z1 = zrow[1]; }
+                wait(bar_full(slot_x(c)), half(c));
+                wait(bar(B_DS0 + st), half(c));            // D has read the tile that y replaces
+                wait(bar(B_Y0 + st), half(c));
+                tc::fence_after_sync();
+                unsigned char *X = sm + L::RING + slot_x(c) * kTile + side * kHalfTile + row * 128;
+                __nv_bfloat16 *yrow = (__nv_bfloat16 *)a.y + t * out_cols + (long long)h0 * P + side * 64;
+#pragma unroll 1
+                for (int j = 0; j < 4; ++j) {
+                    float v[16];
+                    tc::tmem_ld16(ycol + 16 * j, v);
+                    if (j == 3) {
                         tc::fence_before_sync();
                         tc::mbar_arrive(bar(B_YE));
                     }
+                    const uint4 zc[2] = {z0, z1};
+                    if (has_z && live && j < 3) { z0 = zrow[2 * j + 2]; z1 = zrow[2 * j + 3]; }
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t off = (uint32_t)(((j * 4 + k) ^ (row & 7)) << 4);
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t off = (uint32_t)(((j * 2 + k) ^ (row & 7)) << 4);
                         const uint4 xv = *reinterpret_cast<const uint4 *>(X + off);
                         const uint32_t xs[4] = {xv.x, xv.y, xv.z, xv.w};
-                        float o[8];
+                        f32x2 o[4];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            o[2 * q] = fmaf(skip, bf16_lo(xs[q]), v[8 * k + 2 * q]);
-                            o[2 * q + 1] = fmaf(skip, bf16_hi(xs[q]), v[8 * k + 2 * q + 1]);
-                        }
+                        for (int q = 0; q < 4; ++q)
+                            o[q] = fma2(skip2, bf16_pair(xs[q]), pack2(v[8 * k + 2 * q], v[8 * k + 2 * q + 1]));
                         if (has_z) {
-                            const uint4 zv = *reinterpret_cast<const uint4 *>(Z + off);
-                            const uint32_t zs[4] = {zv.x, zv.y, zv.z, zv.w};
+                            const uint32_t zs[4] = {zc[k].x, zc[k].y, zc[k].z, zc[k].w};
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                o[2 * q] *= silu_fast(bf16_lo(zs[q]));
-                                o[2 * q + 1] *= silu_fast(bf16_hi(zs[q]));
-                            }
+                            for (int q = 0; q < 4; ++q) o[q] = gate2(o[q], bf16_pair(zs[q]));
                         }
-                        const uint4 u = make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]),
-                                                   pack_bf16(o[6], o[7]));
+                        const uint4 u = make_uint4(pack_bf16(o[0]), pack_bf16(o[1]), pack_bf16(o[2]), pack_bf16(o[3]));
                         if (!short_chunk) *reinterpret_cast<uint4 *>(X + off) = u;
-                        else if (direct) *reinterpret_cast<uint4 *>(yrow + j * 32 + k * 8) = u;
+                        else if (live) *reinterpret_cast<uint4 *>(yrow + j * 16 + k * 8) = u;
                     }
                 }
                 tc::fence_async_smem();
-                tc::mbar_arrive(bar(B_ST0 + st));
+               tc::mbar_arrive(bar(B_ST0 + st));
             }
         }
-    } else if (warp >= 20) {
+    } else if (warp >= 20 && warp < 28) {
         // ------------------------------------------------- D: w X in three parts
-        // 16 tokens at a time: a thread's token, and two of its 16 blocks of 8 columns
-        const int k = (tid & 7) + 8 * ((tid >> 3) & 1), pb0 = (tid - 640) >> 4;
+        // Group 0 takes the even, group 1 the odd sixteens of tokens: a thread's token, and two
+        // of its 16 blocks of 8 columns.  Each part is the next 8 bits of the value, cut off: the
+        // three hold all 24.
+        const int t128 = (tid - 640) & 127, buf = (tid - 640) >> 7;
+        const int k = (t128 & 7) + 8 * ((t128 >> 3) & 1), pb0 = t128 >> 4;
+        unsigned char *to = sm + L::XW + buf * kXwBuf;
+#pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
             const int st = c & 1;
-            if (!wait(bar(B_A0 + st), (uint32_t)(c >> 1)) ||
-                !wait(bar_full(slot_of_tile(c, tX)), use_of_tile(c, tX)))
-                break;
-            const unsigned char *X = sm + L::RING + slot_of_tile(c, tX) * kTile;
+            wait(bar(B_A0 + st), half(c));
+            wait(bar_full(slot_x(c)), half(c));
+            const unsigned char *X = sm + L::RING + slot_x(c) * kTile;
             const int count = c == chunks - 1 ? tail : kL;
-            for (int e = 0; e < 8; ++e) {
-                const int n = c * 8 + e, buf = e & 1;
-                if (n >= 2 && !wait(bar(B_XE0 + buf), (uint32_t)((n >> 1) - 1))) break;
-                const int tok = e * 16 + k;
-                unsigned char *to = sm + L::XW + buf * kXwBuf;
+#pragma unroll 1
+            for (int e = buf; e < 8; e += 2) {
+                const int tok = e * 16 + k, n = c * 4 + (e >> 1);
+                uint4 xv[2];
+                float w[2];
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    const int pb = pb0 + 8 * q;
-                    const float w = arr[((st * HU + (HU == 2 ? q : 0)) * 3 + 1) * 128 + tok];
-                    uint4 xv = *reinterpret_cast<const uint4 *>(X + q * kHalfTile + tok * 128 + (((pb & 7) ^ (tok & 7)) << 4));
-                    if (tok >= count) xv = make_uint4(0, 0, 0, 0);
-                    const uint32_t xs[4] = {xv.x, xv.y, xv.z, xv.w};
-                    uint32_t hi[4], mid[4], lo[4];
+                    w[q] = array(st, HU == 2 ? q : 0, 2)[tok];
+                    xv[q] = *reinterpret_cast<const uint4 *>(X + q * kHalfTile + tok * 128 + ((pb0 ^ (tok & 7)) << 4));
+                    if (tok >= count) xv[q] = make_uint4(0, 0, 0, 0);
+                }
+                if (n >= 1) wait(bar(B_XE0 + buf), (uint32_t)(n - 1));
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const uint32_t xs[4] = {xv[q].x, xv[q].y, xv[q].z, xv[q].w};
+                    uint32_t part[3][4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        float v0 = w * bf16_lo(xs[i]), v1 = w * bf16_hi(xs[i]);
-                        hi[i] = pack_bf16(v0, v1);
-                        v0 -= bf16_lo(hi[i]); v1 -= bf16_hi(hi[i]);
-                        mid[i] = pack_bf16(v0, v1);
-                        v0 -= bf16_lo(mid[i]); v1 -= bf16_hi(mid[i]);
-                        lo[i] = pack_bf16(v0, v1);
+                        f32x2 v = mul2(pack2(w[q], w[q]), bf16_pair(xs[i]));
+#pragma unroll
+                        for (int r = 0; r < 3; ++r) {
+                            const float2 f = unpack2(v);
+                            const uint32_t f0 = __float_as_uint(f.x), f1 = __float_as_uint(f.y);
+                            part[r][i] = __byte_perm(f0, f1, 0x7632);
+                            if (r < 2) v = add2(v, pack2(-bf16_hi(f0), -bf16_hi(f1)));
+                        }
                     }
-                    const uint32_t off = tc::mnmaj_off(pb * 8, k, 128);
-                    *reinterpret_cast<uint4 *>(to + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4 *>(to + kXwPart + off) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
-                    *reinterpret_cast<uint4 *>(to + 2 * kXwPart + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    const uint32_t off = tc::mnmaj_off((pb0 + 8 * q) * 8, k, 128);
+#pragma unroll
+                    for (int r = 0; r < 3; ++r)
+                        *reinterpret_cast<uint4 *>(to + r * kXwPart + off) =
+                            make_uint4(part[r][0], part[r][1], part[r][2], part[r][3]);
                 }
                 tc::fence_async_smem();
-                tc::mbar_arrive(bar(B_XF0 + buf));
+               tc::mbar_arrive(bar(B_XF0 + buf));
             }
-            if (!ok) break;
         }
+    } else if (warp >= 28) {
+        // ------------ E: log-decays of one head in every other chunk, four tokens a lane
+        // cs_i summed from the chunk's start, in powers of two; cp_i = log2(dt_i) - cs_i; w_i from
+        // the sum behind i; e_i = exp(cs_i); the chunk's decay.  Tokens behind the end: no weight.
+        const int st = (warp - 28) / HU, hh = (warp - 28) % HU;
+        const bool mine = hh < heads;
+        const int h = h0 + min(hh, heads - 1);
+        const float rate = -expf(a.A_log[h]), bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+        const __nv_bfloat16 *pdt = (const __nv_bfloat16 *)a.dt + h;
+        double log_sum = 0.0;
+        float raw[4];
+        auto fetch = [&](int c) {
+            const long long t = sg.t0 + (long long)c * kL + 4 * lane;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) raw[i] = t + i < sg.t1 ? to_f32(pdt[(t + i) * a.ld_dt]) : 0.f;
+        };
+        if (st < chunks) fetch(st);
+#pragma unroll 1
+        for (int c = st; c < chunks; c += 2) {
+            const int count = c == chunks - 1 ? tail : kL;
+            float dt[4], g[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool valid = 4 * lane + i < count && mine;
+                dt[i] = valid ? ssm_dt(raw[i], bias, d) : 0.f;
+                g[i] = valid ? fmaxf(rate * dt[i], kMinLog) : 0.f;
+            }
+            if (c + 2 < chunks) fetch(c + 2);
+            const float sum = (g[0] + g[1]) + (g[2] + g[3]);
+            float pre = sum, suf = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float u = __shfl_up_sync(0xffffffffu, pre, o), v = __shfl_down_sync(0xffffffffu, suf, o);
+                if (lane >= o) pre += u;
+                if (lane + o < 32) suf += v;
+            }
+            const float total = __shfl_sync(0xffffffffu, pre, 31);
+            float before = __shfl_up_sync(0xffffffffu, pre, 1), behind = __shfl_down_sync(0xffffffffu, suf, 1);
+            if (lane == 0) before = 0.f;
+            if (lane == 31) behind = 0.f;
+            float cs[4], cp[4], w[4], e[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                before += g[i];
+                cs[i] = before * kLog2e;
+                e[i] = exp2_fast(cs[i]);
+                cp[i] = 4 * lane + i < count ? __log2f(dt[i]) - cs[i] : -__int_as_float(0x7f800000);
+            }
+#pragma unroll
+            for (int i = 3; i >= 0; --i) {
+                w[i] = exp2_fast(behind * kLog2e) * dt[i];
+                behind += g[i];
+            }
+            if (STATES && lane == 0) log_sum += (double)total;
+
+            // chunk c - 2 is done with these arrays: its decay was read before its dS, w before dS was
+            // done, cp and e before its last product
+            if (c >= 2) {
+                wait(bar(B_DS0 + st), half(c) - 1);
+                if (!STATES) wait(bar(B_Y0 + st), half(c) - 1);
+            }
+            store4f(array(st, hh, 0) + 4 * lane, make_float4(cs[0], cs[1], cs[2], cs[3]));
+            store4f(array(st, hh, 1) + 4 * lane, make_float4(cp[0], cp[1], cp[2], cp[3]));
+            store4f(array(st, hh, 2) + 4 * lane, make_float4(w[0], w[1], w[2], w[3]));
+            store4f(array(st, hh, 3) + 4 * lane, make_float4(e[0], e[1], e[2], e[3]));
+            if (lane == 0) decs[st * HU + hh] = exp2_fast(total * kLog2e);
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(bar(B_A0 + st));
+        }
+        if (STATES && lane == 0) logs[st * HU + hh] = log_sum;
     }
-    if (!ok) set_error(a.err, GDN_DEVERR_TIMEOUT);
     __syncwarp();
     tc::fence_before_sync();
     __syncthreads();
+    if (!STATES) await_previous();
+    if (tid == 0 && *gave_up) set_error(a.err, GDN_DEVERR_TIMEOUT);
     if (warp == 1) tc::tmem_dealloc(tmem, 512);
+    if (STATES && tid < heads) a.seg_log[(long long)sg.entry * d.heads + h0 + tid] = (float)(logs[tid] + logs[HU + tid]);
 }
 
 namespace {
@@ -662,7 +832,8 @@ cudaError_t run(const SsmScanArgs &a, const SsmMaps &m, unsigned grid, cudaStrea
     constexpr int bytes = TcSmem<N, HU>::BYTES;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    kern<<<grid, kThreads, bytes, s>>>(a, m);
+    if (!STATES && a.seg_len < a.T) return launch_early(kern, dim3(grid), kThreads<HU>, bytes, s, a, m);
+    kern<<<grid, kThreads<HU>, bytes, s>>>(a, m);
     return cudaGetLastError();
 }
 
