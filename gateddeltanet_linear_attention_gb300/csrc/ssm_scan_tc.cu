@@ -64,7 +64,7 @@ template <int N, int HU> struct TcSmem {
     static constexpr int DEC = ARR + 2 * HU * 4 * 512;       // [2][HU] chunk decays
     static constexpr int LOG = DEC + 2 * HU * 4;             // [2][HU] doubles: summed log-decays
     static constexpr int BAR = LOG + 2 * HU * 8;
-    static constexpr int NBAR = 2 * kSlots + 22;
+    static constexpr int NBAR = 2 * kSlots + 23;
     static constexpr int SLOT = (BAR + 7) / 8 * 8 + NBAR * 8;
     static constexpr int BYTES = SLOT + 16;
     static_assert(BYTES <= 232448, "shared memory of an SM");
@@ -72,9 +72,9 @@ template <int N, int HU> struct TcSmem {
 
 // Barriers behind the ring's full[] and empty[].
 // Where a waiter may be a phase
-// behind (G, DS, Y, A, ST), even and odd chunks have a barrier each: the next phase of either then
+// behind (G, S, DS, Y, A, ST), even and odd chunks have a barrier each: the next phase of either then
 // needs the waiter's own progress.
-enum { B_G0 = 0, B_G1, B_P, B_S, B_XF0, B_XF1, B_XE0, B_XE1, B_DS0, B_DS1, B_Y2, B_YC, B_Y0, B_Y1, B_YE, B_A0, B_A1, B_ST0, B_ST1,
+enum { B_G0 = 0, B_G1, B_P, B_S0, B_S1, B_XF0, B_XF1, B_XE0, B_XE1, B_DS0, B_DS1, B_Y2, B_YC, B_Y0, B_Y1, B_YE, B_A0, B_A1, B_ST0, B_ST1,
        B_FIX, B_END, B_END2, B_COUNT };
 
 // 128-byte-swizzled operands: rows of 128 bytes, 8-row groups of 1,024 bytes, 64-element blocks
@@ -133,35 +133,48 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return r;
 }
 // A bounded wait.  Waiting warps share the issue slots and the instruction cache with the working
-// ones: a poll is a few instructions, and the wall clock is read out of line, once in 256 polls.
-__device__ __forceinline__ uint32_t poll256(uint32_t b, uint32_t parity) {
+// ones, so all but the first poll is out of line, a few instructions long, and the wall clock is
+// read once in 256 polls.  A wait that ran out sets the CTA's flag: the roles then run on without
+// waiting (over their own tiles and rows, with no copy started), the state is not stored, and the
+// error is reported.
+__device__ __forceinline__ uint32_t poll(uint32_t b, uint32_t parity) {
     uint32_t done;
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
-        "mov.u32 n, 256;\n\t"
-        "POLL%=:\n\t"
+        "{\n\t.reg .pred p;\n\t"
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "@p bra DONE%=;\n\t"
-        "sub.u32 n, n, 1;\n\t"
-        "setp.ne.u32 q, n, 0;\n\t"
-        "@q bra POLL%=;\n\t"
-        "DONE%=:\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}\n"
         : "=r"(done) : "r"(b), "r"(parity) : "memory");
     return done;
 }
-// A wait that ran out sets the CTA's flag: the roles then run on without waiting (over their own
-// tiles and rows, with no copy started), the state is not stored, and the error is reported.
-__device__ __noinline__ void poll_to_limit(uint32_t b, uint32_t parity, uint64_t limit_ns, volatile uint32_t *gave_up) {
-    const uint64_t t0 = tc::globaltimer_ns();
-    while (!*gave_up) {
-        if (poll256(b, parity)) return;
-        if (tc::globaltimer_ns() - t0 > limit_ns) *gave_up = 1;
+__device__ __forceinline__ uint32_t poll8(uint32_t b, uint32_t parity) {
+    uint32_t done;
+#define GDN_POLL                                                                   \
+    "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"                    \
+    "@p bra DONE%=;\n\t"
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t" GDN_POLL GDN_POLL GDN_POLL GDN_POLL GDN_POLL GDN_POLL GDN_POLL GDN_POLL
+        "DONE%=:\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(done) : "r"(b), "r"(parity) : "memory");
+#undef GDN_POLL
+    return done;
+}
+__device__ __noinline__ void poll_to_limit(uint32_t b, uint32_t parity, uint64_t limit_ns, uint32_t flag) {
+    uint64_t t0 = 0;
+    for (uint32_t i = 1;; ++i) {
+        if (poll8(b, parity)) return;
+        if ((i & 31u) != 0) continue;
+        uint32_t over;
+        asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(over) : "r"(flag) : "memory");
+        const uint64_t t = tc::globaltimer_ns();
+        if (t0 == 0) t0 = t;
+        if (over) return;
+        if (t - t0 > limit_ns) asm volatile("st.volatile.shared.u32 [%0], 1;" :: "r"(flag) : "memory");
     }
 }
 __device__ __noinline__ void poll_some(uint32_t b, uint32_t parity, uint64_t limit_ns) {
     const uint64_t t0 = tc::globaltimer_ns();
-    while (!poll256(b, parity) && tc::globaltimer_ns() - t0 <= limit_ns) {}
+    while (!poll8(b, parity) && tc::globaltimer_ns() - t0 <= limit_ns) {}
 }
 // Products, commits, copies and arrivals of one lane (`lead`) of a warp that stays together: the
 // instructions take their operands from warp-uniform registers, and in a branch of one lane the
@@ -228,6 +241,17 @@ __device__ __forceinline__ uint32_t pack_bf16(f32x2 v) {
     const float2 f = unpack2(v);
     return pack_bf16(f.x, f.y);
 }
+// 32 bytes (a memory sector) of a row, in one load where the row starts on 32 bytes.
+__device__ __forceinline__ void load_32b(const uint4 *p, bool wide, uint32_t (&v)[8]) {
+    if (wide) {
+        asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                     : "l"(p));
+    } else {
+        const uint4 a = p[0], b = p[1];
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
+}
 __device__ __forceinline__ float rcp_fast(float x) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -283,6 +307,7 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
     const int tail = uniform((int)(sg.t1 - sg.t0)) - (chunks - 1) * kL;      // tokens of the last chunk
     const bool partial = chunks > 0 && tail < kL;
     const bool has_z = !STATES && a.z != nullptr;
+    const bool z_wide = (((uintptr_t)a.z | (uintptr_t)(a.ld_z * 2)) & 31u) == 0;      // rows on 32 bytes
 
     const uint32_t sbase = tc::smem_u32(sm), bars = sbase + (L::BAR + 7) / 8 * 8;
     auto bar_full = [&](int s) { return bars + 8u * s; };
@@ -298,7 +323,7 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
     if (tid == 0) {
         *gave_up = 0;
         for (int s = 0; s < kSlots; ++s) { tc::mbar_init(bar_full(s), 1); tc::mbar_init(bar_empty(s), 1); }
-        const int counts[B_COUNT] = {1, 1, 128, 128, 128, 128, 1, 1, 1, 1, 1, 256, 1, 1, 256, HU, HU, 256, 256, 128, 1, 1};
+        const int counts[B_COUNT] = {1, 1, 128, 128, 128, 128, 128, 1, 1, 1, 1, 1, 128, 1, 1, 256, HU, HU, 256, 256, 128, 1, 1};
         for (int k = 0; k < B_COUNT; ++k) tc::mbar_init(bar(k), counts[k]);
         tc::mbar_fence_init();
     }
@@ -312,7 +337,7 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
     const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
 
     auto wait = [&](uint32_t b, uint32_t parity) {
-        if (!poll256(b, parity & 1u)) poll_to_limit(b, parity & 1u, a.wait_ns, gave_up);
+        if (!poll(b, parity & 1u)) poll_to_limit(b, parity & 1u, a.wait_ns, sbase + L::SLOT + 4);
         __syncwarp();
     };
     // the slots of a chunk's tiles (also their barriers), and the parity of their use
@@ -322,6 +347,9 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
     auto tile = [&](int slot) { return sbase + L::RING + slot * kTile; };
     constexpr int kSlotC = 0;
 
+    // dS has a second set of columns where there is room for one (without outputs: Y's)
+    constexpr bool kTwoDS = STATES || N == 64;
+    auto col_ds = [&](int c) { return kTwoDS && (c & 1) ? (N == 64 ? kColDS + 64 : kColY) : kColDS; };
     const int wq = warp & 3;                       // TMEM lanes of a warp: 32 wq ..
     const int row = wq * 32 + lane;
     const uint32_t lanes = (uint32_t)(wq * 32) << 16;
@@ -341,9 +369,6 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
             if (c >= 2) wait(bar_empty(slot_b(c)), half(c) - 1);
             if (*gave_up) break;
             load(slot_b(c), &maps.b, g * N, N / 64, t);
-            if (c >= 2) wait(bar_empty(slot_x(c)), half(c) - 1);
-            if (*gave_up) break;
-            load(slot_x(c), &maps.x, h0 * P, 2, t);
             if (!STATES) {
                 if (c >= 1) wait(bar_empty(kSlotC), c - 1);
                 if (*gave_up) break;
@@ -353,6 +378,9 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
                     tma_prefetch(lead, &maps.z, h0 * P + 64, t);
                 }
             }
+            if (c >= 2) wait(bar_empty(slot_x(c)), half(c) - 1);
+            if (*gave_up) break;
+            load(slot_x(c), &maps.x, h0 * P, 2, t);
         }
         // copies in flight land before the CTA ends (a slot whose last copy was not started runs out)
         if (*gave_up) {
@@ -379,7 +407,7 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
 #pragma unroll
                 for (int k = 0; k < N / 16; ++k) mma_ss(lead, tmem + kColG, dC + step_k(k), dB + step_k(k), id_full, k > 0);
                 commit(lead, bar(B_G0 + (c & 1)));
-                wait(bar(B_S), c);
+                wait(bar(B_S0 + (c & 1)), half(c));
                 if (c > 0) wait(bar(B_YE), c - 1);
                 tc::fence_after_sync();
 #pragma unroll
@@ -410,8 +438,9 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
         for (int c = 0; c < chunks; ++c) {
             wait(bar_full(slot_b(c)), half(c));
             if (partial && c == chunks - 1) wait(bar(B_FIX), 0);
-            if (!STATES) wait(bar(B_G0 + (c & 1)), half(c));   // G has read B too before the slot is given back
-            wait(bar(B_S), c);
+            // dS(c)'s columns are free: of the chunk before, or with two sets the one before that
+            if (!kTwoDS) wait(bar(B_S0 + (c & 1)), half(c));
+            else if (c >= 1) wait(bar(B_S0 + ((c - 1) & 1)), half(c - 1));
             const uint64_t dBt = desc_mn(tile(slot_b(c)));
 #pragma unroll 1
             for (int e = 0; e < 8; ++e) {
@@ -420,9 +449,10 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
                 const uint64_t dW = tc::mnmaj_desc(sbase + L::XW + (e & 1) * kXwBuf, 128, 0);
 #pragma unroll
                 for (int part = 2; part >= 0; --part)      // smallest first
-                    mma_ss(lead, tmem + kColDS, dW + part * (kXwPart >> 4), dBt + step_mn(e), id_ds, e > 0 || part < 2);
+                    mma_ss(lead, tmem + col_ds(c), dW + part * (kXwPart >> 4), dBt + step_mn(e), id_ds, e > 0 || part < 2);
                 commit(lead, bar(B_XE0 + (e & 1)));
             }
+            if (!STATES) wait(bar(B_G0 + (c & 1)), half(c));   // G has read B too before the slot is given back
             commit(lead, bar(B_DS0 + (c & 1)));
             commit(lead, bar_empty(slot_b(c)));
             if (STATES) commit(lead, bar_empty(slot_x(c)));
@@ -484,7 +514,7 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
 #pragma unroll
                         for (int i = 0; i < 16; ++i) G[i] = 16 * j + i <= row ? G[i] : 0.f;
                     }
-#pragma unroll 1
+#pragma unroll
                     for (int hh = 0; hh < HU; ++hh) {
                         const float csr = array(st, hh, 0)[row];
                         const f32x2 cs = pack2(csr, csr);
@@ -510,7 +540,7 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
                     for (int hh = 0; hh < HU; ++hh) tmem_st8(tmem + lanes + p_col(j, hh), zero);
                 tmem_wait_st();
                 tc::fence_before_sync();
-               tc::mbar_arrive(bar(B_P));
+                tc::mbar_arrive(bar(B_P));
             }
         }
     } else if (warp >= 8 && warp < 12) {
@@ -552,19 +582,40 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
             tc::fence_before_sync();
             wait(bar(B_A0 + (c & 1)), half(c));
             dec = decs[(c & 1) * HU + hh];
-            tc::mbar_arrive(bar(B_S));
+            tc::mbar_arrive(bar(B_S0 + (c & 1)));
         };
         announce(0);
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
+            if (!STATES) {
+                // Y2 of this chunk times exp(cs): row r of the chunk on this thread
+                wait(bar(B_Y2), c);
+                tc::fence_after_sync();
+#pragma unroll 1
+                for (int j = 0; j < 8; ++j) {
+                    const float e = array(c & 1, HU == 2 ? j >> 2 : 0, 3)[row];
+                    const f32x2 e2 = pack2(e, e);
+                    float v[16];
+                    tc::tmem_ld16(tmem + lanes + kColY + 16 * j, v);
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2) {
+                        const float2 u = unpack2(mul2(pack2(v[i], v[i + 1]), e2));
+                        v[i] = u.x;
+                        v[i + 1] = u.y;
+                    }
+                    tmem_st16f(tmem + lanes + kColY + 16 * j, v);
+                }
+                tmem_wait_st();
+                tc::fence_before_sync();
+                tc::mbar_arrive(bar(B_YC));
+            }
             wait(bar(B_DS0 + (c & 1)), half(c));
-            if (!STATES) wait(bar(B_Y2), c);
             tc::fence_after_sync();
             const bool next = c + 1 < chunks;
 #pragma unroll 1
             for (int j = 0; j < N / 16; ++j) {
                 float v[16], s[16];
-                tmem_ld16x2(tmem + lanes + kColDS + 16 * j, tmem + lanes + kColS + 16 * j, v, s);
+                tmem_ld16x2(tmem + lanes + col_ds(c) + 16 * j, tmem + lanes + kColS + 16 * j, v, s);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) v[i] = fmaf(dec, s[i], v[i]);
                 tmem_st16f(tmem + lanes + kColS + 16 * j, v);
@@ -600,33 +651,13 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
 #pragma unroll 1
             for (int c = 0; c < chunks; ++c) {
                 const int st = c & 1;
-                wait(bar(B_A0 + st), half(c));
-                wait(bar(B_Y2), c);
-                tc::fence_after_sync();
-                const float e = array(st, hh, 3)[row];
-                const f32x2 e2 = pack2(e, e);
-#pragma unroll 1
-                for (int j = 0; j < 4; ++j) {
-                    float v[16];
-                    tc::tmem_ld16(ycol + 16 * j, v);
-#pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
-                        const float2 u = unpack2(mul2(pack2(v[i], v[i + 1]), e2));
-                        v[i] = u.x;
-                        v[i + 1] = u.y;
-                    }
-                    tmem_st16f(ycol + 16 * j, v);
-                }
-                tmem_wait_st();
-                tc::fence_before_sync();
-               tc::mbar_arrive(bar(B_YC));
                 const bool short_chunk = partial && c == chunks - 1;
                 const bool live = mine && !(short_chunk && row >= tail);
                 const long long t = sg.t0 + (long long)c * kL + row;
                 const uint4 *zrow = reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)a.z + t * a.ld_z +
                                                                     (long long)h0 * P + side * 64);
-                uint4 z0 = make_uint4(0, 0, 0, 0), z1 = z0;    // z of the next 16 columns
-                if (has_z && live) { z0 = zrow[0]; z1 = zrow[1]; }
+                uint32_t zn[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};   // z of the next 16 columns
+                if (has_z && live) load_32b(zrow, z_wide, zn);
                 wait(bar_full(slot_x(c)), half(c));
                 wait(bar(B_DS0 + st), half(c));            // D has read the tile that y replaces
                 wait(bar(B_Y0 + st), half(c));
@@ -641,8 +672,10 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
                         tc::fence_before_sync();
                         tc::mbar_arrive(bar(B_YE));
                     }
-                    const uint4 zc[2] = {z0, z1};
-                    if (has_z && live && j < 3) { z0 = zrow[2 * j + 2]; z1 = zrow[2 * j + 3]; }
+                    uint32_t zc[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) zc[k] = zn[k];
+                    if (has_z && live && j < 3) load_32b(zrow + 2 * j + 2, z_wide, zn);
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         const uint32_t off = (uint32_t)(((j * 2 + k) ^ (row & 7)) << 4);
@@ -653,9 +686,8 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
                         for (int q = 0; q < 4; ++q)
                             o[q] = fma2(skip2, bf16_pair(xs[q]), pack2(v[8 * k + 2 * q], v[8 * k + 2 * q + 1]));
                         if (has_z) {
-                            const uint32_t zs[4] = {zc[k].x, zc[k].y, zc[k].z, zc[k].w};
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) o[q] = gate2(o[q], bf16_pair(zs[q]));
+                            for (int q = 0; q < 4; ++q) o[q] = gate2(o[q], bf16_pair(zc[4 * k + q]));
                         }
                         const uint4 u = make_uint4(pack_bf16(o[0]), pack_bf16(o[1]), pack_bf16(o[2]), pack_bf16(o[3]));
                         if (!short_chunk) *reinterpret_cast<uint4 *>(X + off) = u;
@@ -663,7 +695,7 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
                     }
                 }
                 tc::fence_async_smem();
-               tc::mbar_arrive(bar(B_ST0 + st));
+                tc::mbar_arrive(bar(B_ST0 + st));
             }
         }
     } else if (warp >= 20 && warp < 28) {
@@ -715,7 +747,7 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
                             make_uint4(part[r][0], part[r][1], part[r][2], part[r][3]);
                 }
                 tc::fence_async_smem();
-               tc::mbar_arrive(bar(B_XF0 + buf));
+                tc::mbar_arrive(bar(B_XF0 + buf));
             }
         }
     } else if (warp >= 28) {
@@ -778,6 +810,7 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
             if (c >= 2) {
                 wait(bar(B_DS0 + st), half(c) - 1);
                 if (!STATES) wait(bar(B_Y0 + st), half(c) - 1);
+                if (kTwoDS) wait(bar(B_S0 + st), half(c) - 1);      // (else implied by its dS)
             }
             store4f(array(st, hh, 0) + 4 * lane, make_float4(cs[0], cs[1], cs[2], cs[3]));
             store4f(array(st, hh, 1) + 4 * lane, make_float4(cp[0], cp[1], cp[2], cp[3]));
