@@ -64,7 +64,7 @@ template <int N, int HU> struct TcSmem {
     static constexpr int DEC = ARR + 2 * HU * 4 * 512;       // [2][HU] chunk decays
     static constexpr int LOG = DEC + 2 * HU * 4;             // [2][HU] doubles: summed log-decays
     static constexpr int BAR = LOG + 2 * HU * 8;
-    static constexpr int NBAR = 2 * kSlots + 23;
+    static constexpr int NBAR = 2 * kSlots + 27;
     static constexpr int SLOT = (BAR + 7) / 8 * 8 + NBAR * 8;
     static constexpr int BYTES = SLOT + 16;
     static_assert(BYTES <= 232448, "shared memory of an SM");
@@ -74,7 +74,7 @@ template <int N, int HU> struct TcSmem {
 // Where a waiter may be a phase
 // behind (G, S, DS, Y, A, ST), even and odd chunks have a barrier each: the next phase of either then
 // needs the waiter's own progress.
-enum { B_G0 = 0, B_G1, B_P, B_S0, B_S1, B_XF0, B_XF1, B_XE0, B_XE1, B_DS0, B_DS1, B_Y2, B_YC, B_Y0, B_Y1, B_YE, B_A0, B_A1, B_ST0, B_ST1,
+enum { B_G0 = 0, B_G1, B_P, B_S0, B_S1, B_XF, B_XE = B_XF + 4, B_DS0 = B_XE + 4, B_DS1, B_Y2, B_YC, B_Y0, B_Y1, B_YE, B_A0, B_A1, B_ST0, B_ST1,
        B_FIX, B_END, B_END2, B_COUNT };
 
 // 128-byte-swizzled operands: rows of 128 bytes, 8-row groups of 1,024 bytes, 64-element blocks
@@ -323,7 +323,8 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
     if (tid == 0) {
         *gave_up = 0;
         for (int s = 0; s < kSlots; ++s) { tc::mbar_init(bar_full(s), 1); tc::mbar_init(bar_empty(s), 1); }
-        const int counts[B_COUNT] = {1, 1, 128, 128, 128, 128, 128, 1, 1, 1, 1, 1, 128, 1, 1, 256, HU, HU, 256, 256, 128, 1, 1};
+        const int counts[B_COUNT] = {1, 1, 128, 128, 128, 128, 128, 128, 128, 1, 1, 1, 1, 1, 1, 1, 128, 1, 1, 256, HU, HU,
+                                     256, 256, 128, 1, 1};
         for (int k = 0; k < B_COUNT; ++k) tc::mbar_init(bar(k), counts[k]);
         tc::mbar_fence_init();
     }
@@ -347,6 +348,10 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
     auto tile = [&](int slot) { return sbase + L::RING + slot * kTile; };
     constexpr int kSlotC = 0;
 
+    // Groups of D's warps, and a buffer of w X for each: without outputs the warps of
+    // role C and the slot of tile C serve as well.
+    constexpr int kGroups = STATES ? 4 : 2, kFirstD = STATES ? 12 : 20;
+    auto xw_buffer = [&](int buf) { return sbase + (buf < 2 ? L::XW + buf * kXwBuf : L::RING + (buf - 2) * kXwBuf); };
     // dS has a second set of columns where there is room for one (without outputs: Y's)
     constexpr bool kTwoDS = STATES || N == 64;
     auto col_ds = [&](int c) { return kTwoDS && (c & 1) ? (N == 64 ? kColDS + 64 : kColY) : kColDS; };
@@ -444,13 +449,14 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
             const uint64_t dBt = desc_mn(tile(slot_b(c)));
 #pragma unroll 1
             for (int e = 0; e < 8; ++e) {
-                wait(bar(B_XF0 + (e & 1)), (uint32_t)(c * 4 + (e >> 1)));
+                const int buf = e % kGroups;
+                wait(bar(B_XF + buf), (uint32_t)(c * (8 / kGroups) + e / kGroups));
                 tc::fence_after_sync();
-                const uint64_t dW = tc::mnmaj_desc(sbase + L::XW + (e & 1) * kXwBuf, 128, 0);
+                const uint64_t dW = tc::mnmaj_desc(xw_buffer(buf), 128, 0);
 #pragma unroll
                 for (int part = 2; part >= 0; --part)      // smallest first
                     mma_ss(lead, tmem + col_ds(c), dW + part * (kXwPart >> 4), dBt + step_mn(e), id_ds, e > 0 || part < 2);
-                commit(lead, bar(B_XE0 + (e & 1)));
+                commit(lead, bar(B_XE + buf));
             }
             if (!STATES) wait(bar(B_G0 + (c & 1)), half(c));   // G has read B too before the slot is given back
             commit(lead, bar(B_DS0 + (c & 1)));
@@ -640,7 +646,7 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
         } else if (to && mine) {                         // no tokens: the state as it came, bit for bit
             for (int i = 0; i < N; ++i) to[(long long)i * P] = from ? from[(long long)i * P] : 0.f;
         }
-    } else if (warp >= 12 && warp < 20) {
+    } else if (warp >= 12 && warp < kFirstD) {
         // ------------------------------------------------- C: outputs (side = 64 columns)
         if (!STATES) {
             const int side = (warp - 12) >> 2, hh = HU == 2 ? side : 0;
@@ -698,14 +704,14 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
                 tc::mbar_arrive(bar(B_ST0 + st));
             }
         }
-    } else if (warp >= 20 && warp < 28) {
+    } else if (warp >= kFirstD && warp < 28) {
         // ------------------------------------------------- D: w X in three parts
-        // Group 0 takes the even, group 1 the odd sixteens of tokens: a thread's token, and two
-        // of its 16 blocks of 8 columns.  Each part is the next 8 bits of the value, cut off: the
-        // three hold all 24.
-        const int t128 = (tid - 640) & 127, buf = (tid - 640) >> 7;
+        // Group b takes every kGroups-th sixteen of tokens: a thread's token, and two of its 16
+        // blocks of 8 columns.  Each part is the next 8 bits of the value, cut off: the three hold
+        // all 24.
+        const int t128 = (tid - kFirstD * 32) & 127, buf = uniform((tid - kFirstD * 32) >> 7);
         const int k = (t128 & 7) + 8 * ((t128 >> 3) & 1), pb0 = t128 >> 4;
-        unsigned char *to = sm + L::XW + buf * kXwBuf;
+        unsigned char *to = sm + (xw_buffer(buf) - sbase);
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
             const int st = c & 1;
@@ -714,8 +720,8 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
             const unsigned char *X = sm + L::RING + slot_x(c) * kTile;
             const int count = c == chunks - 1 ? tail : kL;
 #pragma unroll 1
-            for (int e = buf; e < 8; e += 2) {
-                const int tok = e * 16 + k, n = c * 4 + (e >> 1);
+            for (int e = buf; e < 8; e += kGroups) {
+                const int tok = e * 16 + k, n = c * (8 / kGroups) + e / kGroups;
                 uint4 xv[2];
                 float w[2];
 #pragma unroll
@@ -724,7 +730,7 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
                     xv[q] = *reinterpret_cast<const uint4 *>(X + q * kHalfTile + tok * 128 + ((pb0 ^ (tok & 7)) << 4));
                     if (tok >= count) xv[q] = make_uint4(0, 0, 0, 0);
                 }
-                if (n >= 1) wait(bar(B_XE0 + buf), (uint32_t)(n - 1));
+                if (n >= 1) wait(bar(B_XE + buf), (uint32_t)(n - 1));
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     const uint32_t xs[4] = {xv[q].x, xv[q].y, xv[q].z, xv[q].w};
@@ -747,7 +753,7 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
                             make_uint4(part[r][0], part[r][1], part[r][2], part[r][3]);
                 }
                 tc::fence_async_smem();
-                tc::mbar_arrive(bar(B_XF0 + buf));
+                tc::mbar_arrive(bar(B_XF + buf));
             }
         }
     } else if (warp >= 28) {
