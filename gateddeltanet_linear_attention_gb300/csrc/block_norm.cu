@@ -22,12 +22,19 @@ constexpr int kWarpRows = 4;       // rows of a CTA where a warp owns a row
 template <typename T> struct Raw8;
 template <> struct Raw8<float> {
     float4 a, b;
+    __device__ __forceinline__ void from(const unsigned char *p, bool in) {
+        a = b = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (in) { a = load4f((const float *)p); b = load4f((const float *)p + 4); }
+    }
     __device__ __forceinline__ void get(float (&v)[8]) const {
         v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
     }
 };
 template <> struct Raw8<__nv_bfloat16> {
     uint4 u;
+    __device__ __forceinline__ void from(const unsigned char *p, bool in) {
+        u = in ? *reinterpret_cast<const uint4 *>(p) : make_uint4(0u, 0u, 0u, 0u);
+    }
     __device__ __forceinline__ void get(float (&v)[8]) const {
         const float4 a = bf16x4_f32(make_uint2(u.x, u.y)), b = bf16x4_f32(make_uint2(u.z, u.w));
         v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
@@ -98,6 +105,11 @@ __device__ __forceinline__ void store8v(const C &c, __nv_bfloat16 *p, const floa
     }
 }
 
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                 :: "r"((unsigned)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+}
+
 // Sum over the threads of a row; every thread gets it.  `buf` holds a value per
 // warp, twice: successive sums take turns (`turn`), so that one barrier per sum
 // is enough: a half is written again only after the other half's barrier.
@@ -128,14 +140,13 @@ template <bool WARP> __device__ __forceinline__ float row_sum(float v, float2 (*
 
 }  // namespace
 
-// Blocks of MAXT threads at most, and how many of them an SM's registers hold.  Rows that fill
-// 1,024 threads leave 64 registers a thread: those kernels read the weights at every row (from
-// L1) and do not load ahead (LEAN).
-constexpr int fwd_blocks(int maxt) { return 1024 / maxt; }
-constexpr int bwd_blocks(int maxt) { return maxt >= 512 ? 1 : 512 / maxt; }
+// Blocks of MAXT threads at most, 1,024 threads on an SM.  Rows that fill 1,024 threads leave 64
+// registers a thread: the forward kernel then reads the weights at every row (from L1) and does
+// not load ahead (LEAN).
+constexpr int sm_blocks(int maxt) { return 1024 / maxt; }
 
 template <typename TA, typename TR, int NV, int MAXT, bool WARP, bool VEC>
-__global__ void __launch_bounds__(MAXT, fwd_blocks(MAXT)) block_norm_kernel(NormArgs a) {
+__global__ void __launch_bounds__(MAXT, sm_blocks(MAXT)) block_norm_kernel(NormArgs a) {
     __shared__ float2 buf[2][32];
     int turn = 0;
     using Ch = Chunk<VEC>;
@@ -244,7 +255,7 @@ __global__ void __launch_bounds__(MAXT, fwd_blocks(MAXT)) block_norm_kernel(Norm
 // The weight gradients are summed in registers over a CTA's rows, then over the
 // CTAs by norm_weight_grad_kernel, always in the same order.
 template <typename TA, typename TR, int NV, int MAXT, bool WARP, bool VEC>
-__global__ void __launch_bounds__(MAXT, bwd_blocks(MAXT)) block_norm_bwd_kernel(NormArgs a) {
+__global__ void __launch_bounds__(MAXT, sm_blocks(MAXT)) block_norm_bwd_kernel(NormArgs a) {
     __shared__ float2 buf[2][32];
     int turn = 0;
     using Ch = Chunk<VEC>;
@@ -259,34 +270,56 @@ __global__ void __launch_bounds__(MAXT, bwd_blocks(MAXT)) block_norm_bwd_kernel(
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw1[i][j] = dw2[i][j] = 0.f;
 
-    Raw8<TA> np[NV], ng[NV], nh[NV];
-    Raw8<TR> nu[NV], nd[NV];
-    auto fetch = [&](long long row) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const Ch c(i, lane, nt, a.dim);
-            if (a.dh) {
-                load_raw<VEC>(c, (const TA *)a.dh + row * a.ld_dh, nh[i]);
-                load_raw<VEC>(c, (const TR *)a.residual + row * a.ld_res, nu[i]);
-            }
-            if (a.d_res_out) load_raw<VEC>(c, (const TR *)a.d_res_out + row * a.ld_dout, nd[i]);
-            if (a.block) load_raw<VEC>(c, (const TA *)a.block + row * a.ld_block, np[i]);
-            if (channel_gate) load_raw<VEC>(c, (const TA *)a.gate + row * a.ld_gate, ng[i]);
-        }
+    // The five operands of the next row come into shared memory while this one is computed: every
+    // thread copies and reads its own 16- or 32-byte pieces, so no barrier is needed.  (Rows that
+    // take two pieces a thread, or single elements, are loaded when their turn comes.)
+    constexpr bool AHEAD = VEC && NV == 1 && MAXT < 1024;
+    constexpr int EA = sizeof(Raw8<TA>), ER = sizeof(Raw8<TR>);
+    extern __shared__ __align__(16) unsigned char stage[];
+    const Ch mine(0, lane, nt, a.dim);
+    auto piece = [&](int s, int k) {       // operand k of stage s: dh, block, gate, then r', d_r'
+        return stage + (s * (3 * EA + 2 * ER) + (k < 3 ? k * EA : 3 * EA + (k - 3) * ER)) * blockDim.x +
+               threadIdx.x * (k < 3 ? EA : ER);
     };
-    constexpr bool LEAN = MAXT == 1024;
-    if (!LEAN && first < a.rows) fetch(first);
-    for (long long row = first; row < a.rows; row += step) {
-        if (LEAN) fetch(row);
+    auto ahead = [&](long long row, int s) {
+        if (row < a.rows && mine.in(0)) {
+            auto copy = [&](int k, const void *p, long long ld, int bytes) {
+                const char *src = (const char *)p + (row * ld + mine.base) * (bytes / 8);
+                for (int q = 0; q < bytes; q += 16) cp_async16(piece(s, k) + q, src + q);
+            };
+            if (a.dh) { copy(0, a.dh, a.ld_dh, EA); copy(3, a.residual, a.ld_res, ER); }
+            if (a.block) copy(1, a.block, a.ld_block, EA);
+            if (channel_gate) copy(2, a.gate, a.ld_gate, EA);
+            if (a.d_res_out) copy(4, a.d_res_out, a.ld_dout, ER);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    if (AHEAD) ahead(first, 0);
+    int turn_row = 0;
+    for (long long row = first; row < a.rows; row += step, turn_row ^= 1) {
         Raw8<TA> rp[NV], rg[NV], rh[NV];
         Raw8<TR> ru[NV], rd[NV];
+        if (AHEAD) {
+            ahead(row + step, turn_row ^ 1);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+        } else {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) { rp[i] = np[i]; rg[i] = ng[i]; rh[i] = nh[i]; ru[i] = nu[i]; rd[i] = nd[i]; }
-        if (!LEAN && row + step < a.rows) fetch(row + step);
+            for (int i = 0; i < NV; ++i) {
+                const Ch c(i, lane, nt, a.dim);
+                if (a.dh) {
+                    load_raw<VEC>(c, (const TA *)a.dh + row * a.ld_dh, rh[i]);
+                    load_raw<VEC>(c, (const TR *)a.residual + row * a.ld_res, ru[i]);
+                }
+                if (a.d_res_out) load_raw<VEC>(c, (const TR *)a.d_res_out + row * a.ld_dout, rd[i]);
+                if (a.block) load_raw<VEC>(c, (const TA *)a.block + row * a.ld_block, rp[i]);
+                if (channel_gate) load_raw<VEC>(c, (const TA *)a.gate + row * a.ld_gate, rg[i]);
+            }
+        }
         float du[NV][8];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if (a.d_res_out) {
+                if (AHEAD) rd[i].from(piece(turn_row, 4), mine.in(0));
                 rd[i].get(du[i]);
             } else {
 #pragma unroll
@@ -303,6 +336,10 @@ __global__ void __launch_bounds__(MAXT, bwd_blocks(MAXT)) block_norm_bwd_kernel(
                 float w[8];
                 load_raw<VEC>(c, a.w_pre, rw);
                 rw.get(w);
+                if (AHEAD) {
+                    rh[i].from(piece(turn_row, 0), mine.in(0));
+                    ru[i].from(piece(turn_row, 3), mine.in(0));
+                }
                 rh[i].get(g[i]);
                 ru[i].get(uh[i]);
 #pragma unroll
@@ -332,6 +369,10 @@ __global__ void __launch_bounds__(MAXT, bwd_blocks(MAXT)) block_norm_bwd_kernel(
             for (int i = 0; i < NV; ++i) {
                 const Ch c(i, lane, nt, a.dim);
                 float ph[8], gt[8], w[8];
+                if (AHEAD) {
+                    rp[i].from(piece(turn_row, 1), mine.in(0));
+                    if (channel_gate) rg[i].from(piece(turn_row, 2), mine.in(0));
+                }
                 rp[i].get(ph);
                 if (channel_gate) rg[i].get(gt);
                 if (a.w_post) {
@@ -362,6 +403,7 @@ __global__ void __launch_bounds__(MAXT, bwd_blocks(MAXT)) block_norm_bwd_kernel(
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
                     float ph[8], v[8];
+                    if (AHEAD) rp[i].from(piece(turn_row, 1), mine.in(0));
                     rp[i].get(ph);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) v[j] = a.w_post ? k * (du[i][j] - ph[j] * k * m) : du[i][j];
@@ -370,6 +412,7 @@ __global__ void __launch_bounds__(MAXT, bwd_blocks(MAXT)) block_norm_bwd_kernel(
             }
         }
     }
+    let_next_start();
     if (!a.ws) return;
     // this CTA's (or warp's) part of the weight gradients: [2][dim]
     const long long part = WARP ? blockIdx.x * (long long)kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
@@ -391,6 +434,7 @@ __global__ void __launch_bounds__(MAXT, bwd_blocks(MAXT)) block_norm_bwd_kernel(
 __global__ void __launch_bounds__(1024) norm_weight_grad_kernel(const float *ws, int parts, int dim,
                                                                 float *dw_post, float *dw_pre) {
     __shared__ float s[32][33];
+    await_previous();
     float *dw = blockIdx.y == 0 ? dw_post : dw_pre;
     if (!dw) return;
     const int col = blockIdx.x * 32 + (threadIdx.x & 31), r = threadIdx.x >> 5;
@@ -407,40 +451,51 @@ namespace {
 
 // A warp owns a row of up to 256 elements, a CTA a longer one.
 bool warp_rows(int dim) { return dim <= 256; }
-int max_threads(int dim) { return dim <= 1024 ? 128 : dim <= 4096 ? 512 : 1024; }
+int row_threads(int dim) {
+    const int chunks = (dim + 7) / 8;
+    return warp_rows(dim) ? 32 * kWarpRows : chunks <= 1024 ? (chunks + 31) / 32 * 32 : (chunks + 63) / 64 * 32;
+}
 
-// CTAs of the backward, and the parts of the weight gradients that they leave.
+// CTAs of the backward (1,024 threads on an SM), and so the parts of the weight gradients.
 int bwd_ctas(long long rows, int dim) {
-    const long long cap = (long long)sm_count() * bwd_blocks(max_threads(dim));
+    const long long cap = (long long)sm_count() * (1024 / row_threads(dim));
     const long long want = warp_rows(dim) ? (rows + kWarpRows - 1) / kWarpRows : rows;
     return (int)(want < cap ? want : cap);
 }
 
 template <typename TA, typename TR, int NV, int MAXT, bool WARP, bool VEC>
-void run(const NormArgs &a, bool backward, int threads, cudaStream_t s) {
+cudaError_t run(const NormArgs &a, bool backward, cudaStream_t s) {
+    const int threads = row_threads(a.dim);
     if (backward) {
-        const int ctas = bwd_ctas(a.rows, a.dim);
-        block_norm_bwd_kernel<TA, TR, NV, MAXT, WARP, VEC><<<ctas, threads, 0, s>>>(a);
+        auto kern = block_norm_bwd_kernel<TA, TR, NV, MAXT, WARP, VEC>;
+        int smem = 0;
+        if (VEC && NV == 1 && MAXT < 1024) {
+            smem = 2 * (3 * (int)sizeof(Raw8<TA>) + 2 * (int)sizeof(Raw8<TR>)) * threads;
+            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e != cudaSuccess) return e;
+        }
+        kern<<<bwd_ctas(a.rows, a.dim), threads, smem, s>>>(a);
     } else {
-        const long long cap = (long long)sm_count() * fwd_blocks(MAXT);
+        const long long cap = (long long)sm_count() * (1024 / threads);
         const long long want = WARP ? (a.rows + kWarpRows - 1) / kWarpRows : a.rows;
         block_norm_kernel<TA, TR, NV, MAXT, WARP, VEC><<<(unsigned)(want < cap ? want : cap), threads, 0, s>>>(a);
     }
+    return cudaGetLastError();
 }
 
-template <typename TA, typename TR, bool VEC> void run_dim(const NormArgs &a, bool backward, cudaStream_t s) {
-    const int chunks = (a.dim + 7) / 8, threads = (chunks + 31) / 32 * 32;
-    if (warp_rows(a.dim)) run<TA, TR, 1, 32 * kWarpRows, true, VEC>(a, backward, 32 * kWarpRows, s);
-    else if (chunks <= 128) run<TA, TR, 1, 128, false, VEC>(a, backward, threads, s);
-    else if (chunks <= 512) run<TA, TR, 1, 512, false, VEC>(a, backward, threads, s);
-    else if (chunks <= 1024) run<TA, TR, 1, 1024, false, VEC>(a, backward, threads, s);
-    else run<TA, TR, 2, 1024, false, VEC>(a, backward, (chunks + 63) / 64 * 32, s);
+template <typename TA, typename TR, bool VEC> cudaError_t run_dim(const NormArgs &a, bool backward, cudaStream_t s) {
+    const int chunks = (a.dim + 7) / 8;
+    if (warp_rows(a.dim)) return run<TA, TR, 1, 32 * kWarpRows, true, VEC>(a, backward, s);
+    if (chunks <= 128) return run<TA, TR, 1, 128, false, VEC>(a, backward, s);
+    if (chunks <= 512) return run<TA, TR, 1, 512, false, VEC>(a, backward, s);
+    if (chunks <= 1024) return run<TA, TR, 1, 1024, false, VEC>(a, backward, s);
+    return run<TA, TR, 2, 1024, false, VEC>(a, backward, s);
 }
 
-template <bool VEC> void run_types(const NormArgs &a, bool backward, cudaStream_t s) {
-    if (!a.act_bf16) run_dim<float, float, VEC>(a, backward, s);
-    else if (a.res_bf16) run_dim<__nv_bfloat16, __nv_bfloat16, VEC>(a, backward, s);
-    else run_dim<__nv_bfloat16, float, VEC>(a, backward, s);
+template <bool VEC> cudaError_t run_types(const NormArgs &a, bool backward, cudaStream_t s) {
+    if (!a.act_bf16) return run_dim<float, float, VEC>(a, backward, s);
+    if (a.res_bf16) return run_dim<__nv_bfloat16, __nv_bfloat16, VEC>(a, backward, s);
+    return run_dim<__nv_bfloat16, float, VEC>(a, backward, s);
 }
 
 }  // namespace
@@ -450,21 +505,18 @@ size_t norm_bwd_ws_bytes(long long rows, int dim) {
 }
 
 cudaError_t launch_block_norm(const NormArgs &a, cudaStream_t s) {
-    if (a.vec) run_types<true>(a, false, s);
-    else run_types<false>(a, false, s);
-    return cudaGetLastError();
+    return a.vec ? run_types<true>(a, false, s) : run_types<false>(a, false, s);
 }
 
 cudaError_t launch_block_norm_backward(const NormArgs &a, cudaStream_t s) {
     if (a.rows > 0) {
-        if (a.vec) run_types<true>(a, true, s);
-        else run_types<false>(a, true, s);
+        const cudaError_t e = a.vec ? run_types<true>(a, true, s) : run_types<false>(a, true, s);
+        if (e != cudaSuccess) return e;
     }
-    if (a.dw_post || a.dw_pre) {
-        const int parts = a.rows > 0 ? bwd_ctas(a.rows, a.dim) * (warp_rows(a.dim) ? kWarpRows : 1) : 0;
-        norm_weight_grad_kernel<<<dim3((a.dim + 31) / 32, 2), 1024, 0, s>>>(a.ws, parts, a.dim, a.dw_post, a.dw_pre);
-    }
-    return cudaGetLastError();
+    if (!a.dw_post && !a.dw_pre) return cudaSuccess;
+    const int parts = a.rows > 0 ? bwd_ctas(a.rows, a.dim) * (warp_rows(a.dim) ? kWarpRows : 1) : 0;
+    return launch_early(norm_weight_grad_kernel, dim3((a.dim + 31) / 32, 2), 1024, 0, s, (const float *)a.ws, parts, a.dim,
+                        a.dw_post, a.dw_pre);
 }
 
 }  // namespace gdn

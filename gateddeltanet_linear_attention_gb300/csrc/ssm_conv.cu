@@ -6,32 +6,20 @@ namespace gdn {
 
 namespace {
 
-constexpr int kVec = 8;          // channels of a thread
+constexpr int kVec = 4;          // channels of a thread
 constexpr int kConvThreads = 128;
 constexpr int kRun = 16;         // tokens of a thread
 constexpr int kStepThreads = 128; // of the one-token state kernel
-constexpr int kBatch = 4;        // tokens whose loads are issued together
+constexpr int kBatch = 8;        // tokens whose loads are issued together
 
-// Eight channels as the memory holds them, and as fp32.
-struct Raw8F { float4 a, b; };
-__device__ __forceinline__ Raw8F load_raw8(const float *p) { return {load4f(p), load4f(p + 4)}; }
-__device__ __forceinline__ uint4 load_raw8(const __nv_bfloat16 *p) { return *reinterpret_cast<const uint4 *>(p); }
-__device__ __forceinline__ void raw_f32(const Raw8F &r, float (&v)[8]) {
-    v[0] = r.a.x; v[1] = r.a.y; v[2] = r.a.z; v[3] = r.a.w; v[4] = r.b.x; v[5] = r.b.y; v[6] = r.b.z; v[7] = r.b.w;
-}
-__device__ __forceinline__ void raw_f32(const uint4 &u, float (&v)[8]) {
-    raw_f32(Raw8F{bf16x4_f32(make_uint2(u.x, u.y)), bf16x4_f32(make_uint2(u.z, u.w))}, v);
-}
-template <typename T> __device__ __forceinline__ void load8(const T *p, float (&v)[8]) { raw_f32(load_raw8(p), v); }
-__device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
+// Four channels as the memory holds them, and as fp32.
+__device__ __forceinline__ float4 load_raw(const float *p) { return load4f(p); }
+__device__ __forceinline__ uint2 load_raw(const __nv_bfloat16 *p) { return *reinterpret_cast<const uint2 *>(p); }
+__device__ __forceinline__ void raw_f32(const float4 &r, float (&v)[4]) { v[0] = r.x; v[1] = r.y; v[2] = r.z; v[3] = r.w; }
+__device__ __forceinline__ void raw_f32(const uint2 &r, float (&v)[4]) { raw_f32(bf16x4_f32(r), v); }
+template <typename T> __device__ __forceinline__ void load4(const T *p, float (&v)[4]) { raw_f32(load_raw(p), v); }
+template <typename T> __device__ __forceinline__ void store4(T *p, const float (&v)[4]) {
     store4f(p, make_float4(v[0], v[1], v[2], v[3]));
-    store4f(p + 4, make_float4(v[4], v[5], v[6], v[7]));
-}
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8]) {
-    __nv_bfloat162 h[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-    *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(h);
 }
 
 // Sequence that holds token t, or -1 (in front of the first or behind the last one).
@@ -47,7 +35,7 @@ __device__ __forceinline__ int seq_of(const int32_t *cu, int n_seqs, long long t
 }  // namespace
 
 // ------------------------------------------------------------- packed prompts
-// out_t[c] = SiLU(bias[c] + sum_j w[c][j] x_{t-3+j}[c]).  A thread owns 8
+// out_t[c] = SiLU(bias[c] + sum_j w[c][j] x_{t-3+j}[c]).  A thread owns 4
 // channels of kRun packed tokens and slides the three-token window in
 // registers.  HBM-bound: the input once (three tokens in kRun again, from L2)
 // and the output once.
@@ -58,7 +46,7 @@ __device__ __forceinline__ int seq_of(const int32_t *cu, int n_seqs, long long t
 // history and may then overwrite it.  The two tokens' own run leaves them out.
 template <typename TA>
 __global__ void __launch_bounds__(kConvThreads) ssm_conv_kernel(SsmConvArgs a) {
-    using Raw = decltype(load_raw8((const TA *)nullptr));
+    using Raw = decltype(load_raw((const TA *)nullptr));
     const SsmDims &d = a.d;
     const int c0 = (blockIdx.y * kConvThreads + threadIdx.x) * kVec;
     if (c0 >= d.ch) return;
@@ -68,15 +56,15 @@ __global__ void __launch_bounds__(kConvThreads) ssm_conv_kernel(SsmConvArgs a) {
     const long long r0 = (long long)blockIdx.x * kRun, r1 = r0 + kRun < a.T ? r0 + kRun : a.T;
     float w[4][kVec], bias[kVec];
 #pragma unroll
-    for (int i = 0; i < kVec / 2; ++i) {
-        float u[8];
-        load8((const TA *)a.w + (long long)c0 * 4 + 8 * i, u);
+    for (int i = 0; i < kVec; ++i) {
+        float u[4];
+        load4((const TA *)a.w + (long long)(c0 + i) * 4, u);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) { w[j][2 * i] = u[j]; w[j][2 * i + 1] = u[4 + j]; }
+        for (int j = 0; j < 4; ++j) w[j][i] = u[j];
     }
 #pragma unroll
     for (int i = 0; i < kVec; ++i) bias[i] = 0.f;
-    if (a.bias) load8((const TA *)a.bias + c0, bias);
+    if (a.bias) load4((const TA *)a.bias + c0, bias);
 
     // first sequence that has a token at r0 or later
     int n = seq_of(a.cu, a.n_seqs, r0);
@@ -93,8 +81,8 @@ __global__ void __launch_bounds__(kConvThreads) ssm_conv_kernel(SsmConvArgs a) {
         const long long end = (starts && head_end > r1) ? head_end : (e < r1 ? e : r1);
         if (t >= end && !starts) continue;
         if (slot < 0) {
-            const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            for (; t < end; ++t) store8(out + t * d.ch, zero);
+            const float zero[kVec] = {0.f, 0.f, 0.f, 0.f};
+            for (; t < end; ++t) store4(out + t * d.ch, zero);
             continue;
         }
         float win[3][kVec];
@@ -105,20 +93,20 @@ __global__ void __launch_bounds__(kConvThreads) ssm_conv_kernel(SsmConvArgs a) {
                 for (int i = 0; i < kVec; ++i) win[j][i] = 0.f;
             if (hist) {
                 TA *hp = hist + ((long long)slot * d.ch + c0) * 3;
-                float u[3][8];
+                float u[3][4];
 #pragma unroll
-                for (int i = 0; i < 3; ++i) load8(hp + 8 * i, u[i]);
+                for (int i = 0; i < 3; ++i) load4(hp + 4 * i, u[i]);
 #pragma unroll
                 for (int i = 0; i < kVec; ++i)
 #pragma unroll
-                    for (int j = 0; j < 3; ++j) win[j][i] = u[(3 * i + j) / 8][(3 * i + j) % 8];
+                    for (int j = 0; j < 3; ++j) win[j][i] = u[(3 * i + j) / 4][(3 * i + j) % 4];
                 // the new history: the last three inputs, of the old history where e - s < 3
                 float last[3][kVec];
 #pragma unroll
                 for (int j = 0; j < 3; ++j) {
                     const long long tt = e - 3 + j;
                     if (tt >= s) {
-                        load8(x + tt * a.ld_x, last[j]);
+                        load4(x + tt * a.ld_x, last[j]);
                     } else {
                         const int k = (int)(tt - s + 3);
 #pragma unroll
@@ -126,17 +114,17 @@ __global__ void __launch_bounds__(kConvThreads) ssm_conv_kernel(SsmConvArgs a) {
                             last[j][i] = k == 1 ? win[1][i] : k == 2 ? win[2][i] : win[0][i];
                     }
                 }
-                float v[3][8];
+                float v[3][4];
 #pragma unroll
                 for (int i = 0; i < kVec; ++i)
 #pragma unroll
-                    for (int j = 0; j < 3; ++j) v[(3 * i + j) / 8][(3 * i + j) % 8] = last[j][i];
+                    for (int j = 0; j < 3; ++j) v[(3 * i + j) / 4][(3 * i + j) % 4] = last[j][i];
 #pragma unroll
-                for (int i = 0; i < 3; ++i) store8(hp + 8 * i, v[i]);
+                for (int i = 0; i < 3; ++i) store4(hp + 4 * i, v[i]);
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < 3; ++j) load8(x + (t - 3 + j) * a.ld_x, win[j]);
+            for (int j = 0; j < 3; ++j) load4(x + (t - 3 + j) * a.ld_x, win[j]);
         }
         auto emit = [&](const float (&cur)[kVec], long long at) {
             float o[kVec];
@@ -149,12 +137,12 @@ __global__ void __launch_bounds__(kConvThreads) ssm_conv_kernel(SsmConvArgs a) {
                 win[1][i] = win[2][i];
                 win[2][i] = cur[i];
             }
-            store8(out + at * d.ch, o);
+            store4(out + at * d.ch, o);
         };
         for (; t + kBatch <= end; t += kBatch) {       // the loads of kBatch tokens in flight at once
             Raw raw[kBatch];
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) raw[k] = load_raw8(x + (t + k) * a.ld_x);
+            for (int k = 0; k < kBatch; ++k) raw[k] = load_raw(x + (t + k) * a.ld_x);
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
                 float cur[kVec];
@@ -164,7 +152,7 @@ __global__ void __launch_bounds__(kConvThreads) ssm_conv_kernel(SsmConvArgs a) {
         }
         for (; t < end; ++t) {
             float cur[kVec];
-            load8(x + t * a.ld_x, cur);
+            load4(x + t * a.ld_x, cur);
             emit(cur, t);
         }
     }
