@@ -140,10 +140,10 @@ template <bool WARP> __device__ __forceinline__ float row_sum(float v, float2 (*
 
 }  // namespace
 
-// Blocks of MAXT threads at most, 1,024 threads on an SM.  Rows that fill 1,024 threads leave 64
-// registers a thread: the forward kernel then reads the weights at every row (from L1) and does
-// not load ahead (LEAN).
-constexpr int sm_blocks(int maxt) { return 1024 / maxt; }
+// Blocks of MAXT threads at most, 512 threads on an SM and so 128 registers each.  Rows that need
+// 1,024 threads leave 64 registers a thread: the forward kernel then reads the weights at every
+// row (from L1) and does not load ahead (LEAN).
+constexpr int sm_blocks(int maxt) { return maxt >= 512 ? 1 : 512 / maxt; }
 
 template <typename TA, typename TR, int NV, int MAXT, bool WARP, bool VEC>
 __global__ void __launch_bounds__(MAXT, sm_blocks(MAXT)) block_norm_kernel(NormArgs a) {
@@ -247,6 +247,12 @@ __global__ void __launch_bounds__(MAXT, sm_blocks(MAXT)) block_norm_kernel(NormA
     }
 }
 
+// Shared memory for two rows' operands, 0 where that is more than an SM has.
+template <typename TA, typename TR, int NV, bool VEC> constexpr int stage_bytes(int threads) {
+    const int bytes = 2 * NV * (3 * (int)sizeof(Raw8<TA>) + 2 * (int)sizeof(Raw8<TR>)) * threads;
+    return VEC && bytes <= 224 * 1024 ? bytes : 0;
+}
+
 // The gradients, from the kept r', rstd(p) and rstd(r'); p^ = p rstd(p), r^ = r' rstd(r'):
 //   du    = d_r' + rstd(r') (dh w2 - r^ mean(dh w2 r^))        (d_r of the residual input)
 //   dn    = s sigmoid(gate) du,  d_gate = s du n sigmoid' (summed over the row for a gate per row)
@@ -271,21 +277,25 @@ __global__ void __launch_bounds__(MAXT, sm_blocks(MAXT)) block_norm_bwd_kernel(N
         for (int j = 0; j < 8; ++j) dw1[i][j] = dw2[i][j] = 0.f;
 
     // The five operands of the next row come into shared memory while this one is computed: every
-    // thread copies and reads its own 16- or 32-byte pieces, so no barrier is needed.  (Rows that
-    // take two pieces a thread, or single elements, are loaded when their turn comes.)
-    constexpr bool AHEAD = VEC && NV == 1 && MAXT < 1024;
+    // thread copies and reads its own 16- or 32-byte pieces, so no barrier is needed.  (Rows whose
+    // two stages do not fit, or of single elements, are loaded when their turn comes.)
     constexpr int EA = sizeof(Raw8<TA>), ER = sizeof(Raw8<TR>);
+    constexpr bool AHEAD = stage_bytes<TA, TR, NV, VEC>(MAXT) > 0;
     extern __shared__ __align__(16) unsigned char stage[];
-    const Ch mine(0, lane, nt, a.dim);
-    auto piece = [&](int s, int k) {       // operand k of stage s: dh, block, gate, then r', d_r'
-        return stage + (s * (3 * EA + 2 * ER) + (k < 3 ? k * EA : 3 * EA + (k - 3) * ER)) * blockDim.x +
+    // piece i of operand k (dh, block, gate, then r', d_r') in stage s
+    auto piece = [&](int s, int k, int i) {
+        return stage + ((s * NV + i) * (3 * EA + 2 * ER) + (k < 3 ? k * EA : 3 * EA + (k - 3) * ER)) * blockDim.x +
                threadIdx.x * (k < 3 ? EA : ER);
     };
     auto ahead = [&](long long row, int s) {
-        if (row < a.rows && mine.in(0)) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const Ch c(i, lane, nt, a.dim);
+            if (row >= a.rows || !c.in(0)) continue;
             auto copy = [&](int k, const void *p, long long ld, int bytes) {
-                const char *src = (const char *)p + (row * ld + mine.base) * (bytes / 8);
-                for (int q = 0; q < bytes; q += 16) cp_async16(piece(s, k) + q, src + q);
+                const char *src = (const char *)p + (row * ld + c.base) * (bytes / 8);
+#pragma unroll
+                for (int q = 0; q < bytes; q += 16) cp_async16(piece(s, k, i) + q, src + q);
             };
             if (a.dh) { copy(0, a.dh, a.ld_dh, EA); copy(3, a.residual, a.ld_res, ER); }
             if (a.block) copy(1, a.block, a.ld_block, EA);
@@ -319,7 +329,7 @@ __global__ void __launch_bounds__(MAXT, sm_blocks(MAXT)) block_norm_bwd_kernel(N
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if (a.d_res_out) {
-                if (AHEAD) rd[i].from(piece(turn_row, 4), mine.in(0));
+                if (AHEAD) rd[i].from(piece(turn_row, 4, i), Ch(i, lane, nt, a.dim).in(0));
                 rd[i].get(du[i]);
             } else {
 #pragma unroll
@@ -337,8 +347,8 @@ __global__ void __launch_bounds__(MAXT, sm_blocks(MAXT)) block_norm_bwd_kernel(N
                 load_raw<VEC>(c, a.w_pre, rw);
                 rw.get(w);
                 if (AHEAD) {
-                    rh[i].from(piece(turn_row, 0), mine.in(0));
-                    ru[i].from(piece(turn_row, 3), mine.in(0));
+                    rh[i].from(piece(turn_row, 0, i), Ch(i, lane, nt, a.dim).in(0));
+                    ru[i].from(piece(turn_row, 3, i), Ch(i, lane, nt, a.dim).in(0));
                 }
                 rh[i].get(g[i]);
                 ru[i].get(uh[i]);
@@ -370,8 +380,8 @@ __global__ void __launch_bounds__(MAXT, sm_blocks(MAXT)) block_norm_bwd_kernel(N
                 const Ch c(i, lane, nt, a.dim);
                 float ph[8], gt[8], w[8];
                 if (AHEAD) {
-                    rp[i].from(piece(turn_row, 1), mine.in(0));
-                    if (channel_gate) rg[i].from(piece(turn_row, 2), mine.in(0));
+                    rp[i].from(piece(turn_row, 1, i), Ch(i, lane, nt, a.dim).in(0));
+                    if (channel_gate) rg[i].from(piece(turn_row, 2, i), Ch(i, lane, nt, a.dim).in(0));
                 }
                 rp[i].get(ph);
                 if (channel_gate) rg[i].get(gt);
@@ -403,7 +413,7 @@ __global__ void __launch_bounds__(MAXT, sm_blocks(MAXT)) block_norm_bwd_kernel(N
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
                     float ph[8], v[8];
-                    if (AHEAD) rp[i].from(piece(turn_row, 1), mine.in(0));
+                    if (AHEAD) rp[i].from(piece(turn_row, 1, i), Ch(i, lane, nt, a.dim).in(0));
                     rp[i].get(ph);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) v[j] = a.w_post ? k * (du[i][j] - ph[j] * k * m) : du[i][j];
@@ -449,16 +459,15 @@ __global__ void __launch_bounds__(1024) norm_weight_grad_kernel(const float *ws,
 
 namespace {
 
-// A warp owns a row of up to 256 elements, a CTA a longer one.
-bool warp_rows(int dim) { return dim <= 256; }
-int row_threads(int dim) {
-    const int chunks = (dim + 7) / 8;
-    return warp_rows(dim) ? 32 * kWarpRows : chunks <= 1024 ? (chunks + 31) / 32 * 32 : (chunks + 63) / 64 * 32;
-}
+// A warp owns a row of up to 512 elements, a CTA a longer one; a thread has 8 or 16 elements (with
+// 8 alone the sums over a CTA's warps took a third of the instructions: 8,192 x 4,096 forward 63 us).
+bool warp_rows(int dim) { return dim <= 512; }
+int row_threads(int dim) { return warp_rows(dim) ? 32 * kWarpRows : ((dim + 15) / 16 + 31) / 32 * 32; }
 
-// CTAs of the backward (1,024 threads on an SM), and so the parts of the weight gradients.
+// CTAs of the backward, and so the parts of the weight gradients.
 int bwd_ctas(long long rows, int dim) {
-    const long long cap = (long long)sm_count() * (1024 / row_threads(dim));
+    const int threads = row_threads(dim);
+    const long long cap = (long long)sm_count() * (threads < 512 ? 512 / threads : 1);
     const long long want = warp_rows(dim) ? (rows + kWarpRows - 1) / kWarpRows : rows;
     return (int)(want < cap ? want : cap);
 }
@@ -468,15 +477,14 @@ cudaError_t run(const NormArgs &a, bool backward, cudaStream_t s) {
     const int threads = row_threads(a.dim);
     if (backward) {
         auto kern = block_norm_bwd_kernel<TA, TR, NV, MAXT, WARP, VEC>;
-        int smem = 0;
-        if (VEC && NV == 1 && MAXT < 1024) {
-            smem = 2 * (3 * (int)sizeof(Raw8<TA>) + 2 * (int)sizeof(Raw8<TR>)) * threads;
+        const int smem = stage_bytes<TA, TR, NV, VEC>(MAXT) > 0 ? stage_bytes<TA, TR, NV, VEC>(threads) : 0;
+        if (smem > 0) {
             const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
             if (e != cudaSuccess) return e;
         }
         kern<<<bwd_ctas(a.rows, a.dim), threads, smem, s>>>(a);
     } else {
-        const long long cap = (long long)sm_count() * (1024 / threads);
+        const long long cap = (long long)sm_count() * (threads < 1024 ? 1024 / threads : 1);
         const long long want = WARP ? (a.rows + kWarpRows - 1) / kWarpRows : a.rows;
         block_norm_kernel<TA, TR, NV, MAXT, WARP, VEC><<<(unsigned)(want < cap ? want : cap), threads, 0, s>>>(a);
     }
@@ -484,11 +492,10 @@ cudaError_t run(const NormArgs &a, bool backward, cudaStream_t s) {
 }
 
 template <typename TA, typename TR, bool VEC> cudaError_t run_dim(const NormArgs &a, bool backward, cudaStream_t s) {
-    const int chunks = (a.dim + 7) / 8;
-    if (warp_rows(a.dim)) return run<TA, TR, 1, 32 * kWarpRows, true, VEC>(a, backward, s);
-    if (chunks <= 128) return run<TA, TR, 1, 128, false, VEC>(a, backward, s);
-    if (chunks <= 512) return run<TA, TR, 1, 512, false, VEC>(a, backward, s);
-    if (chunks <= 1024) return run<TA, TR, 1, 1024, false, VEC>(a, backward, s);
+    if (a.dim <= 256) return run<TA, TR, 1, 32 * kWarpRows, true, VEC>(a, backward, s);
+    if (warp_rows(a.dim)) return run<TA, TR, 2, 32 * kWarpRows, true, VEC>(a, backward, s);
+    if (a.dim <= 4096) return run<TA, TR, 2, 256, false, VEC>(a, backward, s);
+    if (a.dim <= 8192) return run<TA, TR, 2, 512, false, VEC>(a, backward, s);
     return run<TA, TR, 2, 1024, false, VEC>(a, backward, s);
 }
 

@@ -45,7 +45,7 @@ __device__ __forceinline__ int seq_of(const int32_t *cu, int n_seqs, long long t
 // still reach into the history) wherever they lie, so it alone reads that
 // history and may then overwrite it.  The two tokens' own run leaves them out.
 template <typename TA>
-__global__ void __launch_bounds__(kConvThreads) ssm_conv_kernel(SsmConvArgs a) {
+__global__ void __launch_bounds__(kConvThreads, 7) ssm_conv_kernel(SsmConvArgs a) {
     using Raw = decltype(load_raw((const TA *)nullptr));
     const SsmDims &d = a.d;
     const int c0 = (blockIdx.y * kConvThreads + threadIdx.x) * kVec;
