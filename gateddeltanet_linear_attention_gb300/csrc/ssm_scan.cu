@@ -144,26 +144,29 @@ __global__ void __launch_bounds__(256) ssm_chain_states_kernel(SsmScanArgs a) {
 // while this one is computed; the row slices' parts of y are summed per block.
 // FP32-bound: 3 packed operations per two state elements and token.
 // STATES: pass 1, no outputs: the leaving state from zero and the log-decay.
-template <int N, int P> struct ScanShape {
-    static constexpr int NPT = N * P / 128 >= 16 ? 16 : N * P / 128;   // rows of a thread
+// WIDE: 4 to 16 rows a thread, as many threads as 256 allow, for batches that do not fill the GPU.
+template <int N, int P, bool WIDE> struct ScanShape {
+    static constexpr int MOST = WIDE ? N * P / 1024 : N * P / 128;
+    static constexpr int NPT = MOST >= 16 ? 16 : MOST < 4 ? 4 : MOST;  // rows of a thread
     static constexpr int LP = P / 4;                                   // threads across the columns
     static constexpr int NS = N / NPT;                                 // row slices
     static constexpr int NT = LP * NS;
     static constexpr int TB = 8;
     static constexpr int ROW = P + 2 * N;                              // x | B | C of a token
     static constexpr int VPT = (TB * ROW / 4 + NT - 1) / NT;           // vectors of a thread
+    static constexpr int OPT = (TB * LP + NT - 1) / NT;                // output (and z) vectors of a thread
 };
 template <typename TA> struct Vec4Of { using type = float4; };
 template <> struct Vec4Of<__nv_bfloat16> { using type = uint2; };
 __device__ __forceinline__ float4 vec4_f32(float4 v) { return v; }
 __device__ __forceinline__ float4 vec4_f32(uint2 v) { return bf16x4_f32(v); }
 
-template <int N, int P, typename TA, bool STATES>
-__global__ void __launch_bounds__(ScanShape<N, P>::NT) ssm_scan_kernel(SsmScanArgs a) {
-    using Sh = ScanShape<N, P>;
+template <int N, int P, typename TA, bool STATES, bool WIDE>
+__global__ void __launch_bounds__(ScanShape<N, P, WIDE>::NT) ssm_scan_kernel(SsmScanArgs a) {
+    using Sh = ScanShape<N, P, WIDE>;
     using V4 = typename Vec4Of<TA>::type;
     constexpr int NPT = Sh::NPT, LP = Sh::LP, NS = Sh::NS, NT = Sh::NT, TB = Sh::TB, ROW = Sh::ROW,
-                  VPT = Sh::VPT;
+                  VPT = Sh::VPT, OPT = Sh::OPT;
     __shared__ __align__(16) float tok[TB][ROW];
     __shared__ __align__(16) float part[STATES ? 1 : TB][NS][P];
     __shared__ float s_dt[TB], s_g[TB], s_a[TB];
@@ -207,7 +210,7 @@ __global__ void __launch_bounds__(ScanShape<N, P>::NT) ssm_scan_kernel(SsmScanAr
     const float rate = -expf(a.A_log[h]), bias = a.dt_bias ? a.dt_bias[h] : 0.f;
     const float skip = a.D ? a.D[h] : 0.f;
     double log_sum = 0.0;
-    V4 raw[VPT];
+    V4 raw[VPT], zraw[OPT];                    // the next block's x, B and C, this block's z
     float raw_dt = 0.f;
     auto fetch = [&](long long t0) {          // the block at t0 into registers
 #pragma unroll
@@ -240,6 +243,15 @@ __global__ void __launch_bounds__(ScanShape<N, P>::NT) ssm_scan_kernel(SsmScanAr
             s_a[tid] = expf(rate * dt);
         }
         __syncthreads();
+        if (!STATES && a.z) {
+#pragma unroll
+            for (int k = 0; k < OPT; ++k) {
+                const int i = k * NT + tid, r = i / LP;
+                if (r < count)
+                    zraw[k] = *reinterpret_cast<const V4 *>((const TA *)a.z + (tb + r) * a.ld_z + (long long)h * P +
+                                                            (i % LP) * 4);
+            }
+        }
         if (tb + TB < sg.t1) fetch(tb + TB);
         if (STATES) {
             float sum = 0.f;
@@ -284,20 +296,22 @@ __global__ void __launch_bounds__(ScanShape<N, P>::NT) ssm_scan_kernel(SsmScanAr
         __syncthreads();
         if (!STATES) {
             TA *y = (TA *)a.y;
-            for (int i = tid; i < count * LP; i += NT) {
-                const int r = i / LP, c = (i % LP) * 4;
+#pragma unroll
+            for (int k = 0; k < OPT; ++k) {
+                const int i = k * NT + tid, r = i / LP, c = (i % LP) * 4;
+                if (r >= count) break;
                 const long long t = tb + r;
                 float4 o = load4f(&part[r][0][c]);
 #pragma unroll
-                for (int k = 1; k < NS; ++k) {
-                    const float4 q = load4f(&part[r][k][c]);
+                for (int n = 1; n < NS; ++n) {
+                    const float4 q = load4f(&part[r][n][c]);
                     o.x += q.x; o.y += q.y; o.z += q.z; o.w += q.w;
                 }
                 const float4 x = load4f(&tok[r][c]);
                 o.x = fmaf(skip, x.x, o.x); o.y = fmaf(skip, x.y, o.y);
                 o.z = fmaf(skip, x.z, o.z); o.w = fmaf(skip, x.w, o.w);
                 if (a.z) {
-                    const float4 z = load4f((const TA *)a.z + t * a.ld_z + (long long)h * P + c);
+                    const float4 z = vec4_f32(zraw[k]);
                     o.x *= silu_for<TA>(z.x); o.y *= silu_for<TA>(z.y);
                     o.z *= silu_for<TA>(z.z); o.w *= silu_for<TA>(z.w);
                 }
@@ -368,14 +382,25 @@ ScanWs scan_ws(const SsmDims &d, long long entries, long long n_seqs) {
     return w;
 }
 
+template <int N, int P, typename TA, bool WIDE>
+cudaError_t run_scan_as(const SsmScanArgs &a, bool states, unsigned grid, cudaStream_t s) {
+    constexpr int NT = ScanShape<N, P, WIDE>::NT;
+    if (states) {
+        ssm_scan_kernel<N, P, TA, true, WIDE><<<grid, NT, 0, s>>>(a);
+        return cudaGetLastError();
+    }
+    if (a.seg_len < a.T) return launch_early(ssm_scan_kernel<N, P, TA, false, WIDE>, dim3(grid), NT, 0, s, a);
+    ssm_scan_kernel<N, P, TA, false, WIDE><<<grid, NT, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
 template <int N, int P, typename TA>
 cudaError_t run_scan(const SsmScanArgs &a, bool states, unsigned segments, cudaStream_t s) {
-    constexpr int NT = ScanShape<N, P>::NT;
     const unsigned grid = a.d.heads * segments;   // the heads of a group side by side: B and C come from L2
-    if (!states && a.seg_len < a.T) return launch_early(ssm_scan_kernel<N, P, TA, false>, dim3(grid), NT, 0, s, a);
-    if (states) ssm_scan_kernel<N, P, TA, true><<<grid, NT, 0, s>>>(a);
-    else ssm_scan_kernel<N, P, TA, false><<<grid, NT, 0, s>>>(a);
-    return cudaGetLastError();
+    constexpr bool kTwoShapes = ScanShape<N, P, true>::NPT != ScanShape<N, P, false>::NPT;
+    // (fp32, 64 x 64, 512 tokens: 128 CTAs 253 -> 157 us, 512 CTAs 426 -> 395 us, 2,048 CTAs 928 -> 997 us)
+    if (kTwoShapes && grid <= 6 * (unsigned)sm_count()) return run_scan_as<N, P, TA, kTwoShapes>(a, states, grid, s);
+    return run_scan_as<N, P, TA, false>(a, states, grid, s);
 }
 
 template <int N, typename TA> cudaError_t run_scan_p(const SsmScanArgs &a, bool states, unsigned segments, cudaStream_t s) {

@@ -60,8 +60,8 @@ template <int N, int HU> struct TcSmem {
     static constexpr int RING = 0;
     static constexpr int S = RING + kSlots * kTile;          // bf16 state, 128 rows (value columns) x N
     static constexpr int XW = S + N * 256;
-    static constexpr int ARR = XW + 2 * kXwBuf;              // [2][HU][4][128]: cs, cp, w, e
-    static constexpr int DEC = ARR + 2 * HU * 4 * 512;       // [2][HU] chunk decays
+    static constexpr int ARR = XW + 2 * kXwBuf;              // [2][HU][5][128]: cs, cp, w, e, v
+    static constexpr int DEC = ARR + 2 * HU * 5 * 512;       // [2][HU] chunk decays
     static constexpr int LOG = DEC + 2 * HU * 4;             // [2][HU] doubles: summed log-decays
     static constexpr int BAR = LOG + 2 * HU * 8;
     static constexpr int NBAR = 2 * kSlots + 27;
@@ -314,8 +314,8 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
     auto bar_empty = [&](int s) { return bars + 8u * (kSlots + s); };
     auto bar = [&](int k) { return bars + 8u * (2 * kSlots + k); };
     float *arr = reinterpret_cast<float *>(sm + L::ARR);
-    // one of a chunk's arrays (0 cs, 1 cp, 2 w, 3 e, see role E), and its decays
-    auto array = [&](int st, int hh, int k) { return arr + ((st * HU + hh) * 4 + k) * 128; };
+    // one of a chunk's arrays (0 cs, 1 cp, 2 w, 3 e, 4 v, see role E), and its decays
+    auto array = [&](int st, int hh, int k) { return arr + ((st * HU + hh) * 5 + k) * 128; };
     float *decs = reinterpret_cast<float *>(sm + L::DEC);
     double *logs = reinterpret_cast<double *>(sm + L::LOG);
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(sm + L::SLOT), *gave_up = tmem_slot + 1;
@@ -512,14 +512,34 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
                 wait(bar(B_A0 + st), half(c));
                 wait(bar(B_G0 + st), half(c));
                 tc::fence_after_sync();
+                // Tokens i in front of this warp's rows, 16 at a time: exp(cs_r - cs_i) dt_i is
+                // exp(cs_r - cs of the 16's last) v_i, both factors' exponents below zero.
 #pragma unroll 1
-                for (int j = 0; j <= 2 * wq + 1; ++j) {                   // 16 tokens i at a time
+                for (int j = 0; j < 2 * wq; ++j) {
                     float G[16];
                     tc::tmem_ld16(tmem + lanes + kColG + 16 * j, G);
-                    if (16 * j + 15 > wq * 32) {                          // across the diagonal: i <= r
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) G[i] = 16 * j + i <= row ? G[i] : 0.f;
+                    for (int hh = 0; hh < HU; ++hh) {
+                        const float *cs = array(st, hh, 0), *v = array(st, hh, 4) + 16 * j;
+                        const float u = exp2_fast(cs[row] - cs[16 * j + 15]);
+                        const f32x2 u2 = pack2(u, u);
+                        uint32_t p[8];
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4) {
+                            const ulonglong2 k = *reinterpret_cast<const ulonglong2 *>(v + i);
+                            p[i / 2] = pack_bf16(mul2(mul2(pack2(G[i], G[i + 1]), k.x), u2));
+                            p[i / 2 + 1] = pack_bf16(mul2(mul2(pack2(G[i + 2], G[i + 3]), k.y), u2));
+                        }
+                        tmem_st8(tmem + lanes + p_col(j, hh), p);
                     }
+                }
+                // Tokens beside the rows: i <= r, exponents of their own
+#pragma unroll 1
+                for (int j = 2 * wq; j < 2 * wq + 2; ++j) {
+                    float G[16];
+                    tc::tmem_ld16(tmem + lanes + kColG + 16 * j, G);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) G[i] = 16 * j + i <= row ? G[i] : 0.f;
 #pragma unroll
                     for (int hh = 0; hh < HU; ++hh) {
                         const float csr = array(st, hh, 0)[row];
@@ -759,7 +779,8 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
     } else if (warp >= 28) {
         // ------------ E: log-decays of one head in every other chunk, four tokens a lane
         // cs_i summed from the chunk's start, in powers of two; cp_i = log2(dt_i) - cs_i; w_i from
-        // the sum behind i; e_i = exp(cs_i); the chunk's decay.  Tokens behind the end: no weight.
+        // the sum behind i; e_i = exp(cs_i); v_i = dt_i exp(cs of the last of i's 16 - cs_i); the
+        // chunk's decay.  Tokens behind the end: no weight.
         const int st = (warp - 28) / HU, hh = (warp - 28) % HU;
         const bool mine = hh < heads;
         const int h = h0 + min(hh, heads - 1);
@@ -796,7 +817,7 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
             float before = __shfl_up_sync(0xffffffffu, pre, 1), behind = __shfl_down_sync(0xffffffffu, suf, 1);
             if (lane == 0) before = 0.f;
             if (lane == 31) behind = 0.f;
-            float cs[4], cp[4], w[4], e[4];
+            float cs[4], cp[4], w[4], e[4], v[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 before += g[i];
@@ -804,8 +825,10 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
                 e[i] = exp2_fast(cs[i]);
                 cp[i] = 4 * lane + i < count ? __log2f(dt[i]) - cs[i] : -__int_as_float(0x7f800000);
             }
+            const float last = __shfl_sync(0xffffffffu, cs[3], lane | 3);
 #pragma unroll
             for (int i = 3; i >= 0; --i) {
+                v[i] = exp2_fast(last - cs[i]) * dt[i];
                 w[i] = exp2_fast(behind * kLog2e) * dt[i];
                 behind += g[i];
             }
@@ -822,6 +845,7 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
             store4f(array(st, hh, 1) + 4 * lane, make_float4(cp[0], cp[1], cp[2], cp[3]));
             store4f(array(st, hh, 2) + 4 * lane, make_float4(w[0], w[1], w[2], w[3]));
             store4f(array(st, hh, 3) + 4 * lane, make_float4(e[0], e[1], e[2], e[3]));
+            store4f(array(st, hh, 4) + 4 * lane, make_float4(v[0], v[1], v[2], v[3]));
             if (lane == 0) decs[st * HU + hh] = exp2_fast(total * kLog2e);
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(bar(B_A0 + st));
