@@ -22,6 +22,7 @@ struct Dims {
     unsigned lose;
 };
 constexpr unsigned LOSE_DECODE_STATE_COPY = 1u;   // decode streaming kernel: the first head's state
+constexpr unsigned LOSE_SSM_TILE_COPY = 4u;       // tensor-core scan: the first chunk's x tile
 constexpr unsigned LOSE_CHAIN_OPERAND_COPY = 2u;  // state chain: the first chunk's [-W ; Q'] operand
 
 __device__ __forceinline__ float to_f32(float x) { return x; }

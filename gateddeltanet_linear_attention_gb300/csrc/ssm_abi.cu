@@ -112,6 +112,7 @@ gdn_status gdn_ssm_prefill(const gdn_ssm_config *cfg, const gdn_ssm_io *io, void
     a.cu = io->cu_seqlens; a.state_idx = io->state_idx;
     a.state_in = io->state_in; a.state_out = io->state_out; a.y = io->y;
     a.wait_ns = gdn::wait_limit_ns();
+    a.lose = gdn::lost_copies();
     if (!io->state_in && !io->state_out) a.d.n_slots = INT_MAX;
     return launch_status(gdn::launch_ssm_scan(a, bf16, (cudaStream_t)stream));
 }

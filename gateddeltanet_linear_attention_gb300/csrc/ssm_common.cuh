@@ -26,7 +26,8 @@ struct SsmScanArgs {
     void *y;                          // [T][heads*P] activation dtype
     SsmDims d;
     unsigned *err;
-    unsigned long long wait_ns;
+    unsigned long long wait_ns;       // limit of bounded waits, and the copies a test drops
+    unsigned lose;
     // Long sequences are cut into segments of seg_len tokens (seg_len >= T: no cut, and the
     // arrays below are unused).
     long long seg_len;
@@ -271,4 +272,5 @@ cudaError_t launch_block_norm_backward(const NormArgs &a, cudaStream_t s);
 // The device error word of the current device, and the limit of bounded waits.
 gdn_status device_error_word(unsigned **out);
 unsigned long long wait_limit_ns();
+unsigned lost_copies();
 }  // namespace gdn

@@ -172,9 +172,13 @@ __device__ __noinline__ void poll_to_limit(uint32_t b, uint32_t parity, uint64_t
         if (t - t0 > limit_ns) asm volatile("st.volatile.shared.u32 [%0], 1;" :: "r"(flag) : "memory");
     }
 }
-__device__ __noinline__ void poll_some(uint32_t b, uint32_t parity, uint64_t limit_ns) {
+// What is in flight when a CTA ends (products, copies into its shared memory) completes by itself
+// within microseconds; waited for even after a wait ran out.
+__device__ __noinline__ bool poll_in_flight(uint32_t b, uint32_t parity) {
     const uint64_t t0 = tc::globaltimer_ns();
-    while (!poll8(b, parity) && tc::globaltimer_ns() - t0 <= limit_ns) {}
+    while (!poll8(b, parity))
+        if (tc::globaltimer_ns() - t0 > 100000000ull) return false;
+    return true;
 }
 // Products, commits, copies and arrivals of one lane (`lead`) of a warp that stays together: the
 // instructions take their operands from warp-uniform registers, and in a branch of one lane the
@@ -385,14 +389,15 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
             }
             if (c >= 2) wait(bar_empty(slot_x(c)), half(c) - 1);
             if (*gave_up) break;
-            load(slot_x(c), &maps.x, h0 * P, 2, t);
+            if (c == 0 && (a.lose & LOSE_SSM_TILE_COPY)) expect_tx(lead, bar_full(slot_x(c)), kTile);    // tests only
+            else load(slot_x(c), &maps.x, h0 * P, 2, t);
         }
         // copies in flight land before the CTA ends (a slot whose last copy was not started runs out)
         if (*gave_up) {
             for (int k = max(0, c - 2); k <= min(c, chunks - 1); ++k) {
-                poll_some(bar_full(slot_b(k)), half(k) & 1u, a.wait_ns);
-                if (!STATES) poll_some(bar_full(kSlotC), k & 1u, a.wait_ns);
-                poll_some(bar_full(slot_x(k)), half(k) & 1u, a.wait_ns);
+                poll_in_flight(bar_full(slot_b(k)), half(k) & 1u);
+                if (!STATES) poll_in_flight(bar_full(kSlotC), k & 1u);
+                poll_in_flight(bar_full(slot_x(k)), half(k) & 1u);
             }
         }
     } else if (warp == 1) {
@@ -433,7 +438,7 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
                 commit(lead, bar(B_Y0 + (c & 1)));
             }
             commit(lead, bar(B_END));                      // nothing in flight when the CTA ends
-            wait(bar(B_END), 0);
+            if (!poll_in_flight(bar(B_END), 0)) *gave_up = 1;
         }
     } else if (warp == 3) {
         // -------------------------------------------------------- product: dS
@@ -464,7 +469,7 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
             if (STATES) commit(lead, bar_empty(slot_x(c)));
         }
         commit(lead, bar(B_END2));
-        wait(bar(B_END2), 0);
+        if (!poll_in_flight(bar(B_END2), 0)) *gave_up = 1;
     } else if (warp == 2) {
         // ------------------------------------------------------------ y out
         if (!STATES) {

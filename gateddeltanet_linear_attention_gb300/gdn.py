@@ -590,7 +590,7 @@ def gdn_device_error(stream=None) -> int:
 
 def gdn_debug_set_wait(wait_ns=2_000_000_000, lose=0):
     """Limit of every bounded device wait (ns) and the test hook that drops one operand copy
-    (bit 0: decode, bit 1: state chain); gdn_debug_set_wait() restores the defaults."""
+    (bit 0: decode, bit 1: state chain, bit 2: state space scan); gdn_debug_set_wait() restores the defaults."""
     _check(load().gdn_debug_set_wait(wait_ns, lose), "gdn_debug_set_wait")
 
 

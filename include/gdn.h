@@ -513,7 +513,8 @@ gdn_status gdn_block_norm_backward(const gdn_block_norm_io *io, void *workspace,
  * operand copy so that such a wait really runs out: bit 0 the first head
  * state of a gdn_mixer_decode / gdn_mixer_decode_q8 launch, bit 1 the first
  * chunk operand of the tensor-core state chain (gdn_chunk_prefill,
- * gdn_mixer_prefill).  A call that timed out writes no state.  Process-wide,
+ * gdn_mixer_prefill), bit 2 the first x tile of every tensor-core
+ * gdn_ssm_prefill segment.  A call that timed out writes no state.  Process-wide,
  * read at each call; GDN_ERR_INVALID_ARG for wait_ns = 0, above 60 s, or an
  * unknown bit. */
 gdn_status gdn_debug_set_wait(uint64_t wait_ns, uint32_t lose);

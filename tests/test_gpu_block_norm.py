@@ -194,3 +194,45 @@ def test_same_bits_again_and_in_a_graph():
         graph.replay()
     s.synchronize()
     assert torch.equal(h, h2) and torch.equal(ro, ro2)
+
+
+def test_residual_not_kept():
+    """A block without a place for the new residual: h alone."""
+    d = make(9, 700, BF, BF)
+    t = {k: up(v) for k, v in d.items()}
+    h = torch.empty(9, 700, dtype=BF, device="cuda")
+    gdn.gdn_block_norm(t["residual"], t["w_pre"], h, block=t["block"], w_post=t["w_post"], gate=t["gate"], res_scale=0.7, eps=1e-5)
+    ref.check(h, *ref.norm(d["block"], d["gate"], d["residual"], d["w_post"], d["w_pre"], 1e-5, 0.0, 0.7)["h"], rel_fwd(700), "h")
+
+
+def test_in_place_over_many_rows():
+    """More rows than CTAs: rows loaded ahead, written in place."""
+    d = make(3000, 520, BF, BF)
+    forward(d, BF, BF, in_place=True)
+    want = backward(d, BF, BF)
+    f = ref.norm(d["block"], d["gate"], d["residual"], d["w_post"], d["w_pre"], 1e-5, 0.0, 0.7)
+    dro = d["d_res_out"].cuda()
+    gdn.gdn_block_norm_backward(f["res_out"][0].to(BF).cuda(), f["rstd_pre"][0].float().cuda(), up(d["w_pre"]), up(d["dh"]), dro, dro,
+                                block=up(d["block"]), rstd_post=f["rstd_post"][0].float().cuda(), w_post=up(d["w_post"]),
+                                gate=up(d["gate"]), res_scale=0.7)
+    assert torch.equal(dro, want["d_residual"])
+
+
+def test_offsets_past_32_bits():
+    rows, dim = (1 << 31) // 4096 + 700, 4096
+    g = torch.Generator(device="cuda").manual_seed(3)
+    p, r = (torch.empty(rows, dim, dtype=BF, device="cuda").normal_(generator=g) for _ in range(2))
+    w = 1 + 0.1 * torch.randn(dim, generator=g, device="cuda")
+    ro, h = torch.empty_like(p), torch.empty_like(p)
+    k1, k2 = torch.empty(2, rows, device="cuda")
+    gdn.gdn_block_norm(r, w, h, block=p, res_out=ro, w_post=w, rstd_post=k1, rstd_pre=k2)
+    s = slice(rows - 20, rows)
+    want = ref.norm(p[s].cpu(), None, r[s].cpu(), w.cpu(), w.cpu(), 1e-6, 0.0, 1.0)
+    ref.check(ro[s], *want["res_out"], rel_fwd(dim), "r'")
+    ref.check(h[s], *want["h"], rel_fwd(dim), "h")
+    dr, dp = r, torch.empty_like(p)               # the gradient in place of d_r'
+    dro = r[s].cpu()
+    gdn.gdn_block_norm_backward(ro, k2, w, h, r, dr, block=p, rstd_post=k1, w_post=w, d_block=dp)
+    want = ref.norm_backward(p[s].cpu(), None, ro[s].cpu(), w.cpu(), w.cpu(), k1[s].cpu(), k2[s].cpu(), h[s].cpu(), dro, 0.0, 1.0)
+    for k, v in (("d_residual", dr), ("d_block", dp)):
+        ref.check(v[s], *want[k], (2 * dim + 64) * ref.U32, k)

@@ -472,3 +472,79 @@ def test_prompt_then_tokens_then_norm_as_a_model_runs_them(act):
         # the residual stream from the y that the norm was given
         out = ref.norm(got.cpu(), None, res[i], w_post, None, 1e-6, 0.0, 1.0)["res_out"]
         ref.check(torch.cat([r1[i * L:(i + 1) * L]] + [t[i:i + 1] for t in rs]), *out, (dim + 32) * ref.U32, "residual")
+
+
+def test_lost_copy_runs_out_then_recovers():
+    """A tile that never arrives: the call returns by itself, reports the timeout and stores no state;
+    the next call is right.  (Nothing faults or hangs: every wait has the 20 ms limit set here.)"""
+    b = Batch([300, 40], H=2, G=1, N=128, P=64, seed=17).upload()
+    y = torch.empty(340, 128, dtype=b.act, device="cuda")
+    out = torch.full_like(b.d_state, 7.0)
+    assert gdn.gdn_device_error() == 0
+    gdn.gdn_debug_set_wait(20_000_000, 4)
+    try:
+        b.launch(y, out)
+        code = gdn.gdn_device_error()
+    finally:
+        gdn.gdn_debug_set_wait()
+    assert code & gdn.DEVERR_TIMEOUT
+    assert (out == 7).all()
+    b.launch(y, out)
+    assert gdn.gdn_device_error() == 0
+    b.verify(y, out)
+
+
+@pytest.mark.parametrize("act", ["fp32", "bf16"])
+def test_many_sequences_some_cut(act):
+    """More sequences than a warp lays out by itself, long ones among them."""
+    lens = [3, 0, 17] * 13 + [600, 1, 0, 1100, 256, 257]
+    b = Batch(lens, H=2, G=1, N=64, P=64, act=act, seed=18)
+    b.verify(*b.run())
+    assert gdn.gdn_device_error() == 0
+
+
+@pytest.mark.parametrize("act,heads", [("bf16", 64), ("fp32", 32)])
+def test_offsets_past_32_bits(act, heads):
+    """Rows behind 2^31 elements: the last sequences of a long batch are right."""
+    H, G, N, P = heads, 1, 64, 128
+    dt = torch.bfloat16 if act == "bf16" else torch.float32
+    first = (1 << 31) // (H * P) + 1000
+    lens = [first, 90, 1]
+    T = sum(lens)
+    gen = torch.Generator(device="cuda").manual_seed(50)
+    x = torch.empty(T, H * P, dtype=dt, device="cuda").normal_(generator=gen)
+    bc = torch.empty(T, 2 * G * N, dtype=dt, device="cuda").normal_(generator=gen)
+    u = torch.empty(T, H, dtype=dt, device="cuda").normal_(generator=gen)
+    A_log, D = torch.rand(H, generator=gen, device="cuda"), torch.ones(H, device="cuda")
+    cu = torch.tensor([0] + lens, dtype=torch.int64).cumsum(0).to(torch.int32).cuda()
+    cfg = gdn.make_ssm_config(G, H, N, P, act=act, n_slots=3)
+    y, out = torch.empty_like(x), torch.empty(3, H, N, P, device="cuda")
+    ws = torch.empty(gdn.gdn_ssm_workspace_size(cfg, T, 3), dtype=torch.uint8, device="cuda")
+    gdn.gdn_ssm_prefill(cfg, x, bc[:, :G * N], bc[:, G * N:], u, A_log, cu, y, D=D, state_out=out, workspace=ws)
+    h = heads // 2                                              # one head in the middle
+    for n in (1, 2):
+        s, e = int(cu[n]), int(cu[n + 1])
+        L = e - s
+        val, mag, S, M = ref.scan(x[s:e].view(L, H, P)[:, h:h + 1].cpu(), bc[s:e, :G * N].reshape(L, G, N).cpu(),
+                                  bc[s:e, G * N:].reshape(L, G, N).cpu(), u[s:e, h:h + 1].cpu(), A_log[h:h + 1].cpu(), D[h:h + 1].cpu(),
+                                  None, None, torch.zeros(1, N, P), 1)
+        rel = (8 * L + N + 64) * ref.U32
+        rel_y = rel + (2 * 2.0 ** -8 + 2 * 128 * 60 * ref.U32 if act == "bf16" else 0)
+        ref.check(y[s:e].view(L, H, P)[:, h], val[:, 0], mag[:, 0], rel_y, "y")
+        ref.check(out[n, h], S[0], M[0], rel, "state")
+    conv = gdn.make_ssm_config(1, H, 16, P, act=act, n_slots=3)
+    CH = H * P + 32
+    del y, bc
+    xc = torch.empty(T, CH, dtype=dt, device="cuda")
+    xc[:, :H * P] = x
+    xc[:, H * P:].normal_(generator=gen)
+    del x
+    w, hist = torch.empty(CH, 4, dtype=dt, device="cuda").normal_(generator=gen), torch.zeros(3, CH, 3, dtype=dt, device="cuda")
+    oc = torch.empty_like(xc)
+    gdn.gdn_ssm_conv_prefill(conv, xc, cu, w, None, hist, None, oc)
+    for n in (1, 2):
+        s, e = int(cu[n]), int(cu[n + 1])
+        val, mag, new = ref.conv(xc[s:e].cpu(), w.cpu(), None, torch.zeros(CH, 3))
+        ref.check(oc[s:e], val, mag, CONV_REL, "conv")
+        assert torch.equal(hist[n].cpu().double(), new)
+    assert gdn.gdn_device_error() == 0
