@@ -373,7 +373,8 @@ __global__ void __launch_bounds__(MAXT, sm_blocks(MAXT)) block_norm_bwd_kernel(N
         }
         if (a.block) {
             const float k = a.w_post ? a.k_post[row] : 1.0f;
-            const float s1 = row_gate ? sigmoid_f(to_f32(((const TA *)a.gate)[row * a.ld_gate])) : 1.0f;
+            float s1 = 1.0f, q1 = 0.f;
+            if (row_gate) sigmoid_pair<float>(to_f32(((const TA *)a.gate)[row * a.ld_gate]), s1, q1);
             float2 sums = make_float2(0.f, 0.f);      // sum of dn w1 p^, sum of the row gate's gradient
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -394,10 +395,11 @@ __global__ void __launch_bounds__(MAXT, sm_blocks(MAXT)) block_norm_bwd_kernel(N
                 for (int j = 0; j < 8; ++j) {
                     const float wj = a.w_post ? w[j] + a.offset : 1.0f;
                     ph[j] *= k;
-                    const float sg = channel_gate ? sigmoid_for<TA>(gt[j]) : s1;
+                    float sg = s1, rest = q1;
+                    if (channel_gate) sigmoid_pair<TA>(gt[j], sg, rest);
                     const float dn = a.scale * du[i][j] * sg;
                     if (a.gate) {
-                        gt[j] = dn * (1.0f - sg) * ph[j] * wj;
+                        gt[j] = dn * rest * ph[j] * wj;
                         sums.y += gt[j];
                     }
                     dw1[i][j] = fmaf(dn, ph[j], dw1[i][j]);

@@ -39,9 +39,10 @@ struct SsmScanArgs {
     float *seg_log;                   // [max_enter][heads]: a segment's summed log-decay
 };
 
-// Step size and log-decay of one (token, head).
+// Step size of one (token, head); NaN stays NaN.
 __device__ __forceinline__ float ssm_dt(float raw, float bias, const SsmDims &d) {
-    return fminf(fmaxf(softplus_f(raw + bias), d.dt_min), d.dt_max);
+    const float dt = softplus_f(raw + bias);
+    return dt < d.dt_min ? d.dt_min : dt > d.dt_max ? d.dt_max : dt;
 }
 
 // How a batch is cut: every sequence has one segment or more (one of an empty sequence), and a
@@ -77,13 +78,13 @@ __device__ __forceinline__ SsmCut ssm_warp_cut(const SsmScanArgs &a, int lane) {
 }
 
 // Segment `b` of the batch, or (FRONT) of its segments that are not their sequence's last: its
-// sequence, tokens [t0, t1), whether it is the sequence's first or last one, the state slot (-1:
+// sequence, tokens [t0, t1), its index there and whether it is the last one, the state slot (-1:
 // padding lane) and the entry of `enter` that holds the state it starts from (-1: it starts from
 // state_in).  False: nothing to do.  Whole warps call it.
 struct SsmSegment {
-    int seq, slot, entry;
+    int seq, slot, entry, index;
     long long t0, t1;
-    bool first, last;
+    bool last;
 };
 template <bool FRONT> __device__ __forceinline__ bool ssm_segment(const SsmScanArgs &a, int b, SsmSegment &g) {
     SsmCut c{b, 1, -1, 0};
@@ -121,7 +122,7 @@ template <bool FRONT> __device__ __forceinline__ bool ssm_segment(const SsmScanA
     g.t0 = s + (long long)k * a.seg_len;
     g.t1 = g.t0 + a.seg_len < e ? g.t0 + a.seg_len : e;
     if (g.t0 > g.t1) return false;
-    g.first = k == 0;
+    g.index = k;
     g.last = k == c.segs - 1;
     g.entry = c.entry0 >= 0 ? c.entry0 + k : -1;
     g.slot = slot_of(a.state_idx, g.seq, a.d.n_slots, a.err);
@@ -163,6 +164,18 @@ __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
 template <typename T> __device__ __forceinline__ float sigmoid_for(float x) { return sigmoid_f(x); }
 template <> __device__ __forceinline__ float sigmoid_for<__nv_bfloat16>(float x) {
     return __fdividef(1.0f, 1.0f + __expf(-x));
+}
+// sigmoid(x) and 1 - sigmoid(x), neither by a difference, so that the gradient of a gate that is all
+// but open keeps its digits.  (Below -80 both stop changing: 1e-35 and 1.)
+template <typename T> __device__ __forceinline__ void sigmoid_pair(float x, float &s, float &rest) {
+    const float e = expf(x < -80.f ? 80.f : -x);
+    s = 1.0f / (1.0f + e);
+    rest = e * s;
+}
+template <> __device__ __forceinline__ void sigmoid_pair<__nv_bfloat16>(float x, float &s, float &rest) {
+    const float e = __expf(x < -80.f ? 80.f : -x);
+    s = __fdividef(1.0f, 1.0f + e);
+    rest = e * s;
 }
 template <typename T> __device__ __forceinline__ float silu_for(float x) { return silu_f(x); }
 template <> __device__ __forceinline__ float silu_for<__nv_bfloat16>(float x) { return silu_fast(x); }

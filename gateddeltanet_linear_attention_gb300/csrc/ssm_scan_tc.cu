@@ -34,6 +34,7 @@
 // memory), not by memory or the tensor cores.
 #include <cuda.h>   // CUtensorMap (the encoder itself is reached through the runtime)
 
+#include <climits>
 #include <cstring>
 
 #include "ssm_common.cuh"
@@ -63,10 +64,11 @@ template <int N, int HU> struct TcSmem {
     static constexpr int ARR = XW + 2 * kXwBuf;              // [2][HU][5][128]: cs, cp, w, e, v
     static constexpr int DEC = ARR + 2 * HU * 5 * 512;       // [2][HU] chunk decays
     static constexpr int LOG = DEC + 2 * HU * 4;             // [2][HU] doubles: summed log-decays
-    static constexpr int BAR = LOG + 2 * HU * 8;
-    static constexpr int NBAR = 2 * kSlots + 27;
+    static constexpr int BAD = LOG + 2 * HU * 8;             // [128]: first token whose x is not finite
+    static constexpr int BAR = BAD + 512;
+    static constexpr int NBAR = 2 * kSlots + 29;
     static constexpr int SLOT = (BAR + 7) / 8 * 8 + NBAR * 8;
-    static constexpr int BYTES = SLOT + 16;
+    static constexpr int BYTES = SLOT + 16;                  // TMEM address, the two flags
     static_assert(BYTES <= 232448, "shared memory of an SM");
 };
 
@@ -75,7 +77,7 @@ template <int N, int HU> struct TcSmem {
 // behind (G, S, DS, Y, A, ST), even and odd chunks have a barrier each: the next phase of either then
 // needs the waiter's own progress.
 enum { B_G0 = 0, B_G1, B_P, B_S0, B_S1, B_XF, B_XE = B_XF + 4, B_DS0 = B_XE + 4, B_DS1, B_Y2, B_YC, B_Y0, B_Y1, B_YE, B_A0, B_A1, B_ST0, B_ST1,
-       B_FIX, B_END, B_END2, B_COUNT };
+       B_CLEAN0, B_CLEAN1, B_FIX, B_END, B_END2, B_COUNT };
 
 // 128-byte-swizzled operands: rows of 128 bytes, 8-row groups of 1,024 bytes, 64-element blocks
 // kHalfTile apart.  K-major: the row index is M or N, a 16-wide K step is 32 bytes further.
@@ -268,6 +270,37 @@ __device__ __forceinline__ f32x2 gate2(f32x2 v, f32x2 z) {
     return mul2(v, mul2(z, pack2(rcp_fast(q.x), rcp_fast(q.y))));
 }
 
+// P X multiplies a token's x with the zeros of the rows in front of it too, where a value that is
+// not finite would become NaN.  So x goes into that product with zeros in the places of such
+// values, and the outputs of their columns from their tokens on are NaN, as the sums over a state
+// of infinities or NaN are.  The search is the log-decay warps', which have time to spare (by the
+// output warps it cost 6 %).  A warp looks at 128 tokens by 64 columns of x:
+__device__ __forceinline__ bool not_finite(const unsigned char *x, int lane) {
+    uint32_t any = 0u;
+#pragma unroll 4
+    for (int k = 0; k < 32; ++k) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(x + (k * 32 + lane) * 16);
+        any |= ((v.x & 0x7fff7fffu) + 0x00800080u) | ((v.y & 0x7fff7fffu) + 0x00800080u) |
+               ((v.z & 0x7fff7fffu) + 0x00800080u) | ((v.w & 0x7fff7fffu) + 0x00800080u);
+    }
+    return (any & 0x80008000u) != 0;
+}
+// ... puts the zeros in, and keeps the first token of each column (rows from `count` on: no tokens)
+__device__ __noinline__ void clean(unsigned char *x, int lane, int count, int *from, int token) {
+    for (int i = lane; i < count * 64; i += 32) {
+        const int row = i >> 6, col = i & 63;
+        uint16_t *v = reinterpret_cast<uint16_t *>(x + row * 128 + (((col >> 3) ^ (row & 7)) << 4)) + (col & 7);
+        if ((*v & 0x7f80u) != 0x7f80u) continue;
+        *v = 0;
+        atomicMin(from + col, token + row);
+    }
+}
+// 64 columns of a row of y, in memory or (row & 7 to undo) in a tile
+__device__ __noinline__ void spoil(unsigned char *y, int swizzle, const int *from, int token) {
+    for (int i = 0; i < 64; ++i)
+        if (token >= from[i]) *(reinterpret_cast<uint16_t *>(y + (((i >> 3) ^ swizzle) << 4)) + (i & 7)) = 0x7fff;
+}
+
 }  // namespace
 
 // TMEM column of P's tokens 16 j .. 16 j + 15 (8 columns, two tokens each) of a unit's head: in the
@@ -322,16 +355,20 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
     auto array = [&](int st, int hh, int k) { return arr + ((st * HU + hh) * 5 + k) * 128; };
     float *decs = reinterpret_cast<float *>(sm + L::DEC);
     double *logs = reinterpret_cast<double *>(sm + L::LOG);
-    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(sm + L::SLOT), *gave_up = tmem_slot + 1;
+    int *bad_from = reinterpret_cast<int *>(sm + L::BAD);
+    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(sm + L::SLOT), *gave_up = tmem_slot + 1,
+                      *any_bad = tmem_slot + 2;
 
     if (tid == 0) {
         *gave_up = 0;
+        *any_bad = 0;
         for (int s = 0; s < kSlots; ++s) { tc::mbar_init(bar_full(s), 1); tc::mbar_init(bar_empty(s), 1); }
         const int counts[B_COUNT] = {1, 1, 128, 128, 128, 128, 128, 128, 128, 1, 1, 1, 1, 1, 1, 1, 128, 1, 1, 256, HU, HU,
-                                     256, 256, 128, 1, 1};
+                                     256, 256, HU, HU, 128, 1, 1};
         for (int k = 0; k < B_COUNT; ++k) tc::mbar_init(bar(k), counts[k]);
         tc::mbar_fence_init();
     }
+    if (!STATES && tid < 128) bad_from[tid] = INT_MAX;
     if (warp == 1) {
         tc::tmem_alloc(sbase + L::SLOT, 512);
         tc::tmem_relinquish();
@@ -389,7 +426,8 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
             }
             if (c >= 2) wait(bar_empty(slot_x(c)), half(c) - 1);
             if (*gave_up) break;
-            if (c == 0 && (a.lose & LOSE_SSM_TILE_COPY)) expect_tx(lead, bar_full(slot_x(c)), kTile);    // tests only
+            if (c == 0 && (STATES || sg.entry < 0) && (a.lose & LOSE_SSM_TILE_COPY))             // tests only
+                expect_tx(lead, bar_full(slot_x(c)), kTile);
             else load(slot_x(c), &maps.x, h0 * P, 2, t);
         }
         // copies in flight land before the CTA ends (a slot whose last copy was not started runs out)
@@ -425,6 +463,7 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
                 commit(lead, bar(B_Y2));
                 commit(lead, bar_empty(kSlotC));
                 wait(bar_full(slot_x(c)), half(c));
+                wait(bar(B_CLEAN0 + (c & 1)), half(c));
                 wait(bar(B_YC), c);
                 wait(bar(B_P), c);
                 tc::fence_after_sync();
@@ -538,13 +577,12 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
                         tmem_st8(tmem + lanes + p_col(j, hh), p);
                     }
                 }
-                // Tokens beside the rows: i <= r, exponents of their own
+                // Tokens beside the rows: exponents of their own.  What is above the diagonal, finite or
+                // not, is left out of the product's result.
 #pragma unroll 1
                 for (int j = 2 * wq; j < 2 * wq + 2; ++j) {
                     float G[16];
                     tc::tmem_ld16(tmem + lanes + kColG + 16 * j, G);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) G[i] = 16 * j + i <= row ? G[i] : 0.f;
 #pragma unroll
                     for (int hh = 0; hh < HU; ++hh) {
                         const float csr = array(st, hh, 0)[row];
@@ -553,13 +591,14 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
                         uint32_t p[8];
 #pragma unroll
                         for (int i = 0; i < 16; i += 4) {
-                            // above the diagonal an exponent may be anything: finite, for G = 0 there
                             const ulonglong2 k = *reinterpret_cast<const ulonglong2 *>(cp + i);
-                            const float2 u = unpack2(add2(cs, k.x)), v = unpack2(add2(cs, k.y));
-                            p[i / 2] = pack_bf16(mul2(pack2(exp2_fast(fminf(u.x, 126.f)), exp2_fast(fminf(u.y, 126.f))),
-                                                      pack2(G[i], G[i + 1])));
-                            p[i / 2 + 1] = pack_bf16(mul2(pack2(exp2_fast(fminf(v.x, 126.f)), exp2_fast(fminf(v.y, 126.f))),
-                                                          pack2(G[i + 2], G[i + 3])));
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) {
+                                const int n = i + 2 * q;
+                                const float2 u = unpack2(add2(cs, q ? k.y : k.x));
+                                const float2 v = unpack2(mul2(pack2(exp2_fast(u.x), exp2_fast(u.y)), pack2(G[n], G[n + 1])));
+                                p[n / 2] = pack_bf16(16 * j + n <= row ? v.x : 0.f, 16 * j + n + 1 <= row ? v.y : 0.f);
+                            }
                         }
                         tmem_st8(tmem + lanes + p_col(j, hh), p);
                     }
@@ -658,7 +697,14 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
         float *to = nullptr;
         if (STATES) to = a.enter + (long long)(sg.entry + 1) * all + at;
         else if (sg.last && a.state_out) to = a.state_out + (long long)sg.slot * all + at;
-        if (*gave_up) to = nullptr;
+        // a segment in front of this one whose state was not computed: its log-decay is +inf
+        bool lost = false;
+        if (!STATES && to && mine) {
+            for (int k = sg.entry - sg.index + lane; k < sg.entry; k += 32)
+                lost |= a.seg_log[(long long)k * d.heads + h] > 0.f;
+            lost = __any_sync(0xffffffffu, lost);              // (a warp's rows are of one head)
+        }
+        if (*gave_up || lost) to = nullptr;
         if (to && chunks > 0) {
 #pragma unroll 1
             for (int j = 0; j < N / 16; ++j) {
@@ -690,10 +736,10 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
                 uint32_t zn[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};   // z of the next 16 columns
                 if (has_z && live) load_32b(zrow, z_wide, zn);
                 wait(bar_full(slot_x(c)), half(c));
+                unsigned char *X = sm + L::RING + slot_x(c) * kTile + side * kHalfTile + row * 128;
                 wait(bar(B_DS0 + st), half(c));            // D has read the tile that y replaces
                 wait(bar(B_Y0 + st), half(c));
                 tc::fence_after_sync();
-                unsigned char *X = sm + L::RING + slot_x(c) * kTile + side * kHalfTile + row * 128;
                 __nv_bfloat16 *yrow = (__nv_bfloat16 *)a.y + t * out_cols + (long long)h0 * P + side * 64;
 #pragma unroll 1
                 for (int j = 0; j < 4; ++j) {
@@ -725,6 +771,8 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
                         else if (live) *reinterpret_cast<uint4 *>(yrow + j * 16 + k * 8) = u;
                     }
                 }
+                if (*any_bad && (live || !short_chunk))
+                    spoil(short_chunk ? (unsigned char *)yrow : X, short_chunk ? 0 : row & 7, bad_from + side * 64, c * kL + row);
                 tc::fence_async_smem();
                 tc::mbar_arrive(bar(B_ST0 + st));
             }
@@ -854,6 +902,21 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
             if (lane == 0) decs[st * HU + hh] = exp2_fast(total * kLog2e);
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(bar(B_A0 + st));
+            if (!STATES) {
+                wait(bar_full(slot_x(c)), half(c));
+                const int q0 = HU == 2 ? hh : 0, q1 = HU == 2 ? hh + 1 : 2;      // its head's 64 columns, or 128
+#pragma unroll 1
+                for (int q = q0; q < q1; ++q) {
+                    unsigned char *X = sm + L::RING + slot_x(c) * kTile + q * kHalfTile;
+                    if (!__any_sync(0xffffffffu, not_finite(X, lane))) continue;
+                    wait(bar(B_DS0 + st), half(c));        // (D reads x as it is)
+                    clean(X, lane, count, bad_from + q * 64, c * kL);
+                    *any_bad = 1;
+                    tc::fence_async_smem();
+                    __syncwarp();
+                }
+                arrive(lane == 0, bar(B_CLEAN0 + st));
+            }
         }
         if (STATES && lane == 0) logs[st * HU + hh] = log_sum;
     }
@@ -863,7 +926,9 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
     if (!STATES) await_previous();
     if (tid == 0 && *gave_up) set_error(a.err, GDN_DEVERR_TIMEOUT);
     if (warp == 1) tc::tmem_dealloc(tmem, 512);
-    if (STATES && tid < heads) a.seg_log[(long long)sg.entry * d.heads + h0 + tid] = (float)(logs[tid] + logs[HU + tid]);
+    if (STATES && tid < heads)
+        a.seg_log[(long long)sg.entry * d.heads + h0 + tid] =
+            *gave_up ? __int_as_float(0x7f800000) : (float)(logs[tid] + logs[HU + tid]);
 }
 
 namespace {

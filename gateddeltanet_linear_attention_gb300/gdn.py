@@ -542,7 +542,7 @@ def gdn_block_norm(residual, w_pre=None, h=None, block=None, res_out=None, w_pos
     if like is None:
         a.refuse("h", "and block are both missing: nothing to do")
     act, res = like.dtype, residual.dtype
-    cols = 0 if gate is None else gate.shape[1]
+    cols = 0 if gate is None else gate.shape[-1]
     io = BlockNormIO(rows, dim, _dt(like), _dt(residual), eps, weight_offset, res_scale,
                      *a.view(block, "block", wide, act), *a.view(gate, "gate", (rows, cols), act), cols,
                      *a.view(residual, "residual", wide, res), a.whole(w_post, "w_post", (dim,), a.f32),
@@ -564,7 +564,7 @@ def gdn_block_norm_backward(res_out, rstd_pre=None, w_pre=None, dh=None, d_res_o
     if like is None:
         a.refuse("dh", "and block are both missing: nothing to do")
     act, res = like.dtype, res_out.dtype
-    cols = 0 if gate is None else gate.shape[1]
+    cols = 0 if gate is None else gate.shape[-1]
     io = BlockNormIO(rows, dim, _dt(like), _dt(res_out), 0.0, weight_offset, res_scale,
                      *a.view(block, "block", wide, act), *a.view(gate, "gate", (rows, cols), act), cols,
                      *a.view(res_out, "res_out", wide, res), a.whole(w_post, "w_post", (dim,), a.f32),

@@ -389,7 +389,10 @@ gdn_status gdn_state_copy(const gdn_config *cfg, const float *src_state, const v
  * 2*groups*d_state.  The rules of the top of this file hold: slots, padding
  * lanes (zero outputs, nothing written), views, alignment, streams, errors.
  * Packed rows behind cu_seqlens[n_seqs] are neither read nor written, so a
- * captured call may carry a smaller batch than its T.  */
+ * captured call may carry a smaller batch than its T.  A value that is not
+ * finite reaches the outputs and states that it is a part of (which are then
+ * not finite either: NaN where the sum may have been an infinity), never
+ * tokens in front of it, other heads' columns or other sequences.  */
 typedef struct gdn_ssm_config {
     int32_t groups, heads;     /* heads % groups == 0; heads <= 4096 */
     int32_t d_state, head_dim; /* d_state in {16, 32, 64, 128}, head_dim in {32, 64, 128} */
@@ -513,8 +516,9 @@ gdn_status gdn_block_norm_backward(const gdn_block_norm_io *io, void *workspace,
  * operand copy so that such a wait really runs out: bit 0 the first head
  * state of a gdn_mixer_decode / gdn_mixer_decode_q8 launch, bit 1 the first
  * chunk operand of the tensor-core state chain (gdn_chunk_prefill,
- * gdn_mixer_prefill), bit 2 the first x tile of every tensor-core
- * gdn_ssm_prefill segment.  A call that timed out writes no state.  Process-wide,
+ * gdn_mixer_prefill), bit 2 the first x tile of tensor-core
+ * gdn_ssm_prefill (of every sequence that is not cut, and of every segment in
+ * front of the last where one is).  A call that timed out writes no state.  Process-wide,
  * read at each call; GDN_ERR_INVALID_ARG for wait_ns = 0, above 60 s, or an
  * unknown bit. */
 gdn_status gdn_debug_set_wait(uint64_t wait_ns, uint32_t lose);

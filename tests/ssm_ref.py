@@ -113,7 +113,8 @@ def norm_backward(p, gate, u, w1, w2, k1, k2, dh, dro, offset, scale):
         dn, dnm = scale * sg * du, (scale * sg * mag if gate is not None else abs(scale) * mag)
         dnm = dnm.abs()
         if gate is not None:
-            dg, dgm = dn * (1 - sg) * ph * w, (dnm * (1 - sg) * ph * w).abs()
+            shut = torch.sigmoid(-gate.double())           # 1 - sg, without the difference
+            dg, dgm = dn * shut * ph * w, (dnm * shut * ph * w).abs()
             if gate.shape[1] == 1 and dim > 1:
                 dg, dgm = dg.sum(1, keepdim=True), dgm.sum(1, keepdim=True)
             out["d_gate"] = (dg, dgm)

@@ -236,3 +236,39 @@ def test_offsets_past_32_bits():
     want = ref.norm_backward(p[s].cpu(), None, ro[s].cpu(), w.cpu(), w.cpu(), k1[s].cpu(), k2[s].cpu(), h[s].cpu(), dro, 0.0, 1.0)
     for k, v in (("d_residual", dr), ("d_block", dp)):
         ref.check(v[s], *want[k], (2 * dim + 64) * ref.U32, k)
+
+
+@pytest.mark.parametrize("act", [BF, F32])
+@pytest.mark.parametrize("kind", ["channel", "row"])
+def test_gradient_of_gates_that_are_all_but_open_or_shut(act, kind):
+    """1 - sigmoid is not taken as a difference.  With one column and d_r' alone the gradient is a product:
+    a dozen roundings and the exponential's error, 2 + 1.2 |x| units in the last place where it is the fast one."""
+    x = torch.tensor([-70.0, -30.0, -8.0, 0.0, 8.0, 17.0, 30.0, 70.0])
+    rows, dim = (8, 1) if kind == "row" else (8, 8)
+    g = torch.Generator().manual_seed(5)
+    p, u, dro = (torch.randn(rows, dim, generator=g).to(act) for _ in range(3))
+    gate = (x[:, None] if kind == "row" else x[None].expand(8, 8).contiguous()).to(act)
+    w, k = 1 + 0.2 * torch.randn(dim, generator=g), 1 + torch.rand(rows, generator=g)
+    dg = torch.empty(rows, dim, dtype=act, device="cuda")
+    gdn.gdn_block_norm_backward(u.cuda(), d_res_out=dro.cuda(), block=p.cuda(), rstd_post=k.cuda(), w_post=w.cuda(),
+                                gate=gate.cuda(), res_scale=0.7, d_gate=dg)
+    want = ref.norm_backward(p, gate, u, w, None, k, None, None, dro, 0.0, 0.7)["d_gate"][0]
+    ref.check(dg, want, want.abs(), (40 + (2 * (2 + 1.2 * 70) if act == BF else 0)) * ref.U32, "d_gate")
+
+
+def test_binding_refuses_tensors_that_do_not_fit():
+    d = {k: up(v) for k, v in make(6, 64, BF, BF).items()}
+    h = torch.empty(6, 64, dtype=BF, device="cuda")
+
+    def call(**kw):
+        a = dict(residual=d["residual"], w_pre=d["w_pre"], h=h, block=d["block"], res_out=torch.empty_like(h), w_post=d["w_post"],
+                 gate=d["gate"])
+        a.update(kw)
+        gdn.gdn_block_norm(**a)
+
+    call()
+    for bad in (dict(gate=d["gate"][:, :2]), dict(gate=d["gate"][:, 0]), dict(block=d["block"].float()), dict(w_pre=d["w_pre"].cpu()),
+                dict(h=h[:5]), dict(residual=d["residual"][:, :32]), dict(res_out=torch.empty(6, 1, dtype=BF, device="cuda").expand(6, 64)),
+                dict(residual=d["residual"][0]), dict(block=None), dict(w_pre=None)):
+        with pytest.raises((ValueError, RuntimeError)):
+            call(**bad)

@@ -548,3 +548,79 @@ def test_offsets_past_32_bits(act, heads):
         ref.check(oc[s:e], val, mag, CONV_REL, "conv")
         assert torch.equal(hist[n].cpu().double(), new)
     assert gdn.gdn_device_error() == 0
+
+
+@pytest.mark.parametrize("act", ["fp32", "bf16"])
+@pytest.mark.parametrize("fill", [float("nan"), INF])
+@pytest.mark.parametrize("what", ["x", "b", "c", "dt"])
+def test_not_finite_stays_behind_its_token(act, fill, what):
+    """One value that is not finite: tokens in front of it, and the columns, heads and groups that do
+    not see it, are right; what it reaches is not finite either."""
+    b = Batch([600, 90], H=4, G=2, N=64, P=64, act=act, seed=19)
+    at = 341                                       # inside a chunk, of a segment with others on both sides
+    x, bb, c = b.parts(b.xbc)
+    {"x": x, "b": bb, "c": c, "dt": b.u}[what][at, 1] = fill
+    y, out = b.run()
+    for n in (0, 1):
+        s, e = int(b.cu[n]), int(b.cu[n + 1])
+        val, mag, S, M = b.reference(n)
+        L = e - s
+        rel = (8 * L + b.N + 64) * ref.U32
+        rel_y = rel + (2 * 2.0 ** -8 + 2 * 128 * 60 * ref.U32 if act == "bf16" else 0)
+        for got, v, m, r, name in ((y[s:e].cpu(), val.reshape(L, -1), mag.reshape(L, -1), rel_y, "y"), (out[n].cpu(), S, M, rel, "state")):
+            ok = v.isfinite()
+            assert n == 1 or not ok.all() or what == "c"
+            assert not got[~ok].isfinite().any()
+            ref.check(got[ok], v[ok], m[ok], r, name)
+    assert gdn.gdn_device_error() == 0
+
+
+@pytest.mark.parametrize("act", ["fp32", "bf16"])
+def test_conv_and_step_on_another_stream_and_in_a_graph(act):
+    b = Batch([37, 0, 5], act=act, seed=20).upload()
+    CH, n = b.xbc.shape[1], 3
+    g = torch.Generator().manual_seed(21)
+    w, hist = randn(CH, 4, gen=g, dtype=b.act).cuda(), randn(3, CH, 3, gen=g, dtype=b.act).cuda()
+    ws = torch.empty(gdn.gdn_ssm_workspace_size(b.cfg, n, n), dtype=torch.uint8, device="cuda")
+
+    def run(h, state, out, y, stream=None):
+        gdn.gdn_ssm_conv_prefill(b.cfg, b.d_xbc, b.d_cu, w, None, h, None, out, stream=stream)
+        gdn.gdn_ssm_decode(b.cfg, b.d_xbc[:n], b.d_u[:n], w, h, b.d_A_log, state, y, ws, D=b.d_D, stream=stream)
+
+    def fresh():
+        return (hist.clone(), b.d_state.clone(), torch.empty_like(b.d_xbc),
+                torch.empty(n, b.H * b.P, dtype=b.act, device="cuda"))
+
+    want = fresh()
+    run(*want)
+    other, s = fresh(), torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    run(*other, stream=s)
+    s.synchronize()
+    captured, graph = fresh(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(*captured)
+    assert torch.equal(captured[0], hist)          # capturing ran nothing
+    graph.replay()
+    torch.cuda.synchronize()
+    for i in range(4):
+        assert torch.equal(want[i], other[i]) and torch.equal(want[i], captured[i])
+
+
+def test_binding_refuses_tensors_that_do_not_fit():
+    b = Batch([40], H=2, G=1, seed=22).upload()
+    y = torch.empty(40, 128, dtype=b.act, device="cuda")
+    good = dict(y=y, out=b.d_state)
+    b.launch(**good)
+    for k, bad in (("d_xbc", b.d_xbc.float()), ("d_xbc", b.d_xbc[:, :-64]), ("d_u", b.d_u[:-1]), ("d_u", b.u),
+                   ("d_A_log", b.d_A_log.double()), ("d_cu", b.d_cu.long()), ("d_z", b.d_z.T), ("d_D", b.d_D[:1])):
+        kept = getattr(b, k)
+        setattr(b, k, bad)
+        with pytest.raises(ValueError):
+            b.launch(**good)
+        setattr(b, k, kept)
+    for bad in (dict(good, y=y[:, ::2]), dict(good, y=y.expand(40, 128).T), dict(good, out=b.d_state[:0]), dict(good, state=b.state)):
+        with pytest.raises(ValueError):
+            b.launch(**bad)
+    b.ws = b.ws[:0]
+    b.launch(**good)                               # (not cut: no workspace is needed)
