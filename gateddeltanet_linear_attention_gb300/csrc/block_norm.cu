@@ -41,17 +41,28 @@ template <> struct Raw8<__nv_bfloat16> {
     }
 };
 
+// Eight values as four pairs for the packed multiply-adds.
+template <typename R> __device__ __forceinline__ void get_pairs(const R &r, f32x2 (&v)[4]) {
+    float f[8];
+    r.get(f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = pack2(f[2 * j], f[2 * j + 1]);
+}
+__device__ __forceinline__ f32x2 both(float x) { return pack2(x, x); }
+
 // A thread's chunk i of a row: with VEC 8 neighbours from one or two vector
-// loads, otherwise 8 elements NT apart (every load of a warp contiguous).
-template <bool VEC> struct Chunk {
+// loads, otherwise 8 elements 32 apart in its warp's NV x 256 (every load of a
+// warp contiguous, at a constant distance from the one before).
+template <bool VEC, int NV> struct Chunk {
     // elements past the row's end read as zero and add nothing to its sums
-    int base, dim, stride;
+    static constexpr int stride = VEC ? 1 : 32;
+    int base, dim;
     __device__ __forceinline__ Chunk(int i, int lane, int nt, int dim_) : dim(dim_) {
-        base = VEC ? (i * nt + lane) * 8 : i * nt * 8 + lane;
-        stride = VEC ? 1 : nt;
+        base = VEC ? (i * nt + lane) * 8 : ((lane >> 5) * NV + i) * 256 + (lane & 31);
     }
     __device__ __forceinline__ bool in(int j) const { return VEC ? base < dim : base + j * stride < dim; }
     __device__ __forceinline__ int at(int j) const { return base + j * stride; }
+    __device__ __forceinline__ bool whole() const { return in(7); }     // all 8 in the row: one test for them
 };
 
 template <bool VEC, typename C> __device__ __forceinline__ void load_raw(const C &c, const float *p, Raw8<float> &r) {
@@ -60,8 +71,13 @@ template <bool VEC, typename C> __device__ __forceinline__ void load_raw(const C
         else { r.a = r.b = make_float4(0.f, 0.f, 0.f, 0.f); }
     } else {
         float v[8];
+        if (c.whole()) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = c.in(j) ? p[c.at(j)] : 0.f;
+            for (int j = 0; j < 8; ++j) v[j] = p[c.at(j)];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = c.in(j) ? p[c.at(j)] : 0.f;
+        }
         r.a = make_float4(v[0], v[1], v[2], v[3]);
         r.b = make_float4(v[4], v[5], v[6], v[7]);
     }
@@ -71,9 +87,15 @@ __device__ __forceinline__ void load_raw(const C &c, const __nv_bfloat16 *p, Raw
     if (VEC) {
         r.u = c.in(0) ? *reinterpret_cast<const uint4 *>(p + c.base) : make_uint4(0u, 0u, 0u, 0u);
     } else {
+        const uint16_t *q = reinterpret_cast<const uint16_t *>(p);
         unsigned v[8];
+        if (c.whole()) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = c.in(j) ? (unsigned)__bfloat16_as_ushort(p[c.at(j)]) : 0u;
+            for (int j = 0; j < 8; ++j) v[j] = q[c.at(j)];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = c.in(j) ? (unsigned)q[c.at(j)] : 0u;
+        }
         r.u = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
     }
 }
@@ -83,6 +105,9 @@ template <bool VEC, typename C> __device__ __forceinline__ void store8v(const C 
             store4f(p + c.base, make_float4(v[0], v[1], v[2], v[3]));
             store4f(p + c.base + 4, make_float4(v[4], v[5], v[6], v[7]));
         }
+    } else if (c.whole()) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) p[c.at(j)] = v[j];
     } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -98,6 +123,9 @@ __device__ __forceinline__ void store8v(const C &c, __nv_bfloat16 *p, const floa
             for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
             *reinterpret_cast<uint4 *>(p + c.base) = *reinterpret_cast<const uint4 *>(h);
         }
+    } else if (c.whole()) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) p[c.at(j)] = __float2bfloat16_rn(v[j]);
     } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -113,50 +141,35 @@ __device__ __forceinline__ void cp_async16(void *dst, const void *src) {
 // Sum over the threads of a row; every thread gets it.  `buf` holds a value per
 // warp, twice: successive sums take turns (`turn`), so that one barrier per sum
 // is enough: a half is written again only after the other half's barrier.
-template <bool WARP> __device__ __forceinline__ float2 row_sum2(float2 v, float2 (*buf)[32], int &turn) {
-    v.x = warp_sum(v.x);
-    v.y = warp_sum(v.y);
-    if (WARP) return v;
-    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    float2 *half = buf[turn];
-    turn ^= 1;
-    if (lane == 0) half[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float2 u = lane < warps ? half[lane] : make_float2(0.f, 0.f);
-    u.x = warp_sum(u.x);
-    u.y = warp_sum(u.y);
-    return u;
-}
-template <bool WARP> __device__ __forceinline__ float row_sum(float v, float2 (*buf)[32], int &turn) {
+template <bool WARP> __device__ __forceinline__ float row_sum(float v, float (*buf)[32], int &turn) {
     v = warp_sum(v);
     if (WARP) return v;
     const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    float2 *half = buf[turn];
+    float *half = buf[turn];
     turn ^= 1;
-    if (lane == 0) half[threadIdx.x >> 5].x = v;
+    if (lane == 0) half[threadIdx.x >> 5] = v;
     __syncthreads();
-    return warp_sum(lane < warps ? half[lane].x : 0.f);
+    return warp_sum(lane < warps ? half[lane] : 0.f);
 }
 
 }  // namespace
 
-// Blocks of MAXT threads at most, 512 threads on an SM and so 128 registers each.  Rows that need
-// 1,024 threads leave 64 registers a thread: the forward kernel then reads the weights at every
-// row (from L1) and does not load ahead (LEAN).
+// Blocks of MAXT threads at most, in the forward kernel with the registers to keep the weights and
+// to load a row ahead of the one that is computed (KEEP, AHEAD).
 constexpr int sm_blocks(int maxt) { return maxt >= 512 ? 1 : 512 / maxt; }
 
 template <typename TA, typename TR, int NV, int MAXT, bool WARP, bool VEC>
 __global__ void __launch_bounds__(MAXT, sm_blocks(MAXT)) block_norm_kernel(NormArgs a) {
-    __shared__ float2 buf[2][32];
+    __shared__ float buf[2][32];
     int turn = 0;
-    using Ch = Chunk<VEC>;
+    using Ch = Chunk<VEC, NV>;
     const int lane = WARP ? threadIdx.x & 31 : threadIdx.x, nt = WARP ? 32 : blockDim.x;
     const long long first = WARP ? blockIdx.x * (long long)kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
     const long long step = WARP ? gridDim.x * (long long)kWarpRows : gridDim.x;
     const float inv_dim = 1.0f / (float)a.dim;
     const bool channel_gate = a.gate && a.gate_cols > 1, row_gate = a.gate && a.gate_cols == 1;
 
-    constexpr bool LEAN = MAXT == 1024;
+    constexpr bool AHEAD = VEC && MAXT < 1024, KEEP = AHEAD;
     float w1[NV][8], w2[NV][8];
     auto weight = [&](const float *w, int i, float (&v)[8]) {
         Raw8<float> r;
@@ -165,7 +178,7 @@ __global__ void __launch_bounds__(MAXT, sm_blocks(MAXT)) block_norm_kernel(NormA
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] += a.offset;
     };
-    if (!LEAN) {
+    if (KEEP) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if (a.w_post) weight(a.w_post, i, w1[i]);
@@ -185,9 +198,9 @@ __global__ void __launch_bounds__(MAXT, sm_blocks(MAXT)) block_norm_kernel(NormA
         }
         if (row_gate) gate1 = to_f32(((const TA *)a.gate)[row * a.ld_gate]);
     };
-    if (!LEAN && first < a.rows) fetch(first);
+    if (AHEAD && first < a.rows) fetch(first);
     for (long long row = first; row < a.rows; row += step) {
-        if (LEAN) fetch(row);
+        if (!AHEAD) fetch(row);
         float u[NV][8], p[NV][8], gt[NV][8];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -196,7 +209,7 @@ __global__ void __launch_bounds__(MAXT, sm_blocks(MAXT)) block_norm_kernel(NormA
             if (channel_gate) rg[i].get(gt[i]);
         }
         const float g1 = gate1;
-        if (!LEAN && row + step < a.rows) fetch(row + step);
+        if (AHEAD && row + step < a.rows) fetch(row + step);
         if (a.block) {
             float k = 1.0f;
             if (a.w_post) {
@@ -212,7 +225,7 @@ __global__ void __launch_bounds__(MAXT, sm_blocks(MAXT)) block_norm_kernel(NormA
             const float rs = a.scale * (row_gate ? sigmoid_f(g1) : 1.0f);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                if (LEAN && a.w_post) weight(a.w_post, i, w1[i]);
+                if (!KEEP && a.w_post) weight(a.w_post, i, w1[i]);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     float v = a.w_post ? p[i][j] * k * w1[i][j] : p[i][j];
@@ -238,7 +251,7 @@ __global__ void __launch_bounds__(MAXT, sm_blocks(MAXT)) block_norm_kernel(NormA
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 float v[8];
-                if (LEAN) weight(a.w_pre, i, w2[i]);
+                if (!KEEP) weight(a.w_pre, i, w2[i]);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[j] = u[i][j] * k * w2[i][j];
                 store8v<VEC>(Ch(i, lane, nt, a.dim), (TA *)a.h + row * a.ld_h, v);
@@ -262,19 +275,42 @@ template <typename TA, typename TR, int NV, bool VEC> constexpr int stage_bytes(
 // CTAs by norm_weight_grad_kernel, always in the same order.
 template <typename TA, typename TR, int NV, int MAXT, bool WARP, bool VEC>
 __global__ void __launch_bounds__(MAXT, sm_blocks(MAXT)) block_norm_bwd_kernel(NormArgs a) {
-    __shared__ float2 buf[2][32];
+    __shared__ float buf[2][32];
     int turn = 0;
-    using Ch = Chunk<VEC>;
+    using Ch = Chunk<VEC, NV>;
     const int lane = WARP ? threadIdx.x & 31 : threadIdx.x, nt = WARP ? 32 : blockDim.x;
     const long long first = WARP ? blockIdx.x * (long long)kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
     const long long step = WARP ? gridDim.x * (long long)kWarpRows : gridDim.x;
     const float inv_dim = 1.0f / (float)a.dim;
     const bool channel_gate = a.gate && a.gate_cols > 1, row_gate = a.gate && a.gate_cols == 1;
-    float dw1[NV][8], dw2[NV][8];
+    f32x2 dw1[NV][4], dw2[NV][4];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) dw1[i][j] = dw2[i][j] = 0.f;
+        for (int j = 0; j < 4; ++j) dw1[i][j] = dw2[i][j] = 0ull;
+    // piece i of a weight with its offset, 1 where there is none
+    auto weight = [&](const float *w, int i, f32x2 (&v)[4]) {
+        if (w) {
+            Raw8<float> r;
+            load_raw<VEC>(Ch(i, lane, nt, a.dim), w, r);
+            get_pairs(r, v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = add2(v[j], both(a.offset));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = both(1.0f);
+        }
+    };
+    auto store_act = [&](void *p, long long ld, long long row, int i, const f32x2 (&v)[4]) {
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 q = unpack2(v[j]);
+            f[2 * j] = q.x;
+            f[2 * j + 1] = q.y;
+        }
+        store8v<VEC>(Ch(i, lane, nt, a.dim), (TA *)p + row * ld, f);
+    };
 
     // The five operands of the next row come into shared memory while this one is computed: every
     // thread copies and reads its own 16- or 32-byte pieces, so no barrier is needed.  (Rows whose
@@ -306,6 +342,15 @@ __global__ void __launch_bounds__(MAXT, sm_blocks(MAXT)) block_norm_bwd_kernel(N
     };
     if (AHEAD) ahead(first, 0);
     int turn_row = 0;
+    // the next row's factors, loaded a row ahead
+    float n1 = 1.0f, n2 = 0.f, ng = 0.f;
+    auto factors = [&](long long row) {
+        if (row >= a.rows) return;
+        if (a.w_post) n1 = a.k_post[row];
+        if (a.dh) n2 = a.k_pre[row];
+        if (row_gate) ng = to_f32(((const TA *)a.gate)[row * a.ld_gate]);
+    };
+    factors(first);
     for (long long row = first; row < a.rows; row += step, turn_row ^= 1) {
         Raw8<TA> rp[NV], rg[NV], rh[NV];
         Raw8<TR> ru[NV], rd[NV];
@@ -325,101 +370,110 @@ __global__ void __launch_bounds__(MAXT, sm_blocks(MAXT)) block_norm_bwd_kernel(N
                 if (channel_gate) load_raw<VEC>(c, (const TA *)a.gate + row * a.ld_gate, rg[i]);
             }
         }
-        float du[NV][8];
+        const float k1 = n1, k2 = n2;
+        float s1 = 1.0f, q1 = 0.f;
+        if (row_gate) sigmoid_pair<float>(ng, s1, q1);
+        factors(row + step);
+        f32x2 du[NV][4];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if (a.d_res_out) {
                 if (AHEAD) rd[i].from(piece(turn_row, 4, i), Ch(i, lane, nt, a.dim).in(0));
-                rd[i].get(du[i]);
+                get_pairs(rd[i], du[i]);
             } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) du[i][j] = 0.f;
+                for (int j = 0; j < 4; ++j) du[i][j] = 0ull;
             }
         }
         if (a.dh) {
-            const float k = a.k_pre[row];
-            float g[NV][8], uh[NV][8], dot = 0.f;
+            f32x2 g[NV][4], uh[NV][4], dot = 0ull;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const Ch c(i, lane, nt, a.dim);
-                Raw8<float> rw;
-                float w[8];
-                load_raw<VEC>(c, a.w_pre, rw);
-                rw.get(w);
+                f32x2 w[4];
+                weight(a.w_pre, i, w);
                 if (AHEAD) {
                     rh[i].from(piece(turn_row, 0, i), Ch(i, lane, nt, a.dim).in(0));
                     ru[i].from(piece(turn_row, 3, i), Ch(i, lane, nt, a.dim).in(0));
                 }
-                rh[i].get(g[i]);
-                ru[i].get(uh[i]);
+                get_pairs(rh[i], g[i]);
+                get_pairs(ru[i], uh[i]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    uh[i][j] *= k;
-                    dw2[i][j] = fmaf(g[i][j], uh[i][j], dw2[i][j]);
-                    g[i][j] *= w[j] + a.offset;
-                    dot = fmaf(g[i][j], uh[i][j], dot);
+                for (int j = 0; j < 4; ++j) {
+                    uh[i][j] = mul2(uh[i][j], both(k2));
+                    dw2[i][j] = fma2(g[i][j], uh[i][j], dw2[i][j]);
+                    g[i][j] = mul2(g[i][j], w[j]);
+                    dot = fma2(g[i][j], uh[i][j], dot);
                 }
             }
-            const float m = row_sum<WARP>(dot, buf, turn) * inv_dim;
+            const float2 sum = unpack2(dot);
+            const float m = row_sum<WARP>(sum.x + sum.y, buf, turn) * inv_dim;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) du[i][j] = fmaf(k, g[i][j] - uh[i][j] * m, du[i][j]);
+                for (int j = 0; j < 4; ++j) du[i][j] = fma2(both(k2), fma2(both(-m), uh[i][j], g[i][j]), du[i][j]);
         }
         if (a.d_res) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                store8v<VEC>(Ch(i, lane, nt, a.dim), (TR *)a.d_res + row * a.ld_dres, du[i]);
+            for (int i = 0; i < NV; ++i) {
+                float f[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 q = unpack2(du[i][j]);
+                    f[2 * j] = q.x;
+                    f[2 * j + 1] = q.y;
+                }
+                store8v<VEC>(Ch(i, lane, nt, a.dim), (TR *)a.d_res + row * a.ld_dres, f);
+            }
         }
         if (a.block) {
-            const float k = a.w_post ? a.k_post[row] : 1.0f;
-            float s1 = 1.0f, q1 = 0.f;
-            if (row_gate) sigmoid_pair<float>(to_f32(((const TA *)a.gate)[row * a.ld_gate]), s1, q1);
-            float2 sums = make_float2(0.f, 0.f);      // sum of dn w1 p^, sum of the row gate's gradient
+            f32x2 dot = 0ull;                         // of dn w1 and p^
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const Ch c(i, lane, nt, a.dim);
-                float ph[8], gt[8], w[8];
-                if (AHEAD) {
-                    rp[i].from(piece(turn_row, 1, i), Ch(i, lane, nt, a.dim).in(0));
-                    if (channel_gate) rg[i].from(piece(turn_row, 2, i), Ch(i, lane, nt, a.dim).in(0));
-                }
-                rp[i].get(ph);
-                if (channel_gate) rg[i].get(gt);
-                if (a.w_post) {
-                    Raw8<float> rw;
-                    load_raw<VEC>(c, a.w_post, rw);
-                    rw.get(w);
+                f32x2 ph[4], w[4], sg[4], rest[4];
+                if (AHEAD) rp[i].from(piece(turn_row, 1, i), Ch(i, lane, nt, a.dim).in(0));
+                get_pairs(rp[i], ph);
+                weight(a.w_post, i, w);
+                if (channel_gate) {
+                    float x[8];
+                    if (AHEAD) rg[i].from(piece(turn_row, 2, i), Ch(i, lane, nt, a.dim).in(0));
+                    rg[i].get(x);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const f32x2 e = pack2(exp_neg<TA>(x[2 * j]), exp_neg<TA>(x[2 * j + 1]));
+                        const float2 q = unpack2(add2(e, both(1.0f)));
+                        sg[j] = pack2(one_over<TA>(q.x), one_over<TA>(q.y));
+                        rest[j] = mul2(e, sg[j]);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) sg[j] = both(s1);
                 }
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float wj = a.w_post ? w[j] + a.offset : 1.0f;
-                    ph[j] *= k;
-                    float sg = s1, rest = q1;
-                    if (channel_gate) sigmoid_pair<TA>(gt[j], sg, rest);
-                    const float dn = a.scale * du[i][j] * sg;
-                    if (a.gate) {
-                        gt[j] = dn * rest * ph[j] * wj;
-                        sums.y += gt[j];
-                    }
-                    dw1[i][j] = fmaf(dn, ph[j], dw1[i][j]);
-                    du[i][j] = dn * wj;               // du becomes the gradient of p^
-                    sums.x = fmaf(du[i][j], ph[j], sums.x);
+                for (int j = 0; j < 4; ++j) {
+                    ph[j] = mul2(ph[j], both(k1));
+                    const f32x2 dn = mul2(mul2(sg[j], both(a.scale)), du[i][j]);
+                    dw1[i][j] = fma2(dn, ph[j], dw1[i][j]);
+                    du[i][j] = mul2(dn, w[j]);        // du becomes the gradient of p^
+                    dot = fma2(du[i][j], ph[j], dot);
+                    if (channel_gate) rest[j] = mul2(rest[j], mul2(du[i][j], ph[j]));
                 }
-                if (channel_gate && a.d_gate) store8v<VEC>(c, (TA *)a.d_gate + row * a.ld_dgate, gt);
+                if (channel_gate && a.d_gate) store_act(a.d_gate, a.ld_dgate, row, i, rest);
             }
-            if (a.w_post || row_gate) sums = row_sum2<WARP>(sums, buf, turn);
-            if (row_gate && a.d_gate && lane == 0) ((TA *)a.d_gate)[row * a.ld_dgate] = from_f32<TA>(sums.y);
+            const float2 sum2 = unpack2(dot);
+            float sum = sum2.x + sum2.y;
+            if (a.w_post || row_gate) sum = row_sum<WARP>(sum, buf, turn);
+            // (of a row's one gate: the same sum times 1 - sigmoid)
+            if (row_gate && a.d_gate && lane == 0) ((TA *)a.d_gate)[row * a.ld_dgate] = from_f32<TA>(sum * q1);
             if (a.d_block) {
-                const float m = a.w_post ? sums.x * inv_dim : 0.f;
+                const float m = a.w_post ? -k1 * k1 * sum * inv_dim : 0.f;
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
-                    float ph[8], v[8];
+                    f32x2 p[4];
                     if (AHEAD) rp[i].from(piece(turn_row, 1, i), Ch(i, lane, nt, a.dim).in(0));
-                    rp[i].get(ph);
+                    get_pairs(rp[i], p);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] = a.w_post ? k * (du[i][j] - ph[j] * k * m) : du[i][j];
-                    store8v<VEC>(Ch(i, lane, nt, a.dim), (TA *)a.d_block + row * a.ld_dblock, v);
+                    for (int j = 0; j < 4; ++j) p[j] = fma2(both(m), p[j], mul2(both(k1), du[i][j]));
+                    store_act(a.d_block, a.ld_dblock, row, i, p);
                 }
             }
         }
@@ -435,8 +489,9 @@ __global__ void __launch_bounds__(MAXT, sm_blocks(MAXT)) block_norm_bwd_kernel(N
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             if (c.in(j)) {
-                to[c.at(j)] = dw1[i][j];
-                to[a.dim + c.at(j)] = dw2[i][j];
+                const float2 p = unpack2(dw1[i][j / 2]), q = unpack2(dw2[i][j / 2]);
+                to[c.at(j)] = j & 1 ? p.y : p.x;
+                to[a.dim + c.at(j)] = j & 1 ? q.y : q.x;
             }
     }
 }
@@ -461,69 +516,108 @@ __global__ void __launch_bounds__(1024) norm_weight_grad_kernel(const float *ws,
 
 namespace {
 
-// A warp owns a row of up to 512 elements, a CTA a longer one; a thread has 8 or 16 elements (with
-// 8 alone the sums over a CTA's warps took a third of the instructions: 8,192 x 4,096 forward 63 us).
+// A warp owns a row of up to 512 elements, a CTA a longer one; a thread has 8 or 16 elements, see
+// fwd_dim and bwd_dim.
 bool warp_rows(int dim) { return dim <= 512; }
-int row_threads(int dim) { return warp_rows(dim) ? 32 * kWarpRows : ((dim + 15) / 16 + 31) / 32 * 32; }
-
-// CTAs of the backward, and so the parts of the weight gradients.
-int bwd_ctas(long long rows, int dim) {
-    const int threads = row_threads(dim);
-    const long long cap = (long long)sm_count() * (threads < 512 ? 512 / threads : 1);
-    const long long want = warp_rows(dim) ? (rows + kWarpRows - 1) / kWarpRows : rows;
-    return (int)(want < cap ? want : cap);
-}
+int row_threads(int dim, int each) { return warp_rows(dim) ? 32 * kWarpRows : ((dim + each - 1) / each + 31) / 32 * 32; }
+long long row_ctas(long long rows, int dim) { return warp_rows(dim) ? (rows + kWarpRows - 1) / kWarpRows : rows; }
+// Backward CTAs that an SM's registers hold, 512 threads' worth.
+int resident(int threads) { return threads < 512 ? 512 / threads : 1; }
 
 template <typename TA, typename TR, int NV, int MAXT, bool WARP, bool VEC>
-cudaError_t run(const NormArgs &a, bool backward, cudaStream_t s) {
-    const int threads = row_threads(a.dim);
-    if (backward) {
-        auto kern = block_norm_bwd_kernel<TA, TR, NV, MAXT, WARP, VEC>;
-        const int smem = stage_bytes<TA, TR, NV, VEC>(MAXT) > 0 ? stage_bytes<TA, TR, NV, VEC>(threads) : 0;
-        if (smem > 0) {
-            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-            if (e != cudaSuccess) return e;
-        }
-        kern<<<bwd_ctas(a.rows, a.dim), threads, smem, s>>>(a);
-    } else {
-        const long long cap = (long long)sm_count() * (threads < 1024 ? 1024 / threads : 1);
-        const long long want = WARP ? (a.rows + kWarpRows - 1) / kWarpRows : a.rows;
-        block_norm_kernel<TA, TR, NV, MAXT, WARP, VEC><<<(unsigned)(want < cap ? want : cap), threads, 0, s>>>(a);
-    }
+cudaError_t run_fwd(const NormArgs &a, cudaStream_t s) {
+    const int threads = row_threads(a.dim, 8 * NV);
+    const long long cap = (long long)sm_count() * (threads < 1024 ? 1024 / threads : 1);
+    const long long want = row_ctas(a.rows, a.dim);
+    block_norm_kernel<TA, TR, NV, MAXT, WARP, VEC><<<(unsigned)(want < cap ? want : cap), threads, 0, s>>>(a);
     return cudaGetLastError();
 }
 
-template <typename TA, typename TR, bool VEC> cudaError_t run_dim(const NormArgs &a, bool backward, cudaStream_t s) {
-    if (a.dim <= 256) return run<TA, TR, 1, 32 * kWarpRows, true, VEC>(a, backward, s);
-    if (warp_rows(a.dim)) return run<TA, TR, 2, 32 * kWarpRows, true, VEC>(a, backward, s);
-    if (a.dim <= 4096) return run<TA, TR, 2, 256, false, VEC>(a, backward, s);
-    if (a.dim <= 8192) return run<TA, TR, 2, 512, false, VEC>(a, backward, s);
-    return run<TA, TR, 2, 1024, false, VEC>(a, backward, s);
+template <typename TA, typename TR, int NV, int MAXT, bool WARP, bool VEC>
+cudaError_t run_bwd(const NormArgs &a, cudaStream_t s, int &ctas) {
+    const int threads = row_threads(a.dim, 8 * NV);
+    auto kern = block_norm_bwd_kernel<TA, TR, NV, MAXT, WARP, VEC>;
+    const int smem = stage_bytes<TA, TR, NV, VEC>(MAXT) > 0 ? stage_bytes<TA, TR, NV, VEC>(threads) : 0;
+    int per_sm = resident(threads);
+    if (smem > 0) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        const int fit = 228 * 1024 / (smem + 1280);    // (1,024 bytes that the system keeps, 256 of sums)
+        per_sm = per_sm < fit ? per_sm : fit < 1 ? 1 : fit;
+    }
+    // no more than run at once: a CTA's parts of the weight gradients are written once
+    const long long want = row_ctas(a.rows, a.dim), cap = (long long)sm_count() * per_sm;
+    ctas = (int)(want < cap ? want : cap);
+    kern<<<ctas, threads, smem, s>>>(a);
+    return cudaGetLastError();
 }
 
-template <bool VEC> cudaError_t run_types(const NormArgs &a, bool backward, cudaStream_t s) {
-    if (!a.act_bf16) return run_dim<float, float, VEC>(a, backward, s);
-    if (a.res_bf16) return run_dim<__nv_bfloat16, __nv_bfloat16, VEC>(a, backward, s);
-    return run_dim<__nv_bfloat16, float, VEC>(a, backward, s);
+// Threads and elements of a thread by row width (times of 2^25 elements, forward, fp32 unless stated).
+// 16 elements: half as many sums over warps (bf16, 4,096 wide: 60 us, with 8 63 us).  With fp32
+// operands the next row's loads then spill, and 8 elements are faster: 4,096 wide 127 us, with 16
+// 149; 5,120 wide 118, with 16 198 (bf16: 110 and 84).  Rows of single elements keep 16 up to 4,096
+// (2,500 wide 133 us, with 8 249).
+template <typename TA, typename TR, bool VEC> cudaError_t fwd_dim(const NormArgs &a, cudaStream_t s) {
+    constexpr bool kFew = sizeof(TA) == 4;
+    if (a.dim <= 256) return run_fwd<TA, TR, 1, 32 * kWarpRows, true, VEC>(a, s);
+    if (warp_rows(a.dim)) return run_fwd<TA, TR, 2, 32 * kWarpRows, true, VEC>(a, s);
+    if constexpr (kFew && VEC) {
+        if (a.dim <= 2048) return run_fwd<TA, TR, 1, 256, false, VEC>(a, s);
+        if (a.dim <= 4096) return run_fwd<TA, TR, 1, 512, false, VEC>(a, s);
+    }
+    if (a.dim <= 4096) return run_fwd<TA, TR, 2, 256, false, VEC>(a, s);
+    if constexpr (kFew) {
+        if (a.dim <= 5120) return run_fwd<TA, TR, 1, 640, false, VEC>(a, s);
+        if (a.dim <= 8192) return run_fwd<TA, TR, 1, 1024, false, VEC>(a, s);
+    } else {
+        if (a.dim <= 8192) return run_fwd<TA, TR, 2, 512, false, VEC>(a, s);
+    }
+    return run_fwd<TA, TR, 2, 1024, false, VEC>(a, s);
+}
+// Backward: 16 elements but for rows of 4,097 to 5,120 (8 and 640 threads: 134 us in bf16, with 16
+// and 320, 148; at 8,192 wide 138 and 126).
+template <typename TA, typename TR, bool VEC> cudaError_t bwd_dim(const NormArgs &a, cudaStream_t s, int &ctas) {
+    if (a.dim <= 256) return run_bwd<TA, TR, 1, 32 * kWarpRows, true, VEC>(a, s, ctas);
+    if (warp_rows(a.dim)) return run_bwd<TA, TR, 2, 32 * kWarpRows, true, VEC>(a, s, ctas);
+    if constexpr (sizeof(TA) == 4 && VEC) {
+        if (a.dim > 2048 && a.dim <= 4096) return run_bwd<TA, TR, 1, 512, false, VEC>(a, s, ctas);
+    }
+    if (a.dim <= 4096) return run_bwd<TA, TR, 2, 256, false, VEC>(a, s, ctas);
+    if (a.dim <= 5120) return run_bwd<TA, TR, 1, 640, false, VEC>(a, s, ctas);
+    if (a.dim <= 8192) return run_bwd<TA, TR, 2, 512, false, VEC>(a, s, ctas);
+    return run_bwd<TA, TR, 2, 1024, false, VEC>(a, s, ctas);
+}
+template <bool VEC> cudaError_t fwd_types(const NormArgs &a, cudaStream_t s) {
+    if (!a.act_bf16) return fwd_dim<float, float, VEC>(a, s);
+    if (a.res_bf16) return fwd_dim<__nv_bfloat16, __nv_bfloat16, VEC>(a, s);
+    return fwd_dim<__nv_bfloat16, float, VEC>(a, s);
+}
+template <bool VEC> cudaError_t bwd_types(const NormArgs &a, cudaStream_t s, int &ctas) {
+    if (!a.act_bf16) return bwd_dim<float, float, VEC>(a, s, ctas);
+    if (a.res_bf16) return bwd_dim<__nv_bfloat16, __nv_bfloat16, VEC>(a, s, ctas);
+    return bwd_dim<__nv_bfloat16, float, VEC>(a, s, ctas);
 }
 
 }  // namespace
 
 size_t norm_bwd_ws_bytes(long long rows, int dim) {
-    return (size_t)bwd_ctas(rows, dim) * (warp_rows(dim) ? kWarpRows : 1) * 2 * dim * 4;
+    // the most CTAs of any type: those of 16 elements a thread
+    const long long want = row_ctas(rows, dim), cap = (long long)sm_count() * resident(row_threads(dim, 16));
+    return (size_t)(want < cap ? want : cap) * (warp_rows(dim) ? kWarpRows : 1) * 2 * dim * 4;
 }
 
 cudaError_t launch_block_norm(const NormArgs &a, cudaStream_t s) {
-    return a.vec ? run_types<true>(a, false, s) : run_types<false>(a, false, s);
+    return a.vec ? fwd_types<true>(a, s) : fwd_types<false>(a, s);
 }
 
 cudaError_t launch_block_norm_backward(const NormArgs &a, cudaStream_t s) {
+    int ctas = 0;
     if (a.rows > 0) {
-        const cudaError_t e = a.vec ? run_types<true>(a, true, s) : run_types<false>(a, true, s);
+        const cudaError_t e = a.vec ? bwd_types<true>(a, s, ctas) : bwd_types<false>(a, s, ctas);
         if (e != cudaSuccess) return e;
     }
     if (!a.dw_post && !a.dw_pre) return cudaSuccess;
-    const int parts = a.rows > 0 ? bwd_ctas(a.rows, a.dim) * (warp_rows(a.dim) ? kWarpRows : 1) : 0;
+    const int parts = ctas * (warp_rows(a.dim) ? kWarpRows : 1);
     return launch_early(norm_weight_grad_kernel, dim3((a.dim + 31) / 32, 2), 1024, 0, s, (const float *)a.ws, parts, a.dim,
                         a.dw_post, a.dw_pre);
 }

@@ -158,27 +158,44 @@ __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
     return r;
 }
 
-// Sigmoid and SiLU of values that end in the type T: through the approximate exp and quotient
+// 2^x to two units in the last place.  exp(x) through it is off by |x| 2^-24 more.
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Sigmoid and SiLU of values that end in the type T: through the approximate exp and reciprocal
 // (relative error below 2e-6 where the result matters) for 16-bit results, whose half step is
 // 4e-3; through the accurate ones for 32-bit results.
 template <typename T> __device__ __forceinline__ float sigmoid_for(float x) { return sigmoid_f(x); }
 template <> __device__ __forceinline__ float sigmoid_for<__nv_bfloat16>(float x) {
-    return __fdividef(1.0f, 1.0f + __expf(-x));
-}
-// sigmoid(x) and 1 - sigmoid(x), neither by a difference, so that the gradient of a gate that is all
-// but open keeps its digits.  (Below -80 both stop changing: 1e-35 and 1.)
-template <typename T> __device__ __forceinline__ void sigmoid_pair(float x, float &s, float &rest) {
-    const float e = expf(x < -80.f ? 80.f : -x);
-    s = 1.0f / (1.0f + e);
-    rest = e * s;
-}
-template <> __device__ __forceinline__ void sigmoid_pair<__nv_bfloat16>(float x, float &s, float &rest) {
-    const float e = __expf(x < -80.f ? 80.f : -x);
-    s = __fdividef(1.0f, 1.0f + e);
-    rest = e * s;
+    return rcp_fast(1.0f + exp2_fast(-kLog2e * x));
 }
 template <typename T> __device__ __forceinline__ float silu_for(float x) { return silu_f(x); }
-template <> __device__ __forceinline__ float silu_for<__nv_bfloat16>(float x) { return silu_fast(x); }
+template <> __device__ __forceinline__ float silu_for<__nv_bfloat16>(float x) { return x * sigmoid_for<__nv_bfloat16>(x); }
+// e = exp(-x), for sigmoid(x) = 1 / (1 + e) and 1 - sigmoid(x) = e / (1 + e) without the difference,
+// so that the gradient of a gate that is all but open keeps its digits.  (Below -80 they stop
+// changing: a sigmoid of 1e-35.  NaN stays NaN.)
+template <typename T> __device__ __forceinline__ float exp_neg(float x) { return expf(x < -80.f ? 80.f : -x); }
+template <> __device__ __forceinline__ float exp_neg<__nv_bfloat16>(float x) {
+    float t;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(t) : "f"(-kLog2e * x), "f"(115.4f));
+    return exp2_fast(t);
+}
+template <typename T> __device__ __forceinline__ float one_over(float x) { return 1.0f / x; }
+template <> __device__ __forceinline__ float one_over<__nv_bfloat16>(float x) { return rcp_fast(x); }
+template <typename T> __device__ __forceinline__ void sigmoid_pair(float x, float &s, float &rest) {
+    const float e = exp_neg<T>(x);
+    s = one_over<T>(1.0f + e);
+    rest = e * s;
+}
 
 // Row vectors of four elements.
 __device__ __forceinline__ float4 load4f(const float *p) { return *reinterpret_cast<const float4 *>(p); }

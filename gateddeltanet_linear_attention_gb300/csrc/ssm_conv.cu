@@ -44,8 +44,13 @@ __device__ __forceinline__ int seq_of(const int32_t *cu, int n_seqs, long long t
 // sequence's first token also computes the two tokens behind it (the ones that
 // still reach into the history) wherever they lie, so it alone reads that
 // history and may then overwrite it.  The two tokens' own run leaves them out.
+//
+// Bound by the memory's latency: the tokens in flight are the blocks of an SM times kBatch.  bf16:
+// 8 blocks (8,192 tokens of 8,192 channels: 51 us, 5.25 TB/s; 7 blocks 53 us, 6 blocks 55 us, 10
+// blocks of fewer registers 56 us); fp32, whose loads need more registers, 6 (17.3 us a ragged batch
+// of 46 MB; 7 blocks 18.4, 8 blocks 19.4).  Runs of 32 tokens: 51 us and 20.6 us.
 template <typename TA>
-__global__ void __launch_bounds__(kConvThreads, 7) ssm_conv_kernel(SsmConvArgs a) {
+__global__ void __launch_bounds__(kConvThreads, sizeof(TA) == 2 ? 8 : 6) ssm_conv_kernel(SsmConvArgs a) {
     using Raw = decltype(load_raw((const TA *)nullptr));
     const SsmDims &d = a.d;
     const int c0 = (blockIdx.y * kConvThreads + threadIdx.x) * kVec;
@@ -54,17 +59,21 @@ __global__ void __launch_bounds__(kConvThreads, 7) ssm_conv_kernel(SsmConvArgs a
     TA *__restrict__ out = (TA *)a.out + c0;
     TA *hist = (TA *)a.conv_state;
     const long long r0 = (long long)blockIdx.x * kRun, r1 = r0 + kRun < a.T ? r0 + kRun : a.T;
-    float w[4][kVec], bias[kVec];
+    f32x2 w[4][2], bias[2] = {0ull, 0ull};             // of pairs of channels
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-        float u[4];
-        load4((const TA *)a.w + (long long)(c0 + i) * 4, u);
+    for (int i = 0; i < 2; ++i) {
+        float u[4], v[4];
+        load4((const TA *)a.w + (long long)(c0 + 2 * i) * 4, u);
+        load4((const TA *)a.w + (long long)(c0 + 2 * i + 1) * 4, v);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[j][i] = u[j];
+        for (int j = 0; j < 4; ++j) w[j][i] = pack2(u[j], v[j]);
     }
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) bias[i] = 0.f;
-    if (a.bias) load4((const TA *)a.bias + c0, bias);
+    if (a.bias) {
+        float u[4];
+        load4((const TA *)a.bias + c0, u);
+        bias[0] = pack2(u[0], u[1]);
+        bias[1] = pack2(u[2], u[3]);
+    }
 
     // first sequence that has a token at r0 or later
     int n = seq_of(a.cu, a.n_seqs, r0);
@@ -126,16 +135,23 @@ __global__ void __launch_bounds__(kConvThreads, 7) ssm_conv_kernel(SsmConvArgs a
 #pragma unroll
             for (int j = 0; j < 3; ++j) load4(x + (t - 3 + j) * a.ld_x, win[j]);
         }
+        f32x2 past[3][2];                              // the window in pairs of channels
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) past[j][i] = pack2(win[j][2 * i], win[j][2 * i + 1]);
         auto emit = [&](const float (&cur)[kVec], long long at) {
             float o[kVec];
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) {
-                o[i] = silu_for<TA>(fmaf(w[3][i], cur[i],
-                                         fmaf(w[2][i], win[2][i],
-                                              fmaf(w[1][i], win[1][i], fmaf(w[0][i], win[0][i], bias[i])))));
-                win[0][i] = win[1][i];
-                win[1][i] = win[2][i];
-                win[2][i] = cur[i];
+            for (int i = 0; i < 2; ++i) {
+                const f32x2 x = pack2(cur[2 * i], cur[2 * i + 1]);
+                const float2 v = unpack2(
+                    fma2(w[3][i], x, fma2(w[2][i], past[2][i], fma2(w[1][i], past[1][i], fma2(w[0][i], past[0][i], bias[i])))));
+                o[2 * i] = silu_for<TA>(v.x);
+                o[2 * i + 1] = silu_for<TA>(v.y);
+                past[0][i] = past[1][i];
+                past[1][i] = past[2][i];
+                past[2][i] = x;
             }
             store4(out + at * d.ch, o);
         };

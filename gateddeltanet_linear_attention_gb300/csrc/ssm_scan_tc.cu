@@ -51,7 +51,6 @@ constexpr int kTile = kL * 128 * 2;            // bytes of a ring slot
 constexpr int kHalfTile = kTile / 2;           // 128 rows x 128 bytes: one TMA box
 constexpr int kXwPart = 16 * 128 * 2;          // one bf16 part of w X for 16 tokens (MN-major)
 constexpr int kXwBuf = 3 * kXwPart;
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMinLog = -60.0f;
 
 // TMEM columns
@@ -126,13 +125,6 @@ __device__ __forceinline__ void tmem_ld16x2(uint32_t t0, uint32_t t1, float (&a)
         : "r"(t0), "r"(t1) : "memory");
 #pragma unroll
     for (int i = 0; i < 16; ++i) { a[i] = __uint_as_float(r[i]); b[i] = __uint_as_float(r[16 + i]); }
-}
-// 2^x to two units in the last place.  exp(x) through it is off by |x| 2^-24 more: for the weights
-// of a state that is at most 2^-25 of the largest one, |x| exp(x) being below 0.37.
-__device__ __forceinline__ float exp2_fast(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
 }
 // A bounded wait.  Waiting warps share the issue slots and the instruction cache with the working
 // ones, so all but the first poll is out of line, a few instructions long, and the wall clock is
@@ -257,11 +249,6 @@ __device__ __forceinline__ void load_32b(const uint4 *p, bool wide, uint32_t (&v
         const uint4 a = p[0], b = p[1];
         v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
     }
-}
-__device__ __forceinline__ float rcp_fast(float x) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
 }
 // v SiLU(z): approximate exp and reciprocal, two values at a time.
 __device__ __forceinline__ f32x2 gate2(f32x2 v, f32x2 z) {
