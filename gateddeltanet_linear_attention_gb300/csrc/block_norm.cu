@@ -9,7 +9,10 @@
 // and the row lives in registers between its two sums.  HBM-bound.  A row
 // belongs to a warp (short rows) or to a CTA; CTAs walk the rows in a grid
 // stride, which keeps the weights in registers and lets the loads of the next
-// row be issued before the sums of this one.
+// row be issued before the sums of this one.  8,192 x 4,096 bf16 with a gate per
+// channel: 59.5 us, 5.6 TB/s, 0.83 of a plain copy's rate.  Rows of single elements
+// (odd widths, views off 16 bytes) are bound by their load and store instructions:
+// 2^25 elements at 1,001 wide take 152 us, 2.2 TB/s.
 #include "ssm_common.cuh"
 
 namespace gdn {
@@ -273,6 +276,11 @@ template <typename TA, typename TR, int NV, bool VEC> constexpr int stage_bytes(
 //   dw1   = sum over rows of dn p^,  dw2 = sum over rows of dh r^
 // The weight gradients are summed in registers over a CTA's rows, then over the
 // CTAs by norm_weight_grad_kernel, always in the same order.
+// 8,192 x 4,096 bf16 with a gate per channel: 117 us with the sum over CTAs (7 us alone), 4.6 TB/s.
+// Half of the issue slots are used (61 instructions an element in packed arithmetic, 96 without:
+// 132 us); 512 threads of 122 registers fill an SM, and two rows' chains of sums are too few to hide
+// each other's barriers.  All sums of a row behind one barrier, with more arithmetic: 134 us.
+// Rows wider than 8,192 spill (64 registers): 12,288 wide 325 us for 2^25 elements.
 template <typename TA, typename TR, int NV, int MAXT, bool WARP, bool VEC>
 __global__ void __launch_bounds__(MAXT, sm_blocks(MAXT)) block_norm_bwd_kernel(NormArgs a) {
     __shared__ float buf[2][32];
@@ -497,7 +505,8 @@ __global__ void __launch_bounds__(MAXT, sm_blocks(MAXT)) block_norm_bwd_kernel(N
 }
 
 // dw[c] = sum over the parts, 32 columns of one weight per CTA: 32 threads down
-// the parts for each column, then a sum over those 32.
+// the parts for each column, then a sum over those 32.  10 MB of parts (304 of 4,096
+// columns): 7 us alone, bound by latency, launched while the parts are still written.
 __global__ void __launch_bounds__(1024) norm_weight_grad_kernel(const float *ws, int parts, int dim,
                                                                 float *dw_post, float *dw_pre) {
     __shared__ float s[32][33];

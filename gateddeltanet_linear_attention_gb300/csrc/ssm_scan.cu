@@ -83,7 +83,8 @@ __global__ void __launch_bounds__(1024) ssm_segment_map_kernel(SsmScanArgs a) {
 // enter[0] = the initial state, enter[k+1] = exp(log-decay of segment k) *
 // enter[k] + (what pass 1 left in enter[k+1]); one thread per float4 of a head.
 // The loads of kAhead segments are in flight at once: only the multiply-adds
-// form a chain.
+// form a chain.  Bound by latency: 32 heads of 128 x 128 in 4 segments 8 us alone,
+// 17 MB from L2, most of it behind the pass in front of it.
 __global__ void __launch_bounds__(256) ssm_chain_states_kernel(SsmScanArgs a) {
     constexpr int kAhead = 8;
     let_next_start();
@@ -94,22 +95,29 @@ __global__ void __launch_bounds__(256) ssm_chain_states_kernel(SsmScanArgs a) {
     SsmCut mine{0, 0, -1};
     if (small) mine = ssm_warp_cut(a, lane);
     await_previous();
+    // The sequences of two segments or more in turn: of a small batch all at once in the lanes, every
+    // gridDim.z-th of them this CTA's; of a larger one 32 of this CTA's own at a time.
     unsigned cut = __ballot_sync(0xffffffffu, small && mine.segs > 1);
-    for (int n = blockIdx.z, turn = 0;; n += gridDim.z) {
-        int e0, segs;
-        if (small) {                                   // the sequences of two segments or more in turn
-            if (cut == 0) break;
-            n = __ffs(cut) - 1;
-            cut &= cut - 1;
-            if (turn++ % gridDim.z != blockIdx.z) continue;
-            e0 = __shfl_sync(0xffffffffu, mine.entry0, n);
-            segs = __shfl_sync(0xffffffffu, mine.segs, n);
-        } else {
-            if (n >= a.n_seqs) break;
-            e0 = a.enter_base[n];
-            segs = a.seg_base[n + 1] - a.seg_base[n];
+    const int stride = gridDim.z;
+    int next = small ? a.n_seqs : blockIdx.z, first = 0, turn = 0;
+    for (;;) {
+        if (cut == 0) {
+            if (next >= a.n_seqs) break;
+            first = next;
+            const int n = first + lane * stride;
+            if (n < a.n_seqs) {
+                mine.entry0 = a.enter_base[n];
+                mine.segs = a.seg_base[n + 1] - a.seg_base[n];
+            }
+            cut = __ballot_sync(0xffffffffu, n < a.n_seqs && mine.segs > 1);
+            next = a.n_seqs - first > 32 * stride ? first + 32 * stride : a.n_seqs;
+            continue;
         }
-        if (segs < 2 || e0 + segs > a.max_enter) continue;     // (too many: malformed, reported)
+        const int k = __ffs(cut) - 1, n = small ? k : first + k * stride;
+        cut &= cut - 1;
+        if (small && turn++ % gridDim.z != blockIdx.z) continue;
+        const int e0 = __shfl_sync(0xffffffffu, mine.entry0, k), segs = __shfl_sync(0xffffffffu, mine.segs, k);
+        if (e0 + segs > a.max_enter) continue;                 // (too many: malformed, reported)
         const int slot = slot_of(a.state_idx, n, a.d.n_slots, a.err);
         if (slot < 0 || i >= vec) continue;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -142,7 +150,10 @@ __global__ void __launch_bounds__(256) ssm_chain_states_kernel(SsmScanArgs a) {
 // of n so that one packed multiply-add serves two state elements.  Tokens come
 // in blocks of TB through shared memory, the next block's loads in flight
 // while this one is computed; the row slices' parts of y are summed per block.
-// FP32-bound: 3 packed operations per two state elements and token.
+// Bound by the fp32 units, 3 packed operations per two state elements and token, where the batch
+// fills the GPU (256 sequences of 512 tokens, 8 heads of 64 x 64: 788 us, 44 % of their rate; 8,192
+// tokens of 32 heads, 128 x 128, cut: 1,365 us), and by a token's latency, 225 ns, where it does not
+// (7 sequences of up to 256 tokens: 59 us).
 // STATES: pass 1, no outputs: the leaving state from zero and the log-decay.
 // WIDE: 4 to 16 rows a thread, as many threads as 256 allow, for batches that do not fill the GPU.
 template <int N, int P, bool WIDE> struct ScanShape {
@@ -340,13 +351,20 @@ __global__ void __launch_bounds__(ScanShape<N, P, WIDE>::NT) ssm_scan_kernel(Ssm
 // ---------------------------------------------------------------- launching
 namespace {
 
-bool on_tensor_cores(const SsmDims &d, bool act_bf16) { return act_bf16 && ssm_tc_supported(d); }
+bool has_tensor_form(const SsmDims &d, bool act_bf16) { return act_bf16 && ssm_tc_supported(d); }
+// The tensor-core form, but for batches of a few tokens a sequence, which leave its chunks of 128
+// all but empty (32 heads of 128 x 64, 200 sequences of 8 tokens: 148 us in the form of single
+// tokens, 305 us here, of 1 token 80 and 304; a sequence of 16 tokens 5.9 and 10.4 us, of 64 tokens
+// 16.3 and 10.0, of 256 tokens 58 and 14; 8,192 tokens of 32 heads 128 x 128: 1,470 and 114).
+bool on_tensor_cores(const SsmDims &d, bool act_bf16, long long T, long long n_seqs) {
+    return has_tensor_form(d, act_bf16) && T > 32 && T > 8 * n_seqs;
+}
 
 // Segments that run side by side when one sequence has the GPU to itself: the resident CTAs over
 // those of one segment (heads, or units of the tensor-core form, one CTA per SM there).
-int segments_wanted(const SsmDims &d, bool act_bf16) {
+int segments_wanted(const SsmDims &d, bool tensor) {
     int want;
-    if (on_tensor_cores(d, act_bf16)) {
+    if (tensor) {
         want = sm_count() / ssm_tc_units(d);
     } else {
         const int per_sm = d.N * d.P >= 16384 ? 2 : d.N * d.P >= 8192 ? 4 : 8;
@@ -356,9 +374,11 @@ int segments_wanted(const SsmDims &d, bool act_bf16) {
 }
 
 // Tokens of a segment: whole chunks of 128, 256 or more.  A batch whose sequences fill the GPU by
-// themselves is then not cut: none of them is longer than its share of T.
-long long segment_len(const SsmDims &d, bool act_bf16, long long T) {
-    const int want = segments_wanted(d, act_bf16);
+// themselves is then not cut: none of them is longer than its share of T.  (8,192 tokens of 32
+// heads, 128 x 128: 114 us in 4 segments, 274 in one; fp32, 4,096 tokens of 8 heads, 64 x 64: 141
+// and 883.  Four sequences of 2,048 tokens, which lose by it: 88 us and 81.)
+long long segment_len(const SsmDims &d, bool tensor, long long T) {
+    const int want = segments_wanted(d, tensor);
     const long long len = ((T + want - 1) / want + 127) / 128 * 128;
     return len < 256 ? 256 : len;
 }
@@ -423,12 +443,13 @@ template <typename TA> cudaError_t run_scan_np(const SsmScanArgs &a, bool states
 
 // Grows with T: segments are 256 tokens or longer, and a batch has no more than are wanted.
 size_t ssm_scan_ws_bytes(const SsmDims &d, bool act_bf16, long long T, long long n_seqs) {
-    const long long most = segments_wanted(d, act_bf16);
+    long long most = segments_wanted(d, false);        // of either form: a smaller batch may take the other
+    if (has_tensor_form(d, act_bf16) && segments_wanted(d, true) > most) most = segments_wanted(d, true);
     return most < 2 ? 0 : scan_ws(d, 2 * (T / 256 < most ? T / 256 : most), n_seqs).size;
 }
 
 size_t ssm_scan_carve(SsmScanArgs &a, bool act_bf16, void *ws) {
-    a.seg_len = segment_len(a.d, act_bf16, a.T);
+    a.seg_len = segment_len(a.d, on_tensor_cores(a.d, act_bf16, a.T, a.n_seqs), a.T);
     a.max_enter = (int)max_entries(a.T, a.seg_len);
     const ScanWs w = scan_ws(a.d, a.max_enter, a.n_seqs);
     char *p = (char *)ws;
@@ -446,7 +467,7 @@ cudaError_t launch_ssm_scan(const SsmScanArgs &a, bool act_bf16, cudaStream_t s)
     const unsigned all = cut ? (unsigned)(a.n_seqs + a.max_enter / 2) : (unsigned)a.n_seqs;
     auto pass = [&](bool states) {
         const unsigned segments = states ? (unsigned)(a.max_enter / 2) : all;
-        if (on_tensor_cores(a.d, act_bf16)) return launch_ssm_scan_tc(a, states, segments, s);
+        if (on_tensor_cores(a.d, act_bf16, a.T, a.n_seqs)) return launch_ssm_scan_tc(a, states, segments, s);
         return act_bf16 ? run_scan_np<__nv_bfloat16>(a, states, segments, s) : run_scan_np<float>(a, states, segments, s);
     };
     if (cut) {

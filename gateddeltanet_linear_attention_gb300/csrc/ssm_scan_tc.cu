@@ -24,14 +24,21 @@
 // clamped at -60 a token: exp(-60) is nothing beside what the token adds, and
 // differences of running sums keep their meaning.
 //
-// Roles (30 or 32 warps, one CTA per SM): warp 0 loads tiles by TMA, warp 1
-// issues G, Y2 and P X, warp 3 dS, warp 2 stores y by TMA; E (a warp per head
-// and chunk parity): the log-decays' sums and their exponentials, up to two
-// chunks ahead; A: G -> P; B: the state; C (two groups of 64 columns): Y2's scaling, the skip, the gate, y;
-// D (two groups, 16 tokens each in turn): the parts of w X.
+// Roles (30 or 32 warps, one CTA per SM): warp 0 loads the tiles of C, B and x by TMA (one slot of
+// shared memory, two and two) and has z brought into L2; warp 1 issues G, Y2 and P X, warp 3 dS;
+// warp 2 stores y, which takes the place of x in its tile, by TMA; E (a warp per head and chunk
+// parity): the log-decays' sums and their exponentials, up to two chunks ahead, and the search for
+// values of x that are not finite; A: G -> P, which takes the place of G in TMEM; B: Y2's scaling,
+// then the state; C (two groups of 64 columns): the skip, the gate, y; D (two groups, 16 tokens each
+// in turn; four where no outputs are computed): the parts of w X.
 //
-// Bound by instruction issue (conversions between TMEM, registers and shared
-// memory), not by memory or the tensor cores.
+// Bound by the chain of a chunk's steps from Y2 through its scaling and P X to the output's warps,
+// about 8,000 cycles, and by the latency of each role's steps between TMEM, registers and shared
+// memory (half of the issue slots are used, the tensor cores for a third of the time), not by memory.
+// 8,192 tokens of 32 heads, 128 x 128 states, in 4 segments: the states' pass 36 us, the chain of
+// states 8 us, the pass with outputs 82 us, 118 us together with early launches, 2.3 TB/s of what has
+// to be moved; 16 prompts of 256 to 4,096 tokens, 64 heads of 128 x 64: 384 us, 3.4 TB/s; 65,536
+// tokens of 8 heads, 64 x 64: 93 us.  The form of single tokens takes 1,470 us for the first of these.
 #include <cuda.h>   // CUtensorMap (the encoder itself is reached through the runtime)
 
 #include <climits>

@@ -624,3 +624,24 @@ def test_binding_refuses_tensors_that_do_not_fit():
             b.launch(**bad)
     b.ws = b.ws[:0]
     b.launch(**good)                               # (not cut: no workspace is needed)
+
+
+@pytest.mark.parametrize("act,long", [("fp32", 600), ("bf16", 600), ("bf16", 9000)])
+def test_more_sequences_than_a_block_lays_out(act, long):
+    """More than 1,024 of them, few tokens each but for some that are cut: in order, none left out."""
+    lens = [1, 0, 2, 1] * 330
+    for n in (3, 700, 1023, 1100, 1318):
+        lens[n] = 300
+    lens[1024] = long
+    b = Batch(lens, H=2, G=1, N=64, P=64, act=act, seed=23)
+    picked = [0, 1, 2, 3, 4, 699, 700, 701, 1022, 1023, 1024, 1025, 1100, 1317, 1318, 1319]
+    y, out = b.run()
+    b.verify(y, out, seqs=picked + list(range(30, 1000, 61)))
+    assert y.isfinite().all() and not (y == 7).all(1).any()
+    assert gdn.gdn_device_error() == 0
+
+
+@pytest.mark.parametrize("lens", [[8] * 40, [33], [32], [9] * 40, [1] * 64])
+def test_short_sequences_of_either_form(lens):
+    b = Batch(lens, H=4, G=2, N=128, P=64, act="bf16", seed=24)
+    b.verify(*b.run())
