@@ -272,3 +272,36 @@ def test_binding_refuses_tensors_that_do_not_fit():
                 dict(residual=d["residual"][0]), dict(block=None), dict(w_pre=None)):
         with pytest.raises((ValueError, RuntimeError)):
             call(**bad)
+
+
+def test_gradients_in_a_graph_and_on_another_stream():
+    d = make(900, 1300, BF, BF)
+    want = backward(d, BF, BF)
+    f = ref.norm(d["block"], d["gate"], d["residual"], d["w_post"], d["w_pre"], 1e-5, 0.0, 0.7)
+    t = {k: up(v) for k, v in d.items()}
+    u, k1, k2 = f["res_out"][0].to(BF).cuda(), f["rstd_post"][0].float().cuda(), f["rstd_pre"][0].float().cuda()
+    got = {k: torch.full_like(v, 7.0) for k, v in want.items()}
+    ws = torch.empty(gdn.gdn_block_norm_workspace_size(900, 1300), dtype=torch.uint8, device="cuda")
+    s, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=s):
+        gdn.gdn_block_norm_backward(u, k2, t["w_pre"], t["dh"], t["d_res_out"], block=t["block"], rstd_post=k1, w_post=t["w_post"],
+                                    gate=t["gate"], res_scale=0.7, workspace=ws, stream=s, **got)
+    with torch.cuda.stream(s):
+        graph.replay()
+    s.synchronize()
+    assert all(torch.equal(got[k], want[k]) for k in want)
+
+
+@pytest.mark.parametrize("one", ["dw_post", "dw_pre", "d_block", "d_gate", "d_residual"])
+def test_one_gradient_alone(one):
+    d = make(300, 200, BF, F32)
+    want = backward(d, BF, F32)
+    f = ref.norm(d["block"], d["gate"], d["residual"], d["w_post"], d["w_pre"], 1e-5, 0.0, 0.7)
+    t = {k: up(v) for k, v in d.items()}
+    got = torch.full_like(want[one], 7.0)
+    ws = torch.empty(gdn.gdn_block_norm_workspace_size(300, 200), dtype=torch.uint8, device="cuda") if one[:2] == "dw" else None
+    gdn.gdn_block_norm_backward(f["res_out"][0].float().cuda(), f["rstd_pre"][0].float().cuda(), t["w_pre"], t["dh"], t["d_res_out"],
+                                block=t["block"], rstd_post=f["rstd_post"][0].float().cuda(), w_post=t["w_post"], gate=t["gate"],
+                                res_scale=0.7, workspace=ws, **{one: got})
+    assert torch.equal(got, want[one])

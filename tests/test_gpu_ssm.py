@@ -645,3 +645,40 @@ def test_more_sequences_than_a_block_lays_out(act, long):
 def test_short_sequences_of_either_form(lens):
     b = Batch(lens, H=4, G=2, N=128, P=64, act="bf16", seed=24)
     b.verify(*b.run())
+
+
+@pytest.mark.parametrize("act", ["fp32", "bf16"])
+def test_outputs_and_states_on_16_bytes(act):
+    b = Batch([300, 40], H=2, G=1, act=act, seed=25).upload()
+    step = 16 // torch.empty(0, dtype=b.act).element_size()
+    y = torch.full((b.T * 128 + 2 * step,), 7.0, dtype=b.act, device="cuda")
+    out = torch.full((b.d_state.numel() + 8,), 7.0, device="cuda")
+    b.launch(y[step:-step].view(b.T, 128), out[4:-4].view_as(b.d_state))
+    b.verify(y[step:-step].view(b.T, 128), out[4:-4].view_as(b.d_state))
+    for edge in (y[:step], y[-step:], out[:4], out[-4:]):
+        assert (edge == 7).all()
+
+
+def test_as_many_sequences_as_are_allowed():
+    n, lens = 65535, [1] * 65534 + [900]
+    b = Batch(lens, H=1, G=1, N=16, P=32, act="fp32", seed=26)
+    y, out = b.run()
+    seqs = [0, 1, 31, 32, 1023, 1024, 33333, 65533, 65534]
+    b.verify(y, out, seqs=seqs)
+    assert not (y == 7).all(1).any()
+    # the next token of each
+    g = torch.Generator().manual_seed(27)
+    x, w, u = randn(n, 64, gen=g), randn(64, 4, gen=g), randn(n, 1, gen=g)
+    hist, state, ys = torch.zeros(n, 64, 3, device="cuda"), out.clone(), torch.empty(n, 32, device="cuda")
+    ws = torch.empty(gdn.gdn_ssm_workspace_size(b.cfg, n, n), dtype=torch.uint8, device="cuda")
+    gdn.gdn_ssm_decode(b.cfg, x.cuda(), u.cuda(), w.cuda(), hist, b.d_A_log, state, ys, ws)
+    for s in seqs:
+        c, cm, new = ref.conv(x[s:s + 1], w, None, torch.zeros(64, 3))
+        val, mag, S, M = ref.scan(c[:, :32].view(1, 1, 32), c[:, 32:48].view(1, 1, 16), c[:, 48:].view(1, 1, 16), u[s:s + 1], b.A_log, None,
+                                  None, None, out[s].cpu(), 1)
+        # the convolution's 32-bit error enters each factor once: 24 roundings a value, three factors
+        grow = 1 + (cm / c.abs()).max()
+        ref.check(ys[s], val[0, 0], mag[0, 0], 128 * grow * ref.U32, "y")
+        ref.check(state[s], S, M, 128 * grow * ref.U32, "state")
+        assert torch.equal(hist[s].cpu().double(), new)
+    assert gdn.gdn_device_error() == 0
