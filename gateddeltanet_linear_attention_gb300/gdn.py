@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 import threading
 
 from . import build_lib
@@ -396,16 +397,40 @@ def make_ssm_config(groups, heads, d_state, head_dim, act="bf16", n_slots=0, dt_
                      n_slots, dt_min, dt_max)
 
 
+def _packer(cls):
+    """Fill a ctypes structure from its fields' values in order, null pointers as 0: a third of the
+    time that the structure's own constructor takes."""
+    code = {ctypes.c_int32: "i", ctypes.c_int64: "q", ctypes.c_float: "f", ctypes.c_void_p: "P"}
+    pack = struct.Struct("@" + "".join(code[t] for _, t in cls._fields_)).pack
+    tail = bytes(ctypes.sizeof(cls))
+    size, make = len(tail), cls.from_buffer_copy
+
+    def fill(*values):
+        data = pack(*values)
+        return make(data if len(data) == size else data + tail[len(data):])
+    return fill
+
+
+_ssm_io, _norm_io = _packer(SSMIO), _packer(BlockNormIO)
+_torch = None
+
+
 class _Args:
-    """Checks of one call's tensors: all on the current device, of the expected type and shape."""
+    """Checks of one call's tensors: all on the current device, of the expected type and shape.
+    Pointers of missing ones are 0."""
 
     __slots__ = ("where", "device", "f32", "i32", "act")
 
     def __init__(self, where, act=None):
-        import torch
-        self.where, self.device = where, torch.cuda.current_device()
-        self.f32, self.i32 = torch.float32, torch.int32
-        self.act = None if act is None else torch.bfloat16 if act == GDN_BF16 else torch.float32
+        global _torch
+        if _torch is None:
+            import torch
+            torch.cuda.current_device()             # initialises CUDA
+            _torch = torch
+        self.where, self.device = where, _torch._C._cuda_getDevice()
+        self.f32, self.i32 = _torch.float32, _torch.int32
+        if act is not None:
+            self.act = _torch.bfloat16 if act == GDN_BF16 else _torch.float32
 
     def refuse(self, name, what):
         raise ValueError("%s: %s %s" % (self.where, name, what))
@@ -415,14 +440,18 @@ class _Args:
             self.refuse(name, "is %s, not %s" % (t.dtype, dtype))
         if t.get_device() != self.device:
             self.refuse(name, "is on %s, not on the current device cuda:%d" % (t.device, self.device))
-        self.refuse(name, "has shape %s, not %s" % (tuple(t.shape), shape))
+        if t.shape != shape:
+            self.refuse(name, "has shape %s, not %s" % (tuple(t.shape), shape))
+        self.refuse(name, "is not contiguous")
 
     def view(self, t, name, shape, dtype):
         """(pointer, row stride) of a two-dimensional view with contiguous rows."""
         if t is None:
-            return None, 0
+            return 0, 0
         if t.dtype is not dtype or t.shape != shape or t.get_device() != self.device:
             self.explain(t, name, shape, dtype)
+        if t.is_contiguous():
+            return t.data_ptr(), shape[1]
         ld, one = t.stride()
         if one != 1 and shape[1] > 1:
             self.refuse(name, "has rows that are not contiguous")
@@ -435,17 +464,15 @@ class _Args:
     def whole(self, t, name, shape, dtype):
         """Pointer of a contiguous tensor."""
         if t is None:
-            return None
-        if t.dtype is not dtype or t.shape != shape or t.get_device() != self.device:
+            return 0
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != self.device or not t.is_contiguous():
             self.explain(t, name, shape, dtype)
-        if not t.is_contiguous():
-            self.refuse(name, "is not contiguous")
         return t.data_ptr()
 
     def pool(self, t, name, n_slots, shape, dtype):
         """Pointer of a contiguous pool of n_slots slots or more."""
         if t is None:
-            return None
+            return 0
         if t.dim() == 0 or t.shape[0] < n_slots:
             self.refuse(name, "has fewer than the configuration's %d slots" % n_slots)
         return self.whole(t, name, (t.shape[0],) + shape, dtype)
@@ -455,12 +482,11 @@ class _Args:
             return None, 0
         if t.get_device() != self.device or not t.is_contiguous():
             self.refuse("workspace", "is not a contiguous tensor on the current device")
-        return t.data_ptr(), t.numel() * t.element_size()
+        return t.data_ptr(), t.nbytes
 
     def stream(self, stream):
         if stream is None:
-            import torch
-            return torch._C._cuda_getCurrentRawStream(self.device)
+            return _torch._C._cuda_getCurrentRawStream(self.device)
         return getattr(stream, "cuda_stream", stream)
 
 
@@ -494,12 +520,12 @@ def gdn_ssm_prefill(cfg, x, b, c, dt, A_log, cu_seqlens, y, D=None, dt_bias=None
         a.refuse("c", "has another row stride than b")
     pdt, ld_dt = a.view(dt, "dt", (T, H), a.act)
     pz, ld_z = a.view(z, "z", (T, H * P), a.act)
-    io = SSMIO(px, ld_x, pb, pc, ld_bc, pdt, ld_dt, pz, ld_z, a.whole(A_log, "A_log", (H,), a.f32),
-               a.whole(dt_bias, "dt_bias", (H,), a.f32), a.whole(D, "D", (H,), a.f32), None, None,
+    io = _ssm_io(px, ld_x, pb, pc, ld_bc, pdt, ld_dt, pz, ld_z, a.whole(A_log, "A_log", (H,), a.f32),
+               a.whole(dt_bias, "dt_bias", (H,), a.f32), a.whole(D, "D", (H,), a.f32), 0, 0,
                a.whole(cu_seqlens, "cu_seqlens", (n + 1,), a.i32), n, T,
                a.whole(state_idx, "state_idx", (n,), a.i32),
                a.pool(state_in, "state_in", cfg.n_slots, (H, N, P), a.f32),
-               a.pool(state_out, "state_out", cfg.n_slots, (H, N, P), a.f32), None,
+               a.pool(state_out, "state_out", cfg.n_slots, (H, N, P), a.f32), 0,
                a.whole(y, "y", (T, H * P), a.act))
     ws, ws_bytes = a.bytes_of(workspace)
     _check((_lib or load()).gdn_ssm_prefill(ctypes.byref(cfg), ctypes.byref(io), ws, ws_bytes, a.stream(stream)),
@@ -517,10 +543,10 @@ def gdn_ssm_decode(cfg, x, dt, conv_w, conv_state, A_log, state, y, workspace, c
     pdt, ld_dt = a.view(dt, "dt", (n, H), a.act)
     pz, ld_z = a.view(z, "z", (n, H * P), a.act)
     ps = a.pool(state, "state", cfg.n_slots, (H, N, P), a.f32)
-    io = SSMIO(px, ld_x, None, None, 0, pdt, ld_dt, pz, ld_z, a.whole(A_log, "A_log", (H,), a.f32),
+    io = _ssm_io(px, ld_x, 0, 0, 0, pdt, ld_dt, pz, ld_z, a.whole(A_log, "A_log", (H,), a.f32),
                a.whole(dt_bias, "dt_bias", (H,), a.f32), a.whole(D, "D", (H,), a.f32),
                a.whole(conv_w, "conv_w", (CH, 4), a.act), a.whole(conv_bias, "conv_bias", (CH,), a.act),
-               None, n, n, a.whole(state_idx, "state_idx", (n,), a.i32), ps, ps,
+               0, n, n, a.whole(state_idx, "state_idx", (n,), a.i32), ps, ps,
                a.pool(conv_state, "conv_state", cfg.n_slots, (CH, 3), a.act),
                a.whole(y, "y", (n, H * P), a.act))
     ws, ws_bytes = a.bytes_of(workspace)
@@ -543,12 +569,12 @@ def gdn_block_norm(residual, w_pre=None, h=None, block=None, res_out=None, w_pos
         a.refuse("h", "and block are both missing: nothing to do")
     act, res = like.dtype, residual.dtype
     cols = 0 if gate is None else gate.shape[-1]
-    io = BlockNormIO(rows, dim, _dt(like), _dt(residual), eps, weight_offset, res_scale,
+    io = _norm_io(rows, dim, _dt(like), _dt(residual), eps, weight_offset, res_scale,
                      *a.view(block, "block", wide, act), *a.view(gate, "gate", (rows, cols), act), cols,
                      *a.view(residual, "residual", wide, res), a.whole(w_post, "w_post", (dim,), a.f32),
                      a.whole(w_pre, "w_pre", (dim,), a.f32), *a.view(res_out, "res_out", wide, res),
                      *a.view(h, "h", wide, act), a.whole(rstd_post, "rstd_post", (rows,), a.f32),
-                     a.whole(rstd_pre, "rstd_pre", (rows,), a.f32))
+                     a.whole(rstd_pre, "rstd_pre", (rows,), a.f32), 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
     _check((_lib or load()).gdn_block_norm(ctypes.byref(io), a.stream(stream)), "gdn_block_norm")
 
 
@@ -565,10 +591,10 @@ def gdn_block_norm_backward(res_out, rstd_pre=None, w_pre=None, dh=None, d_res_o
         a.refuse("dh", "and block are both missing: nothing to do")
     act, res = like.dtype, res_out.dtype
     cols = 0 if gate is None else gate.shape[-1]
-    io = BlockNormIO(rows, dim, _dt(like), _dt(res_out), 0.0, weight_offset, res_scale,
+    io = _norm_io(rows, dim, _dt(like), _dt(res_out), 0.0, weight_offset, res_scale,
                      *a.view(block, "block", wide, act), *a.view(gate, "gate", (rows, cols), act), cols,
                      *a.view(res_out, "res_out", wide, res), a.whole(w_post, "w_post", (dim,), a.f32),
-                     a.whole(w_pre, "w_pre", (dim,), a.f32), None, 0, None, 0,
+                     a.whole(w_pre, "w_pre", (dim,), a.f32), 0, 0, 0, 0,
                      a.whole(rstd_post, "rstd_post", (rows,), a.f32),
                      a.whole(rstd_pre, "rstd_pre", (rows,), a.f32), *a.view(dh, "dh", wide, act),
                      *a.view(d_res_out, "d_res_out", wide, res),
