@@ -151,17 +151,24 @@ __global__ void __launch_bounds__(256) ssm_chain_states_kernel(SsmScanArgs a) {
 // in blocks of TB through shared memory, the next block's loads in flight
 // while this one is computed; the row slices' parts of y are summed per block.
 // Bound by the fp32 units, 3 packed operations per two state elements and token, where the batch
-// fills the GPU (256 sequences of 512 tokens, 8 heads of 64 x 64: 788 us, 44 % of their rate; 8,192
-// tokens of 32 heads, 128 x 128, cut: 1,365 us), and by a token's latency, 225 ns, where it does not
-// (7 sequences of up to 256 tokens: 59 us).
+// fills the GPU (256 sequences of 512 tokens, 8 heads of 64 x 64: 784 us, 44 % of their rate; 8,192
+// tokens of 32 heads, 128 x 128, cut: 1,223 us), and by a token's latency, 225 ns, where it does not
+// (7 sequences of up to 256 tokens: 57 us).
 // STATES: pass 1, no outputs: the leaving state from zero and the log-decay.
 // WIDE: 4 to 16 rows a thread, as many threads as 256 allow, for batches that do not fill the GPU.
-template <int N, int P, bool WIDE> struct ScanShape {
-    static constexpr int MOST = WIDE ? N * P / 1024 : N * P / 128;
+// ALONE: the same with 128 registers a thread, for batches of up to two CTAs or so an SM, where loads
+// further ahead are worth more than a third CTA.
+enum { WHOLE, WIDE, ALONE };
+template <int N, int P, int SHAPE> struct ScanShape {
+    static constexpr int MOST = SHAPE != WHOLE ? N * P / 1024 : N * P / 128;
     static constexpr int NPT = MOST >= 16 ? 16 : MOST < 4 ? 4 : MOST;  // rows of a thread
     static constexpr int LP = P / 4;                                   // threads across the columns
     static constexpr int NS = N / NPT;                                 // row slices
     static constexpr int NT = LP * NS;
+    // CTAs that an SM's registers are to hold (0: as many as it comes to).  128 x 128 states whole: two,
+    // 100 sequences of 512 tokens, 16 heads, 1,951 us, and 2,217 with the one that it came to; smaller
+    // ones spill for it (256 sequences of 512 tokens, 8 heads of 64 x 64: 784 us, with eight 937).
+    static constexpr int RESIDENT = SHAPE == ALONE || NT == 256 && SHAPE == WHOLE ? 512 / NT : 0;
     static constexpr int TB = 8;
     static constexpr int ROW = P + 2 * N;                              // x | B | C of a token
     static constexpr int VPT = (TB * ROW / 4 + NT - 1) / NT;           // vectors of a thread
@@ -172,9 +179,9 @@ template <> struct Vec4Of<__nv_bfloat16> { using type = uint2; };
 __device__ __forceinline__ float4 vec4_f32(float4 v) { return v; }
 __device__ __forceinline__ float4 vec4_f32(uint2 v) { return bf16x4_f32(v); }
 
-template <int N, int P, typename TA, bool STATES, bool WIDE>
-__global__ void __launch_bounds__(ScanShape<N, P, WIDE>::NT) ssm_scan_kernel(SsmScanArgs a) {
-    using Sh = ScanShape<N, P, WIDE>;
+template <int N, int P, typename TA, bool STATES, int SHAPE>
+__global__ void __launch_bounds__(ScanShape<N, P, SHAPE>::NT, (ScanShape<N, P, SHAPE>::RESIDENT)) ssm_scan_kernel(SsmScanArgs a) {
+    using Sh = ScanShape<N, P, SHAPE>;
     using V4 = typename Vec4Of<TA>::type;
     constexpr int NPT = Sh::NPT, LP = Sh::LP, NS = Sh::NS, NT = Sh::NT, TB = Sh::TB, ROW = Sh::ROW,
                   VPT = Sh::VPT, OPT = Sh::OPT;
@@ -402,25 +409,30 @@ ScanWs scan_ws(const SsmDims &d, long long entries, long long n_seqs) {
     return w;
 }
 
-template <int N, int P, typename TA, bool WIDE>
+template <int N, int P, typename TA, int SHAPE>
 cudaError_t run_scan_as(const SsmScanArgs &a, bool states, unsigned grid, cudaStream_t s) {
-    constexpr int NT = ScanShape<N, P, WIDE>::NT;
+    constexpr int NT = ScanShape<N, P, SHAPE>::NT;
     if (states) {
-        ssm_scan_kernel<N, P, TA, true, WIDE><<<grid, NT, 0, s>>>(a);
+        ssm_scan_kernel<N, P, TA, true, SHAPE><<<grid, NT, 0, s>>>(a);
         return cudaGetLastError();
     }
-    if (a.seg_len < a.T) return launch_early(ssm_scan_kernel<N, P, TA, false, WIDE>, dim3(grid), NT, 0, s, a);
-    ssm_scan_kernel<N, P, TA, false, WIDE><<<grid, NT, 0, s>>>(a);
+    if (a.seg_len < a.T) return launch_early(ssm_scan_kernel<N, P, TA, false, SHAPE>, dim3(grid), NT, 0, s, a);
+    ssm_scan_kernel<N, P, TA, false, SHAPE><<<grid, NT, 0, s>>>(a);
     return cudaGetLastError();
 }
 
 template <int N, int P, typename TA>
 cudaError_t run_scan(const SsmScanArgs &a, bool states, unsigned segments, cudaStream_t s) {
     const unsigned grid = a.d.heads * segments;   // the heads of a group side by side: B and C come from L2
-    constexpr bool kTwoShapes = ScanShape<N, P, true>::NPT != ScanShape<N, P, false>::NPT;
-    // (fp32, 64 x 64, 512 tokens: 128 CTAs 253 -> 157 us, 512 CTAs 426 -> 395 us, 2,048 CTAs 928 -> 997 us)
-    if (kTwoShapes && grid <= 6 * (unsigned)sm_count()) return run_scan_as<N, P, TA, kTwoShapes>(a, states, grid, s);
-    return run_scan_as<N, P, TA, false>(a, states, grid, s);
+    constexpr bool kTwoShapes = ScanShape<N, P, WIDE>::NPT != ScanShape<N, P, WHOLE>::NPT;
+    // (fp32, 8 heads of 64 x 64, CTAs counted as if every segment were there: 16 sequences of 512 tokens,
+    // 384 CTAs, alone 119 us, wide 146, whole 242; 48 of 60 tokens, 472 CTAs, alone 39, wide 33; 50 of 256
+    // tokens, 800 CTAs, alone 129, wide 108; 256 of 512 tokens wide 997, whole 784)
+    if constexpr (kTwoShapes) {
+        if (grid <= 3 * (unsigned)sm_count()) return run_scan_as<N, P, TA, ALONE>(a, states, grid, s);
+        if (grid <= 6 * (unsigned)sm_count()) return run_scan_as<N, P, TA, WIDE>(a, states, grid, s);
+    }
+    return run_scan_as<N, P, TA, WHOLE>(a, states, grid, s);
 }
 
 template <int N, typename TA> cudaError_t run_scan_p(const SsmScanArgs &a, bool states, unsigned segments, cudaStream_t s) {
