@@ -360,9 +360,9 @@ namespace {
 
 bool has_tensor_form(const SsmDims &d, bool act_bf16) { return act_bf16 && ssm_tc_supported(d); }
 // The tensor-core form, but for batches of a few tokens a sequence, which leave its chunks of 128
-// all but empty (32 heads of 128 x 64, 200 sequences of 8 tokens: 148 us in the form of single
-// tokens, 305 us here, of 1 token 80 and 304; a sequence of 16 tokens 5.9 and 10.4 us, of 64 tokens
-// 16.3 and 10.0, of 256 tokens 58 and 14; 8,192 tokens of 32 heads 128 x 128: 1,470 and 114).
+// all but empty (32 heads of 128 x 64, 200 sequences of 8 tokens: 127 us in the form of single
+// tokens, 305 us here, of 1 token 79 and 304; a sequence of 16 tokens 5.6 and 10.4 us, of 64 tokens
+// 15.2 and 10.0, of 256 tokens 54 and 14; 8,192 tokens of 32 heads 128 x 128: 1,182 and 114).
 bool on_tensor_cores(const SsmDims &d, bool act_bf16, long long T, long long n_seqs) {
     return has_tensor_form(d, act_bf16) && T > 32 && T > 8 * n_seqs;
 }
@@ -382,7 +382,7 @@ int segments_wanted(const SsmDims &d, bool tensor) {
 
 // Tokens of a segment: whole chunks of 128, 256 or more.  A batch whose sequences fill the GPU by
 // themselves is then not cut: none of them is longer than its share of T.  (8,192 tokens of 32
-// heads, 128 x 128: 114 us in 4 segments, 274 in one; fp32, 4,096 tokens of 8 heads, 64 x 64: 141
+// heads, 128 x 128: 114 us in 4 segments, 274 in one; fp32, 4,096 tokens of 8 heads, 64 x 64: 111
 // and 883.  Four sequences of 2,048 tokens, which lose by it: 88 us and 81.)
 long long segment_len(const SsmDims &d, bool tensor, long long T) {
     const int want = segments_wanted(d, tensor);
