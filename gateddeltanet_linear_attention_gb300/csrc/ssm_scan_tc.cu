@@ -257,6 +257,12 @@ __device__ __forceinline__ void load_32b(const uint4 *p, bool wide, uint32_t (&v
         v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
     }
 }
+// The larger one; NaN stays NaN (a decay rate of NaN must not become the clamp).
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 // v SiLU(z): approximate exp and reciprocal, two values at a time.
 __device__ __forceinline__ f32x2 gate2(f32x2 v, f32x2 z) {
     const float2 t = unpack2(mul2(z, pack2(-kLog2e, -kLog2e)));
@@ -849,7 +855,7 @@ __global__ void __launch_bounds__(kThreads<HU>, 1)
             for (int i = 0; i < 4; ++i) {
                 const bool valid = 4 * lane + i < count && mine;
                 dt[i] = valid ? ssm_dt(raw[i], bias, d) : 0.f;
-                g[i] = valid ? fmaxf(rate * dt[i], kMinLog) : 0.f;
+                g[i] = valid ? max_nan(rate * dt[i], kMinLog) : 0.f;
             }
             if (c + 2 < chunks) fetch(c + 2);
             const float sum = (g[0] + g[1]) + (g[2] + g[3]);
