@@ -21,8 +21,9 @@
 // accumulator per chunk: the tensor core truncates its sums, which would bias a
 // state that it carried along itself.  w comes from a suffix sum of the
 // log-decays (exact where it matters, near the chunk's end).  Log-decays are
-// clamped at -60 a token: exp(-60) is nothing beside what the token adds, and
-// differences of running sums keep their meaning.
+// clamped at -88 a token, whose exponential is below the least normal number
+// and comes out as 0: what a token forgets is the same with the clamp, also
+// where it adds nothing, and differences of running sums keep their meaning.
 //
 // Roles (30 or 32 warps, one CTA per SM): warp 0 loads the tiles of C, B and x by TMA (one slot of
 // shared memory, two and two) and has z brought into L2; warp 1 issues G, Y2 and P X, warp 3 dS;
@@ -58,7 +59,7 @@ constexpr int kTile = kL * 128 * 2;            // bytes of a ring slot
 constexpr int kHalfTile = kTile / 2;           // 128 rows x 128 bytes: one TMA box
 constexpr int kXwPart = 16 * 128 * 2;          // one bf16 part of w X for 16 tokens (MN-major)
 constexpr int kXwBuf = 3 * kXwPart;
-constexpr float kMinLog = -60.0f;
+constexpr float kMinLog = -88.0f;
 
 // TMEM columns
 constexpr uint32_t kColS = 0, kColDS = 128, kColY = 256, kColG = 384;

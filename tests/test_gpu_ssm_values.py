@@ -29,3 +29,33 @@ def test_parameters_that_are_not_finite(act, P, what, fill):
             assert not got[~ok].isfinite().any(), "%s of sequence %d" % (name, n)
             ref.check(got[ok], v[ok], m[ok], r, name)
     assert gdn.gdn_device_error() == 0
+
+
+@pytest.mark.parametrize("act", ["fp32", "bf16"])
+@pytest.mark.parametrize("decay", [70.0, 80.0, 200.0])
+def test_tokens_that_add_nothing_forget(act, decay):
+    """Tokens of zeros with a log-decay below -60 each: what is left of the state is exp(-decay) of it,
+    not a floor that stands above that."""
+    b = Batch([100, 300, 600], H=2, G=1, N=64, P=64, act=act, seed=71, dt_min=1.0, dt_max=1.0)
+    b.A_log = torch.full((2,), decay).log()
+    b.D = None
+    x, bb, _ = b.parts(b.xbc)
+    for n, L in enumerate(b.lens):
+        s = int(b.cu[n])
+        for t in (3, 40, 41, L // 2, L - 1):
+            x[s + t] = 0
+    b.verify(*b.run())
+
+
+@pytest.mark.parametrize("act", ["fp32", "bf16"])
+def test_slow_tokens_behind_fast_ones(act):
+    """Tokens that forget everything, then tokens that forget little: the latter's decays are differences
+    of sums that the former made large."""
+    b = Batch([110, 300, 520], H=2, G=1, N=64, P=64, act=act, seed=72, rate=(30.0, 40.0), dt_shift=0.0)
+    for n, L in enumerate(b.lens):
+        s = int(b.cu[n])
+        b.u[s:s + L] = -7.0
+        for t in range(0, L - 12, 128):
+            b.u[s + t:s + min(t + 98, L - 12)] = 5.0
+    b.dt_bias = None
+    b.verify(*b.run())
