@@ -136,6 +136,17 @@ __device__ __forceinline__ void store8v(const C &c, __nv_bfloat16 *p, const floa
     }
 }
 
+// The sigmoid of a gate of type TA in a result of type TR.  A 16-bit gate's in a 32-bit one: x times
+// 16 bits of log2(e) is exact, and the rest of log2(e) a factor 1 - 4.9e-6 x behind the exponential, so the
+// error does not grow with |x| (below 10 half steps up to 70; the factor stops changing where the
+// exponential is nothing, so that a gate of +inf is 1).  2^25 elements with a gate per channel, 4,096 and
+// 5,120 wide: 87 and 104 us, with the 16-bit results' sigmoid 87 and 103, with the accurate one 103 and 134.
+template <typename TA, typename TR> __device__ __forceinline__ float gate_sigmoid(float x) { return sigmoid_for<TR>(x); }
+template <> __device__ __forceinline__ float gate_sigmoid<__nv_bfloat16, float>(float x) {
+    const float e = exp2_fast(-1.44268798828125f * x);
+    return rcp_fast(1.0f + fmaf(e, -4.8884952e-6f * fminf(x, 128.f), e));
+}
+
 __device__ __forceinline__ void cp_async16(void *dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
                  :: "r"((unsigned)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
@@ -232,7 +243,7 @@ __global__ void __launch_bounds__(MAXT, sm_blocks(MAXT)) block_norm_kernel(NormA
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     float v = a.w_post ? p[i][j] * k * w1[i][j] : p[i][j];
-                    if (channel_gate) v *= sigmoid_for<TA>(gt[i][j]);
+                    if (channel_gate) v *= gate_sigmoid<TA, TR>(gt[i][j]);
                     u[i][j] = fmaf(rs, v, u[i][j]);
                 }
             }

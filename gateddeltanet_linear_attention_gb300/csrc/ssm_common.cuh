@@ -187,7 +187,9 @@ template <typename T> __device__ __forceinline__ float silu_for(float x) { retur
 template <> __device__ __forceinline__ float silu_for<__nv_bfloat16>(float x) { return x * sigmoid_for<__nv_bfloat16>(x); }
 // e = exp(-x), for sigmoid(x) = 1 / (1 + e) and 1 - sigmoid(x) = e / (1 + e) without the difference,
 // so that the gradient of a gate that is all but open keeps its digits.  (Below -80 they stop
-// changing: a sigmoid of 1e-35.  NaN stays NaN.)
+// changing: a sigmoid of 1e-35.  NaN stays NaN.)  With 16-bit activations dw_post, which is 32 bits,
+// sums terms of the approximate one too: each is off by 2 + 1.2 |x| units in the last place, like the
+// terms' other roundings.
 template <typename T> __device__ __forceinline__ float exp_neg(float x) { return expf(x < -80.f ? 80.f : -x); }
 template <> __device__ __forceinline__ float exp_neg<__nv_bfloat16>(float x) {
     float t;

@@ -1,0 +1,40 @@
+"""The block norms at edges of their arguments."""
+import pytest
+import torch
+
+import ssm_ref as ref
+from gateddeltanet_linear_attention_gb300 import gdn
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.mark.parametrize("dim", [72, 4096, 77])
+def test_residuals_of_32_bits_have_gates_of_32_bits(dim):
+    """r' of a zero residual and a plain block is res_scale sigmoid(gate) block: exponential (2 units in
+    the last place, 4 half steps), sum, quotient, three products: 12 half steps at most, whatever the
+    gate's size."""
+    rows = 40
+    g = torch.Generator().manual_seed(80)
+    p = torch.randn(rows, dim, generator=g).to(BF)
+    gate = (torch.rand(rows, dim, generator=g) * 100 - 70).to(BF)
+    r = torch.zeros(rows, dim)
+    out = torch.empty(rows, dim, device="cuda")
+    gdn.gdn_block_norm(r.cuda(), block=p.cuda(), gate=gate.cuda(), res_scale=0.7, res_out=out)
+    ref.check(out, *ref.norm(p, gate, r, None, None, 0.0, 0.0, 0.7)["res_out"], 12 * ref.U32, "r'")
+
+
+@pytest.mark.parametrize("act,res", [(BF, BF), (BF, F32), (F32, F32)])
+@pytest.mark.parametrize("cols", [64, 1])
+def test_gates_of_infinity(act, res, cols):
+    """Open and shut for good: r + n and r; a NaN is the row's (or the element's) own."""
+    g = torch.Generator().manual_seed(81)
+    p, r = torch.randn(6, 64, generator=g).to(act), torch.randn(6, 64, generator=g).to(res)
+    gate = torch.zeros(6, cols, dtype=act)
+    gate[0], gate[1], gate[2, 0], gate[3], gate[4] = float("inf"), float("-inf"), float("nan"), 300.0, -300.0
+    out = torch.empty(6, 64, dtype=res, device="cuda")
+    gdn.gdn_block_norm(r.cuda(), block=p.cuda(), gate=gate.cuda(), res_out=out)
+    want = ref.norm(p, gate, r, None, None, 0.0, 0.0, 1.0)["res_out"]
+    ref.check(out, *want, 12 * ref.U32, "r'")
+    assert torch.equal(out.cpu().isnan(), want[0].isnan())
+    assert torch.equal(out[1].cpu(), r[1]) and torch.equal(out[4].cpu(), r[4])
