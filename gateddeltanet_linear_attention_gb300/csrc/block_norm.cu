@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(MAXT, sm_blocks(MAXT)) block_norm_bwd_kernel(N
         }
         const float k1 = n1, k2 = n2;
         float s1 = 1.0f, q1 = 0.f;
-        if (row_gate) sigmoid_pair<float>(ng, s1, q1);
+        if (row_gate) sigmoid_pair(ng, s1, q1);
         factors(row + step);
         f32x2 du[NV][4];
 #pragma unroll
@@ -458,10 +458,15 @@ __global__ void __launch_bounds__(MAXT, sm_blocks(MAXT)) block_norm_bwd_kernel(N
                     rg[i].get(x);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const f32x2 e = pack2(exp_neg<TA>(x[2 * j]), exp_neg<TA>(x[2 * j + 1]));
-                        const float2 q = unpack2(add2(e, both(1.0f)));
-                        sg[j] = pack2(one_over<TA>(q.x), one_over<TA>(q.y));
-                        rest[j] = mul2(e, sg[j]);
+                        if constexpr (sizeof(TA) == 2) {
+                            sigmoid_pairs_fast(x[2 * j], x[2 * j + 1], sg[j], rest[j]);
+                        } else {
+                            float s[2], q[2];
+                            sigmoid_pair(x[2 * j], s[0], q[0]);
+                            sigmoid_pair(x[2 * j + 1], s[1], q[1]);
+                            sg[j] = pack2(s[0], s[1]);
+                            rest[j] = pack2(q[0], q[1]);
+                        }
                     }
                 } else {
 #pragma unroll

@@ -185,23 +185,25 @@ template <> __device__ __forceinline__ float sigmoid_for<__nv_bfloat16>(float x)
 }
 template <typename T> __device__ __forceinline__ float silu_for(float x) { return silu_f(x); }
 template <> __device__ __forceinline__ float silu_for<__nv_bfloat16>(float x) { return x * sigmoid_for<__nv_bfloat16>(x); }
-// e = exp(-x), for sigmoid(x) = 1 / (1 + e) and 1 - sigmoid(x) = e / (1 + e) without the difference,
-// so that the gradient of a gate that is all but open keeps its digits.  (Below -80 they stop
-// changing: a sigmoid of 1e-35.  NaN stays NaN.)  With 16-bit activations dw_post, which is 32 bits,
-// sums terms of the approximate one too: each is off by 2 + 1.2 |x| units in the last place, like the
-// terms' other roundings.
-template <typename T> __device__ __forceinline__ float exp_neg(float x) { return expf(x < -80.f ? 80.f : -x); }
-template <> __device__ __forceinline__ float exp_neg<__nv_bfloat16>(float x) {
-    float t;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(t) : "f"(-kLog2e * x), "f"(115.4f));
-    return exp2_fast(t);
+// sigmoid(x) and 1 - sigmoid(x) without the difference, so that the gradient of a gate that is all but
+// open keeps its digits: 1 / (1 + e) and e / (1 + e) with e = exp(-|x|), which is which by x's sign.
+// NaN stays NaN.
+__device__ __forceinline__ void sigmoid_pair(float x, float &s, float &rest) {
+    const float e = expf(-fabsf(x)), most = 1.0f / (1.0f + e), least = e * most;
+    s = x < 0.f ? least : most;
+    rest = x < 0.f ? most : least;
 }
-template <typename T> __device__ __forceinline__ float one_over(float x) { return 1.0f / x; }
-template <> __device__ __forceinline__ float one_over<__nv_bfloat16>(float x) { return rcp_fast(x); }
-template <typename T> __device__ __forceinline__ void sigmoid_pair(float x, float &s, float &rest) {
-    const float e = exp_neg<T>(x);
-    s = one_over<T>(1.0f + e);
-    rest = e * s;
+// The same of two gates for 16-bit results, e = exp(-x): fewer instructions.  Below -88, where the sigmoid
+// leaves the normal numbers, both are 0 (1 - sigmoid is a factor beside the sigmoid only).  dw_post, 32
+// bits, sums terms of it too: each is off by 2 + 1.2 |x| units in the last place.
+__device__ __forceinline__ void sigmoid_pairs_fast(float x0, float x1, f32x2 &s, f32x2 &rest) {
+    float t0, t1;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(t0) : "f"(-kLog2e * x0), "f"(127.5f));
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(t1) : "f"(-kLog2e * x1), "f"(127.5f));
+    const f32x2 e = pack2(exp2_fast(t0), exp2_fast(t1));
+    const float2 q = unpack2(add2(e, pack2(1.0f, 1.0f)));
+    s = pack2(rcp_fast(q.x), rcp_fast(q.y));
+    rest = mul2(e, s);
 }
 
 // Row vectors of four elements.

@@ -38,3 +38,24 @@ def test_gates_of_infinity(act, res, cols):
     ref.check(out, *want, 12 * ref.U32, "r'")
     assert torch.equal(out.cpu().isnan(), want[0].isnan())
     assert torch.equal(out[1].cpu(), r[1]) and torch.equal(out[4].cpu(), r[4])
+
+
+@pytest.mark.parametrize("act,res", [(BF, BF), (BF, F32), (F32, F32)])
+@pytest.mark.parametrize("cols", [64, 1])
+def test_gradients_of_gates_that_are_shut(act, res, cols):
+    """Gates below -80, of -inf and of +inf: what passes them is as small as the sigmoid, or nothing.  The
+    bound is that of gates that are all but shut: a dozen roundings, two sums over 64 elements, and the fast exponential's
+    2 + 1.2 |x| units in the last place."""
+    x = torch.tensor([-70.0, -82.0, -87.0, -95.0, -200.0, float("-inf"), float("inf"), 90.0])
+    g = torch.Generator().manual_seed(82)
+    p, u, dro, = torch.randn(8, 64, generator=g).to(act), torch.randn(8, 64, generator=g).to(res), torch.randn(8, 64, generator=g).to(res)
+    gate = x[:, None].expand(8, cols).contiguous().to(act)
+    w, k = 1 + 0.2 * torch.randn(64, generator=g), 1 + torch.rand(8, generator=g)
+    out = dict(d_block=torch.empty(8, 64, dtype=act, device="cuda"), d_gate=torch.empty(8, cols, dtype=act, device="cuda"),
+               dw_post=torch.empty(64, device="cuda"))
+    ws = torch.empty(gdn.gdn_block_norm_workspace_size(8, 64), dtype=torch.uint8, device="cuda")
+    gdn.gdn_block_norm_backward(u.cuda(), d_res_out=dro.cuda(), block=p.cuda(), rstd_post=k.cuda(), w_post=w.cuda(), gate=gate.cuda(),
+                                workspace=ws, **out)
+    want = ref.norm_backward(p, gate, u, w, None, k, None, None, dro, 0.0, 1.0)
+    for name, got in out.items():
+        ref.check(got, *want[name], (2 * 64 + 64 + 2 * (2 + 1.2 * 88)) * ref.U32, name)
