@@ -54,6 +54,12 @@ __global__ void __launch_bounds__(kConvThreads, sizeof(TA) == 2 ? 8 : 6) ssm_con
     using Raw = decltype(load_raw((const TA *)nullptr));
     const SsmDims &d = a.d;
     const int c0 = (blockIdx.y * kConvThreads + threadIdx.x) * kVec;
+    // every pair of bounds is looked at by some block: a run below stops at the first sequence behind it
+    if (blockIdx.y == 0)
+        for (long long n = blockIdx.x * (long long)kConvThreads + threadIdx.x; n < a.n_seqs; n += gridDim.x * (long long)kConvThreads) {
+            long long s, e;
+            seq_bounds(a.cu, (int)n, a.T, a.err, s, e);
+        }
     if (c0 >= d.ch) return;
     const TA *__restrict__ x = (const TA *)a.x + c0;
     TA *__restrict__ out = (TA *)a.out + c0;

@@ -24,7 +24,7 @@ def test_parameters_that_are_not_finite(act, P, what, fill):
         val, mag, S, M = b.reference(n)
         rel = (8 * L + b.N + 64) * ref.U32
         rel_y = rel + (2 * 2.0 ** -8 + 2 * 128 * 60 * ref.U32 if act == "bf16" else 0)
-        for got, v, m, r, name in ((y[s:e].cpu(), val.reshape(L, -1), mag.reshape(L, -1), rel_y, "y"), (out[n].cpu(), S, M, rel, "state")):
+        for got, v, m, r, name in ((y[s:e].cpu(), val.reshape(L, b.H * b.P), mag.reshape(L, b.H * b.P), rel_y, "y"), (out[n].cpu(), S, M, rel, "state")):
             ok = v.isfinite()
             assert not got[~ok].isfinite().any(), "%s of sequence %d" % (name, n)
             ref.check(got[ok], v[ok], m[ok], r, name)
@@ -59,3 +59,20 @@ def test_slow_tokens_behind_fast_ones(act):
             b.u[s + t:s + min(t + 98, L - 12)] = 5.0
     b.dt_bias = None
     b.verify(*b.run())
+
+
+@pytest.mark.parametrize("act", ["fp32", "bf16"])
+@pytest.mark.parametrize("cu", [[0, 900, 900, 300, 900], [0, 500, 400, 900], [-5, 100, 200, 900], [0, 100, 200, 5000], [0, 900, 0, 900]])
+def test_conv_reports_malformed_lengths(act, cu):
+    """Wherever the pair that goes back stands, also behind the last token.  (Every bound is clamped to the
+    batch before it is used.)"""
+    dt = torch.bfloat16 if act == "bf16" else torch.float32
+    n, CH = len(cu) - 1, 64 + 32
+    cfg = gdn.make_ssm_config(1, 1, 16, 64, act=act, n_slots=n)
+    x, w = torch.zeros(900, CH, dtype=dt, device="cuda"), torch.zeros(CH, 4, dtype=dt, device="cuda")
+    hist, out = torch.zeros(n, CH, 3, dtype=dt, device="cuda"), torch.empty(900, CH, dtype=dt, device="cuda")
+    assert gdn.gdn_device_error() == 0
+    gdn.gdn_ssm_conv_prefill(cfg, x, torch.tensor(cu, dtype=torch.int32, device="cuda"), w, None, hist, None, out)
+    assert gdn.gdn_device_error() & gdn.DEVERR_CU_SEQLENS
+    gdn.gdn_ssm_conv_prefill(cfg, x, torch.tensor([0] * n + [900], dtype=torch.int32, device="cuda"), w, None, hist, None, out)
+    assert gdn.gdn_device_error() == 0
