@@ -59,3 +59,19 @@ def test_gradients_of_gates_that_are_shut(act, res, cols):
     want = ref.norm_backward(p, gate, u, w, None, k, None, None, dro, 0.0, 1.0)
     for name, got in out.items():
         ref.check(got, *want[name], (2 * 64 + 64 + 2 * (2 + 1.2 * 88)) * ref.U32, name)
+
+
+def test_no_rows_in_a_graph_behind_a_copy():
+    """Zero weight gradients of a batch without rows, captured behind an operation that is no kernel."""
+    e, w = torch.empty(0, 64, device="cuda"), torch.ones(64, device="cuda")
+    a, dw = torch.ones(1 << 20, device="cuda"), torch.full((64,), 7.0, device="cuda")
+    b = torch.zeros_like(a)
+    k = torch.empty(0, device="cuda")
+    ws = torch.empty(gdn.gdn_block_norm_workspace_size(0, 64), dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b.copy_(a)
+        gdn.gdn_block_norm_backward(e, k, w, e, dw_pre=dw, workspace=ws)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert (dw == 0).all() and (b == 1).all()

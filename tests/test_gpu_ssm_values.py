@@ -76,3 +76,52 @@ def test_conv_reports_malformed_lengths(act, cu):
     assert gdn.gdn_device_error() & gdn.DEVERR_CU_SEQLENS
     gdn.gdn_ssm_conv_prefill(cfg, x, torch.tensor([0] * n + [900], dtype=torch.int32, device="cuda"), w, None, hist, None, out)
     assert gdn.gdn_device_error() == 0
+
+
+@pytest.mark.parametrize("act", ["fp32", "bf16"])
+@pytest.mark.parametrize("fill", [NAN, INF])
+def test_states_that_are_not_finite(act, fill):
+    """One value of a state that comes in: its column of its head, and nothing else."""
+    b = Batch([200, 600, 0, 40], H=4, G=2, N=64, P=64, act=act, seed=73)
+    b.state[1, 2, 5, 7] = fill
+    b.state[2, 0, 1, 3] = fill
+    y, out = b.run()
+    for n, L in enumerate(b.lens):
+        s, e = int(b.cu[n]), int(b.cu[n + 1])
+        val, mag, S, M = b.reference(n)
+        rel = (8 * L + b.N + 64) * ref.U32
+        rel_y = rel + (2 * 2.0 ** -8 + 2 * 128 * 60 * ref.U32 if act == "bf16" else 0)
+        for got, v, m, r, name in ((y[s:e].cpu(), val.reshape(L, b.H * b.P), mag.reshape(L, b.H * b.P), rel_y, "y"), (out[n].cpu(), S, M, rel, "state")):
+            ok = v.isfinite()
+            assert not got[~ok].isfinite().any(), "%s of sequence %d" % (name, n)
+            ref.check(got[ok], v[ok], m[ok], r, name)
+    assert gdn.gdn_device_error() == 0
+
+
+@pytest.mark.parametrize("act", ["fp32", "bf16"])
+def test_many_sequences_in_a_graph_with_other_lengths(act):
+    """A captured call of more sequences than a warp lays out, some cut, replayed with other lengths, fewer
+    tokens and nothing behind them written; into a pool of its own, then in place."""
+    lens = [5, 0, 40] * 12 + [700, 300, 1, 900]
+    b = Batch(lens, H=2, G=1, act=act, seed=74).upload()
+    y, out = torch.full((b.rows, b.H * b.P), 7.0, dtype=b.act, device="cuda"), torch.full_like(b.d_state, 7.0)
+    state = b.d_state.clone()
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    with torch.cuda.graph(graphs[0]):
+        b.launch(y, out)
+    with torch.cuda.graph(graphs[1]):
+        b.launch(y, state, state=state)
+    graphs[0].replay()
+    b.verify(y, out)
+    assert (out == b.d_state)[[n for n, L in enumerate(lens) if L == 0]].all()
+    b.lens = [300, 0, 3] + [0, 1, 30] * 12 + [513]
+    b.cu = torch.zeros(len(lens) + 1, dtype=torch.int32)
+    b.cu[1:] = torch.tensor(b.lens).cumsum(0)
+    b.d_cu.copy_(b.cu)
+    for graph, to in zip(graphs, (out, state)):
+        y.fill_(7.0)
+        graph.replay()
+        b.verify(y, to)
+        assert (y[int(b.cu[-1]):] == 7).all()
+    assert torch.equal(out, state)
+    assert gdn.gdn_device_error() == 0
