@@ -32,6 +32,15 @@ __device__ __forceinline__ int seq_of(const int32_t *cu, int n_seqs, long long t
     return cu[lo] <= t ? lo : -1;
 }
 
+// Looks at all pairs of bounds, a thread of the grid's first column of blocks at each.  (Out of line: as
+// a part of the kernel it cost it registers.)
+__device__ __noinline__ void check_bounds(const int32_t *cu, int n_seqs, long long T, unsigned *err) {
+    for (long long n = blockIdx.x * (long long)kConvThreads + threadIdx.x; n < n_seqs; n += gridDim.x * (long long)kConvThreads) {
+        long long s, e;
+        seq_bounds(cu, (int)n, T, err, s, e);
+    }
+}
+
 }  // namespace
 
 // ------------------------------------------------------------- packed prompts
@@ -55,11 +64,7 @@ __global__ void __launch_bounds__(kConvThreads, sizeof(TA) == 2 ? 8 : 6) ssm_con
     const SsmDims &d = a.d;
     const int c0 = (blockIdx.y * kConvThreads + threadIdx.x) * kVec;
     // every pair of bounds is looked at by some block: a run below stops at the first sequence behind it
-    if (blockIdx.y == 0)
-        for (long long n = blockIdx.x * (long long)kConvThreads + threadIdx.x; n < a.n_seqs; n += gridDim.x * (long long)kConvThreads) {
-            long long s, e;
-            seq_bounds(a.cu, (int)n, a.T, a.err, s, e);
-        }
+    if (blockIdx.y == 0) check_bounds(a.cu, a.n_seqs, a.T, a.err);
     if (c0 >= d.ch) return;
     const TA *__restrict__ x = (const TA *)a.x + c0;
     TA *__restrict__ out = (TA *)a.out + c0;
