@@ -359,12 +359,20 @@ __global__ void __launch_bounds__(ScanShape<N, P, SHAPE>::NT, (ScanShape<N, P, S
 namespace {
 
 bool has_tensor_form(const SsmDims &d, bool act_bf16) { return act_bf16 && ssm_tc_supported(d); }
-// The tensor-core form, but for batches of a few tokens a sequence, which leave its chunks of 128
-// all but empty (32 heads of 128 x 64, 200 sequences of 8 tokens: 127 us in the form of single
-// tokens, 305 us here, of 1 token 79 and 304; a sequence of 16 tokens 5.6 and 10.4 us, of 64 tokens
-// 15.2 and 10.0, of 256 tokens 54 and 14; 8,192 tokens of 32 heads 128 x 128: 1,182 and 114).
+// The tensor-core form, but for batches of few tokens a sequence, which leave its chunks of 128 all but
+// empty: it takes 12 to 18 us per round of CTAs whatever the lengths, the form of single tokens a time that
+// grows with them.  Batches of equal lengths are even at 30 to 46 tokens a sequence.  But the host knows
+// the mean alone, and where one sequence has most of the tokens the form of single tokens is the slower
+// one, by the more the fewer the sequences.  So the limit is 8 tokens a sequence, and 24 from ten rounds
+// on.  Single tokens / tensor cores, equal lengths | one long sequence among single tokens, us:
+//   190 sequences of 8 heads of 64 x 64 (5 rounds), 8 tokens in the mean  37 / 75 | 166 / 89, 16 tokens 45 / 75 | 167 / 92
+//   95 of 32 heads of 128 x 64 (10 rounds), 16 tokens 112 / 181 | 229 / 205, 24 tokens 140 / 179 | 255 / 209
+//   190 of 32 heads of 128 x 128 (40 rounds), 16 tokens 345 / 655 | 543 / 698, 24 tokens 442 / 653 | 704 / 717, 32 tokens 546 / 649 | 967 / 736
+// and one sequence of 32 heads of 128 x 64, 24 tokens 18 / 29, 48 tokens 27 / 27, 64 tokens 30 / 26.
 bool on_tensor_cores(const SsmDims &d, bool act_bf16, long long T, long long n_seqs) {
-    return has_tensor_form(d, act_bf16) && T > 32 && T > 8 * n_seqs;
+    if (!has_tensor_form(d, act_bf16)) return false;
+    const long long few = n_seqs * ssm_tc_units(d) >= 10LL * sm_count() ? 24 : 8;
+    return T > 32 && T > few * n_seqs;
 }
 
 // Segments that run side by side when one sequence has the GPU to itself: the resident CTAs over

@@ -69,3 +69,28 @@ def test_states_of_many_chunks_uncut():
         worst = float(((out[0, h].cpu().double() - S[0]).abs() / S[0]).max())
         print("head %d: %.1f U" % (h, worst / ref.U32))
         assert worst <= bound(L)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("length", [9, 16, 24])
+def test_many_short_sequences_take_the_form_of_single_tokens(length):
+    """More than ten rounds of CTAs of mostly empty chunks: the form of single tokens, whose outputs have
+    one rounding to 16 bits and 32-bit errors beside it (8 a token in the recurrence, N in a sum)."""
+    b = Batch([length] * 100, H=32, G=2, N=64, P=128, seed=61)
+    y, out = b.run()
+    for n in (0, 31, 32, 99):
+        s, e = int(b.cu[n]), int(b.cu[n + 1])
+        val, mag, S, M = b.reference(n)
+        rel = (8 * length + b.N + 64) * ref.U32
+        ref.check(y[s:e], val.reshape(length, -1), mag.reshape(length, -1), rel, "y of sequence %d" % n)
+        ref.check(out[n], S, M, rel, "state of sequence %d" % n)
+
+
+@pytest.mark.gpu
+def test_a_long_sequence_among_single_tokens():
+    """Either form, and a long sequence that is cut in it."""
+    for count in (30, 99):
+        lens = [1] * count + [1200]
+        b = Batch(lens, H=32, G=2, N=64, P=128, seed=62)
+        y, out = b.run()
+        b.verify(y, out, seqs=[0, 17, count - 1, count])
