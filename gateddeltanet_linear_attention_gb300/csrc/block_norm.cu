@@ -589,8 +589,9 @@ template <typename TA, typename TR, bool VEC> cudaError_t fwd_dim(const NormArgs
     if constexpr (kFew && VEC) {
         if (a.dim <= 2048) return run_fwd<TA, TR, 1, 256, false, VEC>(a, s);
         if (a.dim <= 4096) return run_fwd<TA, TR, 1, 512, false, VEC>(a, s);
+    } else {
+        if (a.dim <= 4096) return run_fwd<TA, TR, 2, 256, false, VEC>(a, s);
     }
-    if (a.dim <= 4096) return run_fwd<TA, TR, 2, 256, false, VEC>(a, s);
     if constexpr (kFew) {
         if (a.dim <= 5120) return run_fwd<TA, TR, 1, 640, false, VEC>(a, s);
         if (a.dim <= 8192) return run_fwd<TA, TR, 1, 1024, false, VEC>(a, s);

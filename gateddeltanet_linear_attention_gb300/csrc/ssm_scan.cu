@@ -11,6 +11,8 @@
 // So a first pass computes every segment's E and summed log-decay at once, a
 // short second one chains them, and the last one runs all segments with
 // outputs, each from the state that enters it.
+#include <climits>
+
 #include "ssm_common.cuh"
 
 namespace gdn {
@@ -375,6 +377,9 @@ bool on_tensor_cores(const SsmDims &d, bool act_bf16, long long T, long long n_s
     return T > 32 && T > few * n_seqs;
 }
 
+// CTAs of an SM that a batch is cut for, in the form of single tokens.
+constexpr int resident_ctas(int N, int P) { return N * P >= 16384 ? 2 : N * P >= 8192 ? 4 : 8; }
+
 // Segments that run side by side when one sequence has the GPU to itself: the resident CTAs over
 // those of one segment (heads, or units of the tensor-core form, one CTA per SM there).
 int segments_wanted(const SsmDims &d, bool tensor) {
@@ -382,8 +387,7 @@ int segments_wanted(const SsmDims &d, bool tensor) {
     if (tensor) {
         want = sm_count() / ssm_tc_units(d);
     } else {
-        const int per_sm = d.N * d.P >= 16384 ? 2 : d.N * d.P >= 8192 ? 4 : 8;
-        want = sm_count() * per_sm / d.heads;
+        want = sm_count() * resident_ctas(d.N, d.P) / d.heads;
     }
     return want < 1 ? 1 : want;
 }
@@ -417,37 +421,44 @@ ScanWs scan_ws(const SsmDims &d, long long entries, long long n_seqs) {
     return w;
 }
 
-template <int N, int P, typename TA, int SHAPE>
-cudaError_t run_scan_as(const SsmScanArgs &a, bool states, unsigned grid, cudaStream_t s) {
+template <int N, int P, typename TA, bool STATES, int SHAPE>
+cudaError_t run_scan_as(const SsmScanArgs &a, unsigned grid, cudaStream_t s) {
     constexpr int NT = ScanShape<N, P, SHAPE>::NT;
-    if (states) {
-        ssm_scan_kernel<N, P, TA, true, SHAPE><<<grid, NT, 0, s>>>(a);
-        return cudaGetLastError();
-    }
-    if (a.seg_len < a.T) return launch_early(ssm_scan_kernel<N, P, TA, false, SHAPE>, dim3(grid), NT, 0, s, a);
-    ssm_scan_kernel<N, P, TA, false, SHAPE><<<grid, NT, 0, s>>>(a);
+    auto kern = ssm_scan_kernel<N, P, TA, STATES, SHAPE>;
+    if (!STATES && a.seg_len < a.T) return launch_early(kern, dim3(grid), NT, 0, s, a);
+    kern<<<grid, NT, 0, s>>>(a);
     return cudaGetLastError();
 }
 
-template <int N, int P, typename TA>
-cudaError_t run_scan(const SsmScanArgs &a, bool states, unsigned segments, cudaStream_t s) {
+template <int N, int P, typename TA, bool STATES>
+cudaError_t run_scan(const SsmScanArgs &a, unsigned segments, cudaStream_t s) {
     const unsigned grid = a.d.heads * segments;   // the heads of a group side by side: B and C come from L2
     constexpr bool kTwoShapes = ScanShape<N, P, WIDE>::NPT != ScanShape<N, P, WHOLE>::NPT;
+    // the first pass has no more CTAs than a batch is cut for
+    constexpr int kMost = STATES ? resident_ctas(N, P) : INT_MAX;
     // (fp32, 8 heads of 64 x 64, CTAs counted as if every segment were there: 16 sequences of 512 tokens,
     // 384 CTAs, alone 119 us, wide 146, whole 242; 48 of 60 tokens, 472 CTAs, alone 39, wide 33; 50 of 256
     // tokens, 800 CTAs, alone 129, wide 108; 256 of 512 tokens wide 997, whole 784)
-    if constexpr (kTwoShapes) {
-        if (grid <= 3 * (unsigned)sm_count()) return run_scan_as<N, P, TA, ALONE>(a, states, grid, s);
-        if (grid <= 6 * (unsigned)sm_count()) return run_scan_as<N, P, TA, WIDE>(a, states, grid, s);
+    if constexpr (!kTwoShapes) {
+        return run_scan_as<N, P, TA, STATES, WHOLE>(a, grid, s);
+    } else {
+        if (grid <= 3 * (unsigned)sm_count()) return run_scan_as<N, P, TA, STATES, ALONE>(a, grid, s);
+        if constexpr (kMost > 6) {
+            if (grid > 6 * (unsigned)sm_count()) return run_scan_as<N, P, TA, STATES, WHOLE>(a, grid, s);
+        }
+        return run_scan_as<N, P, TA, STATES, WIDE>(a, grid, s);
     }
-    return run_scan_as<N, P, TA, WHOLE>(a, states, grid, s);
 }
 
+template <int N, int P, typename TA>
+cudaError_t run_scan_pass(const SsmScanArgs &a, bool states, unsigned segments, cudaStream_t s) {
+    return states ? run_scan<N, P, TA, true>(a, segments, s) : run_scan<N, P, TA, false>(a, segments, s);
+}
 template <int N, typename TA> cudaError_t run_scan_p(const SsmScanArgs &a, bool states, unsigned segments, cudaStream_t s) {
     switch (a.d.P) {
-        case 32: return run_scan<N, 32, TA>(a, states, segments, s);
-        case 64: return run_scan<N, 64, TA>(a, states, segments, s);
-        default: return run_scan<N, 128, TA>(a, states, segments, s);
+        case 32: return run_scan_pass<N, 32, TA>(a, states, segments, s);
+        case 64: return run_scan_pass<N, 64, TA>(a, states, segments, s);
+        default: return run_scan_pass<N, 128, TA>(a, states, segments, s);
     }
 }
 template <typename TA> cudaError_t run_scan_np(const SsmScanArgs &a, bool states, unsigned segments, cudaStream_t s) {

@@ -43,7 +43,6 @@
 #include <cuda.h>   // CUtensorMap (the encoder itself is reached through the runtime)
 
 #include <climits>
-#include <cstring>
 
 #include "ssm_common.cuh"
 #include "tc_sm103.cuh"
@@ -983,17 +982,13 @@ int ssm_tc_units(const SsmDims &d) {
 cudaError_t launch_ssm_scan_tc(const SsmScanArgs &a, bool states, unsigned segments, cudaStream_t s) {
     SsmMaps m;
     const long long hp = (long long)a.d.heads * a.d.P, gn = (long long)a.d.groups * a.d.N;
-    if (a.T > 0) {
-        if (!encode(&m.x, a.x, a.ld_x, hp, a.T) || !encode(&m.b, a.b, a.ld_bc, gn, a.T) ||
-            !encode(&m.c, a.c, a.ld_bc, gn, a.T) || !encode(&m.y, a.y, hp, hp, a.T))
-            return cudaErrorInvalidValue;
-        if (a.z) {
-            if (!encode(&m.z, a.z, a.ld_z, hp, a.T)) return cudaErrorInvalidValue;
-        } else {
-            m.z = m.x;
-        }
+    if (!encode(&m.x, a.x, a.ld_x, hp, a.T) || !encode(&m.b, a.b, a.ld_bc, gn, a.T) ||
+        !encode(&m.c, a.c, a.ld_bc, gn, a.T) || !encode(&m.y, a.y, hp, hp, a.T))
+        return cudaErrorInvalidValue;
+    if (a.z) {
+        if (!encode(&m.z, a.z, a.ld_z, hp, a.T)) return cudaErrorInvalidValue;
     } else {
-        memset(&m, 0, sizeof m);       // no tokens: the maps are not used
+        m.z = m.x;
     }
     const unsigned grid = (unsigned)ssm_tc_units(a.d) * segments;
 #define GDN_SSM_TC(N, HU) return states ? run<N, HU, true>(a, m, grid, s) : run<N, HU, false>(a, m, grid, s)
