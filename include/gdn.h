@@ -388,11 +388,22 @@ gdn_status gdn_state_copy(const gdn_config *cfg, const float *src_state, const v
  * [n_slots][CH][3], oldest input first, CH = heads*head_dim +
  * 2*groups*d_state.  The rules of the top of this file hold: slots, padding
  * lanes (zero outputs, nothing written), views, alignment, streams, errors.
- * Packed rows behind cu_seqlens[n_seqs] are neither read nor written, so a
- * captured call may carry a smaller batch than its T.  A value that is not
+ * Packed rows behind cu_seqlens[n_seqs] are not written and their values not
+ * used, so a captured call may carry a smaller batch than its T.  (They may be
+ * read all the same, whole tiles at a time, and stay valid memory up to T.)
+ * A value that is not
  * finite reaches the outputs and states that it is a part of (which are then
  * not finite either: NaN where the sum may have been an infinity), never
- * tokens in front of it, other heads' columns or other sequences.  */
+ * tokens in front of it, other heads' columns or other sequences.
+ *
+ * Precision: states and sums are 32 bits.  gdn_ssm_prefill with bf16
+ * activations, d_state and head_dim 64 or 128 and not too few tokens a sequence
+ * in the mean (T and n_seqs decide, so the last bits of a sequence's results
+ * depend on its batch) runs on the tensor cores: there the state's copy that
+ * meets C and the scores that meet x are rounded to bf16, which brings y's error
+ * to 1.7e-3 to 2.3e-3 of its size in the mean square (the rounding of y alone
+ * is 1.65e-3).  The states take x in full; theirs is that of 32-bit sums, 1e-7
+ * to 2e-6. */
 typedef struct gdn_ssm_config {
     int32_t groups, heads;     /* heads % groups == 0; heads <= 4096 */
     int32_t d_state, head_dim; /* d_state in {16, 32, 64, 128}, head_dim in {32, 64, 128} */
@@ -472,7 +483,8 @@ gdn_status gdn_ssm_decode(const gdn_ssm_config *cfg, const gdn_ssm_io *io, void 
  * columns; views need element alignment only (all of them 16-byte aligned
  * with 16-byte row strides and dim % 8 == 0 take vector loads).  res_out may
  * be residual, d_residual may be d_res_out; nothing else may alias.
- * dim <= 16384; act fp32 needs res fp32.  rows == 0 is no work (a backward
+ * dim <= 16384; act fp32 needs res fp32.  Squares are summed in 32 bits: where
+ * a row's sum passes 3.4e38, 1 / rms is 0.  rows == 0 is no work (a backward
  * call then writes zero weight gradients). */
 typedef struct gdn_block_norm_io {
     int64_t rows;
@@ -518,7 +530,8 @@ gdn_status gdn_block_norm_backward(const gdn_block_norm_io *io, void *workspace,
  * chunk operand of the tensor-core state chain (gdn_chunk_prefill,
  * gdn_mixer_prefill), bit 2 the first x tile of tensor-core
  * gdn_ssm_prefill (of every sequence that is not cut, and of every segment in
- * front of the last where one is).  A call that timed out writes no state.  Process-wide,
+ * front of the last where one is).  Work that timed out writes no state (a
+ * sequence's heads each for themselves).  Process-wide,
  * read at each call; GDN_ERR_INVALID_ARG for wait_ns = 0, above 60 s, or an
  * unknown bit. */
 gdn_status gdn_debug_set_wait(uint64_t wait_ns, uint32_t lose);
