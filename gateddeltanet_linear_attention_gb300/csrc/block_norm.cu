@@ -577,7 +577,8 @@ cudaError_t run_bwd(const NormArgs &a, cudaStream_t s, int &ctas) {
     return cudaGetLastError();
 }
 
-// Threads and elements of a thread by row width (times of 2^25 elements, forward, fp32 unless stated).
+// Threads and elements of a thread by row width (times of 2^25 elements with a gate per channel,
+// forward, fp32 unless stated).
 // 16 elements: half as many sums over warps (bf16, 4,096 wide: 60 us, with 8 63 us).  With fp32
 // operands the next row's loads then spill, and 8 elements are faster: 4,096 wide 127 us, with 16
 // 149; 5,120 wide 118, with 16 198 (bf16: 110 and 84).  Rows of single elements keep 16 up to 4,096

@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(256) ssm_chain_states_kernel(SsmScanArgs a) {
 // while this one is computed; the row slices' parts of y are summed per block.
 // Bound by the fp32 units, 3 packed operations per two state elements and token, where the batch
 // fills the GPU (256 sequences of 512 tokens, 8 heads of 64 x 64: 784 us, 44 % of their rate; 8,192
-// tokens of 32 heads, 128 x 128, cut: 1,223 us), and by a token's latency, 225 ns, where it does not
+// tokens of 32 heads, 128 x 128, cut: 1,227 us), and by a token's latency, 225 ns, where it does not
 // (7 sequences of up to 256 tokens: 57 us).
 // STATES: pass 1, no outputs: the leaving state from zero and the log-decay.
 // WIDE: 4 to 16 rows a thread, as many threads as 256 allow, for batches that do not fill the GPU.
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(ScanShape<N, P, SHAPE>::NT, (ScanShape<N, P, S
     SsmSegment sg;
     let_next_start();
     const bool run = ssm_segment<STATES>(a, blockIdx.x / d.heads, sg);
-    // a segment that starts from an initial state needs nothing of the passes in front of this one
+    // a sequence that is not cut needs nothing of the passes in front of this one
     if (!STATES && (!run || sg.entry >= 0 || sg.slot < 0)) await_previous();
     if (!run) return;
     if (STATES && (sg.last || sg.slot < 0)) return;
@@ -394,8 +394,8 @@ int segments_wanted(const SsmDims &d, bool tensor) {
 
 // Tokens of a segment: whole chunks of 128, 256 or more.  A batch whose sequences fill the GPU by
 // themselves is then not cut: none of them is longer than its share of T.  (8,192 tokens of 32
-// heads, 128 x 128: 114 us in 4 segments, 274 in one; fp32, 4,096 tokens of 8 heads, 64 x 64: 111
-// and 883.  Four sequences of 2,048 tokens, which lose by it: 88 us and 81.)
+// heads, 128 x 128: 117 us in 4 segments, 275 in one; fp32, 4,096 tokens of 8 heads, 64 x 64: 117
+// and 828.  Four sequences of 2,048 tokens, which lose by it: 91 us and 83.)
 long long segment_len(const SsmDims &d, bool tensor, long long T) {
     const int want = segments_wanted(d, tensor);
     const long long len = ((T + want - 1) / want + 127) / 128 * 128;

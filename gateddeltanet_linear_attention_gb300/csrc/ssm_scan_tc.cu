@@ -37,9 +37,9 @@
 // about 8,000 cycles, and by the latency of each role's steps between TMEM, registers and shared
 // memory (half of the issue slots are used, the tensor cores for a third of the time), not by memory.
 // 8,192 tokens of 32 heads, 128 x 128 states, in 4 segments: the states' pass 36 us, the chain of
-// states 8 us, the pass with outputs 82 us, 118 us together with early launches, 2.3 TB/s of what has
+// states 8 us, the pass with outputs 82 us, 117 us together with early launches, 2.3 TB/s of what has
 // to be moved; 16 prompts of 256 to 4,096 tokens, 64 heads of 128 x 64: 384 us, 3.4 TB/s; 65,536
-// tokens of 8 heads, 64 x 64: 93 us.  The form of single tokens takes 1,182 us for the first of these.
+// tokens of 8 heads, 64 x 64: 93 us.  The form of single tokens takes 1,190 us for the first of these.
 #include <cuda.h>   // CUtensorMap (the encoder itself is reached through the runtime)
 
 #include <climits>
