@@ -1,0 +1,267 @@
+// attn_decode.cu -- attention of a few new tokens over a paged cache.
+//
+//   s_i = scale q . k_i,   m = max s,   l = sum exp(s - m),   o = sum exp(s - m) v_i / l
+//
+// One pass over the visible tokens with the running m, l and o of each query row; the tiles of
+// all sequences and key heads are one line cut into equal shares (AttnWalk).  A unit that one CTA
+// holds whole is written at once; of the others every CTA leaves its (m, l, o), and the join kernel
+// adds them up in the order of the tokens: no atomics, equal calls give equal bits.
+#include "attn_common.cuh"
+
+namespace gdn {
+
+namespace {
+
+constexpr int kSimtThreads = 256;
+constexpr int kSimtTile = 32;
+
+template <typename T> __device__ __forceinline__ void store1(T *p, float v) { *p = from_f32<T>(v); }
+
+// CUDA-core form: RPW query rows a warp, a tile of 32 tokens in shared memory as 32-bit values, a token a
+// lane for the scores and D / 32 columns a lane for the sums.
+template <typename T, int D, int RPW>
+__global__ void __launch_bounds__(kSimtThreads) attn_decode_simt_kernel(const AttnDecodeArgs a) {
+    constexpr int TILE = kSimtTile, LDK = D + 4, CPL = D / 32, WARPS = kSimtThreads / 32, RB = WARPS * RPW;
+    extern __shared__ float4 smem4[];
+    float *ks = reinterpret_cast<float *>(smem4), *vs = ks + TILE * LDK, *qs = vs + TILE * D;
+    __shared__ long long sums[33];
+    __shared__ int found[3], bad_page[TILE];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rows = a.d.grp * a.tokens, row0 = blockIdx.y * RB;
+    let_next_start();
+    AttnWalk w;
+    if (!attn_begin<TILE, kSimtThreads>(a, blockIdx.x, sums, found, w)) {
+        if (blockIdx.y == 0 && tid == 0) a.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
+        return;
+    }
+    const T *kp = (const T *)a.k_pages, *vp = (const T *)a.v_pages;
+    bool unit_first = true;               // this unit is the CTA's first one
+    while (w.left > 0) {
+        const bool whole_front = w.t == 0;
+        const int n = w.n, h = w.h;
+        const AttnSeq s = w.s;
+        // query rows in 32 bits
+        __syncthreads();
+        for (int i = tid; i < RB * (D / 4); i += kSimtThreads) {
+            const int r = row0 + i / (D / 4), c = i % (D / 4) * 4;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < rows) {
+                const int tok = r / a.d.grp, g = r % a.d.grp;
+                v = load4f((const T *)a.q + ((long long)n * a.tokens + tok) * a.ld_q + (long long)(h * a.d.grp + g) * a.hs_q + c);
+            }
+            reinterpret_cast<float4 *>(qs)[i] = v;
+        }
+        float m[RPW], l[RPW], o[RPW][CPL];
+        int end[RPW], begin[RPW];
+#pragma unroll
+        for (int r = 0; r < RPW; ++r) {
+            m[r] = -INFINITY;
+            l[r] = 0.f;
+            const int row = row0 + warp * RPW + r;
+            end[r] = row < rows ? s.len - a.tokens + 1 + row / a.d.grp : 0;
+            begin[r] = a.window > 0 ? end[r] - a.window : 0;
+#pragma unroll
+            for (int c = 0; c < CPL; ++c) o[r][c] = 0.f;
+        }
+        bool unit_end;
+        do {
+            const int i0 = (s.tile0 + w.t) * TILE;
+            __syncthreads();
+            if (tid < TILE) {             // the page of every token, -1: masked
+                const int i = i0 + tid;
+                int page = -1;
+                if (i < s.len && i >= s.first) {
+                    page = a.table[(long long)s.row * a.d.max_pages + (i >> a.d.page_shift)];
+                    if (page < 0 || page >= a.d.n_pages) {
+                        set_error(a.err, GDN_DEVERR_PAGE);
+                        page = -1;
+                    }
+                }
+                bad_page[tid] = page;
+            }
+            __syncthreads();
+            for (int i = tid; i < TILE * (D / 4); i += kSimtThreads) {
+                const int t = i / (D / 4), c = i % (D / 4) * 4, page = bad_page[t];
+                float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
+                if (page >= 0) {
+                    const long long at = (((long long)page * a.d.hkv + h) * a.d.page + ((i0 + t) & (a.d.page - 1))) * D + c;
+                    kv = load4f(kp + at);
+                    vv = load4f(vp + at);
+                }
+                *reinterpret_cast<float4 *>(ks + t * LDK + c) = kv;
+                *reinterpret_cast<float4 *>(vs + t * D + c) = vv;
+            }
+            __syncthreads();
+            float sc[RPW];
+#pragma unroll
+            for (int r = 0; r < RPW; ++r) sc[r] = 0.f;
+            for (int c = 0; c < D; c += 4) {
+                const float4 kv = *reinterpret_cast<const float4 *>(ks + lane * LDK + c);
+#pragma unroll
+                for (int r = 0; r < RPW; ++r) {
+                    const float4 q = *reinterpret_cast<const float4 *>(qs + (warp * RPW + r) * D + c);
+                    sc[r] = fmaf(q.x, kv.x, fmaf(q.y, kv.y, fmaf(q.z, kv.z, fmaf(q.w, kv.w, sc[r]))));
+                }
+            }
+            const int i = i0 + lane;
+            const bool there = bad_page[lane] >= 0;
+            float p[RPW];
+            unsigned seen[RPW];
+#pragma unroll
+            for (int r = 0; r < RPW; ++r) {
+                const bool see = there && i < end[r] && i >= begin[r];
+                seen[r] = __ballot_sync(0xffffffffu, see);
+                float top = see ? sc[r] : -INFINITY;
+#pragma unroll
+                for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+                const float nm = fmaxf(m[r], top * a.scale_log2), ref = nm == -INFINITY ? 0.f : nm;
+                const float back = exp2_fast(m[r] - ref);
+                p[r] = see ? exp2_fast(fmaf(sc[r], a.scale_log2, -ref)) : 0.f;
+                m[r] = nm;
+                l[r] = l[r] * back + p[r];
+#pragma unroll
+                for (int c = 0; c < CPL; ++c) o[r][c] *= back;
+            }
+            for (int t = 0; t < TILE; ++t) {
+                float v[CPL];
+                if constexpr (CPL == 2) {
+                    const float2 x = *reinterpret_cast<const float2 *>(vs + t * D + lane * 2);
+                    v[0] = x.x; v[1] = x.y;
+                } else {
+#pragma unroll
+                    for (int c = 0; c < CPL; c += 4) {
+                        const float4 x = *reinterpret_cast<const float4 *>(vs + t * D + lane * 4 + c * 32);
+                        v[c] = x.x; v[c + 1] = x.y; v[c + 2] = x.z; v[c + 3] = x.w;
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < RPW; ++r) {
+                    if (seen[r] >> t & 1u) {      // what a row does not see may hold anything
+                        const float pt = __shfl_sync(0xffffffffu, p[r], t);
+#pragma unroll
+                        for (int c = 0; c < CPL; ++c) o[r][c] = fmaf(pt, v[c], o[r][c]);
+                    }
+                }
+            }
+            unit_end = attn_next<TILE>(a, w);
+        } while (!unit_end && w.left > 0);
+        // the unit's rows: whole, or a part for the join kernel
+        const bool whole = whole_front && unit_end;
+        const int slot = unit_first ? 0 : 1;
+        float *part = attn_part(a, blockIdx.x, slot);
+#pragma unroll
+        for (int r = 0; r < RPW; ++r) {
+            const int row = row0 + warp * RPW + r;
+            const float lsum = warp_sum(l[r]);
+            if (row < rows) {
+                const int tok = row / a.d.grp, g = row % a.d.grp;
+                const long long orow = ((long long)n * a.tokens + tok) * a.d.hq + h * a.d.grp + g;
+                const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
+#pragma unroll
+                for (int c = 0; c < CPL; ++c) {
+                    const int col = CPL == 2 ? lane * 2 + c : lane * 4 + (c >> 2) * 128 + (c & 3);
+                    if (whole) store1((T *)a.out + orow * D + col, o[r][c] * inv);
+                    else part[row * D + col] = o[r][c];
+                }
+                if (lane == 0) {
+                    if (whole) {
+                        if (a.lse) a.lse[orow] = lsum == 0.f ? -INFINITY : (m[r] + log2f(lsum)) * kLn2;
+                    } else {
+                        part[rows * D + 2 * row] = m[r];
+                        part[rows * D + 2 * row + 1] = lsum;
+                    }
+                }
+            }
+        }
+        if (w.left == 0 && blockIdx.y == 0 && tid == 0) {
+            // the CTA that holds a unit's front joins it: the CTAs behind that hold the rest
+            int parts = 0;
+            if (!unit_end && whole_front) parts = 1 + (int)((s.tiles - w.t + w.per - 1) / w.per);
+            a.joins[blockIdx.x] = make_int4(n, h, slot, parts);
+        }
+        unit_first = false;
+    }
+}
+
+// One query row of a unit that several CTAs hold: block (c, row) adds up the parts of the unit whose front is
+// CTA c's, part p in CTA c + p.
+constexpr int kJoinThreads = 256;
+template <typename T, int D> __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnDecodeArgs a) {
+    constexpr int COLS = D / 4, GROUPS = kJoinThreads / COLS;
+    __shared__ float4 acc[GROUPS][COLS];
+    __shared__ float tops[GROUPS], totals[GROUPS];
+    await_previous();
+    const int4 j = a.joins[blockIdx.x];
+    if (j.w < 2) return;
+    const int rows = a.d.grp * a.tokens, row = blockIdx.y, tid = threadIdx.x, group = tid / COLS, col = tid % COLS;
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p = group; p < j.w; p += GROUPS) {
+        const float *part = attn_part(a, blockIdx.x + p, p == 0 ? j.z : 0);
+        const float pm = part[rows * D + 2 * row], pl = part[rows * D + 2 * row + 1];
+        const float4 po = *reinterpret_cast<const float4 *>(part + row * D + col * 4);
+        const float nm = fmaxf(m, pm), ref = nm == -INFINITY ? 0.f : nm;
+        const float fa = exp2_fast(m - ref), fb = exp2_fast(pm - ref);
+        l = l * fa + pl * fb;
+        o = make_float4(o.x * fa + po.x * fb, o.y * fa + po.y * fb, o.z * fa + po.z * fb, o.w * fa + po.w * fb);
+        m = nm;
+    }
+    acc[group][col] = o;
+    if (col == 0) {
+        tops[group] = m;
+        totals[group] = l;
+    }
+    __syncthreads();
+    if (group != 0) return;
+    for (int g = 1; g < GROUPS; ++g) {
+        const float pm = tops[g], pl = totals[g];
+        const float4 po = acc[g][col];
+        const float nm = fmaxf(m, pm), ref = nm == -INFINITY ? 0.f : nm;
+        const float fa = exp2_fast(m - ref), fb = exp2_fast(pm - ref);
+        l = l * fa + pl * fb;
+        o = make_float4(o.x * fa + po.x * fb, o.y * fa + po.y * fb, o.z * fa + po.z * fb, o.w * fa + po.w * fb);
+        m = nm;
+    }
+    const long long orow = ((long long)j.x * a.tokens + row / a.d.grp) * a.d.hq + j.y * a.d.grp + row % a.d.grp;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    store4f((T *)a.out + orow * D + col * 4, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+    if (col == 0 && a.lse) a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+template <typename T, int D, int RPW> cudaError_t run_simt(const AttnDecodeArgs &a, cudaStream_t s) {
+    constexpr int RB = kSimtThreads / 32 * RPW, smem = (kSimtTile * (D + 4) + kSimtTile * D + RB * D) * 4;
+    const auto kernel = attn_decode_simt_kernel<T, D, RPW>;
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
+    const int rows = a.d.grp * a.tokens;
+    kernel<<<dim3(a.ctas, (rows + RB - 1) / RB), kSimtThreads, smem, s>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_early(attn_join_kernel<T, D>, dim3(a.ctas, rows), kJoinThreads, 0, s, a);
+}
+template <typename T, int D> cudaError_t run_rows(const AttnDecodeArgs &a, cudaStream_t s) {
+    const int rows = a.d.grp * a.tokens;
+    return rows <= 8 ? run_simt<T, D, 1>(a, s) : rows <= 16 ? run_simt<T, D, 2>(a, s) : run_simt<T, D, 4>(a, s);
+}
+template <typename T> cudaError_t run_dim(const AttnDecodeArgs &a, cudaStream_t s) {
+    return a.d.D == 64 ? run_rows<T, 64>(a, s) : a.d.D == 128 ? run_rows<T, 128>(a, s) : run_rows<T, 256>(a, s);
+}
+
+}  // namespace
+
+size_t attn_decode_ws_bytes(const AttnDims &d, int rows) {
+    return (size_t)sm_count() * kAttnCtasPerSm * (sizeof(int4) + 2 * (size_t)attn_part_floats(rows, d.D) * 4);
+}
+
+void attn_decode_carve(AttnDecodeArgs &a, void *ws) {
+    a.ctas = sm_count() * kAttnCtasPerSm;
+    a.joins = (int4 *)ws;
+    a.parts = (float *)(a.joins + a.ctas);
+}
+
+cudaError_t launch_attn_decode(const AttnDecodeArgs &a, bool act_bf16, cudaStream_t s) {
+    return act_bf16 ? run_dim<__nv_bfloat16>(a, s) : run_dim<float>(a, s);
+}
+
+}  // namespace gdn

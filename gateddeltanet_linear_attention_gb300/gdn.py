@@ -19,7 +19,7 @@ from . import build_lib
 
 GDN_BF16, GDN_FP32 = 0, 1
 GDN_FLAG_L2NORM_QK = 1
-DEVERR_CU_SEQLENS, DEVERR_SLOT, DEVERR_TIMEOUT = 1, 2, 4
+DEVERR_CU_SEQLENS, DEVERR_SLOT, DEVERR_TIMEOUT, DEVERR_PAGE = 1, 2, 4, 8
 STATUS = {0: "GDN_OK", 1: "GDN_ERR_INVALID_ARG", 2: "GDN_ERR_UNSUPPORTED",
           3: "GDN_ERR_WORKSPACE", 4: "GDN_ERR_CUDA", 5: "GDN_ERR_DEVICE"}
 
@@ -86,6 +86,38 @@ class BlockNormIO(ctypes.Structure):
                 ("dw_post", ctypes.c_void_p), ("dw_pre", ctypes.c_void_p)]
 
 
+class AttnConfig(ctypes.Structure):
+    _fields_ = [("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("page_size", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("n_rows", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+
+
+class AttnPrepIO(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("ld_q", ctypes.c_int64), ("hs_q", ctypes.c_int64),
+                ("k", ctypes.c_void_p), ("ld_k", ctypes.c_int64), ("hs_k", ctypes.c_int64),
+                ("v", ctypes.c_void_p), ("ld_v", ctypes.c_int64), ("hs_v", ctypes.c_int64),
+                ("T", ctypes.c_int64), ("w_q", ctypes.c_void_p), ("w_k", ctypes.c_void_p),
+                ("weight_offset", ctypes.c_float), ("eps", ctypes.c_float),
+                ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("inv_freq", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("cu_seqlens", ctypes.c_void_p), ("n_seqs", ctypes.c_int32),
+                ("rows", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p),
+                ("q_out", ctypes.c_void_p), ("k_out", ctypes.c_void_p),
+                ("dq_out", ctypes.c_void_p), ("dk_out", ctypes.c_void_p),
+                ("dq", ctypes.c_void_p), ("ld_dq", ctypes.c_int64), ("hs_dq", ctypes.c_int64),
+                ("dk", ctypes.c_void_p), ("ld_dk", ctypes.c_int64), ("hs_dk", ctypes.c_int64),
+                ("dw_q", ctypes.c_void_p), ("dw_k", ctypes.c_void_p)]
+
+
+class AttnDecodeIO(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("ld_q", ctypes.c_int64), ("hs_q", ctypes.c_int64),
+                ("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("rows", ctypes.c_void_p),
+                ("n_seqs", ctypes.c_int32), ("tokens", ctypes.c_int32), ("window", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p)]
+
+
 _lib = None
 _lock = threading.Lock()
 LIB_PATH = build_lib.LIB
@@ -143,6 +175,16 @@ def load(path: str | None = None):
             "gdn_block_norm": ([ctypes.POINTER(BlockNormIO), V], I32),
             "gdn_block_norm_workspace_size": ([I64, I32], SZ),
             "gdn_block_norm_backward": ([ctypes.POINTER(BlockNormIO), P, SZ, V], I32),
+            "gdn_attn_prep": ([ctypes.POINTER(AttnConfig), ctypes.POINTER(AttnPrepIO), V], I32),
+            "gdn_attn_prep_workspace_size": ([ctypes.POINTER(AttnConfig), I64], SZ),
+            "gdn_attn_prep_backward": ([ctypes.POINTER(AttnConfig), ctypes.POINTER(AttnPrepIO), P, SZ, V], I32),
+            "gdn_attn_workspace_size": ([ctypes.POINTER(AttnConfig), I32, I32], SZ),
+            "gdn_attn_decode": ([ctypes.POINTER(AttnConfig), ctypes.POINTER(AttnDecodeIO), P, SZ, V], I32),
+            "gdn_page_workspace_size": ([ctypes.POINTER(AttnConfig), I32], SZ),
+            "gdn_page_resize": ([ctypes.POINTER(AttnConfig), P, P, P, P, P, I32, P, P, P, P, SZ, V], I32),
+            "gdn_page_fork": ([ctypes.POINTER(AttnConfig), P, P, P, P, P, I32, V], I32),
+            "gdn_page_compact": ([ctypes.POINTER(AttnConfig), P, P, P, P, P, P, P, I32, P, SZ, V], I32),
+            "gdn_page_copy": ([ctypes.POINTER(AttnConfig), P, P, I32, P, P, I32, P, P, I32, V], I32),
             "gdn_device_error": ([V, ctypes.POINTER(U32)], I32),
             "gdn_debug_set_wait": ([ctypes.c_uint64, U32], I32),
             "gdn_status_string": ([I32], ctypes.c_char_p),
@@ -461,6 +503,20 @@ class _Args:
             ld = shape[1]
         return t.data_ptr(), ld
 
+    def heads(self, t, name, shape, dtype):
+        """(pointer, token stride, head stride) of a [tokens, heads, dim] view with contiguous heads."""
+        if t is None:
+            return 0, 0, 0
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != self.device:
+            self.explain(t, name, shape, dtype)
+        T, H, D = shape
+        if t.is_contiguous():
+            return t.data_ptr(), H * D, D
+        ld, hs, one = t.stride()
+        if one != 1:
+            self.refuse(name, "has heads that are not contiguous")
+        return t.data_ptr(), ld if T > 1 else H * D, hs if H > 1 else D
+
     def whole(self, t, name, shape, dtype):
         """Pointer of a contiguous tensor."""
         if t is None:
@@ -604,6 +660,164 @@ def gdn_block_norm_backward(res_out, rstd_pre=None, w_pre=None, dh=None, d_res_o
     ws, ws_bytes = a.bytes_of(workspace)
     _check((_lib or load()).gdn_block_norm_backward(ctypes.byref(io), ws, ws_bytes, a.stream(stream)),
            "gdn_block_norm_backward")
+
+
+# ------------------------------------------------- attention layers and their cache
+
+def make_attn_config(q_heads, kv_heads, head_dim, page_size=64, act="bf16", n_pages=0, n_rows=0,
+                     max_pages=0) -> AttnConfig:
+    return AttnConfig(q_heads, kv_heads, head_dim, GDN_BF16 if act == "bf16" else GDN_FP32, page_size, n_pages,
+                      n_rows, max_pages)
+
+
+_prep_io, _decode_io = _packer(AttnPrepIO), _packer(AttnDecodeIO)
+
+
+def _prep_batch(a, T, cu_seqlens, tokens):
+    """(pointer of cu_seqlens, sequences): packed by bounds, or `tokens` to each sequence (None: one sequence)."""
+    if cu_seqlens is not None:
+        if tokens is not None:
+            a.refuse("tokens", "and cu_seqlens are both given")
+        n = cu_seqlens.shape[0] - 1
+        return a.whole(cu_seqlens, "cu_seqlens", (n + 1,), a.i32), n
+    if tokens is None:
+        return 0, 1
+    if tokens < 1 or T % tokens:
+        a.refuse("q", "holds %d tokens, not a multiple of tokens=%s" % (T, tokens))
+    return 0, T // tokens
+
+
+def _pools(a, cfg, k_pages, v_pages):
+    shape = (cfg.kv_heads, cfg.page_size, cfg.head_dim)
+    return a.pool(k_pages, "k_pages", cfg.n_pages, shape, a.act), a.pool(v_pages, "v_pages", cfg.n_pages, shape, a.act)
+
+
+def gdn_attn_prep(cfg, q, k, q_out, inv_freq, k_out=None, v=None, k_pages=None, v_pages=None, page_table=None, lens=None,
+                  rows=None, cu_seqlens=None, tokens=None, positions=None, w_q=None, w_k=None, weight_offset=0.0, eps=1e-6,
+                  interleaved=False, stream=None):
+    """q [T, q_heads, head_dim], k and v [T, kv_heads, head_dim] (views) -> q_out [T, q_heads, head_dim], and k_out or the
+    pools' places of the new tokens.  inv_freq: fp32 [rotary_dim / 2] or None.  The batch is packed by cu_seqlens, or has
+    `tokens` tokens a sequence; lens counts them already.  k may be None."""
+    a = _Args("gdn_attn_prep", cfg.act)
+    T, Hq, Hk, D = q.shape[0], cfg.q_heads, cfg.kv_heads, cfg.head_dim
+    cu, n = _prep_batch(a, T, cu_seqlens, tokens)
+    half = 0 if inv_freq is None else inv_freq.shape[0]
+    io = _prep_io(*a.heads(q, "q", (T, Hq, D), a.act), *a.heads(k, "k", (T, Hk, D), a.act), *a.heads(v, "v", (T, Hk, D), a.act), T,
+                  a.whole(w_q, "w_q", (D,), a.f32), a.whole(w_k, "w_k", (D,), a.f32), weight_offset, eps, 2 * half,
+                  1 if interleaved else 0, a.whole(inv_freq, "inv_freq", (half,), a.f32),
+                  a.whole(positions, "positions", (T,), a.i32), cu, n, a.whole(rows, "rows", (n,), a.i32),
+                  a.whole(lens, "lens", (cfg.n_rows,), a.i32),
+                  a.whole(page_table, "page_table", (cfg.n_rows, cfg.max_pages), a.i32), *_pools(a, cfg, k_pages, v_pages),
+                  a.whole(q_out, "q_out", (T, Hq, D), a.act), a.whole(k_out, "k_out", (T, Hk, D), a.act),
+                  0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
+    _check((_lib or load()).gdn_attn_prep(ctypes.byref(cfg), ctypes.byref(io), a.stream(stream)), "gdn_attn_prep")
+
+
+def gdn_attn_prep_workspace_size(cfg, max_tokens) -> int:
+    return load().gdn_attn_prep_workspace_size(ctypes.byref(cfg), max_tokens)
+
+
+def gdn_attn_prep_backward(cfg, q, k, dq_out, dk_out, inv_freq, dq=None, dk=None, dw_q=None, dw_k=None, w_q=None, w_k=None,
+                           weight_offset=0.0, eps=1e-6, interleaved=False, cu_seqlens=None, tokens=None, positions=None,
+                           workspace=None, stream=None):
+    """Gradients of gdn_attn_prep (without a cache) for sum(dq_out * q_out) + sum(dk_out * k_out): dq and dk (views), dw_q and
+    dw_k fp32 [head_dim], each of which may be None."""
+    a = _Args("gdn_attn_prep_backward", cfg.act)
+    T, Hq, Hk, D = q.shape[0], cfg.q_heads, cfg.kv_heads, cfg.head_dim
+    cu, n = _prep_batch(a, T, cu_seqlens, tokens)
+    half = 0 if inv_freq is None else inv_freq.shape[0]
+    io = _prep_io(*a.heads(q, "q", (T, Hq, D), a.act), *a.heads(k, "k", (T, Hk, D), a.act), 0, 0, 0, T,
+                  a.whole(w_q, "w_q", (D,), a.f32), a.whole(w_k, "w_k", (D,), a.f32), weight_offset, eps, 2 * half,
+                  1 if interleaved else 0, a.whole(inv_freq, "inv_freq", (half,), a.f32),
+                  a.whole(positions, "positions", (T,), a.i32), cu, n, 0, 0, 0, 0, 0, 0, 0,
+                  a.whole(dq_out, "dq_out", (T, Hq, D), a.act), a.whole(dk_out, "dk_out", (T, Hk, D), a.act),
+                  *a.heads(dq, "dq", (T, Hq, D), a.act), *a.heads(dk, "dk", (T, Hk, D), a.act),
+                  a.whole(dw_q, "dw_q", (D,), a.f32), a.whole(dw_k, "dw_k", (D,), a.f32))
+    ws, ws_bytes = a.bytes_of(workspace)
+    _check((_lib or load()).gdn_attn_prep_backward(ctypes.byref(cfg), ctypes.byref(io), ws, ws_bytes, a.stream(stream)),
+           "gdn_attn_prep_backward")
+
+
+def gdn_attn_workspace_size(cfg, max_seqs, tokens=1) -> int:
+    return load().gdn_attn_workspace_size(ctypes.byref(cfg), max_seqs, tokens)
+
+
+def gdn_attn_decode(cfg, q, k_pages, v_pages, page_table, lens, out, workspace, tokens=1, rows=None, window=0, scale=None,
+                    lse=None, stream=None):
+    """Attention of the last `tokens` tokens of each sequence: q [n * tokens, q_heads, head_dim] (a view) -> out of that shape,
+    lse fp32 [n * tokens, q_heads] or None.  scale None: head_dim ** -0.5."""
+    a = _Args("gdn_attn_decode", cfg.act)
+    T, Hq, D = q.shape[0], cfg.q_heads, cfg.head_dim
+    n = T // tokens if tokens > 0 else 0
+    if n * tokens != T:
+        a.refuse("q", "holds %d tokens, not a multiple of tokens=%s" % (T, tokens))
+    io = _decode_io(*a.heads(q, "q", (T, Hq, D), a.act), *_pools(a, cfg, k_pages, v_pages),
+                    a.whole(page_table, "page_table", (cfg.n_rows, cfg.max_pages), a.i32),
+                    a.whole(lens, "lens", (cfg.n_rows,), a.i32), a.whole(rows, "rows", (n,), a.i32), n, tokens, window,
+                    D ** -0.5 if scale is None else scale, a.whole(out, "out", (T, Hq, D), a.act),
+                    a.whole(lse, "lse", (T, Hq), a.f32))
+    ws, ws_bytes = a.bytes_of(workspace)
+    _check((_lib or load()).gdn_attn_decode(ctypes.byref(cfg), ctypes.byref(io), ws, ws_bytes, a.stream(stream)), "gdn_attn_decode")
+
+
+def gdn_page_workspace_size(cfg, max_lanes) -> int:
+    return load().gdn_page_workspace_size(ctypes.byref(cfg), max_lanes)
+
+
+def _page_state(a, cfg, page_table, lens, refs):
+    return (a.whole(page_table, "page_table", (cfg.n_rows, cfg.max_pages), a.i32), a.whole(lens, "lens", (cfg.n_rows,), a.i32),
+            a.whole(refs, "refs", (cfg.n_pages,), a.i32))
+
+
+def gdn_page_resize(cfg, page_table, lens, refs, rows, new_lens, granted, src_idx, dst_idx, workspace, stream=None):
+    """Sets the lengths of `rows` to new_lens: pages taken, let go, or replaced by copies (src_idx -> dst_idx, to be carried out
+    with gdn_page_copy before they are written and before the next resize).  granted: the lengths after the call."""
+    a = _Args("gdn_page_resize")
+    n = rows.shape[0]
+    lane = ((n,), a.i32)
+    state = _page_state(a, cfg, page_table, lens, refs)
+    ws, ws_bytes = a.bytes_of(workspace)
+    _check((_lib or load()).gdn_page_resize(
+        ctypes.byref(cfg), *state, a.whole(rows, "rows", *lane), a.whole(new_lens, "new_lens", *lane), n,
+        a.whole(granted, "granted", *lane), a.whole(src_idx, "src_idx", *lane), a.whole(dst_idx, "dst_idx", *lane), ws, ws_bytes,
+        a.stream(stream)), "gdn_page_resize")
+
+
+def gdn_page_fork(cfg, page_table, lens, refs, src_rows, dst_rows, stream=None):
+    """Empty rows dst_rows become copies of src_rows that share their pages."""
+    a = _Args("gdn_page_fork")
+    n = dst_rows.shape[0]
+    _check((_lib or load()).gdn_page_fork(
+        ctypes.byref(cfg), *_page_state(a, cfg, page_table, lens, refs), a.whole(src_rows, "src_rows", (n,), a.i32),
+        a.whole(dst_rows, "dst_rows", (n,), a.i32), n, a.stream(stream)), "gdn_page_fork")
+
+
+def gdn_page_compact(cfg, page_table, lens, refs, table_out, refs_out, src_idx, dst_idx, workspace, stream=None):
+    """Plans the moves of held pages to the lowest places (src_idx -> dst_idx, -1 behind the last) and writes the table and the
+    counts after them; table_out may be page_table, refs_out refs."""
+    a = _Args("gdn_page_compact")
+    n = src_idx.shape[0]
+    state = _page_state(a, cfg, page_table, lens, refs)
+    ws, ws_bytes = a.bytes_of(workspace)
+    _check((_lib or load()).gdn_page_compact(
+        ctypes.byref(cfg), *state, a.whole(table_out, "table_out", (cfg.n_rows, cfg.max_pages), a.i32),
+        a.whole(refs_out, "refs_out", (cfg.n_pages,), a.i32), a.whole(src_idx, "src_idx", (n,), a.i32),
+        a.whole(dst_idx, "dst_idx", (n,), a.i32), n, ws, ws_bytes, a.stream(stream)), "gdn_page_compact")
+
+
+def gdn_page_copy(cfg, src_k, src_v, dst_k, dst_v, src_idx, dst_idx, stream=None):
+    """Pages src_idx[i] of the src pools to pages dst_idx[i] of the dst pools (src < 0: zeros, dst < 0: nothing); the pools
+    may be the same, and have as many pages as their first dimension says."""
+    a = _Args("gdn_page_copy", cfg.act)
+    shape = (cfg.kv_heads, cfg.page_size, cfg.head_dim)
+    n = dst_idx.shape[0]
+
+    def pages(*ts):
+        return min([t.shape[0] for t in ts if t is not None] or [0])
+    _check((_lib or load()).gdn_page_copy(
+        ctypes.byref(cfg), a.pool(src_k, "src_k", 0, shape, a.act), a.pool(src_v, "src_v", 0, shape, a.act), pages(src_k, src_v),
+        a.pool(dst_k, "dst_k", 0, shape, a.act), a.pool(dst_v, "dst_v", 0, shape, a.act), pages(dst_k, dst_v),
+        a.whole(src_idx, "src_idx", (n,), a.i32), a.whole(dst_idx, "dst_idx", (n,), a.i32), n, a.stream(stream)), "gdn_page_copy")
 
 
 def gdn_device_error(stream=None) -> int:

@@ -83,6 +83,7 @@ typedef enum gdn_dtype { GDN_BF16 = 0, GDN_FP32 = 1 } gdn_dtype;
 #define GDN_DEVERR_CU_SEQLENS 1u   /* cu_seqlens not monotone or beyond T */
 #define GDN_DEVERR_SLOT 2u         /* state_idx entry >= n_slots */
 #define GDN_DEVERR_TIMEOUT 4u      /* a bounded device wait gave up */
+#define GDN_DEVERR_PAGE 8u         /* a page, a length or a position out of range */
 
 /* Flags for gdn_chunk_prefill / gdn_recurrent_decode. */
 #define GDN_FLAG_L2NORM_QK 1u      /* normalise q and k in the kernel (and apply q_scale) */
@@ -518,6 +519,176 @@ gdn_status gdn_block_norm(const gdn_block_norm_io *io, void *stream);
 size_t gdn_block_norm_workspace_size(int64_t rows, int32_t dim);
 gdn_status gdn_block_norm_backward(const gdn_block_norm_io *io, void *workspace, size_t workspace_bytes,
                                    void *stream);
+
+/* ------------------------------------------------------------------------
+ * Full-attention layers of a hybrid model, beside its recurrent mixers: norms
+ * of queries and keys with the position rotation, attention of new tokens over
+ * a paged key-value cache, and the cache's pages.  (haskell-infer-demo README,
+ * "Architecture", kernels/flashinfer_norm.cu: norm and partial rotation of
+ * queries and keys; hyperflare core-design names the paged KV write.  The
+ * pages print no formulas; the forms below are the standard statement.)
+ *
+ * The cache.  K and V pools: act [n_pages][kv_heads][page_size][head_dim] each,
+ * 16-byte aligned.  page_table: int32 [n_rows][max_pages], lens: int32 [n_rows];
+ * token i of the sequence in row r is token i % page_size of page
+ * page_table[r][i / page_size], i < lens[r].  Entries behind a row's last page
+ * (and in front of a window) are not read.  Rows may share pages.  rows (nullable, int32 [n_seqs]) maps
+ * sequence n to a row as state_idx does to a slot: NULL means row n, a negative
+ * entry is a padding lane.  One table serves the pools of all layers.
+ *
+ * Device-side faults: a row >= n_rows is reported as GDN_DEVERR_SLOT and its
+ * lane treated as padding.  A length above max_pages * page_size (the
+ * sequence is then treated as padding), and a page outside [0, n_pages)
+ * (its tokens are neither read nor written, and count as masked) are
+ * reported as GDN_DEVERR_PAGE. */
+typedef struct gdn_attn_config {
+    int32_t q_heads, kv_heads;   /* q_heads % kv_heads == 0, at most 16 query heads a key head */
+    int32_t head_dim;            /* 64, 128 or 256 */
+    gdn_dtype act;               /* q, k, v, outputs, pools */
+    int32_t page_size;           /* tokens of a page: 16, 32, 64 or 128 */
+    int32_t n_pages;             /* pages of each pool (capacity); 0: no cache */
+    int32_t n_rows;              /* rows of the page table, at most 65535 */
+    int32_t max_pages;           /* columns of the page table */
+} gdn_attn_config;
+
+/* Norms and rotation of a packed batch's queries and keys, and its keys' and
+ * values' way into the cache.  Per head vector x of q or k, w^ = weight_offset + w:
+ *
+ *   n = x / sqrt(mean(x^2) + eps) * w^          (w NULL: n = x)
+ *   a' = a cos(p f_i) - b sin(p f_i),  b' = b cos(p f_i) + a sin(p f_i)
+ *
+ * for the pairs (a, b) = (n[i], n[i + R/2]), or with `interleaved` (n[2i],
+ * n[2i+1]), i < R/2, R = rotary_dim, f = inv_freq; columns from R on pass.
+ * The angle is taken from the exact product p f_i (while it is below 10^8), the
+ * rest in 32 bits, one rounding at the end.
+ *
+ * Sequence n has tokens cu_seqlens[n] .. cu_seqlens[n+1]-1, or T / n_seqs tokens
+ * where cu_seqlens is NULL (decode and verification batches).  Its j-th of L has
+ * index lens[row] - L + j in its sequence: lens already counts the new tokens
+ * (gdn_page_resize sets it).  lens NULL: index j.  Its position p is
+ * positions[t] (0 <= p < 2^24; negative: a padding token) or, NULL, its index.
+ * With pools, its k' and v go to its index's place in the cache.
+ * Padding lanes and tokens have zero q_out and k_out and store nothing; a token
+ * whose index is negative or whose position is too large as well, reported as
+ * GDN_DEVERR_PAGE.  Rows behind cu_seqlens[n_seqs] are left as they are.
+ * Two tokens with one place in the cache (rows that share it) race. */
+typedef struct gdn_attn_prep_io {
+    const void *q; int64_t ld_q, hs_q;   /* [T] tokens at ld_q, heads at hs_q elements: multiples of 8 */
+    const void *k; int64_t ld_k, hs_k;   /* NULL: queries only (then no k_out, pools or k gradients) */
+    const void *v; int64_t ld_v, hs_v;   /* given exactly when the pools are */
+    int64_t T;
+    const float *w_q, *w_k;              /* [head_dim] or NULL */
+    float weight_offset, eps;
+    int32_t rotary_dim, interleaved;     /* rotary_dim even, 0 .. head_dim */
+    const float *inv_freq;               /* [rotary_dim / 2]; NULL when rotary_dim is 0 */
+    const int32_t *positions;            /* [T] or NULL */
+    const int32_t *cu_seqlens;           /* [n_seqs + 1] or NULL */
+    int32_t n_seqs;
+    const int32_t *rows, *lens, *page_table;  /* lens, page_table: with the pools (lens also without) */
+    void *k_pages, *v_pages;             /* pools, or both NULL */
+    void *q_out;                         /* [T][q_heads * head_dim], 16-byte aligned as the next */
+    void *k_out;                         /* [T][kv_heads * head_dim] or NULL */
+    /* backward only (v, pools, q_out, k_out, rows, lens and page_table are not used) */
+    const void *dq_out, *dk_out;         /* [T][heads * head_dim]: gradients of q_out and k_out */
+    void *dq; int64_t ld_dq, hs_dq;      /* gradients of q and k, strided as they may be, or NULL */
+    void *dk; int64_t ld_dk, hs_dk;
+    float *dw_q, *dw_k;                  /* [head_dim], summed over tokens and heads, or NULL */
+} gdn_attn_prep_io;
+
+gdn_status gdn_attn_prep(const gdn_attn_config *cfg, const gdn_attn_prep_io *io, void *stream);
+
+/* Gradients for the loss sum(dq_out * q_out) + sum(dk_out * k_out); padding
+ * tokens have zero gradients, rows behind the last sequence are left and add
+ * nothing.  `workspace` of gdn_attn_prep_workspace_size(cfg, T) bytes, 16-byte
+ * aligned, where a weight gradient is asked for.  Sums are taken in a fixed
+ * order: equal calls give equal bits.  dq may be dq_out, and dk dk_out. */
+size_t gdn_attn_prep_workspace_size(const gdn_attn_config *cfg, int64_t max_tokens);
+gdn_status gdn_attn_prep_backward(const gdn_attn_config *cfg, const gdn_attn_prep_io *io, void *workspace,
+                                  size_t workspace_bytes, void *stream);
+
+/* Attention of the last `tokens` (1..8) tokens of each sequence over its cache,
+ * themselves among it.  Token j of sequence n (row n * tokens + j of q and out)
+ * sees the tokens i < e = lens[row] - tokens + j + 1, and with a window only
+ * those with i >= e - window:
+ *
+ *   out = sum_i softmax_i(scale q . k_i) v_i        lse = log sum_i exp(scale q . k_i)
+ *
+ * with query head h reading key head h / (q_heads / kv_heads).  Without a token
+ * to see, out is 0 and lse -inf.  What is masked may hold anything: a value that
+ * is not finite reaches the rows that see it and no others.  Sums and softmax
+ * statistics are 32 bits.  The sequences' cache is split over the GPU by what
+ * `lens` says at run time; `workspace` of gdn_attn_workspace_size(cfg, n_seqs,
+ * tokens) bytes, 16-byte aligned, holds the parts between the two kernels of a
+ * call and nothing between calls. */
+typedef struct gdn_attn_decode_io {
+    const void *q; int64_t ld_q, hs_q;   /* [n_seqs * tokens] tokens, strides as for gdn_attn_prep */
+    const void *k_pages, *v_pages;
+    const int32_t *page_table, *lens, *rows;  /* rows may be NULL */
+    int32_t n_seqs, tokens;
+    int32_t window;                      /* 0: all tokens */
+    float scale;
+    void *out;                           /* [n_seqs * tokens][q_heads * head_dim] */
+    float *lse;                          /* [n_seqs * tokens][q_heads] or NULL */
+} gdn_attn_decode_io;
+
+size_t gdn_attn_workspace_size(const gdn_attn_config *cfg, int32_t max_seqs, int32_t tokens);
+gdn_status gdn_attn_decode(const gdn_attn_config *cfg, const gdn_attn_decode_io *io, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
+/* The cache's pages, kept on the device so that a serving step with its
+ * allocation is one graph.  refs: int32 [n_pages], how many rows hold a page;
+ * 0: free.  A row holds ceil(lens / page_size) pages, the first entries of its
+ * table row; the calls set entries that end to -1.  A lane is one entry of
+ * `rows`; a negative row is an inactive lane.  Rows named twice in a call are
+ * skipped in all their lanes and reported as GDN_DEVERR_SLOT.  Pages are taken
+ * lowest index first, in lane order, from those free when the call starts.
+ *
+ * gdn_page_resize: sets the length of rows[i] to new_lens[i] (negative: an
+ * inactive lane).  A longer row takes pages; if its last page is in part filled
+ * and held by another row as well, a new page takes that one's place, and the
+ * copy to carry out (gdn_page_copy, in every layer's pools, before they are
+ * written and before the next resize) is src_idx[i] -> dst_idx[i], else both are
+ * -1.  A shorter row lets
+ * pages go; 0 frees it.  granted[i]: the row's length after the call (-1: an
+ * inactive lane).  When the free pages do not reach, the lanes that need pages
+ * from the first one on that cannot have all of its own stay as they are.  A
+ * length above max_pages * page_size is reported as GDN_DEVERR_PAGE and the
+ * lane stays as it is.  granted, src_idx, dst_idx: int32 [n].
+ *
+ * gdn_page_fork: row dst_rows[i] becomes a copy of row src_rows[i] that shares
+ * its pages.  It must be empty (lens 0), and no other lane's source or
+ * destination; else the lane is skipped and GDN_DEVERR_SLOT reported.  Many
+ * lanes may have one source.
+ *
+ * gdn_page_compact: moves pages to the lowest places: the k-th free page below
+ * the number of held pages takes the k-th held page above it, k < n.  Writes
+ * the moves (src_idx, dst_idx: int32 [n], -1 behind the last), the counts and
+ * the whole table after them; refs_out may be refs, table_out page_table.
+ * gdn_page_copy then moves the data: no page is both source and destination.
+ *
+ * `workspace` of gdn_page_workspace_size(cfg, n) bytes, 16-byte aligned. */
+size_t gdn_page_workspace_size(const gdn_attn_config *cfg, int32_t max_lanes);
+gdn_status gdn_page_resize(const gdn_attn_config *cfg, int32_t *page_table, int32_t *lens, int32_t *refs,
+                           const int32_t *rows, const int32_t *new_lens, int32_t n, int32_t *granted,
+                           int32_t *src_idx, int32_t *dst_idx, void *workspace, size_t workspace_bytes,
+                           void *stream);
+gdn_status gdn_page_fork(const gdn_attn_config *cfg, int32_t *page_table, int32_t *lens, int32_t *refs,
+                         const int32_t *src_rows, const int32_t *dst_rows, int32_t n, void *stream);
+gdn_status gdn_page_compact(const gdn_attn_config *cfg, const int32_t *page_table, const int32_t *lens,
+                            const int32_t *refs, int32_t *table_out, int32_t *refs_out, int32_t *src_idx,
+                            int32_t *dst_idx, int32_t n, void *workspace, size_t workspace_bytes,
+                            void *stream);
+
+/* Pages copied bit for bit as gdn_state_copy copies slots: page src_idx[i] of
+ * the src pools to page dst_idx[i] of the dst pools (a negative destination is
+ * an inactive lane, a negative source or a NULL source pool zeroes).  dst_v NULL
+ * leaves the V pool, dst_k NULL the K pool.  Pools may be the same; then no page
+ * may be a source and a destination of one call, and destinations are distinct.
+ * An index out of [.., n_src) or [.., n_dst) is reported as GDN_DEVERR_PAGE and
+ * its lane skipped. */
+gdn_status gdn_page_copy(const gdn_attn_config *cfg, const void *src_k, const void *src_v, int32_t n_src,
+                         void *dst_k, void *dst_v, int32_t n_dst, const int32_t *src_idx,
+                         const int32_t *dst_idx, int32_t n, void *stream);
 
 /* Bounded waits (no page counterpart: it makes the device-side timeout
  * testable without a GPU fault).  Every wait of a kernel on another part of
