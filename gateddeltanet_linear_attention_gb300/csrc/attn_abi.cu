@@ -162,6 +162,7 @@ gdn_status gdn_attn_decode(const gdn_attn_config *cfg, const gdn_attn_decode_io 
     a.n_seqs = io->n_seqs; a.tokens = io->tokens; a.window = io->window;
     a.scale_log2 = io->scale * gdn::kLog2e;
     a.out = io->out; a.lse = io->lse; a.wait_ns = gdn::wait_limit_ns();
+    a.lose = gdn::lost_copies();
     gdn::attn_decode_carve(a, workspace);
     return launch_status(gdn::launch_attn_decode(a, cfg->act == GDN_BF16, (cudaStream_t)stream));
 }

@@ -44,7 +44,8 @@ struct AttnDecodeArgs {
     float *lse;
     AttnDims d;
     unsigned *err;
-    unsigned long long wait_ns;
+    unsigned long long wait_ns;       // limit of bounded waits, and the copies that a test drops
+    unsigned lose;
     // workspace: what CTA c leaves of a unit that it does not hold whole, in slot 0 where that unit is its
     // first one, else 1: rows x D sums, then rows x (m, l), m in powers of two; and the join kernel's for CTA c
     float *parts;                     // [ctas][2][attn_part_floats]
@@ -192,4 +193,6 @@ cudaError_t launch_attn_prep_backward(const AttnPrepArgs &a, bool act_bf16, cuda
 size_t attn_decode_ws_bytes(const AttnDims &d, int rows);
 void attn_decode_carve(AttnDecodeArgs &a, void *ws);
 cudaError_t launch_attn_decode(const AttnDecodeArgs &a, bool act_bf16, cudaStream_t s);
+cudaError_t launch_attn_decode_tc(const AttnDecodeArgs &a, cudaStream_t s);
+cudaError_t launch_attn_join(const AttnDecodeArgs &a, bool act_bf16, cudaStream_t s);
 }  // namespace gdn

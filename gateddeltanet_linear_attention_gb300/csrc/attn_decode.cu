@@ -238,7 +238,7 @@ template <typename T, int D, int RPW> cudaError_t run_simt(const AttnDecodeArgs 
     kernel<<<dim3(a.ctas, (rows + RB - 1) / RB), kSimtThreads, smem, s>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_early(attn_join_kernel<T, D>, dim3(a.ctas, rows), kJoinThreads, 0, s, a);
+    return launch_attn_join(a, sizeof(T) == 2, s);
 }
 template <typename T, int D> cudaError_t run_rows(const AttnDecodeArgs &a, cudaStream_t s) {
     const int rows = a.d.grp * a.tokens;
@@ -260,8 +260,19 @@ void attn_decode_carve(AttnDecodeArgs &a, void *ws) {
     a.parts = (float *)(a.joins + a.ctas);
 }
 
+cudaError_t launch_attn_join(const AttnDecodeArgs &a, bool act_bf16, cudaStream_t s) {
+    const dim3 grid(a.ctas, a.d.grp * a.tokens);
+    if (act_bf16)
+        return a.d.D == 64 ? launch_early(attn_join_kernel<__nv_bfloat16, 64>, grid, kJoinThreads, 0, s, a)
+             : a.d.D == 128 ? launch_early(attn_join_kernel<__nv_bfloat16, 128>, grid, kJoinThreads, 0, s, a)
+                            : launch_early(attn_join_kernel<__nv_bfloat16, 256>, grid, kJoinThreads, 0, s, a);
+    return a.d.D == 64 ? launch_early(attn_join_kernel<float, 64>, grid, kJoinThreads, 0, s, a)
+         : a.d.D == 128 ? launch_early(attn_join_kernel<float, 128>, grid, kJoinThreads, 0, s, a)
+                        : launch_early(attn_join_kernel<float, 256>, grid, kJoinThreads, 0, s, a);
+}
+
 cudaError_t launch_attn_decode(const AttnDecodeArgs &a, bool act_bf16, cudaStream_t s) {
-    return act_bf16 ? run_dim<__nv_bfloat16>(a, s) : run_dim<float>(a, s);
+    return act_bf16 ? launch_attn_decode_tc(a, s) : run_dim<float>(a, s);
 }
 
 }  // namespace gdn

@@ -1,0 +1,552 @@
+// attn_decode_tc.cu -- attention of a few new tokens over a paged bf16 cache, on the tensor cores.
+//
+// The shares, parts and join of attn_decode.cu; here a tile is 64 tokens.  One warp copies tiles with TMA into a ring of
+// shared-memory entries (K and V of a tile in entries of their own, 128-byte swizzled), eight warps compute in two sets
+// of four that take turns with the tiles:
+//   S = Q K^T    warp w of a set the tile's tokens 16 w .. 16 w + 15, for all query rows
+//   P = exp(S - m), the set's four warps having passed each other the rows' maxima; m, l and o in 32 bits
+//   O += P V     warp w the columns D/4 w .. of all rows, P passed through shared memory
+// so every byte of K and V is read from shared memory once, however many query rows there are.  The sets' sums are
+// added where a unit ends.
+//
+// HBM-bound by design: 16 rows of m16n8k16 products need 16 operations a byte of the cache.  (The products run as
+// mma.sync: a tcgen05 product has 64 or 128 rows, and the sums over tokens of its transposed form lie across lanes.)
+// P is split in two bf16 parts, so that o loses nothing but its own rounding; the second product is hidden behind the
+// loads.
+#include <cuda.h>
+
+#include "attn_common.cuh"
+#include "tc_sm103.cuh"
+
+namespace gdn {
+
+namespace {
+
+constexpr int kTile = 64;
+constexpr int kConsumers = 256;                    // eight warps, two sets of four
+constexpr int kThreads = kConsumers + 32;
+constexpr int kUnits = 2;                          // query blocks in flight
+constexpr int kPPitch = kTile * 2 + 16;            // bytes of a row of P: ldmatrix without bank conflicts
+constexpr int kMaxEntries = 16;
+
+// A unit's tiles in this CTA, as the copying warp describes them.
+struct Unit {
+    int n, h, len, first, i0, count, seq0, slot;   // slot -1: the unit is whole
+};
+
+template <int D, int MT> struct Smem {
+    static constexpr int entry = kTile * D * 2, q_pitch = D * 2 + 16, q_block = 16 * MT * q_pitch;
+    static constexpr int p_block = 16 * MT * kPPitch, merge = 16 * MT * D * 4;
+    static constexpr int fixed = kUnits * q_block + 4 * p_block + merge + 2 * 4 * 16 * MT * 4 * 2 + 16 * MT * 8 + 1024;
+    static constexpr int limit = 227 * 1024 - 1024;
+    static constexpr int fit = (limit - fixed) / entry;
+    // a multiple of four: an entry then serves tiles of one set alone, and no waiter is ever two phases behind its barrier
+    static constexpr int entries = fit < kMaxEntries ? fit / 4 * 4 : kMaxEntries;
+    static constexpr int bytes = fixed + entries * entry;      // 1,024 of `fixed` to align the entries
+    static_assert(entries >= 4 && entries % 4 == 0, "two tiles in flight, each set's in entries of its own");
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(threads) : "memory"); }
+__device__ __forceinline__ void bar_arrive(int id, int threads) { asm volatile("bar.arrive %0, %1;" :: "r"(id), "r"(threads) : "memory"); }
+// Whether all threads of the barrier say so.
+__device__ __forceinline__ bool bar_all(int id, int threads, bool mine) {
+    int all;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %3, 0;\n\tbar.red.and.pred q, %1, %2, p;\n\tselp.s32 %0, 1, 0, q;\n\t}\n"
+                 : "=r"(all) : "r"(id), "r"(threads), "r"((int)mine) : "memory");
+    return all != 0;
+}
+enum { kBarUnit = 1, kBarSet = 2, kBarMerge = 4 };
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+// Either half's exponent all ones.
+__device__ __forceinline__ bool not_finite2(uint32_t v) {
+    return (v & 0x7f80u) == 0x7f80u || (v & 0x7f800000u) == 0x7f800000u;
+}
+
+struct Maps {
+    CUtensorMap k, v;
+};
+
+template <int D, int MT>
+__global__ void __launch_bounds__(kThreads, 1) attn_decode_tc_kernel(const AttnDecodeArgs a, const __grid_constant__ Maps maps) {
+    using S = Smem<D, MT>;
+    constexpr int KS = D / 16, ROWS = 16 * MT, NT = D / 32;        // NT: 8-column blocks of a warp's share of O
+    constexpr uint32_t E = S::entries;
+    extern __shared__ unsigned char raw[];
+    __shared__ long long sums[33];
+    __shared__ int found[3], lost;
+    __shared__ uint64_t bars[2 * kMaxEntries + 2 * kUnits];
+    __shared__ int pieces_of[kMaxEntries];                          // which 16-token pieces of an entry's tile are there
+    __shared__ Unit units[kUnits];
+    unsigned char *base = raw + ((1024u - (tc::smem_u32(raw) & 1023u)) & 1023u);
+    unsigned char *q_mem = base + E * S::entry, *p_mem = q_mem + kUnits * S::q_block;
+    float *merge = reinterpret_cast<float *>(p_mem + 4 * S::p_block);
+    float *tops = merge + ROWS * D;                                 // [2 sets][ROWS][4 warps]
+    float *totals = tops + 2 * ROWS * 4;                            // the same
+    float2 *stats = reinterpret_cast<float2 *>(totals + 2 * ROWS * 4);   // [ROWS]: m and l of set 1
+    const uint32_t entries = tc::smem_u32(base), full = tc::smem_u32(bars), empty = full + 8 * kMaxEntries,
+                   ufull = empty + 8 * kMaxEntries, uempty = ufull + 8 * kUnits;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rows = a.d.grp * a.tokens, row0 = blockIdx.y * ROWS, mine = min(ROWS, rows - row0);
+    let_next_start();
+    if (tid == 0) {
+        for (uint32_t e = 0; e < E; ++e) {
+            tc::mbar_init(full + 8 * e, 1);
+            tc::mbar_init(empty + 8 * e, 4);
+        }
+        for (int u = 0; u < kUnits; ++u) {
+            tc::mbar_init(ufull + 8 * u, 1);
+            tc::mbar_init(uempty + 8 * u, kConsumers / 32);
+        }
+        tc::mbar_fence_init();
+        lost = 0;
+    }
+    // rows that pad the query block stay zero
+    for (int i = tid; i < kUnits * S::q_block / 16; i += kThreads) reinterpret_cast<uint4 *>(q_mem)[i] = make_uint4(0u, 0u, 0u, 0u);
+    tc::fence_async_smem();
+    AttnWalk w;
+    const bool work = attn_begin<kTile, kThreads>(a, blockIdx.x, sums, found, w);      // synchronises the block
+    if (!work) {
+        if (blockIdx.y == 0 && tid == 0) a.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
+        return;
+    }
+
+    if (warp == kConsumers / 32) {
+        // ------------------------------------------------------------ copies
+        constexpr int NB = D / 64;
+        const int piece = min(a.d.page, kTile), shift = min(a.d.page_shift, 6), boxes = (kTile >> shift) * NB;
+        const int my_piece = lane / NB, my_col = lane % NB;
+        const uint32_t box_bytes = piece * 128u, at = my_col * (kTile * 128u) + my_piece * box_bytes;
+        uint32_t e = 0, phase = 0, issued = 0;
+        int seq = 0, u = 0;
+        bool alive = true, unit_first = true;
+        while (w.left > 0 && alive) {
+            const AttnSeq s = w.s;
+            const int n = w.n, h = w.h, count = (int)min((long long)(s.tiles - w.t), w.left), t0 = w.t;
+            const bool whole = t0 == 0 && count == s.tiles;
+            const int slot = whole ? -1 : unit_first ? 0 : 1;
+            const int32_t *row = a.table + (long long)s.row * a.d.max_pages;
+            // the page of this lane's piece of tile t; -1: not there
+            auto page_of = [&](int t) {
+                const int i = (s.tile0 + t) * kTile + (my_piece << shift);
+                if (lane >= boxes || i >= s.len || i + piece <= s.first) return -1;
+                const int p = row[i >> a.d.page_shift];
+                if (p >= 0 && p < a.d.n_pages) return p;
+                set_error(a.err, GDN_DEVERR_PAGE);
+                return -1;
+            };
+            int page = page_of(t0);
+            const uint32_t us = u % kUnits, uphase = (u / kUnits) & 1;
+            if (u >= kUnits) alive = tc::mbar_wait(uempty + 8 * us, uphase ^ 1, a.wait_ns);
+            alive = __all_sync(0xffffffffu, alive);
+            if (!alive) break;
+            if (lane == 0) {
+                units[us] = Unit{n, h, s.len, s.first, (s.tile0 + t0) * kTile, count, seq, slot};
+                tc::mbar_arrive_expect_tx(ufull + 8 * us, (uint32_t)mine * D * 2);
+            }
+            __syncwarp();
+            for (int r = lane; r < mine; r += 32) {
+                const int tok = (row0 + r) / a.d.grp, g = (row0 + r) - tok * a.d.grp;
+                tc::bulk_g2s(tc::smem_u32(q_mem) + us * S::q_block + r * S::q_pitch,
+                             (const __nv_bfloat16 *)a.q + ((long long)n * a.tokens + tok) * a.ld_q + (long long)(h * a.d.grp + g) * a.hs_q, D * 2,
+                             ufull + 8 * us);
+            }
+            ++u;
+            for (int j = 0; j < count && alive; ++j) {
+                const int here = page, i0 = (s.tile0 + t0 + j) * kTile;
+                if (j + 1 < count) page = page_of(t0 + j + 1);
+                const unsigned there = __ballot_sync(0xffffffffu, here >= 0);
+                const uint32_t bytes = __popc(there) * box_bytes;
+                // the row of the pools where this lane's piece begins
+                const int y = (here * a.d.hkv + h) * a.d.page + ((i0 + (my_piece << shift)) & (a.d.page - 1));
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    if (issued >= E) alive = tc::mbar_wait(empty + 8 * e, phase ^ 1, a.wait_ns);
+                    alive = __all_sync(0xffffffffu, alive);
+                    if (!alive) break;
+                    if (lane == 0) {
+                        if (kv == 0) {
+                            int bits = 0;
+                            for (int p = 0; p < 4; ++p) bits |= (there >> ((p * 16) >> shift) * NB & 1u) << p;
+                            pieces_of[e] = bits;
+                        }
+                        if (bytes) tc::mbar_arrive_expect_tx(full + 8 * e, bytes);
+                        else tc::mbar_arrive(full + 8 * e);
+                    }
+                    __syncwarp();
+                    const bool drop = (a.lose & LOSE_ATTN_TILE_COPY) && issued == 0 && lane == 0;
+                    if (here >= 0 && !drop) tc::tma_load_2d(entries + e * S::entry + at, kv ? &maps.v : &maps.k, my_col * 64, y, full + 8 * e);
+                    ++issued;
+                    if (++e == E) {
+                        e = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            seq += count;
+            bool unit_end = false;
+            for (int j = 0; j < count; ++j) unit_end = attn_next<kTile>(a, w);
+            if (w.left == 0 && blockIdx.y == 0 && lane == 0) {
+                // the CTA that holds a unit's front joins it: the CTAs behind that hold the rest
+                int parts = 0;
+                if (!unit_end && t0 == 0) parts = 1 + (int)((s.tiles - count + w.per - 1) / w.per);
+                a.joins[blockIdx.x] = make_int4(n, h, unit_first ? 0 : 1, parts);
+            }
+            unit_first = false;
+        }
+        if (lane == 0) {
+            if (!alive) {             // nothing more is copied
+                set_error(a.err, GDN_DEVERR_TIMEOUT);
+                if (blockIdx.y == 0) a.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
+            }
+            // what is under way arrives before the block ends
+            for (uint32_t k = 0; k < min(issued, E); ++k) {
+                const uint32_t last = issued - 1 - k;
+                tc::mbar_wait(full + 8 * (last % E), (last / E) & 1, a.wait_ns);
+            }
+            for (int k = 0; k < min(u, kUnits); ++k) {
+                const int last = u - 1 - k;
+                tc::mbar_wait(ufull + 8 * (last % kUnits), (last / kUnits) & 1, a.wait_ns);
+            }
+        }
+        return;
+    }
+
+    // ---------------------------------------------------------------- products
+    const int set = warp >> 2, wg = warp & 3, g = lane >> 2, t4 = lane & 3;
+    int token[MT][2];                                   // the new token of this thread's rows
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        token[mt][0] = min((row0 + mt * 16 + g) / a.d.grp, a.tokens - 1);
+        token[mt][1] = min((row0 + mt * 16 + g + 8) / a.d.grp, a.tokens - 1);
+    }
+    const uint32_t p_hi = tc::smem_u32(p_mem) + set * 2 * S::p_block, p_lo = p_hi + S::p_block;
+    float *my_tops = tops + set * ROWS * 4, *my_totals = totals + set * ROWS * 4;
+    // ldmatrix addresses: rows of Q and P, tokens of K and V
+    const uint32_t q_lane = (lane & 15) * S::q_pitch + (lane >> 4) * 16, p_lane = (lane & 15) * kPPitch + (lane >> 4) * 16;
+    const uint32_t k_token = wg * 16 + (lane & 7) + ((lane >> 4) << 3), k_half = (lane >> 3) & 1;
+    const uint32_t v_token = (lane & 7) + (((lane >> 3) & 1) << 3), v_half = lane >> 4;
+    uint32_t e = 2 * set, phase = 0;                    // the entry of the set's next tile
+    bool ok = true;
+    int u = 0;
+    for (long long left = w.left; left > 0; ++u) {
+        const uint32_t us = u % kUnits;
+        if (!bar_all(kBarUnit, kConsumers, ok && tc::mbar_wait(ufull + 8 * us, (u / kUnits) & 1, a.wait_ns))) {
+            ok = false;
+            break;
+        }
+        const Unit unit = units[us];
+        left -= unit.count;
+        const uint32_t q_base = tc::smem_u32(q_mem) + us * S::q_block + q_lane;
+        float m[MT][2], l[MT][2], o[MT][NT][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            m[mt][0] = m[mt][1] = -INFINITY;
+            l[mt][0] = l[mt][1] = 0.f;
+#pragma unroll
+            for (int c = 0; c < NT; ++c) o[mt][c][0] = o[mt][c][1] = o[mt][c][2] = o[mt][c][3] = 0.f;
+        }
+        // what all rows see lies below `open`, and not below `wide`
+        const int open = unit.len - a.tokens + 1, wide = a.window > 0 ? unit.len - a.window : 0;
+        for (int j = (unit.seq0 & 1) ^ set; j < unit.count; j += 2) {
+            const int i0 = unit.i0 + j * kTile;
+            const uint32_t v_e = e + 1;                 // V follows its K
+            if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(full + 8 * e, phase, a.wait_ns));
+            const int pieces = pieces_of[e];
+            const bool masked = pieces != 15 || i0 + kTile > open || i0 < wide;
+            float s[MT][2][4];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) s[mt][c][0] = s[mt][c][1] = s[mt][c][2] = s[mt][c][3] = 0.f;
+            const uint32_t k_row = entries + e * S::entry + k_token * 128;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                uint32_t b[4];
+                const uint32_t chunk = 2 * ks + k_half;
+                ldsm4(k_row + (chunk >> 3) * (kTile * 128) + (((chunk & 7) ^ (k_token & 7)) << 4), b);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    uint32_t q[4];
+                    ldsm4(q_base + mt * 16 * S::q_pitch + ks * 32, q);
+                    mma16816(s[mt][0], q, b[0], b[1]);
+                    mma16816(s[mt][1], q, b[2], b[3]);
+                }
+            }
+            __syncwarp();
+            if (ok && lane == 0) tc::mbar_arrive(empty + 8 * e);     // what never came is not asked for again
+            if (masked) {
+                const bool piece = pieces >> wg & 1;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const int i = i0 + wg * 16 + c * 8 + t4 * 2 + (x & 1), end = open + token[mt][x >> 1];
+                            if (!(piece && i < end && (a.window == 0 || i >= end - a.window))) s[mt][c][x] = -INFINITY;
+                        }
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    float top = fmaxf(fmaxf(s[mt][0][2 * r], s[mt][0][2 * r + 1]), fmaxf(s[mt][1][2 * r], s[mt][1][2 * r + 1]));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    if (t4 == 0) my_tops[(mt * 16 + r * 8 + g) * 4 + wg] = top;
+                }
+            bar_sync(kBarSet + set, 128);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float4 v = *reinterpret_cast<const float4 *>(my_tops + (mt * 16 + r * 8 + g) * 4);
+                    const float nm = fmaxf(m[mt][r], fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)) * a.scale_log2);
+                    const float ref = nm == -INFINITY ? 0.f : nm, back = exp2_fast(m[mt][r] - ref);
+                    m[mt][r] = nm;
+                    l[mt][r] *= back;
+#pragma unroll
+                    for (int c = 0; c < NT; ++c) {
+                        o[mt][c][2 * r] *= back;
+                        o[mt][c][2 * r + 1] *= back;
+                    }
+                    const uint32_t row = (mt * 16 + r * 8 + g) * kPPitch + (wg * 16 + t4 * 2) * 2;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const float p0 = exp2_fast(fmaf(s[mt][c][2 * r], a.scale_log2, -ref)),
+                                    p1 = exp2_fast(fmaf(s[mt][c][2 * r + 1], a.scale_log2, -ref));
+                        l[mt][r] += p0 + p1;
+                        const uint32_t hi = pack_bf16(p0, p1);
+                        const uint32_t lo = pack_bf16(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xffff0000u));
+                        asm volatile("st.shared.b32 [%0], %1;" :: "r"(p_hi + row + c * 16), "r"(hi) : "memory");
+                        asm volatile("st.shared.b32 [%0], %1;" :: "r"(p_lo + row + c * 16), "r"(lo) : "memory");
+                    }
+                }
+            bar_sync(kBarSet + set, 128);
+            if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(full + 8 * v_e, phase, a.wait_ns));
+            const uint32_t v_base = entries + v_e * S::entry;
+            auto v_addr = [&](int ks, int pair) {
+                const uint32_t chunk = wg * (D / 32) + 2 * pair + v_half, tok = ks * 16 + v_token;
+                return v_base + (chunk >> 3) * (kTile * 128) + tok * 128 + (((chunk & 7) ^ (tok & 7)) << 4);
+            };
+            if (!masked) {
+#pragma unroll
+                for (int ks = 0; ks < kTile / 16; ++ks) {
+                    uint32_t b[NT / 2][4];
+#pragma unroll
+                    for (int pair = 0; pair < NT / 2; ++pair) ldsm4t(v_addr(ks, pair), b[pair]);
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        uint32_t p[4];
+                        ldsm4(p_hi + p_lane + mt * 16 * kPPitch + ks * 32, p);
+#pragma unroll
+                        for (int c = 0; c < NT; ++c) mma16816(o[mt][c], p, b[c >> 1][(c & 1) * 2], b[c >> 1][(c & 1) * 2 + 1]);
+                        ldsm4(p_lo + p_lane + mt * 16 * kPPitch + ks * 32, p);
+#pragma unroll
+                        for (int c = 0; c < NT; ++c) mma16816(o[mt][c], p, b[c >> 1][(c & 1) * 2], b[c >> 1][(c & 1) * 2 + 1]);
+                    }
+                }
+            } else {
+                // Places that no row sees may hold anything and read as zero.  A value that is not finite in a place that
+                // only some rows see would reach the others as 0 * inf: then each new token's rows are taken by themselves.
+                auto kept = [&](int ks, int half, int from, int to) {    // mask of the pair of tokens of a B register
+                    const int i = i0 + ks * 16 + half * 8 + t4 * 2;
+                    const bool there = pieces >> ks & 1;
+                    return (there && i >= from && i < to ? 0xffffu : 0u) | (there && i + 1 >= from && i + 1 < to ? 0xffff0000u : 0u);
+                };
+                bool odd = false;
+                if (a.tokens > 1) {
+                    for (int ks = 0; ks < kTile / 16; ++ks)
+                        for (int pair = 0; pair < NT / 2; ++pair) {
+                            uint32_t b[4];
+                            ldsm4t(v_addr(ks, pair), b);
+                            const uint32_t k0 = kept(ks, 0, unit.first, unit.len), k1 = kept(ks, 1, unit.first, unit.len);
+                            odd |= not_finite2(b[0] & k0) | not_finite2(b[1] & k1) | not_finite2(b[2] & k0) | not_finite2(b[3] & k1);
+                        }
+                    odd = __any_sync(0xffffffffu, odd);
+                }
+                for (int pass = 0; pass < (odd ? a.tokens : 1); ++pass) {
+                    const int to = odd ? open + pass : unit.len, from = odd ? (a.window > 0 ? to - a.window : 0) : unit.first;
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        float x[NT][4];
+#pragma unroll
+                        for (int c = 0; c < NT; ++c)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) x[c][k] = o[mt][c][k];
+#pragma unroll
+                        for (int ks = 0; ks < kTile / 16; ++ks) {
+                            const uint32_t k0 = kept(ks, 0, from, to), k1 = kept(ks, 1, from, to);
+                            uint32_t b[NT / 2][4];
+#pragma unroll
+                            for (int pair = 0; pair < NT / 2; ++pair) {
+                                ldsm4t(v_addr(ks, pair), b[pair]);
+                                b[pair][0] &= k0; b[pair][1] &= k1; b[pair][2] &= k0; b[pair][3] &= k1;
+                            }
+#pragma unroll
+                            for (int part = 0; part < 2; ++part) {
+                                uint32_t p[4];
+                                ldsm4((part ? p_lo : p_hi) + p_lane + mt * 16 * kPPitch + ks * 32, p);
+#pragma unroll
+                                for (int c = 0; c < NT; ++c) mma16816(x[c], p, b[c >> 1][(c & 1) * 2], b[c >> 1][(c & 1) * 2 + 1]);
+                            }
+                        }
+#pragma unroll
+                        for (int c = 0; c < NT; ++c)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (!odd || token[mt][k >> 1] == pass) o[mt][c][k] = x[c][k];
+                    }
+                }
+            }
+            __syncwarp();
+            if (ok && lane == 0) tc::mbar_arrive(empty + 8 * v_e);
+            e += 4;
+            if (e >= E) {
+                e -= E;
+                phase ^= 1;
+            }
+        }
+        if (ok && lane == 0) tc::mbar_arrive(uempty + 8 * us);
+        // the rows' sums over the set's warps; then set 1's into set 0's
+        if (!ok) lost = 1;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float v = l[mt][r];
+                v += __shfl_xor_sync(0xffffffffu, v, 1);
+                v += __shfl_xor_sync(0xffffffffu, v, 2);
+                if (t4 == 0) my_totals[(mt * 16 + r * 8 + g) * 4 + wg] = v;
+            }
+        bar_sync(kBarSet + set, 128);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float4 v = *reinterpret_cast<const float4 *>(my_totals + (mt * 16 + r * 8 + g) * 4);
+                l[mt][r] = (v.x + v.y) + (v.z + v.w);
+            }
+        const int col0 = wg * (D / 4) + t4 * 2;
+        if (set == 1) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int row = mt * 16 + r * 8 + g;
+#pragma unroll
+                    for (int c = 0; c < NT; ++c)
+                        *reinterpret_cast<float2 *>(merge + row * D + col0 + c * 8) = make_float2(o[mt][c][2 * r], o[mt][c][2 * r + 1]);
+                    if (wg == 0 && t4 == 0) stats[row] = make_float2(m[mt][r], l[mt][r]);
+                }
+            bar_arrive(kBarMerge, kConsumers);
+            continue;
+        }
+        bar_sync(kBarMerge, kConsumers);
+        if (*(volatile int *)&lost) continue;
+        float *part = attn_part(a, blockIdx.x, max(unit.slot, 0));
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int row = mt * 16 + r * 8 + g;
+                if (row >= mine) continue;
+                const float2 other = stats[row];
+                const float nm = fmaxf(m[mt][r], other.x), ref = nm == -INFINITY ? 0.f : nm;
+                const float fa = exp2_fast(m[mt][r] - ref), fb = exp2_fast(other.x - ref), total = l[mt][r] * fa + other.y * fb;
+                const int tok = token[mt][r], head = unit.h * a.d.grp + row0 + row - tok * a.d.grp;
+                const long long orow = ((long long)unit.n * a.tokens + tok) * a.d.hq + head;
+                const float inv = unit.slot >= 0 ? 1.f : total == 0.f ? 0.f : 1.f / total;
+#pragma unroll
+                for (int c = 0; c < NT; ++c) {
+                    const float2 x = *reinterpret_cast<const float2 *>(merge + row * D + col0 + c * 8);
+                    const float v0 = (o[mt][c][2 * r] * fa + x.x * fb) * inv, v1 = (o[mt][c][2 * r + 1] * fa + x.y * fb) * inv;
+                    if (unit.slot >= 0)
+                        *reinterpret_cast<float2 *>(part + (row0 + row) * D + col0 + c * 8) = make_float2(v0, v1);
+                    else
+                        *reinterpret_cast<uint32_t *>((__nv_bfloat16 *)a.out + orow * D + col0 + c * 8) = pack_bf16(v0, v1);
+                }
+                if (wg == 0 && t4 == 0) {
+                    if (unit.slot >= 0)
+                        *reinterpret_cast<float2 *>(part + rows * D + 2 * (row0 + row)) = make_float2(nm, total);
+                    else if (a.lse)
+                        a.lse[orow] = total == 0.f ? -INFINITY : (nm + log2f(total)) * kLn2;
+                }
+            }
+    }
+    if (!ok && lane == 0) set_error(a.err, GDN_DEVERR_TIMEOUT);
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_tiled() {
+    static EncodeTiledFn fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess || q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiledFn>(p);
+    }();
+    return fn;
+}
+
+// A pool as rows of D columns (one token of one key head each), in boxes of a piece of a page by 64 columns.
+bool encode(CUtensorMap *m, const void *pool, const AttnDims &d) {
+    const EncodeTiledFn fn = encode_tiled();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)d.D, (cuuint64_t)d.n_pages * d.hkv * d.page}, strides[1] = {(cuuint64_t)d.D * 2};
+    const cuuint32_t box[2] = {64u, (cuuint32_t)(d.page < kTile ? d.page : kTile)}, estr[2] = {1u, 1u};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(pool), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int MT> cudaError_t run(AttnDecodeArgs a, const Maps &maps, cudaStream_t s) {
+    constexpr int bytes = Smem<D, MT>::bytes;
+    const auto kernel = attn_decode_tc_kernel<D, MT>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    // blocks of query rows read the same tiles: at the same time, so that the second one finds them in L2
+    const int blocks = (a.d.grp * a.tokens + 16 * MT - 1) / (16 * MT);
+    a.ctas = sm_count() / blocks;
+    kernel<<<dim3(a.ctas, blocks), kThreads, bytes, s>>>(a, maps);
+    const cudaError_t l = cudaGetLastError();
+    return l != cudaSuccess ? l : launch_attn_join(a, true, s);
+}
+template <int D> cudaError_t run_rows(const AttnDecodeArgs &a, const Maps &maps, cudaStream_t s) {
+    const int rows = a.d.grp * a.tokens;
+    if (rows <= 16) return run<D, 1>(a, maps, s);
+    if constexpr (D == 256) {
+        return run<D, 2>(a, maps, s);
+    } else {
+        return rows <= 32 ? run<D, 2>(a, maps, s) : run<D, 4>(a, maps, s);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_attn_decode_tc(const AttnDecodeArgs &a, cudaStream_t s) {
+    Maps maps;
+    if (!encode(&maps.k, a.k_pages, a.d) || !encode(&maps.v, a.v_pages, a.d)) return cudaErrorInvalidValue;
+    return a.d.D == 64 ? run_rows<64>(a, maps, s) : a.d.D == 128 ? run_rows<128>(a, maps, s) : run_rows<256>(a, maps, s);
+}
+
+}  // namespace gdn

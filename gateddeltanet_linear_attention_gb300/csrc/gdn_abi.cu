@@ -628,7 +628,7 @@ gdn_status gdn_mixer_decode_q8(const gdn_config *cfg, const gdn_mixer_io *io, in
 }
 
 gdn_status gdn_debug_set_wait(uint64_t wait_ns, uint32_t lose) {
-    if (wait_ns == 0 || wait_ns > 60000000000ull || (lose & ~7u)) return GDN_ERR_INVALID_ARG;
+    if (wait_ns == 0 || wait_ns > 60000000000ull || (lose & ~15u)) return GDN_ERR_INVALID_ARG;
     g_wait_ns.store(wait_ns);
     g_lose.store(lose);
     return GDN_OK;

@@ -23,6 +23,7 @@ struct Dims {
 };
 constexpr unsigned LOSE_DECODE_STATE_COPY = 1u;   // decode streaming kernel: the first head's state
 constexpr unsigned LOSE_SSM_TILE_COPY = 4u;       // tensor-core scan: the first chunk's x tile
+constexpr unsigned LOSE_ATTN_TILE_COPY = 8u;      // tensor-core decode attention: the first piece of each CTA's first K tile
 constexpr unsigned LOSE_CHAIN_OPERAND_COPY = 2u;  // state chain: the first chunk's [-W ; Q'] operand
 
 __device__ __forceinline__ float to_f32(float x) { return x; }

@@ -701,7 +701,8 @@ gdn_status gdn_page_copy(const gdn_attn_config *cfg, const void *src_k, const vo
  * chunk operand of the tensor-core state chain (gdn_chunk_prefill,
  * gdn_mixer_prefill), bit 2 the first x tile of tensor-core
  * gdn_ssm_prefill (of every sequence that is not cut, and of every segment in
- * front of the last where one is).  Work that timed out writes no state (a
+ * front of the last where one is), bit 3 a piece of the first K tile of every
+ * CTA of gdn_attn_decode in bf16 (its outputs are then not to be used).  Work that timed out writes no state (a
  * sequence's heads each for themselves).  Process-wide,
  * read at each call; GDN_ERR_INVALID_ARG for wait_ns = 0, above 60 s, or an
  * unknown bit. */

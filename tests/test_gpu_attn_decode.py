@@ -312,3 +312,41 @@ def test_other_stream():
     gdn.gdn_attn_decode(c.cfg, *c.d, out3, c.ws, stream=side)
     side.synchronize()
     assert torch.equal(out3, want)
+
+
+@pytest.mark.parametrize("D,tokens", [(64, 1), (128, 8), (256, 1)])
+def test_a_lost_tile_times_out(D, tokens):
+    """A copy that never comes: the call ends by itself within its limit, says so, and the next one is right."""
+    c = Cache([3000, 40, 700], 8, 1, D, 16, "bf16", tokens, seed=14).upload()
+    want, want_lse = c.run()
+    torch.cuda.synchronize()
+    gdn.gdn_debug_set_wait(20_000_000, 8)
+    try:
+        c.run()
+        assert gdn.gdn_device_error() == gdn.DEVERR_TIMEOUT
+    finally:
+        gdn.gdn_debug_set_wait()
+    out, lse = c.run()
+    assert torch.equal(out, want) and torch.equal(lse, want_lse) and gdn.gdn_device_error() == 0
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,page,tokens", [(16, 2, 256, 128, 1), (4, 1, 256, 16, 8), (8, 1, 128, 64, 8), (6, 2, 128, 32, 3), (1, 1, 64, 64, 1),
+                                                  (16, 1, 64, 128, 8)])
+def test_every_layout_walks_its_ring(Hq, Hkv, D, page, tokens):
+    """More tiles a CTA than it has places for, so that every place is filled again and again."""
+    c = Cache([80000, 64, 60001], Hq, Hkv, D, page, "bf16", tokens, seed=15)
+    c.upload()
+    out, lse = c.run()
+    k = tokens
+    for n in range(3):
+        for j in (0, k - 1):
+            t = n * k + j
+            L = c.lens[n] - k + 1 + j
+            K, V = c.K[n][:, :L].double(), c.V[n][:, :L].double()
+            q = c.q[t].double().view(Hkv, Hq // Hkv, D)
+            s = torch.einsum("hgd,htd->hgt", q, K) * D ** -0.5
+            top = (torch.einsum("hgd,htd->hgt", q.abs(), K.abs()) * D ** -0.5).amax(-1).view(1, Hq)
+            p = torch.softmax(s, -1)
+            want, mag = (torch.einsum("hgt,htd->hgd", p, x).reshape(1, Hq, D) for x in (V, V.abs()))
+            compare(out[t:t + 1].double().cpu(), lse[t:t + 1].double().cpu(), (want, torch.logsumexp(s, -1).view(1, Hq), mag, top), L, D, c.act)
+    assert gdn.gdn_device_error() == 0
