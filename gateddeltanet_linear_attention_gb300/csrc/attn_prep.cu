@@ -7,10 +7,12 @@
 // Backward, with g the gradient turned back by -t and x^ = x rstd:
 //   dw = sum g x^,   dx = rstd (g w - x^ mean(g w x^))
 //
-// HBM-bound: q, k and v are read once and written once.  A warp takes a token (in small batches a part of its heads);
-// D / 8 lanes own a head vector and keep it in registers.  The token's angles are computed once, a pair or a few a
-// lane, and kept in registers for all its heads; the loads of the next heads are issued before a batch of them is
-// worked on.
+// HBM-bound: q, k and v are read once and written once.  D / 8 lanes own a head vector and keep it in registers.  A
+// warp takes a few tokens at a time: what they are and their angles come first, a lane a token, then a lane an angle;
+// then it goes through their heads in batches, the loads of the next batch (of the next kind of heads, of the next token)
+// under way.  No warp waits for another.
+#include <type_traits>
+
 #include "attn_common.cuh"
 
 namespace gdn {
@@ -19,48 +21,54 @@ namespace {
 
 constexpr int kPrepThreads = 256;
 constexpr int kPrepWarps = kPrepThreads / 32;
+constexpr int kPrepBlocks = 2;       // of the forward kernel on an SM
 
-// Eight neighbouring values of a head as the memory holds them.
+// A lane's eight values of a head, two pieces of four, as the memory holds them and as pairs for the packed
+// multiply-adds.
 template <typename T> struct Raw;
 template <> struct Raw<float> {
     float4 a, b;
-    __device__ __forceinline__ void load(const float *p) { a = load4f(p); b = load4f(p + 4); }
+    __device__ __forceinline__ void load(const float *p, const float *q) { a = load4f(p); b = load4f(q); }
     __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-    __device__ __forceinline__ void get(float (&v)[8]) const {
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    __device__ __forceinline__ void get(f32x2 (&v)[4]) const {
+        v[0] = pack2(a.x, a.y); v[1] = pack2(a.z, a.w); v[2] = pack2(b.x, b.y); v[3] = pack2(b.z, b.w);
     }
-    __device__ __forceinline__ Raw from(int lane) const {
-        Raw r;
-        r.a = make_float4(__shfl_sync(0xffffffffu, a.x, lane), __shfl_sync(0xffffffffu, a.y, lane), __shfl_sync(0xffffffffu, a.z, lane),
-                          __shfl_sync(0xffffffffu, a.w, lane));
-        r.b = make_float4(__shfl_sync(0xffffffffu, b.x, lane), __shfl_sync(0xffffffffu, b.y, lane), __shfl_sync(0xffffffffu, b.z, lane),
-                          __shfl_sync(0xffffffffu, b.w, lane));
-        return r;
-    }
+    __device__ __forceinline__ void store(float *p, float *q) const { store4f(p, a); store4f(q, b); }
 };
 template <> struct Raw<__nv_bfloat16> {
-    uint4 u;
-    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { u = *reinterpret_cast<const uint4 *>(p); }
-    __device__ __forceinline__ void clear() { u = make_uint4(0u, 0u, 0u, 0u); }
-    __device__ __forceinline__ void get(float (&v)[8]) const {
-        const float4 a = bf16x4_f32(make_uint2(u.x, u.y)), b = bf16x4_f32(make_uint2(u.z, u.w));
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    uint2 a, b;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p, const __nv_bfloat16 *q) {
+        a = *reinterpret_cast<const uint2 *>(p);
+        b = *reinterpret_cast<const uint2 *>(q);
     }
-    __device__ __forceinline__ Raw from(int lane) const {
-        Raw r;
-        r.u = make_uint4(__shfl_sync(0xffffffffu, u.x, lane), __shfl_sync(0xffffffffu, u.y, lane), __shfl_sync(0xffffffffu, u.z, lane),
-                         __shfl_sync(0xffffffffu, u.w, lane));
-        return r;
+    __device__ __forceinline__ void clear() { a = b = make_uint2(0u, 0u); }
+    static __device__ __forceinline__ f32x2 pair(uint32_t x) { return pack2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)); }
+    __device__ __forceinline__ void get(f32x2 (&v)[4]) const { v[0] = pair(a.x); v[1] = pair(a.y); v[2] = pair(b.x); v[3] = pair(b.y); }
+    __device__ __forceinline__ void store(__nv_bfloat16 *p, __nv_bfloat16 *q) const {
+        *reinterpret_cast<uint2 *>(p) = a;
+        *reinterpret_cast<uint2 *>(q) = b;
     }
 };
-__device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
-    store4f(p, make_float4(v[0], v[1], v[2], v[3]));
-    store4f(p + 4, make_float4(v[4], v[5], v[6], v[7]));
+__device__ __forceinline__ void store8(float *p, float *q, const f32x2 (&v)[4]) {
+    const float2 a = unpack2(v[0]), b = unpack2(v[1]), c = unpack2(v[2]), d = unpack2(v[3]);
+    store4f(p, make_float4(a.x, a.y, b.x, b.y));
+    store4f(q, make_float4(c.x, c.y, d.x, d.y));
 }
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8]) {
-    __nv_bfloat162 h[4] = {__floats2bfloat162_rn(v[0], v[1]), __floats2bfloat162_rn(v[2], v[3]),
-                           __floats2bfloat162_rn(v[4], v[5]), __floats2bfloat162_rn(v[6], v[7])};
-    *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(h);
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, __nv_bfloat16 *q, const f32x2 (&v)[4]) {
+    __nv_bfloat162 h[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h[j] = __float22bfloat162_rn(unpack2(v[j]));
+    *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<const uint2 *>(h);
+    *reinterpret_cast<uint2 *>(q) = *reinterpret_cast<const uint2 *>(h + 2);
+}
+__device__ __forceinline__ f32x2 both(float x) { return pack2(x, x); }
+// Sum of the products of two rows of eight.
+__device__ __forceinline__ float dot8(const f32x2 (&a)[4], const f32x2 (&b)[4]) {
+    f32x2 s = mul2(a[0], b[0]), t = mul2(a[1], b[1]);
+    s = fma2(a[2], b[2], s);
+    t = fma2(a[3], b[3], t);
+    const float2 r = unpack2(add2(s, t));
+    return r.x + r.y;
 }
 
 // a + b = sum + rest exactly.
@@ -84,52 +92,57 @@ __device__ __forceinline__ float2 cos_sin(float p, float f) {
     float e0, e1;
     const float s = two_sum(two_sum(fmaf(-k, C1, hi), lo, e0), t, e1);
     const float rest = (e0 + e1) + fmaf(-k, C3, t_lo);
+    // in half turns, whose sine and cosine need no further reduction
+    constexpr double kInv = 1.0 / 3.14159265358979323846;
+    constexpr float I1 = (float)kInv, I2 = (float)(kInv - (double)I1);
+    const float y = s * I1, y_lo = fmaf(s, I1, -y) + fmaf(s, I2, rest * I1);
     float sn, cs;
-    sincosf(s, &sn, &cs);
-    return make_float2(fmaf(-rest, sn, cs), fmaf(rest, cs, sn));
+    sincospif(y, &sn, &cs);
+    const float d = y_lo * (float)(kTurn / 2);
+    return make_float2(fmaf(-d, sn, cs), fmaf(d, cs, sn));
 }
 
-// What a token is: its kind, position, and where its key and value go (in rows of D elements of the pools, for key
-// head 0; -1: nowhere).  Whole warps call it.
+// What a token is: its kind and position, and where its key and value go (in rows of D elements of the pools, for key
+// head 0; -1: nowhere).
 enum { kBehind = 0, kPadding = 1, kLive = 2 };
 struct PrepToken {
     int kind;
     float pos;
     long long place;
 };
-__device__ __forceinline__ PrepToken prep_token(const AttnPrepArgs &a, long long t, bool pools) {
+__device__ PrepToken prep_token(const AttnPrepArgs &a, long long t, bool pools) {
     PrepToken o{kBehind, 0.f, -1};
+    if (t >= a.T) return o;
     int n = 0;
-    long long j = t, L = a.T;
+    long long at = t, L = a.T;
     if (a.cu) {
-        // the last sequence that begins at or before t: 32 places at a time, so that the loads in turn are few
-        int lo = 0;
+        // the last sequence that begins at or before t
         for (int count = a.n_seqs; count > 1;) {
-            const int step = (count + 31) >> 5, at = lo + (int)(threadIdx.x & 31) * step;
-            const bool le = at < lo + count && a.cu[at] <= t;
-            const int k = 31 - __clz(__ballot_sync(0xffffffffu, le) | 1u);
-            lo += k * step;
-            count = min(step, count - k * step);
+            const int half = count >> 1;
+            if (a.cu[n + half] <= t) {
+                n += half;
+                count -= half;
+            } else {
+                count = half;
+            }
         }
-        n = lo;
         long long s, e;
         seq_bounds(a.cu, n, a.T, a.err, s, e);
         if (t < s || t >= e) return o;
-        j = t - s;
+        at = t - s;
         L = e - s;
     } else if (a.n_seqs > 1) {
         L = a.T / a.n_seqs;
         n = (int)t / (int)L;
-        j = t - n * L;
+        at = t - n * L;
     }
     o.kind = kPadding;
-    long long at = j;
     int row = n;
     if (a.lens) {
         row = attn_row(a.rows, n, a.d, a.err);
         if (row < 0) return o;
         const int len = a.lens[row];
-        at = (long long)len - L + j;
+        at += (long long)len - L;
         if (at < 0 || (pools && len > a.d.max_pages * a.d.page)) {
             set_error(a.err, GDN_DEVERR_PAGE);
             return o;
@@ -169,245 +182,366 @@ template <int LPR> __device__ __forceinline__ float head_sum(float v) {
     return v;
 }
 
-// How the rotation meets a lane's 8 columns: their partners are 8 neighbours in one other lane (kLanes; most
-// models), the columns next to them (kPairs), or, where half the rotated width is no multiple of 8, scattered (kAny):
-// then partners come from memory, one by one.
-enum { kLanes = 0, kPairs = 1, kAny = 2 };
+// Which 8 columns of a head a lane has, and where their partners under the rotation are.
+//   kHalves  most models: four columns and the four that they are turned with, from the other half; behind the
+//            rotated columns 8 neighbours
+//   kPairs   8 neighbours, each turned with the one beside it
+//   kAny     half the rotated width is no multiple of 4: 8 neighbours, partners from memory one by one
+enum { kHalves = 0, kPairs = 1, kAny = 2 };
 template <int MODE, int LPR> struct Turn {
-    int c0, half, from;               // the lane's first column; the partners' lane
-    __device__ __forceinline__ Turn(int half_) : c0((threadIdx.x & 31) % LPR * 8), half(half_) {
-        const int lane = threadIdx.x & 31;
-        from = MODE != kLanes || c0 >= 2 * half ? lane : c0 < half ? lane + (half >> 3) : lane - (half >> 3);
+    int half, ca, cb;                 // columns ca .. ca + 3 and cb .. cb + 3
+    __device__ __forceinline__ Turn(int half_) : half(half_) {
+        const int l = (threadIdx.x & 31) % LPR;
+        const bool turned = MODE == kHalves && 4 * l < half;
+        ca = turned ? 4 * l : 8 * l;
+        cb = turned ? 4 * l + half : 8 * l + 4;
     }
-    __device__ __forceinline__ bool rotated(int e) const { return c0 + e < 2 * half; }
-    __device__ __forceinline__ bool lower(int e) const { return MODE == kPairs ? !(e & 1) : MODE == kLanes ? c0 < half : c0 + e < half; }
-    // the column that column e meets (itself, if it is not rotated)
-    __device__ __forceinline__ int partner(int e) const {
-        const int c = c0 + e;
-        return !rotated(e) ? c : MODE == kPairs ? c ^ 1 : lower(e) ? c + half : c - half;
+    __device__ __forceinline__ int column(int e) const { return e < 4 ? ca + e : cb + e - 4; }
+    __device__ __forceinline__ bool rotated(int e) const { return MODE == kHalves ? ca < half : column(e) < 2 * half; }
+    __device__ __forceinline__ int partner(int e) const {     // of a rotated column
+        const int c = column(e);
+        return MODE == kPairs ? c ^ 1 : c < half ? c + half : c - half;
     }
-    // v' = v x own + u x other with the angles of a token's pairs, `sign` -1 to turn back
-    __device__ __forceinline__ void angles(const float2 *turns, float sign, float (&own)[8], float (&other)[8]) const {
+    // The factors of a token's heads of one kind, v' = v x own + u x other with u the partners' values: its angles,
+    // `sign` -1 to turn back, times the weights that the columns and their partners have (`w` null: none).
+    __device__ __forceinline__ void factors(const float2 *turns, float sign, const float *w, float offset, f32x2 (&own)[4], f32x2 (&other)[4]) const {
+        f32x2 x[4], y[4];
+        if (w) {
+            Raw<float> r;
+            r.load(w + ca, w + cb);
+            r.get(x);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            float2 t = make_float2(1.f, 0.f);
-            if (rotated(e)) t = turns[MODE == kPairs ? (c0 + e) >> 1 : lower(e) ? c0 + e : c0 + e - half];
-            own[e] = t.x;
-            other[e] = lower(e) ? -sign * t.y : sign * t.y;
+            for (int j = 0; j < 4; ++j) x[j] = add2(x[j], both(offset));
         }
-    }
-    // The partners' values of a head; `p`: the head in memory, for kAny.
-    template <typename T> __device__ __forceinline__ void partners(const Raw<T> &raw, const float (&v)[8], const T *p, float (&u)[8]) const {
-        if (MODE == kLanes) {
-            raw.from(from).get(u);
+        if (MODE == kHalves) {
+            const bool turned = ca < half;
+            const float4 *t = reinterpret_cast<const float4 *>(turns + (turned ? ca : 0));      // two pairs each
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float4 p = turned ? t[j] : make_float4(1.f, 0.f, 1.f, 0.f);
+                own[j] = own[j + 2] = pack2(p.x, p.z);
+                other[j] = pack2(-sign * p.y, -sign * p.w);
+                other[j + 2] = pack2(sign * p.y, sign * p.w);
+                y[j] = x[j + 2];
+                y[j + 2] = x[j];
+            }
         } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) u[e] = !rotated(e) ? v[e] : MODE == kPairs ? v[e ^ 1] : to_f32(p[partner(e)]);
+            for (int j = 0; j < 4; ++j) {
+                float c[2], s[2], p[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int e = 2 * j + k;
+                    const bool low = MODE == kPairs ? k == 0 : column(e) < half;
+                    const float2 t = rotated(e) ? turns[MODE == kPairs ? column(e) >> 1 : low ? column(e) : column(e) - half] : make_float2(1.f, 0.f);
+                    c[k] = t.x;
+                    s[k] = low ? -sign * t.y : sign * t.y;
+                    p[k] = w && rotated(e) ? w[partner(e)] + offset : 0.f;
+                }
+                own[j] = pack2(c[0], c[1]);
+                other[j] = pack2(s[0], s[1]);
+                y[j] = pack2(p[0], p[1]);
+            }
+        }
+        if (!w) return;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            own[j] = mul2(own[j], x[j]);
+            other[j] = mul2(other[j], y[j]);
         }
     }
+    // v turned.  What is not rotated stays as it is, whatever stands beside it.  `p`: the head in memory (null: none), for kAny.
+    template <typename T> __device__ __forceinline__ void turn(f32x2 (&v)[4], const f32x2 (&own)[4], const f32x2 (&other)[4], const T *p) const {
+        f32x2 r[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            r[j] = mul2(v[j], own[j]);
+            if (MODE == kHalves) {
+                if (ca < half) r[j] = fma2(v[j ^ 2], other[j], r[j]);
+            } else if (MODE == kPairs) {
+                const float2 x = unpack2(v[j]);
+                if (rotated(2 * j)) r[j] = fma2(pack2(x.y, x.x), other[j], r[j]);
+            } else if (p) {
+                float2 x = unpack2(r[j]);
+                const float2 o = unpack2(other[j]);
+                if (rotated(2 * j)) x.x = fmaf(to_f32(p[partner(2 * j)]), o.x, x.x);
+                if (rotated(2 * j + 1)) x.y = fmaf(to_f32(p[partner(2 * j + 1)]), o.y, x.y);
+                r[j] = pack2(x.x, x.y);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = r[j];
+    }
 };
 
-// A token's cosines and sines into the warp's part of shared memory.
-__device__ __forceinline__ void make_turns(const AttnPrepArgs &a, float2 *turns, float pos) {
-    __syncwarp();                     // the token before has been read
-    for (int i = threadIdx.x & 31; i < a.half; i += 32) turns[i] = cos_sin(pos, a.inv_freq[i]);
+// What a warp keeps of its next kPrepTokens tokens, `step` apart: lane i the i-th one's kind and place, shared memory their
+// cosines and sines [token][half].
+constexpr int kPrepTokens = 4;
+__device__ __forceinline__ PrepToken prep_tokens(const AttnPrepArgs &a, long long t, long long step, bool pools, float2 *turns) {
+    const int lane = threadIdx.x & 31;
+    PrepToken mine{kBehind, 0.f, -1};
+    if (lane < kPrepTokens) mine = prep_token(a, t + lane * step, pools);
+    __syncwarp();                     // the angles before have been read
+    for (int k = 0; k < kPrepTokens; ++k) {
+        const float pos = __shfl_sync(0xffffffffu, mine.pos, k);
+        if (__shfl_sync(0xffffffffu, mine.kind, k) == kLive)
+            for (int i = lane; i < a.half; i += 32) turns[k * a.half + i] = cos_sin(pos, a.inv_freq[i]);
+    }
     __syncwarp();
+    return mine;
 }
 
-// A token's heads as a warp walks over them, HPW at a time: q's, then k's, then v's.
-template <int HPW> struct Walk {
-    int hq, hk, nq, nk, all;
-    __device__ __forceinline__ Walk(int hq_, int hk_, int hv) : hq(hq_), hk(hk_) {
-        nq = (hq + HPW - 1) / HPW;
-        nk = nq + (hk + HPW - 1) / HPW;
-        all = nk + (hv + HPW - 1) / HPW;
-    }
-    __device__ __forceinline__ int kind(int i) const { return i < nq ? 0 : i < nk ? 1 : 2; }
-    __device__ __forceinline__ int head(int i, int kind, int sub) const { return (i - (kind == 0 ? 0 : kind == 1 ? nq : nk)) * HPW + sub; }
-    __device__ __forceinline__ bool in(int head, int kind) const { return head < (kind == 0 ? hq : hk); }
+// A lane's share of a token's heads of one kind, `by` apart: its own, those that every lane of the warp has, and those that
+// any lane has.
+struct Share {
+    int mine, full, any;
+    __device__ __forceinline__ Share(int heads, int first, int hpw, int by, int sub)
+        : mine(max(0, (heads - first - sub + by - 1) / by)), full(max(0, (heads - first - hpw + by) / by)), any(max(0, (heads - first + by - 1) / by)) {}
 };
 
-template <typename T, int D, int MODE>
-__global__ void __launch_bounds__(kPrepThreads, 3) attn_prep_kernel(const AttnPrepArgs a, const int split) {
+// PLAIN: heads stand one after another in q, k and v, and a warp has all of a token's: the distances from one to the next
+// are constants of the code.  (Address arithmetic was half of the instructions, and the kernels issue half of the time.)
+template <typename T, int D, int MODE, bool PLAIN>
+__global__ void __launch_bounds__(kPrepThreads, kPrepBlocks) attn_prep_kernel(const AttnPrepArgs a) {
     constexpr int LPR = D / 8, HPW = 32 / LPR, UN = sizeof(T) == 2 ? 4 : 2;
-    extern __shared__ float2 all_turns[];                   // [warps][half]
+    extern __shared__ float4 smem4[];                       // cosines and sines [warps][kPrepTokens][half]
     const int warp = threadIdx.x >> 5, sub = (threadIdx.x & 31) / LPR;
-    if (blockIdx.x == 0) check_bounds(a);
-    const long long id = (long long)blockIdx.x * kPrepWarps + warp, t = split == 1 ? id : id / split;
-    const int part = (int)(id - t * split);
+    float2 *turns = reinterpret_cast<float2 *>(smem4) + warp * kPrepTokens * a.half;
+    const long long tokens = (long long)gridDim.x * kPrepWarps;      // side by side
+    long long t = (long long)blockIdx.x * kPrepWarps + warp;
+    if (blockIdx.x == 0 && blockIdx.y == 0) check_bounds(a);
     if (t >= a.T) return;
     const bool pools = a.k_pages != nullptr;
     const Turn<MODE, LPR> rot(a.half);
-    const Walk<HPW> walk(a.d.hq, a.k ? a.d.hkv : 0, pools ? a.d.hkv : 0);
-    const T *q = (const T *)a.q + t * a.ld_q, *k = (const T *)a.k + t * a.ld_k, *v = (const T *)a.v + t * a.ld_v;
-    auto head_at = [&](int kind, int h) { return kind == 0 ? q + h * a.hs_q : kind == 1 ? k + h * a.hs_k : v + h * a.hs_v; };
-    Raw<T> next[UN];
-    auto fetch = [&](int i0) {
+    const int ca = rot.ca, cb = rot.cb, by = PLAIN ? HPW : HPW * gridDim.y, first = PLAIN ? 0 : (int)blockIdx.y * HPW;
+    const Share nq(a.d.hq, first, HPW, by, sub), nk(a.k ? a.d.hkv : 0, first, HPW, by, sub), nv(pools ? a.d.hkv : 0, first, HPW, by, sub);
+    const long long sq = PLAIN ? HPW * D : by * a.hs_q, sk = PLAIN ? HPW * D : by * a.hs_k, sv = PLAIN ? HPW * D : by * a.hs_v;
+    const T *qp = (const T *)a.q + t * a.ld_q + (first + sub) * (PLAIN ? D : a.hs_q);
+    const T *kp = (const T *)a.k + t * a.ld_k + (first + sub) * (PLAIN ? D : a.hs_k);
+    const T *vp = (const T *)a.v + t * a.ld_v + (first + sub) * (PLAIN ? D : a.hs_v);
+    Raw<T> held[UN];
 #pragma unroll
-        for (int j = 0; j < UN; ++j) {
-            const int i = i0 + j * split, kind = walk.kind(i), h = walk.head(i, kind, sub);
-            if (i < walk.all && walk.in(h, kind)) next[j].load(head_at(kind, h) + rot.c0);
-            else next[j].clear();
+    for (int j = 0; j < UN; ++j) {                          // whatever the tokens turn out to be
+        held[j].clear();
+        if (j < nq.mine) held[j].load(qp + j * sq + ca, qp + j * sq + cb);
+    }
+    f32x2 own[4], other[4];
+    // The heads of one kind of a token, a batch of UN loads ahead: of its next ones or, at the end, of those at `then`.
+    auto run = [&](auto kind_of, const Share &n, const T *p, long long step, const T *then, long long then_step, int then_mine, int state,
+                   T *out, T *cache) {
+        constexpr int kind = decltype(kind_of)::value;
+        const float *w = kind == 0 ? a.w_q : kind == 1 ? a.w_k : nullptr;
+        const int cache_step = kind == 0 ? 0 : by * a.d.page * D;
+        for (int i = 0; i < n.any; i += UN) {
+            const bool more = i + UN < n.any;
+            const T *next = more ? p + UN * step : then;
+            const long long next_step = PLAIN ? step : more ? step : then_step;
+            const int next_mine = more ? n.mine - i - UN : then_mine;
+            auto refill = [&](int j) {
+                if (j < next_mine) held[j].load(next + j * next_step + ca, next + j * next_step + cb);
+            };
+            auto work = [&](int j, bool in) {
+                f32x2 x[4];
+                held[j].get(x);
+                refill(j);
+                float rstd = 1.f;
+                if (w) rstd = rsqrtf(fmaf(head_sum<LPR>(dot8(x, x)), 1.f / D, a.eps));
+                rot.turn(x, own, other, in ? p + j * step : nullptr);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = mul2(x[e], both(rstd));
+                if (in) {
+                    if (kind == 0 || out) store8(out + j * by * D + ca, out + j * by * D + cb, x);
+                    if (kind == 1 && cache) store8(cache + j * cache_step + ca, cache + j * cache_step + cb, x);
+                }
+            };
+            if (kind == 2 || state != kLive) {
+                // values as they are; zeros for a padding token, nothing for one behind the last sequence
+#pragma unroll
+                for (int j = 0; j < UN; ++j) {
+                    Raw<T> raw = held[j];
+                    refill(j);
+                    if (i + j >= n.mine) continue;
+                    if (kind == 2 && cache) raw.store(cache + j * cache_step + ca, cache + j * cache_step + cb);
+                    raw.clear();
+                    if (kind < 2 && out && state == kPadding) raw.store(out + j * by * D + ca, out + j * by * D + cb);
+                }
+            } else if (i + UN <= n.full) {
+#pragma unroll
+                for (int j = 0; j < UN; ++j) work(j, true);
+            } else {
+#pragma unroll
+                for (int j = 0; j < UN; ++j) work(j, i + j < n.mine);
+            }
+            p = next;
+            if (kind < 2 && out) out += UN * by * D;
+            if (kind > 0 && cache) cache += UN * cache_step;
         }
     };
-    fetch(part);                                            // whatever the token turns out to be
-    const PrepToken tok = prep_token(a, t, pools);
-    if (tok.kind == kBehind) return;
-    const bool live = tok.kind == kLive;
-    float2 *turns = all_turns + warp * a.half;
-    if (live) make_turns(a, turns, tok.pos);
-    // the columns' factors: angles with the weights, of q's heads or of k's
-    float own[8], other[8];
-    int factors = -1;
-    for (int i0 = part; i0 < walk.all; i0 += UN * split) {
-        Raw<T> raw[UN];
-#pragma unroll
-        for (int j = 0; j < UN; ++j) raw[j] = next[j];
-        if (i0 + UN * split < walk.all) fetch(i0 + UN * split);
-#pragma unroll
-        for (int j = 0; j < UN; ++j) {
-            const int i = i0 + j * split;
-            if (i >= walk.all) break;
-            const int kind = walk.kind(i), h = walk.head(i, kind, sub);
-            const bool in = walk.in(h, kind);
-            float x[8];
-            raw[j].get(x);
-            if (kind < 2) {
-                const float *w = kind ? a.w_k : a.w_q;
-                if (kind != factors && live) {
-                    rot.angles(turns, 1.f, own, other);
-                    if (w) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            own[e] *= a.offset + w[rot.c0 + e];
-                            other[e] *= a.offset + w[rot.partner(e)];
-                        }
-                    }
-                    factors = kind;
-                }
-                float u[8], sq = 0.f;
-                rot.partners(raw[j], x, in ? head_at(kind, h) : q, u);
-                float rstd = 1.f;
-                if (w) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) sq = fmaf(x[e], x[e], sq);
-                    rstd = rsqrtf(head_sum<LPR>(sq) * (1.f / D) + a.eps);
-                }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = live ? fmaf(x[e] * rstd, own[e], u[e] * rstd * other[e]) : 0.f;
-            }
-            if (in) {
-                if (kind == 0) store8((T *)a.q_out + (t * a.d.hq + h) * D + rot.c0, x);
-                if (kind == 1 && a.k_out) store8((T *)a.k_out + (t * a.d.hkv + h) * D + rot.c0, x);
-                if (kind > 0 && tok.place >= 0)
-                    store8((T *)(kind == 1 ? a.k_pages : a.v_pages) + (tok.place + (long long)h * a.d.page) * D + rot.c0, x);
+    PrepToken mine;
+    for (int k = 0; t < a.T; t += tokens, k = (k + 1) % kPrepTokens) {
+        if (k == 0) mine = prep_tokens(a, t, tokens, pools, turns);
+        const int state = __shfl_sync(0xffffffffu, mine.kind, k);
+        const float2 *angles = turns + k * a.half;
+        T *k_out = a.k_out ? (T *)a.k_out + (t * a.d.hkv + first + sub) * D : nullptr, *k_cache = nullptr, *v_cache = nullptr;
+        if (pools) {
+            long long place = __shfl_sync(0xffffffffu, mine.place, k);
+            if (place >= 0) {
+                place = (place + (long long)(first + sub) * a.d.page) * D;
+                k_cache = (T *)a.k_pages + place;
+                v_cache = (T *)a.v_pages + place;
             }
         }
+        const T *next_q = qp + tokens * a.ld_q;
+        const int next_mine = t + tokens < a.T ? nq.mine : 0;
+        if (state == kLive) rot.factors(angles, 1.f, a.w_q, a.offset, own, other);
+        run(std::integral_constant<int, 0>(), nq, qp, sq, nk.any ? kp : next_q, nk.any ? sk : sq, nk.any ? nk.mine : next_mine, state,
+            (T *)a.q_out + (t * a.d.hq + first + sub) * D, nullptr);
+        if (nk.any) {
+            if (state == kLive) rot.factors(angles, 1.f, a.w_k, a.offset, own, other);
+            run(std::integral_constant<int, 1>(), nk, kp, sk, nv.any ? vp : next_q, nv.any ? sv : sq, nv.any ? nv.mine : next_mine, state, k_out,
+                k_cache);
+            if (nv.any) run(std::integral_constant<int, 2>(), nv, vp, sv, next_q, sq, next_mine, state, nullptr, v_cache);
+        }
+        qp = next_q;
+        kp += tokens * a.ld_k;
+        vp += tokens * a.ld_v;
     }
 }
 
-// A warp walks over tokens; the weights' gradients gather in registers over a token's heads of one kind, in shared
-// memory over the tokens, each lane for itself, and at the end over the block in a fixed order.
-template <typename T, int D, int MODE>
+// The weights' gradients gather in registers over a token's heads of one kind, then in shared memory over the tokens, each
+// lane for itself, and at the end over the block in a fixed order.
+template <typename T, int D, int MODE, bool PLAIN>
 __global__ void __launch_bounds__(kPrepThreads, 2) attn_prep_backward_kernel(const AttnPrepArgs a) {
     constexpr int LPR = D / 8, HPW = 32 / LPR, UN = sizeof(T) == 2 ? 4 : 2;
-    extern __shared__ float2 all_turns[];                   // [warps][half], then sums[2][warps][lanes][8]
+    extern __shared__ float4 smem4[];                       // sums[2][warps][lanes][8], cosines and sines [warps][kPrepTokens][half]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / LPR;
-    float2 *turns = all_turns + warp * a.half;
-    float *sums = reinterpret_cast<float *>(all_turns + kPrepWarps * a.half) + (warp * 32 + lane) * 8;
     constexpr int kKind = kPrepWarps * 32 * 8;
+    float *all = reinterpret_cast<float *>(smem4), *sums = all + (warp * 32 + lane) * 8;
+    float2 *turns = reinterpret_cast<float2 *>(all + 2 * kKind) + warp * kPrepTokens * a.half;
     if (blockIdx.x == 0) check_bounds(a);
 #pragma unroll
     for (int e = 0; e < 8; ++e) sums[e] = sums[kKind + e] = 0.f;
     const Turn<MODE, LPR> rot(a.half);
-    const Walk<HPW> walk(a.d.hq, a.k ? a.d.hkv : 0, 0);
-    const long long step = (long long)gridDim.x * kPrepWarps;
-    for (long long t = (long long)blockIdx.x * kPrepWarps + warp; t < a.T; t += step) {
-        const T *q = (const T *)a.q + t * a.ld_q, *k = (const T *)a.k + t * a.ld_k;
-        const T *gq = (const T *)a.dq_out + t * a.d.hq * D, *gk = (const T *)a.dk_out + t * a.d.hkv * D;
-        Raw<T> next_x[UN], next_g[UN];
-        auto fetch = [&](int i0) {
+    const int ca = rot.ca, cb = rot.cb;
+    const Share nq(a.d.hq, 0, HPW, HPW, sub), nk(a.k ? a.d.hkv : 0, 0, HPW, HPW, sub);
+    const long long sq = PLAIN ? HPW * D : HPW * a.hs_q, sk = PLAIN ? HPW * D : HPW * a.hs_k;
+    const long long tokens = (long long)gridDim.x * kPrepWarps;      // side by side
+    long long t = (long long)blockIdx.x * kPrepWarps + warp;
+    if (t < a.T) {
+        const T *qp = (const T *)a.q + t * a.ld_q + sub * (PLAIN ? D : a.hs_q);
+        const T *kp = (const T *)a.k + t * a.ld_k + sub * (PLAIN ? D : a.hs_k);
+        const T *gqp = (const T *)a.dq_out + (t * a.d.hq + sub) * D, *gkp = (const T *)a.dk_out + (t * a.d.hkv + sub) * D;
+        Raw<T> held_x[UN], held_g[UN];
 #pragma unroll
-            for (int j = 0; j < UN; ++j) {
-                const int i = i0 + j, kind = walk.kind(i), h = walk.head(i, kind, sub);
-                next_x[j].clear();
-                next_g[j].clear();
-                if (i < walk.all && walk.in(h, kind)) {
-                    if (kind ? a.w_k : a.w_q) next_x[j].load((kind ? k + h * a.hs_k : q + h * a.hs_q) + rot.c0);
-                    next_g[j].load((kind ? gk : gq) + h * D + rot.c0);
+        for (int j = 0; j < UN; ++j) {
+            held_x[j].clear();
+            held_g[j].clear();
+            if (j < nq.mine) {
+                held_g[j].load(gqp + j * HPW * D + ca, gqp + j * HPW * D + cb);
+                held_x[j].load(qp + j * sq + ca, qp + j * sq + cb);
+            }
+        }
+        f32x2 own[4], other[4];
+        // The heads of one kind of a token, a batch of UN loads ahead: of its next ones or, at the end, of those at `then`.
+        auto run = [&](auto kind_of, const Share &n, const T *p, long long step, const T *grad, const T *then, long long then_step,
+                       const T *then_grad, int then_mine, int state, T *to, long long to_step) {
+            constexpr int kind = decltype(kind_of)::value;
+            const float *w = kind == 0 ? a.w_q : a.w_k;
+            f32x2 acc[4] = {}, wv[4] = {};
+            if (w) {
+                Raw<float> r;
+                r.load(w + ca, w + cb);
+                r.get(wv);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) wv[e] = add2(wv[e], both(a.offset));
+            }
+            for (int i = 0; i < n.any; i += UN) {
+                const bool more = i + UN < n.any;
+                const T *next = more ? p + UN * step : then, *next_grad = more ? grad + UN * HPW * D : then_grad;
+                const long long next_step = PLAIN ? step : more ? step : then_step;
+                const int next_mine = more ? n.mine - i - UN : then_mine;
+                auto refill = [&](int j) {
+                    if (j < next_mine) {
+                        held_g[j].load(next_grad + j * HPW * D + ca, next_grad + j * HPW * D + cb);
+                        held_x[j].load(next + j * next_step + ca, next + j * next_step + cb);
+                    }
+                };
+                auto work = [&](int j, bool in) {
+                    f32x2 g[4], x[4];
+                    held_g[j].get(g);
+                    held_x[j].get(x);
+                    refill(j);
+                    rot.turn(g, own, other, in ? grad + j * HPW * D : nullptr);
+                    if (w) {
+                        const float mean_sq = head_sum<LPR>(dot8(x, x)) * (1.f / D);
+                        const f32x2 rstd = both(rsqrtf(mean_sq + a.eps));
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            x[e] = mul2(x[e], rstd);
+                            if (in) acc[e] = fma2(g[e], x[e], acc[e]);
+                            g[e] = mul2(g[e], wv[e]);
+                        }
+                        const f32x2 mean = both(head_sum<LPR>(dot8(g, x)) * (-1.f / D));
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) g[e] = mul2(fma2(x[e], mean, g[e]), rstd);
+                    }
+                    if (MODE == kAny) __syncwarp();     // the partners' gradients have been read: dq may be dq_out
+                    if (in && to) store8(to + j * to_step + ca, to + j * to_step + cb, g);
+                };
+                if (state != kLive) {
+                    const f32x2 zero[4] = {};
+#pragma unroll
+                    for (int j = 0; j < UN; ++j) {
+                        refill(j);
+                        if (i + j < n.mine && to && state == kPadding) store8(to + j * to_step + ca, to + j * to_step + cb, zero);
+                    }
+                } else if (i + UN <= n.full) {
+#pragma unroll
+                    for (int j = 0; j < UN; ++j) work(j, true);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < UN; ++j) work(j, i + j < n.mine);
+                }
+                p = next;
+                grad = next_grad;
+                if (to) to += UN * to_step;
+            }
+            if (w) {
+                float *sum = sums + kind * kKind;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 v = unpack2(acc[e]);
+                    sum[2 * e] += v.x;
+                    sum[2 * e + 1] += v.y;
                 }
             }
         };
-        fetch(0);
-        const PrepToken tok = prep_token(a, t, false);
-        if (tok.kind == kBehind) continue;
-        const bool live = tok.kind == kLive;
-        if (live) make_turns(a, turns, tok.pos);
-        float own[8], other[8], acc[8];
-        rot.angles(turns, -1.f, own, other);
-        int at = 0;                                         // whose sums are in acc
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-        for (int i0 = 0; i0 < walk.all; i0 += UN) {
-            Raw<T> raw_x[UN], raw_g[UN];
-#pragma unroll
-            for (int j = 0; j < UN; ++j) {
-                raw_x[j] = next_x[j];
-                raw_g[j] = next_g[j];
-            }
-            if (i0 + UN < walk.all) fetch(i0 + UN);
-#pragma unroll
-            for (int j = 0; j < UN; ++j) {
-                const int i = i0 + j;
-                if (i >= walk.all) break;
-                const int kind = walk.kind(i), h = walk.head(i, kind, sub);
-                const bool in = walk.in(h, kind);
-                const float *w = kind ? a.w_k : a.w_q;
-                if (kind != at) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        sums[e] += acc[e];
-                        acc[e] = 0.f;
-                    }
-                    at = kind;
-                }
-                float g[8], u[8];
-                raw_g[j].get(g);
-                rot.partners(raw_g[j], g, (kind ? gk : gq) + (in ? h : 0) * D, u);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) g[e] = live ? fmaf(g[e], own[e], u[e] * other[e]) : 0.f;
-                if (w) {
-                    float x[8], sq = 0.f, dot = 0.f;
-                    raw_x[j].get(x);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) sq = fmaf(x[e], x[e], sq);
-                    const float mean = head_sum<LPR>(sq) * (1.f / D), rstd = live && in ? rsqrtf(mean + a.eps) : 0.f;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        x[e] = live ? x[e] * rstd : 0.f;
-                        acc[e] = fmaf(g[e], x[e], acc[e]);
-                        g[e] *= a.offset + w[rot.c0 + e];
-                        dot = fmaf(g[e], x[e], dot);
-                    }
-                    dot = head_sum<LPR>(dot) * (1.f / D);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) g[e] = rstd * (g[e] - x[e] * dot);
-                }
-                __syncwarp();         // the partners' gradients have been read: dq may be dq_out
-                T *to = kind ? (T *)a.dk : (T *)a.dq;
-                if (in && to) store8(to + t * (kind ? a.ld_dk : a.ld_dq) + h * (kind ? a.hs_dk : a.hs_dq) + rot.c0, g);
-            }
+        PrepToken mine;
+        for (int k = 0; t < a.T; t += tokens, k = (k + 1) % kPrepTokens) {
+            if (k == 0) mine = prep_tokens(a, t, tokens, false, turns);
+            const int state = __shfl_sync(0xffffffffu, mine.kind, k);
+            const T *next_q = qp + tokens * a.ld_q, *next_g = gqp + tokens * a.d.hq * D;
+            const int next_mine = t + tokens < a.T ? nq.mine : 0;
+            if (state == kLive) rot.factors(turns + k * a.half, -1.f, nullptr, 0.f, own, other);
+            run(std::integral_constant<int, 0>(), nq, qp, sq, gqp, nk.any ? kp : next_q, nk.any ? sk : sq, nk.any ? gkp : next_g,
+                nk.any ? nk.mine : next_mine, state, a.dq ? (T *)a.dq + t * a.ld_dq + sub * a.hs_dq : nullptr, HPW * a.hs_dq);
+            if (nk.any)
+                run(std::integral_constant<int, 1>(), nk, kp, sk, gkp, next_q, sq, next_g, next_mine, state,
+                    a.dk ? (T *)a.dk + t * a.ld_dk + sub * a.hs_dk : nullptr, HPW * a.hs_dk);
+            qp = next_q;
+            gqp = next_g;
+            kp += tokens * a.ld_k;
+            gkp += tokens * a.d.hkv * D;
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sums[(at ? kKind : 0) + e] += acc[e];
     }
     if (!a.ws) return;
     __syncthreads();
-    const float *all = reinterpret_cast<const float *>(all_turns + kPrepWarps * a.half);
     for (int i = threadIdx.x; i < 2 * D; i += kPrepThreads) {
         const int kind = i / D, c = i - kind * D;
+        // the lane and value that hold column c
+        const int at = MODE != kHalves || c >= 2 * a.half ? c : c < a.half ? (c >> 2) * 8 + (c & 3) : ((c - a.half) >> 2) * 8 + 4 + (c & 3);
         float s = 0.f;
-        for (int w = 0; w < kPrepWarps * HPW; ++w) s += all[kind * kKind + ((w / HPW) * 32 + (w % HPW) * LPR) * 8 + c];
+        for (int w = 0; w < kPrepWarps * HPW; ++w) s += all[kind * kKind + ((w / HPW) * 32 + (w % HPW) * LPR) * 8 + at];
         a.ws[((long long)blockIdx.x * 2 + kind) * D + c] = s;
     }
 }
@@ -425,37 +559,45 @@ __global__ void __launch_bounds__(256) attn_prep_weights_kernel(const AttnPrepAr
     if (lane == 0) to[c] = s;
 }
 
-// Blocks of a backward call: as many as run at once, each over several tokens.
-int backward_blocks(long long T) {
-    const long long most = (long long)sm_count() * 2, all = (T + kPrepWarps - 1) / kPrepWarps;
+// Blocks of a call: as many as run at once, each warp over several tokens.
+int prep_blocks(long long T, int per_sm) {
+    const long long most = (long long)sm_count() * per_sm, all = (T + kPrepWarps - 1) / kPrepWarps;
     return (int)(all < 1 ? 1 : all < most ? all : most);
 }
+int backward_blocks(long long T) { return prep_blocks(T, 2); }
 
-// Warps of a token: one, or in batches too small to fill the GPU so many that each has a head or a few.
-int warps_per_token(const AttnPrepArgs &a) {
-    const int heads = a.d.hq + (a.k ? a.d.hkv : 0) + (a.k_pages ? a.d.hkv : 0), hpw = 256 / a.d.D;
-    const long long want = (long long)sm_count() * 24 / a.T, most = (heads + hpw - 1) / hpw;
-    return (int)(want < 1 ? 1 : want < most ? want : most);
+template <typename K> cudaError_t with_smem(K kernel, int bytes) {
+    return bytes <= 48 * 1024 ? cudaSuccess : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
 template <typename T, int D, int MODE> cudaError_t run_prep(const AttnPrepArgs &a, cudaStream_t s) {
-    const int split = warps_per_token(a);
-    const long long blocks = (a.T * split + kPrepWarps - 1) / kPrepWarps;
-    attn_prep_kernel<T, D, MODE><<<(unsigned)blocks, kPrepThreads, kPrepWarps * a.half * 8, s>>>(a, split);
+    const int hpw = 256 / D, smem = kPrepWarps * kPrepTokens * a.half * 8, blocks = prep_blocks(a.T, kPrepBlocks);
+    // a token's heads over several warps where there are few tokens
+    const long long most = (a.d.hq + hpw - 1) / hpw, want = (long long)sm_count() * 24 / a.T;
+    const unsigned split = (unsigned)(want < 1 ? 1 : want < most ? want : most);
+    const bool plain = MODE == kHalves && split == 1 && a.hs_q == D && (!a.k || a.hs_k == D) && (!a.k_pages || a.hs_v == D);
+    const auto kernel = plain ? attn_prep_kernel<T, D, MODE, MODE == kHalves> : attn_prep_kernel<T, D, MODE, false>;
+    const cudaError_t e = with_smem(kernel, smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<dim3((unsigned)blocks, split), kPrepThreads, smem, s>>>(a);
     return cudaGetLastError();
 }
 template <typename T, int D, int MODE> cudaError_t run_backward(const AttnPrepArgs &a, cudaStream_t s) {
-    const int blocks = backward_blocks(a.T);
-    attn_prep_backward_kernel<T, D, MODE><<<blocks, kPrepThreads, kPrepWarps * (a.half * 8 + 2 * 32 * 8 * 4), s>>>(a);
-    const cudaError_t e = cudaGetLastError();
+    const int blocks = backward_blocks(a.T), smem = 2 * kPrepThreads * 8 * 4 + kPrepWarps * kPrepTokens * a.half * 8;
+    const bool plain = MODE == kHalves && a.hs_q == D && (!a.k || a.hs_k == D);
+    const auto kernel = plain ? attn_prep_backward_kernel<T, D, MODE, MODE == kHalves> : attn_prep_backward_kernel<T, D, MODE, false>;
+    cudaError_t e = with_smem(kernel, smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<blocks, kPrepThreads, smem, s>>>(a);
+    e = cudaGetLastError();
     if (e != cudaSuccess || !a.ws) return e;
     return launch_early(attn_prep_weights_kernel, dim3((2 * D + 7) / 8), 256, 0, s, a, blocks);
 }
 
-int mode_of(const AttnPrepArgs &a) { return a.interleaved ? kPairs : a.half % 8 == 0 ? kLanes : kAny; }
+int mode_of(const AttnPrepArgs &a) { return a.interleaved ? kPairs : a.half % 4 == 0 ? kHalves : kAny; }
 
 #define GDN_PREP_MODES(RUN, T, D)                                                                    \
-    return mode_of(a) == kLanes ? RUN<T, D, kLanes>(a, s) : mode_of(a) == kPairs ? RUN<T, D, kPairs>(a, s) : RUN<T, D, kAny>(a, s)
+    return mode_of(a) == kHalves ? RUN<T, D, kHalves>(a, s) : mode_of(a) == kPairs ? RUN<T, D, kPairs>(a, s) : RUN<T, D, kAny>(a, s)
 #define GDN_PREP_DIMS(RUN, T)                \
     if (a.d.D == 64) GDN_PREP_MODES(RUN, T, 64);   \
     if (a.d.D == 128) GDN_PREP_MODES(RUN, T, 128); \
