@@ -53,7 +53,7 @@ struct AttnDecodeArgs {
     int ctas;
 };
 // Most CTAs that share the work of a decode: the workspace is laid out for them.
-constexpr int kAttnCtasPerSm = 2;
+constexpr int kAttnCtasPerSm = 2, kAttnMaxCtas = 512;
 
 constexpr float kLn2 = 0.6931471805599453f;
 __host__ __device__ inline long long attn_part_floats(int rows, int D) { return (long long)rows * D + ((2 * rows + 3) & ~3); }

@@ -182,49 +182,52 @@ __global__ void __launch_bounds__(kSimtThreads) attn_decode_simt_kernel(const At
     }
 }
 
-// One query row of a unit that several CTAs hold: block (c, row) adds up the parts of the unit whose front is
-// CTA c's, part p in CTA c + p.
-constexpr int kJoinThreads = 256;
+// Adds up the parts of the units that several CTAs hold: part p of the unit whose front is CTA c's lies in CTA c + p.  Blocks
+// (c, y) take query rows: one at a time, groups of D / 4 threads taking parts in turn, or, where rows are many and parts few,
+// a row a group.
+constexpr int kJoinThreads = 256, kJoinRows = 16;
+struct Joined {
+    float m, l;
+    float4 o;
+    __device__ __forceinline__ void add(float pm, float pl, const float4 &po) {
+        const float nm = fmaxf(m, pm), ref = nm == -INFINITY ? 0.f : nm;
+        const float fa = exp2_fast(m - ref), fb = exp2_fast(pm - ref);
+        l = l * fa + pl * fb;
+        o = make_float4(o.x * fa + po.x * fb, o.y * fa + po.y * fb, o.z * fa + po.z * fb, o.w * fa + po.w * fb);
+        m = nm;
+    }
+};
 template <typename T, int D> __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnDecodeArgs a) {
     constexpr int COLS = D / 4, GROUPS = kJoinThreads / COLS;
     __shared__ float4 acc[GROUPS][COLS];
-    __shared__ float tops[GROUPS], totals[GROUPS];
+    __shared__ float2 stats[GROUPS];
+    const int tid = threadIdx.x, group = tid / COLS, col = tid % COLS, rows = a.d.grp * a.tokens;
+    let_next_start();
     await_previous();
     const int4 j = a.joins[blockIdx.x];
     if (j.w < 2) return;
-    const int rows = a.d.grp * a.tokens, row = blockIdx.y, tid = threadIdx.x, group = tid / COLS, col = tid % COLS;
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int p = group; p < j.w; p += GROUPS) {
-        const float *part = attn_part(a, blockIdx.x + p, p == 0 ? j.z : 0);
-        const float pm = part[rows * D + 2 * row], pl = part[rows * D + 2 * row + 1];
-        const float4 po = *reinterpret_cast<const float4 *>(part + row * D + col * 4);
-        const float nm = fmaxf(m, pm), ref = nm == -INFINITY ? 0.f : nm;
-        const float fa = exp2_fast(m - ref), fb = exp2_fast(pm - ref);
-        l = l * fa + pl * fb;
-        o = make_float4(o.x * fa + po.x * fb, o.y * fa + po.y * fb, o.z * fa + po.z * fb, o.w * fa + po.w * fb);
-        m = nm;
+    const bool shared = rows <= kJoinRows || j.w > 4;       // a row by all groups
+    const int sharing = shared ? GROUPS : 1;
+    for (int row = shared ? blockIdx.y : blockIdx.y * GROUPS + group; row < rows; row += gridDim.y * (shared ? 1 : GROUPS)) {
+        Joined x{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+        for (int p = shared ? group : 0; p < j.w; p += sharing) {      // (four at a time were slower: 52.6 -> 56.8 us a call of 76 parts)
+            const float *part = attn_part(a, blockIdx.x + p, p == 0 ? j.z : 0);
+            const float2 ml = *reinterpret_cast<const float2 *>(part + rows * D + 2 * row);
+            x.add(ml.x, ml.y, *reinterpret_cast<const float4 *>(part + row * D + col * 4));
+        }
+        if (shared) {
+            __syncthreads();                                // the row before has been read
+            acc[group][col] = x.o;
+            if (col == 0) stats[group] = make_float2(x.m, x.l);
+            __syncthreads();
+            if (group != 0) continue;
+            for (int g = 1; g < GROUPS; ++g) x.add(stats[g].x, stats[g].y, acc[g][col]);
+        }
+        const long long orow = ((long long)j.x * a.tokens + row / a.d.grp) * a.d.hq + j.y * a.d.grp + row % a.d.grp;
+        const float inv = x.l == 0.f ? 0.f : 1.f / x.l;
+        store4f((T *)a.out + orow * D + col * 4, make_float4(x.o.x * inv, x.o.y * inv, x.o.z * inv, x.o.w * inv));
+        if (col == 0 && a.lse) a.lse[orow] = x.l == 0.f ? -INFINITY : (x.m + log2f(x.l)) * kLn2;
     }
-    acc[group][col] = o;
-    if (col == 0) {
-        tops[group] = m;
-        totals[group] = l;
-    }
-    __syncthreads();
-    if (group != 0) return;
-    for (int g = 1; g < GROUPS; ++g) {
-        const float pm = tops[g], pl = totals[g];
-        const float4 po = acc[g][col];
-        const float nm = fmaxf(m, pm), ref = nm == -INFINITY ? 0.f : nm;
-        const float fa = exp2_fast(m - ref), fb = exp2_fast(pm - ref);
-        l = l * fa + pl * fb;
-        o = make_float4(o.x * fa + po.x * fb, o.y * fa + po.y * fb, o.z * fa + po.z * fb, o.w * fa + po.w * fb);
-        m = nm;
-    }
-    const long long orow = ((long long)j.x * a.tokens + row / a.d.grp) * a.d.hq + j.y * a.d.grp + row % a.d.grp;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    store4f((T *)a.out + orow * D + col * 4, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-    if (col == 0 && a.lse) a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 template <typename T, int D, int RPW> cudaError_t run_simt(const AttnDecodeArgs &a, cudaStream_t s) {
@@ -248,20 +251,26 @@ template <typename T> cudaError_t run_dim(const AttnDecodeArgs &a, cudaStream_t 
     return a.d.D == 64 ? run_rows<T, 64>(a, s) : a.d.D == 128 ? run_rows<T, 128>(a, s) : run_rows<T, 256>(a, s);
 }
 
+int most_ctas() {
+    const int n = sm_count() * kAttnCtasPerSm;
+    return n < kAttnMaxCtas ? n : kAttnMaxCtas;
+}
+
 }  // namespace
 
 size_t attn_decode_ws_bytes(const AttnDims &d, int rows) {
-    return (size_t)sm_count() * kAttnCtasPerSm * (sizeof(int4) + 2 * (size_t)attn_part_floats(rows, d.D) * 4);
+    return (size_t)most_ctas() * (sizeof(int4) + 2 * (size_t)attn_part_floats(rows, d.D) * 4);
 }
 
 void attn_decode_carve(AttnDecodeArgs &a, void *ws) {
-    a.ctas = sm_count() * kAttnCtasPerSm;
+    a.ctas = most_ctas();
     a.joins = (int4 *)ws;
     a.parts = (float *)(a.joins + a.ctas);
 }
 
 cudaError_t launch_attn_join(const AttnDecodeArgs &a, bool act_bf16, cudaStream_t s) {
-    const dim3 grid(a.ctas, a.d.grp * a.tokens);
+    const int rows = a.d.grp * a.tokens;
+    const dim3 grid(a.ctas, rows < kJoinRows ? rows : kJoinRows);
     if (act_bf16)
         return a.d.D == 64 ? launch_early(attn_join_kernel<__nv_bfloat16, 64>, grid, kJoinThreads, 0, s, a)
              : a.d.D == 128 ? launch_early(attn_join_kernel<__nv_bfloat16, 128>, grid, kJoinThreads, 0, s, a)

@@ -1,18 +1,17 @@
 // attn_decode_tc.cu -- attention of a few new tokens over a paged bf16 cache, on the tensor cores.
 //
 // The shares, parts and join of attn_decode.cu; here a tile is 64 tokens.  One warp copies tiles with TMA into a ring of
-// shared-memory entries (K and V of a tile in entries of their own, 128-byte swizzled), eight warps compute in two sets
-// of four that take turns with the tiles:
-//   S = Q K^T    warp w of a set the tile's tokens 16 w .. 16 w + 15, for all query rows
-//   P = exp(S - m), the set's four warps having passed each other the rows' maxima; m, l and o in 32 bits
-//   O += P V     warp w the columns D/4 w .. of all rows, P passed through shared memory
-// so every byte of K and V is read from shared memory once, however many query rows there are.  The sets' sums are
-// added where a unit ends.
+// shared-memory entries (K and V of a tile in entries of their own, 128-byte swizzled).  Groups of four warps compute:
+//   S = Q K^T    warp w the tile's tokens 16 w .. 16 w + 15, for the group's query rows
+//   P = exp(S - m), the four warps having passed each other the rows' maxima; m, l and o in 32 bits
+//   O += P V     warp w the columns D/4 w .. of the group's rows, P passed through shared memory
+// so that a byte of K and V is read from shared memory once for up to 32 query rows.  Groups of other rows take the same
+// tiles; groups of the same rows (sets) take turns with them, and their sums are added where a unit ends.
 //
-// HBM-bound by design: 16 rows of m16n8k16 products need 16 operations a byte of the cache.  (The products run as
-// mma.sync: a tcgen05 product has 64 or 128 rows, and the sums over tokens of its transposed form lie across lanes.)
-// P is split in two bf16 parts, so that o loses nothing but its own rounding; the second product is hidden behind the
-// loads.
+// HBM-bound by design: 16 rows of m16n8k16 products need 16 operations a byte of the cache, 64 rows 64: at the 600
+// TFLOP/s that these products reach on this GPU, 0.2 and 0.7 of the time that the bytes take.  (They run as mma.sync: a
+// tcgen05 product has 64 or 128 rows, and the sums over tokens of its transposed form lie across lanes.)
+// P is split in two bf16 parts, so that o loses nothing but its own rounding.
 #include <cuda.h>
 
 #include "attn_common.cuh"
@@ -23,27 +22,29 @@ namespace gdn {
 namespace {
 
 constexpr int kTile = 64;
-constexpr int kConsumers = 256;                    // eight warps, two sets of four
-constexpr int kThreads = kConsumers + 32;
-constexpr int kUnits = 2;                          // query blocks in flight
 constexpr int kPPitch = kTile * 2 + 16;            // bytes of a row of P: ldmatrix without bank conflicts
-constexpr int kMaxEntries = 16;
+constexpr int kMaxEntries = 24;
 
 // A unit's tiles in this CTA, as the copying warp describes them.
 struct Unit {
     int n, h, len, first, i0, count, seq0, slot;   // slot -1: the unit is whole
 };
 
-template <int D, int MT> struct Smem {
-    static constexpr int entry = kTile * D * 2, q_pitch = D * 2 + 16, q_block = 16 * MT * q_pitch;
-    static constexpr int p_block = 16 * MT * kPPitch, merge = 16 * MT * D * 4;
-    static constexpr int fixed = kUnits * q_block + 4 * p_block + merge + 2 * 4 * 16 * MT * 4 * 2 + 16 * MT * 8 + 1024;
+// MT blocks of 16 query rows a group, GR groups of rows, GS sets of each.
+template <int D, int MT, int GR, int GS> struct Shape {
+    static constexpr int groups = GR * GS, consumers = groups * 128, threads = consumers + 32, rows = 16 * MT * GR;
+    static constexpr int units = MT > 1 ? 1 : 2;           // query blocks in flight
+    static constexpr int entry = kTile * D * 2, q_pitch = D * 2 + 16, q_block = rows * q_pitch;
+    static constexpr int p_block = 16 * MT * kPPitch, merge = 16 * MT * D * 4;     // merge: of each set but the first
+    static constexpr int stats = groups * 16 * MT;         // rows of all groups
+    static constexpr int fixed = units * q_block + 2 * groups * p_block + GR * (GS - 1) * merge + stats * (4 * 4 * 2 + 8) + 1024;
     static constexpr int limit = 227 * 1024 - 1024;
-    static constexpr int fit = (limit - fixed) / entry;
-    // a multiple of four: an entry then serves tiles of one set alone, and no waiter is ever two phases behind its barrier
-    static constexpr int entries = fit < kMaxEntries ? fit / 4 * 4 : kMaxEntries;
+    static constexpr int fit = (limit - fixed) / entry, turn = 2 * GS;
+    // a multiple of the sets' entries: an entry then serves tiles of one set alone, and no waiter is ever two phases
+    // behind its barrier
+    static constexpr int entries = fit < kMaxEntries ? fit / turn * turn : kMaxEntries;
     static constexpr int bytes = fixed + entries * entry;      // 1,024 of `fixed` to align the entries
-    static_assert(entries >= 4 && entries % 4 == 0, "two tiles in flight, each set's in entries of its own");
+    static_assert(entries >= turn && entries % turn == 0, "a tile of each set in flight, in entries of its own");
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -59,7 +60,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(threads) : "memory"); }
-__device__ __forceinline__ void bar_arrive(int id, int threads) { asm volatile("bar.arrive %0, %1;" :: "r"(id), "r"(threads) : "memory"); }
 // Whether all threads of the barrier say so.
 __device__ __forceinline__ bool bar_all(int id, int threads, bool mine) {
     int all;
@@ -67,7 +67,7 @@ __device__ __forceinline__ bool bar_all(int id, int threads, bool mine) {
                  : "=r"(all) : "r"(id), "r"(threads), "r"((int)mine) : "memory");
     return all != 0;
 }
-enum { kBarUnit = 1, kBarSet = 2, kBarMerge = 4 };
+enum { kBarGroup = 1 };              // the first group's named barrier
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -82,43 +82,48 @@ struct Maps {
     CUtensorMap k, v;
 };
 
-template <int D, int MT>
-__global__ void __launch_bounds__(kThreads, 1) attn_decode_tc_kernel(const AttnDecodeArgs a, const __grid_constant__ Maps maps) {
-    using S = Smem<D, MT>;
-    constexpr int KS = D / 16, ROWS = 16 * MT, NT = D / 32;        // NT: 8-column blocks of a warp's share of O
+template <int D, int MT, int GR, int GS>
+__global__ void __launch_bounds__((Shape<D, MT, GR, GS>::threads), 1) attn_decode_tc_kernel(const AttnDecodeArgs a, const __grid_constant__ Maps maps) {
+    using S = Shape<D, MT, GR, GS>;
+    constexpr int KS = D / 16, ROWS = S::rows, GROWS = 16 * MT, NT = D / 32;       // NT: 8-column blocks of a warp's share of O
+    constexpr int kUnits = S::units, kThreads = S::threads, kConsumers = S::consumers;
     constexpr uint32_t E = S::entries;
     extern __shared__ unsigned char raw[];
     __shared__ long long sums[33];
-    __shared__ int found[3], lost;
-    __shared__ uint64_t bars[2 * kMaxEntries + 2 * kUnits];
+    __shared__ int found[3];
+    __shared__ uint64_t bars[2 * kMaxEntries + 2 * kUnits + 2 * GR];
     __shared__ int pieces_of[kMaxEntries];                          // which 16-token pieces of an entry's tile are there
     __shared__ Unit units[kUnits];
     unsigned char *base = raw + ((1024u - (tc::smem_u32(raw) & 1023u)) & 1023u);
     unsigned char *q_mem = base + E * S::entry, *p_mem = q_mem + kUnits * S::q_block;
-    float *merge = reinterpret_cast<float *>(p_mem + 4 * S::p_block);
-    float *tops = merge + ROWS * D;                                 // [2 sets][ROWS][4 warps]
-    float *totals = tops + 2 * ROWS * 4;                            // the same
-    float2 *stats = reinterpret_cast<float2 *>(totals + 2 * ROWS * 4);   // [ROWS]: m and l of set 1
+    float *merge = reinterpret_cast<float *>(p_mem + 2 * S::groups * S::p_block);  // [sets - 1][groups of rows][GROWS][D]
+    float *tops = merge + GR * (GS - 1) * GROWS * D;                // [groups][GROWS][4 warps]
+    float *totals = tops + S::stats * 4;                            // the same
+    float2 *stats = reinterpret_cast<float2 *>(totals + S::stats * 4);   // [groups][GROWS]: m and l
     const uint32_t entries = tc::smem_u32(base), full = tc::smem_u32(bars), empty = full + 8 * kMaxEntries,
-                   ufull = empty + 8 * kMaxEntries, uempty = ufull + 8 * kUnits;
+                   ufull = empty + 8 * kMaxEntries, uempty = ufull + 8 * kUnits, merged = uempty + 8 * kUnits, taken = merged + 8 * GR;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rows = a.d.grp * a.tokens, row0 = blockIdx.y * ROWS, mine = min(ROWS, rows - row0);
-    let_next_start();
     if (tid == 0) {
         for (uint32_t e = 0; e < E; ++e) {
             tc::mbar_init(full + 8 * e, 1);
-            tc::mbar_init(empty + 8 * e, 4);
+            tc::mbar_init(empty + 8 * e, 4 * GR);
         }
         for (int u = 0; u < kUnits; ++u) {
             tc::mbar_init(ufull + 8 * u, 1);
             tc::mbar_init(uempty + 8 * u, kConsumers / 32);
         }
+        for (int r = 0; r < GR; ++r) {
+            tc::mbar_init(merged + 8 * r, 4 * (GS - 1) + (GS == 1));
+            tc::mbar_init(taken + 8 * r, 4);
+        }
         tc::mbar_fence_init();
-        lost = 0;
     }
     // rows that pad the query block stay zero
     for (int i = tid; i < kUnits * S::q_block / 16; i += kThreads) reinterpret_cast<uint4 *>(q_mem)[i] = make_uint4(0u, 0u, 0u, 0u);
     tc::fence_async_smem();
+    await_previous();
+    let_next_start();
     AttnWalk w;
     const bool work = attn_begin<kTile, kThreads>(a, blockIdx.x, sums, found, w);      // synchronises the block
     if (!work) {
@@ -134,23 +139,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_tc_kernel(const AttnD
         const uint32_t box_bytes = piece * 128u, at = my_col * (kTile * 128u) + my_piece * box_bytes;
         uint32_t e = 0, phase = 0, issued = 0;
         int seq = 0, u = 0;
-        bool alive = true, unit_first = true;
-        while (w.left > 0 && alive) {
-            const AttnSeq s = w.s;
-            const int n = w.n, h = w.h, count = (int)min((long long)(s.tiles - w.t), w.left), t0 = w.t;
-            const bool whole = t0 == 0 && count == s.tiles;
-            const int slot = whole ? -1 : unit_first ? 0 : 1;
-            const int32_t *row = a.table + (long long)s.row * a.d.max_pages;
-            // the page of this lane's piece of tile t; -1: not there
-            auto page_of = [&](int t) {
-                const int i = (s.tile0 + t) * kTile + (my_piece << shift);
-                if (lane >= boxes || i >= s.len || i + piece <= s.first) return -1;
-                const int p = row[i >> a.d.page_shift];
-                if (p >= 0 && p < a.d.n_pages) return p;
-                set_error(a.err, GDN_DEVERR_PAGE);
-                return -1;
-            };
-            int page = page_of(t0);
+        bool alive = true;
+        // the page of this lane's piece of tile t of a sequence; -1: not there
+        auto page_of = [&](const AttnSeq &s, int t) {
+            const int i = (s.tile0 + t) * kTile + (my_piece << shift);
+            if (lane >= boxes || i >= s.len || i + piece <= s.first) return -1;
+            const int p = a.table[(long long)s.row * a.d.max_pages + (i >> a.d.page_shift)];
+            if (p >= 0 && p < a.d.n_pages) return p;
+            set_error(a.err, GDN_DEVERR_PAGE);
+            return -1;
+        };
+        AttnSeq s = w.s;
+        int n = w.n, h = w.h, t0 = w.t, page = page_of(s, t0);
+        for (long long left = w.left; left > 0 && alive; ++u) {
+            const int count = (int)min((long long)(s.tiles - t0), left);
+            const bool unit_end = t0 + count == s.tiles;
+            const int slot = t0 == 0 && unit_end ? -1 : u == 0 ? 0 : 1;
             const uint32_t us = u % kUnits, uphase = (u / kUnits) & 1;
             if (u >= kUnits) alive = tc::mbar_wait(uempty + 8 * us, uphase ^ 1, a.wait_ns);
             alive = __all_sync(0xffffffffu, alive);
@@ -166,10 +170,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_tc_kernel(const AttnD
                              (const __nv_bfloat16 *)a.q + ((long long)n * a.tokens + tok) * a.ld_q + (long long)(h * a.d.grp + g) * a.hs_q, D * 2,
                              ufull + 8 * us);
             }
-            ++u;
+            // the unit behind this one, and where its first tile lies: known before this one's last tile is asked for
+            AttnSeq next_s = s;
+            int next_n = n, next_h = h + 1, next_page = -1;
             for (int j = 0; j < count && alive; ++j) {
                 const int here = page, i0 = (s.tile0 + t0 + j) * kTile;
-                if (j + 1 < count) page = page_of(t0 + j + 1);
+                if (j + 1 < count) page = page_of(s, t0 + j + 1);
                 const unsigned there = __ballot_sync(0xffffffffu, here >= 0);
                 const uint32_t bytes = __popc(there) * box_bytes;
                 // the row of the pools where this lane's piece begins
@@ -197,17 +203,27 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_tc_kernel(const AttnD
                         phase ^= 1;
                     }
                 }
+                if (j == 0 && left > count) {
+                    if (next_h == a.d.hkv) {
+                        next_h = 0;
+                        next_s = attn_seq<kTile>(a, ++next_n);
+                    }
+                    next_page = page_of(next_s, 0);
+                }
             }
             seq += count;
-            bool unit_end = false;
-            for (int j = 0; j < count; ++j) unit_end = attn_next<kTile>(a, w);
-            if (w.left == 0 && blockIdx.y == 0 && lane == 0) {
+            left -= count;
+            if (left == 0 && blockIdx.y == 0 && lane == 0) {
                 // the CTA that holds a unit's front joins it: the CTAs behind that hold the rest
                 int parts = 0;
                 if (!unit_end && t0 == 0) parts = 1 + (int)((s.tiles - count + w.per - 1) / w.per);
-                a.joins[blockIdx.x] = make_int4(n, h, unit_first ? 0 : 1, parts);
+                a.joins[blockIdx.x] = make_int4(n, h, u == 0 ? 0 : 1, parts);
             }
-            unit_first = false;
+            s = next_s;
+            n = next_n;
+            h = next_h;
+            t0 = 0;
+            page = next_page;
         }
         if (lane == 0) {
             if (!alive) {             // nothing more is copied
@@ -228,15 +244,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_tc_kernel(const AttnD
     }
 
     // ---------------------------------------------------------------- products
-    const int set = warp >> 2, wg = warp & 3, g = lane >> 2, t4 = lane & 3;
+    const int group = warp >> 2, wg = warp & 3, rg = group % GR, set = group / GR, g = lane >> 2, t4 = lane & 3, row_g = rg * GROWS;
     int token[MT][2];                                   // the new token of this thread's rows
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-        token[mt][0] = min((row0 + mt * 16 + g) / a.d.grp, a.tokens - 1);
-        token[mt][1] = min((row0 + mt * 16 + g + 8) / a.d.grp, a.tokens - 1);
+        token[mt][0] = min((row0 + row_g + mt * 16 + g) / a.d.grp, a.tokens - 1);
+        token[mt][1] = min((row0 + row_g + mt * 16 + g + 8) / a.d.grp, a.tokens - 1);
     }
-    const uint32_t p_hi = tc::smem_u32(p_mem) + set * 2 * S::p_block, p_lo = p_hi + S::p_block;
-    float *my_tops = tops + set * ROWS * 4, *my_totals = totals + set * ROWS * 4;
+    const uint32_t p_hi = tc::smem_u32(p_mem) + group * 2 * S::p_block, p_lo = p_hi + S::p_block;
+    float *my_tops = tops + group * GROWS * 4, *my_totals = totals + group * GROWS * 4;
     // ldmatrix addresses: rows of Q and P, tokens of K and V
     const uint32_t q_lane = (lane & 15) * S::q_pitch + (lane >> 4) * 16, p_lane = (lane & 15) * kPPitch + (lane >> 4) * 16;
     const uint32_t k_token = wg * 16 + (lane & 7) + ((lane >> 4) << 3), k_half = (lane >> 3) & 1;
@@ -246,13 +262,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_tc_kernel(const AttnD
     int u = 0;
     for (long long left = w.left; left > 0; ++u) {
         const uint32_t us = u % kUnits;
-        if (!bar_all(kBarUnit, kConsumers, ok && tc::mbar_wait(ufull + 8 * us, (u / kUnits) & 1, a.wait_ns))) {
+        // a group's warps give up together: they meet at its barrier
+        if (!bar_all(kBarGroup + group, 128, ok && tc::mbar_wait(ufull + 8 * us, (u / kUnits) & 1, a.wait_ns))) {
             ok = false;
             break;
         }
         const Unit unit = units[us];
         left -= unit.count;
-        const uint32_t q_base = tc::smem_u32(q_mem) + us * S::q_block + q_lane;
+        const uint32_t q_base = tc::smem_u32(q_mem) + us * S::q_block + row_g * S::q_pitch + q_lane;
         float m[MT][2], l[MT][2], o[MT][NT][4];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
@@ -263,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_tc_kernel(const AttnD
         }
         // what all rows see lies below `open`, and not below `wide`
         const int open = unit.len - a.tokens + 1, wide = a.window > 0 ? unit.len - a.window : 0;
-        for (int j = (unit.seq0 & 1) ^ set; j < unit.count; j += 2) {
+        for (int j = (set - unit.seq0) & (GS - 1); j < unit.count; j += GS) {
             const int i0 = unit.i0 + j * kTile;
             const uint32_t v_e = e + 1;                 // V follows its K
             if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(full + 8 * e, phase, a.wait_ns));
@@ -311,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_tc_kernel(const AttnD
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                     if (t4 == 0) my_tops[(mt * 16 + r * 8 + g) * 4 + wg] = top;
                 }
-            bar_sync(kBarSet + set, 128);
+            bar_sync(kBarGroup + group, 128);
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -338,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_tc_kernel(const AttnD
                         asm volatile("st.shared.b32 [%0], %1;" :: "r"(p_lo + row + c * 16), "r"(lo) : "memory");
                     }
                 }
-            bar_sync(kBarSet + set, 128);
+            bar_sync(kBarGroup + group, 128);
             if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(full + 8 * v_e, phase, a.wait_ns));
             const uint32_t v_base = entries + v_e * S::entry;
             auto v_addr = [&](int ks, int pair) {
@@ -417,15 +434,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_tc_kernel(const AttnD
             }
             __syncwarp();
             if (ok && lane == 0) tc::mbar_arrive(empty + 8 * v_e);
-            e += 4;
+            e += 2 * GS;
             if (e >= E) {
                 e -= E;
                 phase ^= 1;
             }
         }
         if (ok && lane == 0) tc::mbar_arrive(uempty + 8 * us);
-        // the rows' sums over the set's warps; then set 1's into set 0's
-        if (!ok) lost = 1;
+        // the rows' sums over the group's warps; then the sets' together, by the first one, while the others go on
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -435,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_tc_kernel(const AttnD
                 v += __shfl_xor_sync(0xffffffffu, v, 2);
                 if (t4 == 0) my_totals[(mt * 16 + r * 8 + g) * 4 + wg] = v;
             }
-        bar_sync(kBarSet + set, 128);
+        bar_sync(kBarGroup + group, 128);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -444,7 +460,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_tc_kernel(const AttnD
                 l[mt][r] = (v.x + v.y) + (v.z + v.w);
             }
         const int col0 = wg * (D / 4) + t4 * 2;
-        if (set == 1) {
+        if (GS > 1 && set > 0) {
+            if (u > 0 && ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(taken + 8 * rg, (u - 1) & 1, a.wait_ns));
+            float *mine_o = merge + ((set - 1) * GR + rg) * GROWS * D;
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -452,31 +470,52 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_tc_kernel(const AttnD
                     const int row = mt * 16 + r * 8 + g;
 #pragma unroll
                     for (int c = 0; c < NT; ++c)
-                        *reinterpret_cast<float2 *>(merge + row * D + col0 + c * 8) = make_float2(o[mt][c][2 * r], o[mt][c][2 * r + 1]);
-                    if (wg == 0 && t4 == 0) stats[row] = make_float2(m[mt][r], l[mt][r]);
+                        *reinterpret_cast<float2 *>(mine_o + row * D + col0 + c * 8) = make_float2(o[mt][c][2 * r], o[mt][c][2 * r + 1]);
+                    if (wg == 0 && t4 == 0) stats[group * GROWS + row] = make_float2(m[mt][r], l[mt][r]);
                 }
-            bar_arrive(kBarMerge, kConsumers);
+            __syncwarp();
+            if (ok && lane == 0) tc::mbar_arrive(merged + 8 * rg);
             continue;
         }
-        bar_sync(kBarMerge, kConsumers);
-        if (*(volatile int *)&lost) continue;
+        if (GS > 1 && ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(merged + 8 * rg, u & 1, a.wait_ns));
+        if (!ok) continue;
         float *part = attn_part(a, blockIdx.x, max(unit.slot, 0));
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const int row = mt * 16 + r * 8 + g;
+                const int in_group = mt * 16 + r * 8 + g, row = row_g + in_group;
                 if (row >= mine) continue;
-                const float2 other = stats[row];
-                const float nm = fmaxf(m[mt][r], other.x), ref = nm == -INFINITY ? 0.f : nm;
-                const float fa = exp2_fast(m[mt][r] - ref), fb = exp2_fast(other.x - ref), total = l[mt][r] * fa + other.y * fb;
+                // the sets' sums on the largest of their maxima
+                float top = m[mt][r];
+#pragma unroll
+                for (int k = 1; k < GS; ++k) top = fmaxf(top, stats[(k * GR + rg) * GROWS + in_group].x);
+                const float ref = top == -INFINITY ? 0.f : top, own = exp2_fast(m[mt][r] - ref);
+                float total = l[mt][r] * own;
+#pragma unroll
+                for (int c = 0; c < NT; ++c) {
+                    o[mt][c][2 * r] *= own;
+                    o[mt][c][2 * r + 1] *= own;
+                }
+#pragma unroll
+                for (int k = 1; k < GS; ++k) {
+                    const float2 other = stats[(k * GR + rg) * GROWS + in_group];
+                    const float f = exp2_fast(other.x - ref);
+                    total = fmaf(other.y, f, total);
+                    const float *from = merge + (((k - 1) * GR + rg) * GROWS + in_group) * D + col0;
+#pragma unroll
+                    for (int c = 0; c < NT; ++c) {
+                        const float2 x = *reinterpret_cast<const float2 *>(from + c * 8);
+                        o[mt][c][2 * r] = fmaf(x.x, f, o[mt][c][2 * r]);
+                        o[mt][c][2 * r + 1] = fmaf(x.y, f, o[mt][c][2 * r + 1]);
+                    }
+                }
                 const int tok = token[mt][r], head = unit.h * a.d.grp + row0 + row - tok * a.d.grp;
                 const long long orow = ((long long)unit.n * a.tokens + tok) * a.d.hq + head;
                 const float inv = unit.slot >= 0 ? 1.f : total == 0.f ? 0.f : 1.f / total;
 #pragma unroll
                 for (int c = 0; c < NT; ++c) {
-                    const float2 x = *reinterpret_cast<const float2 *>(merge + row * D + col0 + c * 8);
-                    const float v0 = (o[mt][c][2 * r] * fa + x.x * fb) * inv, v1 = (o[mt][c][2 * r + 1] * fa + x.y * fb) * inv;
+                    const float v0 = o[mt][c][2 * r] * inv, v1 = o[mt][c][2 * r + 1] * inv;
                     if (unit.slot >= 0)
                         *reinterpret_cast<float2 *>(part + (row0 + row) * D + col0 + c * 8) = make_float2(v0, v1);
                     else
@@ -484,11 +523,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_tc_kernel(const AttnD
                 }
                 if (wg == 0 && t4 == 0) {
                     if (unit.slot >= 0)
-                        *reinterpret_cast<float2 *>(part + rows * D + 2 * (row0 + row)) = make_float2(nm, total);
+                        *reinterpret_cast<float2 *>(part + rows * D + 2 * (row0 + row)) = make_float2(top, total);
                     else if (a.lse)
-                        a.lse[orow] = total == 0.f ? -INFINITY : (nm + log2f(total)) * kLn2;
+                        a.lse[orow] = total == 0.f ? -INFINITY : (top + log2f(total)) * kLn2;
                 }
             }
+        __syncwarp();
+        if (GS > 1 && lane == 0) tc::mbar_arrive(taken + 8 * rg);
     }
     if (!ok && lane == 0) set_error(a.err, GDN_DEVERR_TIMEOUT);
 }
@@ -519,25 +560,24 @@ bool encode(CUtensorMap *m, const void *pool, const AttnDims &d) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int MT> cudaError_t run(AttnDecodeArgs a, const Maps &maps, cudaStream_t s) {
-    constexpr int bytes = Smem<D, MT>::bytes;
-    const auto kernel = attn_decode_tc_kernel<D, MT>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+template <int D, int MT, int GR, int GS> cudaError_t run(AttnDecodeArgs a, const Maps &maps, cudaStream_t s) {
+    using S = Shape<D, MT, GR, GS>;
+    const auto kernel = attn_decode_tc_kernel<D, MT, GR, GS>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::bytes);
     if (e != cudaSuccess) return e;
     // blocks of query rows read the same tiles: at the same time, so that the second one finds them in L2
-    const int blocks = (a.d.grp * a.tokens + 16 * MT - 1) / (16 * MT);
+    const int blocks = (a.d.grp * a.tokens + S::rows - 1) / S::rows;
     a.ctas = sm_count() / blocks;
-    kernel<<<dim3(a.ctas, blocks), kThreads, bytes, s>>>(a, maps);
-    const cudaError_t l = cudaGetLastError();
+    const cudaError_t l = launch_early(kernel, dim3(a.ctas, blocks), S::threads, S::bytes, s, a, maps);
     return l != cudaSuccess ? l : launch_attn_join(a, true, s);
 }
 template <int D> cudaError_t run_rows(const AttnDecodeArgs &a, const Maps &maps, cudaStream_t s) {
     const int rows = a.d.grp * a.tokens;
-    if (rows <= 16) return run<D, 1>(a, maps, s);
     if constexpr (D == 256) {
-        return run<D, 2>(a, maps, s);
+        // two tiles fill shared memory
+        return rows <= 16 ? run<D, 1, 1, 2>(a, maps, s) : run<D, 1, 2, 1>(a, maps, s);
     } else {
-        return rows <= 32 ? run<D, 2>(a, maps, s) : run<D, 4>(a, maps, s);
+        return rows <= 16 ? run<D, 1, 1, 2>(a, maps, s) : rows <= 32 ? run<D, 1, 2, 2>(a, maps, s) : run<D, 1, 4, 1>(a, maps, s);
     }
 }
 
