@@ -175,11 +175,11 @@ def load(path: str | None = None):
             "gdn_block_norm": ([ctypes.POINTER(BlockNormIO), V], I32),
             "gdn_block_norm_workspace_size": ([I64, I32], SZ),
             "gdn_block_norm_backward": ([ctypes.POINTER(BlockNormIO), P, SZ, V], I32),
-            "gdn_attn_prep": ([ctypes.POINTER(AttnConfig), ctypes.POINTER(AttnPrepIO), V], I32),
+            "gdn_attn_prep": ([ctypes.POINTER(AttnConfig), P, V], I32),
             "gdn_attn_prep_workspace_size": ([ctypes.POINTER(AttnConfig), I64], SZ),
-            "gdn_attn_prep_backward": ([ctypes.POINTER(AttnConfig), ctypes.POINTER(AttnPrepIO), P, SZ, V], I32),
+            "gdn_attn_prep_backward": ([ctypes.POINTER(AttnConfig), P, P, SZ, V], I32),
             "gdn_attn_workspace_size": ([ctypes.POINTER(AttnConfig), I32, I32], SZ),
-            "gdn_attn_decode": ([ctypes.POINTER(AttnConfig), ctypes.POINTER(AttnDecodeIO), P, SZ, V], I32),
+            "gdn_attn_decode": ([ctypes.POINTER(AttnConfig), P, P, SZ, V], I32),
             "gdn_page_workspace_size": ([ctypes.POINTER(AttnConfig), I32], SZ),
             "gdn_page_resize": ([ctypes.POINTER(AttnConfig), P, P, P, P, P, I32, P, P, P, P, SZ, V], I32),
             "gdn_page_fork": ([ctypes.POINTER(AttnConfig), P, P, P, P, P, I32, V], I32),
@@ -503,20 +503,6 @@ class _Args:
             ld = shape[1]
         return t.data_ptr(), ld
 
-    def heads(self, t, name, shape, dtype):
-        """(pointer, token stride, head stride) of a [tokens, heads, dim] view with contiguous heads."""
-        if t is None:
-            return 0, 0, 0
-        if t.dtype is not dtype or t.shape != shape or t.get_device() != self.device:
-            self.explain(t, name, shape, dtype)
-        T, H, D = shape
-        if t.is_contiguous():
-            return t.data_ptr(), H * D, D
-        ld, hs, one = t.stride()
-        if one != 1:
-            self.refuse(name, "has heads that are not contiguous")
-        return t.data_ptr(), ld if T > 1 else H * D, hs if H > 1 else D
-
     def whole(self, t, name, shape, dtype):
         """Pointer of a contiguous tensor."""
         if t is None:
@@ -663,6 +649,9 @@ def gdn_block_norm_backward(res_out, rstd_pre=None, w_pre=None, dh=None, d_res_o
 
 
 # ------------------------------------------------- attention layers and their cache
+#
+# The checks of _Args as plain functions (a third of its time), and argument structures passed as packed bytes: a call's
+# host time counts where a decode step is not captured.
 
 def make_attn_config(q_heads, kv_heads, head_dim, page_size=64, act="bf16", n_pages=0, n_rows=0,
                      max_pages=0) -> AttnConfig:
@@ -670,26 +659,84 @@ def make_attn_config(q_heads, kv_heads, head_dim, page_size=64, act="bf16", n_pa
                       n_rows, max_pages)
 
 
-_prep_io, _decode_io = _packer(AttnPrepIO), _packer(AttnDecodeIO)
+def _bytes_packer(cls):
+    """The memory image of a structure from its fields' values in order, null pointers as 0."""
+    code = {ctypes.c_int32: "i", ctypes.c_int64: "q", ctypes.c_float: "f", ctypes.c_void_p: "P"}
+    return struct.Struct("@" + "".join(code[t] for _, t in cls._fields_) + "0P").pack
 
 
-def _prep_batch(a, T, cu_seqlens, tokens):
+_prep_io, _decode_io = _bytes_packer(AttnPrepIO), _bytes_packer(AttnDecodeIO)
+_get_device = _get_stream = _ACT = _F32 = _I32 = None
+
+
+def _start():
+    """What the functions below take from torch, at the first call."""
+    global _get_device, _get_stream, _ACT, _F32, _I32
+    _Args("")                                       # imports torch and initialises CUDA
+    _get_stream, _ACT, _F32, _I32 = _torch._C._cuda_getCurrentRawStream, (_torch.bfloat16, _torch.float32), _torch.float32, _torch.int32
+    load()
+    _get_device = _torch._C._cuda_getDevice
+
+
+def _whole(where, dev, t, name, shape, dtype):
+    """Pointer of a contiguous tensor; 0 for none."""
+    if t is None:
+        return 0
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _Args(where).explain(t, name, shape, dtype)
+
+
+def _heads(where, dev, t, name, shape, dtype):
+    """(pointer, token stride, head stride) of a [tokens, heads, dim] view with contiguous heads."""
+    if t is None:
+        return 0, 0, 0
+    if not (t.dtype is dtype and t.shape == shape and t.get_device() == dev):
+        _Args(where).explain(t, name, shape, dtype)
+    T, H, D = shape
+    ld, hs, one = t.stride()
+    if one != 1 and not t.is_contiguous():
+        _Args(where).refuse(name, "has heads that are not contiguous")
+    return t.data_ptr(), ld if T > 1 else H * D, hs if H > 1 else D
+
+
+def _pool(where, dev, t, name, n_pages, shape, dtype):
+    """Pointer of a contiguous pool of n_pages pages or more."""
+    if t is None:
+        return 0
+    have = t.shape
+    if len(have) == 4 and have[0] >= n_pages and t.dtype is dtype and have[1:] == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    a = _Args(where)
+    if not have or have[0] < n_pages:
+        a.refuse(name, "has fewer than the configuration's %d pages" % n_pages)
+    a.explain(t, name, (have[0],) + shape, dtype)
+
+
+def _workspace(where, dev, t):
+    if t is None:
+        return 0, 0
+    if t.get_device() != dev or not t.is_contiguous():
+        _Args(where).bytes_of(t)
+    return t.data_ptr(), t.nbytes
+
+
+def _on(stream, dev):
+    return _get_stream(dev) if stream is None else getattr(stream, "cuda_stream", stream)
+
+
+def _prep_batch(where, dev, T, cu_seqlens, tokens):
     """(pointer of cu_seqlens, sequences): packed by bounds, or `tokens` to each sequence (None: one sequence)."""
     if cu_seqlens is not None:
         if tokens is not None:
-            a.refuse("tokens", "and cu_seqlens are both given")
+            raise ValueError("%s: tokens and cu_seqlens are both given" % where)
         n = cu_seqlens.shape[0] - 1
-        return a.whole(cu_seqlens, "cu_seqlens", (n + 1,), a.i32), n
+        return _whole(where, dev, cu_seqlens, "cu_seqlens", (n + 1,), _I32), n
     if tokens is None:
         return 0, 1
     if tokens < 1 or T % tokens:
-        a.refuse("q", "holds %d tokens, not a multiple of tokens=%s" % (T, tokens))
+        raise ValueError("%s: q holds %d tokens, not a multiple of tokens=%s" % (where, T, tokens))
     return 0, T // tokens
-
-
-def _pools(a, cfg, k_pages, v_pages):
-    shape = (cfg.kv_heads, cfg.page_size, cfg.head_dim)
-    return a.pool(k_pages, "k_pages", cfg.n_pages, shape, a.act), a.pool(v_pages, "v_pages", cfg.n_pages, shape, a.act)
 
 
 def gdn_attn_prep(cfg, q, k, q_out, inv_freq, k_out=None, v=None, k_pages=None, v_pages=None, page_table=None, lens=None,
@@ -698,23 +745,29 @@ def gdn_attn_prep(cfg, q, k, q_out, inv_freq, k_out=None, v=None, k_pages=None, 
     """q [T, q_heads, head_dim], k and v [T, kv_heads, head_dim] (views) -> q_out [T, q_heads, head_dim], and k_out or the
     pools' places of the new tokens.  inv_freq: fp32 [rotary_dim / 2] or None.  The batch is packed by cu_seqlens, or has
     `tokens` tokens a sequence; lens counts them already.  k may be None."""
-    a = _Args("gdn_attn_prep", cfg.act)
-    T, Hq, Hk, D = q.shape[0], cfg.q_heads, cfg.kv_heads, cfg.head_dim
-    cu, n = _prep_batch(a, T, cu_seqlens, tokens)
+    if _get_device is None:
+        _start()
+    where, dev, act = "gdn_attn_prep", _get_device(), _ACT[cfg.act]
+    T, Hk, D = q.shape[0], cfg.kv_heads, cfg.head_dim
+    wide, narrow, page = (T, cfg.q_heads, D), (T, Hk, D), (Hk, cfg.page_size, D)
+    cu, n = _prep_batch(where, dev, T, cu_seqlens, tokens)
     half = 0 if inv_freq is None else inv_freq.shape[0]
-    io = _prep_io(*a.heads(q, "q", (T, Hq, D), a.act), *a.heads(k, "k", (T, Hk, D), a.act), *a.heads(v, "v", (T, Hk, D), a.act), T,
-                  a.whole(w_q, "w_q", (D,), a.f32), a.whole(w_k, "w_k", (D,), a.f32), weight_offset, eps, 2 * half,
-                  1 if interleaved else 0, a.whole(inv_freq, "inv_freq", (half,), a.f32),
-                  a.whole(positions, "positions", (T,), a.i32), cu, n, a.whole(rows, "rows", (n,), a.i32),
-                  a.whole(lens, "lens", (cfg.n_rows,), a.i32),
-                  a.whole(page_table, "page_table", (cfg.n_rows, cfg.max_pages), a.i32), *_pools(a, cfg, k_pages, v_pages),
-                  a.whole(q_out, "q_out", (T, Hq, D), a.act), a.whole(k_out, "k_out", (T, Hk, D), a.act),
+    io = _prep_io(*_heads(where, dev, q, "q", wide, act), *_heads(where, dev, k, "k", narrow, act), *_heads(where, dev, v, "v", narrow, act), T,
+                  _whole(where, dev, w_q, "w_q", (D,), _F32), _whole(where, dev, w_k, "w_k", (D,), _F32), weight_offset, eps, 2 * half,
+                  1 if interleaved else 0, _whole(where, dev, inv_freq, "inv_freq", (half,), _F32),
+                  _whole(where, dev, positions, "positions", (T,), _I32), cu, n, _whole(where, dev, rows, "rows", (n,), _I32),
+                  _whole(where, dev, lens, "lens", (cfg.n_rows,), _I32),
+                  _whole(where, dev, page_table, "page_table", (cfg.n_rows, cfg.max_pages), _I32),
+                  _pool(where, dev, k_pages, "k_pages", cfg.n_pages, page, act), _pool(where, dev, v_pages, "v_pages", cfg.n_pages, page, act),
+                  _whole(where, dev, q_out, "q_out", wide, act), _whole(where, dev, k_out, "k_out", narrow, act),
                   0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
-    _check((_lib or load()).gdn_attn_prep(ctypes.byref(cfg), ctypes.byref(io), a.stream(stream)), "gdn_attn_prep")
+    st = _lib.gdn_attn_prep(ctypes.byref(cfg), io, _on(stream, dev))
+    if st:
+        raise GDNError(st, where)
 
 
 def gdn_attn_prep_workspace_size(cfg, max_tokens) -> int:
-    return load().gdn_attn_prep_workspace_size(ctypes.byref(cfg), max_tokens)
+    return (_lib or load()).gdn_attn_prep_workspace_size(ctypes.byref(cfg), max_tokens)
 
 
 def gdn_attn_prep_backward(cfg, q, k, dq_out, dk_out, inv_freq, dq=None, dk=None, dw_q=None, dw_k=None, w_q=None, w_k=None,
@@ -722,102 +775,121 @@ def gdn_attn_prep_backward(cfg, q, k, dq_out, dk_out, inv_freq, dq=None, dk=None
                            workspace=None, stream=None):
     """Gradients of gdn_attn_prep (without a cache) for sum(dq_out * q_out) + sum(dk_out * k_out): dq and dk (views), dw_q and
     dw_k fp32 [head_dim], each of which may be None."""
-    a = _Args("gdn_attn_prep_backward", cfg.act)
-    T, Hq, Hk, D = q.shape[0], cfg.q_heads, cfg.kv_heads, cfg.head_dim
-    cu, n = _prep_batch(a, T, cu_seqlens, tokens)
+    if _get_device is None:
+        _start()
+    where, dev, act = "gdn_attn_prep_backward", _get_device(), _ACT[cfg.act]
+    T, D = q.shape[0], cfg.head_dim
+    wide, narrow, width = (T, cfg.q_heads, D), (T, cfg.kv_heads, D), (D,)
+    cu, n = _prep_batch(where, dev, T, cu_seqlens, tokens)
     half = 0 if inv_freq is None else inv_freq.shape[0]
-    io = _prep_io(*a.heads(q, "q", (T, Hq, D), a.act), *a.heads(k, "k", (T, Hk, D), a.act), 0, 0, 0, T,
-                  a.whole(w_q, "w_q", (D,), a.f32), a.whole(w_k, "w_k", (D,), a.f32), weight_offset, eps, 2 * half,
-                  1 if interleaved else 0, a.whole(inv_freq, "inv_freq", (half,), a.f32),
-                  a.whole(positions, "positions", (T,), a.i32), cu, n, 0, 0, 0, 0, 0, 0, 0,
-                  a.whole(dq_out, "dq_out", (T, Hq, D), a.act), a.whole(dk_out, "dk_out", (T, Hk, D), a.act),
-                  *a.heads(dq, "dq", (T, Hq, D), a.act), *a.heads(dk, "dk", (T, Hk, D), a.act),
-                  a.whole(dw_q, "dw_q", (D,), a.f32), a.whole(dw_k, "dw_k", (D,), a.f32))
-    ws, ws_bytes = a.bytes_of(workspace)
-    _check((_lib or load()).gdn_attn_prep_backward(ctypes.byref(cfg), ctypes.byref(io), ws, ws_bytes, a.stream(stream)),
-           "gdn_attn_prep_backward")
+    io = _prep_io(*_heads(where, dev, q, "q", wide, act), *_heads(where, dev, k, "k", narrow, act), 0, 0, 0, T,
+                  _whole(where, dev, w_q, "w_q", width, _F32), _whole(where, dev, w_k, "w_k", width, _F32), weight_offset, eps, 2 * half,
+                  1 if interleaved else 0, _whole(where, dev, inv_freq, "inv_freq", (half,), _F32),
+                  _whole(where, dev, positions, "positions", (T,), _I32), cu, n, 0, 0, 0, 0, 0, 0, 0,
+                  _whole(where, dev, dq_out, "dq_out", wide, act), _whole(where, dev, dk_out, "dk_out", narrow, act),
+                  *_heads(where, dev, dq, "dq", wide, act), *_heads(where, dev, dk, "dk", narrow, act),
+                  _whole(where, dev, dw_q, "dw_q", width, _F32), _whole(where, dev, dw_k, "dw_k", width, _F32))
+    st = _lib.gdn_attn_prep_backward(ctypes.byref(cfg), io, *_workspace(where, dev, workspace), _on(stream, dev))
+    if st:
+        raise GDNError(st, where)
 
 
 def gdn_attn_workspace_size(cfg, max_seqs, tokens=1) -> int:
-    return load().gdn_attn_workspace_size(ctypes.byref(cfg), max_seqs, tokens)
+    return (_lib or load()).gdn_attn_workspace_size(ctypes.byref(cfg), max_seqs, tokens)
 
 
 def gdn_attn_decode(cfg, q, k_pages, v_pages, page_table, lens, out, workspace, tokens=1, rows=None, window=0, scale=None,
                     lse=None, stream=None):
     """Attention of the last `tokens` tokens of each sequence: q [n * tokens, q_heads, head_dim] (a view) -> out of that shape,
     lse fp32 [n * tokens, q_heads] or None.  scale None: head_dim ** -0.5."""
-    a = _Args("gdn_attn_decode", cfg.act)
+    if _get_device is None:
+        _start()
+    where, dev, act = "gdn_attn_decode", _get_device(), _ACT[cfg.act]
     T, Hq, D = q.shape[0], cfg.q_heads, cfg.head_dim
     n = T // tokens if tokens > 0 else 0
     if n * tokens != T:
-        a.refuse("q", "holds %d tokens, not a multiple of tokens=%s" % (T, tokens))
-    io = _decode_io(*a.heads(q, "q", (T, Hq, D), a.act), *_pools(a, cfg, k_pages, v_pages),
-                    a.whole(page_table, "page_table", (cfg.n_rows, cfg.max_pages), a.i32),
-                    a.whole(lens, "lens", (cfg.n_rows,), a.i32), a.whole(rows, "rows", (n,), a.i32), n, tokens, window,
-                    D ** -0.5 if scale is None else scale, a.whole(out, "out", (T, Hq, D), a.act),
-                    a.whole(lse, "lse", (T, Hq), a.f32))
-    ws, ws_bytes = a.bytes_of(workspace)
-    _check((_lib or load()).gdn_attn_decode(ctypes.byref(cfg), ctypes.byref(io), ws, ws_bytes, a.stream(stream)), "gdn_attn_decode")
+        raise ValueError("%s: q holds %d tokens, not a multiple of tokens=%s" % (where, T, tokens))
+    wide, page = (T, Hq, D), (cfg.kv_heads, cfg.page_size, D)
+    io = _decode_io(*_heads(where, dev, q, "q", wide, act), _pool(where, dev, k_pages, "k_pages", cfg.n_pages, page, act),
+                    _pool(where, dev, v_pages, "v_pages", cfg.n_pages, page, act),
+                    _whole(where, dev, page_table, "page_table", (cfg.n_rows, cfg.max_pages), _I32),
+                    _whole(where, dev, lens, "lens", (cfg.n_rows,), _I32), _whole(where, dev, rows, "rows", (n,), _I32), n, tokens, window,
+                    D ** -0.5 if scale is None else scale, _whole(where, dev, out, "out", wide, act),
+                    _whole(where, dev, lse, "lse", (T, Hq), _F32))
+    st = _lib.gdn_attn_decode(ctypes.byref(cfg), io, *_workspace(where, dev, workspace), _on(stream, dev))
+    if st:
+        raise GDNError(st, where)
 
 
 def gdn_page_workspace_size(cfg, max_lanes) -> int:
-    return load().gdn_page_workspace_size(ctypes.byref(cfg), max_lanes)
+    return (_lib or load()).gdn_page_workspace_size(ctypes.byref(cfg), max_lanes)
 
 
-def _page_state(a, cfg, page_table, lens, refs):
-    return (a.whole(page_table, "page_table", (cfg.n_rows, cfg.max_pages), a.i32), a.whole(lens, "lens", (cfg.n_rows,), a.i32),
-            a.whole(refs, "refs", (cfg.n_pages,), a.i32))
+def _page_state(where, dev, cfg, page_table, lens, refs):
+    n_rows = cfg.n_rows
+    return (_whole(where, dev, page_table, "page_table", (n_rows, cfg.max_pages), _I32), _whole(where, dev, lens, "lens", (n_rows,), _I32),
+            _whole(where, dev, refs, "refs", (cfg.n_pages,), _I32))
 
 
 def gdn_page_resize(cfg, page_table, lens, refs, rows, new_lens, granted, src_idx, dst_idx, workspace, stream=None):
     """Sets the lengths of `rows` to new_lens: pages taken, let go, or replaced by copies (src_idx -> dst_idx, to be carried out
     with gdn_page_copy before they are written and before the next resize).  granted: the lengths after the call."""
-    a = _Args("gdn_page_resize")
-    n = rows.shape[0]
-    lane = ((n,), a.i32)
-    state = _page_state(a, cfg, page_table, lens, refs)
-    ws, ws_bytes = a.bytes_of(workspace)
-    _check((_lib or load()).gdn_page_resize(
-        ctypes.byref(cfg), *state, a.whole(rows, "rows", *lane), a.whole(new_lens, "new_lens", *lane), n,
-        a.whole(granted, "granted", *lane), a.whole(src_idx, "src_idx", *lane), a.whole(dst_idx, "dst_idx", *lane), ws, ws_bytes,
-        a.stream(stream)), "gdn_page_resize")
+    if _get_device is None:
+        _start()
+    where, dev, i32, n = "gdn_page_resize", _get_device(), _I32, rows.shape[0]
+    lane = (n,)
+    st = _lib.gdn_page_resize(
+        ctypes.byref(cfg), *_page_state(where, dev, cfg, page_table, lens, refs), _whole(where, dev, rows, "rows", lane, i32),
+        _whole(where, dev, new_lens, "new_lens", lane, i32), n, _whole(where, dev, granted, "granted", lane, i32),
+        _whole(where, dev, src_idx, "src_idx", lane, i32), _whole(where, dev, dst_idx, "dst_idx", lane, i32),
+        *_workspace(where, dev, workspace), _on(stream, dev))
+    if st:
+        raise GDNError(st, where)
 
 
 def gdn_page_fork(cfg, page_table, lens, refs, src_rows, dst_rows, stream=None):
     """Empty rows dst_rows become copies of src_rows that share their pages."""
-    a = _Args("gdn_page_fork")
-    n = dst_rows.shape[0]
-    _check((_lib or load()).gdn_page_fork(
-        ctypes.byref(cfg), *_page_state(a, cfg, page_table, lens, refs), a.whole(src_rows, "src_rows", (n,), a.i32),
-        a.whole(dst_rows, "dst_rows", (n,), a.i32), n, a.stream(stream)), "gdn_page_fork")
+    if _get_device is None:
+        _start()
+    where, dev, n = "gdn_page_fork", _get_device(), dst_rows.shape[0]
+    st = _lib.gdn_page_fork(
+        ctypes.byref(cfg), *_page_state(where, dev, cfg, page_table, lens, refs), _whole(where, dev, src_rows, "src_rows", (n,), _I32),
+        _whole(where, dev, dst_rows, "dst_rows", (n,), _I32), n, _on(stream, dev))
+    if st:
+        raise GDNError(st, where)
 
 
 def gdn_page_compact(cfg, page_table, lens, refs, table_out, refs_out, src_idx, dst_idx, workspace, stream=None):
     """Plans the moves of held pages to the lowest places (src_idx -> dst_idx, -1 behind the last) and writes the table and the
     counts after them; table_out may be page_table, refs_out refs."""
-    a = _Args("gdn_page_compact")
-    n = src_idx.shape[0]
-    state = _page_state(a, cfg, page_table, lens, refs)
-    ws, ws_bytes = a.bytes_of(workspace)
-    _check((_lib or load()).gdn_page_compact(
-        ctypes.byref(cfg), *state, a.whole(table_out, "table_out", (cfg.n_rows, cfg.max_pages), a.i32),
-        a.whole(refs_out, "refs_out", (cfg.n_pages,), a.i32), a.whole(src_idx, "src_idx", (n,), a.i32),
-        a.whole(dst_idx, "dst_idx", (n,), a.i32), n, ws, ws_bytes, a.stream(stream)), "gdn_page_compact")
+    if _get_device is None:
+        _start()
+    where, dev, n = "gdn_page_compact", _get_device(), src_idx.shape[0]
+    st = _lib.gdn_page_compact(
+        ctypes.byref(cfg), *_page_state(where, dev, cfg, page_table, lens, refs),
+        _whole(where, dev, table_out, "table_out", (cfg.n_rows, cfg.max_pages), _I32),
+        _whole(where, dev, refs_out, "refs_out", (cfg.n_pages,), _I32), _whole(where, dev, src_idx, "src_idx", (n,), _I32),
+        _whole(where, dev, dst_idx, "dst_idx", (n,), _I32), n, *_workspace(where, dev, workspace), _on(stream, dev))
+    if st:
+        raise GDNError(st, where)
 
 
 def gdn_page_copy(cfg, src_k, src_v, dst_k, dst_v, src_idx, dst_idx, stream=None):
     """Pages src_idx[i] of the src pools to pages dst_idx[i] of the dst pools (src < 0: zeros, dst < 0: nothing); the pools
     may be the same, and have as many pages as their first dimension says."""
-    a = _Args("gdn_page_copy", cfg.act)
-    shape = (cfg.kv_heads, cfg.page_size, cfg.head_dim)
-    n = dst_idx.shape[0]
+    if _get_device is None:
+        _start()
+    where, dev, act, n = "gdn_page_copy", _get_device(), _ACT[cfg.act], dst_idx.shape[0]
+    page = (cfg.kv_heads, cfg.page_size, cfg.head_dim)
 
-    def pages(*ts):
-        return min([t.shape[0] for t in ts if t is not None] or [0])
-    _check((_lib or load()).gdn_page_copy(
-        ctypes.byref(cfg), a.pool(src_k, "src_k", 0, shape, a.act), a.pool(src_v, "src_v", 0, shape, a.act), pages(src_k, src_v),
-        a.pool(dst_k, "dst_k", 0, shape, a.act), a.pool(dst_v, "dst_v", 0, shape, a.act), pages(dst_k, dst_v),
-        a.whole(src_idx, "src_idx", (n,), a.i32), a.whole(dst_idx, "dst_idx", (n,), a.i32), n, a.stream(stream)), "gdn_page_copy")
+    def pages(a, b):
+        return min(a.shape[0], b.shape[0]) if a is not None and b is not None else 0 if a is b else (b if a is None else a).shape[0]
+    st = _lib.gdn_page_copy(
+        ctypes.byref(cfg), _pool(where, dev, src_k, "src_k", 0, page, act), _pool(where, dev, src_v, "src_v", 0, page, act), pages(src_k, src_v),
+        _pool(where, dev, dst_k, "dst_k", 0, page, act), _pool(where, dev, dst_v, "dst_v", 0, page, act), pages(dst_k, dst_v),
+        _whole(where, dev, src_idx, "src_idx", (n,), _I32), _whole(where, dev, dst_idx, "dst_idx", (n,), _I32), n, _on(stream, dev))
+    if st:
+        raise GDNError(st, where)
 
 
 def gdn_device_error(stream=None) -> int:
