@@ -27,6 +27,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_decode_simt_kernel(const At
     __shared__ long long sums[33];
     __shared__ int found[3], bad_page[TILE];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rows = a.d.grp * a.tokens, row0 = blockIdx.y * RB;
+    await_previous();
     let_next_start();
     AttnWalk w;
     if (!attn_begin<TILE, kSimtThreads>(a, blockIdx.x, sums, found, w)) {
@@ -238,8 +239,7 @@ template <typename T, int D, int RPW> cudaError_t run_simt(const AttnDecodeArgs 
         if (e != cudaSuccess) return e;
     }
     const int rows = a.d.grp * a.tokens;
-    kernel<<<dim3(a.ctas, (rows + RB - 1) / RB), kSimtThreads, smem, s>>>(a);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_early(kernel, dim3(a.ctas, (rows + RB - 1) / RB), kSimtThreads, smem, s, a);
     if (e != cudaSuccess) return e;
     return launch_attn_join(a, sizeof(T) == 2, s);
 }

@@ -309,6 +309,8 @@ __global__ void __launch_bounds__(kPrepThreads, kPrepBlocks) attn_prep_kernel(co
     float2 *turns = reinterpret_cast<float2 *>(smem4) + warp * kPrepTokens * a.half;
     const long long tokens = (long long)gridDim.x * kPrepWarps;      // side by side
     long long t = (long long)blockIdx.x * kPrepWarps + warp;
+    await_previous();
+    let_next_start();
     if (blockIdx.x == 0 && blockIdx.y == 0) check_bounds(a);
     if (t >= a.T) return;
     const bool pools = a.k_pages != nullptr;
@@ -418,6 +420,8 @@ __global__ void __launch_bounds__(kPrepThreads, 2) attn_prep_backward_kernel(con
     constexpr int kKind = kPrepWarps * 32 * 8;
     float *all = reinterpret_cast<float *>(smem4), *sums = all + (warp * 32 + lane) * 8;
     float2 *turns = reinterpret_cast<float2 *>(all + 2 * kKind) + warp * kPrepTokens * a.half;
+    await_previous();
+    let_next_start();
     if (blockIdx.x == 0) check_bounds(a);
 #pragma unroll
     for (int e = 0; e < 8; ++e) sums[e] = sums[kKind + e] = 0.f;
@@ -579,8 +583,7 @@ template <typename T, int D, int MODE> cudaError_t run_prep(const AttnPrepArgs &
     const auto kernel = plain ? attn_prep_kernel<T, D, MODE, MODE == kHalves> : attn_prep_kernel<T, D, MODE, false>;
     const cudaError_t e = with_smem(kernel, smem);
     if (e != cudaSuccess) return e;
-    kernel<<<dim3((unsigned)blocks, split), kPrepThreads, smem, s>>>(a);
-    return cudaGetLastError();
+    return launch_early(kernel, dim3((unsigned)blocks, split), kPrepThreads, smem, s, a);
 }
 template <typename T, int D, int MODE> cudaError_t run_backward(const AttnPrepArgs &a, cudaStream_t s) {
     const int blocks = backward_blocks(a.T), smem = 2 * kPrepThreads * 8 * 4 + kPrepWarps * kPrepTokens * a.half * 8;
@@ -588,8 +591,7 @@ template <typename T, int D, int MODE> cudaError_t run_backward(const AttnPrepAr
     const auto kernel = plain ? attn_prep_backward_kernel<T, D, MODE, MODE == kHalves> : attn_prep_backward_kernel<T, D, MODE, false>;
     cudaError_t e = with_smem(kernel, smem);
     if (e != cudaSuccess) return e;
-    kernel<<<blocks, kPrepThreads, smem, s>>>(a);
-    e = cudaGetLastError();
+    e = launch_early(kernel, dim3(blocks), kPrepThreads, smem, s, a);
     if (e != cudaSuccess || !a.ws) return e;
     return launch_early(attn_prep_weights_kernel, dim3((2 * D + 7) / 8), 256, 0, s, a, blocks);
 }

@@ -110,16 +110,27 @@ __device__ __forceinline__ Resize resize_lane(const PageArgs &a, int i, const un
     return r;
 }
 
-// Workspace: free pages in order; per lane the place of its first one among them, and the page that it copies.
+// What a lane does once it is granted, as its warp finds it: in shared memory for the first kPageThreads lanes, where every
+// CTA has them from its own sums; beyond, the place and the copied page come from the workspace, the rest again from the
+// tables.
+struct Lanes {
+    int row[kPageThreads], old[kPageThreads], len[kPageThreads], last[kPageThreads], first[kPageThreads];
+};
+
+// Workspace: per lane the place of its first page among the free ones and the page that it copies; the free pages in order.
 __global__ void __cluster_dims__(kPageCluster, 1, 1) __launch_bounds__(kPageThreads) page_resize_kernel(const PageArgs a) {
-    __shared__ unsigned seen[kRowWords], twice[kRowWords];
+    extern __shared__ unsigned char raw[];
+    Lanes &lanes = *reinterpret_cast<Lanes *>(raw);
+    unsigned *seen = reinterpret_cast<unsigned *>(raw + sizeof(Lanes)), *twice = seen + kRowWords;
     __shared__ int sums[32], counted;
     __shared__ long long lane_sums[32];
     cg::cluster_group cluster = cg::this_cluster();
     const int tid = threadIdx.x, rank = (int)cluster.block_rank();
     int32_t *first = a.ws, *copied = a.ws + a.n, *fresh = a.ws + 2 * (size_t)a.n;
+    await_previous();
+    let_next_start();
     mark_rows(a.rows, a.new_lens, a.n, a.d.n_rows, seen, twice);
-    // every CTA sums all lanes' needs; the first one writes the lanes' places
+    // every CTA sums all lanes' needs; the first one writes the places of the lanes that shared memory does not hold
     long long needed = 0;
     for (int i0 = 0; i0 < a.n; i0 += kPageThreads) {
         const int i = i0 + tid;
@@ -127,58 +138,71 @@ __global__ void __cluster_dims__(kPageCluster, 1, 1) __launch_bounds__(kPageThre
         if (i < a.n) r = resize_lane(a, i, twice);
         long long total;
         const long long upto = block_scan((long long)r.need(), lane_sums, total);
-        if (rank == 0 && i < a.n) {
-            // places behind the last page are no places: such a lane is not granted
-            first[i] = (int)min(needed + upto - r.need(), (long long)a.d.n_pages);
+        // places behind the last page are no places: such a lane is not granted
+        const int at = (int)min(needed + upto - r.need(), (long long)a.d.n_pages);
+        if (i0 == 0) {
+            lanes.row[tid] = r.row;
+            lanes.old[tid] = r.old;
+            lanes.len[tid] = r.len;
+            lanes.last[tid] = r.last;
+            lanes.first[tid] = at;
+        } else if (rank == 0 && i < a.n) {
+            first[i] = at;
             copied[i] = r.last;
         }
         needed += total;
     }
     // the free pages of this CTA's part of the counts, then their places among all
-    const int part = (((a.d.n_pages + kPageCluster - 1) / kPageCluster) + 3) & ~3;
-    const int lo = min(part * rank, a.d.n_pages), hi = min(lo + part, a.d.n_pages);
-    int mine = 0;
+    int n_free = 0;
     if (needed > 0) {
+        const int part = (((a.d.n_pages + kPageCluster - 1) / kPageCluster) + 3) & ~3;
+        const int lo = min(part * rank, a.d.n_pages), hi = min(lo + part, a.d.n_pages);
+        int mine = 0, total;
         for (int p = lo + tid; p < hi; p += kPageThreads) mine += a.refs[p] == 0;
-        int total;
         block_scan(mine, sums, total);
         if (tid == 0) counted = total;
-    } else if (tid == 0) {
-        counted = 0;
-    }
-    cluster.sync();
-    int before = 0, n_free = 0;
-    for (int k = 0; k < kPageCluster; ++k) {
-        const int c = *cluster.map_shared_rank(&counted, k);
-        before += k < rank ? c : 0;
-        n_free += c;
-    }
-    for (int p0 = lo; p0 < hi && before < needed; p0 += kPageThreads) {
-        const int p = p0 + tid;
-        const bool free = p < hi && a.refs[p] == 0;
-        int total;
-        const int place = before + block_scan(free ? 1 : 0, sums, total) - 1;
-        if (free && place < needed) fresh[place] = p;
-        before += total;
+        cluster.sync();
+        int before = 0;
+        for (int k = 0; k < kPageCluster; ++k) {
+            const int c = *cluster.map_shared_rank(&counted, k);
+            before += k < rank ? c : 0;
+            n_free += c;
+        }
+        for (int p0 = lo; p0 < hi && before < needed; p0 += kPageThreads) {
+            const int p = p0 + tid;
+            const bool free = p < hi && a.refs[p] == 0;
+            const int place = before + block_scan(free ? 1 : 0, sums, total) - 1;
+            if (free && place < needed) fresh[place] = p;
+            before += total;
+        }
     }
     __threadfence();
-    cluster.sync();
+    cluster.sync();                   // the lists are there, and all have read the tables as they were
     // a warp a lane
     for (int i = rank * kPageWarps + (tid >> 5); i < a.n; i += kPageCluster * kPageWarps) {
         const int lane = tid & 31;
-        // the counts have changed by now: what is copied was decided above
         Resize r{-1, 0, 0, 0, 0, -1};
-        const int at = first[i];
-        const int row = a.rows[i], len = a.new_lens[i], most = a.d.max_pages * a.d.page;
-        if (len >= 0 && row >= 0 && row < a.d.n_rows && !marked(twice, row)) {
-            r.row = row;
-            r.old = min(max(a.lens[row], 0), most);
-            r.len = len > most ? r.old : len;
-            r.have = pages_of(r.old, a.d);
-            r.want = pages_of(r.len, a.d);
-            r.last = copied[i];
+        int at;
+        if (i < kPageThreads) {
+            r.row = lanes.row[i];
+            r.old = lanes.old[i];
+            r.len = lanes.len[i];
+            r.last = lanes.last[i];
+            at = lanes.first[i];
+        } else {
+            // the counts have changed by now: what is copied was decided above
+            at = first[i];
+            const int row = a.rows[i], len = a.new_lens[i], most = a.d.max_pages * a.d.page;
+            if (len >= 0 && row >= 0 && row < a.d.n_rows && !marked(twice, row)) {
+                r.row = row;
+                r.old = min(max(a.lens[row], 0), most);
+                r.len = len > most ? r.old : len;
+                r.last = copied[i];
+            }
+            __syncwarp();
         }
-        __syncwarp();
+        r.have = pages_of(r.old, a.d);
+        r.want = pages_of(r.len, a.d);
         const bool granted = r.row >= 0 && (r.need() == 0 || (long long)at + r.need() <= n_free);
         int place = at, to = -1;
         int32_t *entry = a.table + (long long)r.row * a.d.max_pages;
@@ -209,13 +233,14 @@ __global__ void __cluster_dims__(kPageCluster, 1, 1) __launch_bounds__(kPageThre
             a.dst[i] = to;
         }
     }
-    // no CTA leaves while another may still read its shared memory
-    cluster.sync();
+    // (no CTA reads another's shared memory behind the last cluster.sync)
 }
 
 constexpr int kForkThreads = 256;
 __global__ void __launch_bounds__(kForkThreads) page_fork_kernel(const PageArgs a) {
     __shared__ unsigned seen[kRowWords], twice[kRowWords];
+    await_previous();
+    let_next_start();
     mark_rows(a.rows, a.new_lens, a.n, a.d.n_rows, seen, twice);
     const int lane = threadIdx.x & 31;
     for (int i = blockIdx.x * (kForkThreads / 32) + (threadIdx.x >> 5); i < a.n; i += gridDim.x * (kForkThreads / 32)) {
@@ -248,6 +273,8 @@ __global__ void __cluster_dims__(kPageCluster, 1, 1) __launch_bounds__(kPageThre
     cg::cluster_group cluster = cg::this_cluster();
     const int tid = threadIdx.x, rank = (int)cluster.block_rank();
     int32_t *goes = a.ws + 1;
+    await_previous();
+    let_next_start();
     const int part = (a.d.n_pages + kPageCluster - 1) / kPageCluster;
     const int lo = min(part * rank, a.d.n_pages), hi = min(lo + part, a.d.n_pages);
     int held = 0, total;
@@ -300,6 +327,7 @@ __global__ void __cluster_dims__(kPageCluster, 1, 1) __launch_bounds__(kPageThre
 }
 
 __global__ void __launch_bounds__(256) page_table_kernel(const PageArgs a) {
+    let_next_start();
     await_previous();
     const long long all = (long long)a.d.n_rows * a.d.max_pages;
     for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < all; i += (long long)gridDim.x * 256) {
@@ -318,6 +346,8 @@ __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const uint4 *sr
                                                                  int n_dst, const int32_t *src_idx, const int32_t *dst_idx, int n,
                                                                  long long page_words, int pieces, unsigned *err) {
     const int per_lane = pieces * 2;
+    let_next_start();
+    await_previous();
     for (long long i = blockIdx.x; i < (long long)n * per_lane; i += gridDim.x) {
         const int lane = (int)(i / per_lane), k = (int)(i - (long long)lane * per_lane);
         const bool v = k >= pieces;
@@ -345,19 +375,18 @@ __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const uint4 *sr
 size_t page_ws_ints(const AttnDims &d, long long lanes) { return 2 * (size_t)lanes + (size_t)d.n_pages + 4; }
 
 cudaError_t launch_page_resize(const PageArgs &a, cudaStream_t s) {
-    page_resize_kernel<<<kPageCluster, kPageThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    constexpr int smem = sizeof(Lanes) + 2 * kRowWords * 4;
+    static_assert(smem <= 48 * 1024, "without opting in");
+    return launch_early(page_resize_kernel, dim3(kPageCluster), kPageThreads, smem, s, a);
 }
 
 cudaError_t launch_page_fork(const PageArgs &a, cudaStream_t s) {
     const int blocks = (a.n + kForkThreads / 32 - 1) / (kForkThreads / 32), most = sm_count() * 4;
-    page_fork_kernel<<<blocks < most ? blocks : most, kForkThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_early(page_fork_kernel, dim3(blocks < most ? blocks : most), kForkThreads, 0, s, a);
 }
 
 cudaError_t launch_page_compact(const PageArgs &a, cudaStream_t s) {
-    page_compact_kernel<<<kPageCluster, kPageThreads, 0, s>>>(a);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_early(page_compact_kernel, dim3(kPageCluster), kPageThreads, 0, s, a);
     if (e != cudaSuccess) return e;
     const long long all = (long long)a.d.n_rows * a.d.max_pages, blocks = (all + 255) / 256, most = (long long)sm_count() * 8;
     return launch_early(page_table_kernel, dim3((unsigned)(blocks < most ? blocks : most)), 256, 0, s, a);
@@ -368,10 +397,8 @@ cudaError_t launch_page_copy(const void *src_k, const void *src_v, int n_src, vo
                              cudaStream_t s) {
     const int pieces = (int)((page_bytes + kCopyPiece - 1) / kCopyPiece);
     const long long all = (long long)n * pieces * 2, most = (long long)sm_count() * 8;
-    page_copy_kernel<<<(unsigned)(all < most ? all : most), kCopyThreads, 0, s>>>(
-        (const uint4 *)src_k, (const uint4 *)src_v, n_src, (uint4 *)dst_k, (uint4 *)dst_v, n_dst, src_idx, dst_idx, n,
-        page_bytes / 16, pieces, err);
-    return cudaGetLastError();
+    return launch_early(page_copy_kernel, dim3((unsigned)(all < most ? all : most)), kCopyThreads, 0, s, (const uint4 *)src_k, (const uint4 *)src_v,
+                        n_src, (uint4 *)dst_k, (uint4 *)dst_v, n_dst, src_idx, dst_idx, n, page_bytes / 16, pieces, err);
 }
 
 }  // namespace gdn
