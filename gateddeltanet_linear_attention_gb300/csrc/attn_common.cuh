@@ -194,5 +194,6 @@ size_t attn_decode_ws_bytes(const AttnDims &d, int rows);
 void attn_decode_carve(AttnDecodeArgs &a, void *ws);
 cudaError_t launch_attn_decode(const AttnDecodeArgs &a, bool act_bf16, cudaStream_t s);
 cudaError_t launch_attn_decode_tc(const AttnDecodeArgs &a, cudaStream_t s);
+cudaError_t launch_attn_decode_rows(const AttnDecodeArgs &a, cudaStream_t s);
 cudaError_t launch_attn_join(const AttnDecodeArgs &a, bool act_bf16, cudaStream_t s);
 }  // namespace gdn

@@ -281,7 +281,8 @@ cudaError_t launch_attn_join(const AttnDecodeArgs &a, bool act_bf16, cudaStream_
 }
 
 cudaError_t launch_attn_decode(const AttnDecodeArgs &a, bool act_bf16, cudaStream_t s) {
-    return act_bf16 ? launch_attn_decode_tc(a, s) : run_dim<float>(a, s);
+    if (!act_bf16) return run_dim<float>(a, s);
+    return a.d.grp * a.tokens <= 16 ? launch_attn_decode_tc(a, s) : launch_attn_decode_rows(a, s);
 }
 
 }  // namespace gdn

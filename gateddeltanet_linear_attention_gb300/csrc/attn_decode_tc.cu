@@ -12,23 +12,15 @@
 // TFLOP/s that these products reach on this GPU, 0.2 and 0.7 of the time that the bytes take.  (They run as mma.sync: a
 // tcgen05 product has 64 or 128 rows, and the sums over tokens of its transposed form lie across lanes.)
 // P is split in two bf16 parts, so that o loses nothing but its own rounding.
-#include <cuda.h>
-
-#include "attn_common.cuh"
-#include "tc_sm103.cuh"
+#include "attn_tc.cuh"
 
 namespace gdn {
 
 namespace {
 
-constexpr int kTile = 64;
-constexpr int kPPitch = kTile * 2 + 16;            // bytes of a row of P: ldmatrix without bank conflicts
-constexpr int kMaxEntries = 24;
+using namespace attn_tc;
 
-// A unit's tiles in this CTA, as the copying warp describes them.
-struct Unit {
-    int n, h, len, first, i0, count, seq0, slot;   // slot -1: the unit is whole
-};
+constexpr int kPPitch = kTile * 2 + 16;            // bytes of a row of P: ldmatrix without bank conflicts
 
 // MT blocks of 16 query rows a group, GR groups of rows, GS sets of each.
 template <int D, int MT, int GR, int GS> struct Shape {
@@ -60,27 +52,7 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(threads) : "memory"); }
-// Whether all threads of the barrier say so.
-__device__ __forceinline__ bool bar_all(int id, int threads, bool mine) {
-    int all;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %3, 0;\n\tbar.red.and.pred q, %1, %2, p;\n\tselp.s32 %0, 1, 0, q;\n\t}\n"
-                 : "=r"(all) : "r"(id), "r"(threads), "r"((int)mine) : "memory");
-    return all != 0;
-}
 enum { kBarGroup = 1 };              // the first group's named barrier
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&v);
-}
-// Either half's exponent all ones.
-__device__ __forceinline__ bool not_finite2(uint32_t v) {
-    return (v & 0x7f80u) == 0x7f80u || (v & 0x7f800000u) == 0x7f800000u;
-}
-
-struct Maps {
-    CUtensorMap k, v;
-};
 
 template <int D, int MT, int GR, int GS>
 __global__ void __launch_bounds__((Shape<D, MT, GR, GS>::threads), 1) attn_decode_tc_kernel(const AttnDecodeArgs a, const __grid_constant__ Maps maps) {
@@ -133,113 +105,15 @@ __global__ void __launch_bounds__((Shape<D, MT, GR, GS>::threads), 1) attn_decod
 
     if (warp == kConsumers / 32) {
         // ------------------------------------------------------------ copies
-        constexpr int NB = D / 64;
-        const int piece = min(a.d.page, kTile), shift = min(a.d.page_shift, 6), boxes = (kTile >> shift) * NB;
-        const int my_piece = lane / NB, my_col = lane % NB;
-        const uint32_t box_bytes = piece * 128u, at = my_col * (kTile * 128u) + my_piece * box_bytes;
-        uint32_t e = 0, phase = 0, issued = 0;
-        int seq = 0, u = 0;
-        bool alive = true;
-        // the page of this lane's piece of tile t of a sequence; -1: not there
-        auto page_of = [&](const AttnSeq &s, int t) {
-            const int i = (s.tile0 + t) * kTile + (my_piece << shift);
-            if (lane >= boxes || i >= s.len || i + piece <= s.first) return -1;
-            const int p = a.table[(long long)s.row * a.d.max_pages + (i >> a.d.page_shift)];
-            if (p >= 0 && p < a.d.n_pages) return p;
-            set_error(a.err, GDN_DEVERR_PAGE);
-            return -1;
-        };
-        AttnSeq s = w.s;
-        int n = w.n, h = w.h, t0 = w.t, page = page_of(s, t0);
-        for (long long left = w.left; left > 0 && alive; ++u) {
-            const int count = (int)min((long long)(s.tiles - t0), left);
-            const bool unit_end = t0 + count == s.tiles;
-            const int slot = t0 == 0 && unit_end ? -1 : u == 0 ? 0 : 1;
-            const uint32_t us = u % kUnits, uphase = (u / kUnits) & 1;
-            if (u >= kUnits) alive = tc::mbar_wait(uempty + 8 * us, uphase ^ 1, a.wait_ns);
-            alive = __all_sync(0xffffffffu, alive);
-            if (!alive) break;
-            if (lane == 0) {
-                units[us] = Unit{n, h, s.len, s.first, (s.tile0 + t0) * kTile, count, seq, slot};
-                tc::mbar_arrive_expect_tx(ufull + 8 * us, (uint32_t)mine * D * 2);
-            }
-            __syncwarp();
+        copy_tiles<D, E, kUnits>(a, w, maps, entries, full, empty, ufull, uempty, pieces_of, units, (uint32_t)mine * D * 2,
+                                 [&](uint32_t us, int n, int h, uint32_t bar) {
             for (int r = lane; r < mine; r += 32) {
                 const int tok = (row0 + r) / a.d.grp, g = (row0 + r) - tok * a.d.grp;
                 tc::bulk_g2s(tc::smem_u32(q_mem) + us * S::q_block + r * S::q_pitch,
                              (const __nv_bfloat16 *)a.q + ((long long)n * a.tokens + tok) * a.ld_q + (long long)(h * a.d.grp + g) * a.hs_q, D * 2,
-                             ufull + 8 * us);
+                             bar);
             }
-            // the unit behind this one, and where its first tile lies: known before this one's last tile is asked for
-            AttnSeq next_s = s;
-            int next_n = n, next_h = h + 1, next_page = -1;
-            for (int j = 0; j < count && alive; ++j) {
-                const int here = page, i0 = (s.tile0 + t0 + j) * kTile;
-                if (j + 1 < count) page = page_of(s, t0 + j + 1);
-                const unsigned there = __ballot_sync(0xffffffffu, here >= 0);
-                const uint32_t bytes = __popc(there) * box_bytes;
-                // the row of the pools where this lane's piece begins
-                const int y = (here * a.d.hkv + h) * a.d.page + ((i0 + (my_piece << shift)) & (a.d.page - 1));
-#pragma unroll
-                for (int kv = 0; kv < 2; ++kv) {
-                    if (issued >= E) alive = tc::mbar_wait(empty + 8 * e, phase ^ 1, a.wait_ns);
-                    alive = __all_sync(0xffffffffu, alive);
-                    if (!alive) break;
-                    if (lane == 0) {
-                        if (kv == 0) {
-                            int bits = 0;
-                            for (int p = 0; p < 4; ++p) bits |= (there >> ((p * 16) >> shift) * NB & 1u) << p;
-                            pieces_of[e] = bits;
-                        }
-                        if (bytes) tc::mbar_arrive_expect_tx(full + 8 * e, bytes);
-                        else tc::mbar_arrive(full + 8 * e);
-                    }
-                    __syncwarp();
-                    const bool drop = (a.lose & LOSE_ATTN_TILE_COPY) && issued == 0 && lane == 0;
-                    if (here >= 0 && !drop) tc::tma_load_2d(entries + e * S::entry + at, kv ? &maps.v : &maps.k, my_col * 64, y, full + 8 * e);
-                    ++issued;
-                    if (++e == E) {
-                        e = 0;
-                        phase ^= 1;
-                    }
-                }
-                if (j == 0 && left > count) {
-                    if (next_h == a.d.hkv) {
-                        next_h = 0;
-                        next_s = attn_seq<kTile>(a, ++next_n);
-                    }
-                    next_page = page_of(next_s, 0);
-                }
-            }
-            seq += count;
-            left -= count;
-            if (left == 0 && blockIdx.y == 0 && lane == 0) {
-                // the CTA that holds a unit's front joins it: the CTAs behind that hold the rest
-                int parts = 0;
-                if (!unit_end && t0 == 0) parts = 1 + (int)((s.tiles - count + w.per - 1) / w.per);
-                a.joins[blockIdx.x] = make_int4(n, h, u == 0 ? 0 : 1, parts);
-            }
-            s = next_s;
-            n = next_n;
-            h = next_h;
-            t0 = 0;
-            page = next_page;
-        }
-        if (lane == 0) {
-            if (!alive) {             // nothing more is copied
-                set_error(a.err, GDN_DEVERR_TIMEOUT);
-                if (blockIdx.y == 0) a.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
-            }
-            // what is under way arrives before the block ends
-            for (uint32_t k = 0; k < min(issued, E); ++k) {
-                const uint32_t last = issued - 1 - k;
-                tc::mbar_wait(full + 8 * (last % E), (last / E) & 1, a.wait_ns);
-            }
-            for (int k = 0; k < min(u, kUnits); ++k) {
-                const int last = u - 1 - k;
-                tc::mbar_wait(ufull + 8 * (last % kUnits), (last / kUnits) & 1, a.wait_ns);
-            }
-        }
+        });
         return;
     }
 
@@ -534,32 +408,6 @@ __global__ void __launch_bounds__((Shape<D, MT, GR, GS>::threads), 1) attn_decod
     if (!ok && lane == 0) set_error(a.err, GDN_DEVERR_TIMEOUT);
 }
 
-using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiledFn encode_tiled() {
-    static EncodeTiledFn fn = [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
-                cudaSuccess || q != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<EncodeTiledFn>(p);
-    }();
-    return fn;
-}
-
-// A pool as rows of D columns (one token of one key head each), in boxes of a piece of a page by 64 columns.
-bool encode(CUtensorMap *m, const void *pool, const AttnDims &d) {
-    const EncodeTiledFn fn = encode_tiled();
-    if (!fn) return false;
-    const cuuint64_t dims[2] = {(cuuint64_t)d.D, (cuuint64_t)d.n_pages * d.hkv * d.page}, strides[1] = {(cuuint64_t)d.D * 2};
-    const cuuint32_t box[2] = {64u, (cuuint32_t)(d.page < kTile ? d.page : kTile)}, estr[2] = {1u, 1u};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(pool), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int D, int MT, int GR, int GS> cudaError_t run(AttnDecodeArgs a, const Maps &maps, cudaStream_t s) {
     using S = Shape<D, MT, GR, GS>;
     const auto kernel = attn_decode_tc_kernel<D, MT, GR, GS>;
@@ -585,7 +433,8 @@ template <int D> cudaError_t run_rows(const AttnDecodeArgs &a, const Maps &maps,
 
 cudaError_t launch_attn_decode_tc(const AttnDecodeArgs &a, cudaStream_t s) {
     Maps maps;
-    if (!encode(&maps.k, a.k_pages, a.d) || !encode(&maps.v, a.v_pages, a.d)) return cudaErrorInvalidValue;
+    if (!encode_pool(&maps.k, a.k_pages, a.d) || !encode_pool(&maps.v, a.v_pages, a.d)) return cudaErrorInvalidValue;
+    maps.q = maps.k;
     return a.d.D == 64 ? run_rows<64>(a, maps, s) : a.d.D == 128 ? run_rows<128>(a, maps, s) : run_rows<256>(a, maps, s);
 }
 
