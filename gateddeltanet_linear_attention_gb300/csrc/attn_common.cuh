@@ -50,7 +50,7 @@ struct AttnDecodeArgs {
     // first one, else 1: rows x D sums, then rows x (m, l), m in powers of two; and the join kernel's for CTA c
     float *parts;                     // [ctas][2][attn_part_floats]
     int4 *joins;                      // [ctas]: sequence, key head, slot of the first part, parts
-    int ctas;
+    int ctas, lead;                   // lead: see AttnWalk
 };
 // Most CTAs that share the work of a decode: the workspace is laid out for them.
 constexpr int kAttnCtasPerSm = 2, kAttnMaxCtas = 512;
@@ -92,11 +92,12 @@ template <int TILE> __device__ __forceinline__ AttnSeq attn_seq(const AttnDecode
 }
 
 // The batch as one line of tiles, sequence after sequence, in each its key heads after another, cut into
-// equal shares: CTA c takes tiles [c * per, (c + 1) * per) whatever sequences they belong to, so that mixed
-// lengths and single long ones keep every SM busy alike.  A unit is one key head of one sequence.
+// equal shares: CTA c takes places [c * per, (c + 1) * per) whatever sequences they belong to, so that mixed
+// lengths and single long ones keep every SM busy alike.  A unit is one key head of one sequence; in front of its
+// tiles lie `lead` places without any, as many as its end costs in tiles, so that who gets many short ones is not late.
 struct AttnWalk {
-    long long per, left;              // share of a CTA; tiles of this one still to do
-    long long at;                     // place of the tile on the line
+    long long per, left;              // places of a CTA; of this one still to do
+    int lead;                         // of them in front of the first unit
     int n, h, t;                      // sequence, key head, tile in the unit
     AttnSeq s;
 };
@@ -108,7 +109,7 @@ __device__ __forceinline__ bool attn_begin(const AttnDecodeArgs &a, int c, long 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int each = (a.n_seqs + THREADS - 1) / THREADS, lo = min(tid * each, a.n_seqs), hi = min(lo + each, a.n_seqs);
     long long mine = 0;
-    for (int n = lo; n < hi; ++n) mine += attn_seq<TILE>(a, n).tiles;
+    for (int n = lo; n < hi; ++n) mine += attn_seq<TILE>(a, n).tiles + a.lead;
     long long upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -130,33 +131,33 @@ __device__ __forceinline__ bool attn_begin(const AttnDecodeArgs &a, int c, long 
     const long long total = sums[WARPS - 1] * a.d.hkv;
     upto += warp > 0 ? sums[warp - 1] : 0;
     w.per = (total + a.ctas - 1) / a.ctas;
-    w.at = w.per * c;
-    if (w.at >= total) return false;
-    w.left = min(w.per, total - w.at);
+    const long long at = w.per * c;
+    if (at >= total) return false;
+    w.left = min(w.per, total - at);
     // the thread whose sequences hold the first tile finds which
-    if (w.at < upto * a.d.hkv && w.at >= (upto - mine) * a.d.hkv) {
+    if (at < upto * a.d.hkv && at >= (upto - mine) * a.d.hkv) {
         long long base = (upto - mine) * a.d.hkv;
         for (int n = lo; n < hi; ++n) {
-            const int tiles = attn_seq<TILE>(a, n).tiles;
-            if (w.at < base + (long long)tiles * a.d.hkv) {
+            const int places = attn_seq<TILE>(a, n).tiles + a.lead;
+            if (at < base + (long long)places * a.d.hkv) {
                 found[0] = n;
-                found[1] = (int)((w.at - base) / tiles);
-                found[2] = (int)((w.at - base) % tiles);
+                found[1] = (int)((at - base) / places);
+                found[2] = (int)((at - base) % places);
                 break;
             }
-            base += (long long)tiles * a.d.hkv;
+            base += (long long)places * a.d.hkv;
         }
     }
     __syncthreads();
     w.n = found[0];
     w.h = found[1];
-    w.t = found[2];
+    w.lead = max(a.lead - found[2], 0);
+    w.t = max(found[2] - a.lead, 0);
     w.s = attn_seq<TILE>(a, w.n);
-    return true;
+    return w.left > w.lead;
 }
-// To the next tile; true where a new unit begins.
+// To the next tile, where units lead with none; true where a new unit begins.
 template <int TILE> __device__ __forceinline__ bool attn_next(const AttnDecodeArgs &a, AttnWalk &w) {
-    ++w.at;
     --w.left;
     if (++w.t < w.s.tiles) return false;
     w.t = 0;

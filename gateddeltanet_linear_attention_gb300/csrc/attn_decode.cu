@@ -264,6 +264,7 @@ size_t attn_decode_ws_bytes(const AttnDims &d, int rows) {
 
 void attn_decode_carve(AttnDecodeArgs &a, void *ws) {
     a.ctas = most_ctas();
+    a.lead = 0;
     a.joins = (int4 *)ws;
     a.parts = (float *)(a.joins + a.ctas);
 }

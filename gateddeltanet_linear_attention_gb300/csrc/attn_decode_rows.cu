@@ -12,8 +12,8 @@
 // m is the maximum of a row's first tile and is raised only where a score passes it by 8 powers of two: P stays below 256,
 // which changes no rounding, and O is seldom scaled again.
 //
-// HBM-bound by design; what stands in the way is the chain of a tile, about 2,000 cycles (scores, 64 exponentials a thread,
-// products), two of which overlap.
+// Each group has S twice, so that the next tile's scores are there when its warps are done with one: a tile costs them about
+// 1,500 cycles (64 exponentials a thread), two groups one in 750, against 1,400 that its bytes take at 128 columns.  HBM-bound.
 #include "attn_tc.cuh"
 
 namespace gdn {
@@ -22,6 +22,7 @@ namespace {
 
 using namespace attn_tc;
 
+constexpr int kLead = 2;                           // tiles that a unit's end costs
 constexpr float kSlack = 8.f;                      // powers of two that a score may pass m by
 
 // NG groups; room for RB query rows (products read 128: behind them whatever follows, into lanes that nobody reads).
@@ -35,9 +36,9 @@ template <int D, int NG, int RB> struct Shape {
     // a multiple of the groups' entries: an entry then serves tiles of one group alone
     static constexpr int entries = fit < kMaxEntries ? fit / turn * turn : kMaxEntries;
     static constexpr int bytes = fixed + entries * entry;
-    static constexpr uint32_t col_o = 128;         // TMEM: S and P of group g at 64 g, its O at 128 + g D
+    static constexpr uint32_t col_o = 128 * NG;    // TMEM: S and P of group g's even and odd tiles at 128 g and 64 on, its O at col_o + g D
     static_assert(entries >= turn && entries % turn == 0, "a tile of each group in flight, in entries of its own");
-    static_assert(128 + NG * D <= 512, "tensor memory");
+    static_assert(128 * NG + NG * D <= 512, "tensor memory");
     static_assert(q_block + entries * entry >= 128 * 128 * (D / 64), "products read 128 rows of the last block");
 };
 
@@ -72,7 +73,15 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8])
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(threads) : "memory"); }
-enum { kBarGroup = 1, kBarActive = 3 };            // of each group, of its warps that have rows
+enum { kBarGroup = 1 };                            // of each group
+
+// Whether the phase of this parity is over.
+__device__ __forceinline__ bool test_wait(uint32_t b, uint32_t parity) {
+    uint32_t done;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+                 : "=r"(done) : "r"(b), "r"(parity) : "memory");
+    return done != 0;
+}
 
 // 128-byte-swizzled operands, 64-column blocks `block` bytes apart.  K-major: the row index is M or N; MN-major: it is K.
 __device__ __forceinline__ uint64_t desc_k(uint32_t saddr) { return tc::smem_desc(saddr, 16, 1024) | (2ull << 61); }
@@ -90,7 +99,7 @@ __global__ void __launch_bounds__((Shape<D, NG, RB>::threads), 1) attn_decode_ro
     __shared__ long long sums[33];
     __shared__ int found[3], spoiled[NG];
     __shared__ uint32_t tmem_base;
-    __shared__ uint64_t bars[2 * kMaxEntries + 2 * kUnits + 4 * NG + 2];
+    __shared__ uint64_t bars[2 * kMaxEntries + 2 * kUnits + 9 * NG];
     __shared__ int pieces_of[kMaxEntries];
     __shared__ Unit units[kUnits];
     unsigned char *base = raw + ((1024u - (tc::smem_u32(raw) & 1023u)) & 1023u);
@@ -99,8 +108,8 @@ __global__ void __launch_bounds__((Shape<D, NG, RB>::threads), 1) attn_decode_ro
     float2 *stats = reinterpret_cast<float2 *>(ring + E * S::entry);               // [groups][128]: m and l
     unsigned *spoil = reinterpret_cast<unsigned *>(stats + NG * 128);              // [groups][D]: new tokens whose sum is not finite
     const uint32_t entries = tc::smem_u32(ring), full = tc::smem_u32(bars), empty = full + 8 * kMaxEntries,
-                   ufull = empty + 8 * kMaxEntries, uempty = ufull + 8 * kUnits, s_full = uempty + 8 * kUnits, p_ready = s_full + 8 * NG,
-                   pv_done = p_ready + 8 * NG, ended = pv_done + 8 * NG, merged = ended + 8 * NG, taken = merged + 8;
+                   ufull = empty + 8 * kMaxEntries, uempty = ufull + 8 * kUnits, s_full = uempty + 8 * kUnits, p_ready = s_full + 16 * NG,
+                   pv_done = p_ready + 16 * NG, ended = pv_done + 16 * NG, merged = ended + 8 * NG, taken = merged + 8 * NG;
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int rows = a.d.grp * a.tokens, active = (rows + 31) / 32;                // warps of a group that have rows
     if (tid == 0) {
@@ -112,15 +121,18 @@ __global__ void __launch_bounds__((Shape<D, NG, RB>::threads), 1) attn_decode_ro
             tc::mbar_init(ufull + 8 * u, 1);
             tc::mbar_init(uempty + 8 * u, 5 * NG);
         }
-        for (int g = 0; g < NG; ++g) {
+        // even and odd tiles of a group on barriers of their own: no waiter is ever two phases behind
+        for (int g = 0; g < 2 * NG; ++g) {
             tc::mbar_init(s_full + 8 * g, 1);
             tc::mbar_init(p_ready + 8 * g, active);
             tc::mbar_init(pv_done + 8 * g, 1);
+        }
+        for (int g = 0; g < NG; ++g) {
             tc::mbar_init(ended + 8 * g, 1);
+            tc::mbar_init(merged + 8 * g, active);
+            tc::mbar_init(taken + 8 * g, active);
             spoiled[g] = 0;
         }
-        tc::mbar_init(merged, active);
-        tc::mbar_init(taken, active);
         tc::mbar_fence_init();
     }
     for (int i = tid; i < NG * D; i += kThreads) spoil[i] = 0u;
@@ -158,49 +170,73 @@ __global__ void __launch_bounds__((Shape<D, NG, RB>::threads), 1) attn_decode_ro
         // ---------------------------------------------------------- products
         constexpr uint32_t id_s = tc::idesc_bf16(128, kTile), id_pv = tc::idesc_bf16(128, D) | tc::kTransB;
         const int g = warp - 4 * NG - 1;
-        const uint32_t lead = elect_lane(), t_s = tmem + g * 64, t_o = tmem + S::col_o + g * D;
-        uint32_t e = 2 * g, phase = 0, k = 0;               // k: tiles of the group so far
-        bool ok = true;
-        auto wait = [&](uint32_t b, uint32_t parity) { ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(b, parity, a.wait_ns)); };
-        int u = 0;
-        for (long long left = w.left; left > 0 && ok; ++u) {
-            const uint32_t us = u % kUnits;
-            wait(ufull + 8 * us, (u / kUnits) & 1);
-            if (!ok) break;
-            const int count = units[us].count, seq0 = units[us].seq0;
-            left -= count;
-            const uint64_t q_desc = desc_k(tc::smem_u32(q_mem) + us * S::q_block);
-            uint32_t sum = 0;                               // whether O holds this unit's sums
-            for (int j = (g - seq0) & (NG - 1); j < count && ok; j += NG) {
-                wait(full + 8 * e, phase);
-                if (k > 0) wait(pv_done + 8 * g, (k - 1) & 1);      // P of the tile before has been read
-                if (!ok) break;
-                tc::fence_after_sync();
-                const uint64_t k_desc = desc_k(entries + e * S::entry);
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks) mma_ss(lead, t_s, q_desc + step_k(ks, kQBlock), k_desc + step_k(ks, kBlock), id_s, ks > 0);
-                commit(lead, s_full + 8 * g);
-                commit(lead, empty + 8 * e);
-                wait(full + 8 * (e + 1), phase);
-                wait(p_ready + 8 * g, k & 1);
-                if (!ok) break;
-                tc::fence_after_sync();
-                const uint64_t v_desc = desc_mn(entries + (e + 1) * S::entry, kBlock);
-#pragma unroll
-                for (int ks = 0; ks < 2 * kTile / 16; ++ks) {       // the leading parts of P, then the rest
-                    mma_ts(lead, t_o, t_s + ks * 8, v_desc + step_mn(ks & (kTile / 16 - 1)), id_pv, sum);
-                    sum = 1;
-                }
-                commit(lead, pv_done + 8 * g);
-                commit(lead, empty + 8 * (e + 1));
-                ++k;
-                e += 2 * NG;
-                if (e >= E) {
-                    e -= E;
-                    phase ^= 1;
-                }
+        const uint32_t lead = elect_lane(), t_s = tmem + g * 128, t_o = tmem + S::col_o + g * D;
+        // Scores of tile `ks` of the group, one ahead at most of the sums of tile `kp`: whatever can go first goes.
+        uint32_t se = 2 * g, sphase = 0, ks = 0, pe = 2 * g, pphase = 0, kp = 0, fresh = 0;      // fresh: tiles that begin a unit's sums
+        int u = 0, j = 0, count = 0, opened = 0;            // the unit that the scores are in; whether its queries are there
+        bool ok = true, first = true, more = true;
+        uint64_t q_desc = 0, t0 = 0;
+        auto there = [&](uint32_t b, uint32_t parity) { return __all_sync(0xffffffffu, test_wait(b, parity)); };
+        while (more || opened || kp < ks) {
+            bool moved = false;
+            if (!opened && more && there(ufull + 8 * (u % kUnits), (u / kUnits) & 1)) {
+                const Unit &unit = units[u % kUnits];
+                count = unit.count;
+                more = unit.more;
+                j = (g - unit.seq0) & (NG - 1);
+                q_desc = desc_k(tc::smem_u32(q_mem) + (u % kUnits) * S::q_block);
+                opened = 1;
+                first = true;
+                moved = true;
             }
-            if (ok) commit(lead, uempty + 8 * us);
+            if (opened && j < count && ks - kp < 2 && there(full + 8 * se, sphase) &&
+                (ks < 2 || there(pv_done + 16 * g + 8 * (ks & 1), ((ks - 2) >> 1) & 1))) {
+                tc::fence_after_sync();
+                const uint64_t k_desc = desc_k(entries + se * S::entry);
+#pragma unroll
+                for (int c = 0; c < KS; ++c) mma_ss(lead, t_s + (ks & 1) * 64, q_desc + step_k(c, kQBlock), k_desc + step_k(c, kBlock), id_s, c > 0);
+                commit(lead, s_full + 16 * g + 8 * (ks & 1));
+                commit(lead, empty + 8 * se);
+                fresh = first ? fresh | 1u << (ks & 1) : fresh & ~(1u << (ks & 1));
+                first = false;
+                ++ks;
+                j += NG;
+                se += 2 * NG;
+                if (se >= E) {
+                    se -= E;
+                    sphase ^= 1;
+                }
+                moved = true;
+            }
+            if (opened && j >= count) {                     // the unit's queries have been used
+                commit(lead, uempty + 8 * (u % kUnits));
+                ++u;
+                opened = 0;
+            }
+            if (kp < ks && there(full + 8 * (pe + 1), pphase) && there(p_ready + 16 * g + 8 * (kp & 1), (kp >> 1) & 1)) {
+                tc::fence_after_sync();
+                const uint64_t v_desc = desc_mn(entries + (pe + 1) * S::entry, kBlock);
+                const uint32_t t_p = t_s + (kp & 1) * 64;
+#pragma unroll
+                for (int c = 0; c < 2 * kTile / 16; ++c)    // the leading parts of P, then the rest
+                    mma_ts(lead, t_o, t_p + c * 8, v_desc + step_mn(c & (kTile / 16 - 1)), id_pv, c > 0 || !(fresh >> (kp & 1) & 1));
+                commit(lead, pv_done + 16 * g + 8 * (kp & 1));
+                commit(lead, empty + 8 * (pe + 1));
+                ++kp;
+                pe += 2 * NG;
+                if (pe >= E) {
+                    pe -= E;
+                    pphase ^= 1;
+                }
+                moved = true;
+            }
+            if (moved) {
+                t0 = 0;
+            } else {
+                const uint64_t t = tc::globaltimer_ns();
+                if (t0 == 0) t0 = t;
+                if (!(ok = __all_sync(0xffffffffu, t - t0 <= a.wait_ns))) break;
+            }
         }
         if (!ok && lane == 0) set_error(a.err, GDN_DEVERR_TIMEOUT);
         // products under way end before tensor memory is given back
@@ -211,13 +247,13 @@ __global__ void __launch_bounds__((Shape<D, NG, RB>::threads), 1) attn_decode_ro
         const int g = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
         const bool on = quarter < active;                   // this warp has rows
         const int token = min(row / a.d.grp, a.tokens - 1);
-        const uint32_t lanes = (uint32_t)(quarter * 32) << 16, t_s = tmem + lanes + g * 64, t_o = tmem + lanes + S::col_o + g * D;
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16, t_s0 = tmem + lanes + g * 128, t_o0 = tmem + lanes + S::col_o, t_o = t_o0 + g * D;
         unsigned *my_spoil = spoil + g * D;
         uint32_t e = 2 * g, phase = 0, k = 0;
         bool ok = true;
         auto wait = [&](uint32_t b, uint32_t parity) { ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(b, parity, a.wait_ns)); };
         int u = 0;
-        for (long long left = w.left; left > 0; ++u) {
+        for (bool more = true; more; ++u) {
             const uint32_t us = u % kUnits;
             // a group's warps give up together: they meet at its barrier
             if (!bar_all(kBarGroup + g, 128, ok && tc::mbar_wait(ufull + 8 * us, (u / kUnits) & 1, a.wait_ns))) {
@@ -225,14 +261,14 @@ __global__ void __launch_bounds__((Shape<D, NG, RB>::threads), 1) attn_decode_ro
                 break;
             }
             const Unit unit = units[us];
-            left -= unit.count;
+            more = unit.more;
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(uempty + 8 * us);
             const int first_j = (g - unit.seq0) & (NG - 1), tiles = unit.count > first_j ? (unit.count - first_j + NG - 1) / NG : 0;
-            // the second group's O and statistics are the first one's until it has taken them
-            bool mine = g == 0 || u == 0;
+            // a group's O and statistics are the other's too until that has taken them
+            bool mine = NG == 1 || u == 0;
             auto take_back = [&]() {
-                if (!mine) wait(taken, (u - 1) & 1);
+                if (!mine) wait(taken + 8 * (NG - 1 - g), (u - 1) & 1);
                 mine = true;
             };
             if (spoiled[g]) {
@@ -249,7 +285,8 @@ __global__ void __launch_bounds__((Shape<D, NG, RB>::threads), 1) attn_decode_ro
             const int end = open + token, begin = a.window > 0 ? end - a.window : 0;
             for (int j = first_j; j < unit.count; j += NG) {
                 const int i0 = unit.i0 + j * kTile;
-                wait(s_full + 8 * g, k & 1);
+                const uint32_t t_s = t_s0 + (k & 1) * 64;
+                wait(s_full + 16 * g + 8 * (k & 1), (k >> 1) & 1);
                 // V's entry stays this tile's until its product is done; K's may be another tile's by now
                 wait(full + 8 * (e + 1), phase);
                 tc::fence_after_sync();
@@ -279,7 +316,7 @@ __global__ void __launch_bounds__((Shape<D, NG, RB>::threads), 1) attn_decode_ro
                     const float back = nm == m ? 1.f : exp2_fast(m - nm);
                     m = nm;
                     l *= back;
-                    wait(pv_done + 8 * g, (k - 1) & 1);     // the sums are whole
+                    wait(pv_done + 16 * g + 8 * ((k - 1) & 1), ((k - 1) >> 1) & 1);      // the sums are whole
                     tc::fence_after_sync();
                     for (int c = 0; c < D; c += 16) {
                         float o[16];
@@ -347,7 +384,7 @@ __global__ void __launch_bounds__((Shape<D, NG, RB>::threads), 1) attn_decode_ro
                 tc::fence_before_sync();
                 if (j == first_j) take_back();              // O is written anew
                 __syncwarp();
-                if (ok && lane == 0) tc::mbar_arrive(p_ready + 8 * g);
+                if (ok && lane == 0) tc::mbar_arrive(p_ready + 16 * g + 8 * (k & 1));
                 ++k;
                 e += 2 * NG;
                 if (e >= E) {
@@ -355,39 +392,30 @@ __global__ void __launch_bounds__((Shape<D, NG, RB>::threads), 1) attn_decode_ro
                     phase ^= 1;
                 }
             }
-            if (tiles > 0) wait(pv_done + 8 * g, (k - 1) & 1);
+            if (tiles > 0) wait(pv_done + 16 * g + 8 * ((k - 1) & 1), ((k - 1) >> 1) & 1);
+            take_back();
+            stats[g * 128 + row] = make_float2(m, l);
+            tc::fence_before_sync();
+            __syncwarp();
+            if (ok && lane == 0) tc::mbar_arrive(merged + 8 * g);
+            // all warps' statistics and sums (and what any of them spoiled); each group then ends a share of the columns
+            for (int i = 0; i < NG; ++i) wait(merged + 8 * i, u & 1);
             tc::fence_after_sync();
-            if (g > 0) {
-                take_back();
-                stats[g * 128 + row] = make_float2(m, l);
-                bar_sync(kBarActive + g, active * 32);      // (and what any of its warps spoiled)
-                if (ok && lane == 0) tc::mbar_arrive(merged);
-                continue;
-            }
-            bar_sync(kBarActive, active * 32);
-            // whether the second group has sums of this unit
-            const bool two = NG > 1 && unit.count > ((1 - unit.seq0) & (NG - 1));
-            float f0 = 1.f, f1 = 0.f, total = l, nm = m;
-            if (NG > 1) {
-                wait(merged, u & 1);
-                tc::fence_after_sync();
-                const float2 other = stats[128 * (NG - 1) + row];
-                nm = fmaxf(m, other.x);
-                const float ref = nm == -INFINITY ? 0.f : nm;
-                f0 = exp2_fast(m - ref);
-                f1 = exp2_fast(other.x - ref);
-                total = l * f0 + other.y * f1;
-            }
+            const float2 s0 = stats[row], s1 = NG > 1 ? stats[128 * (NG - 1) + row] : make_float2(-INFINITY, 0.f);
+            const float nm = fmaxf(s0.x, s1.x), ref = nm == -INFINITY ? 0.f : nm;
+            const float f0 = exp2_fast(s0.x - ref), f1 = exp2_fast(s1.x - ref), total = s0.y * f0 + s1.y * f1;
+            // whether the groups have sums of this unit
+            const bool one = unit.count > ((0 - unit.seq0) & (NG - 1)), two = NG > 1 && unit.count > ((1 - unit.seq0) & (NG - 1));
             if (ok) {
                 const bool bad = spoiled[0] || (NG > 1 && spoiled[NG - 1]);
                 const bool whole = unit.slot < 0, there = row < rows;
                 const long long orow = ((long long)unit.n * a.tokens + token) * a.d.hq + unit.h * a.d.grp + row - token * a.d.grp;
                 float *part = attn_part(a, blockIdx.x, max(unit.slot, 0));
                 const float inv = whole ? (total == 0.f ? 0.f : 1.f / total) : 1.f;
-                for (int c = 0; c < D; c += 16) {
+                for (int c = g * (D / NG); c < (g + 1) * (D / NG); c += 16) {
                     float x[16];
-                    if (tiles > 0) {
-                        tc::tmem_ld16(t_o + c, x);
+                    if (one) {
+                        tc::tmem_ld16(t_o0 + c, x);
 #pragma unroll
                         for (int i = 0; i < 16; ++i) x[i] *= f0;
                     } else {
@@ -396,7 +424,7 @@ __global__ void __launch_bounds__((Shape<D, NG, RB>::threads), 1) attn_decode_ro
                     }
                     if (two) {
                         float y[16];
-                        tc::tmem_ld16(t_o + D + c, y);
+                        tc::tmem_ld16(t_o0 + D + c, y);
 #pragma unroll
                         for (int i = 0; i < 16; ++i) x[i] = fmaf(y[i], f1, x[i]);
                     }
@@ -417,14 +445,14 @@ __global__ void __launch_bounds__((Shape<D, NG, RB>::threads), 1) attn_decode_ro
                         for (int i = 0; i < 4; ++i) store4f(part + row * D + c + 4 * i, make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]));
                     }
                 }
-                if (there) {
+                if (there && g == 0) {
                     if (!whole) *reinterpret_cast<float2 *>(part + rows * D + 2 * row) = make_float2(nm, total);
                     else if (a.lse) a.lse[orow] = total == 0.f ? -INFINITY : (nm + log2f(total)) * kLn2;
                 }
             }
             tc::fence_before_sync();
             __syncwarp();
-            if (NG > 1 && ok && lane == 0) tc::mbar_arrive(taken);
+            if (NG > 1 && ok && lane == 0) tc::mbar_arrive(taken + 8 * g);
         }
         if (!ok && lane == 0) set_error(a.err, GDN_DEVERR_TIMEOUT);
     }
@@ -440,6 +468,7 @@ template <int D, int NG, int RB> cudaError_t run(AttnDecodeArgs a, const Maps &m
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::bytes);
     if (e != cudaSuccess) return e;
     a.ctas = sm_count();
+    a.lead = kLead;
     const cudaError_t l = launch_early(kernel, dim3(a.ctas), S::threads, S::bytes, s, a, maps);
     return l != cudaSuccess ? l : launch_attn_join(a, true, s);
 }

@@ -20,6 +20,7 @@ namespace {
 
 using namespace attn_tc;
 
+constexpr int kLead = 1;                           // tiles that a unit's end costs
 constexpr int kPPitch = kTile * 2 + 16;            // bytes of a row of P: ldmatrix without bank conflicts
 
 // MT blocks of 16 query rows a group, GR groups of rows, GS sets of each.
@@ -134,7 +135,7 @@ __global__ void __launch_bounds__((Shape<D, MT, GR, GS>::threads), 1) attn_decod
     uint32_t e = 2 * set, phase = 0;                    // the entry of the set's next tile
     bool ok = true;
     int u = 0;
-    for (long long left = w.left; left > 0; ++u) {
+    for (bool more = true; more; ++u) {
         const uint32_t us = u % kUnits;
         // a group's warps give up together: they meet at its barrier
         if (!bar_all(kBarGroup + group, 128, ok && tc::mbar_wait(ufull + 8 * us, (u / kUnits) & 1, a.wait_ns))) {
@@ -142,7 +143,7 @@ __global__ void __launch_bounds__((Shape<D, MT, GR, GS>::threads), 1) attn_decod
             break;
         }
         const Unit unit = units[us];
-        left -= unit.count;
+        more = unit.more;
         const uint32_t q_base = tc::smem_u32(q_mem) + us * S::q_block + row_g * S::q_pitch + q_lane;
         float m[MT][2], l[MT][2], o[MT][NT][4];
 #pragma unroll
@@ -416,6 +417,7 @@ template <int D, int MT, int GR, int GS> cudaError_t run(AttnDecodeArgs a, const
     // blocks of query rows read the same tiles: at the same time, so that the second one finds them in L2
     const int blocks = (a.d.grp * a.tokens + S::rows - 1) / S::rows;
     a.ctas = sm_count() / blocks;
+    a.lead = kLead;
     const cudaError_t l = launch_early(kernel, dim3(a.ctas, blocks), S::threads, S::bytes, s, a, maps);
     return l != cudaSuccess ? l : launch_attn_join(a, true, s);
 }

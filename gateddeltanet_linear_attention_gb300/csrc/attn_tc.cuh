@@ -16,6 +16,7 @@ constexpr int kMaxEntries = 24;                    // of the ring of K and V til
 // A unit's tiles in this CTA, as the copying warp describes them.
 struct Unit {
     int n, h, len, first, i0, count, seq0, slot;   // slot -1: the unit is whole
+    bool more;                                     // the CTA has another one
 };
 
 struct Maps {
@@ -65,16 +66,19 @@ __device__ __forceinline__ void copy_tiles(const AttnDecodeArgs &a, const AttnWa
     };
     AttnSeq s = w.s;
     int n = w.n, h = w.h, t0 = w.t, page = page_of(s, t0);
-    for (long long left = w.left; left > 0 && alive; ++u) {
+    long long left = w.left - w.lead;
+    for (bool more = true; more && alive; ++u) {
         const int count = (int)min((long long)(s.tiles - t0), left);
         const bool unit_end = t0 + count == s.tiles;
+        left -= count + a.lead;
+        more = unit_end && left > 0;                        // (what remains has tiles of the next unit)
         const int slot = t0 == 0 && unit_end ? -1 : u == 0 ? 0 : 1;
         const uint32_t us = u % kUnits, uphase = (u / kUnits) & 1;
         if (u >= kUnits) alive = tc::mbar_wait(uempty + 8 * us, uphase ^ 1, a.wait_ns);
         alive = __all_sync(0xffffffffu, alive);
         if (!alive) break;
         if (lane == 0) {
-            units[us] = Unit{n, h, s.len, s.first, (s.tile0 + t0) * kTile, count, seq, slot};
+            units[us] = Unit{n, h, s.len, s.first, (s.tile0 + t0) * kTile, count, seq, slot, more};
             tc::mbar_arrive_expect_tx(ufull + 8 * us, q_bytes);
         }
         __syncwarp();
@@ -110,7 +114,7 @@ __device__ __forceinline__ void copy_tiles(const AttnDecodeArgs &a, const AttnWa
                     phase ^= 1;
                 }
             }
-            if (j == 0 && left > count) {
+            if (j == 0 && more) {
                 if (next_h == a.d.hkv) {
                     next_h = 0;
                     next_s = attn_seq<kTile>(a, ++next_n);
@@ -119,8 +123,7 @@ __device__ __forceinline__ void copy_tiles(const AttnDecodeArgs &a, const AttnWa
             }
         }
         seq += count;
-        left -= count;
-        if (left == 0 && blockIdx.y == 0 && lane == 0) {
+        if (!more && blockIdx.y == 0 && lane == 0) {
             // the CTA that holds a unit's front joins it: the CTAs behind that hold the rest
             int parts = 0;
             if (!unit_end && t0 == 0) parts = 1 + (int)((s.tiles - count + w.per - 1) / w.per);
