@@ -15,11 +15,9 @@ namespace {
 constexpr int kSimtThreads = 256;
 constexpr int kSimtTile = 32;
 
-template <typename T> __device__ __forceinline__ void store1(T *p, float v) { *p = from_f32<T>(v); }
-
-// CUDA-core form: RPW query rows a warp, a tile of 32 tokens in shared memory as 32-bit values, a token a
-// lane for the scores and D / 32 columns a lane for the sums.
-template <typename T, int D, int RPW>
+// The 32-bit form, on the CUDA cores: RPW query rows a warp, a tile of 32 tokens in shared memory, a token a lane for the
+// scores and D / 32 columns a lane for the sums.
+template <int D, int RPW>
 __global__ void __launch_bounds__(kSimtThreads) attn_decode_simt_kernel(const AttnDecodeArgs a) {
     constexpr int TILE = kSimtTile, LDK = D + 4, CPL = D / 32, WARPS = kSimtThreads / 32, RB = WARPS * RPW;
     extern __shared__ float4 smem4[];
@@ -34,7 +32,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_decode_simt_kernel(const At
         if (blockIdx.y == 0 && tid == 0) a.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
         return;
     }
-    const T *kp = (const T *)a.k_pages, *vp = (const T *)a.v_pages;
+    const float *kp = (const float *)a.k_pages, *vp = (const float *)a.v_pages;
     bool unit_first = true;               // this unit is the CTA's first one
     while (w.left > 0) {
         const bool whole_front = w.t == 0;
@@ -47,7 +45,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_decode_simt_kernel(const At
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < rows) {
                 const int tok = r / a.d.grp, g = r % a.d.grp;
-                v = load4f((const T *)a.q + ((long long)n * a.tokens + tok) * a.ld_q + (long long)(h * a.d.grp + g) * a.hs_q + c);
+                v = load4f((const float *)a.q + ((long long)n * a.tokens + tok) * a.ld_q + (long long)(h * a.d.grp + g) * a.hs_q + c);
             }
             reinterpret_cast<float4 *>(qs)[i] = v;
         }
@@ -160,7 +158,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_decode_simt_kernel(const At
 #pragma unroll
                 for (int c = 0; c < CPL; ++c) {
                     const int col = CPL == 2 ? lane * 2 + c : lane * 4 + (c >> 2) * 128 + (c & 3);
-                    if (whole) store1((T *)a.out + orow * D + col, o[r][c] * inv);
+                    if (whole) ((float *)a.out)[orow * D + col] = o[r][c] * inv;
                     else part[row * D + col] = o[r][c];
                 }
                 if (lane == 0) {
@@ -231,24 +229,20 @@ template <typename T, int D> __global__ void __launch_bounds__(kJoinThreads) att
     }
 }
 
-template <typename T, int D, int RPW> cudaError_t run_simt(const AttnDecodeArgs &a, cudaStream_t s) {
+template <int D, int RPW> cudaError_t run_simt(const AttnDecodeArgs &a, cudaStream_t s) {
     constexpr int RB = kSimtThreads / 32 * RPW, smem = (kSimtTile * (D + 4) + kSimtTile * D + RB * D) * 4;
-    const auto kernel = attn_decode_simt_kernel<T, D, RPW>;
+    const auto kernel = attn_decode_simt_kernel<D, RPW>;
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
     }
     const int rows = a.d.grp * a.tokens;
     const cudaError_t e = launch_early(kernel, dim3(a.ctas, (rows + RB - 1) / RB), kSimtThreads, smem, s, a);
-    if (e != cudaSuccess) return e;
-    return launch_attn_join(a, sizeof(T) == 2, s);
+    return e != cudaSuccess ? e : launch_attn_join(a, false, s);
 }
-template <typename T, int D> cudaError_t run_rows(const AttnDecodeArgs &a, cudaStream_t s) {
+template <int D> cudaError_t run_rows(const AttnDecodeArgs &a, cudaStream_t s) {
     const int rows = a.d.grp * a.tokens;
-    return rows <= 8 ? run_simt<T, D, 1>(a, s) : rows <= 16 ? run_simt<T, D, 2>(a, s) : run_simt<T, D, 4>(a, s);
-}
-template <typename T> cudaError_t run_dim(const AttnDecodeArgs &a, cudaStream_t s) {
-    return a.d.D == 64 ? run_rows<T, 64>(a, s) : a.d.D == 128 ? run_rows<T, 128>(a, s) : run_rows<T, 256>(a, s);
+    return rows <= 8 ? run_simt<D, 1>(a, s) : rows <= 16 ? run_simt<D, 2>(a, s) : run_simt<D, 4>(a, s);
 }
 
 int most_ctas() {
@@ -281,8 +275,12 @@ cudaError_t launch_attn_join(const AttnDecodeArgs &a, bool act_bf16, cudaStream_
                         : launch_early(attn_join_kernel<float, 256>, grid, kJoinThreads, 0, s, a);
 }
 
+// bf16: where 16 query rows hold all of a key head's, their products keep up with the memory (64 sequences of up to 16,384
+// tokens, 4 rows: 378 us against 424 us in the kernel of many rows; 32 of up to 8,192, 16 rows: 57 against 71).  Above, tcgen05
+// products of 128 rows take what 16 rows would read again: 32 rows in two blocks that share tiles took 451 us against 427 in
+// the first batch (in small calls less, 11 us against 13 for one sequence of 700 tokens; not worth a kernel of its own).
 cudaError_t launch_attn_decode(const AttnDecodeArgs &a, bool act_bf16, cudaStream_t s) {
-    if (!act_bf16) return run_dim<float>(a, s);
+    if (!act_bf16) return a.d.D == 64 ? run_rows<64>(a, s) : a.d.D == 128 ? run_rows<128>(a, s) : run_rows<256>(a, s);
     return a.d.grp * a.tokens <= 16 ? launch_attn_decode_tc(a, s) : launch_attn_decode_rows(a, s);
 }
 

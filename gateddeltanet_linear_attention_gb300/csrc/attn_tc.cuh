@@ -123,7 +123,7 @@ __device__ __forceinline__ void copy_tiles(const AttnDecodeArgs &a, const AttnWa
             }
         }
         seq += count;
-        if (!more && blockIdx.y == 0 && lane == 0) {
+        if (!more && lane == 0) {
             // the CTA that holds a unit's front joins it: the CTAs behind that hold the rest
             int parts = 0;
             if (!unit_end && t0 == 0) parts = 1 + (int)((s.tiles - count + w.per - 1) / w.per);
@@ -138,7 +138,7 @@ __device__ __forceinline__ void copy_tiles(const AttnDecodeArgs &a, const AttnWa
     if (lane == 0) {
         if (!alive) {             // nothing more is copied
             set_error(a.err, GDN_DEVERR_TIMEOUT);
-            if (blockIdx.y == 0) a.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
+            a.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
         }
         // what is under way arrives before the block ends
         for (uint32_t k = 0; k < min(issued, E); ++k) {
