@@ -113,6 +113,9 @@ __global__ void __launch_bounds__((Shape<D, NG, RB>::threads), 1) attn_decode_ro
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int rows = a.d.grp * a.tokens, active = (rows + 31) / 32;                // warps of a group that have rows
     if (tid == 0) {
+        prefetch_map(&maps.k);
+        prefetch_map(&maps.v);
+        prefetch_map(&maps.q);
         for (uint32_t e = 0; e < E; ++e) {
             tc::mbar_init(full + 8 * e, 1);
             tc::mbar_init(empty + 8 * e, 1);

@@ -74,6 +74,8 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) attn_decode_tc_k
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rows = a.d.grp * a.tokens;
     if (tid == 0) {
+        prefetch_map(&maps.k);
+        prefetch_map(&maps.v);
         for (uint32_t e = 0; e < E; ++e) {
             tc::mbar_init(full + 8 * e, 1);
             tc::mbar_init(empty + 8 * e, 4);

@@ -23,6 +23,9 @@ struct Maps {
     CUtensorMap k, v, q;                           // q: where the kernel takes query rows by TMA
 };
 
+// The maps on their way before the first copy asks for them.
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *m) { asm volatile("prefetch.tensormap [%0];" :: "l"(m) : "memory"); }
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
