@@ -9,6 +9,7 @@ namespace {
 
 constexpr int kMaxRows = 65535;
 constexpr int kMaxPages = 1 << 24;
+constexpr int kMaxLength = 1 << 30;
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
@@ -33,8 +34,8 @@ gdn_status check_cfg(const gdn_attn_config *c, gdn::AttnDims *d) {
     if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128) return GDN_ERR_UNSUPPORTED;
     if (c->q_heads / c->kv_heads > gdn::kAttnMaxGroup || c->q_heads > 4096 || c->n_rows > kMaxRows || c->n_pages > kMaxPages)
         return GDN_ERR_UNSUPPORTED;
-    // lengths, and the rows of a pool (one token of one key head each), are 32-bit numbers
-    if ((long long)c->max_pages * c->page_size > INT_MAX || (long long)c->n_pages * c->kv_heads * c->page_size > INT_MAX)
+    // lengths with a tile behind them, and the rows of a pool (one token of one key head each), are 32-bit numbers
+    if ((long long)c->max_pages * c->page_size > kMaxLength || (long long)c->n_pages * c->kv_heads * c->page_size > INT_MAX)
         return GDN_ERR_UNSUPPORTED;
     d->hq = c->q_heads; d->hkv = c->kv_heads; d->grp = c->q_heads / c->kv_heads; d->D = c->head_dim;
     d->page = c->page_size;
@@ -44,7 +45,7 @@ gdn_status check_cfg(const gdn_attn_config *c, gdn::AttnDims *d) {
 }
 
 // What both directions of the norm and rotation share.
-gdn_status check_prep(const gdn_attn_config *cfg, const gdn_attn_prep_io *io, bool backward, gdn::AttnPrepArgs *a) {
+gdn_status check_prep(const gdn_attn_config *cfg, const gdn_attn_prep_io *io, gdn::AttnPrepArgs *a) {
     gdn_status st = check_cfg(cfg, &a->d);
     if (st != GDN_OK) return st;
     if (!io || io->T < 0 || io->n_seqs < 0) return GDN_ERR_INVALID_ARG;
@@ -78,7 +79,7 @@ extern "C" {
 
 gdn_status gdn_attn_prep(const gdn_attn_config *cfg, const gdn_attn_prep_io *io, void *stream) {
     gdn::AttnPrepArgs a{};
-    gdn_status st = check_prep(cfg, io, false, &a);
+    gdn_status st = check_prep(cfg, io, &a);
     if (st != GDN_OK) return st;
     const gdn::AttnDims &d = a.d;
     const bool pools = io->k_pages != nullptr;
@@ -108,7 +109,7 @@ size_t gdn_attn_prep_workspace_size(const gdn_attn_config *cfg, int64_t max_toke
 gdn_status gdn_attn_prep_backward(const gdn_attn_config *cfg, const gdn_attn_prep_io *io, void *workspace,
                                   size_t workspace_bytes, void *stream) {
     gdn::AttnPrepArgs a{};
-    gdn_status st = check_prep(cfg, io, true, &a);
+    gdn_status st = check_prep(cfg, io, &a);
     if (st != GDN_OK) return st;
     const gdn::AttnDims &d = a.d;
     if (!aligned16(io->dq_out) || !aligned16(io->dk_out) || !aligned4(io->dw_q) || !aligned4(io->dw_k) ||
@@ -144,7 +145,7 @@ gdn_status gdn_attn_decode(const gdn_attn_config *cfg, const gdn_attn_decode_io 
     gdn::AttnDecodeArgs a{};
     gdn_status st = check_cfg(cfg, &a.d);
     if (st != GDN_OK) return st;
-    if (!io || io->n_seqs < 0 || io->tokens < 1 || io->window < 0 || !std::isfinite(io->scale) || !(io->scale > 0.f))
+    if (!io || io->n_seqs < 0 || io->tokens < 1 || io->window < 0 || !std::isfinite(io->scale * gdn::kLog2e) || !(io->scale > 0.f))
         return GDN_ERR_INVALID_ARG;
     if (io->tokens > gdn::kAttnMaxTokens || io->n_seqs > kMaxRows) return GDN_ERR_UNSUPPORTED;
     if (io->n_seqs == 0) return GDN_OK;
@@ -159,7 +160,9 @@ gdn_status gdn_attn_decode(const gdn_attn_config *cfg, const gdn_attn_decode_io 
     if ((st = gdn::device_error_word(&a.err)) != GDN_OK) return st;
     a.q = io->q; a.ld_q = io->ld_q; a.hs_q = io->hs_q; a.k_pages = io->k_pages; a.v_pages = io->v_pages;
     a.table = io->page_table; a.lens = io->lens; a.rows = io->rows;
-    a.n_seqs = io->n_seqs; a.tokens = io->tokens; a.window = io->window;
+    a.n_seqs = io->n_seqs; a.tokens = io->tokens;
+    // a window that no length reaches is none, and no difference of a length and a window leaves 32 bits
+    a.window = io->window < d.max_pages * d.page ? io->window : 0;
     a.scale_log2 = io->scale * gdn::kLog2e;
     a.out = io->out; a.lse = io->lse; a.wait_ns = gdn::wait_limit_ns();
     a.lose = gdn::lost_copies();

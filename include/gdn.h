@@ -540,7 +540,10 @@ gdn_status gdn_block_norm_backward(const gdn_block_norm_io *io, void *workspace,
  * lane treated as padding.  A length above max_pages * page_size (the
  * sequence is then treated as padding), and a page outside [0, n_pages)
  * (its tokens are neither read nor written, and count as masked) are
- * reported as GDN_DEVERR_PAGE. */
+ * reported as GDN_DEVERR_PAGE.
+ *
+ * Outputs overlap no input, and no other output, where a call does not say
+ * otherwise. */
 typedef struct gdn_attn_config {
     int32_t q_heads, kv_heads;   /* q_heads % kv_heads == 0, at most 16 query heads a key head */
     int32_t head_dim;            /* 64, 128 or 256 */
@@ -548,7 +551,7 @@ typedef struct gdn_attn_config {
     int32_t page_size;           /* tokens of a page: 16, 32, 64 or 128 */
     int32_t n_pages;             /* pages of each pool (capacity); 0: no cache */
     int32_t n_rows;              /* rows of the page table, at most 65535 */
-    int32_t max_pages;           /* columns of the page table */
+    int32_t max_pages;           /* columns of the page table; max_pages * page_size at most 2^30 */
 } gdn_attn_config;
 
 /* Norms and rotation of a packed batch's queries and keys, and its keys' and
@@ -626,7 +629,7 @@ typedef struct gdn_attn_decode_io {
     const int32_t *page_table, *lens, *rows;  /* rows may be NULL */
     int32_t n_seqs, tokens;
     int32_t window;                      /* 0: all tokens */
-    float scale;
+    float scale;                         /* > 0 */
     void *out;                           /* [n_seqs * tokens][q_heads * head_dim] */
     float *lse;                          /* [n_seqs * tokens][q_heads] or NULL */
 } gdn_attn_decode_io;

@@ -161,6 +161,17 @@ def test_decode_limits(lib):
     assert gdn.gdn_attn_workspace_size(cfg(), 3, 0) == gdn.gdn_attn_workspace_size(cfg(), 3, 9) == gdn.gdn_attn_workspace_size(cfg(), -1, 1) == 0
 
 
+def test_longest_length(lib):
+    """Lengths leave room for a tile in 32 bits."""
+    assert gdn.gdn_attn_workspace_size(cfg(page_size=64, max_pages=1 << 24), 3, 1) > 0
+    assert decode(lib, cfg(page_size=64, max_pages=(1 << 24) + 1)) == UNSUPPORTED
+
+
+def test_scale_beyond_the_powers_of_two(lib):
+    """A scale whose product with log2(e) is no 32-bit number."""
+    assert decode(lib, scale=3e38) == INVALID
+
+
 def test_page_refusals(lib):
     for kw in (dict(table=None), dict(lens=None), dict(refs=A + 2), dict(rows=None), dict(new=A + 1), dict(granted=None), dict(src=None),
                dict(dst=B + 2), dict(n=-1)):

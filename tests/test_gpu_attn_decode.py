@@ -107,6 +107,17 @@ def test_windows(act, window, tokens):
     assert torch.equal(out, out2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("act,Hq", [("bf16", 2), ("bf16", 8), ("fp32", 2)])
+@pytest.mark.parametrize("window", [2**31 - 1, 2**31 - 7, 2**30])
+def test_windows_without_end(act, Hq, window):
+    """A window of any size that no length reaches changes nothing, in sequences shorter than the new tokens either."""
+    c = Cache([0, 1, 3, 7, 8, 40, 130], Hq, 1, 64, 16, act, 8, seed=5).upload()
+    out, lse = c.run(window=window)
+    c.check(out, lse)
+    plain, _ = c.run()
+    assert torch.equal(out, plain)
+
+
 @pytest.mark.parametrize("act", ["bf16", "fp32"])
 def test_lengths_around_tiles(act):
     """Every length around the tiles' and pages' ends, in one batch."""
@@ -312,6 +323,20 @@ def test_other_stream():
     gdn.gdn_attn_decode(c.cfg, *c.d, out3, c.ws, stream=side)
     side.synchronize()
     assert torch.equal(out3, want)
+
+
+def test_calls_at_once():
+    """Calls on two streams, each with a workspace of its own, while the other's kernels run."""
+    pair = [Cache([900, 30, 2500, 0, 640], 8, 2, 128, 32, "bf16", tokens, seed=tokens).upload() for tokens in (8, 2)]
+    want = [c.run()[0] for c in pair]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in pair], [[torch.empty_like(w) for _ in range(20)] for w in want]
+    for i in range(20):
+        for c, s, g in zip(pair, streams, got):
+            gdn.gdn_attn_decode(c.cfg, *c.d, g[i], c.ws, tokens=c.tokens, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, w) for g, w in zip(got, want) for x in g)
+    assert gdn.gdn_device_error() == 0
 
 
 @pytest.mark.parametrize("D,tokens", [(64, 1), (128, 8), (256, 1)])
