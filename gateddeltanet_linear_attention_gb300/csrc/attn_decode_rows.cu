@@ -27,7 +27,7 @@ constexpr float kSlack = 8.f;                      // powers of two that a score
 
 // NG groups; room for RB query rows (products read 128: behind them whatever follows, into lanes that nobody reads).
 template <int D, int NG, int RB> struct Shape {
-    static constexpr int threads = (5 * NG + 1) * 32;
+    static constexpr int threads = (5 * NG + 2) * 32;
     static constexpr int units = D == 256 && RB == 128 ? 1 : 2;
     static constexpr int entry = kTile * D * 2, q_block = RB * D * 2;
     static constexpr int fixed = units * q_block + NG * (128 * 8 + D * 4) + 1024;
@@ -159,9 +159,9 @@ __global__ void __launch_bounds__((Shape<D, NG, RB>::threads), 1) attn_decode_ro
     tc::fence_after_sync();
     const uint32_t tmem = *(volatile uint32_t *)&tmem_base;
 
-    if (warp == 4 * NG) {
+    if (warp == 4 * NG || warp == 5 * NG + 1) {
         // ------------------------------------------------------------ copies
-        copy_tiles<D, E, kUnits>(a, w, maps, entries, full, empty, ufull, uempty, pieces_of, units, (uint32_t)rows * D * 2,
+        copy_tiles<D, E, kUnits>(a, w, maps, warp == 4 * NG ? 0 : 1, entries, full, empty, ufull, uempty, pieces_of, units, (uint32_t)rows * D * 2,
                                  [&](uint32_t us, int n, int h, uint32_t bar) {
             if (lane < D / 64)
                 asm volatile(

@@ -1,6 +1,6 @@
 // attn_decode_tc.cu -- attention of a few new tokens over a paged bf16 cache, on the tensor cores.
 //
-// The shares, parts and join of attn_decode.cu; here a tile is 64 tokens.  One warp copies tiles with TMA into a ring of
+// The shares, parts and join of attn_decode.cu; here a tile is 64 tokens.  Two warps copy tiles with TMA into a ring of
 // shared-memory entries (K and V of a tile in entries of their own, 128-byte swizzled).  Two sets of four warps take turns
 // with the tiles, for up to 16 query rows:
 //   S = Q K^T    warp w the tile's tokens 16 w .. 16 w + 15
@@ -23,7 +23,7 @@ constexpr int kLead = 1;                           // tiles that a unit's end co
 constexpr int kPPitch = kTile * 2 + 16;            // bytes of a row of P: ldmatrix without bank conflicts
 
 constexpr int kRows = 16, kSets = 2, kUnits = 2;   // query rows of a product, sets of warps, query blocks in flight
-constexpr int kConsumers = kSets * 128, kThreads = kConsumers + 32;
+constexpr int kConsumers = kSets * 128, kThreads = kConsumers + 64;
 
 template <int D> struct Shape {
     static constexpr int entry = kTile * D * 2, q_pitch = D * 2 + 16, q_block = kRows * q_pitch;
@@ -100,9 +100,9 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) attn_decode_tc_k
         return;
     }
 
-    if (warp == kConsumers / 32) {
+    if (warp >= kConsumers / 32) {
         // ------------------------------------------------------------ copies
-        copy_tiles<D, E, kUnits>(a, w, maps, entries, full, empty, ufull, uempty, pieces_of, units, (uint32_t)rows * D * 2,
+        copy_tiles<D, E, kUnits>(a, w, maps, warp - kConsumers / 32, entries, full, empty, ufull, uempty, pieces_of, units, (uint32_t)rows * D * 2,
                                  [&](uint32_t us, int n, int h, uint32_t bar) {
             if (lane < rows) {
                 const int tok = lane / a.d.grp, g = lane - tok * a.d.grp;

@@ -42,12 +42,13 @@ __device__ __forceinline__ bool bar_all(int id, int threads, bool mine) {
     return all != 0;
 }
 
-// The copying warp: the CTA's tiles into a ring of E entries, K's and V's of a tile one after the other, each as D / 64 blocks
-// of 64 tokens by 128 bytes in the 128-byte swizzle; its units into `units`, their query rows (q_bytes of them) by
-// load_q(slot, sequence, key head, barrier).  The barriers: full[E], empty[E]; ufull, uempty [kUnits].  pieces_of: which
-// 16-token pieces of an entry's tile are there (what is not there is not copied: the entry holds what it held).
+// The two copying warps: the CTA's tiles into a ring of E entries, K's and V's of a tile one after the other, each as D / 64
+// blocks of 64 tokens by 128 bytes in the 128-byte swizzle.  One warp (kv 0) copies K, one V: V's entries are needed longer,
+// and K's that are free would wait behind them.  The first also writes the units into `units` and fetches their query rows
+// (q_bytes of them) by load_q(slot, sequence, key head, barrier).  The barriers: full[E], empty[E]; ufull, uempty [kUnits].
+// pieces_of: which 16-token pieces of an entry's tile are there (what is not there is not copied: the entry holds what it held).
 template <int D, uint32_t E, int kUnits, typename LoadQ>
-__device__ __forceinline__ void copy_tiles(const AttnDecodeArgs &a, const AttnWalk &w, const Maps &maps, uint32_t entries, uint32_t full,
+__device__ __forceinline__ void copy_tiles(const AttnDecodeArgs &a, const AttnWalk &w, const Maps &maps, uint32_t kv, uint32_t entries, uint32_t full,
                                            uint32_t empty, uint32_t ufull, uint32_t uempty, int *pieces_of, Unit *units, uint32_t q_bytes,
                                            LoadQ load_q) {
     const int lane = threadIdx.x & 31;
@@ -55,7 +56,8 @@ __device__ __forceinline__ void copy_tiles(const AttnDecodeArgs &a, const AttnWa
     const int piece = min(a.d.page, kTile), shift = min(a.d.page_shift, 6), boxes = (kTile >> shift) * NB;
     const int my_piece = lane / NB, my_col = lane % NB;
     const uint32_t box_bytes = piece * 128u, at = my_col * (kTile * 128u) + my_piece * box_bytes;
-    uint32_t e = 0, phase = 0, issued = 0;
+    const CUtensorMap *map = kv ? &maps.v : &maps.k;
+    uint32_t e = kv, phase = 0, issued = 0;
     int seq = 0, u = 0;
     bool alive = true;
     // the page of this lane's piece of tile t of a sequence; -1: not there
@@ -76,16 +78,18 @@ __device__ __forceinline__ void copy_tiles(const AttnDecodeArgs &a, const AttnWa
         left -= count + a.lead;
         more = unit_end && left > 0;                        // (what remains has tiles of the next unit)
         const int slot = t0 == 0 && unit_end ? -1 : u == 0 ? 0 : 1;
-        const uint32_t us = u % kUnits, uphase = (u / kUnits) & 1;
-        if (u >= kUnits) alive = tc::mbar_wait(uempty + 8 * us, uphase ^ 1, a.wait_ns);
-        alive = __all_sync(0xffffffffu, alive);
-        if (!alive) break;
-        if (lane == 0) {
-            units[us] = Unit{n, h, s.len, s.first, (s.tile0 + t0) * kTile, count, seq, slot, more};
-            tc::mbar_arrive_expect_tx(ufull + 8 * us, q_bytes);
+        if (kv == 0) {
+            const uint32_t us = u % kUnits, uphase = (u / kUnits) & 1;
+            if (u >= kUnits) alive = tc::mbar_wait(uempty + 8 * us, uphase ^ 1, a.wait_ns);
+            alive = __all_sync(0xffffffffu, alive);
+            if (!alive) break;
+            if (lane == 0) {
+                units[us] = Unit{n, h, s.len, s.first, (s.tile0 + t0) * kTile, count, seq, slot, more};
+                tc::mbar_arrive_expect_tx(ufull + 8 * us, q_bytes);
+            }
+            __syncwarp();
+            load_q(us, n, h, ufull + 8 * us);
         }
-        __syncwarp();
-        load_q(us, n, h, ufull + 8 * us);
         // the unit behind this one, and where its first tile lies: known before this one's last tile is asked for
         AttnSeq next_s = s;
         int next_n = n, next_h = h + 1, next_page = -1;
@@ -96,26 +100,24 @@ __device__ __forceinline__ void copy_tiles(const AttnDecodeArgs &a, const AttnWa
             const uint32_t bytes = __popc(there) * box_bytes;
             // the row of the pools where this lane's piece begins
             const int y = (here * a.d.hkv + h) * a.d.page + ((i0 + (my_piece << shift)) & (a.d.page - 1));
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {
-                if (issued >= E) alive = tc::mbar_wait(empty + 8 * e, phase ^ 1, a.wait_ns);
-                alive = __all_sync(0xffffffffu, alive);
-                if (!alive) break;
-                if (lane == 0) {
-                    int bits = 0;
-                    for (int p = 0; p < 4; ++p) bits |= (there >> ((p * 16) >> shift) * NB & 1u) << p;
-                    pieces_of[e] = bits;
-                    if (bytes) tc::mbar_arrive_expect_tx(full + 8 * e, bytes);
-                    else tc::mbar_arrive(full + 8 * e);
-                }
-                __syncwarp();
-                const bool drop = (a.lose & LOSE_ATTN_TILE_COPY) && issued == 0 && lane == 0;
-                if (here >= 0 && !drop) tc::tma_load_2d(entries + e * (kTile * D * 2) + at, kv ? &maps.v : &maps.k, my_col * 64, y, full + 8 * e);
-                ++issued;
-                if (++e == E) {
-                    e = 0;
-                    phase ^= 1;
-                }
+            if (issued >= E / 2) alive = tc::mbar_wait(empty + 8 * e, phase ^ 1, a.wait_ns);
+            alive = __all_sync(0xffffffffu, alive);
+            if (!alive) break;
+            if (lane == 0) {
+                int bits = 0;
+                for (int p = 0; p < 4; ++p) bits |= (there >> ((p * 16) >> shift) * NB & 1u) << p;
+                pieces_of[e] = bits;
+                if (bytes) tc::mbar_arrive_expect_tx(full + 8 * e, bytes);
+                else tc::mbar_arrive(full + 8 * e);
+            }
+            __syncwarp();
+            const bool drop = (a.lose & LOSE_ATTN_TILE_COPY) && kv == 0 && issued == 0 && lane == 0;
+            if (here >= 0 && !drop) tc::tma_load_2d(entries + e * (kTile * D * 2) + at, map, my_col * 64, y, full + 8 * e);
+            ++issued;
+            e += 2;
+            if (e >= E) {
+                e = kv;
+                phase ^= 1;
             }
             if (j == 0 && more) {
                 if (next_h == a.d.hkv) {
@@ -126,7 +128,7 @@ __device__ __forceinline__ void copy_tiles(const AttnDecodeArgs &a, const AttnWa
             }
         }
         seq += count;
-        if (!more && lane == 0) {
+        if (!more && kv == 0 && lane == 0) {
             // the CTA that holds a unit's front joins it: the CTAs behind that hold the rest
             int parts = 0;
             if (!unit_end && t0 == 0) parts = 1 + (int)((s.tiles - count + w.per - 1) / w.per);
@@ -141,14 +143,14 @@ __device__ __forceinline__ void copy_tiles(const AttnDecodeArgs &a, const AttnWa
     if (lane == 0) {
         if (!alive) {             // nothing more is copied
             set_error(a.err, GDN_DEVERR_TIMEOUT);
-            a.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
+            if (kv == 0) a.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
         }
         // what is under way arrives before the block ends
-        for (uint32_t k = 0; k < min(issued, E); ++k) {
+        for (uint32_t k = 0; k < min(issued, E / 2); ++k) {
             const uint32_t last = issued - 1 - k;
-            tc::mbar_wait(full + 8 * (last % E), (last / E) & 1, a.wait_ns);
+            tc::mbar_wait(full + 8 * (last % (E / 2) * 2 + kv), (last / (E / 2)) & 1, a.wait_ns);
         }
-        for (int k = 0; k < min(u, kUnits); ++k) {
+        for (int k = 0; kv == 0 && k < min(u, kUnits); ++k) {
             const int last = u - 1 - k;
             tc::mbar_wait(ufull + 8 * (last % kUnits), (last / kUnits) & 1, a.wait_ns);
         }
