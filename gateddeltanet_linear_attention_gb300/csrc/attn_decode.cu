@@ -16,7 +16,8 @@ constexpr int kSimtThreads = 256;
 constexpr int kSimtTile = 32;
 
 // The 32-bit form, on the CUDA cores: RPW query rows a warp, a tile of 32 tokens in shared memory, a token a lane for the
-// scores and D / 32 columns a lane for the sums.
+// scores and D / 32 columns a lane for the sums.  Bound by its multiply-adds and by loads that wait for no other tile; for checks
+// of a model rather than serving: 7 sequences of up to 2,047 tokens, 2 new ones, window 500: 9.1 us, most of it latency.
 template <int D, int RPW>
 __global__ void __launch_bounds__(kSimtThreads) attn_decode_simt_kernel(const AttnDecodeArgs a) {
     constexpr int TILE = kSimtTile, LDK = D + 4, CPL = D / 32, WARPS = kSimtThreads / 32, RB = WARPS * RPW;
@@ -276,9 +277,10 @@ cudaError_t launch_attn_join(const AttnDecodeArgs &a, bool act_bf16, cudaStream_
 }
 
 // bf16: where 16 query rows hold all of a key head's, their products keep up with the memory (64 sequences of up to 16,384
-// tokens, 4 rows: 378 us against 424 us in the kernel of many rows; 32 of up to 8,192, 16 rows: 57 against 71).  Above, tcgen05
-// products of 128 rows take what 16 rows would read again: 32 rows in two blocks that share tiles took 451 us against 427 in
-// the first batch (in small calls less, 11 us against 13 for one sequence of 700 tokens; not worth a kernel of its own).
+// tokens, 4 rows: 339 us against 357 us in the kernel of many rows; 32 of up to 8,192, 16 rows: 53 against 67; one of 700, 8 rows:
+// 8 against 12).  Above, tcgen05 products of 128 rows take what 16 rows would read again: with 32 rows in two groups that share
+// tiles this kernel was slower in large batches (451 us against 427 in the first one, both then) and faster in small calls (11
+// against 13 for one sequence of 700 tokens; not worth a kernel of its own).
 cudaError_t launch_attn_decode(const AttnDecodeArgs &a, bool act_bf16, cudaStream_t s) {
     if (!act_bf16) return a.d.D == 64 ? run_rows<64>(a, s) : a.d.D == 128 ? run_rows<128>(a, s) : run_rows<256>(a, s);
     return a.d.grp * a.tokens <= 16 ? launch_attn_decode_tc(a, s) : launch_attn_decode_rows(a, s);

@@ -7,13 +7,15 @@
 //   P = exp(S - m) a thread a row: maximum and sum need no other lane; P, in two bf16 parts, in the place of S
 //   O += P V      P from TMEM, V from shared memory as TMA left it
 // Two groups of four warps (one at 256 columns) take turns with the tiles, each with its own S, O, m and l; O of both lies in
-// the same lanes, so the first group adds the second one's to its own where a unit ends.
+// the same lanes, so where a unit ends each group adds both, in half of the columns.
 //
 // m is the maximum of a row's first tile and is raised only where a score passes it by 8 powers of two: P stays below 256,
 // which changes no rounding, and O is seldom scaled again.
 //
-// Each group has S twice, so that the next tile's scores are there when its warps are done with one: a tile costs them about
-// 1,500 cycles (64 exponentials a thread), two groups one in 750, against 1,400 that its bytes take at 128 columns.  HBM-bound.
+// Each group has S twice, so that the next tile's scores are there when its warps are done with one.  With 32 sequences of up to
+// 8,192 tokens, 8 new ones each, 4 key heads of 128 columns, 8 query heads each (278 MB): 58 us with the join kernel, 0.71 of the
+// copy rate.  A tile takes a group's warps 2,300 to 2,600 cycles (745 of them 64 exponentials a thread), two groups one in 1,200
+// to 1,300; its bytes take 1,400.  The rest is the first tile's way (5 us of 58), units' ends and the join.
 #include "attn_tc.cuh"
 
 namespace gdn {
@@ -22,7 +24,10 @@ namespace {
 
 using namespace attn_tc;
 
-constexpr int kLead = 2;                           // tiles that a unit's end costs
+// Tiles that a unit's end and the next one's start cost: sums whole 1,100 cycles, the groups' meeting 2,000 to 2,600, outputs
+// 2,300 to 3,000, first scores 1,000.  With 0, 2, 4 and 6: 70, 63, 59 and 58 us for the 32 sequences below, and 133, 124 and 116
+// (2, 4, 6) for 64 sequences of up to 4,096 tokens, 8 key heads, 4 query heads each.
+constexpr int kLead = 6;
 constexpr float kSlack = 8.f;                      // powers of two that a score may pass m by
 
 // NG groups; room for RB query rows (products read 128: behind them whatever follows, into lanes that nobody reads).

@@ -10,7 +10,12 @@
 // HBM-bound: q, k and v are read once and written once.  D / 8 lanes own a head vector and keep it in registers.  A
 // warp takes a few tokens at a time: what they are and their angles come first, a lane a token, then a lane an angle;
 // then it goes through their heads in batches, the loads of the next batch (of the next kind of heads, of the next token)
-// under way.  No warp waits for another.
+// under way.  No warp waits for another.  Tokens that share a block's angles instead took 70 us where this takes 40.
+//
+// Measured in bf16: 9,600 prompt tokens into the cache (16 + 2 + 2 heads of 256, 64 columns rotated) 40 us, 0.73 of the copy
+// rate; the backward of 8,192 tokens (32 + 8 heads of 128) 56 us, 0.66; 64 tokens of a decode step 6 us.  Issue is half busy;
+// what is missing are loads in flight, 2 KB a warp and 32 KB an SM (3 blocks an SM: spills, 47 us; batches of 6 or 8 heads: no
+// gain).
 #include <type_traits>
 
 #include "attn_common.cuh"
