@@ -13,9 +13,9 @@
 // which changes no rounding, and O is seldom scaled again.
 //
 // Each group has S twice, so that the next tile's scores are there when its warps are done with one.  With 32 sequences of up to
-// 8,192 tokens, 8 new ones each, 4 key heads of 128 columns, 8 query heads each (278 MB): 58 us with the join kernel, 0.71 of the
-// copy rate.  A tile takes a group's warps 2,300 to 2,600 cycles (745 of them 64 exponentials a thread), two groups one in 1,200
-// to 1,300; its bytes take 1,400.  The rest is the first tile's way (5 us of 58), units' ends and the join.
+// 8,192 tokens, 8 new ones each, 4 key heads of 128 columns, 8 query heads each (278 MB): 57 us with the join kernel, 0.72 of the
+// copy rate.  A tile takes a group's warps 1,500 cycles (745 of them 64 exponentials a thread), and both groups wait for tiles: one
+// comes in 1,500 to 1,600 cycles, its bytes take 1,400.  The rest is the first tile's way (5 us of 57), units' ends and the join.
 #include "attn_tc.cuh"
 
 namespace gdn {
@@ -37,12 +37,13 @@ template <int D, int NG, int RB> struct Shape {
     static constexpr int entry = kTile * D * 2, q_block = RB * D * 2;
     static constexpr int fixed = units * q_block + NG * (128 * 8 + D * 4) + 1024;
     static constexpr int limit = 227 * 1024 - 1024;
-    static constexpr int fit = (limit - fixed) / entry, turn = 2 * NG;
-    // a multiple of the groups' entries: an entry then serves tiles of one group alone
-    static constexpr int entries = fit < kMaxEntries ? fit / turn * turn : kMaxEntries;
+    static constexpr int fit = (limit - fixed) / entry, most = fit < kMaxEntries ? fit : kMaxEntries, each = most / NG;
+    // Multiples of the groups: an entry then serves tiles of one group alone.  (V's are held longer, but a third for K and two
+    // for V left the scores waiting: 67 us against 57.)
+    static constexpr int k_entries = NG * (each / 2), entries = NG * each, v_entries = entries - k_entries;
     static constexpr int bytes = fixed + entries * entry;
     static constexpr uint32_t col_o = 128 * NG;    // TMEM: S and P of group g's even and odd tiles at 128 g and 64 on, its O at col_o + g D
-    static_assert(entries >= turn && entries % turn == 0, "a tile of each group in flight, in entries of its own");
+    static_assert(k_entries >= NG && v_entries >= NG, "a tile of each group in flight, in entries of its own");
     static_assert(128 * NG + NG * D <= 512, "tensor memory");
     static_assert(q_block + entries * entry >= 128 * 128 * (D / 64), "products read 128 rows of the last block");
 };
@@ -99,7 +100,7 @@ template <int D, int NG, int RB>
 __global__ void __launch_bounds__((Shape<D, NG, RB>::threads), 1) attn_decode_rows_kernel(const AttnDecodeArgs a, const __grid_constant__ Maps maps) {
     using S = Shape<D, NG, RB>;
     constexpr int KS = D / 16, kUnits = S::units, kThreads = S::threads;
-    constexpr uint32_t E = S::entries, kBlock = kTile * 128, kQBlock = RB * 128;
+    constexpr uint32_t E = S::entries, KE = S::k_entries, VE = S::v_entries, kBlock = kTile * 128, kQBlock = RB * 128;
     extern __shared__ unsigned char raw[];
     __shared__ long long sums[33];
     __shared__ int found[3], spoiled[NG];
@@ -166,7 +167,9 @@ __global__ void __launch_bounds__((Shape<D, NG, RB>::threads), 1) attn_decode_ro
 
     if (warp == 4 * NG || warp == 5 * NG + 1) {
         // ------------------------------------------------------------ copies
-        copy_tiles<D, E, kUnits>(a, w, maps, warp == 4 * NG ? 0 : 1, entries, full, empty, ufull, uempty, pieces_of, units, (uint32_t)rows * D * 2,
+        const uint32_t kv = warp == 4 * NG ? 0 : 1, at = kv * KE;
+        copy_tiles<D, kUnits>(a, w, maps, kv, kv ? VE : KE, entries + at * S::entry, full + 8 * at, empty + 8 * at, ufull, uempty, pieces_of + at,
+                              units, (uint32_t)rows * D * 2,
                                  [&](uint32_t us, int n, int h, uint32_t bar) {
             if (lane < D / 64)
                 asm volatile(
@@ -180,7 +183,7 @@ __global__ void __launch_bounds__((Shape<D, NG, RB>::threads), 1) attn_decode_ro
         const int g = warp - 4 * NG - 1;
         const uint32_t lead = elect_lane(), t_s = tmem + g * 128, t_o = tmem + S::col_o + g * D;
         // Scores of tile `ks` of the group, one ahead at most of the sums of tile `kp`: whatever can go first goes.
-        uint32_t se = 2 * g, sphase = 0, ks = 0, pe = 2 * g, pphase = 0, kp = 0, fresh = 0;      // fresh: tiles that begin a unit's sums
+        uint32_t se = g, sphase = 0, ks = 0, pe = KE + g, pphase = 0, kp = 0, fresh = 0;      // fresh: tiles that begin a unit's sums
         int u = 0, j = 0, count = 0, opened = 0;            // the unit that the scores are in; whether its queries are there
         bool ok = true, first = true, more = true;
         uint64_t q_desc = 0, t0 = 0;
@@ -209,9 +212,9 @@ __global__ void __launch_bounds__((Shape<D, NG, RB>::threads), 1) attn_decode_ro
                 first = false;
                 ++ks;
                 j += NG;
-                se += 2 * NG;
-                if (se >= E) {
-                    se -= E;
+                se += NG;
+                if (se >= KE) {
+                    se -= KE;
                     sphase ^= 1;
                 }
                 moved = true;
@@ -221,19 +224,19 @@ __global__ void __launch_bounds__((Shape<D, NG, RB>::threads), 1) attn_decode_ro
                 ++u;
                 opened = 0;
             }
-            if (kp < ks && there(full + 8 * (pe + 1), pphase) && there(p_ready + 16 * g + 8 * (kp & 1), (kp >> 1) & 1)) {
+            if (kp < ks && there(full + 8 * pe, pphase) && there(p_ready + 16 * g + 8 * (kp & 1), (kp >> 1) & 1)) {
                 tc::fence_after_sync();
-                const uint64_t v_desc = desc_mn(entries + (pe + 1) * S::entry, kBlock);
+                const uint64_t v_desc = desc_mn(entries + pe * S::entry, kBlock);
                 const uint32_t t_p = t_s + (kp & 1) * 64;
 #pragma unroll
                 for (int c = 0; c < 2 * kTile / 16; ++c)    // the leading parts of P, then the rest
                     mma_ts(lead, t_o, t_p + c * 8, v_desc + step_mn(c & (kTile / 16 - 1)), id_pv, c > 0 || !(fresh >> (kp & 1) & 1));
                 commit(lead, pv_done + 16 * g + 8 * (kp & 1));
-                commit(lead, empty + 8 * (pe + 1));
+                commit(lead, empty + 8 * pe);
                 ++kp;
-                pe += 2 * NG;
+                pe += NG;
                 if (pe >= E) {
-                    pe -= E;
+                    pe -= VE;
                     pphase ^= 1;
                 }
                 moved = true;
@@ -257,7 +260,7 @@ __global__ void __launch_bounds__((Shape<D, NG, RB>::threads), 1) attn_decode_ro
         const int token = min(row / a.d.grp, a.tokens - 1);
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16, t_s0 = tmem + lanes + g * 128, t_o0 = tmem + lanes + S::col_o, t_o = t_o0 + g * D;
         unsigned *my_spoil = spoil + g * D;
-        uint32_t e = 2 * g, phase = 0, k = 0;
+        uint32_t e = KE + g, phase = 0, k = 0;             // V's entry of the group's next tile
         bool ok = true;
         auto wait = [&](uint32_t b, uint32_t parity) { ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(b, parity, a.wait_ns)); };
         int u = 0;
@@ -296,9 +299,9 @@ __global__ void __launch_bounds__((Shape<D, NG, RB>::threads), 1) attn_decode_ro
                 const uint32_t t_s = t_s0 + (k & 1) * 64;
                 wait(s_full + 16 * g + 8 * (k & 1), (k >> 1) & 1);
                 // V's entry stays this tile's until its product is done; K's may be another tile's by now
-                wait(full + 8 * (e + 1), phase);
+                wait(full + 8 * e, phase);
                 tc::fence_after_sync();
-                const int pieces = pieces_of[e + 1];
+                const int pieces = pieces_of[e];
                 const bool masked = pieces != 15 || i0 + kTile > open || i0 < wide;
                 float v[64];
                 tc::tmem_ld64(t_s, v);
@@ -360,7 +363,7 @@ __global__ void __launch_bounds__((Shape<D, NG, RB>::threads), 1) attn_decode_ro
                     // Places that no row sees may hold anything: they become zeros.  A value that is not finite in a place that
                     // only some new tokens see becomes zero too, and the sums of its column for those tokens are NaN, as sums
                     // with it are not finite.
-                    const uint32_t tile = entries + (e + 1) * S::entry;
+                    const uint32_t tile = entries + e * S::entry;
                     for (int c = quarter * 32 + lane; c < kTile * (D / 8); c += active * 32) {
                         const int t = c / (D / 8), chunk = c % (D / 8), i = i0 + t;
                         const uint32_t at = tile + (chunk >> 3) * kBlock + t * 128 + (((chunk & 7) ^ (t & 7)) << 4);
@@ -394,9 +397,9 @@ __global__ void __launch_bounds__((Shape<D, NG, RB>::threads), 1) attn_decode_ro
                 __syncwarp();
                 if (ok && lane == 0) tc::mbar_arrive(p_ready + 16 * g + 8 * (k & 1));
                 ++k;
-                e += 2 * NG;
+                e += NG;
                 if (e >= E) {
-                    e -= E;
+                    e -= VE;
                     phase ^= 1;
                 }
             }

@@ -59,7 +59,7 @@ enum { kBarSet = 1 };                // the first set's named barrier
 template <int D> __global__ void __launch_bounds__(kThreads, 1) attn_decode_tc_kernel(const AttnDecodeArgs a, const __grid_constant__ Maps maps) {
     using S = Shape<D>;
     constexpr int KS = D / 16, NT = D / 32;                         // NT: 8-column blocks of a warp's share of O
-    constexpr uint32_t E = S::entries;
+    constexpr uint32_t E = S::entries, R = E / 2;                   // entries of K, then as many of V
     extern __shared__ unsigned char raw[];
     __shared__ long long sums[33];
     __shared__ int found[3];
@@ -105,7 +105,8 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) attn_decode_tc_k
 
     if (warp >= kConsumers / 32) {
         // ------------------------------------------------------------ copies
-        copy_tiles<D, E, kUnits>(a, w, maps, warp - kConsumers / 32, entries, full, empty, ufull, uempty, pieces_of, units, (uint32_t)rows * D * 2,
+        const uint32_t kv = warp - kConsumers / 32, at = kv * R;
+        copy_tiles<D, kUnits>(a, w, maps, kv, R, entries + at * S::entry, full + 8 * at, empty + 8 * at, ufull, uempty, pieces_of + at, units, (uint32_t)rows * D * 2,
                                  [&](uint32_t us, int n, int h, uint32_t bar) {
             if (lane < rows) {
                 const int tok = lane / a.d.grp, g = lane - tok * a.d.grp;
@@ -127,7 +128,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) attn_decode_tc_k
     const uint32_t q_lane = (lane & 15) * S::q_pitch + (lane >> 4) * 16, p_lane = (lane & 15) * kPPitch + (lane >> 4) * 16;
     const uint32_t k_token = wg * 16 + (lane & 7) + ((lane >> 4) << 3), k_half = (lane >> 3) & 1;
     const uint32_t v_token = (lane & 7) + (((lane >> 3) & 1) << 3), v_half = lane >> 4;
-    uint32_t e = 2 * set, phase = 0;                    // the entry of the set's next tile
+    uint32_t e = set, phase = 0;                        // K's entry of the set's next tile
     bool ok = true;
     int u = 0;
     for (bool more = true; more; ++u) {
@@ -149,7 +150,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) attn_decode_tc_k
         const int open = unit.len - a.tokens + 1, wide = a.window > 0 ? unit.len - a.window : 0;
         for (int j = (set - unit.seq0) & (kSets - 1); j < unit.count; j += kSets) {
             const int i0 = unit.i0 + j * kTile;
-            const uint32_t v_e = e + 1;                 // V follows its K
+            const uint32_t v_e = R + e;
             if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(full + 8 * e, phase, a.wait_ns));
             const int pieces = pieces_of[e];
             const bool masked = pieces != 15 || i0 + kTile > open || i0 < wide;
@@ -284,9 +285,9 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) attn_decode_tc_k
             }
             __syncwarp();
             if (ok && lane == 0) tc::mbar_arrive(empty + 8 * v_e);
-            e += 2 * kSets;
-            if (e >= E) {
-                e -= E;
+            e += kSets;
+            if (e >= R) {
+                e -= R;
                 phase ^= 1;
             }
         }

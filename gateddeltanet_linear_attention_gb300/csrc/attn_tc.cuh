@@ -42,13 +42,13 @@ __device__ __forceinline__ bool bar_all(int id, int threads, bool mine) {
     return all != 0;
 }
 
-// The two copying warps: the CTA's tiles into a ring of E entries, K's and V's of a tile one after the other, each as D / 64
-// blocks of 64 tokens by 128 bytes in the 128-byte swizzle.  One warp (kv 0) copies K, one V: V's entries are needed longer,
-// and K's that are free would wait behind them.  The first also writes the units into `units` and fetches their query rows
-// (q_bytes of them) by load_q(slot, sequence, key head, barrier).  The barriers: full[E], empty[E]; ufull, uempty [kUnits].
-// pieces_of: which 16-token pieces of an entry's tile are there (what is not there is not copied: the entry holds what it held).
-template <int D, uint32_t E, int kUnits, typename LoadQ>
-__device__ __forceinline__ void copy_tiles(const AttnDecodeArgs &a, const AttnWalk &w, const Maps &maps, uint32_t kv, uint32_t entries, uint32_t full,
+// The two copying warps: K (kv 0) and V of the CTA's tiles into a ring of `ring` entries each, as D / 64 blocks of 64 tokens by
+// 128 bytes in the 128-byte swizzle.  A warp each: V's entries are needed longer, and K's that are free would wait behind them.
+// The first also writes the units into `units` and fetches their query rows (q_bytes of them) by load_q(slot, sequence, key
+// head, barrier).  Of the ring: entries, full, empty (barriers), pieces_of (which 16-token pieces of an entry's tile are there;
+// what is not there is not copied: the entry holds what it held).  Of the units: ufull, uempty [kUnits].
+template <int D, int kUnits, typename LoadQ>
+__device__ __forceinline__ void copy_tiles(const AttnDecodeArgs &a, const AttnWalk &w, const Maps &maps, uint32_t kv, uint32_t ring, uint32_t entries, uint32_t full,
                                            uint32_t empty, uint32_t ufull, uint32_t uempty, int *pieces_of, Unit *units, uint32_t q_bytes,
                                            LoadQ load_q) {
     const int lane = threadIdx.x & 31;
@@ -57,7 +57,7 @@ __device__ __forceinline__ void copy_tiles(const AttnDecodeArgs &a, const AttnWa
     const int my_piece = lane / NB, my_col = lane % NB;
     const uint32_t box_bytes = piece * 128u, at = my_col * (kTile * 128u) + my_piece * box_bytes;
     const CUtensorMap *map = kv ? &maps.v : &maps.k;
-    uint32_t e = kv, phase = 0, issued = 0;
+    uint32_t e = 0, phase = 0, issued = 0;
     int seq = 0, u = 0;
     bool alive = true;
     // the page of this lane's piece of tile t of a sequence; -1: not there
@@ -100,7 +100,7 @@ __device__ __forceinline__ void copy_tiles(const AttnDecodeArgs &a, const AttnWa
             const uint32_t bytes = __popc(there) * box_bytes;
             // the row of the pools where this lane's piece begins
             const int y = (here * a.d.hkv + h) * a.d.page + ((i0 + (my_piece << shift)) & (a.d.page - 1));
-            if (issued >= E / 2) alive = tc::mbar_wait(empty + 8 * e, phase ^ 1, a.wait_ns);
+            if (issued >= ring) alive = tc::mbar_wait(empty + 8 * e, phase ^ 1, a.wait_ns);
             alive = __all_sync(0xffffffffu, alive);
             if (!alive) break;
             if (lane == 0) {
@@ -114,9 +114,8 @@ __device__ __forceinline__ void copy_tiles(const AttnDecodeArgs &a, const AttnWa
             const bool drop = (a.lose & LOSE_ATTN_TILE_COPY) && kv == 0 && issued == 0 && lane == 0;
             if (here >= 0 && !drop) tc::tma_load_2d(entries + e * (kTile * D * 2) + at, map, my_col * 64, y, full + 8 * e);
             ++issued;
-            e += 2;
-            if (e >= E) {
-                e = kv;
+            if (++e == ring) {
+                e = 0;
                 phase ^= 1;
             }
             if (j == 0 && more) {
@@ -146,9 +145,9 @@ __device__ __forceinline__ void copy_tiles(const AttnDecodeArgs &a, const AttnWa
             if (kv == 0) a.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
         }
         // what is under way arrives before the block ends
-        for (uint32_t k = 0; k < min(issued, E / 2); ++k) {
+        for (uint32_t k = 0; k < min(issued, ring); ++k) {
             const uint32_t last = issued - 1 - k;
-            tc::mbar_wait(full + 8 * (last % (E / 2) * 2 + kv), (last / (E / 2)) & 1, a.wait_ns);
+            tc::mbar_wait(full + 8 * (last % ring), (last / ring) & 1, a.wait_ns);
         }
         for (int k = 0; kv == 0 && k < min(u, kUnits); ++k) {
             const int last = u - 1 - k;
