@@ -183,50 +183,116 @@ __global__ void __launch_bounds__(kSimtThreads) attn_decode_simt_kernel(const At
 }
 
 // Adds up the parts of the units that several CTAs hold: part p of the unit whose front is CTA c's lies in CTA c + p.  Blocks
-// (c, y) take query rows: one at a time, groups of D / 4 threads taking parts in turn, or, where rows are many and parts few,
-// a row a group.
-constexpr int kJoinThreads = 256, kJoinRows = 16;
-struct Joined {
-    float m, l;
-    float4 o;
-    __device__ __forceinline__ void add(float pm, float pl, const float4 &po) {
-        const float nm = fmaxf(m, pm), ref = nm == -INFINITY ? 0.f : nm;
-        const float fa = exp2_fast(m - ref), fb = exp2_fast(pm - ref);
-        l = l * fa + pl * fb;
-        o = make_float4(o.x * fa + po.x * fb, o.y * fa + po.y * fb, o.z * fa + po.z * fb, o.w * fa + po.w * fb);
-        m = nm;
-    }
-};
-template <typename T, int D> __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnDecodeArgs a) {
-    constexpr int COLS = D / 4, GROUPS = kJoinThreads / COLS;
+// (c, y) take query rows.  What a part counts, 2^(m_p - max m), is known from the statistics, so the sums' loads wait for
+// nothing and four are under way (two, three, eight: slower, by loads that wait or registers): a row a group of D / 4 threads,
+// or, of more than 16 parts, a row by all groups.  Against groups that carry m and l from part to part: 76 parts of 8 rows, 256
+// columns, 52 -> 49 us a call; 64 rows, one sequence of 700 tokens 16.3 -> 12.6; 3 rows, 700 tokens 8.1 -> 8.7, where a row by
+// all groups would be as fast, and slower (10.3 against 9.5) with 6 rows of 64 columns.  Fixed orders throughout.
+constexpr int kJoinThreads = 256, kJoinRows = 16, kJoinAhead = 4;
+__device__ __forceinline__ void add_part(float4 &x, const float4 &o, float f) {
+    x = make_float4(fmaf(o.x, f, x.x), fmaf(o.y, f, x.y), fmaf(o.z, f, x.z), fmaf(o.w, f, x.w));
+}
+template <typename T, int D> __global__ void __launch_bounds__(kJoinThreads, 5) attn_join_kernel(const AttnDecodeArgs a) {
+    constexpr int COLS = D / 4, GROUPS = kJoinThreads / COLS, WARPS = kJoinThreads / 32, AHEAD = kJoinAhead;
+    static_assert(kAttnMaxCtas <= 2 * kJoinThreads, "two parts a thread");
     __shared__ float4 acc[GROUPS][COLS];
-    __shared__ float2 stats[GROUPS];
-    const int tid = threadIdx.x, group = tid / COLS, col = tid % COLS, rows = a.d.grp * a.tokens;
+    __shared__ float factor[kAttnMaxCtas], tops[WARPS], totals[WARPS];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = tid / COLS, col = tid % COLS, rows = a.d.grp * a.tokens;
     let_next_start();
     await_previous();
     const int4 j = a.joins[blockIdx.x];
     if (j.w < 2) return;
-    const bool shared = rows <= kJoinRows || j.w > 4;       // a row by all groups
-    const int sharing = shared ? GROUPS : 1;
-    for (int row = shared ? blockIdx.y : blockIdx.y * GROUPS + group; row < rows; row += gridDim.y * (shared ? 1 : GROUPS)) {
-        Joined x{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-        for (int p = shared ? group : 0; p < j.w; p += sharing) {      // (four at a time were slower: 52.6 -> 56.8 us a call of 76 parts)
-            const float *part = attn_part(a, blockIdx.x + p, p == 0 ? j.z : 0);
-            const float2 ml = *reinterpret_cast<const float2 *>(part + rows * D + 2 * row);
-            x.add(ml.x, ml.y, *reinterpret_cast<const float4 *>(part + row * D + col * 4));
-        }
-        if (shared) {
-            __syncthreads();                                // the row before has been read
-            acc[group][col] = x.o;
-            if (col == 0) stats[group] = make_float2(x.m, x.l);
-            __syncthreads();
-            if (group != 0) continue;
-            for (int g = 1; g < GROUPS; ++g) x.add(stats[g].x, stats[g].y, acc[g][col]);
-        }
+    const int parts = min(j.w, a.ctas - (int)blockIdx.x);
+    auto part = [&](int p) { return attn_part(a, blockIdx.x + p, p == 0 ? j.z : 0); };
+    auto write = [&](int row, float4 x, float m, float l) {
         const long long orow = ((long long)j.x * a.tokens + row / a.d.grp) * a.d.hq + j.y * a.d.grp + row % a.d.grp;
-        const float inv = x.l == 0.f ? 0.f : 1.f / x.l;
-        store4f((T *)a.out + orow * D + col * 4, make_float4(x.o.x * inv, x.o.y * inv, x.o.z * inv, x.o.w * inv));
-        if (col == 0 && a.lse) a.lse[orow] = x.l == 0.f ? -INFINITY : (x.m + log2f(x.l)) * kLn2;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        store4f((T *)a.out + orow * D + col * 4, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
+        if (col == 0 && a.lse) a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    };
+    if (parts <= 16) {
+        // a row a group: 16 lanes have the statistics, a part each
+        const unsigned mask = 0xffffu << (lane & 16);
+        for (int row = blockIdx.y * GROUPS + group; row < rows; row += gridDim.y * GROUPS) {
+            float2 ml = make_float2(-INFINITY, 0.f);
+            if ((lane & 15) < parts) ml = *reinterpret_cast<const float2 *>(part(lane & 15) + rows * D + 2 * row);
+            float4 o[AHEAD], x = make_float4(0.f, 0.f, 0.f, 0.f);
+            auto load = [&](int p0) {
+#pragma unroll
+                for (int k = 0; k < AHEAD; ++k)
+                    if (p0 + k < parts) o[k] = *reinterpret_cast<const float4 *>(part(p0 + k) + row * D + col * 4);
+            };
+            load(0);
+            float m = ml.x;
+#pragma unroll
+            for (int k = 8; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(mask, m, k));
+            const float f = exp2_fast(ml.x - (m == -INFINITY ? 0.f : m));
+            float l = ml.y * f;
+#pragma unroll
+            for (int k = 8; k > 0; k >>= 1) l += __shfl_xor_sync(mask, l, k);
+            for (int p0 = 0; p0 < parts; p0 += AHEAD) {
+                if (p0 > 0) load(p0);
+#pragma unroll
+                for (int k = 0; k < AHEAD; ++k) {
+                    const float g = __shfl_sync(mask, f, (p0 + k) & 15, 16);
+                    if (p0 + k < parts) add_part(x, o[k], g);
+                }
+            }
+            write(row, x, m, l);
+        }
+        return;
+    }
+    for (int row = blockIdx.y; row < rows; row += gridDim.y) {
+        float2 ml[2];
+        float4 o[AHEAD];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int p = tid + k * kJoinThreads;
+            ml[k] = p < parts ? *reinterpret_cast<const float2 *>(part(p) + rows * D + 2 * row) : make_float2(-INFINITY, 0.f);
+        }
+        auto load = [&](int p0) {
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k)
+                if (p0 + k * GROUPS < parts) o[k] = *reinterpret_cast<const float4 *>(part(p0 + k * GROUPS) + row * D + col * 4);
+        };
+        load(group);
+        float m = fmaxf(ml[0].x, ml[1].x);
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+        __syncthreads();                                    // the row before has been read
+        if (lane == 0) tops[warp] = m;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < WARPS; ++k) m = fmaxf(m, tops[k]);
+        const float ref = m == -INFINITY ? 0.f : m;
+        float l = 0.f;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int p = tid + k * kJoinThreads;
+            const float f = exp2_fast(ml[k].x - ref);
+            if (p < parts) factor[p] = f;
+            l = fmaf(ml[k].y, f, l);
+        }
+        l = warp_sum(l);
+        if (lane == 0) totals[warp] = l;
+        __syncthreads();
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int p0 = group; p0 < parts; p0 += AHEAD * GROUPS) {
+            if (p0 > group) load(p0);
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k)
+                if (p0 + k * GROUPS < parts) add_part(x, o[k], factor[p0 + k * GROUPS]);
+        }
+        acc[group][col] = x;
+        __syncthreads();
+        if (group != 0) continue;
+        for (int k = 1; k < GROUPS; ++k) {
+            const float4 y = acc[k][col];
+            x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+        }
+        l = 0.f;
+        for (int k = 0; k < WARPS; ++k) l += totals[k];
+        write(row, x, m, l);
     }
 }
 
@@ -279,8 +345,8 @@ cudaError_t launch_attn_join(const AttnDecodeArgs &a, bool act_bf16, cudaStream_
 // bf16: where 16 query rows hold all of a key head's, their products keep up with the memory (64 sequences of up to 16,384
 // tokens, 4 rows: 339 us against 357 us in the kernel of many rows; 32 of up to 8,192, 16 rows: 53 against 67; one of 700, 8 rows:
 // 8 against 12).  Above, tcgen05 products of 128 rows take what 16 rows would read again: with 32 rows in two groups that share
-// tiles this kernel was slower in large batches (451 us against 427 in the first one, both then) and faster in small calls (11
-// against 13 for one sequence of 700 tokens; not worth a kernel of its own).
+// tiles this kernel was slower in large batches (451 us against 427 in the first one, both then) and hardly faster in small calls
+// (11 us against 13 for one sequence of 700 tokens).
 cudaError_t launch_attn_decode(const AttnDecodeArgs &a, bool act_bf16, cudaStream_t s) {
     if (!act_bf16) return a.d.D == 64 ? run_rows<64>(a, s) : a.d.D == 128 ? run_rows<128>(a, s) : run_rows<256>(a, s);
     return a.d.grp * a.tokens <= 16 ? launch_attn_decode_tc(a, s) : launch_attn_decode_rows(a, s);
