@@ -8,12 +8,12 @@
 //   O += P V     warp w the columns D/4 w .., P passed through shared memory
 // and their sums are added where a unit ends.  P is split in two bf16 parts, so that o loses nothing but its own rounding.
 //
-// HBM-bound: 64 sequences of up to 16,384 tokens, 8 key heads of 128 columns (2.3 GB) take 340 us, 0.99 of the copy rate; one of
-// 131,072 tokens, 2 key heads of 256 columns (268 MB) 49 us, 0.81: 5 us until the first tile is there, and shared memory holds two
-// tiles of 256 columns, so that none is under way for a set that computes.  One token over 700 takes 8 us, most of it latency.
-// 16 rows of m16n8k16 products need 16 operations a byte of the cache, at the 600 TFLOP/s that they reach on this GPU 0.2 of the
-// time that the bytes take.  (A tcgen05 product has 64 or 128 rows, and the sums over tokens of its transposed
-// form lie across lanes.)
+// HBM-bound: 64 sequences of up to 16,384 tokens, 8 key heads of 128 columns (2.3 GB) take 346 us, 0.98 of the copy rate; one of
+// 131,072 tokens, 2 key heads of 256 columns (268 MB) 49 us, 0.81: 2 us until lengths and shares are known, 3 until the first
+// tile is there, 3 for the join (a third tile of 256 columns in shared memory, with room for 8 query rows: no gain, 50.7).  One
+// token over 700 takes 8.7 us, all latency.  16 rows of m16n8k16 products need 16 operations a byte of the cache, at the 600
+// TFLOP/s that they reach on this GPU 0.2 of the time that the bytes take.  (A tcgen05 product has 64 or 128 rows, and the sums
+// over tokens of its transposed form lie across lanes.)
 #include "attn_tc.cuh"
 
 namespace gdn {
