@@ -9,13 +9,13 @@
 //
 // HBM-bound: q, k and v are read once and written once.  D / 8 lanes own a head vector and keep it in registers.  A
 // warp takes a few tokens at a time: what they are and their angles come first, a lane a token, then a lane an angle;
-// then it goes through their heads in batches, the loads of the next batch (of the next kind of heads, of the next token)
-// under way.  No warp waits for another.  Tokens that share a block's angles instead took 70 us where this takes 40.
+// then it goes through their heads in batches, the next batches (of the next kind of heads, of the next token) under way:
+// forward two, by asynchronous copies of each lane's pieces to shared memory, backward one, in registers.  No warp waits for
+// another.  Tokens that share a block's angles instead took 70 us where this takes 36.
 //
-// Measured in bf16: 9,600 prompt tokens into the cache (16 + 2 + 2 heads of 256, 64 columns rotated) 40 us, 0.73 of the copy
-// rate; the backward of 8,192 tokens (32 + 8 heads of 128) 56 us, 0.66; 64 tokens of a decode step 6 us.  Issue is half busy;
-// what is missing are loads in flight, 2 KB a warp and 32 KB an SM (3 blocks an SM: spills, 47 us; batches of 6 or 8 heads: no
-// gain).
+// Measured in bf16: 9,600 prompt tokens into the cache (16 + 2 + 2 heads of 256, 64 columns rotated) 36 us, 0.81 of the copy
+// rate (one batch ahead in registers 40; three ahead 37, four 38; three blocks an SM 47 and 53: spills); the backward of 8,192
+// tokens (32 + 8 heads of 128) 56 us, 0.66, issue used by 0.57; 64 tokens of a decode step 6 us.
 #include <type_traits>
 
 #include "attn_common.cuh"
@@ -304,14 +304,39 @@ struct Share {
         : mine(max(0, (heads - first - sub + by - 1) / by)), full(max(0, (heads - first - hpw + by) / by)), any(max(0, (heads - first + by - 1) / by)) {}
 };
 
+// What a lane has asked for lies in shared memory, a batch of UN heads a stage: each lane copies and reads its own pieces.
+template <typename T, int UN> struct Stage {
+    uint4 v[UN][sizeof(T) / 2][32];
+    __device__ __forceinline__ void ask(int j, int lane, const T *p, const T *q) {
+        if (sizeof(T) == 2) {
+            const uint32_t to = smem_addr(&v[j][0][lane]);
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" :: "r"(to), "l"(p) : "memory");
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" :: "r"(to + 8), "l"(q) : "memory");
+        } else {
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(smem_addr(&v[j][0][lane])), "l"(p) : "memory");
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(smem_addr(&v[j][sizeof(T) / 2 - 1][lane])), "l"(q) : "memory");
+        }
+    }
+    __device__ __forceinline__ Raw<T> get(int j, int lane) const {
+        Raw<T> r;
+        if constexpr (sizeof(T) == 2) r = *reinterpret_cast<const Raw<T> *>(&v[j][0][lane]);
+        else r.load(reinterpret_cast<const T *>(&v[j][0][lane]), reinterpret_cast<const T *>(&v[j][1][lane]));
+        return r;
+    }
+    static __device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+};
+
 // PLAIN: heads stand one after another in q, k and v, and a warp has all of a token's: the distances from one to the next
 // are constants of the code.  (Address arithmetic was half of the instructions, and the kernels issue half of the time.)
+constexpr int kStages = 3;           // one that is worked on, two under way
+template <typename T> constexpr int kBatch = sizeof(T) == 2 ? 4 : 2;
 template <typename T, int D, int MODE, bool PLAIN>
 __global__ void __launch_bounds__(kPrepThreads, kPrepBlocks) attn_prep_kernel(const AttnPrepArgs a) {
-    constexpr int LPR = D / 8, HPW = 32 / LPR, UN = sizeof(T) == 2 ? 4 : 2;
-    extern __shared__ float4 smem4[];                       // cosines and sines [warps][kPrepTokens][half]
-    const int warp = threadIdx.x >> 5, sub = (threadIdx.x & 31) / LPR;
-    float2 *turns = reinterpret_cast<float2 *>(smem4) + warp * kPrepTokens * a.half;
+    constexpr int LPR = D / 8, HPW = 32 / LPR, UN = kBatch<T>;
+    extern __shared__ float4 smem4[];                       // stages [warps][kStages], cosines and sines [warps][kPrepTokens][half]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / LPR;
+    Stage<T, UN> *stages = reinterpret_cast<Stage<T, UN> *>(smem4) + warp * kStages;
+    float2 *turns = reinterpret_cast<float2 *>(reinterpret_cast<Stage<T, UN> *>(smem4) + kPrepWarps * kStages) + warp * kPrepTokens * a.half;
     const long long tokens = (long long)gridDim.x * kPrepWarps;      // side by side
     long long t = (long long)blockIdx.x * kPrepWarps + warp;
     await_previous();
@@ -326,31 +351,66 @@ __global__ void __launch_bounds__(kPrepThreads, kPrepBlocks) attn_prep_kernel(co
     const T *qp = (const T *)a.q + t * a.ld_q + (first + sub) * (PLAIN ? D : a.hs_q);
     const T *kp = (const T *)a.k + t * a.ld_k + (first + sub) * (PLAIN ? D : a.hs_k);
     const T *vp = (const T *)a.v + t * a.ld_v + (first + sub) * (PLAIN ? D : a.hs_v);
-    Raw<T> held[UN];
+    // the next batch to ask for: of token t_ask, of q, k or v (kind_ask), heads from p_ask on
+    long long t_ask = t;
+    const T *p_ask = qp, *q_ask = qp, *k_ask = kp, *v_ask = vp;
+    int kind_ask = 0, left_ask = nq.any, mine_ask = nq.mine, in_stage = 0, out_stage = 0;
+    auto ask = [&]() {
+        if (t_ask < a.T) {
+            const long long step = PLAIN || kind_ask == 0 ? sq : kind_ask == 1 ? sk : sv;
 #pragma unroll
-    for (int j = 0; j < UN; ++j) {                          // whatever the tokens turn out to be
-        held[j].clear();
-        if (j < nq.mine) held[j].load(qp + j * sq + ca, qp + j * sq + cb);
-    }
+            for (int j = 0; j < UN; ++j)
+                if (j < mine_ask) stages[in_stage].ask(j, lane, p_ask + j * step + ca, p_ask + j * step + cb);
+            p_ask += UN * step;
+            left_ask -= UN;
+            mine_ask -= UN;
+            if (left_ask <= 0) {
+                if (kind_ask == 0 && nk.any) {
+                    kind_ask = 1;
+                    p_ask = k_ask;
+                    left_ask = nk.any;
+                    mine_ask = nk.mine;
+                } else if (kind_ask == 1 && nv.any) {
+                    kind_ask = 2;
+                    p_ask = v_ask;
+                    left_ask = nv.any;
+                    mine_ask = nv.mine;
+                } else {
+                    t_ask += tokens;
+                    q_ask += tokens * a.ld_q;
+                    k_ask += tokens * a.ld_k;
+                    v_ask += tokens * a.ld_v;
+                    kind_ask = 0;
+                    p_ask = q_ask;
+                    left_ask = nq.any;
+                    mine_ask = nq.mine;
+                }
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        in_stage = (in_stage + 1) % kStages;
+    };
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) ask();            // whatever the tokens turn out to be
     f32x2 own[4], other[4];
-    // The heads of one kind of a token, a batch of UN loads ahead: of its next ones or, at the end, of those at `then`.
-    auto run = [&](auto kind_of, const Share &n, const T *p, long long step, const T *then, long long then_step, int then_mine, int state,
-                   T *out, T *cache) {
+    // The heads of one kind of a token, a batch of UN at a time, while the next ones are under way.
+    auto run = [&](auto kind_of, const Share &n, const T *p, long long step, int state, T *out, T *cache) {
         constexpr int kind = decltype(kind_of)::value;
         const float *w = kind == 0 ? a.w_q : kind == 1 ? a.w_k : nullptr;
         const int cache_step = kind == 0 ? 0 : by * a.d.page * D;
         for (int i = 0; i < n.any; i += UN) {
-            const bool more = i + UN < n.any;
-            const T *next = more ? p + UN * step : then;
-            const long long next_step = PLAIN ? step : more ? step : then_step;
-            const int next_mine = more ? n.mine - i - UN : then_mine;
-            auto refill = [&](int j) {
-                if (j < next_mine) held[j].load(next + j * next_step + ca, next + j * next_step + cb);
-            };
+            asm volatile("cp.async.wait_group %0;" :: "n"(kStages - 2) : "memory");
+            Raw<T> held[UN];
+#pragma unroll
+            for (int j = 0; j < UN; ++j) {
+                held[j].clear();
+                if (i + j < n.mine) held[j] = stages[out_stage].get(j, lane);
+            }
+            out_stage = (out_stage + 1) % kStages;
+            ask();                                          // into the stage that was read before this one
             auto work = [&](int j, bool in) {
                 f32x2 x[4];
                 held[j].get(x);
-                refill(j);
                 float rstd = 1.f;
                 if (w) rstd = rsqrtf(fmaf(head_sum<LPR>(dot8(x, x)), 1.f / D, a.eps));
                 rot.turn(x, own, other, in ? p + j * step : nullptr);
@@ -366,7 +426,6 @@ __global__ void __launch_bounds__(kPrepThreads, kPrepBlocks) attn_prep_kernel(co
 #pragma unroll
                 for (int j = 0; j < UN; ++j) {
                     Raw<T> raw = held[j];
-                    refill(j);
                     if (i + j >= n.mine) continue;
                     if (kind == 2 && cache) raw.store(cache + j * cache_step + ca, cache + j * cache_step + cb);
                     raw.clear();
@@ -379,7 +438,7 @@ __global__ void __launch_bounds__(kPrepThreads, kPrepBlocks) attn_prep_kernel(co
 #pragma unroll
                 for (int j = 0; j < UN; ++j) work(j, i + j < n.mine);
             }
-            p = next;
+            p += UN * step;
             if (kind < 2 && out) out += UN * by * D;
             if (kind > 0 && cache) cache += UN * cache_step;
         }
@@ -398,18 +457,14 @@ __global__ void __launch_bounds__(kPrepThreads, kPrepBlocks) attn_prep_kernel(co
                 v_cache = (T *)a.v_pages + place;
             }
         }
-        const T *next_q = qp + tokens * a.ld_q;
-        const int next_mine = t + tokens < a.T ? nq.mine : 0;
         if (state == kLive) rot.factors(angles, 1.f, a.w_q, a.offset, own, other);
-        run(std::integral_constant<int, 0>(), nq, qp, sq, nk.any ? kp : next_q, nk.any ? sk : sq, nk.any ? nk.mine : next_mine, state,
-            (T *)a.q_out + (t * a.d.hq + first + sub) * D, nullptr);
+        run(std::integral_constant<int, 0>(), nq, qp, sq, state, (T *)a.q_out + (t * a.d.hq + first + sub) * D, nullptr);
         if (nk.any) {
             if (state == kLive) rot.factors(angles, 1.f, a.w_k, a.offset, own, other);
-            run(std::integral_constant<int, 1>(), nk, kp, sk, nv.any ? vp : next_q, nv.any ? sv : sq, nv.any ? nv.mine : next_mine, state, k_out,
-                k_cache);
-            if (nv.any) run(std::integral_constant<int, 2>(), nv, vp, sv, next_q, sq, next_mine, state, nullptr, v_cache);
+            run(std::integral_constant<int, 1>(), nk, kp, sk, state, k_out, k_cache);
+            if (nv.any) run(std::integral_constant<int, 2>(), nv, vp, sv, state, nullptr, v_cache);
         }
-        qp = next_q;
+        qp += tokens * a.ld_q;
         kp += tokens * a.ld_k;
         vp += tokens * a.ld_v;
     }
@@ -580,7 +635,7 @@ template <typename K> cudaError_t with_smem(K kernel, int bytes) {
 }
 
 template <typename T, int D, int MODE> cudaError_t run_prep(const AttnPrepArgs &a, cudaStream_t s) {
-    const int hpw = 256 / D, smem = kPrepWarps * kPrepTokens * a.half * 8, blocks = prep_blocks(a.T, kPrepBlocks);
+    const int hpw = 256 / D, smem = kPrepWarps * (kStages * (int)sizeof(Stage<T, kBatch<T>>) + kPrepTokens * a.half * 8), blocks = prep_blocks(a.T, kPrepBlocks);
     // a token's heads over several warps where there are few tokens
     const long long most = (a.d.hq + hpw - 1) / hpw, want = (long long)sm_count() * 24 / a.T;
     const unsigned split = (unsigned)(want < 1 ? 1 : want < most ? want : most);
