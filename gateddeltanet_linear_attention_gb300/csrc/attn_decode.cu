@@ -12,28 +12,69 @@ namespace gdn {
 
 namespace {
 
-constexpr int kSimtThreads = 256;
 constexpr int kSimtTile = 32;
 
 // The 32-bit form, on the CUDA cores: RPW query rows a warp, a tile of 32 tokens in shared memory, a token a lane for the
-// scores and D / 32 columns a lane for the sums.  Bound by its multiply-adds and by loads that wait for no other tile; for checks
-// of a model rather than serving: 7 sequences of up to 2,047 tokens, 2 new ones, window 500: 9.1 us, most of it latency.
+// scores and D / 32 columns a lane for the sums.  The next tile is on its way while one is worked on, the pages of the one
+// behind it are looked up.  Bound by its reads of shared memory and multiply-adds (a warp reads all of a tile for its rows): 64
+// sequences of up to 8,192 tokens, 8 key heads of 128 columns, 4 query heads each (2.2 GB) 558 us, 0.58 of the copy rate (1,258
+// with a tile loaded and worked on in turn); 16 of up to 4,096, 4 key heads, 64 rows each 236 us.
+// Two tiles of 256 columns leave room for one CTA an SM: with many rows it is twice as large.
+template <int D, int RPW> constexpr int simt_threads = D == 256 && RPW == 4 ? 512 : 256;
 template <int D, int RPW>
-__global__ void __launch_bounds__(kSimtThreads) attn_decode_simt_kernel(const AttnDecodeArgs a) {
-    constexpr int TILE = kSimtTile, LDK = D + 4, CPL = D / 32, WARPS = kSimtThreads / 32, RB = WARPS * RPW;
+__global__ void __launch_bounds__((simt_threads<D, RPW>)) attn_decode_simt_kernel(const AttnDecodeArgs a) {
+    constexpr int THREADS = simt_threads<D, RPW>, TILE = kSimtTile, LDK = D + 4, CPL = D / 32, WARPS = THREADS / 32, RB = WARPS * RPW, BUFFER = TILE * (LDK + D);
+    constexpr int PASS = THREADS / (D / 4);            // tokens that the block copies at a time
+    static_assert(16 % PASS == 0, "of one piece of a page");
     extern __shared__ float4 smem4[];
-    float *ks = reinterpret_cast<float *>(smem4), *vs = ks + TILE * LDK, *qs = vs + TILE * D;
+    float *tiles = reinterpret_cast<float *>(smem4), *qs = tiles + 2 * BUFFER;
     __shared__ long long sums[33];
-    __shared__ int found[3], bad_page[TILE];
+    __shared__ int found[3];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rows = a.d.grp * a.tokens, row0 = blockIdx.y * RB;
     await_previous();
     let_next_start();
     AttnWalk w;
-    if (!attn_begin<TILE, kSimtThreads>(a, blockIdx.x, sums, found, w)) {
+    if (!attn_begin<TILE, THREADS>(a, blockIdx.x, sums, found, w)) {
         if (blockIdx.y == 0 && tid == 0) a.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
         return;
     }
     const float *kp = (const float *)a.k_pages, *vp = (const float *)a.v_pages;
+    // the tile to copy next, and the pages of its two pieces of 16 tokens (-1: masked)
+    AttnWalk next = w;
+    int page[2], there_now = 0, buffer = 0;
+    auto look_up = [&]() {
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const int i = (next.s.tile0 + next.t) * TILE + p * 16;
+            page[p] = -1;
+            if (i < next.s.len && i + 16 > next.s.first) {
+                page[p] = a.table[(long long)next.s.row * a.d.max_pages + (i >> a.d.page_shift)];
+                if (page[p] < 0 || page[p] >= a.d.n_pages) {
+                    set_error(a.err, GDN_DEVERR_PAGE);
+                    page[p] = -1;
+                }
+            }
+        }
+    };
+    auto copy = [&](int to) {                               // what is masked is zero; which pieces are there
+        const int i0 = (next.s.tile0 + next.t) * TILE, c = tid % (D / 4) * 4;
+        const uint32_t ks = (uint32_t)__cvta_generic_to_shared(tiles + to * BUFFER), vs = ks + TILE * LDK * 4;
+#pragma unroll
+        for (int t0 = 0; t0 < TILE; t0 += PASS) {
+            const int t = t0 + tid / (D / 4), i = i0 + t, from = page[t0 >> 4];
+            const bool in = from >= 0 && i < next.s.len && i >= next.s.first;
+            const long long at = in ? (((long long)from * a.d.hkv + next.h) * a.d.page + (i & (a.d.page - 1))) * D + c : 0;
+            const int bytes = in ? 16 : 0;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(ks + (t * LDK + c) * 4), "l"(kp + at), "r"(bytes) : "memory");
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(vs + (t * D + c) * 4), "l"(vp + at), "r"(bytes) : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        return (page[0] >= 0 ? 1 : 0) | (page[1] >= 0 ? 2 : 0);
+    };
+    look_up();
+    int there_next = copy(0);
+    attn_next<TILE>(a, next);
+    if (next.left > 0) look_up();
     bool unit_first = true;               // this unit is the CTA's first one
     while (w.left > 0) {
         const bool whole_front = w.t == 0;
@@ -41,7 +82,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_decode_simt_kernel(const At
         const AttnSeq s = w.s;
         // query rows in 32 bits
         __syncthreads();
-        for (int i = tid; i < RB * (D / 4); i += kSimtThreads) {
+        for (int i = tid; i < RB * (D / 4); i += THREADS) {
             const int r = row0 + i / (D / 4), c = i % (D / 4) * 4;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < rows) {
@@ -65,32 +106,18 @@ __global__ void __launch_bounds__(kSimtThreads) attn_decode_simt_kernel(const At
         bool unit_end;
         do {
             const int i0 = (s.tile0 + w.t) * TILE;
-            __syncthreads();
-            if (tid < TILE) {             // the page of every token, -1: masked
-                const int i = i0 + tid;
-                int page = -1;
-                if (i < s.len && i >= s.first) {
-                    page = a.table[(long long)s.row * a.d.max_pages + (i >> a.d.page_shift)];
-                    if (page < 0 || page >= a.d.n_pages) {
-                        set_error(a.err, GDN_DEVERR_PAGE);
-                        page = -1;
-                    }
-                }
-                bad_page[tid] = page;
+            const float *ks = tiles + buffer * BUFFER, *vs = ks + TILE * LDK;
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            __syncthreads();              // the tile is there, and the one before has been read
+            there_now = there_next;
+            if (next.left > 0) {
+                there_next = copy(buffer ^ 1);
+                attn_next<TILE>(a, next);
+                if (next.left > 0) look_up();
             }
-            __syncthreads();
-            for (int i = tid; i < TILE * (D / 4); i += kSimtThreads) {
-                const int t = i / (D / 4), c = i % (D / 4) * 4, page = bad_page[t];
-                float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
-                if (page >= 0) {
-                    const long long at = (((long long)page * a.d.hkv + h) * a.d.page + ((i0 + t) & (a.d.page - 1))) * D + c;
-                    kv = load4f(kp + at);
-                    vv = load4f(vp + at);
-                }
-                *reinterpret_cast<float4 *>(ks + t * LDK + c) = kv;
-                *reinterpret_cast<float4 *>(vs + t * D + c) = vv;
-            }
-            __syncthreads();
+            buffer ^= 1;
+            unit_end = attn_next<TILE>(a, w);
+            if (row0 + warp * RPW >= rows) continue;
             float sc[RPW];
 #pragma unroll
             for (int r = 0; r < RPW; ++r) sc[r] = 0.f;
@@ -103,7 +130,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_decode_simt_kernel(const At
                 }
             }
             const int i = i0 + lane;
-            const bool there = bad_page[lane] >= 0;
+            const bool there = (there_now >> (lane >> 4) & 1) && i >= s.first && i < s.len;
             float p[RPW];
             unsigned seen[RPW];
 #pragma unroll
@@ -142,7 +169,6 @@ __global__ void __launch_bounds__(kSimtThreads) attn_decode_simt_kernel(const At
                     }
                 }
             }
-            unit_end = attn_next<TILE>(a, w);
         } while (!unit_end && w.left > 0);
         // the unit's rows: whole, or a part for the join kernel
         const bool whole = whole_front && unit_end;
@@ -296,15 +322,16 @@ template <typename T, int D> __global__ void __launch_bounds__(kJoinThreads, 5) 
     }
 }
 
-template <int D, int RPW> cudaError_t run_simt(const AttnDecodeArgs &a, cudaStream_t s) {
-    constexpr int RB = kSimtThreads / 32 * RPW, smem = (kSimtTile * (D + 4) + kSimtTile * D + RB * D) * 4;
+template <int D, int RPW> cudaError_t run_simt(AttnDecodeArgs a, cudaStream_t s) {
+    constexpr int THREADS = simt_threads<D, RPW>, RB = THREADS / 32 * RPW, smem = (2 * kSimtTile * (2 * D + 4) + RB * D) * 4;
     const auto kernel = attn_decode_simt_kernel<D, RPW>;
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
     }
+    if (2 * (smem + 1024) > 227 * 1024) a.ctas = sm_count();      // one CTA an SM
     const int rows = a.d.grp * a.tokens;
-    const cudaError_t e = launch_early(kernel, dim3(a.ctas, (rows + RB - 1) / RB), kSimtThreads, smem, s, a);
+    const cudaError_t e = launch_early(kernel, dim3(a.ctas, (rows + RB - 1) / RB), THREADS, smem, s, a);
     return e != cudaSuccess ? e : launch_attn_join(a, false, s);
 }
 template <int D> cudaError_t run_rows(const AttnDecodeArgs &a, cudaStream_t s) {
