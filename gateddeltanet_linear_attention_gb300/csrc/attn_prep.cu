@@ -639,16 +639,16 @@ template <typename T, int D, int MODE> cudaError_t run_prep(const AttnPrepArgs &
     // a token's heads over several warps where there are few tokens
     const long long most = (a.d.hq + hpw - 1) / hpw, want = (long long)sm_count() * 24 / a.T;
     const unsigned split = (unsigned)(want < 1 ? 1 : want < most ? want : most);
-    const bool plain = MODE == kHalves && split == 1 && a.hs_q == D && (!a.k || a.hs_k == D) && (!a.k_pages || a.hs_v == D);
-    const auto kernel = plain ? attn_prep_kernel<T, D, MODE, MODE == kHalves> : attn_prep_kernel<T, D, MODE, false>;
+    const bool plain = MODE != kAny && split == 1 && a.hs_q == D && (!a.k || a.hs_k == D) && (!a.k_pages || a.hs_v == D);
+    const auto kernel = plain ? attn_prep_kernel<T, D, MODE, MODE != kAny> : attn_prep_kernel<T, D, MODE, false>;
     const cudaError_t e = with_smem(kernel, smem);
     if (e != cudaSuccess) return e;
     return launch_early(kernel, dim3((unsigned)blocks, split), kPrepThreads, smem, s, a);
 }
 template <typename T, int D, int MODE> cudaError_t run_backward(const AttnPrepArgs &a, cudaStream_t s) {
     const int blocks = backward_blocks(a.T), smem = 2 * kPrepThreads * 8 * 4 + kPrepWarps * kPrepTokens * a.half * 8;
-    const bool plain = MODE == kHalves && a.hs_q == D && (!a.k || a.hs_k == D);
-    const auto kernel = plain ? attn_prep_backward_kernel<T, D, MODE, MODE == kHalves> : attn_prep_backward_kernel<T, D, MODE, false>;
+    const bool plain = MODE != kAny && a.hs_q == D && (!a.k || a.hs_k == D);
+    const auto kernel = plain ? attn_prep_backward_kernel<T, D, MODE, MODE != kAny> : attn_prep_backward_kernel<T, D, MODE, false>;
     cudaError_t e = with_smem(kernel, smem);
     if (e != cudaSuccess) return e;
     e = launch_early(kernel, dim3(blocks), kPrepThreads, smem, s, a);
