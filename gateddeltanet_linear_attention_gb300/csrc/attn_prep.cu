@@ -10,12 +10,13 @@
 // HBM-bound: q, k and v are read once and written once.  D / 8 lanes own a head vector and keep it in registers.  A
 // warp takes a few tokens at a time: what they are and their angles come first, a lane a token, then a lane an angle;
 // then it goes through their heads in batches, the next batches (of the next kind of heads, of the next token) under way:
-// forward two, by asynchronous copies of each lane's pieces to shared memory, backward one, in registers.  No warp waits for
+// forward four, by asynchronous copies of each lane's pieces to shared memory, backward one, in registers.  No warp waits for
 // another.  Tokens that share a block's angles instead took 70 us where this takes 36.
 //
 // Measured in bf16: 9,600 prompt tokens into the cache (16 + 2 + 2 heads of 256, 64 columns rotated) 36 us, 0.81 of the copy
-// rate (one batch ahead in registers 40; three ahead 37, four 38; three blocks an SM 47 and 53: spills); the backward of 8,192
-// tokens (32 + 8 heads of 128) 56 us, 0.66, issue used by 0.57; 64 tokens of a decode step 6 us.
+// rate, issue used by 0.55 (one batch of four heads ahead in registers 40, two to four of them in shared memory 36 to 38; three
+// blocks an SM 47 to 53: spills); the backward of 8,192
+// tokens (32 + 8 heads of 128) 56 us, 0.66, issue used by 0.57; 64 tokens of a decode step 5.5 us.
 #include <type_traits>
 
 #include "attn_common.cuh"
@@ -328,11 +329,10 @@ template <typename T, int UN> struct Stage {
 
 // PLAIN: heads stand one after another in q, k and v, and a warp has all of a token's: the distances from one to the next
 // are constants of the code.  (Address arithmetic was half of the instructions, and the kernels issue half of the time.)
-constexpr int kStages = 3;           // one that is worked on, two under way
-template <typename T> constexpr int kBatch = sizeof(T) == 2 ? 4 : 2;
+constexpr int kStages = 5, kBatch = 2;       // stages: one that is worked on, four under way
 template <typename T, int D, int MODE, bool PLAIN>
 __global__ void __launch_bounds__(kPrepThreads, kPrepBlocks) attn_prep_kernel(const AttnPrepArgs a) {
-    constexpr int LPR = D / 8, HPW = 32 / LPR, UN = kBatch<T>;
+    constexpr int LPR = D / 8, HPW = 32 / LPR, UN = kBatch;
     extern __shared__ float4 smem4[];                       // stages [warps][kStages], cosines and sines [warps][kPrepTokens][half]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / LPR;
     Stage<T, UN> *stages = reinterpret_cast<Stage<T, UN> *>(smem4) + warp * kStages;
@@ -635,7 +635,7 @@ template <typename K> cudaError_t with_smem(K kernel, int bytes) {
 }
 
 template <typename T, int D, int MODE> cudaError_t run_prep(const AttnPrepArgs &a, cudaStream_t s) {
-    const int hpw = 256 / D, smem = kPrepWarps * (kStages * (int)sizeof(Stage<T, kBatch<T>>) + kPrepTokens * a.half * 8), blocks = prep_blocks(a.T, kPrepBlocks);
+    const int hpw = 256 / D, smem = kPrepWarps * (kStages * (int)sizeof(Stage<T, kBatch>) + kPrepTokens * a.half * 8), blocks = prep_blocks(a.T, kPrepBlocks);
     // a token's heads over several warps where there are few tokens
     const long long most = (a.d.hq + hpw - 1) / hpw, want = (long long)sm_count() * 24 / a.T;
     const unsigned split = (unsigned)(want < 1 ? 1 : want < most ? want : most);
