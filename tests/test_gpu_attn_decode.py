@@ -375,3 +375,29 @@ def test_every_layout_walks_its_ring(Hq, Hkv, D, page, tokens):
             want, mag = (torch.einsum("hgt,htd->hgd", p, x).reshape(1, Hq, D) for x in (V, V.abs()))
             compare(out[t:t + 1].double().cpu(), lse[t:t + 1].double().cpu(), (want, torch.logsumexp(s, -1).view(1, Hq), mag, top), L, D, c.act)
     assert gdn.gdn_device_error() == 0
+
+
+@pytest.mark.parametrize("window", [0, 90])
+@pytest.mark.parametrize("act,Hq,Hkv,D,tokens", [("bf16", 8, 1, 64, 8), ("bf16", 16, 1, 64, 8), ("bf16", 6, 2, 128, 7), ("bf16", 16, 1, 128, 8), ("bf16", 4, 1, 256, 8),
+                                                 ("bf16", 16, 1, 256, 8), ("bf16", 16, 2, 256, 2), ("bf16", 4, 2, 64, 1), ("fp32", 6, 2, 64, 1),
+                                                 ("fp32", 8, 1, 128, 3), ("fp32", 16, 1, 256, 8)])
+def test_many_short_units(act, Hq, Hkv, D, tokens, window):
+    """Every CTA has several units, of no to a few tiles, and some begin or end inside one."""
+    g = torch.Generator().manual_seed(D + tokens)
+    lens = torch.randint(0, 260, (600,), generator=g).tolist()
+    lens[100], lens[101], lens[300] = 3000, 0, 1500
+    c = Cache(lens, Hq, Hkv, D, 32, act, tokens, seed=16).upload()
+    out, lse = c.run(window=window)
+    c.check(out, lse, window=window, seqs=list(range(0, 600, 23)) + [99, 100, 101, 102, 299, 300, 301, 599])
+    assert gdn.gdn_device_error() == 0
+    again, _ = c.run(window=window)
+    assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,page,tokens", [(16, 1, 256, 64, 8), (8, 1, 64, 16, 8), (16, 1, 128, 128, 8)])
+def test_long_cache_of_many_rows(Hq, Hkv, D, page, tokens):
+    """One long sequence of many query rows beside a short one, in more tiles a CTA than its rings hold."""
+    c = Cache([150000, 5], Hq, Hkv, D, page, "bf16", tokens, seed=17).upload()
+    out, lse = c.run()
+    c.check(out, lse)
+    assert gdn.gdn_device_error() == 0
