@@ -18,7 +18,8 @@ constexpr int kSimtTile = 32;
 // scores and D / 32 columns a lane for the sums.  The next tile is on its way while one is worked on, the pages of the one
 // behind it are looked up.  Bound by its reads of shared memory and multiply-adds (a warp reads all of a tile for its rows): 64
 // sequences of up to 8,192 tokens, 8 key heads of 128 columns, 4 query heads each (2.2 GB) 558 us, 0.58 of the copy rate (1,258
-// with a tile loaded and worked on in turn); 16 of up to 4,096, 4 key heads, 64 rows each 236 us.
+// with a tile loaded and worked on in turn); 16 of up to 4,096, 4 key heads, 64 rows each 236 us
+// (eight rows a warp: 342, registers).
 // Two tiles of 256 columns leave room for one CTA an SM: with many rows it is twice as large.
 template <int D, int RPW> constexpr int simt_threads = D == 256 && RPW == 4 ? 512 : 256;
 template <int D, int RPW>
