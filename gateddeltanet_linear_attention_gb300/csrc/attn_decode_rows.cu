@@ -261,16 +261,20 @@ __global__ void __launch_bounds__((Shape<D, NG, RB>::threads), 1) attn_decode_ro
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16, t_s0 = tmem + lanes + g * 128, t_o0 = tmem + lanes + S::col_o, t_o = t_o0 + g * D;
         unsigned *my_spoil = spoil + g * D;
         uint32_t e = KE + g, phase = 0, k = 0;             // V's entry of the group's next tile
-        bool ok = true;
+        bool ok = true, marked = false;                    // marked: by this thread, in the unit before
         auto wait = [&](uint32_t b, uint32_t parity) { ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(b, parity, a.wait_ns)); };
         int u = 0;
         for (bool more = true; more; ++u) {
             const uint32_t us = u % kUnits;
-            // a group's warps give up together: they meet at its barrier
-            if (!bar_all(kBarGroup + g, 128, ok && tc::mbar_wait(ufull + 8 * us, (u / kUnits) & 1, a.wait_ns))) {
+            // A group's warps give up together, and clear their marks together: they meet at its barrier, and what decides is
+            // known to all of them.  (The marks themselves may be those of a faster warp of this unit already.)
+            const bool here = ok && tc::mbar_wait(ufull + 8 * us, (u / kUnits) & 1, a.wait_ns);
+            const bool clean = bar_all(kBarGroup + g, 128, here && !marked);
+            if (!clean && !bar_all(kBarGroup + g, 128, here)) {
                 ok = false;
                 break;
             }
+            marked = false;
             const Unit unit = units[us];
             more = unit.more;
             __syncwarp();
@@ -282,7 +286,7 @@ __global__ void __launch_bounds__((Shape<D, NG, RB>::threads), 1) attn_decode_ro
                 if (!mine) wait(taken + 8 * (NG - 1 - g), (u - 1) & 1);
                 mine = true;
             };
-            if (spoiled[g]) {
+            if (!clean) {
                 take_back();
                 for (int c = tid & 127; c < D; c += 128) my_spoil[c] = 0u;
                 bar_sync(kBarGroup + g, 128);
@@ -385,6 +389,7 @@ __global__ void __launch_bounds__((Shape<D, NG, RB>::threads), 1) attn_decode_ro
                                     }
                                 }
                                 spoiled[g] = 1;
+                                marked = true;
                                 asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" :: "r"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]) : "memory");
                             }
                         }

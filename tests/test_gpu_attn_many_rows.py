@@ -1,0 +1,71 @@
+"""Attention of new tokens where a key head has 17 to 128 query rows: values that are not finite in places that only some of
+the new tokens see, in many units one after another, so that every unit finds the marks of the one before."""
+import math
+import random
+
+import pytest
+import torch
+
+from test_gpu_attn_decode import Cache
+from gateddeltanet_linear_attention_gb300 import gdn
+
+pytestmark = pytest.mark.gpu
+
+# query heads, key heads, columns, tokens of a page, new tokens
+ONE_GROUP = [(4, 1, 256, 16, 8), (16, 1, 256, 64, 8), (16, 2, 256, 128, 3)]      # of warps takes all tiles of a unit
+
+
+def spoil(c, pool, window, seed, share):
+    """Puts values that are not finite where the newest token alone or only some see them, in `share` of the units; which outputs
+    [T, Hq, D] and sums [T, Hq] then are not finite."""
+    rng, k, G = random.Random(seed), c.tokens, c.Hq // c.Hkv
+    out = torch.zeros(c.q.shape, dtype=torch.bool)
+    kp, vp = c.kp.clone(), c.vp.clone()
+    for r, length in enumerate(c.lens):
+        for h in range(c.Hkv):
+            # of the tokens that some see: the newest ones, or those that the window leaves behind
+            edge = rng.randrange(length - k + 1, length) if not window or rng.random() < 0.5 else rng.randrange(length - k + 1 - window, length - window)
+            if rng.random() >= share or edge < 0:
+                continue
+            col, at = rng.randrange(c.D), (c.table[r, edge // c.page], h, edge % c.page)
+            (kp if pool == "k" else vp)[at][col] = math.nan if pool == "k" else rng.choice([math.inf, -math.inf, math.nan])
+            for j in range(k):
+                end = length - k + 1 + j
+                if edge < end and (not window or edge >= end - window):
+                    out[r * k + j, h * G:(h + 1) * G, slice(None) if pool == "k" else col] = True
+    c.d[1].copy_(kp)
+    c.d[2].copy_(vp)
+    return out.cuda()
+
+
+def check(layout, pool, window, lens, share=0.6, turns=20):
+    Hq, Hkv, D, page, tokens = layout
+    assert 16 < Hq // Hkv * tokens <= 128
+    c = Cache(lens, Hq, Hkv, D, page, "bf16", tokens, seed=D + tokens).upload()
+    clean, clean_lse = c.run(window=window)
+    assert torch.isfinite(clean).all()
+    for turn in range(turns):
+        bad = spoil(c, pool, window, turn, share) if turn % 5 == 0 else bad
+        out, lse = c.run(window=window)
+        assert torch.equal(torch.isfinite(out), ~bad)
+        assert torch.equal(torch.where(bad, 0, out), torch.where(bad, 0, clean))
+        if pool == "k":
+            assert torch.equal(torch.isnan(lse), bad.any(-1))
+            lse = torch.where(bad.any(-1), clean_lse, lse)
+        assert torch.equal(lse, clean_lse)
+    assert gdn.gdn_device_error() == 0
+
+
+@pytest.mark.parametrize("pool", ["v", "k"])
+@pytest.mark.parametrize("window", [0, 40])
+@pytest.mark.parametrize("layout", ONE_GROUP)
+def test_values_that_are_not_finite_in_unit_after_unit(layout, window, pool):
+    """Units of one to a few tiles, several a CTA, most of them with such a value: the marks are set and cleared all the time."""
+    g = torch.Generator().manual_seed(1)
+    check(layout, pool, window, torch.randint(0, 200, (400,), generator=g).tolist())
+
+
+@pytest.mark.parametrize("layout", ONE_GROUP)
+def test_values_that_are_not_finite_in_parts(layout):
+    """Units that several CTAs hold: the marks are those of the last tiles' CTA, and reach the sums through the join."""
+    check(layout, "v", 0, [30000, 70, 64, 9001, 3, 12345], share=1.0, turns=6)
