@@ -280,7 +280,7 @@ __global__ void __launch_bounds__((Shape<D, NG, RB>::threads), 1) attn_decode_ro
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(uempty + 8 * us);
             const int first_j = (g - unit.seq0) & (NG - 1), tiles = unit.count > first_j ? (unit.count - first_j + NG - 1) / NG : 0;
-            // a group's O and statistics are the other's too until that has taken them
+            // a group's O, statistics and marks are the other's too until that has taken them
             bool mine = NG == 1 || u == 0;
             auto take_back = [&]() {
                 if (!mine) wait(taken + 8 * (NG - 1 - g), (u - 1) & 1);
@@ -364,6 +364,7 @@ __global__ void __launch_bounds__((Shape<D, NG, RB>::threads), 1) attn_decode_ro
                 }
                 l += (part[0] + part[1]) + (part[2] + part[3]);
                 if (masked) {
+                    if (j == first_j) take_back();          // the other group may still read this one's marks of the unit before
                     // Places that no row sees may hold anything: they become zeros.  A value that is not finite in a place that
                     // only some new tokens see becomes zero too, and the sums of its column for those tokens are NaN, as sums
                     // with it are not finite.

@@ -13,6 +13,7 @@ pytestmark = pytest.mark.gpu
 
 # query heads, key heads, columns, tokens of a page, new tokens
 ONE_GROUP = [(4, 1, 256, 16, 8), (16, 1, 256, 64, 8), (16, 2, 256, 128, 3)]      # of warps takes all tiles of a unit
+TWO_GROUPS = [(8, 1, 64, 16, 8), (6, 2, 128, 32, 7), (16, 1, 64, 64, 8), (16, 1, 128, 128, 8), (10, 1, 128, 16, 2), (8, 2, 64, 128, 5)]  # take turns
 
 
 def spoil(c, pool, window, seed, share):
@@ -58,14 +59,22 @@ def check(layout, pool, window, lens, share=0.6, turns=20):
 
 @pytest.mark.parametrize("pool", ["v", "k"])
 @pytest.mark.parametrize("window", [0, 40])
-@pytest.mark.parametrize("layout", ONE_GROUP)
+@pytest.mark.parametrize("layout", ONE_GROUP + TWO_GROUPS)
 def test_values_that_are_not_finite_in_unit_after_unit(layout, window, pool):
     """Units of one to a few tiles, several a CTA, most of them with such a value: the marks are set and cleared all the time."""
     g = torch.Generator().manual_seed(1)
     check(layout, pool, window, torch.randint(0, 200, (400,), generator=g).tolist())
 
 
-@pytest.mark.parametrize("layout", ONE_GROUP)
+@pytest.mark.parametrize("layout", ONE_GROUP + TWO_GROUPS)
 def test_values_that_are_not_finite_in_parts(layout):
     """Units that several CTAs hold: the marks are those of the last tiles' CTA, and reach the sums through the join."""
     check(layout, "v", 0, [30000, 70, 64, 9001, 3, 12345], share=1.0, turns=6)
+
+
+@pytest.mark.parametrize("layout", TWO_GROUPS)
+@pytest.mark.parametrize("length", [60, 128])
+def test_marks_of_one_unit_stay_out_of_the_next(layout, length):
+    """Every second unit has such a value, all of one or two tiles: one group marks in a unit while the other writes the outputs
+    of the unit before."""
+    check(layout, "v", 0, [length - i % 2 * (i % 7) for i in range(2000)], share=0.5, turns=40)
