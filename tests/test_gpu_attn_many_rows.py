@@ -1,12 +1,13 @@
 """Attention of new tokens where a key head has 17 to 128 query rows: values that are not finite in places that only some of
-the new tokens see, in many units one after another, so that every unit finds the marks of the one before."""
+the new tokens see, in many units one after another, so that every unit finds the marks of the one before; faults and keys of
+-inf in that kernel."""
 import math
 import random
 
 import pytest
 import torch
 
-from test_gpu_attn_decode import Cache
+from test_gpu_attn_decode import Cache, compare
 from gateddeltanet_linear_attention_gb300 import gdn
 
 pytestmark = pytest.mark.gpu
@@ -78,3 +79,52 @@ def test_marks_of_one_unit_stay_out_of_the_next(layout, length):
     """Every second unit has such a value, all of one or two tiles: one group marks in a unit while the other writes the outputs
     of the unit before."""
     check(layout, "v", 0, [length - i % 2 * (i % 7) for i in range(2000)], share=0.5, turns=40)
+
+
+LAYOUTS = [(8, 1, 64, 16, 8), (16, 1, 128, 16, 8), (4, 1, 256, 16, 8), (16, 1, 256, 16, 8)]
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,page,tokens", LAYOUTS)
+def test_faults_are_reported(Hq, Hkv, D, page, tokens):
+    """A row beyond the table and a length beyond it are padding lanes; tokens of bad pages are masked, whole tiles of them too."""
+    k = tokens
+    c = Cache([30, 250, 50], Hq, Hkv, D, page, "bf16", k, seed=7).upload()
+    good, good_lse = c.run()
+    out, lse = c.run(rows=torch.tensor([0, 3, 2], dtype=torch.int32, device="cuda"))
+    assert gdn.gdn_device_error() == gdn.DEVERR_SLOT
+    assert not out[k:2 * k].any() and torch.equal(out[:k], good[:k]) and torch.equal(out[2 * k:], good[2 * k:])
+    assert (lse[k:2 * k] == -math.inf).all()
+    c.d[4][1] = page * c.table.shape[1] + 1
+    out, lse = c.run()
+    assert gdn.gdn_device_error() == gdn.DEVERR_PAGE
+    assert not out[k:2 * k].any() and torch.equal(out[:k], good[:k]) and (lse[k:2 * k] == -math.inf).all()
+    c.d[4][1] = 250
+    table = c.d[3].clone()
+    # one page inside a tile; the first tile; the last pages, the newest tokens among them; all
+    for bad, first, last in ((-1, 2, 3), (c.n_pages, 0, 4), (1 << 30, 13, 16), (-(1 << 31), 0, 16)):
+        c.d[3].copy_(table)
+        c.d[3][1, first:last] = bad
+        out, lse = c.run()
+        assert gdn.gdn_device_error() == gdn.DEVERR_PAGE
+        compare(out[k:2 * k].double().cpu(), lse[k:2 * k].double().cpu(), c.want(1, seen=[not first * page <= i < last * page for i in range(250)]), 250, D,
+                c.act)
+        assert torch.equal(out[:k], good[:k]) and torch.equal(out[2 * k:], good[2 * k:]) and torch.equal(lse[:k], good_lse[:k])
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,page,tokens", LAYOUTS + [(2, 1, 64, 16, 2), (4, 1, 256, 16, 1)])
+def test_scores_of_minus_infinity(Hq, Hkv, D, page, tokens):
+    """Keys of -inf where the query is positive are masked by their own score, a first tile of them too; a row of them alone is
+    empty."""
+    k = tokens
+    c = Cache([200, 40, 300], Hq, Hkv, D, page, "bf16", k, seed=9)
+    c.q = c.q.abs() + 0.1
+    gone = [[i < 70 or i == 150 for i in range(200)], [True] * 40, [i % 3 > 0 or i > 200 for i in range(300)]]
+    for r, which in enumerate(gone):
+        for i, x in enumerate(which):
+            if x:
+                c.K[r][:, i] = c.kp[c.table[r, i // page], :, i % page] = -math.inf
+    c.upload()
+    out, lse = c.run()
+    for r, which in enumerate(gone):
+        compare(out[r * k:(r + 1) * k].double().cpu(), lse[r * k:(r + 1) * k].double().cpu(), c.want(r, seen=[not x for x in which]), len(which), D, c.act)
+    assert not out[k:2 * k].any() and (lse[k:2 * k] == -math.inf).all() and gdn.gdn_device_error() == 0
