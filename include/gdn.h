@@ -659,9 +659,10 @@ gdn_status gdn_attn_decode(const gdn_attn_config *cfg, const gdn_attn_decode_io 
  * lane stays as it is.  granted, src_idx, dst_idx: int32 [n].
  *
  * gdn_page_fork: row dst_rows[i] becomes a copy of row src_rows[i] that shares
- * its pages.  It must be empty (lens 0), and no other lane's source or
- * destination; else the lane is skipped and GDN_DEVERR_SLOT reported.  Many
- * lanes may have one source.
+ * its pages.  It must be empty (lens 0) and no other lane's destination, and its
+ * source must be no lane's destination, skipped ones among them; else the lane is
+ * skipped and GDN_DEVERR_SLOT reported.  (Where lane i's destination is lane j's
+ * source, lane j is skipped and lane i is not.)  Many lanes may have one source.
  *
  * gdn_page_compact: moves pages to the lowest places: the k-th free page below
  * the number of held pages takes the k-th held page above it, k < n.  Writes
