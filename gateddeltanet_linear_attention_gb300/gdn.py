@@ -833,7 +833,7 @@ def _page_state(where, dev, cfg, page_table, lens, refs):
 
 def gdn_page_resize(cfg, page_table, lens, refs, rows, new_lens, granted, src_idx, dst_idx, workspace, stream=None):
     """Sets the lengths of `rows` to new_lens: pages taken, let go, or replaced by copies (src_idx -> dst_idx, to be carried out
-    with gdn_page_copy before they are written and before the next resize).  granted: the lengths after the call."""
+    with gdn_page_copy before they are written and before the next resize or compaction).  granted: the lengths after the call."""
     if _get_device is None:
         _start()
     where, dev, i32, n = "gdn_page_resize", _get_device(), _I32, rows.shape[0]

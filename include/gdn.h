@@ -649,9 +649,11 @@ gdn_status gdn_attn_decode(const gdn_attn_config *cfg, const gdn_attn_decode_io 
  * gdn_page_resize: sets the length of rows[i] to new_lens[i] (negative: an
  * inactive lane).  A longer row takes pages; if its last page is in part filled
  * and held by another row as well, a new page takes that one's place, and the
- * copy to carry out (gdn_page_copy, in every layer's pools, before they are
- * written and before the next resize) is src_idx[i] -> dst_idx[i], else both are
- * -1.  A shorter row lets
+ * copy to carry out is src_idx[i] -> dst_idx[i], else both are -1: by
+ * gdn_page_copy, in every layer's pools, before they are written and before the
+ * next gdn_page_resize or gdn_page_compact.  (The source may be free from now on,
+ * when all its holders have moved: either call may give it away, and a
+ * compaction may move the destination.)  A shorter row lets
  * pages go; 0 frees it.  granted[i]: the row's length after the call (-1: an
  * inactive lane).  When the free pages do not reach, the lanes that need pages
  * from the first one on that cannot have all of its own stay as they are.  A

@@ -1,5 +1,6 @@
 """Rules of the cache's pages by worked examples, apart from the list model: what the header says of each case."""
 import pytest
+import torch
 
 from test_gpu_pages import Device, ints
 from gateddeltanet_linear_attention_gb300 import gdn
@@ -26,3 +27,28 @@ def test_fork_lanes_that_name_one_another():
     assert fork([0, -1, 5, 2], [5, 6, -1, 6]) == 0                   # inactive lanes name nothing
     rows[5] = rows[6] = rows[0]
     assert d.lens.tolist() == [20, 0, 20, 0, 0, 20, 20, 5] and d.table.equal(rows) and d.refs.tolist()[:3] == [4, 4, 1]
+
+
+def test_copies_before_a_compaction():
+    """A shared last page that all its holders leave is free before its copies are carried out: copies first, then the
+    compaction, which closes it up."""
+    d = Device(10, 4, 4)
+    d.resize([3], [40])                                              # pages 0 to 2, which end: holes in front
+    d.resize([0], [20])                                              # pages 3, 4
+    d.fork([0], [1])
+    d.resize([3], [0])
+    pools = [torch.zeros(10, 1, 16, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    for f, pool in enumerate(pools):
+        pool[3], pool[4] = 3 + 10 * f, 4 + 10 * f
+    src, dst = d.resize([0, 1], [21, 22])
+    assert src.tolist() == [4, 4] and dst.tolist() == [0, 1] and d.refs[4] == 0
+    gdn.gdn_page_copy(d.cfg, *pools, *pools, src, dst)
+    src, dst = d.compact(10, True)
+    assert src.tolist()[:2] == [3, -1] and dst.tolist()[:2] == [2, -1]
+    gdn.gdn_page_copy(d.cfg, *pools, *pools, src, dst)
+    for row in (0, 1):
+        first, last = d.table[row, :2].tolist()
+        for f, pool in enumerate(pools):
+            assert (pool[first] == 3 + 10 * f).all() and (pool[last] == 4 + 10 * f).all()
+    assert gdn.gdn_device_error() == 0
+    d.m.check()
