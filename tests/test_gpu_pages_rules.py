@@ -1,4 +1,6 @@
 """Rules of the cache's pages by worked examples, apart from the list model: what the header says of each case."""
+import random
+
 import pytest
 import torch
 
@@ -51,4 +53,36 @@ def test_copies_before_a_compaction():
         for f, pool in enumerate(pools):
             assert (pool[first] == 3 + 10 * f).all() and (pool[last] == 4 + 10 * f).all()
     assert gdn.gdn_device_error() == 0
+    d.m.check()
+
+
+def test_pool_that_runs_out_behind_the_first_thousand_lanes():
+    """Places of lanes that a block's threads do not hold, granted and refused."""
+    d = Device(60_000, 4000, 40, 16, lanes=4000)
+    rng = random.Random(5)
+    rows = list(range(4000))
+    rng.shuffle(rows)
+    new = [rng.randint(1, 640) for _ in rows]
+    d.resize(rows, new)
+    refused = [i for i, (r, v) in enumerate(zip(rows, new)) if d.m.lens[r] != v]
+    assert 1100 < refused[0] < 3900 and refused == list(range(refused[0], 4000)) and all(d.m.lens[rows[i]] == 0 for i in refused)
+    # Some end, others shrink: nothing is granted to who asks in the same call (pages are taken from those free when it starts), and
+    # in the next one a part is.
+    new = [0 if i % 5 == 0 else v if i >= refused[0] else rng.choice([v, v // 2]) for i, v in enumerate(new)]
+    d.resize(rows, new)
+    assert all(d.m.lens[rows[i]] == 0 for i in refused)
+    d.resize(rows, new)
+    assert 0 < sum(d.m.lens[rows[i]] == new[i] > 0 for i in refused)
+    d.m.check()
+
+
+def test_copies_behind_the_first_thousand_lanes():
+    """Samples of one prompt that all grow in its last page: pages for 1,500 of 1,600 copies."""
+    d = Device(1502, 1700, 4, 16, lanes=1600)
+    d.resize([0], [20])
+    rows = list(range(1, 1601))
+    d.fork([0] * 1600, rows)
+    src, dst = d.resize(rows, [21] * 1600)
+    assert src.tolist() == [1] * 1500 + [-1] * 100 and dst.tolist() == list(range(2, 1502)) + [-1] * 100
+    assert d.lens.tolist()[1:1601] == [21] * 1500 + [20] * 100
     d.m.check()
