@@ -128,3 +128,21 @@ def test_scores_of_minus_infinity(Hq, Hkv, D, page, tokens):
     for r, which in enumerate(gone):
         compare(out[r * k:(r + 1) * k].double().cpu(), lse[r * k:(r + 1) * k].double().cpu(), c.want(r, seen=[not x for x in which]), len(which), D, c.act)
     assert not out[k:2 * k].any() and (lse[k:2 * k] == -math.inf).all() and gdn.gdn_device_error() == 0
+
+
+@pytest.mark.parametrize("act,Hq,Hkv,D,tokens", [("bf16", 4, 2, 64, 1), ("bf16", 4, 2, 128, 4), ("bf16", 4, 2, 256, 1)] + [("bf16", 16, 2, D, 8) for D in (64, 128, 256)] +
+                         [("fp32", 4, 2, 64, 1), ("fp32", 16, 2, 128, 8)])
+@pytest.mark.parametrize("value", [math.inf, -math.inf])
+@pytest.mark.parametrize("length", [300, 5000])
+def test_infinite_values_that_all_rows_see(act, Hq, Hkv, D, tokens, value, length):
+    """The column of the value is not finite in the rows of its key head, and infinite in fp32; nothing else changes."""
+    c = Cache([length, 90], Hq, Hkv, D, 16, act, tokens, seed=3).upload()
+    clean, clean_lse = c.run()
+    c.d[2][c.table[0, 2], 1, 7, 11] = value
+    out, lse = c.run()
+    bad = torch.zeros_like(out, dtype=torch.bool)
+    bad[:tokens, Hq // 2:, 11] = True
+    assert torch.equal(torch.isfinite(out), ~bad) and torch.equal(torch.where(bad, 0, out), torch.where(bad, 0, clean)) and torch.equal(lse, clean_lse)
+    if act == "fp32":
+        assert (out[bad] == value).all()
+    assert gdn.gdn_device_error() == 0
