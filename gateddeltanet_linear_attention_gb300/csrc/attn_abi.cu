@@ -24,6 +24,10 @@ bool valid_out_heads(const void *p, long long ld, long long hs, long long rows, 
     return valid_heads(p, ld, hs, rows, heads, D) &&
            (rows <= 1 || heads <= 1 || ld >= (heads - 1) * hs + D || hs >= (rows - 1) * ld + D);
 }
+// `to` in the place of a contiguous `from`: each vector in its own, for others are still to be read.
+bool in_place(const void *to, long long ld, long long hs, const void *from, long long rows, long long heads, long long D) {
+    return to != from || ((rows <= 1 || ld == heads * D) && (heads <= 1 || hs == D));
+}
 
 gdn_status check_cfg(const gdn_attn_config *c, gdn::AttnDims *d) {
     if (!c) return GDN_ERR_INVALID_ARG;
@@ -117,7 +121,9 @@ gdn_status gdn_attn_prep_backward(const gdn_attn_config *cfg, const gdn_attn_pre
         return GDN_ERR_INVALID_ARG;
     if (io->T > 0 && (!io->dq_out || (io->dq && !valid_out_heads(io->dq, io->ld_dq, io->hs_dq, io->T, d.hq, d.D)) ||
                       (io->k != nullptr) != (io->dk_out != nullptr) || (io->dk && !io->k) ||
-                      (io->dk && !valid_out_heads(io->dk, io->ld_dk, io->hs_dk, io->T, d.hkv, d.D))))
+                      (io->dk && !valid_out_heads(io->dk, io->ld_dk, io->hs_dk, io->T, d.hkv, d.D)) ||
+                      (io->dq && !in_place(io->dq, io->ld_dq, io->hs_dq, io->dq_out, io->T, d.hq, d.D)) ||
+                      (io->dk && !in_place(io->dk, io->ld_dk, io->hs_dk, io->dk_out, io->T, d.hkv, d.D))))
         return GDN_ERR_INVALID_ARG;
     const bool weights = io->dw_q || io->dw_k;
     if (weights) {

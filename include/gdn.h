@@ -604,7 +604,8 @@ gdn_status gdn_attn_prep(const gdn_attn_config *cfg, const gdn_attn_prep_io *io,
  * tokens have zero gradients, rows behind the last sequence are left and add
  * nothing.  `workspace` of gdn_attn_prep_workspace_size(cfg, T) bytes, 16-byte
  * aligned, where a weight gradient is asked for.  Sums are taken in a fixed
- * order: equal calls give equal bits.  dq may be dq_out, and dk dk_out. */
+ * order: equal calls give equal bits.  dq may be dq_out, and dk dk_out, each with
+ * that one's layout (contiguous); another layout there is refused. */
 size_t gdn_attn_prep_workspace_size(const gdn_attn_config *cfg, int64_t max_tokens);
 gdn_status gdn_attn_prep_backward(const gdn_attn_config *cfg, const gdn_attn_prep_io *io, void *workspace,
                                   size_t workspace_bytes, void *stream);
