@@ -619,13 +619,15 @@ gdn_status gdn_attn_prep_backward(const gdn_attn_config *cfg, const gdn_attn_pre
  *
  * with query head h reading key head h / (q_heads / kv_heads).  Without a token
  * to see, out is 0 and lse -inf.  What is masked may hold anything: a value that
- * is not finite reaches the rows that see it and no others.  An infinite v that
- * a row sees makes its column of the row infinite in fp32 (while its weight is
- * not 0) and infinite or NaN in bf16, where a weight is two 16-bit parts and
- * either may be 0.  Sums and softmax statistics are 32 bits.  The sequences'
- * cache is split over the GPU by what `lens` says at run time; `workspace` of
- * gdn_attn_workspace_size(cfg, n_seqs, tokens) bytes, 16-byte aligned, holds the
- * parts between the two kernels of a call and nothing between calls. */
+ * is not finite reaches the rows that see it and no others.  A score (times
+ * log2 e) above the range of fp32 makes its row NaN, one below it counts as
+ * masked.  An infinite v that a row sees makes its column of the row infinite in
+ * fp32 (while its weight is not 0) and infinite or NaN in bf16, where a weight is
+ * two 16-bit parts and either may be 0.  Sums and softmax statistics are 32 bits.
+ * The sequences' cache is split over the GPU by what `lens` says at run time;
+ * `workspace` of gdn_attn_workspace_size(cfg, n_seqs, tokens) bytes, 16-byte
+ * aligned, holds the parts between the two kernels of a call and nothing between
+ * calls. */
 typedef struct gdn_attn_decode_io {
     const void *q; int64_t ld_q, hs_q;   /* [n_seqs * tokens] tokens, strides as for gdn_attn_prep */
     const void *k_pages, *v_pages;
