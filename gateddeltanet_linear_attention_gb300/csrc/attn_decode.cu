@@ -178,8 +178,9 @@ __global__ void __launch_bounds__((simt_threads<D, RPW>)) attn_decode_simt_kerne
 #pragma unroll
         for (int r = 0; r < RPW; ++r) {
             const int row = row0 + warp * RPW + r;
-            // (a largest score above the range leaves no weight to any token)
-            const float lsum = m[r] == INFINITY ? NAN : warp_sum(l[r]);
+            // a largest score above the range leaves no weight to any token
+            if (m[r] == INFINITY) l[r] = NAN;
+            const float lsum = warp_sum(l[r]);
             if (row < rows) {
                 const int tok = row / a.d.grp, g = row % a.d.grp;
                 const long long orow = ((long long)n * a.tokens + tok) * a.d.hq + h * a.d.grp + g;
