@@ -35,7 +35,7 @@ template <int D, int NG, int RB> struct Shape {
     static constexpr int threads = (5 * NG + 2) * 32;
     static constexpr int units = D == 256 && RB == 128 ? 1 : 2;
     static constexpr int entry = kTile * D * 2, q_block = RB * D * 2;
-    static constexpr int fixed = units * q_block + NG * (128 * 8 + D * 4) + 1024;
+    static constexpr int fixed = units * q_block + NG * (128 * 8 + 2 * D * 4) + 1024;
     static constexpr int limit = 227 * 1024 - 1024;
     static constexpr int fit = (limit - fixed) / entry, most = fit < kMaxEntries ? fit : kMaxEntries, each = most / NG;
     // Multiples of the groups: an entry then serves tiles of one group alone.  (V's are held longer, but a third for K and two
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__((Shape<D, NG, RB>::threads), 1) attn_decode_ro
     constexpr uint32_t E = S::entries, KE = S::k_entries, VE = S::v_entries, kBlock = kTile * 128, kQBlock = RB * 128;
     extern __shared__ unsigned char raw[];
     __shared__ long long sums[33];
-    __shared__ int found[3], spoiled[NG];
+    __shared__ int found[3], spoiled[2][NG];
     __shared__ uint32_t tmem_base;
     __shared__ uint64_t bars[2 * kMaxEntries + 2 * kUnits + 9 * NG];
     __shared__ int pieces_of[kMaxEntries];
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__((Shape<D, NG, RB>::threads), 1) attn_decode_ro
     // queries in front of the ring, so that what products read behind them is shared memory of this CTA
     unsigned char *q_mem = base, *ring = base + kUnits * S::q_block;
     float2 *stats = reinterpret_cast<float2 *>(ring + E * S::entry);               // [groups][128]: m and l
-    unsigned *spoil = reinterpret_cast<unsigned *>(stats + NG * 128);              // [groups][D]: new tokens whose sum is not finite
+    unsigned *spoil = reinterpret_cast<unsigned *>(stats + NG * 128);              // [even, odd units][groups][D]: new tokens whose sum is not finite
     const uint32_t entries = tc::smem_u32(ring), full = tc::smem_u32(bars), empty = full + 8 * kMaxEntries,
                    ufull = empty + 8 * kMaxEntries, uempty = ufull + 8 * kUnits, s_full = uempty + 8 * kUnits, p_ready = s_full + 16 * NG,
                    pv_done = p_ready + 16 * NG, ended = pv_done + 16 * NG, merged = ended + 8 * NG, taken = merged + 8 * NG;
@@ -140,11 +140,11 @@ __global__ void __launch_bounds__((Shape<D, NG, RB>::threads), 1) attn_decode_ro
             tc::mbar_init(ended + 8 * g, 1);
             tc::mbar_init(merged + 8 * g, active);
             tc::mbar_init(taken + 8 * g, active);
-            spoiled[g] = 0;
+            spoiled[0][g] = spoiled[1][g] = 0;
         }
         tc::mbar_fence_init();
     }
-    for (int i = tid; i < NG * D; i += kThreads) spoil[i] = 0u;
+    for (int i = tid; i < 2 * NG * D; i += kThreads) spoil[i] = 0u;
     // rows that pad the query block stay zero
     for (int i = tid; i < kUnits * S::q_block / 16; i += kThreads) reinterpret_cast<uint4 *>(q_mem)[i] = make_uint4(0u, 0u, 0u, 0u);
     tc::fence_async_smem();
@@ -259,40 +259,36 @@ __global__ void __launch_bounds__((Shape<D, NG, RB>::threads), 1) attn_decode_ro
         const bool on = quarter < active;                   // this warp has rows
         const int token = min(row / a.d.grp, a.tokens - 1);
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16, t_s0 = tmem + lanes + g * 128, t_o0 = tmem + lanes + S::col_o, t_o = t_o0 + g * D;
-        unsigned *my_spoil = spoil + g * D;
         uint32_t e = KE + g, phase = 0, k = 0;             // V's entry of the group's next tile
-        bool ok = true, marked = false;                    // marked: by this thread, in the unit before
+        bool ok = true;
         auto wait = [&](uint32_t b, uint32_t parity) { ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(b, parity, a.wait_ns)); };
         int u = 0;
         for (bool more = true; more; ++u) {
             const uint32_t us = u % kUnits;
-            // A group's warps give up together, and clear their marks together: they meet at its barrier, and what decides is
-            // known to all of them.  (The marks themselves may be those of a faster warp of this unit already.)
+            // A group's warps give up together, and clear their marks of two units before together: they meet at its barrier, and
+            // what decides is known to all of them.  (Marked then, read in front of the barrier, marked anew behind it.)
             const bool here = ok && tc::mbar_wait(ufull + 8 * us, (u / kUnits) & 1, a.wait_ns);
-            const bool clean = bar_all(kBarGroup + g, 128, here && !marked);
-            if (!clean && !bar_all(kBarGroup + g, 128, here)) {
-                ok = false;
-                break;
+            if (!bar_all(kBarGroup + g, 128, here && !spoiled[u & 1][g])) {
+                if (!bar_all(kBarGroup + g, 128, here)) {
+                    ok = false;
+                    break;
+                }
+                // (the other group has taken that unit: this one's warps waited for it in the last one)
+                for (int c = tid & 127; c < D; c += 128) spoil[((u & 1) * NG + g) * D + c] = 0u;
+                spoiled[u & 1][g] = 0;
+                bar_sync(kBarGroup + g, 128);
             }
-            marked = false;
             const Unit unit = units[us];
             more = unit.more;
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(uempty + 8 * us);
             const int first_j = (g - unit.seq0) & (NG - 1), tiles = unit.count > first_j ? (unit.count - first_j + NG - 1) / NG : 0;
-            // a group's O, statistics and marks are the other's too until that has taken them
+            // a group's O and statistics are the other's too until that has taken them
             bool mine = NG == 1 || u == 0;
             auto take_back = [&]() {
                 if (!mine) wait(taken + 8 * (NG - 1 - g), (u - 1) & 1);
                 mine = true;
             };
-            if (!clean) {
-                take_back();
-                for (int c = tid & 127; c < D; c += 128) my_spoil[c] = 0u;
-                bar_sync(kBarGroup + g, 128);
-                spoiled[g] = 0;
-                bar_sync(kBarGroup + g, 128);
-            }
             if (!on) continue;
             float m = -INFINITY, l = 0.f;
             // what all rows see lies below `open`, and not below `wide`
@@ -364,7 +360,6 @@ __global__ void __launch_bounds__((Shape<D, NG, RB>::threads), 1) attn_decode_ro
                 }
                 l += (part[0] + part[1]) + (part[2] + part[3]);
                 if (masked) {
-                    if (j == first_j) take_back();          // the other group may still read this one's marks of the unit before
                     // Places that no row sees may hold anything: they become zeros.  A value that is not finite in a place that
                     // only some new tokens see becomes zero too, and the sums of its column for those tokens are NaN, as sums
                     // with it are not finite.
@@ -385,12 +380,11 @@ __global__ void __launch_bounds__((Shape<D, NG, RB>::threads), 1) attn_decode_ro
                                 for (int q = 0; q < 8; ++q) {
                                     const uint32_t half = q & 1 ? 0xffff0000u : 0xffffu;
                                     if (not_finite2(x[q >> 1] & half)) {
-                                        atomicOr(my_spoil + chunk * 8 + q, who);
+                                        atomicOr(spoil + ((u & 1) * NG + g) * D + chunk * 8 + q, who);
                                         x[q >> 1] &= ~half;
                                     }
                                 }
-                                spoiled[g] = 1;
-                                marked = true;
+                                spoiled[u & 1][g] = 1;
                                 asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" :: "r"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]) : "memory");
                             }
                         }
@@ -424,7 +418,7 @@ __global__ void __launch_bounds__((Shape<D, NG, RB>::threads), 1) attn_decode_ro
             // whether the groups have sums of this unit
             const bool one = unit.count > ((0 - unit.seq0) & (NG - 1)), two = NG > 1 && unit.count > ((1 - unit.seq0) & (NG - 1));
             if (ok) {
-                const bool bad = spoiled[0] || (NG > 1 && spoiled[NG - 1]);
+                const bool bad = spoiled[u & 1][0] || (NG > 1 && spoiled[u & 1][NG - 1]);
                 const bool whole = unit.slot < 0, there = row < rows;
                 const long long orow = ((long long)unit.n * a.tokens + token) * a.d.hq + unit.h * a.d.grp + row - token * a.d.grp;
                 float *part = attn_part(a, blockIdx.x, max(unit.slot, 0));
@@ -446,9 +440,10 @@ __global__ void __launch_bounds__((Shape<D, NG, RB>::threads), 1) attn_decode_ro
                         for (int i = 0; i < 16; ++i) x[i] = fmaf(y[i], f1, x[i]);
                     }
                     if (bad) {
+                        const unsigned *who = spoil + (u & 1) * NG * D + c;
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            if ((spoil[c + i] | (NG > 1 ? spoil[(NG - 1) * D + c + i] : 0u)) >> token & 1) x[i] = NAN;
+                            if ((who[i] | who[(NG - 1) * D + i]) >> token & 1) x[i] = NAN;
                     }
                     if (!there) continue;
                     if (whole) {
