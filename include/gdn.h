@@ -563,7 +563,8 @@ typedef struct gdn_attn_config {
  * for the pairs (a, b) = (n[i], n[i + R/2]), or with `interleaved` (n[2i],
  * n[2i+1]), i < R/2, R = rotary_dim, f = inv_freq; columns from R on pass.
  * The angle is taken from the exact product p f_i (while it is below 10^8), the
- * rest in 32 bits, one rounding at the end.
+ * rest in 32 bits, one rounding at the end.  Where a head's sum of squares passes
+ * 3.4e38, n is 0, and its gradients are.
  *
  * Sequence n has tokens cu_seqlens[n] .. cu_seqlens[n+1]-1, or T / n_seqs tokens
  * where cu_seqlens is NULL (decode and verification batches).  Its j-th of L has
@@ -573,7 +574,8 @@ typedef struct gdn_attn_config {
  * With pools, its k' and v go to its index's place in the cache.
  * Padding lanes and tokens have zero q_out and k_out and store nothing; a token
  * whose index is negative or whose position is too large as well, reported as
- * GDN_DEVERR_PAGE.  Rows behind cu_seqlens[n_seqs] are left as they are.
+ * GDN_DEVERR_PAGE.  Rows behind cu_seqlens[n_seqs] are left as they are (and may
+ * be read: they are valid memory up to T).
  * Two tokens with one place in the cache (rows that share it) race. */
 typedef struct gdn_attn_prep_io {
     const void *q; int64_t ld_q, hs_q;   /* [T] tokens at ld_q, heads at hs_q elements: multiples of 8 */

@@ -1,4 +1,4 @@
-"""Attention of new tokens whose scores leave the range of 32-bit numbers."""
+"""Operators of the attention layers on values that leave the range of 32-bit numbers: scores, and squares of heads."""
 import math
 
 import pytest
@@ -28,4 +28,30 @@ def test_scores_beyond_the_range(act, Hq, Hkv, D, tokens, sign):
         assert torch.isnan(out[sees]).all() and torch.isnan(lse[sees]).all()
         out, lse = out[~sees], lse[~sees]
     assert not out.any() and (lse == -math.inf).all()
+    assert gdn.gdn_device_error() == 0
+
+
+@pytest.mark.parametrize("D,R,interleaved", [(64, 64, False), (128, 20, False), (256, 64, True)])
+@pytest.mark.parametrize("act", [torch.bfloat16, torch.float32])
+def test_squares_beyond_the_range(act, D, R, interleaved):
+    """Head vectors whose squares leave the range have norms and gradients of 0; their neighbours are as without them."""
+    T, Hq, Hkv = 40, 6, 2
+    cfg = gdn.make_attn_config(Hq, Hkv, D, act="bf16" if act == torch.bfloat16 else "fp32")
+    g = torch.Generator(device="cuda").manual_seed(D)
+    q, dq_out, k, dk_out = (torch.randn(T, h, D, generator=g, device="cuda").to(act) for h in (Hq, Hq, Hkv, Hkv))
+    w = 1 + 0.1 * torch.randn(2, D, generator=g, device="cuda")
+    f = (1000.0 ** (-torch.arange(0, R, 2, device="cuda").double() / R)).float()
+    kw = dict(w_q=w[0], w_k=w[1], interleaved=interleaved)
+
+    def run():
+        q_out, dq, k_out, dk = (torch.full_like(x, 7.0) for x in (q, q, k, k))
+        gdn.gdn_attn_prep(cfg, q, k, q_out, f, k_out=k_out, **kw)
+        gdn.gdn_attn_prep_backward(cfg, q, k, dq_out, dk_out, f, dq=dq, dk=dk, **kw)
+        return q_out, dq, k_out, dk
+    clean = run()
+    q[5, 3] *= 1e20
+    k[17, 1, 9] = -1e20
+    for x, want, at in zip(run(), clean, ((5, 3), (5, 3), (17, 1), (17, 1))):
+        want[at] = 0
+        assert torch.equal(x, want)
     assert gdn.gdn_device_error() == 0
