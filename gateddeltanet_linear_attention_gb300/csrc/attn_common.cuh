@@ -190,7 +190,7 @@ cudaError_t launch_attn_prep(const AttnPrepArgs &a, bool act_bf16, cudaStream_t 
 size_t attn_prep_ws_floats(const AttnDims &d, long long T);
 cudaError_t launch_attn_prep_backward(const AttnPrepArgs &a, bool act_bf16, cudaStream_t s);
 
-// Floats of the workspace for `rows` query rows of a unit; carve lays it out.
+// Bytes of the workspace for `rows` query rows of a unit; carve lays it out.
 size_t attn_decode_ws_bytes(const AttnDims &d, int rows);
 void attn_decode_carve(AttnDecodeArgs &a, void *ws);
 cudaError_t launch_attn_decode(const AttnDecodeArgs &a, bool act_bf16, cudaStream_t s);

@@ -17,9 +17,11 @@ constexpr int kSimtTile = 32;
 // The 32-bit form, on the CUDA cores: RPW query rows a warp, a tile of 32 tokens in shared memory, a token a lane for the
 // scores and D / 32 columns a lane for the sums.  The next tile is on its way while one is worked on, the pages of the one
 // behind it are looked up.  Bound by its reads of shared memory and multiply-adds (a warp reads all of a tile for its rows): 64
-// sequences of up to 8,192 tokens, 8 key heads of 128 columns, 4 query heads each (2.2 GB) 558 us, 0.58 of the copy rate (1,258
-// with a tile loaded and worked on in turn); 16 of up to 4,096, 4 key heads, 64 rows each 236 us
-// (eight rows a warp: 342, registers).
+// sequences of 256 to 8,192 tokens, 8 key heads of 128 columns, 4 query heads each (2.1 GB) 556 us, 0.56 of the copy rate (1,258
+// with a tile loaded and worked on in turn); 32 of them, 4 key heads, 12 rows each 307 us, 0.28; 16 of up to 4,096, 4 key heads,
+// 64 rows each 237 us, 0.07 (eight rows a warp: 342, registers).
+// Exponentials are ex2.approx: 2^-22 of a weight and zeros below 2^-126, in a sum whose scores err by more (16 roundings of 2^-24
+// and more, times their size).
 // Two tiles of 256 columns leave room for one CTA an SM: with many rows it is twice as large.
 template <int D, int RPW> constexpr int simt_threads = D == 256 && RPW == 4 ? 512 : 256;
 template <int D, int RPW>
@@ -372,11 +374,10 @@ cudaError_t launch_attn_join(const AttnDecodeArgs &a, bool act_bf16, cudaStream_
                         : launch_early(attn_join_kernel<float, 256>, grid, kJoinThreads, 0, s, a);
 }
 
-// bf16: where 16 query rows hold all of a key head's, their products keep up with the memory (64 sequences of up to 16,384
-// tokens, 4 rows: 339 us against 357 us in the kernel of many rows; 32 of up to 8,192, 16 rows: 53 against 67; one of 700, 8 rows:
-// 8 against 12).  Above, tcgen05 products of 128 rows take what 16 rows would read again: with 32 rows in two groups that share
-// tiles this kernel was slower in large batches (451 us against 427 in the first one, both then) and hardly faster in small calls
-// (11 us against 13 for one sequence of 700 tokens).
+// bf16: where 16 query rows hold all of a key head's, their products keep up with the memory and a call's ends are short: against
+// the kernel of many rows one sequence of 700 tokens, 8 rows takes 8.2 us to 12.3, one of 131,072, 2 key heads of 256 columns, 8 rows
+// 49.2 to 55.0, 32 of up to 8,192, 16 rows 52.4 to 54.2; only where a large batch has few rows is this one slower (64 of up to 16,384
+// tokens, 8 key heads, 4 rows: 348 to 338, floor 339).  Above 16 rows it would read each tile again.
 cudaError_t launch_attn_decode(const AttnDecodeArgs &a, bool act_bf16, cudaStream_t s) {
     if (!act_bf16) return a.d.D == 64 ? run_rows<64>(a, s) : a.d.D == 128 ? run_rows<128>(a, s) : run_rows<256>(a, s);
     return a.d.grp * a.tokens <= 16 ? launch_attn_decode_tc(a, s) : launch_attn_decode_rows(a, s);

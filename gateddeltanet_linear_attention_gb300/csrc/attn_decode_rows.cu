@@ -4,7 +4,7 @@
 // The shares, parts and join of attn_decode.cu, tiles of 64 tokens copied as for the kernel of few rows.  With the query rows
 // as the 128 rows of the products, both accumulators in TMEM:
 //   S = Q K^T     rows x 64 tokens; K from shared memory as TMA left it
-//   P = exp(S - m) a thread a row: maximum and sum need no other lane; P, in two bf16 parts, in the place of S
+//   P = exp(S - m) a thread a row: maximum and sum need no other lane; P, in two bf16 parts (16 bits), in the place of S
 //   O += P V      P from TMEM, V from shared memory as TMA left it
 // Two groups of four warps (one at 256 columns) take turns with the tiles, each with its own S, O, m and l; O of both lies in
 // the same lanes, so where a unit ends each group adds both, in half of the columns.
@@ -16,6 +16,8 @@
 // 8,192 tokens, 8 new ones each, 4 key heads of 128 columns, 8 query heads each (278 MB): 57 us with the join kernel, 0.72 of the
 // copy rate.  A tile takes a group's warps 1,500 cycles (745 of them 64 exponentials a thread), and both groups wait for tiles: one
 // comes in 1,500 to 1,600 cycles, its bytes take 1,400.  The rest is the first tile's way (5 us of 57), units' ends and the join.
+// With 16 query heads each, 128 rows, the same cache takes 65 us; 2 key heads of 256 columns 71 (one group); one sequence of 131,072
+// tokens, 2 key heads of 128 columns, 128 rows 55 us, floor 20 (by themselves the kernel 35, the join of 76 parts of 128 rows 32).
 #include "attn_tc.cuh"
 
 namespace gdn {
@@ -25,7 +27,7 @@ namespace {
 using namespace attn_tc;
 
 // Tiles that a unit's end and the next one's start cost: sums whole 1,100 cycles, the groups' meeting 2,000 to 2,600, outputs
-// 2,300 to 3,000, first scores 1,000.  With 0, 2, 4 and 6: 70, 63, 59 and 58 us for the 32 sequences below, and 133, 124 and 116
+// 2,300 to 3,000, first scores 1,000.  With 0, 2, 4 and 6: 70, 63, 59 and 58 us for the 32 sequences above, and 133, 124 and 116
 // (2, 4, 6) for 64 sequences of up to 4,096 tokens, 8 key heads, 4 query heads each.
 constexpr int kLead = 6;
 constexpr float kSlack = 8.f;                      // powers of two that a score may pass m by

@@ -16,7 +16,10 @@
 // Measured in bf16: 9,600 prompt tokens into the cache (16 + 2 + 2 heads of 256, 64 columns rotated) 36 us, 0.81 of the copy
 // rate, issue used by 0.55 (one batch of four heads ahead in registers 40, two to four of them in shared memory 36 to 38; three
 // blocks an SM 47 to 53: spills); the backward of 8,192
-// tokens (32 + 8 heads of 128) 56 us, 0.66, issue used by 0.57; 64 tokens of a decode step 5.5 us.
+// tokens (32 + 8 heads of 128) 56 us, 0.66, issue used by 0.57; 64 tokens of a decode step 5.2 us.  Of 32 + 8 heads of 128, all
+// columns rotated, 6,905 tokens forward (floor 21, fp32 42) and 8,192 backward (floor 37, fp32 74), in us: halves 27 and 56 (fp32 49
+// and 87), neighbouring pairs 30 and 62 (70 and 96), half of 50 columns 74 and 128 (97 and 150): its partners come from memory one by
+// one.  The backward kernels of the pairs and of the free width spill 64 to 144 bytes.
 #include <type_traits>
 
 #include "attn_common.cuh"
